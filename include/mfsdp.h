@@ -19,6 +19,12 @@
  *   mfsdp_apply_update            scaled update with decoupled weight decay        §5.1
  *   mfsdp_adamw_tail              AdamW on the packed non-2D tail                  §3, §5.1
  *
+ * and the operators whose weights live in the AdamW share of such a step and whose backward
+ * passes produce its gradients:
+ *
+ *   mfsdp_norm_forward / _backward            layer norm and RMS norm
+ *   mfsdp_embedding_forward / _backward       lookup with a scale; gradient by sorted tokens
+ *
  * Conventions shared by every call:
  *   - Pointers named *_dev / buffers are DEVICE pointers (cudaMalloc'd or torch tensors on the
  *     current device); descriptor arrays (mfsdp_param_desc, mfsdp_matrix, contribution pointer
@@ -56,7 +62,8 @@ typedef enum {
   MFSDP_ETIMEOUT = -7,    /* device status: a bounded device-side wait ran out */
   MFSDP_ENONFINITE = -8,  /* device status: a matrix norm (Muon) or update (Shampoo, SOAP) was
                              NaN or Inf */
-  MFSDP_ENODEVICE = -9    /* no usable sm_103 device for a device call */
+  MFSDP_ENODEVICE = -9,   /* no usable sm_103 device for a device call */
+  MFSDP_EINDEX = -10      /* device status: a token id or a label lies outside its table */
 } mfsdp_status;
 
 /* ------------------------------------------------------------------------------------------
@@ -542,12 +549,94 @@ int mfsdp_owner_reduce_momentum_noalloc(const mfsdp_matrix* mats, int32_t n_mats
                                         float* reduced_grad_out, float* norm_out, void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Operators of the parameters that the AdamW share of the step owns: normalisation vectors,
+ * the embedding table and the output head.  Their gradients are what mfsdp_adamw_tail takes as
+ * contributions.  The paper has no counterpart to them.
+ *
+ * Common to all of them: matrices are row-major with a pitch `ld_*` in elements (>= the row
+ * length); element types are an mfsdp_dtype each; arithmetic, sums and statistics are fp32 and
+ * a result is rounded once, to nearest even, when it is stored.  Buffers may start at any
+ * element boundary (rows that start on 16-byte boundaries and hold a multiple of 8 elements
+ * are read and written as 16-byte vectors).  Every sum has a fixed order: results repeat bit
+ * for bit.  Nothing is kept between calls.  Inputs and outputs must not overlap except where
+ * stated.  Work is enqueued on `stream`; the calls can be captured in a CUDA graph.  Errors:
+ * MFSDP_EINVAL (null pointer, bad enum, a pitch below the row length), MFSDP_ESHAPE,
+ * MFSDP_EALIGN (a buffer is not aligned to its element, a workspace not to 256 bytes),
+ * MFSDP_EWORKSPACE, MFSDP_ENODEVICE, MFSDP_ECUDA.
+ * ------------------------------------------------------------------------------------------ */
+
+typedef enum { MFSDP_NORM_LAYER = 0, MFSDP_NORM_RMS = 1 } mfsdp_norm_kind;
+typedef enum { MFSDP_INDEX_I32 = 0, MFSDP_INDEX_I64 = 1 } mfsdp_index_dtype;
+
+/*
+ * Layer norm or RMS norm of every row of x [rows x cols]:
+ *     mu = sum(x) / cols (RMS: 0);  r = 1 / sqrt(sum((x - mu)^2) / cols + eps);
+ *     y = (x - mu) r weight + bias
+ *   dtype        type of x and y;  param_dtype  type of weight and bias.
+ *   weight, bias [cols], nullable (1 and 0); an RMS norm takes no bias.
+ *   mean, rstd   fp32 [rows], nullable outputs: mu (layer norm only) and r, which the backward
+ *                pass takes.
+ * y may be x's buffer (same pitch).  rows == 0 is no work.  rows, cols < 2^31.
+ */
+int mfsdp_norm_forward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                       int32_t param_dtype, const void* x, int64_t ld_x, const void* weight,
+                       const void* bias, float eps, void* y, int64_t ld_y, float* mean,
+                       float* rstd, void* stream);
+
+int mfsdp_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes_out);
+
+/*
+ * Gradient of mfsdp_norm_forward.  With z = (x - mean) rstd and g = dy weight, per row:
+ *     dx = rstd (g - sum(g) / cols [layer norm] - z sum(g z) / cols)
+ * and over the rows, reduced in a fixed order: dweight = sum(dy z), dbias = sum(dy).
+ *   mean (layer norm only), rstd   as written by the forward pass.
+ *   dweight, dbias  [cols] of param_dtype, nullable, overwritten (zero for rows == 0); an RMS
+ *                   norm has no dbias.
+ *   workspace       >= mfsdp_norm_backward_workspace_bytes(rows, cols).
+ * dx may be dy's or x's buffer (same pitch).
+ */
+int mfsdp_norm_backward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                        int32_t param_dtype, const void* dy, int64_t ld_dy, const void* x,
+                        int64_t ld_x, const void* weight, const float* mean, const float* rstd,
+                        void* dx, int64_t ld_dx, void* dweight, void* dbias, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Embedding lookup: out[t] = scale * table[ids[t]] for t < n_tokens (table [vocab x dim]).  The
+ * types of the table and of the output are independent (an fp32 master table can feed bf16
+ * activations).  An id outside [0, vocab) gives a zero row and sets MFSDP_EINDEX in the device
+ * status word.  n_tokens == 0 is no work.  vocab, n_tokens < 2^31, dim < 2^27.
+ */
+int mfsdp_embedding_forward(int64_t vocab, int64_t dim, int32_t table_dtype, const void* table,
+                            int64_t ld_table, int64_t n_tokens, int32_t index_dtype,
+                            const void* ids, float scale, int32_t out_dtype, void* out,
+                            int64_t ld_out, void* stream);
+
+int mfsdp_embedding_backward_workspace_bytes(int64_t vocab, int64_t dim, int64_t n_tokens,
+                                             size_t* bytes_out);
+
+/*
+ * Gradient of the table: dtable[v] = scale * sum of dy[t] over the tokens with ids[t] == v, in
+ * a fixed order.  The whole table is written (rows of absent ids become zero); with
+ * `accumulate` the gradient is added to what dtable holds instead (a head tied to the
+ * embedding, or several micro-batches), and rows of absent ids are left alone.
+ *   padding_idx  an id whose tokens take no part; any value outside [0, vocab) for none.
+ * An id outside [0, vocab) other than padding_idx takes no part and sets MFSDP_EINDEX in the
+ * device status word.
+ */
+int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_tokens, int32_t index_dtype,
+                             const void* ids, int64_t padding_idx, float scale, int32_t dy_dtype,
+                             const void* dy, int64_t ld_dy, int32_t accumulate,
+                             int32_t grad_dtype, void* dtable, int64_t ld_dtable,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------------------------ */
 
 /* Synchronise `stream`, read and clear the current device's status word.  *device_status_out
- * is MFSDP_OK, MFSDP_ETIMEOUT or MFSDP_ENONFINITE (timeout wins).  Returns MFSDP_ECUDA if the
- * synchronisation itself failed. */
+ * is MFSDP_OK, MFSDP_ETIMEOUT, MFSDP_ENONFINITE or MFSDP_EINDEX (the first of these that
+ * occurred, in this order).  Returns MFSDP_ECUDA if the synchronisation itself failed. */
 int mfsdp_query_status(void* stream, int32_t* device_status_out);
 
 /* Static description of a status code. */

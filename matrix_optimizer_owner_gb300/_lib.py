@@ -15,7 +15,7 @@ MFSDP_OK = 0
 STATUS_NAMES = {
     0: "MFSDP_OK", -1: "MFSDP_EINVAL", -2: "MFSDP_ESHAPE", -3: "MFSDP_EALIGN",
     -4: "MFSDP_ENOTCONTIG", -5: "MFSDP_EWORKSPACE", -6: "MFSDP_ECUDA", -7: "MFSDP_ETIMEOUT",
-    -8: "MFSDP_ENONFINITE", -9: "MFSDP_ENODEVICE",
+    -8: "MFSDP_ENONFINITE", -9: "MFSDP_ENODEVICE", -10: "MFSDP_EINDEX",
 }
 
 
@@ -110,6 +110,17 @@ SIGNATURES = {
     "mfsdp_owner_reduce_momentum_noalloc": (C.c_int, [C.POINTER(Matrix), _i32, _i64,
                                                       C.POINTER(_vp), _i32, _i32, _f32, _f32,
                                                       _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mfsdp_norm_forward": (C.c_int, [_i32, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _f32,
+                                     _vp, _i64, _vp, _vp, _vp]),
+    "mfsdp_norm_backward_workspace_bytes": (C.c_int, [_i64, _i64, C.POINTER(C.c_size_t)]),
+    "mfsdp_norm_backward": (C.c_int, [_i32, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp,
+                                      _vp, _vp, _vp, _i64, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "mfsdp_embedding_forward": (C.c_int, [_i64, _i64, _i32, _vp, _i64, _i64, _i32, _vp, _f32,
+                                          _i32, _vp, _i64, _vp]),
+    "mfsdp_embedding_backward_workspace_bytes": (C.c_int, [_i64, _i64, _i64,
+                                                           C.POINTER(C.c_size_t)]),
+    "mfsdp_embedding_backward": (C.c_int, [_i64, _i64, _i64, _i32, _vp, _i64, _f32, _i32, _vp,
+                                           _i64, _i32, _i32, _vp, _i64, _vp, C.c_size_t, _vp]),
     "mfsdp_query_status": (C.c_int, [_vp, C.POINTER(_i32)]),
     "mfsdp_status_string": (C.c_char_p, [C.c_int]),
     "mfsdp_set_wait_limit_ns": (C.c_int, [_u64]),

@@ -172,6 +172,25 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUD
 
 uint64_t mfsdp::wait_limit_ns() { return g_wait_limit_ns.load(); }
 
+int mfsdp::device_sms(int* sms) {
+  constexpr int kCached = 64;
+  static std::atomic<int> cache[kCached];   // per device: SM count, or -1 (not sm_103); 0 unknown
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MFSDP_ENODEVICE;
+  int n = dev < kCached ? cache[dev].load() : 0;
+  if (n == 0) {
+    int major = 0, minor = 0, count = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return MFSDP_ENODEVICE;
+    n = major == 10 && minor == 3 ? count : -1;
+    if (dev < kCached) cache[dev].store(n);
+  }
+  *sms = n;
+  return n > 0 ? MFSDP_OK : MFSDP_ENODEVICE;
+}
+
 extern "C" {
 
 int mfsdp_version(void) { return 100; }
@@ -188,6 +207,7 @@ const char* mfsdp_status_string(int st) {
     case MFSDP_ETIMEOUT: return "device wait timed out";
     case MFSDP_ENONFINITE: return "non-finite norm or update";
     case MFSDP_ENODEVICE: return "no usable sm_103 device";
+    case MFSDP_EINDEX: return "token id or label out of range";
     default: return "unknown status";
   }
 }
@@ -721,6 +741,7 @@ int mfsdp_query_status(void* stream, int32_t* device_status_out) {
   *device_status_out = (v & kStatusTimeout)        ? MFSDP_ETIMEOUT
                        : (v & kStatusTmemMismatch) ? MFSDP_ECUDA
                        : (v & kStatusNonFinite)    ? MFSDP_ENONFINITE
+                       : (v & kStatusBadIndex)     ? MFSDP_EINDEX
                                                    : MFSDP_OK;
   return MFSDP_OK;
 }

@@ -14,6 +14,7 @@ namespace mfsdp {
 constexpr int kStatusTimeout = 1;
 constexpr int kStatusNonFinite = 2;
 constexpr int kStatusTmemMismatch = 4;  // a CTA pair received different tensor-memory bases
+constexpr int kStatusBadIndex = 8;      // a token id or label outside its table
 
 // ---- streaming kernels (gradient deposit + momentum + norm, update) -----------------------
 constexpr int kMaxContrib = 64;
@@ -116,6 +117,7 @@ cudaError_t launch_copy2d(const CopyParams& p, cudaStream_t s);
 cudaError_t launch_wait_timeout_selftest(uint64_t limit_ns, int* status, cudaStream_t s);
 int* status_word_address();  // device address of this device's status word (nullptr on error)
 uint64_t wait_limit_ns();    // limit of every bounded device-side wait (mfsdp_set_wait_limit_ns)
+int device_sms(int* sms);    // MFSDP status; the current device's SM count (sm_103 devices only)
 
 // ---- batched fp32 GEMM on the tensor cores, 3xTF32 (second-order optimizers) --------------
 struct GemmDesc {          // C = alpha op(A) op(B) + beta C, row-major, one problem

@@ -1,0 +1,547 @@
+// Layer norm and RMS norm of the rows of a matrix, forward and backward.
+//
+// Forward, per row x of n elements (layer norm; RMS norm has mu = 0 and no bias):
+//     mu = sum(x) / n,  r = 1 / sqrt(sum((x - mu)^2) / n + eps),  y = (x - mu) r w + b.
+// The row is held in registers, so it is read once, and the squares are summed of the centred
+// values (no cancellation of large means).  Backward, with z = (x - mu) r and g = dy w:
+//     dx = r (g - sum(g) / n [layer] - z sum(g z) / n),  dw = sum_rows dy z,  db = sum_rows dy.
+//
+// Both directions are bound by memory: forward moves 2 and backward 3 values per element.
+// Rows of up to 1024 elements take a warp each (no block barrier; 8 rows in flight per block),
+// longer ones a block each with at most 32 elements per thread; rows beyond 32768 elements are
+// read in passes.  Backward keeps every column's dw and db sums in registers over the rows a
+// block walks; the blocks' sums go to the workspace and a second launch adds them in block
+// order: no atomics, the result does not depend on timing.
+#include "elem.cuh"
+#include "mfsdp.h"
+
+namespace mfsdp {
+namespace {
+
+constexpr int kNormWarps = 8;         // warps per block of the warp-per-row kernels
+constexpr int kWarpRowMax = 1024;     // longest row one warp takes
+constexpr int kMaxChunks = 4;         // 8-element chunks per thread
+constexpr int kRegRowMax = 1024 * 8 * kMaxChunks;
+
+struct NormArgs {
+  int64_t rows, cols;
+  const void *x, *dy;
+  const void *w, *b;          // nullable
+  void *y, *dx;
+  int64_t ld_x, ld_y, ld_dy, ld_dx;
+  float *mean, *rstd;         // forward: nullable outputs
+  const float *mean_in, *rstd_in;
+  float* partials;            // [blocks][2][cols]
+  float eps, inv_n;
+  int layer, wbf16, has_dw, has_db;
+};
+
+__device__ __forceinline__ float load_param(const void* p, int is_bf16, int64_t e) {
+  return is_bf16 ? to_f32(static_cast<const bf16_t*>(p)[e]) : static_cast<const float*>(p)[e];
+}
+
+// How a row lies over the TPR threads that share it: chunk k of thread t holds 8 consecutive
+// elements (VEC) or 8 elements TPR apart (rows without 16-byte alignment); both coalesce.
+template <int TPR, bool VEC>
+__device__ __forceinline__ int64_t elem_of(int t, int k, int j) {
+  return VEC ? ((int64_t)k * TPR + t) * 8 + j : ((int64_t)k * 8 + j) * TPR + t;
+}
+
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ void load_chunk(const T* row, int64_t n, int t, int k, float (&v)[8]) {
+  if (VEC) {
+    const int64_t e = elem_of<TPR, VEC>(t, k, 0);
+    Pack8<T> p;
+    if (e < n) p.load(row + e); else p.zero();
+    p.get(v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t e = elem_of<TPR, VEC>(t, k, j);
+      v[j] = e < n ? to_f32(row[e]) : 0.f;
+    }
+  }
+}
+
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ void store_chunk(T* row, int64_t n, int t, int k, const float (&v)[8]) {
+  if (VEC) {
+    const int64_t e = elem_of<TPR, VEC>(t, k, 0);
+    Pack8<T> p;
+    p.set(v);
+    if (e < n) p.store(row + e);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t e = elem_of<TPR, VEC>(t, k, j);
+      if (e < n) row[e] = from_f32<T>(v[j]);
+    }
+  }
+}
+
+// Sums of two values over the threads of a row, in every one of them.  Block rows use two
+// buffers in turn, so one barrier per call is enough.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* red, int& turn) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if (TPR == 32) return;
+  constexpr int W = TPR / 32;
+  float* buf = red + turn * 2 * W;
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) {
+    buf[threadIdx.x >> 5] = a;
+    buf[W + (threadIdx.x >> 5)] = b;
+  }
+  __syncthreads();
+  a = b = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    a += buf[i];
+    b += buf[W + i];
+  }
+}
+
+// ---------------------------------------------------------------- forward
+template <typename T, int TPR, int K, bool VEC>
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
+    norm_forward_kernel(const __grid_constant__ NormArgs p) {
+  __shared__ float red[TPR == 32 ? 1 : 4 * (TPR / 32)];
+  pdl_launch();
+  pdl_wait();
+  const int t = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5)
+                                : (int64_t)blockIdx.x;
+  if (row >= p.rows) return;  // whole warps (or the whole block) leave
+  int turn = 0;
+  const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
+  float v[K][8];
+  float s = 0.f, zero = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    load_chunk<T, TPR, VEC>(xr, p.cols, t, k, v[k]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[k][j];
+  }
+  float mu = 0.f;
+  if (p.layer) {
+    row_sum2<TPR>(s, zero, red, turn);
+    mu = s * p.inv_n;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = elem_of<TPR, VEC>(t, k, j) < p.cols ? v[k][j] - mu : 0.f;
+      q = fmaf(d, d, q);
+    }
+  zero = 0.f;
+  row_sum2<TPR>(q, zero, red, turn);
+  const float r = rsqrtf(fmaf(q, p.inv_n, p.eps));
+  if (t == 0) {
+    if (p.mean) p.mean[row] = mu;
+    if (p.rstd) p.rstd[row] = r;
+  }
+  T* yr = static_cast<T*>(p.y) + row * p.ld_y;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t e = elem_of<TPR, VEC>(t, k, j);
+      const float w = p.w && e < p.cols ? load_param(p.w, p.wbf16, e) : 1.f;
+      const float b = p.b && e < p.cols ? load_param(p.b, p.wbf16, e) : 0.f;
+      v[k][j] = fmaf((v[k][j] - mu) * r, w, b);
+    }
+    store_chunk<T, TPR, VEC>(yr, p.cols, t, k, v[k]);
+  }
+}
+
+// Rows too long for registers: three passes over the row (the second and third hit the L2).
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_forward_long_kernel(const __grid_constant__ NormArgs p) {
+  __shared__ float red[4 * 32];
+  pdl_launch();
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
+  T* yr = static_cast<T*>(p.y) + row * p.ld_y;
+  int turn = 0;
+  float mu = 0.f, zero = 0.f;
+  if (p.layer) {
+    float s = 0.f;
+    for (int64_t e = threadIdx.x; e < p.cols; e += 1024) s += to_f32(xr[e]);
+    row_sum2<1024>(s, zero, red, turn);
+    mu = s * p.inv_n;
+  }
+  float q = 0.f;
+  zero = 0.f;
+  for (int64_t e = threadIdx.x; e < p.cols; e += 1024) {
+    const float d = to_f32(xr[e]) - mu;
+    q = fmaf(d, d, q);
+  }
+  row_sum2<1024>(q, zero, red, turn);
+  const float r = rsqrtf(fmaf(q, p.inv_n, p.eps));
+  if (threadIdx.x == 0) {
+    if (p.mean) p.mean[row] = mu;
+    if (p.rstd) p.rstd[row] = r;
+  }
+  for (int64_t e = threadIdx.x; e < p.cols; e += 1024) {
+    const float w = p.w ? load_param(p.w, p.wbf16, e) : 1.f;
+    const float b = p.b ? load_param(p.b, p.wbf16, e) : 0.f;
+    yr[e] = from_f32<T>(fmaf((to_f32(xr[e]) - mu) * r, w, b));
+  }
+}
+
+// ---------------------------------------------------------------- backward
+template <typename T, int TPR, int K, bool VEC>
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
+    norm_backward_kernel(const __grid_constant__ NormArgs p) {
+  constexpr int kRowsPerBlock = TPR == 32 ? kNormWarps : 1;
+  __shared__ float red[TPR == 32 ? 1 : 4 * (TPR / 32)];
+  __shared__ float comb[TPR == 32 ? kNormWarps * 32 * 8 : 1];
+  pdl_launch();
+  pdl_wait();
+  const int t = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  const int sub = TPR == 32 ? (threadIdx.x >> 5) : 0;
+  int turn = 0;
+  float aw[K][8], ab[K][8], w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t e = elem_of<TPR, VEC>(t, k, j);
+      w[k][j] = p.w && e < p.cols ? load_param(p.w, p.wbf16, e) : 1.f;
+      aw[k][j] = ab[k][j] = 0.f;
+    }
+  for (int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + sub; row < p.rows;
+       row += (int64_t)gridDim.x * kRowsPerBlock) {
+    const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
+    const T* gr = static_cast<const T*>(p.dy) + row * p.ld_dy;
+    T* dr = static_cast<T*>(p.dx) + row * p.ld_dx;
+    const float r = p.rstd_in[row], mu = p.layer ? p.mean_in[row] : 0.f;
+    float z[K][8], g[K][8];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      load_chunk<T, TPR, VEC>(xr, p.cols, t, k, z[k]);
+      load_chunk<T, TPR, VEC>(gr, p.cols, t, k, g[k]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {   // past the row's end dy is 0: no contribution
+        z[k][j] = (z[k][j] - mu) * r;
+        aw[k][j] = fmaf(g[k][j], z[k][j], aw[k][j]);
+        ab[k][j] += g[k][j];
+        g[k][j] *= w[k][j];
+        s1 += g[k][j];
+        s2 = fmaf(g[k][j], z[k][j], s2);
+      }
+    }
+    row_sum2<TPR>(s1, s2, red, turn);
+    s1 = p.layer ? s1 * p.inv_n : 0.f;
+    s2 *= p.inv_n;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[k][j] = (g[k][j] - s1 - z[k][j] * s2) * r;
+      store_chunk<T, TPR, VEC>(dr, p.cols, t, k, g[k]);
+    }
+  }
+  // this block's column sums, its warps added in warp order
+  float* part = p.partials + (int64_t)blockIdx.x * 2 * p.cols;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (!(h == 0 ? p.has_dw : p.has_db)) continue;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (TPR == 32) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          comb[(sub * 8 + j) * 32 + t] = h == 0 ? aw[k][j] : ab[k][j];
+        __syncthreads();
+        // thread (sub, t) adds element j = sub of lane t over the warps
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kNormWarps; ++i) s += comb[(i * 8 + sub) * 32 + t];
+        const int64_t e = elem_of<TPR, VEC>(t, k, sub);
+        if (e < p.cols) part[h * p.cols + e] = s;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t e = elem_of<TPR, VEC>(t, k, j);
+          if (e < p.cols) part[h * p.cols + e] = h == 0 ? aw[k][j] : ab[k][j];
+        }
+      }
+    }
+  }
+}
+
+// Rows too long for registers: the two row sums, then dx; a block owns whole rows, and its
+// column sums live in the workspace (only this block's threads touch its slice).
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_backward_long_kernel(const __grid_constant__ NormArgs p) {
+  __shared__ float red[4 * 32];
+  pdl_launch();
+  pdl_wait();
+  int turn = 0;
+  float* part = p.partials + (int64_t)blockIdx.x * 2 * p.cols;
+  for (int64_t e = threadIdx.x; e < p.cols; e += 1024) part[e] = part[p.cols + e] = 0.f;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
+    const T* gr = static_cast<const T*>(p.dy) + row * p.ld_dy;
+    T* dr = static_cast<T*>(p.dx) + row * p.ld_dx;
+    const float r = p.rstd_in[row], mu = p.layer ? p.mean_in[row] : 0.f;
+    float s1 = 0.f, s2 = 0.f;
+    for (int64_t e = threadIdx.x; e < p.cols; e += 1024) {
+      const float z = (to_f32(xr[e]) - mu) * r, d = to_f32(gr[e]);
+      part[e] = fmaf(d, z, part[e]);
+      part[p.cols + e] += d;
+      const float g = p.w ? d * load_param(p.w, p.wbf16, e) : d;
+      s1 += g;
+      s2 = fmaf(g, z, s2);
+    }
+    row_sum2<1024>(s1, s2, red, turn);
+    s1 = p.layer ? s1 * p.inv_n : 0.f;
+    s2 *= p.inv_n;
+    for (int64_t e = threadIdx.x; e < p.cols; e += 1024) {
+      const float z = (to_f32(xr[e]) - mu) * r, d = to_f32(gr[e]);
+      const float g = p.w ? d * load_param(p.w, p.wbf16, e) : d;
+      dr[e] = from_f32<T>((g - s1 - z * s2) * r);
+    }
+  }
+}
+
+// Adds the blocks' column sums in block order: 32 columns per block, eight groups of rows
+// whose sums are added in group order.
+template <typename P>
+__global__ void __launch_bounds__(256)
+    norm_param_grad_kernel(const float* partials, int blocks, int64_t cols, P* dw, P* db) {
+  __shared__ float s[8][33];
+  pdl_launch();
+  pdl_wait();
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t e = (int64_t)blockIdx.x * 32 + c;
+  for (int h = 0; h < 2; ++h) {
+    P* out = h == 0 ? dw : db;
+    if (!out) continue;
+    const int per = (blocks + 7) / 8, b0 = g * per, b1 = min(blocks, b0 + per);
+    float a = 0.f;
+    if (e < cols)
+      for (int b = b0; b < b1; ++b) a += partials[((int64_t)b * 2 + h) * cols + e];
+    s[g][c] = a;
+    __syncthreads();
+    if (g == 0 && e < cols) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += s[i][c];
+      out[e] = from_f32<P>(v);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- dispatch
+// TPR and K are the smallest that hold the row; f is called with the kernel's shape.
+template <typename T, bool VEC, typename F>
+cudaError_t by_shape(int64_t cols, F&& f) {
+  auto k_of = [&](int tpr) { return (int)((cols + 8 * tpr - 1) / (8 * tpr)); };
+#define MFSDP_NORM_K(TPR)                                                                      \
+  switch (k_of(TPR)) {                                                                         \
+    case 1: return f.template operator()<T, TPR, 1, VEC>();                                    \
+    case 2: return f.template operator()<T, TPR, 2, VEC>();                                    \
+    case 3: return f.template operator()<T, TPR, 3, VEC>();                                    \
+    default: return f.template operator()<T, TPR, 4, VEC>();                                   \
+  }
+  if (cols <= kWarpRowMax) { MFSDP_NORM_K(32) }
+  if (cols <= 2048) return f.template operator()<T, 128, 2, VEC>();
+  if (cols <= 4096) return f.template operator()<T, 256, 2, VEC>();
+  if (cols <= 8192) return f.template operator()<T, 512, 2, VEC>();
+  if (cols <= 16384) return f.template operator()<T, 512, 4, VEC>();
+  return f.template operator()<T, 1024, 4, VEC>();
+#undef MFSDP_NORM_K
+}
+
+struct FwdLaunch {
+  const NormArgs& a;
+  cudaStream_t st;
+  template <typename T, int TPR, int K, bool VEC>
+  cudaError_t operator()() const {
+    const int64_t per = TPR == 32 ? kNormWarps : 1;
+    return launch_pdl(norm_forward_kernel<T, TPR, K, VEC>,
+                      dim3((unsigned)((a.rows + per - 1) / per)),
+                      dim3(TPR == 32 ? 32 * kNormWarps : TPR), 0, st, a);
+  }
+};
+
+struct BwdLaunch {
+  const NormArgs& a;
+  int max_blocks, sms;
+  cudaStream_t st;
+  int* blocks;
+  template <typename T, int TPR, int K, bool VEC>
+  cudaError_t operator()() const {
+    const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
+    int occ = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &occ, norm_backward_kernel<T, TPR, K, VEC>, threads, 0);
+    if (e != cudaSuccess) return e;
+    const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
+    int64_t g = (int64_t)sms * (occ < 1 ? 1 : occ);
+    if (g > max_blocks) g = max_blocks;
+    if (g > need) g = need;
+    *blocks = (int)g;
+    return launch_pdl(norm_backward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), 0,
+                      st, a);
+  }
+};
+
+constexpr int kNormMaxBlocks = 152 * 8;   // blocks of one backward launch (bounds the workspace)
+
+// 16-byte accesses of eight elements: every row starts on a 16-byte boundary and has whole
+// chunks.
+bool rows_vec(const void* p, int64_t ld, int64_t cols, int32_t dtype) {
+  return aligned_to(p, 16) && cols % 8 == 0 && (ld * (int64_t)dtype_bytes(dtype)) % 16 == 0;
+}
+
+int check_shape(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, int32_t param_dtype) {
+  if (kind != MFSDP_NORM_LAYER && kind != MFSDP_NORM_RMS) return MFSDP_EINVAL;
+  if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return MFSDP_EINVAL;
+  if (rows < 0 || cols < 1 || rows >= (1ll << 31) || cols >= (1ll << 31)) return MFSDP_ESHAPE;
+  return MFSDP_OK;
+}
+
+int blocks_bound(int64_t rows) {
+  return (int)(rows < kNormMaxBlocks ? (rows < 1 ? 1 : rows) : kNormMaxBlocks);
+}
+
+}  // namespace
+}  // namespace mfsdp
+
+using namespace mfsdp;
+
+extern "C" int mfsdp_norm_forward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                                  int32_t param_dtype, const void* x, int64_t ld_x,
+                                  const void* weight, const void* bias, float eps, void* y,
+                                  int64_t ld_y, float* mean, float* rstd, void* stream) {
+  const int chk = check_shape(kind, rows, cols, dtype, param_dtype);
+  if (chk != MFSDP_OK) return chk;
+  if (!(eps >= 0.f) || (kind == MFSDP_NORM_RMS && (bias || mean))) return MFSDP_EINVAL;
+  if (rows == 0) return MFSDP_OK;
+  if (!x || !y || ld_x < cols || ld_y < cols) return MFSDP_EINVAL;
+  const size_t es = dtype_bytes(dtype), ps = dtype_bytes(param_dtype);
+  if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(weight, ps) ||
+      !aligned_to(bias, ps) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return MFSDP_EALIGN;
+  int sms = 0;
+  const int dst = device_sms(&sms);
+  if (dst != MFSDP_OK) return dst;
+  NormArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.x = x;
+  a.ld_x = ld_x;
+  a.w = weight;
+  a.b = bias;
+  a.y = y;
+  a.ld_y = ld_y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.eps = eps;
+  a.inv_n = (float)(1.0 / (double)cols);
+  a.layer = kind == MFSDP_NORM_LAYER;
+  a.wbf16 = param_dtype == MFSDP_DTYPE_BF16;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (cols > kRegRowMax) {
+    e = dtype == MFSDP_DTYPE_BF16
+            ? launch_pdl(norm_forward_long_kernel<bf16_t>, dim3((unsigned)rows), dim3(1024), 0, st, a)
+            : launch_pdl(norm_forward_long_kernel<float>, dim3((unsigned)rows), dim3(1024), 0, st, a);
+  } else {
+    const bool vec = rows_vec(x, ld_x, cols, dtype) && rows_vec(y, ld_y, cols, dtype);
+    const FwdLaunch f{a, st};
+    if (dtype == MFSDP_DTYPE_BF16)
+      e = vec ? by_shape<bf16_t, true>(cols, f) : by_shape<bf16_t, false>(cols, f);
+    else
+      e = vec ? by_shape<float, true>(cols, f) : by_shape<float, false>(cols, f);
+  }
+  return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
+}
+
+extern "C" int mfsdp_norm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes_out) {
+  if (!bytes_out) return MFSDP_EINVAL;
+  if (rows < 0 || cols < 1 || rows >= (1ll << 31) || cols >= (1ll << 31)) return MFSDP_ESHAPE;
+  *bytes_out = (size_t)blocks_bound(rows) * 2 * (size_t)cols * sizeof(float);
+  return MFSDP_OK;
+}
+
+extern "C" int mfsdp_norm_backward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                                   int32_t param_dtype, const void* dy, int64_t ld_dy,
+                                   const void* x, int64_t ld_x, const void* weight,
+                                   const float* mean, const float* rstd, void* dx, int64_t ld_dx,
+                                   void* dweight, void* dbias, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  const int chk = check_shape(kind, rows, cols, dtype, param_dtype);
+  if (chk != MFSDP_OK) return chk;
+  if (kind == MFSDP_NORM_RMS && (mean || dbias)) return MFSDP_EINVAL;
+  if (rows > 0 && (!dy || !x || !dx || !rstd || (kind == MFSDP_NORM_LAYER && !mean) ||
+                   ld_dy < cols || ld_x < cols || ld_dx < cols))
+    return MFSDP_EINVAL;
+  if (!workspace) return MFSDP_EINVAL;
+  const size_t es = dtype_bytes(dtype), ps = dtype_bytes(param_dtype);
+  if (!aligned_to(dy, es) || !aligned_to(x, es) || !aligned_to(dx, es) ||
+      !aligned_to(weight, ps) || !aligned_to(dweight, ps) || !aligned_to(dbias, ps) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(workspace, 16))
+    return MFSDP_EALIGN;
+  size_t need = 0;
+  mfsdp_norm_backward_workspace_bytes(rows, cols, &need);
+  if (workspace_bytes < need) return MFSDP_EWORKSPACE;
+  int sms = 0;
+  const int dst = device_sms(&sms);
+  if (dst != MFSDP_OK) return dst;
+  NormArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.x = x;
+  a.ld_x = ld_x;
+  a.dy = dy;
+  a.ld_dy = ld_dy;
+  a.w = weight;
+  a.dx = dx;
+  a.ld_dx = ld_dx;
+  a.mean_in = mean;
+  a.rstd_in = rstd;
+  a.partials = static_cast<float*>(workspace);
+  a.inv_n = (float)(1.0 / (double)cols);
+  a.layer = kind == MFSDP_NORM_LAYER;
+  a.wbf16 = param_dtype == MFSDP_DTYPE_BF16;
+  a.has_dw = dweight != nullptr;
+  a.has_db = dbias != nullptr;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  int blocks = 0;
+  if (rows > 0) {
+    if (cols > kRegRowMax) {
+      blocks = blocks_bound(rows) < sms ? blocks_bound(rows) : sms;
+      e = dtype == MFSDP_DTYPE_BF16
+              ? launch_pdl(norm_backward_long_kernel<bf16_t>, dim3(blocks), dim3(1024), 0, st, a)
+              : launch_pdl(norm_backward_long_kernel<float>, dim3(blocks), dim3(1024), 0, st, a);
+    } else {
+      const bool vec = rows_vec(x, ld_x, cols, dtype) && rows_vec(dy, ld_dy, cols, dtype) &&
+                       rows_vec(dx, ld_dx, cols, dtype);
+      const BwdLaunch f{a, blocks_bound(rows), sms, st, &blocks};
+      if (dtype == MFSDP_DTYPE_BF16)
+        e = vec ? by_shape<bf16_t, true>(cols, f) : by_shape<bf16_t, false>(cols, f);
+      else
+        e = vec ? by_shape<float, true>(cols, f) : by_shape<float, false>(cols, f);
+    }
+  }
+  if (e == cudaSuccess && (dweight || dbias)) {
+    const dim3 grid((unsigned)((cols + 31) / 32));
+    e = param_dtype == MFSDP_DTYPE_BF16
+            ? launch_pdl(norm_param_grad_kernel<bf16_t>, grid, dim3(256), 0, st, a.partials,
+                         blocks, cols, static_cast<bf16_t*>(dweight), static_cast<bf16_t*>(dbias))
+            : launch_pdl(norm_param_grad_kernel<float>, grid, dim3(256), 0, st, a.partials,
+                         blocks, cols, static_cast<float*>(dweight), static_cast<float*>(dbias));
+  }
+  return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
+}

@@ -18,6 +18,10 @@ POLICY_ROLE_GREEDY = 0
 POLICY_SCOPE_GREEDY = 1
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+INDEX_I32 = 0
+INDEX_I64 = 1
+NORM_LAYER = 0
+NORM_RMS = 1
 LR_ORIGINAL = 0
 LR_MATCH_RMS_ADAMW = 1
 
@@ -438,3 +442,167 @@ def mfsdp_gemm_f32_batched(problems, trans_a: bool = False, trans_b: bool = Fals
            lib.mfsdp_gemm_f32_batched(tab, n, 1 if trans_a else 0, 1 if trans_b else 0,
                                       _ptr(workspace), workspace.numel(), _stream(stream)))
 
+
+
+# ------------------------------------------------------------------------------- operators
+def _matrix(t, rows: int, cols: int, name: str) -> int:
+    """Pitch of a rows x cols tensor with unit column stride."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: expected a {rows} x {cols} tensor, got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected unit column stride, got strides {t.stride()}")
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _vector(t, n: int, name: str, dtype=None) -> None:
+    if t is None:
+        return
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+
+
+def _index_code(t, name: str) -> int:
+    import torch
+    if t.dtype == torch.int64:
+        return INDEX_I64
+    if t.dtype == torch.int32:
+        return INDEX_I32
+    raise TypeError(f"{name}: expected int32 or int64, got {t.dtype}")
+
+
+def _float_code(t, name: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor on the current CUDA device (a host pointer would fault the GPU)."""
+    import torch
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and (t.device.type != "cuda"
+                              or (cur is not None and t.device.index != cur)):
+            raise ValueError(f"expected tensors on the current CUDA device, got {t.device}")
+
+
+def _workspace(ws, nbytes: int, device, stream):
+    """The caller's uint8 workspace, or a fresh one that lives until `stream` is done with it."""
+    import torch
+    if ws is not None:
+        return ws, ws.numel() * ws.element_size()
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream if hasattr(stream, "cuda_stream")
+                         else torch.cuda.ExternalStream(stream))
+    return ws, nbytes
+
+
+def _params_code(named) -> int:
+    """The one dtype of the given parameter vectors (fp32 when there is none)."""
+    codes = {_float_code(t, name) for name, t in named if t is not None}
+    if len(codes) > 1:
+        raise TypeError("the norm's parameters and their gradients must share one dtype")
+    return codes.pop() if codes else DTYPE_F32
+
+
+def mfsdp_norm_forward(kind: int, x, weight, bias, eps: float, y, mean=None, rstd=None,
+                       stream=None) -> None:
+    """Layer norm (``kind`` NORM_LAYER) or RMS norm (NORM_RMS) of the rows of ``x`` into ``y``.
+    ``weight`` and ``bias`` may be None; ``mean`` and ``rstd`` (fp32, per row) are written where
+    given, for ``mfsdp_norm_backward``."""
+    import torch
+    rows, cols = x.shape
+    code = _float_code(x, "x")
+    if y.dtype != x.dtype:
+        raise TypeError(f"y: expected {x.dtype}, got {y.dtype}")
+    ld_x, ld_y = _matrix(x, rows, cols, "x"), _matrix(y, rows, cols, "y")
+    _vector(weight, cols, "weight")
+    _vector(bias, cols, "bias")
+    _vector(mean, rows, "mean", torch.float32)
+    _vector(rstd, rows, "rstd", torch.float32)
+    pcode = _params_code((("weight", weight), ("bias", bias)))
+    _same_device(x, weight, bias, y, mean, rstd)
+    _check("mfsdp_norm_forward", _lib.load().mfsdp_norm_forward(
+        kind, rows, cols, code, pcode, _ptr(x), ld_x, _ptr(weight), _ptr(bias), eps, _ptr(y),
+        ld_y, _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def mfsdp_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    out = C.c_size_t(0)
+    _check("mfsdp_norm_backward_workspace_bytes",
+           _lib.load().mfsdp_norm_backward_workspace_bytes(rows, cols, C.byref(out)))
+    return out.value
+
+
+def mfsdp_norm_backward(kind: int, dy, x, weight, mean, rstd, dx, dweight=None, dbias=None,
+                        workspace=None, stream=None) -> None:
+    """Gradients of ``mfsdp_norm_forward`` for its input and, where given, for the weight and
+    the bias.  ``workspace`` (uint8) defaults to a fresh one."""
+    import torch
+    rows, cols = x.shape
+    code = _float_code(x, "x")
+    for name, t in (("dy", dy), ("dx", dx)):
+        if t.dtype != x.dtype:
+            raise TypeError(f"{name}: expected {x.dtype}, got {t.dtype}")
+    ld_dy, ld_x = _matrix(dy, rows, cols, "dy"), _matrix(x, rows, cols, "x")
+    ld_dx = _matrix(dx, rows, cols, "dx")
+    for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
+        _vector(t, cols, name)
+    _vector(mean, rows, "mean", torch.float32)
+    _vector(rstd, rows, "rstd", torch.float32)
+    pcode = _params_code((("weight", weight), ("dweight", dweight), ("dbias", dbias)))
+    _same_device(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+    ws, nbytes = _workspace(workspace, mfsdp_norm_backward_workspace_bytes(rows, cols), x.device,
+                            stream)
+    _check("mfsdp_norm_backward", _lib.load().mfsdp_norm_backward(
+        kind, rows, cols, code, pcode, _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(weight), _ptr(mean),
+        _ptr(rstd), _ptr(dx), ld_dx, _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes,
+        _stream(stream)))
+
+
+def mfsdp_embedding_forward(table, ids, scale: float, out, stream=None) -> None:
+    """``out[t] = scale * table[ids[t]]``; the table and the output may differ in dtype."""
+    vocab, dim = table.shape
+    n = ids.numel()
+    tcode, ocode = _float_code(table, "table"), _float_code(out, "out")
+    icode = _index_code(ids, "ids")
+    _vector(ids, n, "ids")
+    ld_t, ld_o = _matrix(table, vocab, dim, "table"), _matrix(out, n, dim, "out")
+    _same_device(table, ids, out)
+    _check("mfsdp_embedding_forward", _lib.load().mfsdp_embedding_forward(
+        vocab, dim, tcode, _ptr(table), ld_t, n, icode, _ptr(ids), scale, ocode, _ptr(out), ld_o,
+        _stream(stream)))
+
+
+def mfsdp_embedding_backward_workspace_bytes(vocab: int, dim: int, n_tokens: int) -> int:
+    out = C.c_size_t(0)
+    _check("mfsdp_embedding_backward_workspace_bytes",
+           _lib.load().mfsdp_embedding_backward_workspace_bytes(vocab, dim, n_tokens,
+                                                                C.byref(out)))
+    return out.value
+
+
+def mfsdp_embedding_backward(ids, dy, scale: float, dtable, padding_idx: int = -1,
+                             accumulate: bool = False, workspace=None, stream=None) -> None:
+    """Gradient of the table of ``mfsdp_embedding_forward``: overwrites ``dtable``, or adds to
+    it with ``accumulate``.  Tokens of ``padding_idx`` take no part.  ``workspace`` (uint8)
+    defaults to a fresh one."""
+    vocab, dim = dtable.shape
+    n = ids.numel()
+    dcode, gcode = _float_code(dy, "dy"), _float_code(dtable, "dtable")
+    icode = _index_code(ids, "ids")
+    _vector(ids, n, "ids")
+    ld_dy, ld_dt = _matrix(dy, n, dim, "dy"), _matrix(dtable, vocab, dim, "dtable")
+    _same_device(ids, dy, dtable, workspace)
+    ws, nbytes = _workspace(workspace, mfsdp_embedding_backward_workspace_bytes(vocab, dim, n),
+                            dtable.device, stream)
+    _check("mfsdp_embedding_backward", _lib.load().mfsdp_embedding_backward(
+        vocab, dim, n, icode, _ptr(ids), padding_idx, scale, dcode, _ptr(dy), ld_dy,
+        1 if accumulate else 0, gcode, _ptr(dtable), ld_dt, _ptr(ws), nbytes, _stream(stream)))

@@ -1,0 +1,131 @@
+"""Host-side checks of the norm and embedding entry points: refusals before any launch, and
+workspace sizes.  Pointers here are made-up addresses that no kernel ever sees."""
+
+import ctypes as C
+import os
+
+import pytest
+
+P = 4096          # an address with every alignment
+EINVAL, ESHAPE, EALIGN, EWORKSPACE = -1, -2, -3, -5
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from matrix_optimizer_owner_gb300 import _lib
+    if not os.path.exists(_lib.LIB_PATH):
+        from matrix_optimizer_owner_gb300 import build
+        build.build()
+    return _lib.load()
+
+
+def _call(fn, good, **changes):
+    args = dict(good, **changes)
+    assert set(args) == set(good)
+    return fn(*args.values())
+
+
+NORM_FWD = dict(kind=0, rows=4, cols=64, dtype=1, pdtype=0, x=P, ld_x=64, w=P, b=P, eps=1e-5, y=P,
+                ld_y=64, mean=P, rstd=P, stream=None)
+NORM_BWD = dict(kind=0, rows=4, cols=64, dtype=1, pdtype=0, dy=P, ld_dy=64, x=P, ld_x=64, w=P,
+                mean=P, rstd=P, dx=P, ld_dx=64, dw=P, db=P, ws=P, ws_bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(kind=2), EINVAL), (dict(dtype=2), EINVAL), (dict(pdtype=-1), EINVAL),
+    (dict(rows=-1), ESHAPE), (dict(cols=0), ESHAPE), (dict(cols=1 << 31), ESHAPE),
+    (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(x=None), EINVAL),
+    (dict(y=None), EINVAL), (dict(ld_x=63), EINVAL), (dict(ld_y=63), EINVAL),
+    (dict(kind=1, mean=None), EINVAL),            # an RMS norm with a bias
+    (dict(kind=1, b=None), EINVAL),               # an RMS norm with a mean
+    (dict(x=P + 1), EALIGN), (dict(w=P + 2), EALIGN), (dict(rstd=P + 2), EALIGN),
+    (dict(rows=0, x=None, y=None), 0),
+])
+def test_norm_forward_refusals(lib, change, status):
+    assert _call(lib.mfsdp_norm_forward, NORM_FWD, **change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(kind=-1), EINVAL), (dict(dtype=5), EINVAL), (dict(rows=1 << 31), ESHAPE),
+    (dict(dy=None), EINVAL), (dict(x=None), EINVAL), (dict(dx=None), EINVAL),
+    (dict(rstd=None), EINVAL), (dict(mean=None), EINVAL), (dict(ld_dx=10), EINVAL),
+    (dict(kind=1, mean=None), EINVAL),            # an RMS norm with a bias gradient
+    (dict(ws=None), EINVAL), (dict(ws=P + 8), EALIGN), (dict(dy=P + 1), EALIGN),
+    (dict(ws_bytes=0), EWORKSPACE), (dict(ws_bytes=4 * 2 * 64 * 4 - 1), EWORKSPACE),
+])
+def test_norm_backward_refusals(lib, change, status):
+    assert _call(lib.mfsdp_norm_backward, NORM_BWD, **change) == status
+
+
+def test_norm_workspace(lib):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    assert mfsdp.mfsdp_norm_backward_workspace_bytes(4, 64) == 4 * 2 * 64 * 4
+    # bounded by the blocks of a launch, not by the rows
+    assert (mfsdp.mfsdp_norm_backward_workspace_bytes(1 << 20, 64)
+            == mfsdp.mfsdp_norm_backward_workspace_bytes(1 << 30, 64))
+    out = C.c_size_t(0)
+    assert lib.mfsdp_norm_backward_workspace_bytes(4, 0, C.byref(out)) == ESHAPE
+    assert lib.mfsdp_norm_backward_workspace_bytes(4, 64, None) == EINVAL
+
+
+EMB_FWD = dict(vocab=100, dim=64, tdtype=0, table=P, ld_t=64, n=5, idtype=1, ids=P, scale=1.0,
+               odtype=1, out=P, ld_o=64, stream=None)
+EMB_BWD = dict(vocab=100, dim=64, n=5, idtype=1, ids=P, pad=-1, scale=1.0, dydtype=1, dy=P,
+               ld_dy=64, acc=0, gdtype=1, dt=P, ld_dt=64, ws=P, ws_bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(vocab=0), ESHAPE), (dict(dim=0), ESHAPE), (dict(n=-1), ESHAPE),
+    (dict(vocab=1 << 31), ESHAPE), (dict(tdtype=2), EINVAL), (dict(odtype=2), EINVAL),
+    (dict(idtype=2), EINVAL), (dict(table=None), EINVAL), (dict(ids=None), EINVAL),
+    (dict(out=None), EINVAL), (dict(ld_t=63), EINVAL), (dict(ld_o=1), EINVAL),
+    (dict(table=P + 2), EALIGN), (dict(ids=P + 4), EALIGN), (dict(out=P + 1), EALIGN),
+    (dict(n=0, table=None, ids=None, out=None), 0),
+])
+def test_embedding_forward_refusals(lib, change, status):
+    assert _call(lib.mfsdp_embedding_forward, EMB_FWD, **change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(vocab=0), ESHAPE), (dict(n=(1 << 31) - 1), ESHAPE), (dict(dydtype=2), EINVAL),
+    (dict(gdtype=7), EINVAL), (dict(idtype=-1), EINVAL), (dict(dt=None), EINVAL),
+    (dict(dy=None), EINVAL), (dict(ids=None), EINVAL), (dict(ld_dy=2), EINVAL),
+    (dict(ld_dt=2), EINVAL), (dict(ws=None), EINVAL), (dict(ws=P + 16), EALIGN),
+    (dict(dt=P + 1), EALIGN), (dict(ws_bytes=256), EWORKSPACE),
+])
+def test_embedding_backward_refusals(lib, change, status):
+    assert _call(lib.mfsdp_embedding_backward, EMB_BWD, **change) == status
+
+
+def test_embedding_workspace(lib):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    need = mfsdp.mfsdp_embedding_backward_workspace_bytes(100, 64, 5)
+    assert need % 256 == 0 and need >= 5 * 16 + 100 + 2 * 64 * 4
+    assert _call(lib.mfsdp_embedding_backward, EMB_BWD, ws_bytes=need - 1) == EWORKSPACE
+    out = C.c_size_t(0)
+    assert lib.mfsdp_embedding_backward_workspace_bytes(0, 64, 5, C.byref(out)) == ESHAPE
+    assert lib.mfsdp_embedding_backward_workspace_bytes(1, 64, 5, None) == EINVAL
+
+
+def test_binding_refuses_wrong_tensors():
+    import torch
+
+    from matrix_optimizer_owner_gb300 import mfsdp
+    x, w = torch.zeros(4, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="CUDA device"):      # host tensors
+        mfsdp.mfsdp_norm_forward(mfsdp.NORM_LAYER, x, w, None, 1e-5, x)
+    with pytest.raises(TypeError):
+        mfsdp.mfsdp_norm_forward(mfsdp.NORM_LAYER, x.half(), w, None, 1e-5, x.half())
+    with pytest.raises(TypeError):
+        mfsdp.mfsdp_norm_forward(mfsdp.NORM_LAYER, x, w, w.bfloat16(), 1e-5, x)
+    with pytest.raises(ValueError):
+        mfsdp.mfsdp_norm_forward(mfsdp.NORM_LAYER, x, torch.zeros(9), None, 1e-5, x)
+    with pytest.raises(ValueError):
+        mfsdp.mfsdp_norm_forward(mfsdp.NORM_LAYER, x, w, None, 1e-5, torch.zeros(8, 4).T)
+    table, ids = torch.zeros(10, 8), torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(TypeError):
+        mfsdp.mfsdp_embedding_forward(table, ids.short(), 1.0, x)
+    with pytest.raises(ValueError):
+        mfsdp.mfsdp_embedding_forward(table, ids[:3], 1.0, x)
+    with pytest.raises(ValueError, match="CUDA device"):
+        mfsdp.mfsdp_embedding_backward(ids, x, 1.0, table)
