@@ -36,11 +36,11 @@
 #include <algorithm>
 
 #include "mfsdp_internal.h"
+#include "umma.cuh"
 
 namespace mfsdp {
 namespace {
 
-constexpr uint32_t kBoxBytes = 64 * 64 * 2;               // one 64 x 64 bf16 TMA box
 constexpr uint32_t kABytes = kBM * kBK * 2;               // 16 KB
 constexpr uint32_t kBBytes = kBN * kBK * 2;               // 32 KB
 constexpr uint32_t kTmemCols = 2 * kBN;                   // two fp32 accumulators
@@ -56,147 +56,6 @@ struct Cfg {
   static constexpr uint32_t kBarOffset = kStages * kStageBytes;
   static constexpr uint32_t kSmem = 1024 + kBarOffset + 256;
 };
-
-// ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ uint64_t globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-struct Guard {                 // shared abort flag + the launch's wait limit
-  volatile int* abort;
-  uint64_t limit_ns;
-  int* status;
-};
-
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const Guard& g,
-                                            bool honor_abort) {
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 31) == 0) {
-      if (honor_abort && *g.abort) return false;
-      if (globaltimer() - t0 > g.limit_ns) {
-        atomicOr(g.status, kStatusTimeout);
-        *g.abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
-// Wait for the phase of `parity` to complete (CTA-scope acquire): inline fast path, bounded slow
-// path.  Returns false if the kernel is aborting or the wait ran out (which starts the abort).
-// `honor_abort` = false is used during teardown.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Guard& g,
-                                          bool honor_abort = true) {
-  return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, g, honor_abort);
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-
-// 32 consecutive fp32 columns of this thread's TMEM lane; waits for the load to land.
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// Shared-memory matrix descriptor, 128-byte swizzle (tcgen05 layout: start >> 4 at bit 0,
-// leading-dimension byte offset >> 4 at bit 16, stride-dimension byte offset >> 4 at bit 32,
-// version 1 at bit 46, swizzle mode 2 = 128B at bit 61).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// K-major operand: rows of 64 k-values (128 B), 8-row swizzle atoms 1024 B apart; the k-step
-// j of 16 elements starts 32 bytes further.  MN-major operand: 64-wide output-index chunks
-// (one box each, 8 KB apart), 8 k-rows of 128 B per atom; k-step j starts 16 rows further.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t base, int mn_major, int j) {
-  return mn_major ? smem_desc(base + (uint32_t)j * 2048u, kBoxBytes, 1024u)
-                  : smem_desc(base + (uint32_t)j * 32u, 16u, 1024u);
-}
-
-// Instruction descriptor, kind::f16: fp32 accumulator (bit 4), bf16 A (bits 7-9) and B
-// (bits 10-12), A / B major-ness (bits 15 / 16), N >> 3 (bits 17-22), M >> 4 (bits 24-28).
-__device__ __forceinline__ uint32_t make_idesc(int a_mn, int b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-}
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
-
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ uint16_t f2bf(float x) {
-  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-__device__ __forceinline__ float bf2f(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
-// Two floats rounded to nearest-even bf16 in one conversion: lo in bits 0-15, hi in 16-31.
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // 32 consecutive bf16 of row r starting at column c0 (c0 % 8 == 0, pitch % 8 == 0) as fp32.
 __device__ __forceinline__ void load_row32(const uint16_t* p, int64_t ld, int r, int c0, int N,
@@ -238,7 +97,6 @@ __device__ __forceinline__ void store_row32(uint16_t* p, int64_t ld, int r, int 
       if (c0 + j >= cmin && c0 + j < N) row[j] = h[j];
   }
 }
-
 
 // ---------------------------------------------------------------- multi-lane TMA producers
 // A thread's TMA loads run one after another (a 64 x 128 box costs a thread ~600-750 cycles,
@@ -292,24 +150,6 @@ struct KCursor {
     }
   }
 };
-
-__device__ __forceinline__ void tma_load_p(bool p, uint32_t dst, const CUtensorMap* map, int x,
-                                           int y, uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
-      " @p cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"((uint32_t)p)
-      : "memory");
-}
-
-__device__ __forceinline__ void expect_tx_p(bool p, uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n"
-      " @p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
-      "r"(bytes), "r"((uint32_t)p)
-      : "memory");
-}
 
 // `rows` rows (128 or 256) of one operand tile: MN-major as 64-wide boxes (map), K-major as
 // 128-row boxes (map + 1); the same predicated instructions run in every lane.
@@ -588,7 +428,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_kernel(const __grid_con
   }
 }
 
-
 // ================================================================ CTA-pair kernel
 // The same three phases on 256 x 256 output tiles computed by a pair of CTAs (a cluster of
 // two) with tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 16): CTA rank r holds rows
@@ -624,133 +463,6 @@ struct PairCfgT {
 };
 using PairCfg = PairCfgT<false>;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// shared::cluster address of the variable at shared::cta address `a` in CTA `rank`.
-__device__ __forceinline__ uint32_t map_rank(uint32_t a, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  return r;
-}
-
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cl(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __noinline__ bool mbar_wait_cl_slow(uint32_t bar, uint32_t parity, const Guard& g,
-                                               bool honor_abort) {
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cl(bar, parity)) return true;
-    if ((i & 31) == 0) {
-      if (honor_abort && *g.abort) return false;
-      if (globaltimer() - t0 > g.limit_ns) {
-        atomicOr(g.status, kStatusTimeout);
-        *g.abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
-// The same with cluster-scope acquire, for barriers that receive arrivals from the peer CTA's
-// threads (the accumulator-empty barrier).
-__device__ __forceinline__ bool mbar_wait_cl(uint32_t bar, uint32_t parity, const Guard& g,
-                                             bool honor_abort = true) {
-  return mbar_try_wait_cl(bar, parity) || mbar_wait_cl_slow(bar, parity, g, honor_abort);
-}
-
-// Arrival on a barrier of either CTA of the pair (the accumulator-empty barrier, in the
-// leader).  What it publishes is that this warp's tensor-memory reads have completed
-// (tcgen05.wait::ld, then tcgen05.fence::before_thread_sync); the MMA issuer reads no memory
-// this thread wrote, so the release is CTA-scoped.  A cluster-scoped release made every
-// epilogue warp wait at each tile's end for its outstanding memory operations (3 % of the
-// GPT-2-small Newton-Schulz time).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
-
-__device__ __forceinline__ void tma_load3d_pair_p(bool p, uint32_t dst, const CUtensorMap* map,
-                                                  int x, int y, int z, uint32_t leader_bar) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " @p cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(leader_bar),
-      "r"((uint32_t)p)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_pair_p(bool p, uint32_t dst, const CUtensorMap* map,
-                                                int x, int y, uint32_t leader_bar) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
-      " @p cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_bar), "r"((uint32_t)p)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// ---------------------------------------------------------------- pair-kernel epilogue helpers
-// Staging block of one epilogue warp: 32 rows x 32 bf16, 64 B per row, the four 16-byte
-// chunks of row r stored in the order k ^ ((r >> 1) & 3).  With that permutation a warp
-// access of one chunk of each of 32 rows (one row per lane) and a warp access of 8 whole rows
-// (four lanes per row) both spread over all eight 16-byte bank groups: 4 wavefronts for
-// 512 B, the minimum.
-__device__ __forceinline__ uint32_t stg_off(int r, int k) {
-  return (uint32_t)(r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y),
-               "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void sts16(uint32_t a, uint16_t v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
-}
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
-
 // Eight bf16 at (r, c) of a row-major buffer (c % 8 == 0, ld % 8 == 0), zero outside M x N.
 __device__ __forceinline__ uint4 load_granule(const uint16_t* p, int64_t ld, int r, int c, int M,
                                               int N) {
@@ -761,50 +473,6 @@ __device__ __forceinline__ uint4 load_granule(const uint16_t* p, int64_t ld, int
   for (int e = 0; e < 8; ++e)
     if (c + e < N) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// tcgen05.ld of 32 consecutive fp32 columns of this thread's TMEM lane, split in issue and
-// wait so that other work overlaps the load; the registers are read-write operands of the
-// wait, so no use of them can move above it.
-__device__ __forceinline__ void tc_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tc_ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-
-__device__ __forceinline__ void tma_store_block(const CUtensorMap* map, uint32_t src, int x,
-                                                int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(src)
-               : "memory");
-}
-
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint16_t cta_mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"(cta_mask)
-      : "memory");
 }
 
 template <bool SPLIT>
@@ -1360,7 +1028,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_gemm_pair_kernel(const __gri
 }
 
 }  // namespace
-
 
 cudaError_t ns_prepare_kernels() {
   cudaError_t e = cudaFuncSetAttribute(ns_gemm_pair_kernel<false>,
