@@ -24,6 +24,7 @@
  *
  *   mfsdp_norm_forward / _backward            layer norm and RMS norm
  *   mfsdp_embedding_forward / _backward       lookup with a scale; gradient by sorted tokens
+ *   mfsdp_head_loss_forward / _backward       softmax cross entropy of the output head
  *
  * Conventions shared by every call:
  *   - Pointers named *_dev / buffers are DEVICE pointers (cudaMalloc'd or torch tensors on the
@@ -629,6 +630,52 @@ int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_tokens, int32
                              const void* dy, int64_t ld_dy, int32_t accumulate,
                              int32_t grad_dtype, void* dtable, int64_t ld_dtable,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace of the head loss.  `backward` selects the call it is for; `weight` and `ld_weight`
+ * are what that call will be given (only their alignment is looked at: a bf16 weight whose rows
+ * do not start on 16-byte boundaries is copied piece by piece); `piece` as below, 0 for the
+ * forward pass.
+ */
+int mfsdp_head_loss_workspace_bytes(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,
+                                    int32_t backward, const void* weight, int64_t ld_weight,
+                                    int64_t piece, size_t* bytes_out);
+
+/*
+ * Softmax cross entropy of an output head, per token, without keeping the logits.  With
+ * z_t = weight hidden_t (hidden [n_tokens x dim], weight [vocab x dim], both of `dtype`):
+ *     lse[t] = log sum_v exp(z_tv),   loss[t] = lse[t] - z_t,labels[t]
+ *   labels       a token whose label is ignore_index is dropped: its loss and lse are 0 and what
+ *                its hidden row holds is not looked at.  A label outside [0, vocab) other than
+ *                ignore_index is dropped too and sets MFSDP_EINDEX in the device status word.
+ *   loss, lse    fp32 [n_tokens], nullable outputs; the backward pass takes lse.
+ * bf16 products run on the tensor cores with fp32 accumulation; fp32 ones as 3xTF32
+ * (mfsdp_gemm_f32_batched's accuracy).  The vocabulary is walked in tiles and never stored
+ * beyond one piece.  n_tokens == 0 is no work.
+ */
+int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,
+                            const void* hidden, int64_t ld_hidden, const void* weight,
+                            int64_t ld_weight, int32_t index_dtype, const void* labels,
+                            int64_t ignore_index, float* loss, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum_t dloss[t] loss[t].  With g_tv = (exp(z_tv - lse[t]) - [v = labels[t]])
+ * dloss[t] (0 for dropped tokens), recomputed in pieces of `piece` columns of the vocabulary
+ * (rounded up to 256; 0 chooses about 64 Mi entries of g per piece):
+ *     dhidden = g weight,   dweight = g^T hidden
+ *   lse          as written by the forward pass;  dloss  fp32 [n_tokens].
+ *   dhidden, dweight   of `dtype`, nullable, overwritten (rows of dropped tokens are zero).
+ * With bf16 inputs g is rounded to bf16 between its two products (relative 2^-8 an entry); sums
+ * are fp32 and each gradient is rounded once.  dhidden may be hidden's buffer (same pitch).
+ */
+int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,
+                             const void* hidden, int64_t ld_hidden, const void* weight,
+                             int64_t ld_weight, int32_t index_dtype, const void* labels,
+                             int64_t ignore_index, const float* lse, const float* dloss,
+                             int64_t piece, void* dhidden, int64_t ld_dhidden, void* dweight,
+                             int64_t ld_dweight, void* workspace, size_t workspace_bytes,
+                             void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * Status and diagnostics.

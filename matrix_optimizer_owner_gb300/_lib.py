@@ -121,6 +121,13 @@ SIGNATURES = {
                                                            C.POINTER(C.c_size_t)]),
     "mfsdp_embedding_backward": (C.c_int, [_i64, _i64, _i64, _i32, _vp, _i64, _f32, _i32, _vp,
                                            _i64, _i32, _i32, _vp, _i64, _vp, C.c_size_t, _vp]),
+    "mfsdp_head_loss_workspace_bytes": (C.c_int, [_i64, _i64, _i64, _i32, _i32, _vp, _i64, _i64,
+                                                  C.POINTER(C.c_size_t)]),
+    "mfsdp_head_loss_forward": (C.c_int, [_i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _vp,
+                                          _i64, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "mfsdp_head_loss_backward": (C.c_int, [_i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _i32,
+                                           _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                           C.c_size_t, _vp]),
     "mfsdp_query_status": (C.c_int, [_vp, C.POINTER(_i32)]),
     "mfsdp_status_string": (C.c_char_p, [C.c_int]),
     "mfsdp_set_wait_limit_ns": (C.c_int, [_u64]),

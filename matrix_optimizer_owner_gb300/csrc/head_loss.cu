@@ -1,0 +1,1329 @@
+// Softmax cross entropy of an output head, per token, without keeping the logits, and its
+// gradient for the hidden states and the head's weight.
+//
+//     Z = H W^T,  lse_t = log sum_v exp Z_tv,  loss_t = lse_t - Z_{t, label_t}
+//     G_tv = (exp(Z_tv - lse_t) - [v = label_t]) dloss_t,  dH = G W,  dW = G^T H
+//
+// Forward computes Z tile by tile on the tensor cores; a tile's epilogue reduces each row to
+// (max, sum of exp(z - max)) and picks the label's logit, so Z never leaves the SM.  A small
+// launch then joins the tiles' pairs.  Backward walks the vocabulary in pieces: it recomputes a
+// piece of Z from the same operands, writes that piece of G (bf16 operands: the only rounding
+// between the inputs and the gradients, within 2^-8 of an entry, the precision the product's
+// other factor has), and multiplies it with W's rows for dH and with H for that piece's rows of
+// dW.  dH is summed over the pieces in fp32.
+//
+// Tokens with the ignored label are dropped before any product: a first launch copies the live
+// rows of H together (padded to whole TMA rows), so they cost nothing, and whatever they hold
+// (NaN too) reaches no output.  The number of live rows stays on the device.
+//
+// bf16 inputs run on the CTA-pair tcgen05 kernel below (256 x 256 tiles, TMA operands,
+// accumulators in tensor memory).  fp32 inputs run on the library's fp32 GEMM (3xTF32) with a
+// piece of Z in the workspace.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+#include <vector>
+
+#include "elem.cuh"
+#include "mfsdp.h"
+#include "umma.cuh"
+
+namespace mfsdp {
+namespace {
+
+constexpr int kTile = 256;                 // tile rows and columns of a CTA pair
+constexpr int kHeadThreads = 320;          // warp 0 TMA, warp 1 MMA, warps 2-9 epilogue
+constexpr int kHeadEpiWarps = 8;
+constexpr int kHeadChunks = 4;             // 32-column chunks per epilogue warp
+constexpr int kHeadStages = 6;
+constexpr uint32_t kHalf = 128 * kBK * 2;  // 16 KB: one operand half of one CTA
+constexpr uint32_t kHeadStageBytes = 2 * kHalf;
+constexpr uint32_t kHeadStaging = kHeadStages * kHeadStageBytes;
+constexpr uint32_t kStagePerWarp = 4096;   // two 32 x 32 bf16 blocks or one of fp32
+constexpr uint32_t kHeadBars = kHeadStaging + kHeadEpiWarps * kStagePerWarp;
+constexpr uint32_t kHeadSmem = 1024 + kHeadBars + 256;
+static_assert(kHeadSmem <= 227 * 1024, "shared memory");
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Phase : int { kStats = 0, kGrad = 1, kOut = 2 };
+
+struct HeadArgs {
+  CUtensorMap h_k, h_mn;                   // compacted H: 64 x 128 K-major box, 3D MN-major view
+  CUtensorMap w_k, w_mn;                   // W (or the copy of a piece): 64 x 128, 64 x 64 boxes
+  CUtensorMap g_k, g_mn, g_st;             // G piece: 64 x 128, 3D view, 32 x 32 stores
+  CUtensorMap dw_st, acc_st;               // dW bf16 and dH fp32 32 x 32 stores
+  const int32_t* nlive;                    // live rows
+  const int32_t* label;                    // [rows] of the compacted rows
+  const float* lse2;                       // [rows] lse * log2(e)
+  const float* dl;                         // [rows] dloss
+  float2* part;                            // [column half-tiles][rows] (max, sum)
+  float* zlab;                             // [rows] the label's logit
+  uint16_t* dw;                            // unaligned dW rows (dw_tma == 0)
+  int64_t ld_dw;
+  int32_t dim, vocab;
+  int32_t v0, width;                       // the piece: columns [v0, v0 + width) of the vocabulary
+  int32_t w_row0;                          // W's map row of column v0
+  int32_t rows;                            // allocated rows (pitch of part, slices of acc)
+  int32_t splits;                          // dH: slices of the piece's columns
+  int32_t add;                             // dH: add to the slices instead of writing them
+  int32_t want_dh, want_dw, dw_tma;
+  int32_t group;                           // tile rows that walk the columns together
+  uint64_t wait_limit_ns;
+  int* status;
+};
+
+struct HeadTile {
+  int kind;                                // kOut only: 0 = dH, 1 = dW
+  int tm, tn;
+  int kb0, nk;                             // k-blocks
+  int split;
+};
+
+// The tiles of one pair, in order.  kStats / kGrad: groups of `group` tile rows walk the
+// columns together (a W panel is read once per group, H's group stays in the L2).  kOut: the
+// tiles of the longer contraction first, round robin; the pairs that got one fewer of them
+// then take the shorter tiles that make up for it, and the rest goes round robin.
+template <int PHASE>
+struct TileList {
+  int live, ntm, ntn;                      // kStats / kGrad
+  int n1, n2, first;                       // kOut: tiles of the two classes, class that leads
+  int ntd, ntv, kdh, kdw, e, pair, npairs, group;
+
+  __device__ __forceinline__ TileList(const HeadArgs& p, int pair_, int npairs_) {
+    pair = pair_;
+    npairs = npairs_;
+    live = *p.nlive;
+    ntm = (live + kTile - 1) / kTile;
+    if (PHASE != kOut) {
+      ntn = (p.width + kTile - 1) / kTile;
+      group = p.group;
+    } else {
+      ntd = (p.dim + kTile - 1) / kTile;
+      ntv = (p.width + kTile - 1) / kTile;
+      const int kbp = (p.width + kBK - 1) / kBK;
+      kdh = (kbp + p.splits - 1) / p.splits;
+      kdw = (live + kBK - 1) / kBK;
+      const int ndh = p.want_dh ? ntm * ntd * p.splits : 0, ndw = p.want_dw ? ntv * ntd : 0;
+      first = kdh >= kdw ? 0 : 1;
+      n1 = first == 0 ? ndh : ndw;
+      n2 = first == 0 ? ndw : ndh;
+      const int k1 = first == 0 ? kdh : kdw, k2 = first == 0 ? kdw : kdh;
+      const int r = n1 % npairs;
+      e = r != 0 && k2 > 0 ? min((k1 + k2 / 2) / k2, n2 / (npairs - r)) : 0;
+    }
+  }
+
+  __device__ __forceinline__ bool get(const HeadArgs& p, int j, HeadTile& t) const {
+    if (PHASE != kOut) {
+      const int idx = pair + j * npairs;
+      if (idx >= ntm * ntn) return false;
+      const int per = group * ntn, g = idx / per, in = idx - g * per;
+      const int rows = min(group, ntm - g * group);
+      t.kind = 0;
+      t.tn = in / rows;
+      t.tm = g * group + (in - t.tn * rows);
+      t.kb0 = 0;
+      t.nk = (p.dim + kBK - 1) / kBK;
+      t.split = 0;
+      return true;
+    }
+    const int r = n1 % npairs, mine = n1 / npairs + (pair < r ? 1 : 0);
+    int idx, kind;
+    if (j < mine) {
+      idx = pair + j * npairs;
+      kind = first;
+    } else {
+      const int q = j - mine, late = npairs - r;
+      kind = 1 - first;
+      if (pair >= r && q < e)
+        idx = (pair - r) + q * late;
+      else if (pair >= r)
+        idx = late * e + (pair - r) + (q - e) * npairs;
+      else
+        idx = late * e + late + pair + q * npairs;
+      if (idx >= n2) return false;
+    }
+    t.kind = kind;
+    if (kind == 0) {
+      t.tm = idx % ntm;
+      const int rest = idx / ntm;
+      t.tn = rest % ntd;
+      t.split = rest / ntd;
+      t.kb0 = t.split * kdh;
+      t.nk = min(kdh, (p.width + kBK - 1) / kBK - t.kb0);
+      if (t.nk < 0) t.nk = 0;
+    } else {
+      t.tm = idx / ntd;
+      t.tn = idx - t.tm * ntd;
+      t.split = 0;
+      t.kb0 = 0;
+      t.nk = kdw;
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tma_reduce_add_block(const CUtensorMap* map, uint32_t src, int x,
+                                                     int y) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
+      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(src)
+      : "memory");
+}
+
+// fp32 staging block, 32 rows x 128 bytes in the 128-byte swizzle of the accumulator's map:
+// chunk k (16 bytes) of row r lies at k ^ (r & 7).  The block is 1024-byte aligned.
+__device__ __forceinline__ uint32_t stg32_off(int r, int k) {
+  return (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4));
+}
+
+template <int PHASE>
+__global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid_constant__ HeadArgs P) {
+  constexpr int S = kHeadStages;
+  extern __shared__ uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kHeadBars);
+  // bars: full[S] | empty[S] | tfull[2] | tempty[2] | drain
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int full0 = 0, empty0 = S, tfull0 = 2 * S, tempty0 = 2 * S + 2, drain = 2 * S + 4;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar(full0 + s), 1);
+      mbar_init(bar(empty0 + s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar(tfull0 + a), 1);
+      mbar_init(bar(tempty0 + a), 2 * kHeadEpiWarps);
+    }
+    mbar_init(bar(drain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the previous launch's results
+  const uint32_t tmem_base = *tmem_slot;
+  uint32_t peer_base;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(peer_base)
+               : "r"(map_rank(smem_u32(tmem_slot), rank ^ 1u))
+               : "memory");
+  const bool usable = peer_base == tmem_base;
+  if (!usable && threadIdx.x == 0) atomicOr(P.status, kStatusTmemMismatch);
+  const Guard g{abort_flag, P.wait_limit_ns, P.status};
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const TileList<PHASE> tiles(P, pair, npairs);
+
+  if (!usable) {
+    // nothing runs: fall through to the teardown
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ TMA producers (both CTAs)
+    // Four lanes in lockstep, one round per two k-blocks: lane bit 1 picks the k-block of the
+    // round, lane bit 0 the operand.  The leader's A lane arms the stage's full barrier for
+    // the bytes of both CTAs.
+    if (lane < 4) {
+      const int par = lane >> 1, opnd = lane & 1;
+      int j = 0, kb = par;
+      HeadTile t{};
+      bool have = tiles.get(P, 0, t);
+      auto advance = [&]() {
+        while (have && kb >= t.nk) {
+          kb -= t.nk;
+          have = tiles.get(P, ++j, t);
+        }
+      };
+      advance();
+      uint32_t q = (uint32_t)par;  // position in the k-block sequence
+      uint32_t armed = 0, last_par = 0;
+      for (;;) {
+        bool act = have && !*abort_flag;
+        if (!__any_sync(0xFu, act)) break;
+        const int stage = (int)(q % S);
+        const uint32_t ph = (q / S) & 1u;
+        if (act && !mbar_wait(bar(empty0 + stage), ph ^ 1u, g)) act = false;
+        const uint32_t fb_local = bar(full0 + stage), fb = map_rank(fb_local, 0);
+        const uint32_t dst = sbase + (uint32_t)stage * kHeadStageBytes + (opnd ? kHalf : 0u);
+        const int r0 = (opnd ? t.tn : t.tm) * kTile + 128 * (int)rank;
+        const int k0 = (t.kb0 + kb) * kBK;
+        expect_tx_p(act && leader && opnd == 0, fb_local, 2u * kHeadStageBytes);
+        if (PHASE != kOut) {
+          // A = H rows, B = W rows, both with the contraction contiguous
+          tma_load_pair_p(act, dst, opnd ? &P.w_k : &P.h_k, k0, opnd ? P.w_row0 + r0 : r0, fb);
+        } else {
+          // dH: A = G rows (K-major), B = W (its rows are the contraction: MN-major);
+          // dW: A = G and B = H, both MN-major with the tokens as the contraction
+          const bool dh = t.kind == 0;
+          tma_load_pair_p(act && dh && !opnd, dst, &P.g_k, k0, r0, fb);
+          tma_load_pair_p(act && dh && opnd, dst, &P.w_mn, r0, P.w_row0 + k0, fb);
+          tma_load_pair_p(act && dh && opnd, dst + kBoxBytes, &P.w_mn, r0 + 64, P.w_row0 + k0, fb);
+          tma_load3d_pair_p(act && !dh, dst, opnd ? &P.h_mn : &P.g_mn, 0, k0, r0 / 64, fb);
+        }
+        if (act && opnd == 0) {
+          armed |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (ph << stage);
+        }
+        q += 2;
+        kb += 2;
+        advance();
+      }
+      // teardown: the leader's full barriers count both CTAs' bytes (an even stage count gives
+      // each k-block parity its own stages)
+      if (leader)
+        for (int st = 0; st < S; ++st)
+          if (armed & (1u << st)) mbar_wait(bar(full0 + st), (last_par >> st) & 1u, g, false);
+    }
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    HeadTile t{};
+    for (int j = 0; tiles.get(P, j, t); ++j) {
+      const int a_mn = PHASE == kOut && t.kind == 1, b_mn = PHASE == kOut;
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) |
+                             ((uint32_t)b_mn << 16) | ((uint32_t)(kTile >> 3) << 17) |
+                             ((uint32_t)(kTile >> 4) << 24);
+      if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
+      bool ok = true;
+      for (int kb = 0; kb < t.nk; ++kb) {
+        if (!mbar_wait(bar(full0 + stage), phase, g)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t sa = sbase + (uint32_t)stage * kHeadStageBytes;
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          tc_mma_pair(d_tmem, operand_desc(sa, a_mn, k), operand_desc(sa + kHalf, b_mn, k), idesc,
+                      (kb | k) != 0);
+        tc_commit_pair(bar(empty0 + stage), 0x3);
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+      tc_commit_pair(bar(tfull0 + acc), 0x3);
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    tc_commit_pair(bar(drain), 0x1);
+    mbar_wait(bar(drain), 0u, g, false);
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    // Warp w covers TMEM lane quarter (w & 3), 32 rows of the CTA's 128, and 128 columns.
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t stg0 = sbase + kHeadStaging + (uint32_t)(warp - 2) * kStagePerWarp;
+    uint32_t nstore = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    HeadTile t{};
+    for (int j = 0; tiles.get(P, j, t); ++j) {
+      const int rw = t.tm * kTile + 128 * (int)rank + quarter * 32, r = rw + lane;
+      const int cb = t.tn * kTile + half * 128;   // first column of this warp
+      const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                             (uint32_t)(acc * kTile + half * 128);
+      if (PHASE == kStats) {
+        const bool live = r < tiles.live;
+        const int lab = live ? P.label[r] - P.v0 : -1;
+        if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
+        tc_fence_after();
+        float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+        for (int q = 0; q < kHeadChunks; ++q) {
+          const int c0 = cb + 32 * q;
+          if (c0 >= P.width || rw >= tiles.live) break;   // warp-uniform
+          __syncwarp();
+          uint32_t a32[32];
+          tc_ld32_issue(taddr + (uint32_t)(32 * q), a32);
+          tc_ld_wait(a32);
+          const int left = P.width - c0;                  // columns past the end take no part
+          float mc = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (k >= left) a32[k] = __float_as_uint(-INFINITY);
+            mc = fmaxf(mc, __uint_as_float(a32[k]));
+          }
+          if (live && lab >= c0 && lab < c0 + 32) {
+            float z = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) z += lab - c0 == k ? __uint_as_float(a32[k]) : 0.f;
+            P.zlab[r] = z;
+          }
+          const float mn = fmaxf(m, mc), ref = mn == -INFINITY ? 0.f : mn * kLog2e;
+          float sc = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sc += exp2f(fmaf(__uint_as_float(a32[k]), kLog2e, -ref));
+          s = s * exp2f(fmaf(m, kLog2e, -ref)) + sc;
+          m = mn;
+        }
+        if (live && cb < P.width) P.part[(int64_t)(t.tn * 2 + half) * P.rows + r] = make_float2(m, s);
+      } else if (PHASE == kGrad) {
+        const bool live = r < tiles.live;
+        const int lab = live ? P.label[r] - P.v0 : -1;
+        const float lse2 = live ? P.lse2[r] : 0.f, dl = live ? P.dl[r] : 0.f;
+        if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < kHeadChunks; ++q) {
+          const int c0 = cb + 32 * q;
+          if (c0 >= (P.width + kBK - 1) / kBK * kBK) break;  // warp-uniform; whole k-blocks of G
+          __syncwarp();
+          uint32_t a32[32];
+          tc_ld32_issue(taddr + (uint32_t)(32 * q), a32);
+          const uint32_t stg = stg0 + (nstore & 1u) * 2048u;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+          tc_ld_wait(a32);
+          const int left = P.width - c0, hit = lab - c0;
+          uint32_t hw[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = 2 * k + h;
+              const float z = __uint_as_float(a32[c]);
+              float p = exp2f(fmaf(z, kLog2e, -lse2));
+              if (c == hit) p -= 1.f;
+              v[h] = live && c < left ? p * dl : 0.f;
+            }
+            hw[k] = pack_bf16x2(v[0], v[1]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sts128(stg + stg_off(lane, k),
+                   make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]));
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_block(&P.g_st, stg, c0, rw);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          ++nstore;
+        }
+      } else {
+        if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
+        tc_fence_after();
+        const int row_end = t.kind == 0 ? tiles.live : P.width;
+#pragma unroll 1
+        for (int q = 0; q < kHeadChunks; ++q) {
+          const int c0 = cb + 32 * q;
+          if (c0 >= P.dim || rw >= row_end) break;        // warp-uniform
+          __syncwarp();
+          uint32_t a32[32];
+          if (t.nk > 0) {
+            tc_ld32_issue(taddr + (uint32_t)(32 * q), a32);
+          } else {                                        // an empty contraction
+#pragma unroll
+            for (int k = 0; k < 32; ++k) a32[k] = 0u;
+          }
+          // both kinds stage in the warp's one 4 KB area: the last store has read it
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+          tc_ld_wait(a32);
+          if (t.kind == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              sts128(stg0 + stg32_off(lane, k),
+                     make_uint4(a32[4 * k], a32[4 * k + 1], a32[4 * k + 2], a32[4 * k + 3]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                w[h] = pack_bf16x2(__uint_as_float(a32[8 * k + 2 * h]),
+                                   __uint_as_float(a32[8 * k + 2 * h + 1]));
+              sts128(stg0 + stg_off(lane, k), make_uint4(w[0], w[1], w[2], w[3]));
+            }
+          }
+          if (t.kind == 1 && !P.dw_tma) {
+            // rows without 16-byte alignment: a warp writes one row of the block at a time
+            __syncwarp();
+            for (int i = 0; i < 32; ++i) {
+              if (rw + i >= row_end || c0 + lane >= P.dim) continue;
+              const uint32_t w = lds32(stg0 + stg_off(i, lane >> 3) + (uint32_t)((lane & 6) * 2));
+              P.dw[(int64_t)(P.v0 + rw + i) * P.ld_dw + c0 + lane] =
+                  (uint16_t)(lane & 1 ? w >> 16 : w & 0xFFFFu);
+            }
+            __syncwarp();
+            continue;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (t.kind == 1)
+              tma_store_block(&P.dw_st, stg0, c0, P.v0 + rw);
+            else if (P.add)
+              tma_reduce_add_block(&P.acc_st, stg0, c0, t.split * P.rows + rw);
+            else
+              tma_store_block(&P.acc_st, stg0, c0, t.split * P.rows + rw);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(bar(tempty0 + acc), 0));
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores done
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while its peer may still use its memory
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- live rows
+struct GatherArgs {
+  const void* labels;
+  const void* hidden;
+  void* hc;                                // [rows][pitch]
+  int64_t ld_h, ignore;
+  int32_t n, is64, dim, pitch, vocab, per; // per: tokens per block
+  int32_t vec;
+  int32_t place;                           // keep every token at its own row, dropped ones zero
+  int32_t* nlive;
+  int32_t* label;
+  int32_t* pos;                            // [n] compacted row of a token, -1: dropped
+  int32_t* token;                          // [rows] token of a compacted row
+  const float *lse_in, *dloss;             // backward
+  float *lse2, *dl;
+  float *loss, *lse;                       // forward: zeroed for dropped tokens
+  int* status;
+};
+
+// Every block counts the live tokens before its own (the labels are read from the L2), so one
+// launch compacts without a scan.  The last block also zeroes the rows up to the next k-block.
+// With `place` (the fp32 path, whose GEMM takes its row count from the host) tokens keep their
+// rows; a dropped one gets a zero row and label -1.
+template <typename T>
+__global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant__ GatherArgs p) {
+  __shared__ int32_t red[8], src[256];
+  __shared__ int32_t start_s;
+  pdl_launch();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = blockIdx.x * p.per, t1 = min(p.n, t0 + p.per);
+  auto live_at = [&](int t, int64_t& lab) {
+    lab = load_index(p.labels, p.is64, t);
+    return lab != p.ignore && lab >= 0 && lab < p.vocab;
+  };
+  int cnt = 0;
+  for (int t = tid; t < t0 && !p.place; t += 256) {
+    int64_t lab;
+    cnt += live_at(t, lab);
+  }
+  cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+  if (lane == 0) red[warp] = cnt;
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) base += red[i];
+  if (p.place) base = t0;
+  T* hc = static_cast<T*>(p.hc);
+  for (int b = t0; b < t1; b += 256) {     // 256 tokens at a time
+    __syncthreads();
+    const int t = b + tid;
+    int64_t lab = 0;
+    const bool in = t < t1, live = in && live_at(t, lab);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
+    if (lane == 0) red[warp] = __popc(mask);
+    __syncthreads();
+    int off = __popc(mask & ((1u << lane) - 1u)), total = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) off += red[i];
+      total += red[i];
+    }
+    if (p.place) {
+      off = tid;
+      total = min(256, t1 - b);
+    }
+    if (in) {
+      p.pos[t] = live ? base + off : -1;
+      if (live || p.place) {
+        src[off] = live ? t : -1;
+        p.label[base + off] = live ? (int32_t)lab : -1;
+        p.token[base + off] = t;
+        if (p.dl) {
+          p.dl[base + off] = live ? p.dloss[t] : 0.f;
+          p.lse2[base + off] = live ? p.lse_in[t] * kLog2e : 0.f;
+        }
+      }
+      if (!live) {
+        if (lab != p.ignore) atomicOr(p.status, kStatusBadIndex);
+        if (p.loss) p.loss[t] = 0.f;
+        if (p.lse) p.lse[t] = 0.f;
+      }
+    }
+    __syncthreads();
+    // copy the live rows, a warp per row; columns past dim are zero
+    for (int i = warp; i < total; i += 8) {
+      const int dim = src[i] >= 0 ? p.dim : 0;
+      const T* s = static_cast<const T*>(p.hidden) + (int64_t)max(src[i], 0) * p.ld_h;
+      T* d = hc + (int64_t)(base + i) * p.pitch;
+      if (p.vec) {
+        for (int e = lane * 8; e < p.pitch; e += 256) {
+          Pack8<T> v;
+          if (e < dim) v.load(s + e); else v.zero();
+          v.store(d + e);
+        }
+      } else {
+        for (int e = lane; e < p.pitch; e += 32) d[e] = e < dim ? s[e] : from_f32<T>(0.f);
+      }
+    }
+    base += total;
+  }
+  if (blockIdx.x != gridDim.x - 1) return;
+  if (tid == 0) {
+    *p.nlive = base;
+    start_s = base;
+  }
+  __syncthreads();
+  const int r0 = start_s, r1 = p.place ? r0 : (r0 + kBK - 1) / kBK * kBK;
+  for (int r = r0 + warp; r < r1; r += 8)
+    for (int e = lane; e < p.pitch; e += 32) hc[(int64_t)r * p.pitch + e] = from_f32<T>(0.f);
+}
+
+// ---------------------------------------------------------------- join of the row statistics
+struct JoinArgs {
+  const float2* part;                      // [parts][rows]
+  float2* state;                           // [rows] running (max, sum) over the pieces
+  const float* zlab;
+  const int32_t *nlive, *token;
+  float *loss, *lse;                       // nullable
+  int32_t parts, rows, first, last;
+};
+
+__device__ __forceinline__ void merge_stats(float& m, float& s, float m2, float s2) {
+  const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
+  s = s * exp2f((m - ref) * kLog2e) + s2 * exp2f((m2 - ref) * kLog2e);
+  m = mn;
+}
+
+// 32 rows per block; 32 groups of parts per row, joined in group order.
+__global__ void __launch_bounds__(1024) head_join_kernel(const __grid_constant__ JoinArgs p) {
+  __shared__ float2 sm[32][33];
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int r = blockIdx.x * 32 + lane, live = *p.nlive;
+  if ((int)blockIdx.x * 32 >= live) return;
+  float m = -INFINITY, s = 0.f;
+  if (r < live) {
+#pragma unroll 4
+    for (int i = grp; i < p.parts; i += 32) {
+      const float2 v = p.part[(int64_t)i * p.rows + r];
+      merge_stats(m, s, v.x, v.y);
+    }
+  }
+  sm[grp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (grp != 0 || r >= live) return;
+  if (!p.first) {
+    const float2 v = p.state[r];
+    m = v.x;
+    s = v.y;
+    merge_stats(m, s, sm[0][lane].x, sm[0][lane].y);
+  }
+  for (int i = 1; i < 32; ++i) merge_stats(m, s, sm[i][lane].x, sm[i][lane].y);
+  if (!p.last) {
+    p.state[r] = make_float2(m, s);
+    return;
+  }
+  const float l = m + logf(s);
+  const int t = p.token[r];
+  if (p.lse) p.lse[t] = l;
+  if (p.loss) p.loss[t] = l - p.zlab[r];
+}
+
+// ---------------------------------------------------------------- dH: slices to the caller's rows
+struct FinishArgs {
+  const float* acc;                        // [splits][rows][pitch]
+  const int32_t* pos;
+  void* dh;
+  int64_t ld_dh;
+  int32_t n, dim, pitch, rows, splits, vec;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(128) head_finish_kernel(const __grid_constant__ FinishArgs p) {
+  pdl_launch();
+  pdl_wait();
+  const int t = blockIdx.x;
+  const int r = p.pos[t];
+  T* out = static_cast<T*>(p.dh) + (int64_t)t * p.ld_dh;
+  const int64_t slice = (int64_t)p.rows * p.pitch;
+  const float* a = p.acc + (int64_t)(r < 0 ? 0 : r) * p.pitch;
+  if (p.vec) {
+    for (int e = threadIdx.x * 8; e < p.dim; e += 1024) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (r >= 0)
+        for (int s = 0; s < p.splits; ++s) {
+          Pack8<float> q;
+          q.load(a + s * slice + e);
+          float x[8];
+          q.get(x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] += x[k];
+        }
+      Pack8<T> o;
+      o.set(v);
+      o.store(out + e);
+    }
+  } else {
+    for (int e = threadIdx.x; e < p.dim; e += 128) {
+      float v = 0.f;
+      if (r >= 0)
+        for (int s = 0; s < p.splits; ++s) v += a[s * slice + e];
+      out[e] = from_f32<T>(v);
+    }
+  }
+}
+
+// Rows [0, rows) x cols of a bf16 matrix into a buffer of 16-byte aligned rows; the rows after
+// them (whole k-blocks) are zero.
+__global__ void __launch_bounds__(256)
+    head_copy_rows_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int rows,
+                          int cols) {
+  pdl_launch();
+  pdl_wait();
+  const int64_t r = blockIdx.x;
+  for (int c = threadIdx.x; c < cols; c += 256)
+    dst[r * ld_dst + c] = r < rows ? src[r * ld_src + c] : (uint16_t)0;
+}
+
+// ---------------------------------------------------------------- fp32 path
+// One row of a piece of Z: (max, sum) joined into the running state, and the label's logit; the
+// last piece writes the loss.
+struct Stats32Args {
+  const float* z;                          // [rows][ldz]
+  float2* state;
+  float* zlab;
+  const int32_t *label, *token;
+  float *loss, *lse;
+  int32_t width, v0, first, last;
+  int64_t ldz;
+};
+
+__global__ void __launch_bounds__(256) head_stats32_kernel(const __grid_constant__ Stats32Args p) {
+  __shared__ float2 sm[8];
+  pdl_launch();
+  pdl_wait();
+  const int r = blockIdx.x;
+  if (p.label[r] < 0) return;              // dropped
+  const float* z = p.z + (int64_t)r * p.ldz;
+  float m = -INFINITY, s = 0.f;
+  for (int c = threadIdx.x; c < p.width; c += 256) merge_stats(m, s, z[c], 1.f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    merge_stats(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int i = 1; i < 8; ++i) merge_stats(m, s, sm[i].x, sm[i].y);
+  if (!p.first) merge_stats(m, s, p.state[r].x, p.state[r].y);
+  const int lab = p.label[r] - p.v0;
+  float zl = p.zlab[r];
+  if (lab >= 0 && lab < p.width) p.zlab[r] = zl = z[lab];
+  p.state[r] = make_float2(m, s);
+  if (!p.last) return;
+  const float l = m + logf(s);
+  const int t = p.token[r];
+  if (p.lse) p.lse[t] = l;
+  if (p.loss) p.loss[t] = l - zl;
+}
+
+struct Grad32Args {
+  float* z;                                // [rows][ldz]: Z in, G out
+  const int32_t* label;
+  const float *lse2, *dl;
+  int32_t width, v0;
+  int64_t ldz;
+};
+
+__global__ void __launch_bounds__(256) head_grad32_kernel(const __grid_constant__ Grad32Args p) {
+  pdl_launch();
+  pdl_wait();
+  const int r = blockIdx.x;
+  float* z = p.z + (int64_t)r * p.ldz;
+  const bool live = p.label[r] >= 0;
+  const float lse2 = p.lse2[r], dl = p.dl[r];
+  const int lab = live ? p.label[r] - p.v0 : -1;
+  for (int c = threadIdx.x; c < p.width; c += 256) {
+    float g = 0.f;
+    if (live) {
+      g = exp2f(fmaf(z[c], kLog2e, -lse2));
+      if (c == lab) g -= 1.f;
+      g *= dl;
+    }
+    z[c] = g;
+  }
+}
+
+// The GEMM's problem table, written by a launch (its values travel in the launch's arguments,
+// so a captured graph replays them).
+constexpr int kDescBatch = 48;
+struct DescArgs {
+  GemmDesc d[kDescBatch];
+  int32_t n;
+  GemmDesc* out;
+};
+__global__ void head_descs_kernel(const __grid_constant__ DescArgs p) {
+  pdl_launch();
+  pdl_wait();
+  for (int i = threadIdx.x; i < p.n; i += blockDim.x) p.out[i] = p.d[i];
+}
+
+// ---------------------------------------------------------------- host
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
+
+struct HeadShape {
+  int64_t n, dim, vocab;
+  int32_t dtype;
+  bool backward, copy_w;
+  int64_t rows, pitch;                     // compacted H (and dH slices)
+  int64_t piece, pieces;                   // columns per piece
+  int64_t splits;                          // dH slices
+  int64_t kdh;                             // fp32: columns per dH slice
+};
+
+struct HeadLayout {
+  size_t nlive, label, pos, token, lse2, dl, zlab, state, hc, part, g, acc, wcopy, descs, total;
+};
+
+constexpr int64_t kGElems = 64ll << 20;    // entries of G (or of Z) per piece
+constexpr int64_t kPartBytes = 64ll << 20; // bytes of the forward partials per piece
+constexpr int kMaxSplits = 64;
+constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
+
+// Columns per piece: about 64 Mi entries, whole tiles, at least 4096 columns.  Wider pieces mean
+// fewer launches and fewer passes over dH's sums; narrower ones a smaller workspace.
+int64_t piece_columns(const HeadShape& s, int64_t asked) {
+  int64_t c;
+  if (asked > 0)
+    c = asked;
+  else if (s.backward || s.dtype == MFSDP_DTYPE_F32)
+    c = std::max<int64_t>(kGElems / s.rows, 4096);
+  else if (s.copy_w)
+    c = std::max<int64_t>(kGElems / s.pitch, 4096);
+  else
+    c = std::max<int64_t>(kPartBytes / (8 * s.rows) * 128, 4096);
+  c = up(c, kTile);
+  return std::min(c, up(s.vocab, kTile));
+}
+
+HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool backward,
+                     const void* weight, int64_t ld_w, int64_t piece, int sms) {
+  HeadShape s{};
+  s.n = n;
+  s.dim = dim;
+  s.vocab = vocab;
+  s.dtype = dtype;
+  s.backward = backward;
+  const bool bf = dtype == MFSDP_DTYPE_BF16;
+  s.copy_w = bf && (!aligned_to(weight, 16) || ld_w % 8 != 0);
+  s.rows = up(std::max<int64_t>(n, 1), kTile);
+  s.pitch = up(dim, 64);
+  s.piece = piece_columns(s, piece);
+  s.pieces = cdiv(vocab, s.piece);
+  s.splits = 1;
+  if (backward) {
+    // dH has few tiles when there are few tokens: cut its contraction (the piece's columns)
+    // until the tiles fill the GPU; a slice keeps at least 1024 columns
+    const int64_t units = bf ? sms / 2 : sms;
+    const int64_t tiles = cdiv(std::max<int64_t>(n, 1), bf ? kTile : 128) * cdiv(dim, kTile);
+    const int64_t want = cdiv(units, tiles), most = std::max<int64_t>(1, s.piece / 1024);
+    s.splits = std::max<int64_t>(1, std::min({want, most, (int64_t)kMaxSplits}));
+    s.kdh = up(cdiv(s.piece, s.splits), 64);
+    s.splits = cdiv(s.piece, s.kdh);
+  }
+  return s;
+}
+
+HeadLayout head_layout(const HeadShape& s) {
+  HeadLayout l{};
+  size_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t at = off;
+    off += (size_t)up(bytes, 1024);
+    return at;
+  };
+  const bool bf = s.dtype == MFSDP_DTYPE_BF16;
+  const int64_t es = bf ? 2 : 4;
+  l.nlive = take(4);
+  l.label = take(s.rows * 4);
+  l.pos = take(s.rows * 4);
+  l.token = take(s.rows * 4);
+  l.lse2 = take(s.backward ? s.rows * 4 : 0);
+  l.dl = take(s.backward ? s.rows * 4 : 0);
+  l.zlab = take(s.rows * 4);
+  l.state = take(s.rows * 8);
+  l.hc = take(s.rows * s.pitch * es);
+  l.part = take(!s.backward && bf ? cdiv(s.piece, 128) * s.rows * 8 : 0);
+  l.g = take(s.backward || !bf ? s.rows * s.piece * es : 0);
+  l.acc = take(s.backward ? s.splits * s.rows * s.pitch * 4 : 0);
+  l.wcopy = take(s.copy_w ? s.piece * s.pitch * 2 : 0);
+  l.descs = take(bf ? 0 : (int64_t)sizeof(GemmDesc) * (s.pieces * (2 + s.splits)));
+  l.total = off;
+  return l;
+}
+
+// CTA pairs of the tensor-core kernel that run at the same time (the grid's size).
+int head_pairs(int sms) {
+  constexpr int kCached = 64;
+  static std::atomic<int> cache[kCached];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  int n = dev < kCached ? cache[dev].load() : 0;
+  if (n > 0) return n;
+  const void* kernels[3] = {(const void*)head_gemm_kernel<kStats>, (const void*)head_gemm_kernel<kGrad>,
+                            (const void*)head_gemm_kernel<kOut>};
+  for (const void* k : kernels)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHeadSmem) !=
+        cudaSuccess)
+      return -1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (sms / 2), 1, 1);
+  cfg.blockDim = dim3(kHeadThreads, 1, 1);
+  cfg.dynamicSmemBytes = kHeadSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel<kOut>, &cfg) != cudaSuccess || n < 1)
+    return -1;
+  if (dev < kCached) cache[dev].store(n);
+  return n;
+}
+
+template <int PHASE>
+cudaError_t launch_head(const HeadArgs& a, int64_t tiles, int pairs, cudaStream_t st) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, pairs)), 1, 1);
+  cfg.blockDim = dim3(kHeadThreads, 1, 1);
+  cfg.dynamicSmemBytes = kHeadSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, head_gemm_kernel<PHASE>, a);
+}
+
+struct HeadCall {
+  HeadShape s;
+  HeadLayout l;
+  char* ws;
+  const void *hidden, *weight, *labels;
+  int64_t ld_h, ld_w, ignore;
+  int32_t index_dtype;
+  float *loss, *lse;                       // forward outputs, nullable
+  const float *lse_in, *dloss;
+  void *dh, *dw;
+  int64_t ld_dh, ld_dw;
+  int sms;
+  int* status;
+  cudaStream_t st;
+
+  template <typename T>
+  T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
+
+  cudaError_t gather() const {
+    GatherArgs a{};
+    a.labels = labels;
+    a.hidden = hidden;
+    a.hc = at<void>(l.hc);
+    a.ld_h = ld_h;
+    a.ignore = ignore;
+    a.n = (int32_t)s.n;
+    a.is64 = index_dtype == MFSDP_INDEX_I64;
+    a.dim = (int32_t)s.dim;
+    a.pitch = (int32_t)s.pitch;
+    a.vocab = (int32_t)s.vocab;
+    a.per = (int32_t)std::max<int64_t>(8, cdiv(s.n, 4ll * sms));
+    a.vec = aligned_to(hidden, 16) && s.dim % 8 == 0 &&
+            (ld_h * (int64_t)dtype_bytes(s.dtype)) % 16 == 0;
+    a.place = s.dtype == MFSDP_DTYPE_F32;
+    a.nlive = at<int32_t>(l.nlive);
+    a.label = at<int32_t>(l.label);
+    a.pos = at<int32_t>(l.pos);
+    a.token = at<int32_t>(l.token);
+    if (s.backward) {
+      a.lse_in = lse_in;
+      a.dloss = dloss;
+      a.lse2 = at<float>(l.lse2);
+      a.dl = at<float>(l.dl);
+    }
+    a.loss = loss;
+    a.lse = lse;
+    a.status = status;
+    const dim3 grid((unsigned)cdiv(s.n, a.per));
+    return s.dtype == MFSDP_DTYPE_BF16
+               ? launch_pdl(head_gather_kernel<bf16_t>, grid, dim3(256), 0, st, a)
+               : launch_pdl(head_gather_kernel<float>, grid, dim3(256), 0, st, a);
+  }
+
+  cudaError_t finish() const {
+    FinishArgs f{};
+    f.acc = at<float>(l.acc);
+    f.pos = at<int32_t>(l.pos);
+    f.dh = dh;
+    f.ld_dh = ld_dh;
+    f.n = (int32_t)s.n;
+    f.dim = (int32_t)s.dim;
+    f.pitch = (int32_t)s.pitch;
+    f.rows = (int32_t)s.rows;
+    f.splits = (int32_t)s.splits;
+    f.vec = aligned_to(dh, 16) && s.dim % 8 == 0 &&
+            (ld_dh * (int64_t)dtype_bytes(s.dtype)) % 16 == 0;
+    return s.dtype == MFSDP_DTYPE_BF16
+               ? launch_pdl(head_finish_kernel<bf16_t>, dim3((unsigned)s.n), dim3(128), 0, st, f)
+               : launch_pdl(head_finish_kernel<float>, dim3((unsigned)s.n), dim3(128), 0, st, f);
+  }
+
+  int run_bf16() const {
+    const int pairs = head_pairs(sms);
+    if (pairs < 1) return MFSDP_ECUDA;
+    HeadArgs a{};
+    const uint16_t* hc = at<uint16_t>(l.hc);
+    bool ok = encode_map(&a.h_k, hc, s.rows, s.pitch, s.pitch, 128u);
+    const void* wsrc = s.copy_w ? (const void*)at<uint16_t>(l.wcopy) : weight;
+    const int64_t wrows = s.copy_w ? s.piece : s.vocab, wld = s.copy_w ? s.pitch : ld_w;
+    ok = ok && encode_map(&a.w_k, wsrc, wrows, s.dim, wld, 128u);
+    if (s.backward) {
+      ok = ok && encode_map3d(&a.h_mn, hc, s.rows, s.pitch, s.pitch);
+      ok = ok && encode_map(&a.w_mn, wsrc, wrows, s.dim, wld, 64u);
+      const uint16_t* g = at<uint16_t>(l.g);
+      ok = ok && encode_map(&a.g_k, g, s.rows, s.piece, s.piece, 128u);
+      ok = ok && encode_map3d(&a.g_mn, g, s.rows, s.piece, s.piece);
+      ok = ok && encode_map(&a.g_st, g, s.rows, s.piece, s.piece, 32u, 32u, false);
+      if (dh) ok = ok && encode_map_f32(&a.acc_st, at<float>(l.acc), s.splits * s.rows, s.pitch, s.pitch, 32u);
+      a.dw_tma = dw && aligned_to(dw, 16) && ld_dw % 8 == 0;
+      if (a.dw_tma) ok = ok && encode_map(&a.dw_st, dw, s.vocab, s.dim, ld_dw, 32u, 32u, false);
+    }
+    if (!ok) return MFSDP_ECUDA;
+    a.nlive = at<int32_t>(l.nlive);
+    a.label = at<int32_t>(l.label);
+    a.lse2 = at<float>(l.lse2);
+    a.dl = at<float>(l.dl);
+    a.part = at<float2>(l.part);
+    a.zlab = at<float>(l.zlab);
+    a.dw = static_cast<uint16_t*>(dw);
+    a.ld_dw = ld_dw;
+    a.dim = (int32_t)s.dim;
+    a.vocab = (int32_t)s.vocab;
+    a.rows = (int32_t)s.rows;
+    a.splits = (int32_t)s.splits;
+    a.want_dh = dh != nullptr;
+    a.want_dw = dw != nullptr;
+    // a group's rows of H (all of its columns) stay within a share of the L2
+    a.group = (int32_t)std::max<int64_t>(4, (32ll << 20) / (kTile * s.pitch * 2));
+    a.wait_limit_ns = wait_limit_ns();
+    a.status = status;
+    const int64_t ntm = cdiv(s.n, kTile), ntd = cdiv(s.dim, kTile);
+    cudaError_t e = gather();
+    for (int64_t i = 0; i < s.pieces && e == cudaSuccess; ++i) {
+      a.v0 = (int32_t)(i * s.piece);
+      a.width = (int32_t)std::min(s.piece, s.vocab - i * s.piece);
+      a.w_row0 = s.copy_w ? 0 : a.v0;
+      a.add = i > 0;
+      if (s.copy_w)
+        e = launch_pdl(head_copy_rows_kernel, dim3((unsigned)up(a.width, kBK)), dim3(256), 0, st,
+                       static_cast<const uint16_t*>(weight) + (int64_t)a.v0 * ld_w, ld_w,
+                       at<uint16_t>(l.wcopy), s.pitch, (int)a.width, (int)s.dim);
+      const int64_t ntn = cdiv(a.width, kTile);
+      if (e != cudaSuccess) break;
+      if (!s.backward) {
+        e = launch_head<kStats>(a, ntm * ntn, pairs, st);
+        if (e != cudaSuccess) break;
+        JoinArgs j{};
+        j.part = a.part;
+        j.state = at<float2>(l.state);
+        j.zlab = a.zlab;
+        j.nlive = a.nlive;
+        j.token = at<int32_t>(l.token);
+        j.loss = loss;
+        j.lse = lse;
+        j.parts = (int32_t)cdiv(a.width, 128);
+        j.rows = a.rows;
+        j.first = i == 0;
+        j.last = i == s.pieces - 1;
+        e = launch_pdl(head_join_kernel, dim3((unsigned)cdiv(s.n, 32)), dim3(1024), 0, st, j);
+      } else {
+        e = launch_head<kGrad>(a, ntm * ntn, pairs, st);
+        if (e != cudaSuccess) break;
+        const int64_t tiles = (dh ? ntm * ntd * s.splits : 0) + (dw ? ntn * ntd : 0);
+        e = launch_head<kOut>(a, tiles, pairs, st);
+      }
+    }
+    if (e == cudaSuccess && dh) e = finish();
+    return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
+  }
+
+  int run_f32() const {
+    // problem tables of every piece: Z, dW, and dH's slices
+    const int64_t per = s.backward ? 2 + s.splits : 1;
+    std::vector<GemmDesc> d((size_t)(s.pieces * per));
+    GemmDesc* dev = at<GemmDesc>(l.descs);
+    const float* hc = at<float>(l.hc);
+    float* z = at<float>(l.g);
+    float* acc = at<float>(l.acc);
+    const float* w = static_cast<const float*>(weight);
+    for (int64_t i = 0; i < s.pieces; ++i) {
+      const int64_t v0 = i * s.piece, width = std::min(s.piece, s.vocab - v0);
+      GemmDesc q{};
+      q.a = hc;
+      q.lda = (int32_t)s.pitch;
+      q.b = w + v0 * ld_w;
+      q.ldb = (int32_t)ld_w;
+      q.c = z;
+      q.ldc = (int32_t)s.piece;
+      q.m = (int32_t)s.n;
+      q.n = (int32_t)width;
+      q.k = (int32_t)s.dim;
+      q.alpha = 1.f;
+      d[(size_t)(i * per)] = q;
+      if (!s.backward) continue;
+      q = GemmDesc{};
+      q.a = z;
+      q.lda = (int32_t)s.piece;
+      q.b = hc;
+      q.ldb = (int32_t)s.pitch;
+      q.c = dw ? static_cast<float*>(dw) + v0 * ld_dw : nullptr;
+      q.ldc = (int32_t)ld_dw;
+      q.m = (int32_t)width;
+      q.n = (int32_t)s.dim;
+      q.k = (int32_t)s.n;
+      q.alpha = 1.f;
+      d[(size_t)(i * per + 1)] = q;
+      for (int64_t k = 0; k < s.splits; ++k) {
+        const int64_t c0 = k * s.kdh, cw = std::min(s.kdh, width - c0);
+        q = GemmDesc{};
+        q.a = z + c0;
+        q.lda = (int32_t)s.piece;
+        q.b = w + (v0 + c0) * ld_w;
+        q.ldb = (int32_t)ld_w;
+        q.c = acc + k * s.rows * s.pitch;
+        q.ldc = (int32_t)s.pitch;
+        q.m = (int32_t)s.n;
+        q.n = (int32_t)s.dim;
+        q.k = (int32_t)std::max<int64_t>(cw, 0);
+        q.alpha = 1.f;
+        q.beta = i > 0 ? 1.f : 0.f;
+        d[(size_t)(i * per + 2 + k)] = q;
+      }
+    }
+    cudaError_t e = cudaSuccess;
+    for (size_t b = 0; b < d.size() && e == cudaSuccess; b += kDescBatch) {
+      DescArgs t{};
+      t.n = (int32_t)std::min<size_t>(kDescBatch, d.size() - b);
+      std::memcpy(t.d, d.data() + b, sizeof(GemmDesc) * (size_t)t.n);
+      t.out = dev + b;
+      e = launch_pdl(head_descs_kernel, dim3(1), dim3(64), 0, st, t);
+    }
+    if (e == cudaSuccess) e = gather();
+    if (e != cudaSuccess) return MFSDP_ECUDA;
+    for (int64_t i = 0; i < s.pieces; ++i) {
+      const int64_t v0 = i * s.piece, width = std::min(s.piece, s.vocab - v0), at0 = i * per;
+      int r = launch_gemm(dev + at0, d.data() + at0, 1, 0, 1, st);
+      if (r != MFSDP_OK) return r;
+      if (!s.backward) {
+        Stats32Args a{};
+        a.z = z;
+        a.state = at<float2>(l.state);
+        a.zlab = at<float>(l.zlab);
+        a.label = at<int32_t>(l.label);
+        a.token = at<int32_t>(l.token);
+        a.loss = loss;
+        a.lse = lse;
+        a.width = (int32_t)width;
+        a.v0 = (int32_t)v0;
+        a.first = i == 0;
+        a.last = i == s.pieces - 1;
+        a.ldz = s.piece;
+        e = launch_pdl(head_stats32_kernel, dim3((unsigned)s.n), dim3(256), 0, st, a);
+        if (e != cudaSuccess) return MFSDP_ECUDA;
+        continue;
+      }
+      Grad32Args a{};
+      a.z = z;
+      a.label = at<int32_t>(l.label);
+      a.lse2 = at<float>(l.lse2);
+      a.dl = at<float>(l.dl);
+      a.width = (int32_t)width;
+      a.v0 = (int32_t)v0;
+      a.ldz = s.piece;
+      e = launch_pdl(head_grad32_kernel, dim3((unsigned)s.n), dim3(256), 0, st, a);
+      if (e != cudaSuccess) return MFSDP_ECUDA;
+      if (dw) {
+        r = launch_gemm(dev + at0 + 1, d.data() + at0 + 1, 1, 1, 0, st);
+        if (r != MFSDP_OK) return r;
+      }
+      if (dh) {
+        r = launch_gemm(dev + at0 + 2, d.data() + at0 + 2, (int)s.splits, 0, 0, st);
+        if (r != MFSDP_OK) return r;
+      }
+    }
+    if (dh) e = finish();
+    return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
+  }
+};
+
+int check_head(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, int64_t ld_w, int64_t piece) {
+  if (!dtype_ok(dtype) || piece < 0) return MFSDP_EINVAL;
+  if (n < 0 || dim < 1 || vocab < 1 || n > (1ll << 28) || dim > (1 << 20) || vocab > (1ll << 30) ||
+      piece > (1ll << 30))
+    return MFSDP_ESHAPE;
+  if (ld_w < dim) return MFSDP_EINVAL;
+  if (ld_w >= (1ll << 31) || cdiv(n, kTile) * cdiv(std::min(piece, vocab), kTile) >= (1ll << 31))
+    return MFSDP_ESHAPE;
+  return MFSDP_OK;
+}
+
+int check_common(int64_t n, int64_t dim, int32_t dtype, const void* hidden, int64_t ld_h,
+                 const void* weight, int32_t index_dtype, const void* labels, const void* ws) {
+  if (index_dtype != MFSDP_INDEX_I32 && index_dtype != MFSDP_INDEX_I64) return MFSDP_EINVAL;
+  if (!weight || !ws || (n > 0 && (!hidden || !labels || ld_h < dim))) return MFSDP_EINVAL;
+  const size_t es = dtype_bytes(dtype);
+  if (!aligned_to(hidden, es) || !aligned_to(weight, es) ||
+      !aligned_to(labels, index_dtype == MFSDP_INDEX_I64 ? 8 : 4) || !aligned_to(ws, 256))
+    return MFSDP_EALIGN;
+  return MFSDP_OK;
+}
+
+}  // namespace
+}  // namespace mfsdp
+
+using namespace mfsdp;
+
+extern "C" int mfsdp_head_loss_workspace_bytes(int64_t n_tokens, int64_t dim, int64_t vocab,
+                                               int32_t dtype, int32_t backward,
+                                               const void* weight, int64_t ld_weight,
+                                               int64_t piece, size_t* bytes_out) {
+  if (!bytes_out) return MFSDP_EINVAL;
+  const int chk = check_head(n_tokens, dim, vocab, dtype, ld_weight, piece);
+  if (chk != MFSDP_OK) return chk;
+  *bytes_out = head_layout(head_shape(n_tokens, dim, vocab, dtype, backward != 0, weight, ld_weight,
+                                      piece, kLayoutSms)).total;
+  return MFSDP_OK;
+}
+
+extern "C" int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vocab,
+                                       int32_t dtype, const void* hidden, int64_t ld_hidden,
+                                       const void* weight, int64_t ld_weight,
+                                       int32_t index_dtype, const void* labels,
+                                       int64_t ignore_index, float* loss, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  int chk = check_head(n_tokens, dim, vocab, dtype, ld_weight, 0);
+  if (chk == MFSDP_OK)
+    chk = check_common(n_tokens, dim, dtype, hidden, ld_hidden, weight, index_dtype, labels, workspace);
+  if (chk != MFSDP_OK) return chk;
+  if (!aligned_to(loss, 4) || !aligned_to(lse, 4)) return MFSDP_EALIGN;
+  HeadCall c{};
+  c.s = head_shape(n_tokens, dim, vocab, dtype, false, weight, ld_weight, 0, kLayoutSms);
+  c.l = head_layout(c.s);
+  if (workspace_bytes < c.l.total) return MFSDP_EWORKSPACE;
+  if (n_tokens == 0) return MFSDP_OK;
+  const int dst = device_sms(&c.sms);
+  if (dst != MFSDP_OK) return dst;
+  c.status = status_word_address();
+  if (!c.status) return MFSDP_ECUDA;
+  c.ws = static_cast<char*>(workspace);
+  c.hidden = hidden;
+  c.weight = weight;
+  c.labels = labels;
+  c.ld_h = ld_hidden;
+  c.ld_w = ld_weight;
+  c.ignore = ignore_index;
+  c.index_dtype = index_dtype;
+  c.loss = loss;
+  c.lse = lse;
+  c.st = static_cast<cudaStream_t>(stream);
+  return dtype == MFSDP_DTYPE_BF16 ? c.run_bf16() : c.run_f32();
+}
+
+extern "C" int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab,
+                                        int32_t dtype, const void* hidden, int64_t ld_hidden,
+                                        const void* weight, int64_t ld_weight,
+                                        int32_t index_dtype, const void* labels,
+                                        int64_t ignore_index, const float* lse,
+                                        const float* dloss, int64_t piece, void* dhidden,
+                                        int64_t ld_dhidden, void* dweight, int64_t ld_dweight,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  int chk = check_head(n_tokens, dim, vocab, dtype, ld_weight, piece);
+  if (chk == MFSDP_OK)
+    chk = check_common(n_tokens, dim, dtype, hidden, ld_hidden, weight, index_dtype, labels, workspace);
+  if (chk != MFSDP_OK) return chk;
+  if (n_tokens > 0 && (!lse || !dloss)) return MFSDP_EINVAL;
+  if ((dhidden && ld_dhidden < dim) || (dweight && ld_dweight < dim)) return MFSDP_EINVAL;
+  if (ld_dweight >= (1ll << 31)) return MFSDP_ESHAPE;
+  const size_t es = dtype_bytes(dtype);
+  if (!aligned_to(lse, 4) || !aligned_to(dloss, 4) || !aligned_to(dhidden, es) ||
+      !aligned_to(dweight, es))
+    return MFSDP_EALIGN;
+  HeadCall c{};
+  c.s = head_shape(n_tokens, dim, vocab, dtype, true, weight, ld_weight, piece, kLayoutSms);
+  c.l = head_layout(c.s);
+  if (workspace_bytes < c.l.total) return MFSDP_EWORKSPACE;
+  if (!dhidden && !dweight) return MFSDP_OK;
+  const int dst = device_sms(&c.sms);
+  if (dst != MFSDP_OK) return dst;
+  c.status = status_word_address();
+  if (!c.status) return MFSDP_ECUDA;
+  c.st = static_cast<cudaStream_t>(stream);
+  if (n_tokens == 0) {   // no tokens: the weight's gradient is zero
+    if (!dweight) return MFSDP_OK;
+    return cudaMemset2DAsync(dweight, (size_t)ld_dweight * es, 0, (size_t)dim * es, (size_t)vocab,
+                             c.st) == cudaSuccess
+               ? MFSDP_OK
+               : MFSDP_ECUDA;
+  }
+  c.ws = static_cast<char*>(workspace);
+  c.hidden = hidden;
+  c.weight = weight;
+  c.labels = labels;
+  c.ld_h = ld_hidden;
+  c.ld_w = ld_weight;
+  c.ignore = ignore_index;
+  c.index_dtype = index_dtype;
+  c.lse_in = lse;
+  c.dloss = dloss;
+  c.dh = dhidden;
+  c.ld_dh = ld_dhidden;
+  c.dw = dweight;
+  c.ld_dw = ld_dweight;
+  return dtype == MFSDP_DTYPE_BF16 ? c.run_bf16() : c.run_f32();
+}

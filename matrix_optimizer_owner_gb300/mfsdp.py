@@ -606,3 +606,70 @@ def mfsdp_embedding_backward(ids, dy, scale: float, dtable, padding_idx: int = -
     _check("mfsdp_embedding_backward", _lib.load().mfsdp_embedding_backward(
         vocab, dim, n, icode, _ptr(ids), padding_idx, scale, dcode, _ptr(dy), ld_dy,
         1 if accumulate else 0, gcode, _ptr(dtable), ld_dt, _ptr(ws), nbytes, _stream(stream)))
+
+
+def mfsdp_head_loss_workspace_bytes(n_tokens: int, dim: int, weight, backward: bool,
+                                    piece: int = 0) -> int:
+    out = C.c_size_t(0)
+    vocab = weight.shape[0]
+    _check("mfsdp_head_loss_workspace_bytes", _lib.load().mfsdp_head_loss_workspace_bytes(
+        n_tokens, dim, vocab, _float_code(weight, "weight"), 1 if backward else 0, _ptr(weight),
+        _matrix(weight, vocab, dim, "weight"), piece, C.byref(out)))
+    return out.value
+
+
+def _head_args(hidden, weight, labels):
+    n, dim = hidden.shape
+    vocab = weight.shape[0]
+    code = _float_code(hidden, "hidden")
+    if weight.dtype != hidden.dtype:
+        raise TypeError(f"weight: expected {hidden.dtype}, got {weight.dtype}")
+    icode = _index_code(labels, "labels")
+    _vector(labels, n, "labels")
+    ld_h, ld_w = _matrix(hidden, n, dim, "hidden"), _matrix(weight, vocab, dim, "weight")
+    return n, dim, vocab, code, icode, ld_h, ld_w
+
+
+def mfsdp_head_loss_forward(hidden, weight, labels, loss, lse, ignore_index: int = -100,
+                            workspace=None, stream=None) -> None:
+    """Per-token softmax cross entropy of ``hidden @ weight.T`` against ``labels`` into ``loss``
+    and the log-sum-exp of the logits into ``lse`` (fp32, either may be None).  Tokens labelled
+    ``ignore_index`` get 0 in both.  ``workspace`` (uint8) defaults to a fresh one."""
+    import torch
+    n, dim, vocab, code, icode, ld_h, ld_w = _head_args(hidden, weight, labels)
+    _vector(loss, n, "loss", torch.float32)
+    _vector(lse, n, "lse", torch.float32)
+    _same_device(hidden, weight, labels, loss, lse, workspace)
+    ws, nbytes = _workspace(workspace, mfsdp_head_loss_workspace_bytes(n, dim, weight, False),
+                            hidden.device, stream)
+    _check("mfsdp_head_loss_forward", _lib.load().mfsdp_head_loss_forward(
+        n, dim, vocab, code, _ptr(hidden), ld_h, _ptr(weight), ld_w, icode, _ptr(labels),
+        ignore_index, _ptr(loss), _ptr(lse), _ptr(ws), nbytes, _stream(stream)))
+
+
+def mfsdp_head_loss_backward(hidden, weight, labels, lse, dloss, dhidden=None, dweight=None,
+                             ignore_index: int = -100, piece: int = 0, workspace=None,
+                             stream=None) -> None:
+    """Gradients of ``sum(dloss * loss)`` for the hidden states and the weight (either may be
+    None), with ``lse`` from the forward pass; the logits are recomputed in pieces of ``piece``
+    columns of the vocabulary (0: chosen)."""
+    import torch
+    n, dim, vocab, code, icode, ld_h, ld_w = _head_args(hidden, weight, labels)
+    _vector(lse, n, "lse", torch.float32)
+    _vector(dloss, n, "dloss", torch.float32)
+    ld_dh = ld_dw = dim
+    for name, t in (("dhidden", dhidden), ("dweight", dweight)):
+        if t is not None and t.dtype != hidden.dtype:
+            raise TypeError(f"{name}: expected {hidden.dtype}, got {t.dtype}")
+    if dhidden is not None:
+        ld_dh = _matrix(dhidden, n, dim, "dhidden")
+    if dweight is not None:
+        ld_dw = _matrix(dweight, vocab, dim, "dweight")
+    _same_device(hidden, weight, labels, lse, dloss, dhidden, dweight, workspace)
+    ws, nbytes = _workspace(workspace,
+                            mfsdp_head_loss_workspace_bytes(n, dim, weight, True, piece),
+                            hidden.device, stream)
+    _check("mfsdp_head_loss_backward", _lib.load().mfsdp_head_loss_backward(
+        n, dim, vocab, code, _ptr(hidden), ld_h, _ptr(weight), ld_w, icode, _ptr(labels),
+        ignore_index, _ptr(lse), _ptr(dloss), piece, _ptr(dhidden), ld_dh, _ptr(dweight), ld_dw,
+        _ptr(ws), nbytes, _stream(stream)))

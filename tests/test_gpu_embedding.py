@@ -2,8 +2,8 @@
 
 Forward is one product and one rounding: equal to the oracle's float64 product rounded to fp32
 (and then to bf16).  Backward, with u = 2^-24: an id of k tokens is a sum of k terms, then one
-product, so |d - ref| <= (k + 2) u scale sum |dy| elementwise, plus half an ulp (2^-9 of the
-result, 2^-8 with the shift of the value) where the gradient is bf16.
+product, so |d - ref| <= (k + 2) u scale sum |dy| elementwise, plus the rounding of a bf16
+gradient (8 significant bits: 2^-8 of it).
 """
 
 import numpy as np

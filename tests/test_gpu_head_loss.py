@@ -1,0 +1,265 @@
+"""mfsdp_head_loss_forward / _backward against the float64 oracle.
+
+Tolerances, elementwise.  A logit is a sum of K products, S = sum |h w|:
+  bf16  the products are exact; the tensor cores add them 16 at a time into fp32 without
+        rounding to nearest: |dz| <= (K / 16 + 8) 2^-22 S
+  fp32  3xTF32: 2^-20 per product and 12 accumulations per block of 32, blocks added in fp32:
+        |dz| <= (2^-18 + K / 32 2^-24) S
+so lse, a weighted mean of the logits' errors, is off by at most max_v |dz| plus the sum's own
+rounding, 2^-18 (1 + |lse|); loss adds |dz| of the label and one rounding.  An entry of G has
+relative error 2 max|dz| + 2^-19 (1 + |z| + |lse|) in its probability and, in bf16, is rounded
+(bf16 holds 8 significant bits: to nearest is within 2^-8 of the value).  The gradients add up
+those errors against the other factor, their own accumulation as above with K = vocab or tokens,
+and a bf16 result's rounding (2^-8 of it).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import head_loss as oracle
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _acc(k, dtype):
+    return (k / 16 + 8) * 2.0 ** -22 if dtype == "bf16" else 2.0 ** -18 + k / 32 * 2.0 ** -24
+
+
+def _mat(rows, cols, dtype, gen, std=1.0, pitch=0, offset=0):
+    base = torch.randn(rows * (cols + pitch) + offset, generator=gen, device="cuda") * std
+    return base.to(TYPES[dtype])[offset:].view(rows, cols + pitch)[:, :cols]
+
+
+def _case(n, dim, vocab, dtype="bf16", ignored=0.2, index=torch.int64, seed=0, pitch=0, offset=0,
+          std=None):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    h = _mat(n, dim, dtype, gen, 1.0, pitch, offset)
+    w = _mat(vocab, dim, dtype, gen, std or 2.0 / dim ** 0.5, pitch, offset)
+    lab = torch.randint(vocab, (n,), generator=gen, device="cuda")
+    lab[torch.rand(n, generator=gen, device="cuda") < ignored] = -100
+    dl = torch.rand(n, generator=gen, device="cuda") / max(n, 1) - 0.3 / max(n, 1)
+    return h, w, lab.to(index), dl
+
+
+def _run(h, w, lab, dl, ignore=-100, piece=0, want=("h", "w"), dh=None, dw=None):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    n = h.shape[0]
+    loss, lse = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    mfsdp.mfsdp_head_loss_forward(h, w, lab, loss, lse, ignore_index=ignore)
+    if dh is None:
+        dh = torch.full(h.shape, float("nan"), dtype=h.dtype, device="cuda")
+    if dw is None:
+        dw = torch.full(w.shape, float("nan"), dtype=w.dtype, device="cuda")
+    mfsdp.mfsdp_head_loss_backward(h, w, lab, lse, dl, dh if "h" in want else None,
+                                   dw if "w" in want else None, ignore_index=ignore, piece=piece)
+    return loss, lse, dh, dw
+
+
+def _verify(h, w, lab, dl, out, ignore=-100):
+    loss, lse, dh, dw = out
+    dtype = "bf16" if h.dtype == torch.bfloat16 else "f32"
+    n, dim = h.shape
+    vocab = w.shape[0]
+    H, W, L, D = _np(h), _np(w), lab.cpu().numpy(), _np(dl)
+    rows = oracle.live_rows(L, vocab, ignore)
+    H[np.setdiff1d(np.arange(n), rows)] = 0.0     # what dropped rows hold does not matter
+    rloss, rlse = oracle.forward(H, W, L, ignore)
+    at = (np.arange(len(rows)), L[rows])
+    dz = _acc(dim, dtype) * (np.abs(H[rows]) @ np.abs(W).T)
+    dlse = dz.max(axis=1) + 2.0 ** -18 * (1 + np.abs(rlse[rows])) if len(rows) else np.zeros(0)
+    z = H[rows] @ W.T
+    dloss_tol = dlse + dz[at] + 2.0 ** -23 * (np.abs(rlse[rows]) + np.abs(z[at]))
+    full = np.zeros(n)
+    full[rows] = dlse
+    assert (np.abs(_np(lse) - rlse) <= full).all()
+    full[rows] = dloss_tol
+    assert (np.abs(_np(loss) - rloss) <= full).all()
+    _, G = oracle.logit_gradient(H, W, L, D, ignore)
+    p = np.exp(z - rlse[rows][:, None])
+    rel = 2 * (dz.max(axis=1) + dlse)[:, None] if len(rows) else 0.0
+    dG = p * np.abs(D[rows])[:, None] * (rel + 2.0 ** -19 * (1 + np.abs(z) + np.abs(rlse[rows])[:, None]))
+    dG = dG + np.abs(G) * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22)
+    rdh, rdw = oracle.backward(H, W, L, D, ignore)
+    aG = np.abs(G) + dG
+    out_round = 2.0 ** -8 if dtype == "bf16" else 0.0
+    tol = np.zeros(H.shape)
+    tol[rows] = dG @ np.abs(W) + _acc(vocab, dtype) * (aG @ np.abs(W))
+    assert (np.abs(_np(dh) - rdh) <= tol + out_round * np.abs(rdh) + 1e-38).all()
+    tol = dG.T @ np.abs(H[rows]) + _acc(n, dtype) * (aG.T @ np.abs(H[rows]))
+    assert (np.abs(_np(dw) - rdw) <= tol + out_round * np.abs(rdw) + 1e-38).all()
+
+
+# tile and k-block boundaries, one token, one column, odd sizes
+@pytest.mark.parametrize("n,dim,vocab", [
+    (1, 64, 1000), (2, 1, 300), (7, 768, 513), (64, 64, 64), (255, 72, 255), (256, 128, 256),
+    (257, 200, 257), (300, 100, 1031), (513, 320, 2049), (3, 1030, 1), (40, 136, 4000),
+    (700, 320, 9001)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sizes(n, dim, vocab, dtype):
+    h, w, lab, dl = _case(n, dim, vocab, dtype, ignored=0.2 if n > 2 else 0.0, seed=n)
+    _verify(h, w, lab, dl, _run(h, w, lab, dl))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("piece", [1, 256, 768, 5000])
+def test_pieces(dtype, piece):
+    h, w, lab, dl = _case(300, 96, 2100, dtype, seed=piece)
+    _verify(h, w, lab, dl, _run(h, w, lab, dl, piece=piece))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pitch,offset", [(8, 0), (8, 8), (3, 0), (0, 1), (5, 3)])
+def test_strides_and_offsets(dtype, pitch, offset):
+    h, w, lab, dl = _case(130, 104, 900, dtype, seed=pitch + offset, pitch=pitch, offset=offset)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dh = _mat(130, 104, dtype, gen, 1.0, pitch, offset)
+    dw = _mat(900, 104, dtype, gen, 1.0, pitch, offset)
+    out = _run(h, w, lab, dl, dh=dh, dw=dw)
+    _verify(h, w, lab, dl, out)
+    # unaligned weights are copied in pieces
+    _verify(h, w, lab, dl, _run(h, w, lab, dl, piece=256))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ignored_tokens(dtype):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    for ignored, index, ignore in ((0.0, torch.int32, -100), (0.97, torch.int64, -100),
+                                   (1.0, torch.int32, -100)):
+        h, w, lab, dl = _case(400, 64, 600, dtype, ignored, index, seed=3)
+        out = _run(h, w, lab, dl, ignore=ignore)
+        _verify(h, w, lab, dl, out, ignore)
+        if ignored == 1.0:
+            assert not any(t.any().item() for t in out)
+    # an ignore index inside the vocabulary, and none in use
+    h, w, lab, dl = _case(200, 64, 20, dtype, 0.0, seed=4)
+    _verify(h, w, lab, dl, _run(h, w, lab, dl, ignore=7), 7)
+    assert mfsdp.mfsdp_query_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dropped_rows_may_hold_anything(dtype):
+    from matrix_optimizer_owner_gb300 import _lib, mfsdp
+    h, w, lab, dl = _case(300, 80, 700, dtype, 0.3, seed=5)
+    drop = lab == -100
+    h[drop] = float("nan")
+    dl[drop] = float("inf")
+    out = _run(h, w, lab, dl)
+    dl[drop] = 0.0
+    _verify(h, w, lab, dl, out)
+    assert mfsdp.mfsdp_query_status() == 0
+    lab[:4] = torch.tensor([700, -1, 1 << 20, 699], device="cuda")
+    h[:4] = 1.0
+    out = _run(h, w, lab, dl)
+    assert _lib.STATUS_NAMES[mfsdp.mfsdp_query_status()] == "MFSDP_EINDEX"
+    _verify(h, w, lab, dl, out)
+    assert not out[0][:3].any() and out[0][3] != 0
+
+
+def test_nan_stays_in_its_token():
+    h, w, lab, dl = _case(300, 64, 500, "bf16", 0.0, seed=6)
+    clean = _run(h, w, lab, dl)
+    h[17, 3] = float("nan")
+    loss, lse, dh, _ = _run(h, w, lab, dl)
+    keep = torch.arange(300, device="cuda") != 17
+    assert loss[17].isnan() and lse[17].isnan() and dh[17].isnan().all()
+    assert torch.equal(loss[keep], clean[0][keep]) and torch.equal(dh[keep], clean[2][keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_logits(dtype):
+    # exp of the raw logits overflows and underflows: thousands on either side
+    h, w, lab, dl = _case(260, 64, 800, dtype, 0.0, seed=7, std=60.0)
+    out = _run(h, w, lab, dl)
+    assert all(torch.isfinite(t).all() for t in out)
+    _verify(h, w, lab, dl, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_gradient_alone_and_repeatable(dtype):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    h, w, lab, dl = _case(310, 192, 1500, dtype, seed=8)
+    loss, lse, dh, dw = _run(h, w, lab, dl, piece=512)
+    for _ in range(2):
+        again = _run(h, w, lab, dl, piece=512)
+        assert all(torch.equal(a, b) for a, b in zip(again, (loss, lse, dh, dw)))
+    assert torch.equal(_run(h, w, lab, dl, piece=512, want="h")[2], dh)
+    assert torch.equal(_run(h, w, lab, dl, piece=512, want="w")[3], dw)
+    mfsdp.mfsdp_head_loss_backward(h, w, lab, lse, dl, piece=512)      # neither: no work
+    only = torch.empty_like(loss)
+    mfsdp.mfsdp_head_loss_forward(h, w, lab, only, None)
+    assert torch.equal(only, loss)
+    inplace = h.clone()
+    mfsdp.mfsdp_head_loss_backward(inplace, w, lab, lse, dl, inplace, piece=512)
+    assert torch.equal(inplace, dh)
+
+
+def test_no_tokens():
+    from matrix_optimizer_owner_gb300 import mfsdp
+    w = torch.randn(300, 48, device="cuda").bfloat16()
+    h = torch.empty(0, 48, dtype=torch.bfloat16, device="cuda")
+    lab, f = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    dw = torch.full_like(w, 5.0)
+    mfsdp.mfsdp_head_loss_forward(h, w, lab, f, f)
+    mfsdp.mfsdp_head_loss_backward(h, w, lab, f, f, h, dw)
+    assert not dw.any()
+
+
+def test_gradient_against_differences():
+    """<dH, v> and <dW, v> against central differences of L = sum dloss loss in fp32, extrapolated
+    from steps s and s / 2.  The extrapolation's error is below the difference of the quotients;
+    the loss's rounding (the tolerance of the forward test) enters each quotient over 2 s."""
+    h, w, lab, dl = _case(20, 40, 300, "f32", 0.2, seed=9)
+    from matrix_optimizer_owner_gb300 import mfsdp
+    _, _, dh, dw = _run(h, w, lab, dl)
+    gen = torch.Generator(device="cuda").manual_seed(10)
+
+    def total(hh, ww):
+        loss = torch.empty(20, device="cuda")
+        mfsdp.mfsdp_head_loss_forward(hh, ww, lab, loss, None)
+        return float((loss.double() * dl.double()).sum())
+
+    S = (np.abs(_np(h)) @ np.abs(_np(w)).T).max(axis=1)
+    per_loss = 2 * (2 * _acc(40, "f32") * S + 2.0 ** -17 * (1 + S))
+    noise = float((per_loss * np.abs(_np(dl))).sum())
+    for base, grad, f in ((h, dh, lambda x: total(x, w)), (w, dw, lambda x: total(h, x))):
+        v = torch.randn(base.shape, generator=gen, device="cuda")
+        quot = [(f(base + s * v) - f(base - s * v)) / (2 * s) for s in (2.0 ** -4, 2.0 ** -5)]
+        want = (4 * quot[1] - quot[0]) / 3
+        got = float((grad.double() * v.double()).sum())
+        assert abs(got - want) <= abs(quot[1] - quot[0]) + 3 * noise * 2 ** 5
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_other_stream_and_graph(dtype):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    h, w, lab, dl = _case(270, 128, 1100, dtype, seed=11)
+    want = _run(h, w, lab, dl, piece=512)
+    out = [torch.zeros_like(t) for t in want]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mfsdp.mfsdp_head_loss_forward(h, w, lab, out[0], out[1], stream=s)
+    mfsdp.mfsdp_head_loss_backward(h, w, lab, out[1], dl, out[2], out[3], piece=512, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    ws = [torch.empty(mfsdp.mfsdp_head_loss_workspace_bytes(270, 128, w, back, 512 if back else 0),
+                      dtype=torch.uint8, device="cuda") for back in (False, True)]
+    for t in out:
+        t.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mfsdp.mfsdp_head_loss_forward(h, w, lab, out[0], out[1], workspace=ws[0])
+        mfsdp.mfsdp_head_loss_backward(h, w, lab, out[1], dl, out[2], out[3], piece=512,
+                                       workspace=ws[1])
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert mfsdp.mfsdp_query_status() == 0

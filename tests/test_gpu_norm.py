@@ -7,8 +7,7 @@ A = (|x| + mean|x|) r, which bounds |z| and carries the error of the mean,
     |dx - dx_ref| <= 64 u r (|g| + mean|g| + A mean(|g| A))
     |dw - dw_ref| <= (64 + rows) u sum |dy| A         (any order of the sum over the rows)
     |db - db_ref| <= (64 + rows) u sum |dy|
-plus half an ulp of the result where it is stored in bf16 (2^-9 of it; 2^-8 covers the shift of
-the value under the first bound).  The backward oracle takes the statistics the kernel wrote.
+plus the rounding of a result that is stored in bf16 (8 significant bits: 2^-8 of it).  The backward oracle takes the statistics the kernel wrote.
 """
 
 import numpy as np

@@ -1,4 +1,4 @@
-"""Host-side checks of the norm and embedding entry points: refusals before any launch, and
+"""Host-side checks of the norm, embedding and head-loss entry points: refusals before any launch, and
 workspace sizes.  Pointers here are made-up addresses that no kernel ever sees."""
 
 import ctypes as C
@@ -107,6 +107,58 @@ def test_embedding_workspace(lib):
     assert lib.mfsdp_embedding_backward_workspace_bytes(1, 64, 5, None) == EINVAL
 
 
+HEAD_FWD = dict(n=5, dim=64, vocab=100, dtype=1, h=P, ld_h=64, w=P, ld_w=64, idtype=1, lab=P,
+                ignore=-100, loss=P, lse=P, ws=P, ws_bytes=1 << 30, stream=None)
+HEAD_BWD = dict(n=5, dim=64, vocab=100, dtype=1, h=P, ld_h=64, w=P, ld_w=64, idtype=1, lab=P,
+                ignore=-100, lse=P, dl=P, piece=0, dh=P, ld_dh=64, dw=P, ld_dw=64, ws=P,
+                ws_bytes=1 << 30, stream=None)
+HEAD_BOTH = [
+    (dict(n=-1), ESHAPE), (dict(dim=0), ESHAPE), (dict(vocab=0), ESHAPE),
+    (dict(vocab=(1 << 30) + 1), ESHAPE), (dict(dtype=2), EINVAL), (dict(idtype=2), EINVAL),
+    (dict(h=None), EINVAL), (dict(w=None), EINVAL), (dict(lab=None), EINVAL),
+    (dict(ws=None), EINVAL), (dict(ld_h=63), EINVAL), (dict(ld_w=63), EINVAL),
+    (dict(h=P + 1), EALIGN), (dict(w=P + 1), EALIGN), (dict(lab=P + 4), EALIGN),
+    (dict(lse=P + 2), EALIGN), (dict(ws=P + 64), EALIGN), (dict(ws_bytes=1024), EWORKSPACE),
+]
+
+
+@pytest.mark.parametrize("change,status", HEAD_BOTH + [
+    (dict(loss=P + 1), EALIGN), (dict(n=0, h=None, lab=None, loss=None, lse=None), 0)])
+def test_head_loss_forward_refusals(lib, change, status):
+    assert _call(lib.mfsdp_head_loss_forward, HEAD_FWD, **change) == status
+
+
+@pytest.mark.parametrize("change,status", HEAD_BOTH + [
+    (dict(piece=-1), EINVAL), (dict(piece=1 << 31), ESHAPE), (dict(lse=None), EINVAL),
+    (dict(dl=None), EINVAL), (dict(ld_dh=1), EINVAL), (dict(ld_dw=1), EINVAL),
+    (dict(dh=P + 1), EALIGN), (dict(dw=P + 1), EALIGN), (dict(dl=P + 1), EALIGN),
+    (dict(dh=None, dw=None), 0)])
+def test_head_loss_backward_refusals(lib, change, status):
+    assert _call(lib.mfsdp_head_loss_backward, HEAD_BWD, **change) == status
+
+
+def test_head_loss_workspace(lib):
+    def need(n, dim, vocab, dtype, backward, w=P, ld=None, piece=0):
+        out = C.c_size_t(0)
+        assert lib.mfsdp_head_loss_workspace_bytes(n, dim, vocab, dtype, backward, w, ld or dim,
+                                                   piece, C.byref(out)) == 0
+        return out.value
+    # the logits of 8192 tokens over 128256 entries would take 2.1 GB in bf16; a piece of the
+    # gradient, the compacted hidden rows and the fp32 sums of dhidden take a fraction
+    assert need(8192, 4096, 128256, 1, 1) < 400 << 20
+    assert need(8192, 4096, 128256, 1, 0) < 150 << 20
+    assert need(8192, 4096, 128256, 1, 1, piece=1024) < need(8192, 4096, 128256, 1, 1)
+    # an unaligned weight adds the copy of one piece
+    assert need(64, 100, 5000, 1, 0, ld=101) > need(64, 100, 5000, 1, 0, ld=104)
+    assert need(64, 100, 5000, 1, 0, w=P + 2, ld=104) > need(64, 100, 5000, 1, 0, ld=104)
+    out = C.c_size_t(0)
+    f = lib.mfsdp_head_loss_workspace_bytes
+    assert f(5, 64, 100, 3, 0, P, 64, 0, C.byref(out)) == EINVAL
+    assert f(5, 64, 100, 1, 0, P, 32, 0, C.byref(out)) == EINVAL
+    assert f(5, 64, 0, 1, 0, P, 64, 0, C.byref(out)) == ESHAPE
+    assert f(5, 64, 100, 1, 0, P, 64, 0, None) == EINVAL
+
+
 def test_binding_refuses_wrong_tensors():
     import torch
 
@@ -129,3 +181,12 @@ def test_binding_refuses_wrong_tensors():
         mfsdp.mfsdp_embedding_forward(table, ids[:3], 1.0, x)
     with pytest.raises(ValueError, match="CUDA device"):
         mfsdp.mfsdp_embedding_backward(ids, x, 1.0, table)
+    lab, f = torch.zeros(4, dtype=torch.int64), torch.zeros(4)
+    with pytest.raises(TypeError):                            # two dtypes
+        mfsdp.mfsdp_head_loss_forward(x, table.bfloat16(), lab, f, f)
+    with pytest.raises(ValueError):                           # widths differ
+        mfsdp.mfsdp_head_loss_forward(x, torch.zeros(10, 9), lab, f, f)
+    with pytest.raises(TypeError):                            # loss not fp32
+        mfsdp.mfsdp_head_loss_forward(x, table, lab, f.double(), f)
+    with pytest.raises(ValueError, match="CUDA device"):
+        mfsdp.mfsdp_head_loss_backward(x, table, lab, f, f, x, table)
