@@ -177,6 +177,13 @@ __device__ __forceinline__ uint32_t stg32_off(int r, int k) {
   return (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4));
 }
 
+// 2^x to about 2 ulp, one instruction (results below 2^-126 are 0): the terms of a softmax sum.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <int PHASE>
 __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid_constant__ HeadArgs P) {
   constexpr int S = kHeadStages;
@@ -341,78 +348,94 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
         float m = -INFINITY, s = 0.f;
-#pragma unroll 1
+        // chunks of this warp with columns (and rows); the next one's load from tensor memory
+        // is in flight while one is reduced
+        const int nq = rw < tiles.live ? min(kHeadChunks, (P.width - cb + 31) / 32) : 0;
+        uint32_t buf[2][32];
+        if (nq > 0) tc_ld32_issue(taddr, buf[0]);
+#pragma unroll
         for (int q = 0; q < kHeadChunks; ++q) {
-          const int c0 = cb + 32 * q;
-          if (c0 >= P.width || rw >= tiles.live) break;   // warp-uniform
-          __syncwarp();
-          uint32_t a32[32];
-          tc_ld32_issue(taddr + (uint32_t)(32 * q), a32);
-          tc_ld_wait(a32);
-          const int left = P.width - c0;                  // columns past the end take no part
-          float mc = -INFINITY;
+          if (q < nq) {                                   // warp-uniform
+            __syncwarp();
+            uint32_t (&a32)[32] = buf[q & 1];
+            tc_ld_wait(a32);
+            if (q + 1 < nq) tc_ld32_issue(taddr + (uint32_t)(32 * (q + 1)), buf[(q + 1) & 1]);
+            const int c0 = cb + 32 * q, left = P.width - c0;
+            if (left < 32) {                              // columns past the end take no part
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (k >= left) a32[k] = __float_as_uint(-INFINITY);
-            mc = fmaxf(mc, __uint_as_float(a32[k]));
+              for (int k = 0; k < 32; ++k)
+                if (k >= left) a32[k] = __float_as_uint(-INFINITY);
+            }
+            float mc = m;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mc = fmaxf(mc, __uint_as_float(a32[k]));
+            if (lab >= c0 && lab < c0 + 32) {
+              uint32_t z = 0u;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) z |= a32[k] & (lab - c0 == k ? 0xFFFFFFFFu : 0u);
+              P.zlab[r] = __uint_as_float(z);
+            }
+            const float ref = mc == -INFINITY ? 0.f : mc * kLog2e;
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              sc[k & 3] += ex2(fmaf(__uint_as_float(a32[k]), kLog2e, -ref));
+            s = fmaf(s, ex2(fmaf(m, kLog2e, -ref)), (sc[0] + sc[1]) + (sc[2] + sc[3]));
+            m = mc;
           }
-          if (live && lab >= c0 && lab < c0 + 32) {
-            float z = 0.f;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) z += lab - c0 == k ? __uint_as_float(a32[k]) : 0.f;
-            P.zlab[r] = z;
-          }
-          const float mn = fmaxf(m, mc), ref = mn == -INFINITY ? 0.f : mn * kLog2e;
-          float sc = 0.f;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) sc += exp2f(fmaf(__uint_as_float(a32[k]), kLog2e, -ref));
-          s = s * exp2f(fmaf(m, kLog2e, -ref)) + sc;
-          m = mn;
         }
         if (live && cb < P.width) P.part[(int64_t)(t.tn * 2 + half) * P.rows + r] = make_float2(m, s);
       } else if (PHASE == kGrad) {
         const bool live = r < tiles.live;
         const int lab = live ? P.label[r] - P.v0 : -1;
-        const float lse2 = live ? P.lse2[r] : 0.f, dl = live ? P.dl[r] : 0.f;
+        // a row that holds no token: exp2(z - inf) = 0
+        const float lse2 = live ? P.lse2[r] : INFINITY, dl = live ? P.dl[r] : 0.f;
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
-#pragma unroll 1
+        // whole k-blocks of G are written: the columns past the end are zero
+        const int nq = min(kHeadChunks, ((P.width + kBK - 1) / kBK * kBK - cb + 31) / 32);
+        uint32_t buf[2][32];
+        if (nq > 0) tc_ld32_issue(taddr, buf[0]);
+#pragma unroll
         for (int q = 0; q < kHeadChunks; ++q) {
-          const int c0 = cb + 32 * q;
-          if (c0 >= (P.width + kBK - 1) / kBK * kBK) break;  // warp-uniform; whole k-blocks of G
-          __syncwarp();
-          uint32_t a32[32];
-          tc_ld32_issue(taddr + (uint32_t)(32 * q), a32);
-          const uint32_t stg = stg0 + (nstore & 1u) * 2048u;
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          __syncwarp();
-          tc_ld_wait(a32);
-          const int left = P.width - c0, hit = lab - c0;
-          uint32_t hw[16];
+          if (q < nq) {                                   // warp-uniform
+            __syncwarp();
+            uint32_t (&a32)[32] = buf[q & 1];
+            const uint32_t stg = stg0 + (nstore & 1u) * 2048u;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+            tc_ld_wait(a32);
+            if (q + 1 < nq) tc_ld32_issue(taddr + (uint32_t)(32 * (q + 1)), buf[(q + 1) & 1]);
+            const int c0 = cb + 32 * q, left = P.width - c0, hit = lab - c0;
+            float v[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float v[2];
+            for (int k = 0; k < 32; ++k) v[k] = ex2(fmaf(__uint_as_float(a32[k]), kLog2e, -lse2));
+            if (__any_sync(0xFFFFFFFFu, hit >= 0 && hit < 32)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = 2 * k + h;
-              const float z = __uint_as_float(a32[c]);
-              float p = exp2f(fmaf(z, kLog2e, -lse2));
-              if (c == hit) p -= 1.f;
-              v[h] = live && c < left ? p * dl : 0.f;
+              for (int k = 0; k < 32; ++k) v[k] = fmaf(v[k], dl, k == hit ? -dl : 0.f);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= dl;
             }
-            hw[k] = pack_bf16x2(v[0], v[1]);
-          }
+            if (left < 32) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            sts128(stg + stg_off(lane, k),
-                   make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]));
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_block(&P.g_st, stg, c0, rw);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              for (int k = 0; k < 32; ++k)
+                if (k >= left) v[k] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sts128(stg + stg_off(lane, k),
+                     make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                pack_bf16x2(v[8 * k + 4], v[8 * k + 5]),
+                                pack_bf16x2(v[8 * k + 6], v[8 * k + 7])));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_block(&P.g_st, stg, c0, rw);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            ++nstore;
           }
-          ++nstore;
         }
       } else {
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
@@ -660,6 +683,146 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const __grid_constant__
   if (p.loss) p.loss[t] = l - p.zlab[r];
 }
 
+// ---------------------------------------------------------------- few tokens
+// One to kFewTokens tokens are bound by reading W once: a matrix product's 256-row tile would
+// be empty but for them.  A warp takes kFewRows rows of W at a time (all their loads in flight
+// together), multiplies them with the tokens' hidden rows, which the block holds in shared
+// memory in fp32, and keeps each token's running (max, sum) in registers.
+constexpr int kFewTokens = 4;
+constexpr int kFewRows = 4;
+constexpr int kFewWarps = 8;
+
+struct FewArgs {
+  const void *hidden, *weight, *labels;
+  int64_t ld_h, ld_w, ignore;
+  float2* part;                            // [blocks][kFewTokens]
+  float* zlab;                             // [kFewTokens]
+  float *loss, *lse;
+  int32_t n, dim, vocab, is64, vec, blocks;
+  int* status;
+};
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(32 * kFewWarps) head_few_kernel(const __grid_constant__ FewArgs p) {
+  extern __shared__ float few_h[];         // [NT][dim rounded up to 8]
+  __shared__ float2 red[kFewWarps][NT];
+  pdl_launch();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int dim8 = (p.dim + 7) / 8 * 8;
+  int lab[NT];
+  float m[NT], s[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t l = t < p.n ? load_index(p.labels, p.is64, t) : p.ignore;
+    lab[t] = l != p.ignore && l >= 0 && l < p.vocab ? (int)l : -1;
+    m[t] = -INFINITY;
+    s[t] = 0.f;
+    const T* h = static_cast<const T*>(p.hidden) + (int64_t)t * p.ld_h;
+    for (int e = threadIdx.x; e < dim8; e += 32 * kFewWarps)
+      few_h[t * dim8 + e] = lab[t] >= 0 && e < p.dim ? to_f32(h[e]) : 0.f;
+  }
+  __syncthreads();
+  const T* w = static_cast<const T*>(p.weight);
+  const int step = gridDim.x * kFewWarps * kFewRows;
+  for (int v0 = (blockIdx.x * kFewWarps + warp) * kFewRows; v0 < p.vocab; v0 += step) {
+    float dot[kFewRows][NT];
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) dot[i][t] = 0.f;
+    if (p.vec) {
+#pragma unroll 4
+      for (int e = lane * 8; e < p.dim; e += 256) {
+        Pack8<T> q[kFewRows];
+#pragma unroll
+        for (int i = 0; i < kFewRows; ++i)
+          q[i].load(w + (int64_t)min(v0 + i, p.vocab - 1) * p.ld_w + e);
+        float x[kFewRows][8];
+#pragma unroll
+        for (int i = 0; i < kFewRows; ++i) q[i].get(x[i]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          Pack8<float> hq;
+          hq.load(few_h + t * dim8 + e);
+          float h[8];
+          hq.get(h);
+#pragma unroll
+          for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dot[i][t] = fmaf(x[i][k], h[k], dot[i][t]);
+        }
+      }
+    } else {
+#pragma unroll 4
+      for (int e = lane; e < p.dim; e += 32) {
+        float x[kFewRows];
+#pragma unroll
+        for (int i = 0; i < kFewRows; ++i)
+          x[i] = to_f32(w[(int64_t)min(v0 + i, p.vocab - 1) * p.ld_w + e]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < kFewRows; ++i) dot[i][t] = fmaf(x[i], few_h[t * dim8 + e], dot[i][t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float mc = m[t];
+#pragma unroll
+      for (int i = 0; i < kFewRows; ++i) {
+        dot[i][t] = v0 + i < p.vocab ? warp_sum(dot[i][t]) : -INFINITY;
+        mc = fmaxf(mc, dot[i][t]);
+        if (lane == 0 && v0 + i == lab[t]) p.zlab[t] = dot[i][t];
+      }
+      const float ref = mc == -INFINITY ? 0.f : mc * kLog2e;
+      s[t] *= ex2(fmaf(m[t], kLog2e, -ref));
+#pragma unroll
+      for (int i = 0; i < kFewRows; ++i) s[t] += ex2(fmaf(dot[i][t], kLog2e, -ref));
+      m[t] = mc;
+    }
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) red[warp][t] = make_float2(m[t], s[t]);
+  __syncthreads();
+  if (threadIdx.x < NT) {
+    float a = -INFINITY, b = 0.f;
+    for (int i = 0; i < kFewWarps; ++i)
+      merge_stats(a, b, red[i][threadIdx.x].x, red[i][threadIdx.x].y);
+    p.part[blockIdx.x * kFewTokens + threadIdx.x] = make_float2(a, b);
+  }
+}
+
+// A warp per token joins the blocks' pairs in a fixed order.
+__global__ void __launch_bounds__(32 * kFewTokens) head_few_join_kernel(const __grid_constant__ FewArgs p) {
+  pdl_launch();
+  pdl_wait();
+  const int t = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (t >= p.n) return;
+  const int64_t lab = load_index(p.labels, p.is64, t);
+  if (lab == p.ignore || lab < 0 || lab >= p.vocab) {
+    if (lane != 0) return;
+    if (lab != p.ignore) atomicOr(p.status, kStatusBadIndex);
+    if (p.loss) p.loss[t] = 0.f;
+    if (p.lse) p.lse[t] = 0.f;
+    return;
+  }
+  float m = -INFINITY, s = 0.f;
+#pragma unroll 8
+  for (int i = lane; i < p.blocks; i += 32) {
+    const float2 v = p.part[i * kFewTokens + t];
+    merge_stats(m, s, v.x, v.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    merge_stats(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+  if (lane != 0) return;
+  const float l = m + logf(s);
+  if (p.lse) p.lse[t] = l;
+  if (p.loss) p.loss[t] = l - p.zlab[t];
+}
+
 // ---------------------------------------------------------------- dH: slices to the caller's rows
 struct FinishArgs {
   const float* acc;                        // [splits][rows][pitch]
@@ -806,6 +969,7 @@ struct HeadShape {
   int64_t n, dim, vocab;
   int32_t dtype;
   bool backward, copy_w;
+  bool few;                                // forward of few tokens: head_few_kernel
   int64_t rows, pitch;                     // compacted H (and dH slices)
   int64_t piece, pieces;                   // columns per piece
   int64_t splits;                          // dH slices
@@ -816,13 +980,15 @@ struct HeadLayout {
   size_t nlive, label, pos, token, lse2, dl, zlab, state, hc, part, g, acc, wcopy, descs, total;
 };
 
-constexpr int64_t kGElems = 64ll << 20;    // entries of G (or of Z) per piece
+constexpr int64_t kGElems = 96ll << 20;    // entries of G (or of Z) per piece
 constexpr int64_t kPartBytes = 64ll << 20; // bytes of the forward partials per piece
+constexpr int64_t kSliceBytes = 64ll << 20;   // bytes of dH's slices beyond the first
 constexpr int kMaxSplits = 64;
+constexpr int kFewBlocks = 1024;           // blocks of the few-token kernel (bounds its workspace)
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
 
-// Columns per piece: about 64 Mi entries, whole tiles, at least 4096 columns.  Wider pieces mean
-// fewer launches and fewer passes over dH's sums; narrower ones a smaller workspace.
+// Columns per piece: whole tiles, at least 4096 columns, at most about kGElems entries.  Wider
+// pieces mean fewer launches and fewer passes over dH's sums; narrower ones a smaller workspace.
 int64_t piece_columns(const HeadShape& s, int64_t asked) {
   int64_t c;
   if (asked > 0)
@@ -837,6 +1003,32 @@ int64_t piece_columns(const HeadShape& s, int64_t asked) {
   return std::min(c, up(s.vocab, kTile));
 }
 
+// Modelled time of the backward pass, in k-blocks of a pair: the waves of the logits' tiles, and
+// the longer of the two kinds of pairs in TileList's order for the products (kLaunchCost per
+// launch: its ramp and its last epilogue).
+constexpr int64_t kLaunchCost = 12;
+double model_time(const HeadShape& s, int64_t piece, int64_t splits, int64_t pairs) {
+  const int64_t ntm = cdiv(s.n, kTile), ntd = cdiv(s.dim, kTile), kd = cdiv(s.dim, kBK);
+  const int64_t kn = cdiv(s.n, kBK);
+  auto one = [&](int64_t width) -> int64_t {
+    const int64_t ntn = cdiv(width, kTile);
+    const int64_t kdh = cdiv(cdiv(width, kBK), splits);
+    int64_t n1 = ntm * ntd * splits, k1 = kdh, n2 = ntn * ntd, k2 = kn;
+    if (k1 < k2) {
+      std::swap(n1, n2);
+      std::swap(k1, k2);
+    }
+    const int64_t r = n1 % pairs, late = pairs - r;
+    const int64_t e = r ? std::min((k1 + k2 / 2) / k2, n2 / late) : 0;
+    const int64_t rest = n2 - (r ? late * e : 0), full = rest / pairs, rem = rest % pairs;
+    int64_t t = n1 / pairs * k1 + (e + full + (rem > 0)) * k2;
+    if (r) t = std::max(t, (n1 / pairs + 1) * k1 + (full + (rem > late)) * k2);
+    return cdiv(ntm * ntn, pairs) * kd + t + 2 * kLaunchCost;
+  };
+  const int64_t whole = s.vocab / piece, last = s.vocab % piece;
+  return (double)(whole * one(piece) + (last ? one(last) : 0));
+}
+
 HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool backward,
                      const void* weight, int64_t ld_w, int64_t piece, int sms) {
   HeadShape s{};
@@ -846,7 +1038,9 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   s.dtype = dtype;
   s.backward = backward;
   const bool bf = dtype == MFSDP_DTYPE_BF16;
-  s.copy_w = bf && (!aligned_to(weight, 16) || ld_w % 8 != 0);
+  // the tokens' hidden rows have to fit in shared memory
+  s.few = !backward && n <= kFewTokens && up(dim, 8) * 4 * kFewTokens <= (200 << 10);
+  s.copy_w = bf && !s.few && (!aligned_to(weight, 16) || ld_w % 8 != 0);
   s.rows = up(std::max<int64_t>(n, 1), kTile);
   s.pitch = up(dim, 64);
   s.piece = piece_columns(s, piece);
@@ -857,10 +1051,31 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
     // until the tiles fill the GPU; a slice keeps at least 1024 columns
     const int64_t units = bf ? sms / 2 : sms;
     const int64_t tiles = cdiv(std::max<int64_t>(n, 1), bf ? kTile : 128) * cdiv(dim, kTile);
-    const int64_t want = cdiv(units, tiles), most = std::max<int64_t>(1, s.piece / 1024);
-    s.splits = std::max<int64_t>(1, std::min({want, most, (int64_t)kMaxSplits}));
-    s.kdh = up(cdiv(s.piece, s.splits), 64);
-    s.splits = cdiv(s.piece, s.kdh);
+    auto cut = [&](int64_t splits) {
+      splits = std::max<int64_t>(1, std::min({splits, s.piece / 1024, (int64_t)kMaxSplits}));
+      s.kdh = up(cdiv(s.piece, splits), kBK);
+      s.splits = cdiv(s.piece, s.kdh);
+    };
+    cut(cdiv(units, tiles));
+    if (bf && piece == 0 && s.pieces > 1) {
+      // several pieces: the launches' last waves cost most where tiles are few, so take the
+      // piece (down to half of the largest) and the cut of dH with the least modelled time
+      const int64_t most = s.piece;
+      double best = 0;
+      int64_t best_piece = s.piece, best_splits = 1;
+      for (int64_t c = most; c >= std::max<int64_t>(most / 2, kTile); c -= kTile)
+        for (int64_t k = 1; k <= 4 && (k - 1) * s.rows * s.pitch * 4 <= kSliceBytes; ++k) {
+          const double t = model_time(s, c, k, units);
+          if (best == 0 || t < best) {
+            best = t;
+            best_piece = c;
+            best_splits = k;
+          }
+        }
+      s.piece = best_piece;
+      s.pieces = cdiv(vocab, s.piece);
+      cut(best_splits);
+    }
   }
   return s;
 }
@@ -868,6 +1083,7 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
 HeadLayout head_layout(const HeadShape& s) {
   HeadLayout l{};
   size_t off = 0;
+  // (the few-token kernel needs its partials and the labels' logits only)
   auto take = [&](int64_t bytes) {
     const size_t at = off;
     off += (size_t)up(bytes, 1024);
@@ -875,6 +1091,12 @@ HeadLayout head_layout(const HeadShape& s) {
   };
   const bool bf = s.dtype == MFSDP_DTYPE_BF16;
   const int64_t es = bf ? 2 : 4;
+  if (s.few) {
+    l.zlab = take(kFewTokens * 4);
+    l.part = take(kFewBlocks * kFewTokens * 8);
+    l.total = off;
+    return l;
+  }
   l.nlive = take(4);
   l.label = take(s.rows * 4);
   l.pos = take(s.rows * 4);
@@ -1012,6 +1234,54 @@ struct HeadCall {
     return s.dtype == MFSDP_DTYPE_BF16
                ? launch_pdl(head_finish_kernel<bf16_t>, dim3((unsigned)s.n), dim3(128), 0, st, f)
                : launch_pdl(head_finish_kernel<float>, dim3((unsigned)s.n), dim3(128), 0, st, f);
+  }
+
+  template <typename T, int NT>
+  cudaError_t launch_few(const FewArgs& a, size_t smem) const {
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          head_few_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(head_few_kernel<T, NT>, dim3((unsigned)a.blocks), dim3(32 * kFewWarps), smem, st,
+                      a);
+  }
+
+  // The forward pass of few tokens (few_tokens() of the shape).
+  int run_few() const {
+    FewArgs a{};
+    a.hidden = hidden;
+    a.weight = weight;
+    a.labels = labels;
+    a.ld_h = ld_h;
+    a.ld_w = ld_w;
+    a.ignore = ignore;
+    a.part = at<float2>(l.part);
+    a.zlab = at<float>(l.zlab);
+    a.loss = loss;
+    a.lse = lse;
+    a.n = (int32_t)s.n;
+    a.dim = (int32_t)s.dim;
+    a.vocab = (int32_t)s.vocab;
+    a.is64 = index_dtype == MFSDP_INDEX_I64;
+    a.vec = aligned_to(weight, 16) && s.dim % 8 == 0 &&
+            (ld_w * (int64_t)dtype_bytes(s.dtype)) % 16 == 0;
+    a.status = status;
+    const int nt = s.n == 1 ? 1 : s.n == 2 ? 2 : 4;
+    const size_t smem = (size_t)up(s.dim, 8) * 4 * nt;
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(4, (200 << 10) / (int64_t)smem));
+    a.blocks = (int32_t)std::min<int64_t>(std::min(per_sm * sms, (int64_t)kFewBlocks),
+                                          cdiv(s.vocab, kFewWarps * kFewRows));
+    cudaError_t e;
+    if (s.dtype == MFSDP_DTYPE_BF16)
+      e = nt == 1 ? launch_few<bf16_t, 1>(a, smem)
+          : nt == 2 ? launch_few<bf16_t, 2>(a, smem) : launch_few<bf16_t, 4>(a, smem);
+    else
+      e = nt == 1 ? launch_few<float, 1>(a, smem)
+          : nt == 2 ? launch_few<float, 2>(a, smem) : launch_few<float, 4>(a, smem);
+    if (e == cudaSuccess)
+      e = launch_pdl(head_few_join_kernel, dim3(1), dim3(32 * kFewTokens), 0, st, a);
+    return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
   }
 
   int run_bf16() const {
@@ -1272,6 +1542,7 @@ extern "C" int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vo
   c.loss = loss;
   c.lse = lse;
   c.st = static_cast<cudaStream_t>(stream);
+  if (c.s.few) return c.run_few();
   return dtype == MFSDP_DTYPE_BF16 ? c.run_bf16() : c.run_f32();
 }
 

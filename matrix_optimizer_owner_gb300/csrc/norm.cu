@@ -8,10 +8,12 @@
 //
 // Both directions are bound by memory: forward moves 2 and backward 3 values per element.
 // Rows of up to 1024 elements take a warp each (no block barrier; 8 rows in flight per block),
-// longer ones a block each with at most 32 elements per thread; rows beyond 32768 elements are
+// longer ones a block each with at most 32 elements per thread; rows beyond 16384 elements are
 // read in passes.  Backward keeps every column's dw and db sums in registers over the rows a
 // block walks; the blocks' sums go to the workspace and a second launch adds them in block
 // order: no atomics, the result does not depend on timing.
+#include <algorithm>
+
 #include "elem.cuh"
 #include "mfsdp.h"
 
@@ -21,7 +23,7 @@ namespace {
 constexpr int kNormWarps = 8;         // warps per block of the warp-per-row kernels
 constexpr int kWarpRowMax = 1024;     // longest row one warp takes
 constexpr int kMaxChunks = 4;         // 8-element chunks per thread
-constexpr int kRegRowMax = 1024 * 8 * kMaxChunks;
+constexpr int kRegRowMax = 512 * 8 * kMaxChunks;
 
 struct NormArgs {
   int64_t rows, cols;
@@ -34,6 +36,7 @@ struct NormArgs {
   float* partials;            // [blocks][2][cols]
   float eps, inv_n;
   int layer, wbf16, has_dw, has_db;
+  int pvec;                   // the parameters start on 16-byte boundaries
 };
 
 __device__ __forceinline__ float load_param(const void* p, int is_bf16, int64_t e) {
@@ -48,22 +51,6 @@ __device__ __forceinline__ int64_t elem_of(int t, int k, int j) {
 }
 
 template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ void load_chunk(const T* row, int64_t n, int t, int k, float (&v)[8]) {
-  if (VEC) {
-    const int64_t e = elem_of<TPR, VEC>(t, k, 0);
-    Pack8<T> p;
-    if (e < n) p.load(row + e); else p.zero();
-    p.get(v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = elem_of<TPR, VEC>(t, k, j);
-      v[j] = e < n ? to_f32(row[e]) : 0.f;
-    }
-  }
-}
-
-template <typename T, int TPR, bool VEC>
 __device__ __forceinline__ void store_chunk(T* row, int64_t n, int t, int k, const float (&v)[8]) {
   if (VEC) {
     const int64_t e = elem_of<TPR, VEC>(t, k, 0);
@@ -75,6 +62,64 @@ __device__ __forceinline__ void store_chunk(T* row, int64_t n, int t, int k, con
     for (int j = 0; j < 8; ++j) {
       const int64_t e = elem_of<TPR, VEC>(t, k, j);
       if (e < n) row[e] = from_f32<T>(v[j]);
+    }
+  }
+}
+
+// A thread's share of a row as it lies in memory, so that the next row's loads are in flight
+// while this row is worked on.
+template <typename T, int TPR, int K, bool VEC>
+struct RowChunks {
+  Pack8<T> p[VEC ? K : 1];
+  T e[VEC ? 1 : K][8];
+  __device__ __forceinline__ void load(const T* row, int64_t n, int t) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (VEC) {
+        const int64_t c = elem_of<TPR, VEC>(t, k, 0);
+        if (c < n) p[VEC ? k : 0].load(row + c); else p[VEC ? k : 0].zero();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t c = elem_of<TPR, VEC>(t, k, j);
+          e[VEC ? 0 : k][j] = c < n ? row[c] : from_f32<T>(0.f);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int k, float (&v)[8]) const {
+    if (VEC) {
+      p[VEC ? k : 0].get(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = to_f32(e[VEC ? 0 : k][j]);
+    }
+  }
+};
+
+// The parameters of a thread's columns (`fill` where there are none).
+template <int TPR, int K, bool VEC>
+__device__ __forceinline__ void load_params(const void* src, int is_bf16, int pvec, int64_t n, int t,
+                                            float fill, float (&v)[K][8]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int64_t c = elem_of<TPR, VEC>(t, k, 0);
+    if (VEC && src && pvec && c < n) {
+      if (is_bf16) {
+        Pack8<bf16_t> q;
+        q.load(static_cast<const bf16_t*>(src) + c);
+        q.get(v[k]);
+      } else {
+        Pack8<float> q;
+        q.load(static_cast<const float*>(src) + c);
+        q.get(v[k]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t e = elem_of<TPR, VEC>(t, k, j);
+        v[k][j] = src && e < n ? load_param(src, is_bf16, e) : fill;
+      }
     }
   }
 }
@@ -106,54 +151,58 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* red, int& tu
 template <typename T, int TPR, int K, bool VEC>
 __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
     norm_forward_kernel(const __grid_constant__ NormArgs p) {
+  constexpr int kRowsPerBlock = TPR == 32 ? kNormWarps : 1;
   __shared__ float red[TPR == 32 ? 1 : 4 * (TPR / 32)];
   pdl_launch();
   pdl_wait();
   const int t = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
-  const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5)
-                                : (int64_t)blockIdx.x;
-  if (row >= p.rows) return;  // whole warps (or the whole block) leave
+  const int64_t step = (int64_t)gridDim.x * kRowsPerBlock;
+  int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + (TPR == 32 ? (threadIdx.x >> 5) : 0);
   int turn = 0;
-  const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
-  float v[K][8];
-  float s = 0.f, zero = 0.f;
+  RowChunks<T, TPR, K, VEC> cur, nxt;
+  if (row < p.rows) cur.load(static_cast<const T*>(p.x) + row * p.ld_x, p.cols, t);
+  float w[K][8], b[K][8];
+  load_params<TPR, K, VEC>(p.w, p.wbf16, p.pvec, p.cols, t, 1.f, w);
+  load_params<TPR, K, VEC>(p.b, p.wbf16, p.pvec, p.cols, t, 0.f, b);
+  for (; row < p.rows; row += step) {     // whole warps (or the whole block) stay together
+    if (row + step < p.rows)
+      nxt.load(static_cast<const T*>(p.x) + (row + step) * p.ld_x, p.cols, t);
+    float v[K][8];
+    float s = 0.f, zero = 0.f;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    load_chunk<T, TPR, VEC>(xr, p.cols, t, k, v[k]);
+    for (int k = 0; k < K; ++k) {
+      cur.get(k, v[k]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += v[k][j];
-  }
-  float mu = 0.f;
-  if (p.layer) {
-    row_sum2<TPR>(s, zero, red, turn);
-    mu = s * p.inv_n;
-  }
-  float q = 0.f;
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float d = elem_of<TPR, VEC>(t, k, j) < p.cols ? v[k][j] - mu : 0.f;
-      q = fmaf(d, d, q);
+      for (int j = 0; j < 8; ++j) s += v[k][j];
     }
-  zero = 0.f;
-  row_sum2<TPR>(q, zero, red, turn);
-  const float r = rsqrtf(fmaf(q, p.inv_n, p.eps));
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mu;
-    if (p.rstd) p.rstd[row] = r;
-  }
-  T* yr = static_cast<T*>(p.y) + row * p.ld_y;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = elem_of<TPR, VEC>(t, k, j);
-      const float w = p.w && e < p.cols ? load_param(p.w, p.wbf16, e) : 1.f;
-      const float b = p.b && e < p.cols ? load_param(p.b, p.wbf16, e) : 0.f;
-      v[k][j] = fmaf((v[k][j] - mu) * r, w, b);
+    float mu = 0.f;
+    if (p.layer) {
+      row_sum2<TPR>(s, zero, red, turn);
+      mu = s * p.inv_n;
     }
-    store_chunk<T, TPR, VEC>(yr, p.cols, t, k, v[k]);
+    float q = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = elem_of<TPR, VEC>(t, k, j) < p.cols ? v[k][j] - mu : 0.f;
+        q = fmaf(d, d, q);
+      }
+    zero = 0.f;
+    row_sum2<TPR>(q, zero, red, turn);
+    const float r = rsqrtf(fmaf(q, p.inv_n, p.eps));
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mu;
+      if (p.rstd) p.rstd[row] = r;
+    }
+    T* yr = static_cast<T*>(p.y) + row * p.ld_y;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = fmaf((v[k][j] - mu) * r, w[k][j], b[k][j]);
+      store_chunk<T, TPR, VEC>(yr, p.cols, t, k, v[k]);
+    }
+    cur = nxt;
   }
 }
 
@@ -195,9 +244,12 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const __grid_co
 
 // ---------------------------------------------------------------- backward
 template <typename T, int TPR, int K, bool VEC>
-__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR,
+                                  TPR > 32 && K <= 2 ? 512 / TPR : 1)
     norm_backward_kernel(const __grid_constant__ NormArgs p) {
   constexpr int kRowsPerBlock = TPR == 32 ? kNormWarps : 1;
+  // the next row is loaded ahead where its raw values fit in registers beside this row's
+  constexpr bool kAhead = sizeof(T) * K <= 8;
   __shared__ float red[TPR == 32 ? 1 : 4 * (TPR / 32)];
   __shared__ float comb[TPR == 32 ? kNormWarps * 32 * 8 : 1];
   pdl_launch();
@@ -205,27 +257,31 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
   const int t = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
   const int sub = TPR == 32 ? (threadIdx.x >> 5) : 0;
   int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * kRowsPerBlock;
+  int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + sub;
+  using Chunks = RowChunks<T, TPR, K, VEC>;
+  Chunks xc, gc, xn, gn;
+  auto load_row = [&](Chunks& x, Chunks& g, int64_t i) {
+    x.load(static_cast<const T*>(p.x) + i * p.ld_x, p.cols, t);
+    g.load(static_cast<const T*>(p.dy) + i * p.ld_dy, p.cols, t);
+  };
+  if (row < p.rows) load_row(xc, gc, row);
   float aw[K][8], ab[K][8], w[K][8];
+  load_params<TPR, K, VEC>(p.w, p.wbf16, p.pvec, p.cols, t, 1.f, w);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = elem_of<TPR, VEC>(t, k, j);
-      w[k][j] = p.w && e < p.cols ? load_param(p.w, p.wbf16, e) : 1.f;
-      aw[k][j] = ab[k][j] = 0.f;
-    }
-  for (int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + sub; row < p.rows;
-       row += (int64_t)gridDim.x * kRowsPerBlock) {
-    const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
-    const T* gr = static_cast<const T*>(p.dy) + row * p.ld_dy;
+    for (int j = 0; j < 8; ++j) aw[k][j] = ab[k][j] = 0.f;
+  for (; row < p.rows; row += step) {
+    if (kAhead && row + step < p.rows) load_row(xn, gn, row + step);
     T* dr = static_cast<T*>(p.dx) + row * p.ld_dx;
     const float r = p.rstd_in[row], mu = p.layer ? p.mean_in[row] : 0.f;
     float z[K][8], g[K][8];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      load_chunk<T, TPR, VEC>(xr, p.cols, t, k, z[k]);
-      load_chunk<T, TPR, VEC>(gr, p.cols, t, k, g[k]);
+      xc.get(k, z[k]);
+      gc.get(k, g[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {   // past the row's end dy is 0: no contribution
         z[k][j] = (z[k][j] - mu) * r;
@@ -244,6 +300,12 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[k][j] = (g[k][j] - s1 - z[k][j] * s2) * r;
       store_chunk<T, TPR, VEC>(dr, p.cols, t, k, g[k]);
+    }
+    if (kAhead) {
+      xc = xn;
+      gc = gn;
+    } else if (row + step < p.rows) {
+      load_row(xc, gc, row + step);
     }
   }
   // this block's column sums, its warps added in warp order
@@ -311,33 +373,31 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const __grid_c
   }
 }
 
-// Adds the blocks' column sums in block order: 32 columns per block, eight groups of rows
-// whose sums are added in group order.
+// Adds the blocks' column sums in block order: 32 columns of dw (blockIdx.y = 0) or db (1) per
+// block, 32 groups of consecutive blocks whose sums are added in group order.
 template <typename P>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     norm_param_grad_kernel(const float* partials, int blocks, int64_t cols, P* dw, P* db) {
-  __shared__ float s[8][33];
+  __shared__ float s[32][33];
   pdl_launch();
   pdl_wait();
-  const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5, h = blockIdx.y;
+  P* out = h == 0 ? dw : db;
+  if (!out) return;
   const int64_t e = (int64_t)blockIdx.x * 32 + c;
-  for (int h = 0; h < 2; ++h) {
-    P* out = h == 0 ? dw : db;
-    if (!out) continue;
-    const int per = (blocks + 7) / 8, b0 = g * per, b1 = min(blocks, b0 + per);
-    float a = 0.f;
-    if (e < cols)
-      for (int b = b0; b < b1; ++b) a += partials[((int64_t)b * 2 + h) * cols + e];
-    s[g][c] = a;
-    __syncthreads();
-    if (g == 0 && e < cols) {
-      float v = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v += s[i][c];
-      out[e] = from_f32<P>(v);
-    }
-    __syncthreads();
+  const int per = (blocks + 31) / 32, b0 = g * per, b1 = min(blocks, b0 + per);
+  float a = 0.f;
+  if (e < cols) {
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) a += partials[((int64_t)b * 2 + h) * cols + e];
   }
+  s[g][c] = a;
+  __syncthreads();
+  if (g != 0 || e >= cols) return;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v += s[i][c];
+  out[e] = from_f32<P>(v);
 }
 
 // ---------------------------------------------------------------- dispatch
@@ -356,20 +416,32 @@ cudaError_t by_shape(int64_t cols, F&& f) {
   if (cols <= 2048) return f.template operator()<T, 128, 2, VEC>();
   if (cols <= 4096) return f.template operator()<T, 256, 2, VEC>();
   if (cols <= 8192) return f.template operator()<T, 512, 2, VEC>();
-  if (cols <= 16384) return f.template operator()<T, 512, 4, VEC>();
-  return f.template operator()<T, 1024, 4, VEC>();
+  return f.template operator()<T, 512, 4, VEC>();
 #undef MFSDP_NORM_K
+}
+
+// Blocks of a kernel that an SM holds (at least 1).
+template <typename K>
+int resident(K kernel, int threads) {
+  int occ = 0;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0) == cudaSuccess &&
+                 occ > 0
+             ? occ
+             : 1;
 }
 
 struct FwdLaunch {
   const NormArgs& a;
+  int sms;
   cudaStream_t st;
   template <typename T, int TPR, int K, bool VEC>
   cudaError_t operator()() const {
-    const int64_t per = TPR == 32 ? kNormWarps : 1;
-    return launch_pdl(norm_forward_kernel<T, TPR, K, VEC>,
-                      dim3((unsigned)((a.rows + per - 1) / per)),
-                      dim3(TPR == 32 ? 32 * kNormWarps : TPR), 0, st, a);
+    const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
+    static const int occ = resident(norm_forward_kernel<T, TPR, K, VEC>, threads);
+    const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
+    const int64_t g = std::min<int64_t>((int64_t)sms * occ, need);
+    return launch_pdl(norm_forward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), 0, st,
+                      a);
   }
 };
 
@@ -381,14 +453,9 @@ struct BwdLaunch {
   template <typename T, int TPR, int K, bool VEC>
   cudaError_t operator()() const {
     const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
-    int occ = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &occ, norm_backward_kernel<T, TPR, K, VEC>, threads, 0);
-    if (e != cudaSuccess) return e;
+    static const int occ = resident(norm_backward_kernel<T, TPR, K, VEC>, threads);
     const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
-    int64_t g = (int64_t)sms * (occ < 1 ? 1 : occ);
-    if (g > max_blocks) g = max_blocks;
-    if (g > need) g = need;
+    const int64_t g = std::min({(int64_t)sms * occ, (int64_t)max_blocks, need});
     *blocks = (int)g;
     return launch_pdl(norm_backward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), 0,
                       st, a);
@@ -450,6 +517,7 @@ extern "C" int mfsdp_norm_forward(int32_t kind, int64_t rows, int64_t cols, int3
   a.inv_n = (float)(1.0 / (double)cols);
   a.layer = kind == MFSDP_NORM_LAYER;
   a.wbf16 = param_dtype == MFSDP_DTYPE_BF16;
+  a.pvec = aligned_to(weight, 16) && aligned_to(bias, 16);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cols > kRegRowMax) {
@@ -458,7 +526,7 @@ extern "C" int mfsdp_norm_forward(int32_t kind, int64_t rows, int64_t cols, int3
             : launch_pdl(norm_forward_long_kernel<float>, dim3((unsigned)rows), dim3(1024), 0, st, a);
   } else {
     const bool vec = rows_vec(x, ld_x, cols, dtype) && rows_vec(y, ld_y, cols, dtype);
-    const FwdLaunch f{a, st};
+    const FwdLaunch f{a, sms, st};
     if (dtype == MFSDP_DTYPE_BF16)
       e = vec ? by_shape<bf16_t, true>(cols, f) : by_shape<bf16_t, false>(cols, f);
     else
@@ -514,6 +582,7 @@ extern "C" int mfsdp_norm_backward(int32_t kind, int64_t rows, int64_t cols, int
   a.inv_n = (float)(1.0 / (double)cols);
   a.layer = kind == MFSDP_NORM_LAYER;
   a.wbf16 = param_dtype == MFSDP_DTYPE_BF16;
+  a.pvec = aligned_to(weight, 16);
   a.has_dw = dweight != nullptr;
   a.has_db = dbias != nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -536,11 +605,11 @@ extern "C" int mfsdp_norm_backward(int32_t kind, int64_t rows, int64_t cols, int
     }
   }
   if (e == cudaSuccess && (dweight || dbias)) {
-    const dim3 grid((unsigned)((cols + 31) / 32));
+    const dim3 grid((unsigned)((cols + 31) / 32), 2);
     e = param_dtype == MFSDP_DTYPE_BF16
-            ? launch_pdl(norm_param_grad_kernel<bf16_t>, grid, dim3(256), 0, st, a.partials,
+            ? launch_pdl(norm_param_grad_kernel<bf16_t>, grid, dim3(1024), 0, st, a.partials,
                          blocks, cols, static_cast<bf16_t*>(dweight), static_cast<bf16_t*>(dbias))
-            : launch_pdl(norm_param_grad_kernel<float>, grid, dim3(256), 0, st, a.partials,
+            : launch_pdl(norm_param_grad_kernel<float>, grid, dim3(1024), 0, st, a.partials,
                          blocks, cols, static_cast<float*>(dweight), static_cast<float*>(dbias));
   }
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;

@@ -9,6 +9,7 @@ non-zero status.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import Optional, Sequence, Tuple
 
 from . import _lib
@@ -44,6 +45,9 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # a tenth of the time of building a Stream object
+            return raw(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
@@ -445,71 +449,103 @@ def mfsdp_gemm_f32_batched(problems, trans_a: bool = False, trans_b: bool = Fals
 
 
 # ------------------------------------------------------------------------------- operators
-def _matrix(t, rows: int, cols: int, name: str) -> int:
-    """Pitch of a rows x cols tensor with unit column stride."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name}: expected a {rows} x {cols} tensor, got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: expected unit column stride, got strides {t.stride()}")
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+# A call on a small tensor is bound by the time spent here, so the checks are plain comparisons.
+_FLOAT_CODES, _INDEX_CODES = {}, {}
 
 
-def _vector(t, n: int, name: str, dtype=None) -> None:
-    if t is None:
-        return
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-
-
-def _index_code(t, name: str) -> int:
+def _learn_dtypes() -> None:
     import torch
-    if t.dtype == torch.int64:
-        return INDEX_I64
-    if t.dtype == torch.int32:
-        return INDEX_I32
-    raise TypeError(f"{name}: expected int32 or int64, got {t.dtype}")
+    _FLOAT_CODES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
+    _INDEX_CODES.update({torch.int32: INDEX_I32, torch.int64: INDEX_I64})
 
 
 def _float_code(t, name: str) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    if t.dtype == torch.float32:
-        return DTYPE_F32
-    raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    if not _FLOAT_CODES:
+        _learn_dtypes()
+    code = _FLOAT_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return code
 
 
-def _same_device(*tensors) -> None:
-    """Every tensor on the current CUDA device (a host pointer would fault the GPU)."""
-    import torch
-    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+def _index_code(t, name: str) -> int:
+    if not _INDEX_CODES:
+        _learn_dtypes()
+    code = _INDEX_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected int32 or int64, got {t.dtype}")
+    return code
+
+
+def _like(t, ref, name: str) -> None:
+    if t.dtype != ref.dtype:
+        raise TypeError(f"{name}: expected {ref.dtype}, got {t.dtype}")
+
+
+def _matrix(t, rows: int, cols: int, name: str) -> int:
+    """Pitch of a rows x cols tensor with unit column stride."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected a {rows} x {cols} tensor, got {tuple(t.shape)}")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}: expected unit column stride, got strides {t.stride()}")
+    return pitch if rows > 1 else max(pitch, cols)
+
+
+def _vector(t, n: int, name: str) -> None:
+    if t is None:
+        return
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+
+
+def _stat(t, n: int, name: str) -> None:
+    """A contiguous fp32 vector of n, or None."""
+    if t is None:
+        return
+    _vector(t, n, name)
+    if _float_code(t, name) != DTYPE_F32:
+        raise TypeError(f"{name}: expected float32, got {t.dtype}")
+
+
+def _launch_stream(stream, *tensors) -> Optional[int]:
+    """The stream to launch on, once every tensor is known to lie on the current CUDA device (a
+    host pointer would fault the GPU)."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.device.type != "cuda"
-                              or (cur is not None and t.device.index != cur)):
+        if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError(f"expected tensors on the current CUDA device, got {t.device}")
+    import torch
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"expected tensors on the current CUDA device, got cuda:{dev}")
+    return _stream(stream)
 
 
 def _workspace(ws, nbytes: int, device, stream):
     """The caller's uint8 workspace, or a fresh one that lives until `stream` is done with it."""
-    import torch
     if ws is not None:
         return ws, ws.numel() * ws.element_size()
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    import torch
+    ws = torch.empty(nbytes or 1, dtype=torch.uint8, device=device)
     if stream is not None:
         ws.record_stream(stream if hasattr(stream, "cuda_stream")
                          else torch.cuda.ExternalStream(stream))
     return ws, nbytes
 
 
-def _params_code(named) -> int:
-    """The one dtype of the given parameter vectors (fp32 when there is none)."""
-    codes = {_float_code(t, name) for name, t in named if t is not None}
-    if len(codes) > 1:
-        raise TypeError("the norm's parameters and their gradients must share one dtype")
-    return codes.pop() if codes else DTYPE_F32
+def _params_code(cols: int, named) -> int:
+    """The one dtype of the given vectors of `cols` parameters (fp32 when there is none)."""
+    code = None
+    for name, t in named:
+        if t is None:
+            continue
+        _vector(t, cols, name)
+        c = _float_code(t, name)
+        if code is not None and c != code:
+            raise TypeError("the norm's parameters and their gradients must share one dtype")
+        code = c
+    return DTYPE_F32 if code is None else code
 
 
 def mfsdp_norm_forward(kind: int, x, weight, bias, eps: float, y, mean=None, rstd=None,
@@ -517,23 +553,20 @@ def mfsdp_norm_forward(kind: int, x, weight, bias, eps: float, y, mean=None, rst
     """Layer norm (``kind`` NORM_LAYER) or RMS norm (NORM_RMS) of the rows of ``x`` into ``y``.
     ``weight`` and ``bias`` may be None; ``mean`` and ``rstd`` (fp32, per row) are written where
     given, for ``mfsdp_norm_backward``."""
-    import torch
     rows, cols = x.shape
     code = _float_code(x, "x")
-    if y.dtype != x.dtype:
-        raise TypeError(f"y: expected {x.dtype}, got {y.dtype}")
+    _like(y, x, "y")
     ld_x, ld_y = _matrix(x, rows, cols, "x"), _matrix(y, rows, cols, "y")
-    _vector(weight, cols, "weight")
-    _vector(bias, cols, "bias")
-    _vector(mean, rows, "mean", torch.float32)
-    _vector(rstd, rows, "rstd", torch.float32)
-    pcode = _params_code((("weight", weight), ("bias", bias)))
-    _same_device(x, weight, bias, y, mean, rstd)
+    _stat(mean, rows, "mean")
+    _stat(rstd, rows, "rstd")
+    pcode = _params_code(cols, (("weight", weight), ("bias", bias)))
+    st = _launch_stream(stream, x, weight, bias, y, mean, rstd)
     _check("mfsdp_norm_forward", _lib.load().mfsdp_norm_forward(
-        kind, rows, cols, code, pcode, _ptr(x), ld_x, _ptr(weight), _ptr(bias), eps, _ptr(y),
-        ld_y, _ptr(mean), _ptr(rstd), _stream(stream)))
+        kind, rows, cols, code, pcode, x.data_ptr(), ld_x, _ptr(weight), _ptr(bias), eps,
+        y.data_ptr(), ld_y, _ptr(mean), _ptr(rstd), st))
 
 
+@functools.lru_cache(maxsize=256)
 def mfsdp_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
     out = C.c_size_t(0)
     _check("mfsdp_norm_backward_workspace_bytes",
@@ -545,26 +578,21 @@ def mfsdp_norm_backward(kind: int, dy, x, weight, mean, rstd, dx, dweight=None, 
                         workspace=None, stream=None) -> None:
     """Gradients of ``mfsdp_norm_forward`` for its input and, where given, for the weight and
     the bias.  ``workspace`` (uint8) defaults to a fresh one."""
-    import torch
     rows, cols = x.shape
     code = _float_code(x, "x")
-    for name, t in (("dy", dy), ("dx", dx)):
-        if t.dtype != x.dtype:
-            raise TypeError(f"{name}: expected {x.dtype}, got {t.dtype}")
+    _like(dy, x, "dy")
+    _like(dx, x, "dx")
     ld_dy, ld_x = _matrix(dy, rows, cols, "dy"), _matrix(x, rows, cols, "x")
     ld_dx = _matrix(dx, rows, cols, "dx")
-    for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
-        _vector(t, cols, name)
-    _vector(mean, rows, "mean", torch.float32)
-    _vector(rstd, rows, "rstd", torch.float32)
-    pcode = _params_code((("weight", weight), ("dweight", dweight), ("dbias", dbias)))
-    _same_device(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+    _stat(mean, rows, "mean")
+    _stat(rstd, rows, "rstd")
+    pcode = _params_code(cols, (("weight", weight), ("dweight", dweight), ("dbias", dbias)))
+    st = _launch_stream(stream, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
     ws, nbytes = _workspace(workspace, mfsdp_norm_backward_workspace_bytes(rows, cols), x.device,
                             stream)
     _check("mfsdp_norm_backward", _lib.load().mfsdp_norm_backward(
         kind, rows, cols, code, pcode, _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(weight), _ptr(mean),
-        _ptr(rstd), _ptr(dx), ld_dx, _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes,
-        _stream(stream)))
+        _ptr(rstd), _ptr(dx), ld_dx, _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, st))
 
 
 def mfsdp_embedding_forward(table, ids, scale: float, out, stream=None) -> None:
@@ -575,12 +603,13 @@ def mfsdp_embedding_forward(table, ids, scale: float, out, stream=None) -> None:
     icode = _index_code(ids, "ids")
     _vector(ids, n, "ids")
     ld_t, ld_o = _matrix(table, vocab, dim, "table"), _matrix(out, n, dim, "out")
-    _same_device(table, ids, out)
+    st = _launch_stream(stream, table, ids, out)
     _check("mfsdp_embedding_forward", _lib.load().mfsdp_embedding_forward(
-        vocab, dim, tcode, _ptr(table), ld_t, n, icode, _ptr(ids), scale, ocode, _ptr(out), ld_o,
-        _stream(stream)))
+        vocab, dim, tcode, table.data_ptr(), ld_t, n, icode, ids.data_ptr(), scale, ocode,
+        out.data_ptr(), ld_o, st))
 
 
+@functools.lru_cache(maxsize=256)
 def mfsdp_embedding_backward_workspace_bytes(vocab: int, dim: int, n_tokens: int) -> int:
     out = C.c_size_t(0)
     _check("mfsdp_embedding_backward_workspace_bytes",
@@ -600,30 +629,35 @@ def mfsdp_embedding_backward(ids, dy, scale: float, dtable, padding_idx: int = -
     icode = _index_code(ids, "ids")
     _vector(ids, n, "ids")
     ld_dy, ld_dt = _matrix(dy, n, dim, "dy"), _matrix(dtable, vocab, dim, "dtable")
-    _same_device(ids, dy, dtable, workspace)
+    st = _launch_stream(stream, dtable, dy, ids, workspace)
     ws, nbytes = _workspace(workspace, mfsdp_embedding_backward_workspace_bytes(vocab, dim, n),
                             dtable.device, stream)
     _check("mfsdp_embedding_backward", _lib.load().mfsdp_embedding_backward(
         vocab, dim, n, icode, _ptr(ids), padding_idx, scale, dcode, _ptr(dy), ld_dy,
-        1 if accumulate else 0, gcode, _ptr(dtable), ld_dt, _ptr(ws), nbytes, _stream(stream)))
+        1 if accumulate else 0, gcode, _ptr(dtable), ld_dt, _ptr(ws), nbytes, st))
+
+
+@functools.lru_cache(maxsize=256)
+def _head_workspace(n, dim, vocab, code, backward, misaligned, ld_w, piece) -> int:
+    out = C.c_size_t(0)
+    _check("mfsdp_head_loss_workspace_bytes", _lib.load().mfsdp_head_loss_workspace_bytes(
+        n, dim, vocab, code, backward, misaligned, ld_w, piece, C.byref(out)))
+    return out.value
 
 
 def mfsdp_head_loss_workspace_bytes(n_tokens: int, dim: int, weight, backward: bool,
                                     piece: int = 0) -> int:
-    out = C.c_size_t(0)
     vocab = weight.shape[0]
-    _check("mfsdp_head_loss_workspace_bytes", _lib.load().mfsdp_head_loss_workspace_bytes(
-        n_tokens, dim, vocab, _float_code(weight, "weight"), 1 if backward else 0, _ptr(weight),
-        _matrix(weight, vocab, dim, "weight"), piece, C.byref(out)))
-    return out.value
+    return _head_workspace(n_tokens, dim, vocab, _float_code(weight, "weight"),
+                           1 if backward else 0, weight.data_ptr() % 16,
+                           _matrix(weight, vocab, dim, "weight"), piece)
 
 
 def _head_args(hidden, weight, labels):
     n, dim = hidden.shape
     vocab = weight.shape[0]
     code = _float_code(hidden, "hidden")
-    if weight.dtype != hidden.dtype:
-        raise TypeError(f"weight: expected {hidden.dtype}, got {weight.dtype}")
+    _like(weight, hidden, "weight")
     icode = _index_code(labels, "labels")
     _vector(labels, n, "labels")
     ld_h, ld_w = _matrix(hidden, n, dim, "hidden"), _matrix(weight, vocab, dim, "weight")
@@ -635,16 +669,16 @@ def mfsdp_head_loss_forward(hidden, weight, labels, loss, lse, ignore_index: int
     """Per-token softmax cross entropy of ``hidden @ weight.T`` against ``labels`` into ``loss``
     and the log-sum-exp of the logits into ``lse`` (fp32, either may be None).  Tokens labelled
     ``ignore_index`` get 0 in both.  ``workspace`` (uint8) defaults to a fresh one."""
-    import torch
     n, dim, vocab, code, icode, ld_h, ld_w = _head_args(hidden, weight, labels)
-    _vector(loss, n, "loss", torch.float32)
-    _vector(lse, n, "lse", torch.float32)
-    _same_device(hidden, weight, labels, loss, lse, workspace)
-    ws, nbytes = _workspace(workspace, mfsdp_head_loss_workspace_bytes(n, dim, weight, False),
+    _stat(loss, n, "loss")
+    _stat(lse, n, "lse")
+    st = _launch_stream(stream, hidden, weight, labels, loss, lse, workspace)
+    wp = weight.data_ptr()
+    ws, nbytes = _workspace(workspace, _head_workspace(n, dim, vocab, code, 0, wp % 16, ld_w, 0),
                             hidden.device, stream)
     _check("mfsdp_head_loss_forward", _lib.load().mfsdp_head_loss_forward(
-        n, dim, vocab, code, _ptr(hidden), ld_h, _ptr(weight), ld_w, icode, _ptr(labels),
-        ignore_index, _ptr(loss), _ptr(lse), _ptr(ws), nbytes, _stream(stream)))
+        n, dim, vocab, code, hidden.data_ptr(), ld_h, wp, ld_w, icode, labels.data_ptr(),
+        ignore_index, _ptr(loss), _ptr(lse), ws.data_ptr(), nbytes, st))
 
 
 def mfsdp_head_loss_backward(hidden, weight, labels, lse, dloss, dhidden=None, dweight=None,
@@ -653,23 +687,22 @@ def mfsdp_head_loss_backward(hidden, weight, labels, lse, dloss, dhidden=None, d
     """Gradients of ``sum(dloss * loss)`` for the hidden states and the weight (either may be
     None), with ``lse`` from the forward pass; the logits are recomputed in pieces of ``piece``
     columns of the vocabulary (0: chosen)."""
-    import torch
     n, dim, vocab, code, icode, ld_h, ld_w = _head_args(hidden, weight, labels)
-    _vector(lse, n, "lse", torch.float32)
-    _vector(dloss, n, "dloss", torch.float32)
+    _stat(lse, n, "lse")
+    _stat(dloss, n, "dloss")
     ld_dh = ld_dw = dim
-    for name, t in (("dhidden", dhidden), ("dweight", dweight)):
-        if t is not None and t.dtype != hidden.dtype:
-            raise TypeError(f"{name}: expected {hidden.dtype}, got {t.dtype}")
     if dhidden is not None:
+        _like(dhidden, hidden, "dhidden")
         ld_dh = _matrix(dhidden, n, dim, "dhidden")
     if dweight is not None:
+        _like(dweight, hidden, "dweight")
         ld_dw = _matrix(dweight, vocab, dim, "dweight")
-    _same_device(hidden, weight, labels, lse, dloss, dhidden, dweight, workspace)
+    st = _launch_stream(stream, hidden, weight, labels, lse, dloss, dhidden, dweight, workspace)
+    wp = weight.data_ptr()
     ws, nbytes = _workspace(workspace,
-                            mfsdp_head_loss_workspace_bytes(n, dim, weight, True, piece),
+                            _head_workspace(n, dim, vocab, code, 1, wp % 16, ld_w, piece),
                             hidden.device, stream)
     _check("mfsdp_head_loss_backward", _lib.load().mfsdp_head_loss_backward(
-        n, dim, vocab, code, _ptr(hidden), ld_h, _ptr(weight), ld_w, icode, _ptr(labels),
+        n, dim, vocab, code, hidden.data_ptr(), ld_h, wp, ld_w, icode, labels.data_ptr(),
         ignore_index, _ptr(lse), _ptr(dloss), piece, _ptr(dhidden), ld_dh, _ptr(dweight), ld_dw,
-        _ptr(ws), nbytes, _stream(stream)))
+        ws.data_ptr(), nbytes, st))
