@@ -9,13 +9,15 @@
 //               significant digit first.  Per pass each warp counts the digits of its own
 //               contiguous share, the blocks exchange their digit totals through distributed
 //               shared memory, and every warp then places its share in order.  Cluster barriers
-//               separate the steps, so the whole sort is one launch.
+//               separate the steps, so the whole sort is one launch.  The sort is bound by
+//               latency, so the launch's other blocks meanwhile write zeros over the first
+//               kFillBytes of the gradient, about what fits in the sort's time.
 //   2. sum      the sorted positions are cut into chunks of kChunkPos.  A chunk sums the runs
 //               of equal ids inside it in fp32 and writes each finished row once; a run that
 //               crosses a chunk boundary leaves fp32 partial rows in the workspace.  The work
 //               per block is the same whether one id owns half the tokens or none repeats.
-//               The same launch writes the zero rows (ids that a flag array of the sort marks
-//               as absent), so the gradient is written exactly once.
+//               More blocks of the launch zero the other rows that do not occur (the sort
+//               marks those that do).
 //   3. join     adds the partial rows of the runs that cross chunks, in chunk order.
 // The sum is held in fp32 throughout and rounded once, to the gradient's type.
 #include "elem.cuh"
@@ -34,7 +36,9 @@ constexpr int kBinsMax = 1 << kDigitMax;
 constexpr int kSortSmem = (kSortWarps * kBinsMax + kBinsMax + kBinsMax + 32) * 4;
 constexpr int kChunkPos = 32;               // sorted positions per chunk
 constexpr int kSumThreads = 128;
-constexpr int kZeroRows = 8;                // table rows per zero-fill block
+constexpr int kZeroRows = 8;                // table rows per zeroing block of the sum launch
+constexpr int64_t kFillBytes = 80ll << 20;  // zeros written beside the sort (about 13 us)
+constexpr int kKeep = 4;                    // positions per lane the sort keeps in registers
 
 struct EmbFwd {
   const void* table;
@@ -47,33 +51,53 @@ struct EmbFwd {
 };
 
 // ---------------------------------------------------------------- lookup
-// One thread per 8 elements (VEC) or per element of the output.
-template <typename TT, typename TO, bool VEC>
+// A unit is 8 elements (VEC) or one element of the output; a thread takes U of them, a grid
+// apart, with their loads in flight together.
+template <typename TT, typename TO, bool VEC, int U>
 __global__ void __launch_bounds__(256) embedding_forward_kernel(const __grid_constant__ EmbFwd p) {
   pdl_launch();
   pdl_wait();
   const int per_row = VEC ? p.dim / 8 : p.dim;
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t t = u / per_row;
-  if (t >= p.n) return;
-  const int c = (int)(u - t * per_row) * (VEC ? 8 : 1);
-  const int64_t id = load_index(p.ids, p.is64, t);
-  const bool ok = id >= 0 && id < p.vocab;
-  if (!ok && c == 0) atomicOr(p.status, kStatusBadIndex);
-  const TT* src = static_cast<const TT*>(p.table) + id * p.ld_table + c;
-  TO* dst = static_cast<TO*>(p.out) + t * p.ld_out + c;
-  if (VEC) {
-    Pack8<TT> a;
-    if (ok) a.load(src); else a.zero();
-    float v[8];
-    a.get(v);
+  const int64_t units = p.n * per_row, step = (int64_t)gridDim.x * 256;
+  const int64_t u0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool small = units < (1ll << 31);
+  int64_t t[U], id[U];
+  int c[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= p.scale;
-    Pack8<TO> b;
-    b.set(v);
-    b.store(dst);
-  } else {
-    *dst = from_f32<TO>(ok ? to_f32(*src) * p.scale : 0.f);
+  for (int i = 0; i < U; ++i) {
+    const int64_t u = u0 + i * step;
+    t[i] = u >= units ? -1 : small ? (int64_t)((uint32_t)u / (uint32_t)per_row) : u / per_row;
+    c[i] = (int)(u - t[i] * per_row) * (VEC ? 8 : 1);
+    id[i] = t[i] >= 0 ? load_index(p.ids, p.is64, t[i]) : 0;
+  }
+  Pack8<TT> a[VEC ? U : 1];
+  float e[VEC ? 1 : U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const bool ok = t[i] >= 0 && id[i] >= 0 && id[i] < p.vocab;
+    if (t[i] >= 0 && !ok && c[i] == 0) atomicOr(p.status, kStatusBadIndex);
+    const TT* src = static_cast<const TT*>(p.table) + (ok ? id[i] * p.ld_table + c[i] : 0);
+    if (VEC) {
+      if (ok) a[VEC ? i : 0].load(src); else a[VEC ? i : 0].zero();
+    } else {
+      e[VEC ? 0 : i] = ok ? to_f32(*src) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (t[i] < 0) continue;
+    TO* dst = static_cast<TO*>(p.out) + t[i] * p.ld_out + c[i];
+    if (VEC) {
+      float v[8];
+      a[VEC ? i : 0].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= p.scale;
+      Pack8<TO> b;
+      b.set(v);
+      b.store(dst);
+    } else {
+      *dst = from_f32<TO>(e[VEC ? 0 : i] * p.scale);
+    }
   }
 }
 
@@ -81,11 +105,34 @@ __global__ void __launch_bounds__(256) embedding_forward_kernel(const __grid_con
 struct SortArgs {
   const void* ids;
   uint32_t *key0, *val0, *key1, *val1;   // ping-pong; the result lands in key1, val1
-  uint8_t* present;                      // [vocab] written: 1 where an id occurs
+  uint8_t* present;                      // [vocab] written: 1 where an id occurs; nullable
   int64_t vocab, padding;
   int32_t n, is64, passes, digit;
   int* status;
+  // the zeros: `fill_rows` rows of `fill_units` stores of 16 bytes (fill_vec) or of one element
+  char* fill;
+  int64_t fill_rows, fill_units, fill_pitch;   // pitch in bytes
+  int32_t fill_vec, elem_bytes;
 };
+
+__device__ __forceinline__ void zero_fill(const SortArgs& p, int64_t first, int64_t step) {
+  const int64_t total = p.fill_rows * p.fill_units;
+  const bool flat = p.fill_rows == 1, small = total < (1ll << 31);
+  for (int64_t u = first; u < total; u += step) {
+    int64_t row = 0, c = u;
+    if (!flat) {
+      row = small ? (int64_t)((uint32_t)u / (uint32_t)p.fill_units) : u / p.fill_units;
+      c = u - row * p.fill_units;
+    }
+    char* at = p.fill + row * p.fill_pitch;
+    if (p.fill_vec)
+      reinterpret_cast<uint4*>(at)[c] = make_uint4(0u, 0u, 0u, 0u);
+    else if (p.elem_bytes == 2)
+      reinterpret_cast<uint16_t*>(at)[c] = 0;
+    else
+      reinterpret_cast<uint32_t*>(at)[c] = 0u;
+  }
+}
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -112,16 +159,24 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
   pdl_launch();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x >= kSortBlocks) {                     // whole clusters: zeros only
+    zero_fill(p, (int64_t)(blockIdx.x - kSortBlocks) * kSortThreads + tid,
+              (int64_t)(gridDim.x - kSortBlocks) * kSortThreads);
+    return;
+  }
   const uint32_t rank = cluster_ctarank();
   const int bins = 1 << p.digit;
-  // every warp of the cluster owns one contiguous share of the positions
+  // every warp of the cluster owns one contiguous share of the positions; a short share's keys
+  // stay in registers between counting and placing
   const int64_t share = (p.n + kSortBlocks * kSortWarps - 1) / (kSortBlocks * kSortWarps);
   const int64_t i0 = ((int64_t)rank * kSortWarps + warp) * share;
   const int64_t i1 = i0 + share < p.n ? i0 + share : (int64_t)p.n;
-  // the flags start at zero (the array has 16-byte alignment and is padded to it)
-  for (int64_t i = (int64_t)rank * kSortThreads + tid; i < (p.vocab + 15) / 16;
-       i += kSortBlocks * kSortThreads)
-    reinterpret_cast<uint4*>(p.present)[i] = make_uint4(0u, 0u, 0u, 0u);
+  const bool keep = share <= 32 * kKeep;
+  // (the array is padded to its 16-byte stores; a barrier of the first pass precedes the marks)
+  if (p.present)
+    for (int64_t i = (int64_t)rank * kSortThreads + tid; i < (p.vocab + 15) / 16;
+         i += kSortBlocks * kSortThreads)
+      reinterpret_cast<uint4*>(p.present)[i] = make_uint4(0u, 0u, 0u, 0u);
 
   for (int pass = 0; pass < p.passes; ++pass) {
     // the last pass writes buffer 1
@@ -132,42 +187,61 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     uint32_t* vd = to1 ? p.val1 : p.val0;
     const int shift = pass * p.digit;
     // ids outside the table and the padding id sort behind every row, as key = vocab
-    auto key_at = [&](int64_t i) -> uint32_t {
+    auto key_at = [&](int64_t i, bool check) -> uint32_t {
       if (pass > 0) return ks[i];
       const int64_t id = load_index(p.ids, p.is64, i);
-      return id < 0 || id >= p.vocab || id == p.padding ? (uint32_t)p.vocab : (uint32_t)id;
+      const bool in = id >= 0 && id < p.vocab;
+      if (check && !in && id != p.padding) atomicOr(p.status, kStatusBadIndex);
+      return in && id != p.padding ? (uint32_t)id : (uint32_t)p.vocab;
     };
+    auto val_at = [&](int64_t i) -> uint32_t { return pass > 0 ? vs[i] : (uint32_t)i; };
+    uint32_t kk[kKeep], vv[kKeep];
+    if (keep) {
+#pragma unroll
+      for (int u = 0; u < kKeep; ++u) {
+        const int64_t i = i0 + 32 * u + lane;
+        kk[u] = i < i1 ? key_at(i, true) : 0u;
+        vv[u] = i < i1 ? val_at(i) : 0u;
+      }
+    }
     for (int b = tid; b < kSortWarps * bins; b += kSortThreads) hist[b] = 0u;
     __syncthreads();
-    for (int64_t i = i0 + lane; i < i1; i += 32) {
-      const uint32_t k = key_at(i);
-      if (pass == 0) {
-        const int64_t id = load_index(p.ids, p.is64, i);
-        if ((id < 0 || id >= p.vocab) && id != p.padding) atomicOr(p.status, kStatusBadIndex);
-      }
-      atomicAdd(&hist[warp * bins + ((k >> shift) & (bins - 1))], 1u);
+    uint32_t* mine = hist + warp * bins;
+    if (keep) {
+#pragma unroll
+      for (int u = 0; u < kKeep; ++u)
+        if (i0 + 32 * u + lane < i1) atomicAdd(&mine[(kk[u] >> shift) & (bins - 1)], 1u);
+    } else {
+      for (int64_t i = i0 + lane; i < i1; i += 32)
+        atomicAdd(&mine[(key_at(i, true) >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
     // per digit: exclusive sums over this block's warps, and the block's total
-    for (int b = tid; b < bins; b += kSortThreads) {
-      uint32_t s = 0;
+    if (tid < bins) {
+      uint32_t c[kSortWarps], s = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w * bins + tid];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = hist[w * bins + b];
-        hist[w * bins + b] = s;
-        s += c;
+        hist[w * bins + tid] = s;
+        s += c[w];
       }
-      total[b] = s;
+      total[tid] = s;
     }
     cluster_barrier();
     // digit b of this block starts after all smaller digits and the same digit of the blocks
     // before it
     uint32_t all = 0, before = 0;
-    if (tid < bins)
-      for (uint32_t r = 0; r < (uint32_t)kSortBlocks; ++r) {
-        const uint32_t c = ld_cluster_u32(total + tid, r);
-        all += c;
-        if (r < rank) before += c;
+    if (tid < bins) {
+      uint32_t c[kSortBlocks];
+#pragma unroll
+      for (int q = 0; q < kSortBlocks; ++q) c[q] = ld_cluster_u32(total + tid, (uint32_t)q);
+#pragma unroll
+      for (int q = 0; q < kSortBlocks; ++q) {
+        all += c[q];
+        if ((uint32_t)q < rank) before += c[q];
       }
+    }
     uint32_t x = all;   // inclusive scan over the digits
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,26 +250,15 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
     }
     if (lane == 31) scan[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-      uint32_t s = scan[lane];
+    // the sum of the warps before: at most 16 warps hold digits
+    uint32_t ahead = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += y;
-      }
-      scan[lane] = s;
-    }
-    __syncthreads();
-    if (tid < bins) base[tid] = x - all + (warp > 0 ? scan[warp - 1] : 0u) + before;
+    for (int w = 0; w < kBinsMax / 32; ++w) ahead += w < warp ? scan[w] : 0u;
+    if (tid < bins) base[tid] = x - all + ahead + before;
     __syncthreads();
     // place, 32 positions at a time, in order: a lane's rank is the number of lower lanes with
     // its digit
-    uint32_t* mine = hist + warp * bins;
-    for (int64_t b0 = i0; b0 < i1; b0 += 32) {
-      const int64_t i = b0 + lane;
-      const bool live = i < i1;
-      const uint32_t k = live ? key_at(i) : 0u;
-      const uint32_t v = live ? (pass > 0 ? vs[i] : (uint32_t)i) : 0u;
+    auto place = [&](bool live, uint32_t k, uint32_t v) {
       const uint32_t d = live ? (k >> shift) & (bins - 1) : 0xFFFFFFFFu;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
       const uint32_t below = __popc(same & ((1u << lane) - 1u));
@@ -207,7 +270,16 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
       if (live) {
         kd[pos] = k;
         vd[pos] = v;
-        if (pass == p.passes - 1 && k < (uint32_t)p.vocab) p.present[k] = 1;
+        if (p.present && pass == p.passes - 1 && k < (uint32_t)p.vocab) p.present[k] = 1;
+      }
+    };
+    if (keep) {
+#pragma unroll
+      for (int u = 0; u < kKeep; ++u) place(i0 + 32 * u + lane < i1, kk[u], vv[u]);
+    } else {
+      for (int64_t b = i0; b < i1; b += 32) {
+        const int64_t i = b + lane;
+        place(i < i1, i < i1 ? key_at(i, false) : 0u, i < i1 ? val_at(i) : 0u);
       }
     }
     cluster_barrier();   // the pass's output, and the peers' totals, before the next pass
@@ -218,13 +290,14 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
 struct SumArgs {
   const uint32_t *key, *val;
   const uint8_t* present;
+  int64_t zero_row0;           // rows from here on: zeroed by the blocks after sum_blocks
+  int32_t sum_blocks, row_vec;
   const void* dy;
   void* dtable;
   float* part;                 // [chunks][2][dim]: run from before the chunk, run into the next
   int64_t ld_dy, ld_dt, vocab;
   int32_t n, dim, chunks, accumulate;
   int32_t slabs, cols_shift;   // column threads per chunk = 1 << cols_shift
-  int32_t sum_blocks;          // blocks of the sum part; the rest write zero rows
   float scale;
 };
 
@@ -266,18 +339,16 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
   pdl_launch();
   pdl_wait();
   if ((int)blockIdx.x >= p.sum_blocks) {
-    // rows of absent ids
-    const int64_t r0 = (int64_t)((int)blockIdx.x - p.sum_blocks) * kZeroRows;
-    for (int i = 0; i < kZeroRows; ++i) {
-      const int64_t r = r0 + i;
-      if (r >= p.vocab || p.present[r]) continue;
+    const int64_t r0 = p.zero_row0 + (int64_t)((int)blockIdx.x - p.sum_blocks) * kZeroRows;
+    const int units = p.row_vec ? p.dim * (int)sizeof(TG) / 16 : p.dim;
+    for (int64_t r = r0; r < p.vocab && r < r0 + kZeroRows; ++r) {
+      if (p.present[r]) continue;
       TG* row = static_cast<TG*>(p.dtable) + r * p.ld_dt;
-      if (VEC) {
-        Pack8<TG> z;
-        z.zero();
-        for (int e = threadIdx.x * 8; e < p.dim; e += kSumThreads * 8) z.store(row + e);
-      } else {
-        for (int e = threadIdx.x; e < p.dim; e += kSumThreads) row[e] = from_f32<TG>(0.f);
+      for (int e = threadIdx.x; e < units; e += kSumThreads) {
+        if (p.row_vec)
+          reinterpret_cast<uint4*>(row)[e] = make_uint4(0u, 0u, 0u, 0u);
+        else
+          row[e] = from_f32<TG>(0.f);
       }
     }
     return;
@@ -289,6 +360,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
   const int64_t chunk = unit / p.slabs;
   if (chunk >= p.chunks) return;
   const int i0 = (int)(chunk * kChunkPos), i1 = min(p.n, i0 + kChunkPos);
+  if (VEC && col_of<VEC>(slab, tx, c, 0) >= p.dim) return;
   const uint32_t none = (uint32_t)p.vocab;
   const uint32_t prev = i0 > 0 ? p.key[i0 - 1] : none, next = i1 < p.n ? p.key[i1] : none;
   float acc[8];
@@ -303,10 +375,17 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
       write_row<TG, VEC>(p, cur, slab, tx, c, acc);
     } else {
       float* dst = part + (from_before ? 0 : p.dim);
+      if (VEC) {
+        const int e = col_of<VEC>(slab, tx, c, 0);
+        Pack8<float> q;
+        q.set(acc);
+        if (e < p.dim) q.store(dst + e);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = col_of<VEC>(slab, tx, c, j);
-        if (e < p.dim) dst[e] = acc[j];
+        for (int j = 0; j < 8; ++j) {
+          const int e = col_of<VEC>(slab, tx, c, j);
+          if (e < p.dim) dst[e] = acc[j];
+        }
       }
     }
   };
@@ -317,18 +396,17 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
     float ds[VEC ? 1 : U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      k[u] = b + u < i1 ? p.key[b + u] : none;
-      const TD* row = static_cast<const TD*>(p.dy) +
-                      (k[u] != none ? (int64_t)p.val[b + u] * p.ld_dy : 0);
+      // unconditional loads of clamped positions: the batch is in flight together (a row that
+      // takes no part is flushed under key `none`, which is not written)
+      const int at = min(b + u, i1 - 1);
+      k[u] = p.key[at];
+      const TD* row = static_cast<const TD*>(p.dy) + (int64_t)p.val[at] * p.ld_dy;
       if (VEC) {
-        const int e = col_of<VEC>(slab, tx, c, 0);
-        if (k[u] != none && e < p.dim) d[u].load(row + e); else d[u].zero();
+        d[u].load(row + col_of<VEC>(slab, tx, c, 0));
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = col_of<VEC>(slab, tx, c, j);
-          ds[VEC ? 0 : u][j] = k[u] != none && e < p.dim ? to_f32(row[e]) : 0.f;
-        }
+        for (int j = 0; j < 8; ++j)
+          ds[VEC ? 0 : u][j] = to_f32(row[min(col_of<VEC>(slab, tx, c, j), p.dim - 1)]);
       }
     }
 #pragma unroll
@@ -365,24 +443,56 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const __gri
   const uint32_t k = p.key[i1 - 1];
   if (k == (uint32_t)p.vocab || p.key[i1] != k) return;           // ends here
   if (i0 > 0 && p.key[i0 - 1] == k) return;                       // an earlier chunk's run
+  if (VEC && col_of<VEC>(slab, tx, c, 0) >= p.dim) return;
+  // The chunks the run goes on into: every one whose first position still holds the id.  The
+  // loads are unconditional (indices are clamped instead), so a batch is in flight together.
+  const int64_t last = p.chunks - 1;
+  int64_t end = chunk + 2;
+  for (bool more = true; more;) {
+    constexpr int kAhead = 16;
+    uint32_t next[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) next[u] = p.key[min(end + u, last) * kChunkPos];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      more = more && end <= last && next[u] == k;
+      end += more ? 1 : 0;
+    }
+  }
+  constexpr int U = VEC ? 12 : 4;   // partial rows loaded ahead
   float acc[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int e = col_of<VEC>(slab, tx, c, j);
-    acc[j] = e < p.dim ? p.part[(chunk * 2 + 1) * p.dim + e] : 0.f;
-  }
-  for (int64_t q = chunk + 1; q < p.chunks && p.key[q * kChunkPos] == k; ++q) {
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  for (int64_t q = chunk; q < end; q += U) {
+    float v[U][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = col_of<VEC>(slab, tx, c, j);
-      if (e < p.dim) acc[j] += p.part[q * 2 * p.dim + e];
+    for (int u = 0; u < U; ++u) {
+      // the first chunk's partial row is its run into the next chunk, the others' the run from
+      // before
+      const int64_t at = min(q + u, end - 1);
+      const float* src = p.part + (at * 2 + (at == chunk ? 1 : 0)) * p.dim;
+      if (VEC) {
+        Pack8<float> w;
+        w.load(src + col_of<VEC>(slab, tx, c, 0));
+        w.get(v[u]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[u][j] = src[min(col_of<VEC>(slab, tx, c, j), p.dim - 1)];
+      }
     }
+    asm volatile("" ::: "memory");  // all of them in flight before the first is added
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += q + u < end ? v[u][j] : 0.f;
   }
   write_row<TG, VEC>(p, k, slab, tx, c, acc);
 }
 
 // ---------------------------------------------------------------- host
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
 struct BwdLayout {
   size_t key0, val0, key1, val1, present, part, total;
@@ -416,26 +526,27 @@ bool vec_ok(const void* p, int64_t ld, int64_t dim, int32_t dtype) {
   return aligned_to(p, 16) && dim % 8 == 0 && (ld * (int64_t)dtype_bytes(dtype)) % 16 == 0;
 }
 
-template <typename TT, typename TO>
-cudaError_t run_forward(const EmbFwd& a, bool vec, cudaStream_t st) {
-  const int64_t units = a.n * (vec ? a.dim / 8 : a.dim);
-  const int64_t grid = (units + 255) / 256;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  return vec ? launch_pdl(embedding_forward_kernel<TT, TO, true>, dim3((unsigned)grid), dim3(256),
-                          0, st, a)
-             : launch_pdl(embedding_forward_kernel<TT, TO, false>, dim3((unsigned)grid), dim3(256),
-                          0, st, a);
+template <typename TT, typename TO, bool VEC>
+cudaError_t run_forward(const EmbFwd& a, int sms, cudaStream_t st) {
+  const int64_t units = a.n * (VEC ? a.dim / 8 : a.dim);
+  // four units per thread once that still fills the GPU
+  const bool four = units > (int64_t)sms * 2048 * 2;
+  const int64_t grid = (units + (four ? 1024 : 256) - 1) / (four ? 1024 : 256);
+  return four ? launch_pdl(embedding_forward_kernel<TT, TO, VEC, 4>, dim3((unsigned)grid), dim3(256),
+                           0, st, a)
+              : launch_pdl(embedding_forward_kernel<TT, TO, VEC, 1>, dim3((unsigned)grid), dim3(256),
+                           0, st, a);
 }
 
 template <typename TD, typename TG>
-cudaError_t run_sum(const SumArgs& a, bool vec, int64_t grid, int64_t join_grid, cudaStream_t st) {
+cudaError_t run_sum(const SumArgs& a, bool vec, int64_t zero_blocks, cudaStream_t st) {
   cudaError_t e;
-  const dim3 b(kSumThreads);
-  e = vec ? launch_pdl(embedding_sum_kernel<TD, TG, true>, dim3((unsigned)grid), b, 0, st, a)
-          : launch_pdl(embedding_sum_kernel<TD, TG, false>, dim3((unsigned)grid), b, 0, st, a);
+  const dim3 g((unsigned)a.sum_blocks), all((unsigned)(a.sum_blocks + zero_blocks)), b(kSumThreads);
+  e = vec ? launch_pdl(embedding_sum_kernel<TD, TG, true>, all, b, 0, st, a)
+          : launch_pdl(embedding_sum_kernel<TD, TG, false>, all, b, 0, st, a);
   if (e != cudaSuccess || a.chunks < 2) return e;
-  return vec ? launch_pdl(embedding_join_kernel<TG, true>, dim3((unsigned)join_grid), b, 0, st, a)
-             : launch_pdl(embedding_join_kernel<TG, false>, dim3((unsigned)join_grid), b, 0, st, a);
+  return vec ? launch_pdl(embedding_join_kernel<TG, true>, g, b, 0, st, a)
+             : launch_pdl(embedding_join_kernel<TG, false>, g, b, 0, st, a);
 }
 
 }  // namespace
@@ -460,7 +571,7 @@ extern "C" int mfsdp_embedding_forward(int64_t vocab, int64_t dim, int32_t table
       !aligned_to(ids, is64 ? 8 : 4))
     return MFSDP_EALIGN;
   const bool vec = vec_ok(table, ld_table, dim, table_dtype) && vec_ok(out, ld_out, dim, out_dtype);
-  if (n_tokens * (vec ? dim / 8 : dim) > (1ll << 31) * 256 - 256) return MFSDP_ESHAPE;
+  if (n_tokens * (vec ? dim / 8 : dim) > (1ll << 31) * 1024 - 1024) return MFSDP_ESHAPE;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;
@@ -479,10 +590,13 @@ extern "C" int mfsdp_embedding_forward(int64_t vocab, int64_t dim, int32_t table
   if (!a.status) return MFSDP_ECUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool tb = table_dtype == MFSDP_DTYPE_BF16, ob = out_dtype == MFSDP_DTYPE_BF16;
-  const cudaError_t e = tb ? (ob ? run_forward<bf16_t, bf16_t>(a, vec, st)
-                                 : run_forward<bf16_t, float>(a, vec, st))
-                           : (ob ? run_forward<float, bf16_t>(a, vec, st)
-                                 : run_forward<float, float>(a, vec, st));
+  auto run = [&](auto in, auto out_t) {
+    using TT = decltype(in);
+    using TO = decltype(out_t);
+    return vec ? run_forward<TT, TO, true>(a, sms, st) : run_forward<TT, TO, false>(a, sms, st);
+  };
+  const cudaError_t e = tb ? (ob ? run(bf16_t(), bf16_t()) : run(bf16_t(), 0.f))
+                           : (ob ? run(0.f, bf16_t()) : run(0.f, 0.f));
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }
 
@@ -528,7 +642,6 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   s.val0 = reinterpret_cast<uint32_t*>(ws + l.val0);
   s.key1 = reinterpret_cast<uint32_t*>(ws + l.key1);
   s.val1 = reinterpret_cast<uint32_t*>(ws + l.val1);
-  s.present = reinterpret_cast<uint8_t*>(ws + l.present);
   s.vocab = vocab;
   s.padding = padding_idx;
   s.n = (int32_t)n_tokens;
@@ -542,7 +655,6 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   SumArgs a{};
   a.key = s.key1;
   a.val = s.val1;
-  a.present = s.present;
   a.dy = dy;
   a.dtable = dtable;
   a.part = reinterpret_cast<float*>(ws + l.part);
@@ -558,25 +670,51 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   while ((1 << a.cols_shift) < kSumThreads && (1 << a.cols_shift) < col_threads) ++a.cols_shift;
   const int64_t tx = 1ll << a.cols_shift, ty = kSumThreads / tx;
   a.slabs = (int32_t)((col_threads + tx - 1) / tx);
-  const int64_t sum_blocks = ((int64_t)a.chunks * a.slabs + ty - 1) / ty;
-  const int64_t zero_blocks = accumulate ? 0 : (vocab + kZeroRows - 1) / kZeroRows;
-  if (sum_blocks + zero_blocks >= (1ll << 31)) return MFSDP_ESHAPE;
-  a.sum_blocks = (int32_t)sum_blocks;
-  if (sum_blocks + zero_blocks == 0) return MFSDP_OK;
+  const int64_t grid = ((int64_t)a.chunks * a.slabs + ty - 1) / ty;
+  if (grid >= (1ll << 31)) return MFSDP_ESHAPE;
+  if (n_tokens == 0 && accumulate) return MFSDP_OK;
+
+  // zeros: the first rows beside the sort, the rest beside the sums (all of them beside the
+  // sort where there are no sums); a table without gaps is one row
+  int64_t fill_blocks = 0, zero_blocks = 0;
+  if (!accumulate) {
+    const int64_t gb = (int64_t)dtype_bytes(grad_dtype);
+    const bool flat = ld_dtable == dim || vocab == 1;
+    const int64_t first = std::min(vocab, n_tokens == 0 ? vocab : cdiv(kFillBytes, dim * gb));
+    const int64_t row_bytes = (flat ? first * dim : dim) * gb;
+    s.fill = static_cast<char*>(dtable);
+    s.fill_rows = flat ? 1 : first;
+    s.fill_pitch = ld_dtable * gb;
+    s.fill_vec = aligned_to(dtable, 16) && row_bytes % 16 == 0 && (flat || s.fill_pitch % 16 == 0);
+    s.elem_bytes = (int32_t)gb;
+    s.fill_units = row_bytes / (s.fill_vec ? 16 : gb);
+    fill_blocks = std::min(cdiv(s.fill_rows * s.fill_units, kSortThreads),
+                           (int64_t)(2 * sms - kSortBlocks));
+    fill_blocks = cdiv(fill_blocks, kSortBlocks) * kSortBlocks;
+    if (first < vocab) {
+      s.present = reinterpret_cast<uint8_t*>(ws + l.present);
+      a.present = s.present;
+      a.zero_row0 = first;
+      a.row_vec = aligned_to(dtable, 16) && (dim * gb) % 16 == 0 && s.fill_pitch % 16 == 0;
+      zero_blocks = cdiv(vocab - first, kZeroRows);
+    }
+  }
+  a.sum_blocks = (int32_t)grid;
+  if (grid + zero_blocks >= (1ll << 31)) return MFSDP_ESHAPE;
   const bool vec = vec_ok(dtable, ld_dtable, dim, grad_dtype) &&
                    (n_tokens == 0 || vec_ok(dy, ld_dy, dim, dy_dtype));
 
   cudaError_t e = cudaFuncSetAttribute(embedding_sort_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
   if (e == cudaSuccess)
-    e = launch_pdl(embedding_sort_kernel, dim3(kSortBlocks), dim3(kSortThreads), kSortSmem, st, s);
-  if (e == cudaSuccess) {
+    e = launch_pdl(embedding_sort_kernel, dim3((unsigned)(kSortBlocks + fill_blocks)),
+                   dim3(kSortThreads), kSortSmem, st, s);
+  if (e == cudaSuccess && n_tokens > 0) {
     const bool db = dy_dtype == MFSDP_DTYPE_BF16, gb = grad_dtype == MFSDP_DTYPE_BF16;
-    const int64_t grid = sum_blocks + zero_blocks;
-    e = db ? (gb ? run_sum<bf16_t, bf16_t>(a, vec, grid, sum_blocks, st)
-                 : run_sum<bf16_t, float>(a, vec, grid, sum_blocks, st))
-           : (gb ? run_sum<float, bf16_t>(a, vec, grid, sum_blocks, st)
-                 : run_sum<float, float>(a, vec, grid, sum_blocks, st));
+    e = db ? (gb ? run_sum<bf16_t, bf16_t>(a, vec, zero_blocks, st)
+                 : run_sum<bf16_t, float>(a, vec, zero_blocks, st))
+           : (gb ? run_sum<float, bf16_t>(a, vec, zero_blocks, st)
+                 : run_sum<float, float>(a, vec, zero_blocks, st));
   }
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }
