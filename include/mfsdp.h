@@ -662,7 +662,7 @@ int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_
 /*
  * Gradients of sum_t dloss[t] loss[t].  With g_tv = (exp(z_tv - lse[t]) - [v = labels[t]])
  * dloss[t] (0 for dropped tokens), recomputed in pieces of `piece` columns of the vocabulary
- * (rounded up to 256; 0 chooses about 64 Mi entries of g per piece):
+ * (rounded up to 256; 0 chooses them for a workspace of some 400 MB):
  *     dhidden = g weight,   dweight = g^T hidden
  *   lse          as written by the forward pass;  dloss  fp32 [n_tokens].
  *   dhidden, dweight   of `dtype`, nullable, overwritten (rows of dropped tokens are zero).

@@ -10,7 +10,9 @@
 // piece of Z from the same operands, writes that piece of G (bf16 operands: the only rounding
 // between the inputs and the gradients, within 2^-8 of an entry, the precision the product's
 // other factor has), and multiplies it with W's rows for dH and with H for that piece's rows of
-// dW.  dH is summed over the pieces in fp32.
+// dW.  dH is summed over the pieces in fp32.  One launch multiplies a piece of G and computes
+// the next one (two pieces are kept): the many short tiles of Z fill the SMs that the few long
+// ones of dH and dW would leave idle at a launch's end.
 //
 // Tokens with the ignored label are dropped before any product: a first launch copies the live
 // rows of H together (padded to whole TMA rows), so they cost nothing, and whatever they hold
@@ -22,6 +24,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 #include <vector>
 
 #include "elem.cuh"
@@ -45,11 +48,13 @@ constexpr uint32_t kHeadSmem = 1024 + kHeadBars + 256;
 static_assert(kHeadSmem <= 227 * 1024, "shared memory");
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum Phase : int { kStats = 0, kGrad = 1, kOut = 2 };
+enum Phase : int { kStats = 0, kGrads = 1 };
+enum Kind : int { kDh = 0, kDw = 1, kZ = 2 };  // tiles of a kGrads launch (kStats: kZ only)
 
 struct HeadArgs {
   CUtensorMap h_k, h_mn;                   // compacted H: 64 x 128 K-major box, 3D MN-major view
-  CUtensorMap w_k, w_mn;                   // W (or the copy of a piece): 64 x 128, 64 x 64 boxes
+  CUtensorMap w_k, w_mn;                   // W (or the copy of a piece): 64 x 128 box, and 64 x 64
+                                           // boxes or the 3D view
   CUtensorMap g_k, g_mn, g_st;             // G piece: 64 x 128, 3D view, 32 x 32 stores
   CUtensorMap dw_st, acc_st;               // dW bf16 and dH fp32 32 x 32 stores
   const int32_t* nlive;                    // live rows
@@ -61,105 +66,229 @@ struct HeadArgs {
   uint16_t* dw;                            // unaligned dW rows (dw_tma == 0)
   int64_t ld_dw;
   int32_t dim, vocab;
-  int32_t v0, width;                       // the piece: columns [v0, v0 + width) of the vocabulary
-  int32_t w_row0;                          // W's map row of column v0
+  // the piece whose G is multiplied and the piece of Z that is computed (kGrads: the next one):
+  // columns [v0, v0 + width) of the vocabulary, W's map row of column v0, and the first row of
+  // the piece's G; width 0 where there is none
+  int32_t v0, width, w_row0, g_row0;
+  int32_t z_v0, z_width, z_w_row0, z_g_row0;
   int32_t rows;                            // allocated rows (pitch of part, slices of acc)
   int32_t splits;                          // dH: slices of the piece's columns
   int32_t add;                             // dH: add to the slices instead of writing them
   int32_t want_dh, want_dw, dw_tma;
+  int32_t w_3d;                            // w_mn is the 3D MN-major view (whole 64-column chunks)
   int32_t group;                           // tile rows that walk the columns together
   uint64_t wait_limit_ns;
   int* status;
 };
 
 struct HeadTile {
-  int kind;                                // kOut only: 0 = dH, 1 = dW
-  int tm, tn;
+  int kind, tm, tn;
   int kb0, nk;                             // k-blocks
   int split;
 };
 
-// The tiles of one pair, in order.  kStats / kGrad: groups of `group` tile rows walk the
-// columns together (a W panel is read once per group, H's group stays in the L2).  kOut: the
-// tiles of the longer contraction first, round robin; the pairs that got one fewer of them
-// then take the shorter tiles that make up for it, and the rest goes round robin.
+// The tiles of one pair, in order: the kind with the longest contraction first, each kind dealt
+// so that the pairs' loads (in k-blocks) stay level.  Dealing a kind of n tiles of k: pairs of
+// equal load form a group; every group gets whole rounds up to the mean load, and what is left
+// goes one by one to the pairs in order of load.  Within a group the tiles are interleaved, so
+// pairs that run at the same time work on neighbouring tiles and share operands in the L2.
 template <int PHASE>
 struct TileList {
-  int live, ntm, ntn;                      // kStats / kGrad
-  int n1, n2, first;                       // kOut: tiles of the two classes, class that leads
-  int ntd, ntv, kdh, kdw, e, pair, npairs, group;
+  struct Deal {                            // this pair's share of one kind
+    int kind, count, rounds, base, stride, rest;
+  };
+  static constexpr int kKinds = PHASE == kStats ? 1 : 3;
+  int live, ntm, ntn, ntd, kdh, npairs;
+  Deal deal[kKinds];
+  int z_step, z_dn, z_dm;                  // a step of npairs Z tiles, in columns and rows
 
-  __device__ __forceinline__ TileList(const HeadArgs& p, int pair_, int npairs_) {
-    pair = pair_;
+  __device__ __forceinline__ TileList(const HeadArgs& p, int pair, int npairs_) {
     npairs = npairs_;
     live = *p.nlive;
     ntm = (live + kTile - 1) / kTile;
-    if (PHASE != kOut) {
-      ntn = (p.width + kTile - 1) / kTile;
-      group = p.group;
-    } else {
-      ntd = (p.dim + kTile - 1) / kTile;
-      ntv = (p.width + kTile - 1) / kTile;
-      const int kbp = (p.width + kBK - 1) / kBK;
-      kdh = (kbp + p.splits - 1) / p.splits;
-      kdw = (live + kBK - 1) / kBK;
-      const int ndh = p.want_dh ? ntm * ntd * p.splits : 0, ndw = p.want_dw ? ntv * ntd : 0;
-      first = kdh >= kdw ? 0 : 1;
-      n1 = first == 0 ? ndh : ndw;
-      n2 = first == 0 ? ndw : ndh;
-      const int k1 = first == 0 ? kdh : kdw, k2 = first == 0 ? kdw : kdh;
-      const int r = n1 % npairs;
-      e = r != 0 && k2 > 0 ? min((k1 + k2 / 2) / k2, n2 / (npairs - r)) : 0;
+    ntn = (p.z_width + kTile - 1) / kTile;
+    ntd = (p.dim + kTile - 1) / kTile;
+    z_step = npairs;
+    z_dn = ntm > 0 ? npairs / ntm : 0;
+    z_dm = npairs - z_dn * ntm;
+    const int kbp = (p.width + kBK - 1) / kBK;
+    kdh = (kbp + p.splits - 1) / p.splits;
+    if (PHASE == kStats) {                 // equal tiles: round robin
+      deal[0] = Deal{kZ, ntm * ntn, 0, 0, npairs, pair};
+      return;
+    }
+    int kind[3] = {kDh, kDw, kZ};
+    int n[3] = {p.want_dh && p.width > 0 ? ntm * ntd * p.splits : 0,
+                p.want_dw ? (p.width + kTile - 1) / kTile * ntd : 0, ntm * ntn};
+    int k[3] = {kdh, (live + kBK - 1) / kBK, (p.dim + kBK - 1) / kBK};
+#pragma unroll
+    for (int a = 0; a < 3; ++a)            // longest contraction first
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (k[b] < k[b + 1]) {
+          int t = k[b]; k[b] = k[b + 1]; k[b + 1] = t;
+          t = n[b]; n[b] = n[b + 1]; n[b + 1] = t;
+          t = kind[b]; kind[b] = kind[b + 1]; kind[b + 1] = t;
+        }
+    int cnt[4] = {npairs, 0, 0, 0}, load[4] = {0, 0, 0, 0}, first[4] = {0, 0, 0, 0}, groups = 1;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+      const int kc = max(k[c], 1);
+      int64_t total = (int64_t)n[c] * kc;
+      for (int g = 0; g < groups; ++g) total += (int64_t)cnt[g] * load[g];
+      int level = (int)(total / npairs), given, q[4];
+      for (;; level -= kc) {               // lower where a group is above the mean
+        given = 0;
+        for (int g = 0; g < groups; ++g) {
+          q[g] = max(0, (level - load[g]) / kc);
+          given += q[g] * cnt[g];
+        }
+        if (given <= n[c]) break;
+      }
+      Deal d{kind[c], n[c], 0, 0, 1, 0};
+      int base = 0, mine = 0;
+      for (int g = 0; g < groups; ++g) {
+        if (pair >= first[g] && pair < first[g] + cnt[g]) {
+          mine = g;
+          d.rounds = q[g];
+          d.base = base + pair - first[g];
+          d.stride = cnt[g];
+        }
+        base += q[g] * cnt[g];
+        load[g] += q[g] * kc;
+      }
+      // the rest, in order of load
+      int order[4] = {0, 1, 2, 3};
+      for (int a = 0; a < groups; ++a)
+        for (int b = 0; b + 1 < groups; ++b)
+          if (load[order[b]] > load[order[b + 1]]) {
+            const int t = order[b]; order[b] = order[b + 1]; order[b + 1] = t;
+          }
+      const int rest = n[c] - base, full = rest / npairs, extra = rest - full * npairs;
+      int before = 0, cut = -1, cut_at = 0;
+      for (int a = 0; a < groups; ++a) {
+        const int g = order[a];
+        if (g == mine) d.rest = base + before + pair - first[g];
+        load[g] += full * kc;
+        if (before + cnt[g] <= extra) {
+          load[g] += kc;
+        } else if (before < extra) {
+          cut = g;
+          cut_at = extra - before;
+        }
+        before += cnt[g];
+      }
+      if (cut >= 0 && groups < 4) {        // the front part of one group took one more
+        first[groups] = first[cut] + cut_at;
+        cnt[groups] = cnt[cut] - cut_at;
+        load[groups] = load[cut];
+        cnt[cut] = cut_at;
+        load[cut] += kc;
+        ++groups;
+      }
+      deal[c] = d;
     }
   }
 
-  __device__ __forceinline__ bool get(const HeadArgs& p, int j, HeadTile& t) const {
-    if (PHASE != kOut) {
-      const int idx = pair + j * npairs;
-      if (idx >= ntm * ntn) return false;
-      const int per = group * ntn, g = idx / per, in = idx - g * per;
-      const int rows = min(group, ntm - g * group);
-      t.kind = 0;
-      t.tn = in / rows;
-      t.tm = g * group + (in - t.tn * rows);
-      t.kb0 = 0;
-      t.nk = (p.dim + kBK - 1) / kBK;
-      t.split = 0;
-      return true;
-    }
-    const int r = n1 % npairs, mine = n1 / npairs + (pair < r ? 1 : 0);
-    int idx, kind;
-    if (j < mine) {
-      idx = pair + j * npairs;
-      kind = first;
-    } else {
-      const int q = j - mine, late = npairs - r;
-      kind = 1 - first;
-      if (pair >= r && q < e)
-        idx = (pair - r) + q * late;
-      else if (pair >= r)
-        idx = late * e + (pair - r) + (q - e) * npairs;
-      else
-        idx = late * e + late + pair + q * npairs;
-      if (idx >= n2) return false;
-    }
+  // Tiles of this pair in deal c, and the contraction of its i-th one.
+  __device__ __forceinline__ int tiles_of(int c) const {
+    const Deal& d = deal[c];
+    return d.rounds + (d.rest < d.count ? (d.count - d.rest - 1) / npairs + 1 : 0);
+  }
+  __device__ __forceinline__ int index_of(int c, int i) const {
+    const Deal& d = deal[c];
+    return i < d.rounds ? d.base + i * d.stride : d.rest + (i - d.rounds) * npairs;
+  }
+  __device__ __forceinline__ int blocks_of(const HeadArgs& p, int c, int i) const {
+    if (deal[c].kind == kZ) return (p.dim + kBK - 1) / kBK;
+    if (deal[c].kind == kDw) return (live + kBK - 1) / kBK;
+    const int split = p.splits == 1 ? 0 : index_of(c, i) / (ntm * ntd);
+    return max(0, min(kdh, (p.width + kBK - 1) / kBK - split * kdh));
+  }
+  // The tile of an index.  Z tiles are short, so a tile that lies `step` indices after the one
+  // in t, in the same group of rows, is found without a division.
+  __device__ __forceinline__ void locate(const HeadArgs& p, int kind, int idx, HeadTile& t) const {
     t.kind = kind;
-    if (kind == 0) {
+    t.kb0 = 0;
+    t.split = 0;
+    if (kind == kZ) {
+      // groups of `group` tile rows walk the columns together: a W panel is read once per
+      // group, and the group's rows of H stay in the L2
+      const int per = p.group * ntn, g = idx / per, in = idx - g * per;
+      const int rows = min(p.group, ntm - g * p.group);
+      t.tn = in / rows;
+      t.tm = g * p.group + (in - t.tn * rows);
+      t.nk = (p.dim + kBK - 1) / kBK;
+    } else if (kind == kDh) {
       t.tm = idx % ntm;
       const int rest = idx / ntm;
       t.tn = rest % ntd;
       t.split = rest / ntd;
       t.kb0 = t.split * kdh;
-      t.nk = min(kdh, (p.width + kBK - 1) / kBK - t.kb0);
-      if (t.nk < 0) t.nk = 0;
+      t.nk = max(0, min(kdh, (p.width + kBK - 1) / kBK - t.kb0));
     } else {
       t.tm = idx / ntd;
       t.tn = idx - t.tm * ntd;
-      t.split = 0;
-      t.kb0 = 0;
-      t.nk = kdw;
+      t.nk = (live + kBK - 1) / kBK;
     }
-    return true;
+  }
+};
+
+// Walks the tiles of a pair.
+template <int PHASE>
+struct TileWalk {
+  const TileList<PHASE>& l;
+  int c, i, left, idx;                     // deal, position in it, tiles left in it, index
+  HeadTile t;
+  bool have;
+  __device__ __forceinline__ TileWalk(const HeadArgs& p, const TileList<PHASE>& list) : l(list) {
+    c = -1;
+    i = left = idx = 0;
+    t = HeadTile{};
+    have = true;
+    next(p);
+  }
+  __device__ __forceinline__ void next(const HeadArgs& p) {
+    int kind = kZ, at = 0;
+    if (--left > 0) {
+      ++i;
+#pragma unroll
+      for (int k = 0; k < TileList<PHASE>::kKinds; ++k)
+        if (k == c) {
+          kind = l.deal[k].kind;
+          at = l.index_of(k, i);
+        }
+    } else {
+      left = 0;
+#pragma unroll
+      for (int k = 0; k < TileList<PHASE>::kKinds; ++k)
+        if (k > c && left == 0) {
+          left = l.tiles_of(k);
+          if (left > 0) {
+            c = k;
+            kind = l.deal[k].kind;
+            at = l.index_of(k, 0);
+          }
+        }
+      i = 0;
+      if (left == 0) {
+        have = false;
+        return;
+      }
+    }
+    const int step = at - idx;
+    idx = at;
+    // the common case of short tiles: the next one of the same, only group of rows
+    if (kind == kZ && t.kind == kZ && i > 0 && l.ntm <= p.group && step == l.z_step) {
+      t.tn += l.z_dn;
+      t.tm += l.z_dm;
+      if (t.tm >= l.ntm) {
+        t.tm -= l.ntm;
+        ++t.tn;
+      }
+      return;
+    }
+    l.locate(p, kind, at, t);
   }
 };
 
@@ -243,88 +372,95 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     // nothing runs: fall through to the teardown
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producers (both CTAs)
-    // Four lanes in lockstep, one round per two k-blocks: lane bit 1 picks the k-block of the
-    // round, lane bit 0 the operand.  The leader's A lane arms the stage's full barrier for
-    // the bytes of both CTAs.
-    if (lane < 4) {
-      const int par = lane >> 1, opnd = lane & 1;
-      int j = 0, kb = par;
-      HeadTile t{};
-      bool have = tiles.get(P, 0, t);
-      auto advance = [&]() {
-        while (have && kb >= t.nk) {
-          kb -= t.nk;
-          have = tiles.get(P, ++j, t);
-        }
-      };
-      advance();
-      uint32_t q = (uint32_t)par;  // position in the k-block sequence
+    // One thread issues both operands of every k-block: its copies have warp-uniform operands,
+    // where several issuing lanes make the compiler walk the lanes copy by copy (four lanes:
+    // 1.66 ms for a 768-wide training step of 8192 tokens, one lane 1.59).  The leader arms the
+    // stage's full barrier for the bytes of both CTAs.
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 1;             // of the empty barriers: the first round passes
       uint32_t armed = 0, last_par = 0;
-      for (;;) {
-        bool act = have && !*abort_flag;
-        if (!__any_sync(0xFu, act)) break;
-        const int stage = (int)(q % S);
-        const uint32_t ph = (q / S) & 1u;
-        if (act && !mbar_wait(bar(empty0 + stage), ph ^ 1u, g)) act = false;
-        const uint32_t fb_local = bar(full0 + stage), fb = map_rank(fb_local, 0);
-        const uint32_t dst = sbase + (uint32_t)stage * kHeadStageBytes + (opnd ? kHalf : 0u);
-        const int r0 = (opnd ? t.tn : t.tm) * kTile + 128 * (int)rank;
-        const int k0 = (t.kb0 + kb) * kBK;
-        expect_tx_p(act && leader && opnd == 0, fb_local, 2u * kHeadStageBytes);
-        if (PHASE != kOut) {
-          // A = H rows, B = W rows, both with the contraction contiguous
-          tma_load_pair_p(act, dst, opnd ? &P.w_k : &P.h_k, k0, opnd ? P.w_row0 + r0 : r0, fb);
-        } else {
-          // dH: A = G rows (K-major), B = W (its rows are the contraction: MN-major);
-          // dW: A = G and B = H, both MN-major with the tokens as the contraction
-          const bool dh = t.kind == 0;
-          tma_load_pair_p(act && dh && !opnd, dst, &P.g_k, k0, r0, fb);
-          tma_load_pair_p(act && dh && opnd, dst, &P.w_mn, r0, P.w_row0 + k0, fb);
-          tma_load_pair_p(act && dh && opnd, dst + kBoxBytes, &P.w_mn, r0 + 64, P.w_row0 + k0, fb);
-          tma_load3d_pair_p(act && !dh, dst, opnd ? &P.h_mn : &P.g_mn, 0, k0, r0 / 64, fb);
-        }
-        if (act && opnd == 0) {
+      bool ok = true;
+      for (TileWalk<PHASE> walk(P, tiles); walk.have && ok; walk.next(P)) {
+        const HeadTile& t = walk.t;
+        const int a0 = t.tm * kTile + 128 * (int)rank, b0 = t.tn * kTile + 128 * (int)rank;
+        for (int kb = 0; kb < t.nk; ++kb) {
+          if (!mbar_wait(bar(empty0 + stage), ph, g)) { ok = false; break; }
+          const uint32_t fb_local = bar(full0 + stage), fb = map_rank(fb_local, 0);
+          const uint32_t dst = sbase + (uint32_t)stage * kHeadStageBytes;
+          const int k0 = (t.kb0 + kb) * kBK;
+          expect_tx_p(leader, fb_local, 2u * kHeadStageBytes);
+          // Z: A = H rows, B = W rows, both with the contraction contiguous; dH: A = G rows
+          // (K-major), B = W (its rows are the contraction: MN-major); dW: A = G and B = H, both
+          // MN-major with the tokens as the contraction
+          if (PHASE == kStats || t.kind == kZ) {
+            tma_load_pair_p(true, dst, &P.h_k, k0, a0, fb);
+            tma_load_pair_p(true, dst + kHalf, &P.w_k, k0, P.z_w_row0 + b0, fb);
+          } else if (t.kind == kDh) {
+            tma_load_pair_p(true, dst, &P.g_k, k0, P.g_row0 + a0, fb);
+            if (P.w_3d) {
+              tma_load3d_pair_p(true, dst + kHalf, &P.w_mn, 0, P.w_row0 + k0, b0 / 64, fb);
+            } else {
+              tma_load_pair_p(true, dst + kHalf, &P.w_mn, b0, P.w_row0 + k0, fb);
+              tma_load_pair_p(true, dst + kHalf + kBoxBytes, &P.w_mn, b0 + 64, P.w_row0 + k0, fb);
+            }
+          } else {
+            tma_load3d_pair_p(true, dst, &P.g_mn, 0, P.g_row0 + k0, a0 / 64, fb);
+            tma_load3d_pair_p(true, dst + kHalf, &P.h_mn, 0, k0, b0 / 64, fb);
+          }
           armed |= 1u << stage;
-          last_par = (last_par & ~(1u << stage)) | (ph << stage);
+          last_par = (last_par & ~(1u << stage)) | ((ph ^ 1u) << stage);
+          if (++stage == S) { stage = 0; ph ^= 1u; }
         }
-        q += 2;
-        kb += 2;
-        advance();
       }
-      // teardown: the leader's full barriers count both CTAs' bytes (an even stage count gives
-      // each k-block parity its own stages)
+      // teardown: the leader's full barriers count both CTAs' bytes
       if (leader)
         for (int st = 0; st < S; ++st)
           if (armed & (1u << st)) mbar_wait(bar(full0 + st), (last_par >> st) & 1u, g, false);
     }
   } else if (warp == 1 && lane == 0 && leader) {
     // ------------------------------------------------------------ MMA issuer (leader only)
+    // One thread issues every MMA, so what it does between them has to stay below the MMAs' own
+    // time: the operands' storage is a constant of each loop, and of a tile it needs the number
+    // of k-blocks only.
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
-    HeadTile t{};
-    for (int j = 0; tiles.get(P, j, t); ++j) {
-      const int a_mn = PHASE == kOut && t.kind == 1, b_mn = PHASE == kOut;
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) |
-                             ((uint32_t)b_mn << 16) | ((uint32_t)(kTile >> 3) << 17) |
-                             ((uint32_t)(kTile >> 4) << 24);
-      if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
-      bool ok = true;
-      for (int kb = 0; kb < t.nk; ++kb) {
-        if (!mbar_wait(bar(full0 + stage), phase, g)) { ok = false; break; }
+    auto deal = [&](int c, auto a_mn, auto b_mn) -> bool {
+      constexpr int A = decltype(a_mn)::value, B = decltype(b_mn)::value;
+      constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A << 15) |
+                                 ((uint32_t)B << 16) | ((uint32_t)(kTile >> 3) << 17) |
+                                 ((uint32_t)(kTile >> 4) << 24);
+      const int n = tiles.tiles_of(c);
+      for (int i = 0; i < n; ++i) {
+        const int nk = tiles.blocks_of(P, c, i);
+        if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g)) return false;
         tc_fence_after();
-        const uint32_t sa = sbase + (uint32_t)stage * kHeadStageBytes;
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!mbar_wait(bar(full0 + stage), phase, g)) return false;
+          tc_fence_after();
+          const uint32_t sa = sbase + (uint32_t)stage * kHeadStageBytes;
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)
-          tc_mma_pair(d_tmem, operand_desc(sa, a_mn, k), operand_desc(sa + kHalf, b_mn, k), idesc,
-                      (kb | k) != 0);
-        tc_commit_pair(bar(empty0 + stage), 0x3);
-        if (++stage == S) { stage = 0; phase ^= 1u; }
+          for (int k = 0; k < kBK / 16; ++k)
+            tc_mma_pair(d_tmem, operand_desc(sa, A, k), operand_desc(sa + kHalf, B, k), idesc,
+                        (kb | k) != 0);
+          tc_commit_pair(bar(empty0 + stage), 0x3);
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        tc_commit_pair(bar(tfull0 + acc), 0x3);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
-      if (!ok) break;
-      tc_commit_pair(bar(tfull0 + acc), 0x3);
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      return true;
+    };
+    using K0 = std::integral_constant<int, 0>;
+    using K1 = std::integral_constant<int, 1>;
+#pragma unroll
+    for (int c = 0; c < TileList<PHASE>::kKinds; ++c) {
+      const int kind = tiles.deal[c].kind;
+      if (!(PHASE == kStats || kind == kZ ? deal(c, K0(), K0())
+            : kind == kDh                ? deal(c, K0(), K1())
+                                         : deal(c, K1(), K1())))
+        break;
     }
     tc_commit_pair(bar(drain), 0x1);
     mbar_wait(bar(drain), 0u, g, false);
@@ -336,21 +472,21 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     uint32_t nstore = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
-    HeadTile t{};
-    for (int j = 0; tiles.get(P, j, t); ++j) {
+    for (TileWalk<PHASE> walk(P, tiles); walk.have; walk.next(P)) {
+      const HeadTile& t = walk.t;
       const int rw = t.tm * kTile + 128 * (int)rank + quarter * 32, r = rw + lane;
       const int cb = t.tn * kTile + half * 128;   // first column of this warp
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
                              (uint32_t)(acc * kTile + half * 128);
       if (PHASE == kStats) {
         const bool live = r < tiles.live;
-        const int lab = live ? P.label[r] - P.v0 : -1;
+        const int lab = live ? P.label[r] - P.z_v0 : -1;
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
         float m = -INFINITY, s = 0.f;
         // chunks of this warp with columns (and rows); the next one's load from tensor memory
         // is in flight while one is reduced
-        const int nq = rw < tiles.live ? min(kHeadChunks, (P.width - cb + 31) / 32) : 0;
+        const int nq = rw < tiles.live ? min(kHeadChunks, (P.z_width - cb + 31) / 32) : 0;
         uint32_t buf[2][32];
         if (nq > 0) tc_ld32_issue(taddr, buf[0]);
 #pragma unroll
@@ -360,7 +496,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
             uint32_t (&a32)[32] = buf[q & 1];
             tc_ld_wait(a32);
             if (q + 1 < nq) tc_ld32_issue(taddr + (uint32_t)(32 * (q + 1)), buf[(q + 1) & 1]);
-            const int c0 = cb + 32 * q, left = P.width - c0;
+            const int c0 = cb + 32 * q, left = P.z_width - c0;
             if (left < 32) {                              // columns past the end take no part
 #pragma unroll
               for (int k = 0; k < 32; ++k)
@@ -384,16 +520,16 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
             m = mc;
           }
         }
-        if (live && cb < P.width) P.part[(int64_t)(t.tn * 2 + half) * P.rows + r] = make_float2(m, s);
-      } else if (PHASE == kGrad) {
+        if (live && cb < P.z_width) P.part[(int64_t)(t.tn * 2 + half) * P.rows + r] = make_float2(m, s);
+      } else if (t.kind == kZ) {
         const bool live = r < tiles.live;
-        const int lab = live ? P.label[r] - P.v0 : -1;
+        const int lab = live ? P.label[r] - P.z_v0 : -1;
         // a row that holds no token: exp2(z - inf) = 0
         const float lse2 = live ? P.lse2[r] : INFINITY, dl = live ? P.dl[r] : 0.f;
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
         // whole k-blocks of G are written: the columns past the end are zero
-        const int nq = min(kHeadChunks, ((P.width + kBK - 1) / kBK * kBK - cb + 31) / 32);
+        const int nq = min(kHeadChunks, ((P.z_width + kBK - 1) / kBK * kBK - cb + 31) / 32);
         uint32_t buf[2][32];
         if (nq > 0) tc_ld32_issue(taddr, buf[0]);
 #pragma unroll
@@ -402,11 +538,17 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
             __syncwarp();
             uint32_t (&a32)[32] = buf[q & 1];
             const uint32_t stg = stg0 + (nstore & 1u) * 2048u;
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            // the halves alternate; a store before this tile may have used both
+            if (lane == 0) {
+              if (q == 0)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              else
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            }
             __syncwarp();
             tc_ld_wait(a32);
             if (q + 1 < nq) tc_ld32_issue(taddr + (uint32_t)(32 * (q + 1)), buf[(q + 1) & 1]);
-            const int c0 = cb + 32 * q, left = P.width - c0, hit = lab - c0;
+            const int c0 = cb + 32 * q, left = P.z_width - c0, hit = lab - c0;
             float v[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = ex2(fmaf(__uint_as_float(a32[k]), kLog2e, -lse2));
@@ -431,7 +573,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-              tma_store_block(&P.g_st, stg, c0, rw);
+              tma_store_block(&P.g_st, stg, c0, P.z_g_row0 + rw);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
             ++nstore;
@@ -440,7 +582,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
       } else {
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
-        const int row_end = t.kind == 0 ? tiles.live : P.width;
+        const int row_end = t.kind == kDh ? tiles.live : P.width;
 #pragma unroll 1
         for (int q = 0; q < kHeadChunks; ++q) {
           const int c0 = cb + 32 * q;
@@ -457,7 +599,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
           tc_ld_wait(a32);
-          if (t.kind == 0) {
+          if (t.kind == kDh) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               sts128(stg0 + stg32_off(lane, k),
@@ -473,7 +615,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
               sts128(stg0 + stg_off(lane, k), make_uint4(w[0], w[1], w[2], w[3]));
             }
           }
-          if (t.kind == 1 && !P.dw_tma) {
+          if (t.kind == kDw && !P.dw_tma) {
             // rows without 16-byte alignment: a warp writes one row of the block at a time
             __syncwarp();
             for (int i = 0; i < 32; ++i) {
@@ -488,7 +630,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            if (t.kind == 1)
+            if (t.kind == kDw)
               tma_store_block(&P.dw_st, stg0, c0, P.v0 + rw);
             else if (P.add)
               tma_reduce_add_block(&P.acc_st, stg0, c0, t.split * P.rows + rw);
@@ -974,59 +1116,41 @@ struct HeadShape {
   int64_t piece, pieces;                   // columns per piece
   int64_t splits;                          // dH slices
   int64_t kdh;                             // fp32: columns per dH slice
+  int64_t buffers;                         // pieces of G (and of a copied W) held at a time
 };
 
 struct HeadLayout {
   size_t nlive, label, pos, token, lse2, dl, zlab, state, hc, part, g, acc, wcopy, descs, total;
 };
 
-constexpr int64_t kGElems = 96ll << 20;    // entries of G (or of Z) per piece
+constexpr int64_t kWorkBytes = 390ll << 20;  // what the backward pass's buffers may come to
+constexpr int64_t kMinElems = 32ll << 20;  // least entries of G per piece
+constexpr int64_t kZElems = 64ll << 20;    // entries of Z (fp32), or of a copied W, per piece
 constexpr int64_t kPartBytes = 64ll << 20; // bytes of the forward partials per piece
-constexpr int64_t kSliceBytes = 64ll << 20;   // bytes of dH's slices beyond the first
 constexpr int kMaxSplits = 64;
 constexpr int kFewBlocks = 1024;           // blocks of the few-token kernel (bounds its workspace)
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
 
-// Columns per piece: whole tiles, at least 4096 columns, at most about kGElems entries.  Wider
-// pieces mean fewer launches and fewer passes over dH's sums; narrower ones a smaller workspace.
+// Columns per piece, whole tiles.  Every piece is a launch whose last wave and ramp cost some
+// 20 us, so the backward pass takes what the rows of H and the sums of dH leave of kWorkBytes
+// for its two pieces of G: 8192 tokens x 768 ran in 1.54 ms with 48 Mi entries per piece and in
+// 1.53 with 96, 4096 tokens x 4096 in 7.41 and 7.23.
 int64_t piece_columns(const HeadShape& s, int64_t asked) {
   int64_t c;
-  if (asked > 0)
+  if (asked > 0) {
     c = asked;
-  else if (s.backward || s.dtype == MFSDP_DTYPE_F32)
-    c = std::max<int64_t>(kGElems / s.rows, 4096);
-  else if (s.copy_w)
-    c = std::max<int64_t>(kGElems / s.pitch, 4096);
-  else
+  } else if (s.dtype == MFSDP_DTYPE_F32) {
+    c = std::max<int64_t>(kZElems / s.rows, 4096);
+  } else if (s.backward) {
+    const int64_t fixed = s.rows * s.pitch * (2 + 4);
+    c = std::max<int64_t>(std::max(kMinElems, (kWorkBytes - fixed) / 4) / s.rows, 4096);
+  } else if (s.copy_w) {
+    c = std::max<int64_t>(kZElems / s.pitch, 4096);
+  } else {
     c = std::max<int64_t>(kPartBytes / (8 * s.rows) * 128, 4096);
+  }
   c = up(c, kTile);
   return std::min(c, up(s.vocab, kTile));
-}
-
-// Modelled time of the backward pass, in k-blocks of a pair: the waves of the logits' tiles, and
-// the longer of the two kinds of pairs in TileList's order for the products (kLaunchCost per
-// launch: its ramp and its last epilogue).
-constexpr int64_t kLaunchCost = 12;
-double model_time(const HeadShape& s, int64_t piece, int64_t splits, int64_t pairs) {
-  const int64_t ntm = cdiv(s.n, kTile), ntd = cdiv(s.dim, kTile), kd = cdiv(s.dim, kBK);
-  const int64_t kn = cdiv(s.n, kBK);
-  auto one = [&](int64_t width) -> int64_t {
-    const int64_t ntn = cdiv(width, kTile);
-    const int64_t kdh = cdiv(cdiv(width, kBK), splits);
-    int64_t n1 = ntm * ntd * splits, k1 = kdh, n2 = ntn * ntd, k2 = kn;
-    if (k1 < k2) {
-      std::swap(n1, n2);
-      std::swap(k1, k2);
-    }
-    const int64_t r = n1 % pairs, late = pairs - r;
-    const int64_t e = r ? std::min((k1 + k2 / 2) / k2, n2 / late) : 0;
-    const int64_t rest = n2 - (r ? late * e : 0), full = rest / pairs, rem = rest % pairs;
-    int64_t t = n1 / pairs * k1 + (e + full + (rem > 0)) * k2;
-    if (r) t = std::max(t, (n1 / pairs + 1) * k1 + (full + (rem > late)) * k2);
-    return cdiv(ntm * ntn, pairs) * kd + t + 2 * kLaunchCost;
-  };
-  const int64_t whole = s.vocab / piece, last = s.vocab % piece;
-  return (double)(whole * one(piece) + (last ? one(last) : 0));
 }
 
 HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool backward,
@@ -1046,36 +1170,16 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   s.piece = piece_columns(s, piece);
   s.pieces = cdiv(vocab, s.piece);
   s.splits = 1;
+  s.buffers = 1;
   if (backward) {
     // dH has few tiles when there are few tokens: cut its contraction (the piece's columns)
     // until the tiles fill the GPU; a slice keeps at least 1024 columns
     const int64_t units = bf ? sms / 2 : sms;
     const int64_t tiles = cdiv(std::max<int64_t>(n, 1), bf ? kTile : 128) * cdiv(dim, kTile);
-    auto cut = [&](int64_t splits) {
-      splits = std::max<int64_t>(1, std::min({splits, s.piece / 1024, (int64_t)kMaxSplits}));
-      s.kdh = up(cdiv(s.piece, splits), kBK);
-      s.splits = cdiv(s.piece, s.kdh);
-    };
-    cut(cdiv(units, tiles));
-    if (bf && piece == 0 && s.pieces > 1) {
-      // several pieces: the launches' last waves cost most where tiles are few, so take the
-      // piece (down to half of the largest) and the cut of dH with the least modelled time
-      const int64_t most = s.piece;
-      double best = 0;
-      int64_t best_piece = s.piece, best_splits = 1;
-      for (int64_t c = most; c >= std::max<int64_t>(most / 2, kTile); c -= kTile)
-        for (int64_t k = 1; k <= 4 && (k - 1) * s.rows * s.pitch * 4 <= kSliceBytes; ++k) {
-          const double t = model_time(s, c, k, units);
-          if (best == 0 || t < best) {
-            best = t;
-            best_piece = c;
-            best_splits = k;
-          }
-        }
-      s.piece = best_piece;
-      s.pieces = cdiv(vocab, s.piece);
-      cut(best_splits);
-    }
+    s.splits = std::max<int64_t>(1, std::min({cdiv(units, tiles), s.piece / 1024, (int64_t)kMaxSplits}));
+    s.kdh = up(cdiv(s.piece, s.splits), kBK);
+    s.splits = cdiv(s.piece, s.kdh);
+    s.buffers = bf && s.pieces > 1 ? 2 : 1;
   }
   return s;
 }
@@ -1107,9 +1211,9 @@ HeadLayout head_layout(const HeadShape& s) {
   l.state = take(s.rows * 8);
   l.hc = take(s.rows * s.pitch * es);
   l.part = take(!s.backward && bf ? cdiv(s.piece, 128) * s.rows * 8 : 0);
-  l.g = take(s.backward || !bf ? s.rows * s.piece * es : 0);
+  l.g = take(s.backward || !bf ? s.buffers * s.rows * s.piece * es : 0);
   l.acc = take(s.backward ? s.splits * s.rows * s.pitch * 4 : 0);
-  l.wcopy = take(s.copy_w ? s.piece * s.pitch * 2 : 0);
+  l.wcopy = take(s.copy_w ? s.buffers * s.piece * s.pitch * 2 : 0);
   l.descs = take(bf ? 0 : (int64_t)sizeof(GemmDesc) * (s.pieces * (2 + s.splits)));
   l.total = off;
   return l;
@@ -1123,8 +1227,8 @@ int head_pairs(int sms) {
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
   int n = dev < kCached ? cache[dev].load() : 0;
   if (n > 0) return n;
-  const void* kernels[3] = {(const void*)head_gemm_kernel<kStats>, (const void*)head_gemm_kernel<kGrad>,
-                            (const void*)head_gemm_kernel<kOut>};
+  const void* kernels[2] = {(const void*)head_gemm_kernel<kStats>,
+                            (const void*)head_gemm_kernel<kGrads>};
   for (const void* k : kernels)
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHeadSmem) !=
         cudaSuccess)
@@ -1140,7 +1244,7 @@ int head_pairs(int sms) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel<kOut>, &cfg) != cudaSuccess || n < 1)
+  if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel<kGrads>, &cfg) != cudaSuccess || n < 1)
     return -1;
   if (dev < kCached) cache[dev].store(n);
   return n;
@@ -1291,15 +1395,17 @@ struct HeadCall {
     const uint16_t* hc = at<uint16_t>(l.hc);
     bool ok = encode_map(&a.h_k, hc, s.rows, s.pitch, s.pitch, 128u);
     const void* wsrc = s.copy_w ? (const void*)at<uint16_t>(l.wcopy) : weight;
-    const int64_t wrows = s.copy_w ? s.piece : s.vocab, wld = s.copy_w ? s.pitch : ld_w;
+    const int64_t wrows = s.copy_w ? s.buffers * s.piece : s.vocab, wld = s.copy_w ? s.pitch : ld_w;
     ok = ok && encode_map(&a.w_k, wsrc, wrows, s.dim, wld, 128u);
     if (s.backward) {
       ok = ok && encode_map3d(&a.h_mn, hc, s.rows, s.pitch, s.pitch);
-      ok = ok && encode_map(&a.w_mn, wsrc, wrows, s.dim, wld, 64u);
+      a.w_3d = s.dim % 64 == 0;
+      ok = ok && (a.w_3d ? encode_map3d(&a.w_mn, wsrc, wrows, s.dim, wld)
+                         : encode_map(&a.w_mn, wsrc, wrows, s.dim, wld, 64u));
       const uint16_t* g = at<uint16_t>(l.g);
-      ok = ok && encode_map(&a.g_k, g, s.rows, s.piece, s.piece, 128u);
-      ok = ok && encode_map3d(&a.g_mn, g, s.rows, s.piece, s.piece);
-      ok = ok && encode_map(&a.g_st, g, s.rows, s.piece, s.piece, 32u, 32u, false);
+      ok = ok && encode_map(&a.g_k, g, s.buffers * s.rows, s.piece, s.piece, 128u);
+      ok = ok && encode_map3d(&a.g_mn, g, s.buffers * s.rows, s.piece, s.piece);
+      ok = ok && encode_map(&a.g_st, g, s.buffers * s.rows, s.piece, s.piece, 32u, 32u, false);
       if (dh) ok = ok && encode_map_f32(&a.acc_st, at<float>(l.acc), s.splits * s.rows, s.pitch, s.pitch, 32u);
       a.dw_tma = dw && aligned_to(dw, 16) && ld_dw % 8 == 0;
       if (a.dw_tma) ok = ok && encode_map(&a.dw_st, dw, s.vocab, s.dim, ld_dw, 32u, 32u, false);
@@ -1324,20 +1430,26 @@ struct HeadCall {
     a.wait_limit_ns = wait_limit_ns();
     a.status = status;
     const int64_t ntm = cdiv(s.n, kTile), ntd = cdiv(s.dim, kTile);
+    // piece i as the one whose Z is computed
+    auto set_z = [&](int64_t i) {
+      a.z_v0 = (int32_t)(i * s.piece);
+      a.z_width = i < s.pieces ? (int32_t)std::min(s.piece, s.vocab - i * s.piece) : 0;
+      a.z_w_row0 = s.copy_w ? (int32_t)(i % s.buffers * s.piece) : a.z_v0;
+      a.z_g_row0 = (int32_t)(i % s.buffers * s.rows);
+      if (i >= s.pieces || !s.copy_w) return cudaSuccess;
+      return launch_pdl(head_copy_rows_kernel, dim3((unsigned)up(a.z_width, kBK)), dim3(256), 0, st,
+                        static_cast<const uint16_t*>(weight) + (int64_t)a.z_v0 * ld_w, ld_w,
+                        at<uint16_t>(l.wcopy) + (int64_t)a.z_w_row0 * s.pitch, s.pitch,
+                        (int)a.z_width, (int)s.dim);
+    };
+    auto z_tiles = [&] { return ntm * cdiv(a.z_width, kTile); };
     cudaError_t e = gather();
+    if (e == cudaSuccess) e = set_z(0);
+    if (s.backward && e == cudaSuccess) e = launch_head<kGrads>(a, z_tiles(), pairs, st);
     for (int64_t i = 0; i < s.pieces && e == cudaSuccess; ++i) {
-      a.v0 = (int32_t)(i * s.piece);
-      a.width = (int32_t)std::min(s.piece, s.vocab - i * s.piece);
-      a.w_row0 = s.copy_w ? 0 : a.v0;
-      a.add = i > 0;
-      if (s.copy_w)
-        e = launch_pdl(head_copy_rows_kernel, dim3((unsigned)up(a.width, kBK)), dim3(256), 0, st,
-                       static_cast<const uint16_t*>(weight) + (int64_t)a.v0 * ld_w, ld_w,
-                       at<uint16_t>(l.wcopy), s.pitch, (int)a.width, (int)s.dim);
-      const int64_t ntn = cdiv(a.width, kTile);
-      if (e != cudaSuccess) break;
       if (!s.backward) {
-        e = launch_head<kStats>(a, ntm * ntn, pairs, st);
+        if (i > 0) e = set_z(i);
+        if (e == cudaSuccess) e = launch_head<kStats>(a, z_tiles(), pairs, st);
         if (e != cudaSuccess) break;
         JoinArgs j{};
         j.part = a.part;
@@ -1347,16 +1459,21 @@ struct HeadCall {
         j.token = at<int32_t>(l.token);
         j.loss = loss;
         j.lse = lse;
-        j.parts = (int32_t)cdiv(a.width, 128);
+        j.parts = (int32_t)cdiv(a.z_width, 128);
         j.rows = a.rows;
         j.first = i == 0;
         j.last = i == s.pieces - 1;
         e = launch_pdl(head_join_kernel, dim3((unsigned)cdiv(s.n, 32)), dim3(1024), 0, st, j);
       } else {
-        e = launch_head<kGrad>(a, ntm * ntn, pairs, st);
+        a.v0 = a.z_v0;
+        a.width = a.z_width;
+        a.w_row0 = a.z_w_row0;
+        a.g_row0 = a.z_g_row0;
+        a.add = i > 0;
+        e = set_z(i + 1);
         if (e != cudaSuccess) break;
-        const int64_t tiles = (dh ? ntm * ntd * s.splits : 0) + (dw ? ntn * ntd : 0);
-        e = launch_head<kOut>(a, tiles, pairs, st);
+        const int64_t tiles = (dh ? ntm * ntd * s.splits : 0) + (dw ? cdiv(a.width, kTile) * ntd : 0);
+        e = launch_head<kGrads>(a, tiles + z_tiles(), pairs, st);
       }
     }
     if (e == cudaSuccess && dh) e = finish();
