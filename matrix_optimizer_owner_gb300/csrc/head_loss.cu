@@ -9,7 +9,8 @@
 // launch then joins the tiles' pairs.  Backward walks the vocabulary in pieces: it recomputes a
 // piece of Z from the same operands, writes that piece of G (bf16 operands: the only rounding
 // between the inputs and the gradients, within 2^-8 of an entry, the precision the product's
-// other factor has), and multiplies it with W's rows for dH and with H for that piece's rows of
+// other factor has; dloss enters as its ratio to the largest |dloss|, which the gradients are
+// multiplied with in fp32 at the end, so a uniform dloss is not rounded at all), and multiplies it with W's rows for dH and with H for that piece's rows of
 // dW.  dH is summed over the pieces in fp32.  One launch multiplies a piece of G and computes
 // the next one (two pieces are kept): the many short tiles of Z fill the SMs that the few long
 // ones of dH and dW would leave idle at a launch's end.
@@ -47,6 +48,11 @@ constexpr uint32_t kHeadBars = kHeadStaging + kHeadEpiWarps * kStagePerWarp;
 constexpr uint32_t kHeadSmem = 1024 + kHeadBars + 256;
 static_assert(kHeadSmem <= 227 * 1024, "shared memory");
 constexpr float kLog2e = 1.4426950408889634f;
+// k-blocks added up in tensor memory before the epilogue adds them in registers (forward only).
+// The tensor cores' fp32 accumulation does not round to nearest: each of the K / 16 additions
+// cuts towards zero, which shrinks a logit by some 2e-9 K of itself.  1024 of K per chunk keeps
+// loss and lse within about 1e-6 at any width; the backward pass rounds to bf16 after it.
+constexpr int kSumBlocks = 16;
 
 enum Phase : int { kStats = 0, kGrads = 1 };
 enum Kind : int { kDh = 0, kDw = 1, kZ = 2 };  // tiles of a kGrads launch (kStats: kZ only)
@@ -61,6 +67,9 @@ struct HeadArgs {
   const int32_t* label;                    // [rows] of the compacted rows
   const float* lse2;                       // [rows] lse * log2(e)
   const float* dl;                         // [rows] dloss
+  const float* dl_max;                     // [dl_blocks] largest finite |dloss| per gather block
+  float* scale;                            // the largest of them, for the last launch
+  int32_t dl_blocks;
   float2* part;                            // [column half-tiles][rows] (max, sum)
   float* zlab;                             // [rows] the label's logit
   uint16_t* dw;                            // unaligned dW rows (dw_tma == 0)
@@ -306,6 +315,22 @@ __device__ __forceinline__ uint32_t stg32_off(int r, int k) {
   return (uint32_t)(r * 128 + ((k ^ (r & 7)) << 4));
 }
 
+// 16 consecutive fp32 columns of this thread's TMEM lane; waits for the load to land.
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // 2^x to about 2 ulp, one instruction (results below 2^-126 are 0): the terms of a softmax sum.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -432,23 +457,27 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
                                  ((uint32_t)(kTile >> 4) << 24);
       const int n = tiles.tiles_of(c);
       for (int i = 0; i < n; ++i) {
-        const int nk = tiles.blocks_of(P, c, i);
-        if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g)) return false;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(bar(full0 + stage), phase, g)) return false;
+        int left = tiles.blocks_of(P, c, i);
+        do {                                              // once, or a chunk at a time (kStats)
+          const int nk = PHASE == kStats ? min(left, kSumBlocks) : left;
+          left -= nk;
+          if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g)) return false;
           tc_fence_after();
-          const uint32_t sa = sbase + (uint32_t)stage * kHeadStageBytes;
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTile);
+          for (int kb = 0; kb < nk; ++kb) {
+            if (!mbar_wait(bar(full0 + stage), phase, g)) return false;
+            tc_fence_after();
+            const uint32_t sa = sbase + (uint32_t)stage * kHeadStageBytes;
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            tc_mma_pair(d_tmem, operand_desc(sa, A, k), operand_desc(sa + kHalf, B, k), idesc,
-                        (kb | k) != 0);
-          tc_commit_pair(bar(empty0 + stage), 0x3);
-          if (++stage == S) { stage = 0; phase ^= 1u; }
-        }
-        tc_commit_pair(bar(tfull0 + acc), 0x3);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            for (int k = 0; k < kBK / 16; ++k)
+              tc_mma_pair(d_tmem, operand_desc(sa, A, k), operand_desc(sa + kHalf, B, k), idesc,
+                          (kb | k) != 0);
+            tc_commit_pair(bar(empty0 + stage), 0x3);
+            if (++stage == S) { stage = 0; phase ^= 1u; }
+          }
+          tc_commit_pair(bar(tfull0 + acc), 0x3);
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        } while (left > 0);
       }
       return true;
     };
@@ -472,30 +501,63 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     uint32_t nstore = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
+    float scale = 0.f;                          // largest finite |dloss|
+    if (PHASE == kGrads) {
+      for (int i = lane; i < P.dl_blocks; i += 32) scale = fmaxf(scale, P.dl_max[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) scale = fmaxf(scale, __shfl_xor_sync(0xFFFFFFFFu, scale, o));
+      if (blockIdx.x == 0 && warp == 2 && lane == 0) *P.scale = scale;
+    }
     for (TileWalk<PHASE> walk(P, tiles); walk.have; walk.next(P)) {
       const HeadTile& t = walk.t;
       const int rw = t.tm * kTile + 128 * (int)rank + quarter * 32, r = rw + lane;
       const int cb = t.tn * kTile + half * 128;   // first column of this warp
-      const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                             (uint32_t)(acc * kTile + half * 128);
+      auto taddr_of = [&](int a) {
+        return tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(a * kTile + half * 128);
+      };
+      const uint32_t taddr = taddr_of(acc);
       if (PHASE == kStats) {
         const bool live = r < tiles.live;
         const int lab = live ? P.label[r] - P.z_v0 : -1;
-        if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
-        tc_fence_after();
         float m = -INFINITY, s = 0.f;
-        // chunks of this warp with columns (and rows); the next one's load from tensor memory
-        // is in flight while one is reduced
+        // chunks of columns of this warp that hold columns (and rows)
         const int nq = rw < tiles.live ? min(kHeadChunks, (P.z_width - cb + 31) / 32) : 0;
-        uint32_t buf[2][32];
-        if (nq > 0) tc_ld32_issue(taddr, buf[0]);
+        uint32_t sum[kHeadChunks][32];
+        bool ok = true;
+        for (int left = t.nk, first = 1; left > 0; left -= kSumBlocks, first = 0) {
+          if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t ta = taddr_of(acc);
+          if (first) {
+#pragma unroll
+            for (int q = 0; q < kHeadChunks; ++q)
+              if (q < nq) tc_ld32_issue(ta + (uint32_t)(32 * q), sum[q]);  // warp-uniform
+#pragma unroll
+            for (int q = 0; q < kHeadChunks; ++q)
+              if (q < nq) tc_ld_wait(sum[q]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2 * kHeadChunks; ++q)
+              if (q < 2 * nq) {
+                float part[16];                           // (32 at a time would spill)
+                tc_ld16(ta + (uint32_t)(16 * q), part);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  uint32_t& a = sum[q >> 1][(q & 1) * 16 + k];
+                  a = __float_as_uint(__uint_as_float(a) + part[k]);
+                }
+              }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_rank(bar(tempty0 + acc), 0));
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        }
+        if (!ok) break;
 #pragma unroll
         for (int q = 0; q < kHeadChunks; ++q) {
           if (q < nq) {                                   // warp-uniform
-            __syncwarp();
-            uint32_t (&a32)[32] = buf[q & 1];
-            tc_ld_wait(a32);
-            if (q + 1 < nq) tc_ld32_issue(taddr + (uint32_t)(32 * (q + 1)), buf[(q + 1) & 1]);
+            uint32_t (&a32)[32] = sum[q];
             const int c0 = cb + 32 * q, left = P.z_width - c0;
             if (left < 32) {                              // columns past the end take no part
 #pragma unroll
@@ -521,11 +583,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           }
         }
         if (live && cb < P.z_width) P.part[(int64_t)(t.tn * 2 + half) * P.rows + r] = make_float2(m, s);
+        continue;                                         // the accumulators are released
       } else if (t.kind == kZ) {
         const bool live = r < tiles.live;
         const int lab = live ? P.label[r] - P.z_v0 : -1;
         // a row that holds no token: exp2(z - inf) = 0
-        const float lse2 = live ? P.lse2[r] : INFINITY, dl = live ? P.dl[r] : 0.f;
+        const float lse2 = live ? P.lse2[r] : INFINITY;
+        const float dl = live && scale > 0.f ? P.dl[r] / scale : 0.f;
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
         // whole k-blocks of G are written: the columns past the end are zero
@@ -610,8 +674,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
               uint32_t w[4];
 #pragma unroll
               for (int h = 0; h < 4; ++h)
-                w[h] = pack_bf16x2(__uint_as_float(a32[8 * k + 2 * h]),
-                                   __uint_as_float(a32[8 * k + 2 * h + 1]));
+                w[h] = pack_bf16x2(__uint_as_float(a32[8 * k + 2 * h]) * scale,
+                                   __uint_as_float(a32[8 * k + 2 * h + 1]) * scale);
               sts128(stg0 + stg_off(lane, k), make_uint4(w[0], w[1], w[2], w[3]));
             }
           }
@@ -675,7 +739,7 @@ struct GatherArgs {
   int32_t* pos;                            // [n] compacted row of a token, -1: dropped
   int32_t* token;                          // [rows] token of a compacted row
   const float *lse_in, *dloss;             // backward
-  float *lse2, *dl;
+  float *lse2, *dl, *dl_max;
   float *loss, *lse;                       // forward: zeroed for dropped tokens
   int* status;
 };
@@ -709,6 +773,7 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
   for (int i = 0; i < 8; ++i) base += red[i];
   if (p.place) base = t0;
   T* hc = static_cast<T*>(p.hc);
+  float top = 0.f;                         // largest finite |dloss| of this thread's live tokens
   for (int b = t0; b < t1; b += 256) {     // 256 tokens at a time
     __syncthreads();
     const int t = b + tid;
@@ -734,7 +799,9 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
         p.label[base + off] = live ? (int32_t)lab : -1;
         p.token[base + off] = t;
         if (p.dl) {
-          p.dl[base + off] = live ? p.dloss[t] : 0.f;
+          const float dl = live ? p.dloss[t] : 0.f;
+          p.dl[base + off] = dl;
+          if (fabsf(dl) < INFINITY) top = fmaxf(top, fabsf(dl));
           p.lse2[base + off] = live ? p.lse_in[t] * kLog2e : 0.f;
         }
       }
@@ -761,6 +828,18 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
       }
     }
     base += total;
+  }
+  if (p.dl_max) {
+    __shared__ float tops[8];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, tops[i]);
+      p.dl_max[blockIdx.x] = top;
+    }
   }
   if (blockIdx.x != gridDim.x - 1) return;
   if (tid == 0) {
@@ -968,6 +1047,7 @@ __global__ void __launch_bounds__(32 * kFewTokens) head_few_join_kernel(const __
 // ---------------------------------------------------------------- dH: slices to the caller's rows
 struct FinishArgs {
   const float* acc;                        // [splits][rows][pitch]
+  const float* scale;                      // nullable
   const int32_t* pos;
   void* dh;
   int64_t ld_dh;
@@ -980,6 +1060,7 @@ __global__ void __launch_bounds__(128) head_finish_kernel(const __grid_constant_
   pdl_wait();
   const int t = blockIdx.x;
   const int r = p.pos[t];
+  const float scale = p.scale ? *p.scale : 1.f;
   T* out = static_cast<T*>(p.dh) + (int64_t)t * p.ld_dh;
   const int64_t slice = (int64_t)p.rows * p.pitch;
   const float* a = p.acc + (int64_t)(r < 0 ? 0 : r) * p.pitch;
@@ -995,6 +1076,8 @@ __global__ void __launch_bounds__(128) head_finish_kernel(const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] += x[k];
         }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= scale;
       Pack8<T> o;
       o.set(v);
       o.store(out + e);
@@ -1004,7 +1087,7 @@ __global__ void __launch_bounds__(128) head_finish_kernel(const __grid_constant_
       float v = 0.f;
       if (r >= 0)
         for (int s = 0; s < p.splits; ++s) v += a[s * slice + e];
-      out[e] = from_f32<T>(v);
+      out[e] = from_f32<T>(v * scale);
     }
   }
 }
@@ -1064,29 +1147,58 @@ __global__ void __launch_bounds__(256) head_stats32_kernel(const __grid_constant
 
 struct Grad32Args {
   float* z;                                // [rows][ldz]: Z in, G out
+  float* gt;                               // nullable: [columns][ldt], G transposed
   const int32_t* label;
   const float *lse2, *dl;
-  int32_t width, v0;
-  int64_t ldz;
+  int32_t rows, width, v0;
+  int64_t ldz, ldt;
 };
 
+// A 32 x 32 block of Z to G, in place and transposed.
 __global__ void __launch_bounds__(256) head_grad32_kernel(const __grid_constant__ Grad32Args p) {
+  __shared__ float tile[32][33];
   pdl_launch();
   pdl_wait();
-  const int r = blockIdx.x;
-  float* z = p.z + (int64_t)r * p.ldz;
-  const bool live = p.label[r] >= 0;
-  const float lse2 = p.lse2[r], dl = p.dl[r];
-  const int lab = live ? p.label[r] - p.v0 : -1;
-  for (int c = threadIdx.x; c < p.width; c += 256) {
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, nc = (p.width + 31) / 32;
+  const int c0 = (int)(blockIdx.x % nc) * 32, r0 = (int)(blockIdx.x / nc) * 32;
+#pragma unroll
+  for (int i = y; i < 32; i += 8) {
+    const int r = r0 + i, c = c0 + x;
+    if (r >= p.rows || c >= p.width) continue;
+    float* z = p.z + (int64_t)r * p.ldz + c;
+    const int lab = p.label[r];
     float g = 0.f;
-    if (live) {
-      g = exp2f(fmaf(z[c], kLog2e, -lse2));
-      if (c == lab) g -= 1.f;
-      g *= dl;
+    if (lab >= 0) {
+      g = exp2f(fmaf(*z, kLog2e, -p.lse2[r]));
+      if (c == lab - p.v0) g -= 1.f;
+      g *= p.dl[r];
     }
-    z[c] = g;
+    *z = g;
+    tile[i][x] = g;
   }
+  if (!p.gt) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = y; i < 32; i += 8)
+    if (c0 + i < p.width && r0 + x < p.rows) p.gt[(int64_t)(c0 + i) * p.ldt + r0 + x] = tile[x][i];
+}
+
+// dst[c][r] = src[r][c]: the GEMM's fast path takes operands with the contraction contiguous.
+__global__ void __launch_bounds__(256)
+    head_transpose32_kernel(const float* src, int64_t ld_src, int rows, int cols, float* dst,
+                            int64_t ld_dst) {  // one block per 32 x 32, column blocks fastest
+  __shared__ float tile[32][33];
+  pdl_launch();
+  pdl_wait();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, nc = (cols + 31) / 32;
+  const int c0 = (int)(blockIdx.x % nc) * 32, r0 = (int)(blockIdx.x / nc) * 32;
+#pragma unroll
+  for (int i = y; i < 32; i += 8)
+    if (r0 + i < rows && c0 + x < cols) tile[i][x] = src[(int64_t)(r0 + i) * ld_src + c0 + x];
+  __syncthreads();
+#pragma unroll
+  for (int i = y; i < 32; i += 8)
+    if (c0 + i < cols && r0 + x < rows) dst[(int64_t)(c0 + i) * ld_dst + r0 + x] = tile[x][i];
 }
 
 // The GEMM's problem table, written by a launch (its values travel in the launch's arguments,
@@ -1120,14 +1232,16 @@ struct HeadShape {
 };
 
 struct HeadLayout {
-  size_t nlive, label, pos, token, lse2, dl, zlab, state, hc, part, g, acc, wcopy, descs, total;
+  size_t nlive, label, pos, token, lse2, dl, dl_max, scale, zlab, state, hc, part, g, acc, wcopy;
+  size_t ht, gt, wt, descs, total;
 };
 
 constexpr int64_t kWorkBytes = 390ll << 20;  // what the backward pass's buffers may come to
 constexpr int64_t kMinElems = 32ll << 20;  // least entries of G per piece
-constexpr int64_t kZElems = 64ll << 20;    // entries of Z (fp32), or of a copied W, per piece
+constexpr int64_t kZElems = 32ll << 20;    // entries of Z (fp32), or of a copied W, per piece
 constexpr int64_t kPartBytes = 64ll << 20; // bytes of the forward partials per piece
 constexpr int kMaxSplits = 64;
+constexpr int kGatherBlocks = 608;         // blocks of the gather launch, at most
 constexpr int kFewBlocks = 1024;           // blocks of the few-token kernel (bounds its workspace)
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
 
@@ -1176,7 +1290,9 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
     // until the tiles fill the GPU; a slice keeps at least 1024 columns
     const int64_t units = bf ? sms / 2 : sms;
     const int64_t tiles = cdiv(std::max<int64_t>(n, 1), bf ? kTile : 128) * cdiv(dim, kTile);
-    s.splits = std::max<int64_t>(1, std::min({cdiv(units, tiles), s.piece / 1024, (int64_t)kMaxSplits}));
+    // (fp32: 128, its k-blocks are slower)
+    s.splits = std::max<int64_t>(
+        1, std::min({cdiv(units, tiles), s.piece / (bf ? 1024 : 128), (int64_t)kMaxSplits}));
     s.kdh = up(cdiv(s.piece, s.splits), kBK);
     s.splits = cdiv(s.piece, s.kdh);
     s.buffers = bf && s.pieces > 1 ? 2 : 1;
@@ -1207,6 +1323,8 @@ HeadLayout head_layout(const HeadShape& s) {
   l.token = take(s.rows * 4);
   l.lse2 = take(s.backward ? s.rows * 4 : 0);
   l.dl = take(s.backward ? s.rows * 4 : 0);
+  l.dl_max = take(s.backward ? kGatherBlocks * 4 : 0);
+  l.scale = take(4);
   l.zlab = take(s.rows * 4);
   l.state = take(s.rows * 8);
   l.hc = take(s.rows * s.pitch * es);
@@ -1214,6 +1332,10 @@ HeadLayout head_layout(const HeadShape& s) {
   l.g = take(s.backward || !bf ? s.buffers * s.rows * s.piece * es : 0);
   l.acc = take(s.backward ? s.splits * s.rows * s.pitch * 4 : 0);
   l.wcopy = take(s.copy_w ? s.buffers * s.piece * s.pitch * 2 : 0);
+  const bool t32 = s.backward && !bf;        // fp32: transposed H, G piece and W piece
+  l.ht = take(t32 ? s.pitch * s.rows * 4 : 0);
+  l.gt = take(t32 ? s.piece * s.rows * 4 : 0);
+  l.wt = take(t32 ? s.pitch * s.piece * 4 : 0);
   l.descs = take(bf ? 0 : (int64_t)sizeof(GemmDesc) * (s.pieces * (2 + s.splits)));
   l.total = off;
   return l;
@@ -1299,7 +1421,7 @@ struct HeadCall {
     a.dim = (int32_t)s.dim;
     a.pitch = (int32_t)s.pitch;
     a.vocab = (int32_t)s.vocab;
-    a.per = (int32_t)std::max<int64_t>(8, cdiv(s.n, 4ll * sms));
+    a.per = (int32_t)std::max<int64_t>(8, cdiv(s.n, kGatherBlocks));
     a.vec = aligned_to(hidden, 16) && s.dim % 8 == 0 &&
             (ld_h * (int64_t)dtype_bytes(s.dtype)) % 16 == 0;
     a.place = s.dtype == MFSDP_DTYPE_F32;
@@ -1312,6 +1434,7 @@ struct HeadCall {
       a.dloss = dloss;
       a.lse2 = at<float>(l.lse2);
       a.dl = at<float>(l.dl);
+      a.dl_max = at<float>(l.dl_max);
     }
     a.loss = loss;
     a.lse = lse;
@@ -1325,6 +1448,7 @@ struct HeadCall {
   cudaError_t finish() const {
     FinishArgs f{};
     f.acc = at<float>(l.acc);
+    f.scale = s.dtype == MFSDP_DTYPE_BF16 ? at<float>(l.scale) : nullptr;
     f.pos = at<int32_t>(l.pos);
     f.dh = dh;
     f.ld_dh = ld_dh;
@@ -1415,6 +1539,9 @@ struct HeadCall {
     a.label = at<int32_t>(l.label);
     a.lse2 = at<float>(l.lse2);
     a.dl = at<float>(l.dl);
+    a.dl_max = at<float>(l.dl_max);
+    a.dl_blocks = (int32_t)cdiv(s.n, std::max<int64_t>(8, cdiv(s.n, kGatherBlocks)));
+    a.scale = at<float>(l.scale);
     a.part = at<float2>(l.part);
     a.zlab = at<float>(l.zlab);
     a.dw = static_cast<uint16_t*>(dw);
@@ -1505,10 +1632,10 @@ struct HeadCall {
       d[(size_t)(i * per)] = q;
       if (!s.backward) continue;
       q = GemmDesc{};
-      q.a = z;
-      q.lda = (int32_t)s.piece;
-      q.b = hc;
-      q.ldb = (int32_t)s.pitch;
+      q.a = at<float>(l.gt);
+      q.lda = (int32_t)s.rows;
+      q.b = at<float>(l.ht);
+      q.ldb = (int32_t)s.rows;
       q.c = dw ? static_cast<float*>(dw) + v0 * ld_dw : nullptr;
       q.ldc = (int32_t)ld_dw;
       q.m = (int32_t)width;
@@ -1521,8 +1648,8 @@ struct HeadCall {
         q = GemmDesc{};
         q.a = z + c0;
         q.lda = (int32_t)s.piece;
-        q.b = w + (v0 + c0) * ld_w;
-        q.ldb = (int32_t)ld_w;
+        q.b = at<float>(l.wt) + c0;
+        q.ldb = (int32_t)s.piece;
         q.c = acc + k * s.rows * s.pitch;
         q.ldc = (int32_t)s.pitch;
         q.m = (int32_t)s.n;
@@ -1542,6 +1669,12 @@ struct HeadCall {
       e = launch_pdl(head_descs_kernel, dim3(1), dim3(64), 0, st, t);
     }
     if (e == cudaSuccess) e = gather();
+    auto transpose = [&](const float* src, int64_t ld, int64_t rows, int64_t cols, float* dst,
+                         int64_t ld_dst) {
+      return launch_pdl(head_transpose32_kernel, dim3((unsigned)(cdiv(cols, 32) * cdiv(rows, 32))),
+                        dim3(256), 0, st, src, ld, (int)rows, (int)cols, dst, ld_dst);
+    };
+    if (e == cudaSuccess && dw) e = transpose(hc, s.pitch, s.n, s.dim, at<float>(l.ht), s.rows);
     if (e != cudaSuccess) return MFSDP_ECUDA;
     for (int64_t i = 0; i < s.pieces; ++i) {
       const int64_t v0 = i * s.piece, width = std::min(s.piece, s.vocab - v0), at0 = i * per;
@@ -1567,20 +1700,26 @@ struct HeadCall {
       }
       Grad32Args a{};
       a.z = z;
+      a.gt = dw ? at<float>(l.gt) : nullptr;
       a.label = at<int32_t>(l.label);
       a.lse2 = at<float>(l.lse2);
       a.dl = at<float>(l.dl);
+      a.rows = (int32_t)s.n;
       a.width = (int32_t)width;
       a.v0 = (int32_t)v0;
       a.ldz = s.piece;
-      e = launch_pdl(head_grad32_kernel, dim3((unsigned)s.n), dim3(256), 0, st, a);
+      a.ldt = s.rows;
+      e = launch_pdl(head_grad32_kernel, dim3((unsigned)(cdiv(width, 32) * cdiv(s.n, 32))),
+                     dim3(256), 0, st, a);
+      if (e == cudaSuccess && dh)
+        e = transpose(w + v0 * ld_w, ld_w, width, s.dim, at<float>(l.wt), s.piece);
       if (e != cudaSuccess) return MFSDP_ECUDA;
       if (dw) {
-        r = launch_gemm(dev + at0 + 1, d.data() + at0 + 1, 1, 1, 0, st);
+        r = launch_gemm(dev + at0 + 1, d.data() + at0 + 1, 1, 0, 1, st);
         if (r != MFSDP_OK) return r;
       }
       if (dh) {
-        r = launch_gemm(dev + at0 + 2, d.data() + at0 + 2, (int)s.splits, 0, 0, st);
+        r = launch_gemm(dev + at0 + 2, d.data() + at0 + 2, (int)s.splits, 0, 1, st);
         if (r != MFSDP_OK) return r;
       }
     }
@@ -1595,8 +1734,9 @@ int check_head(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, int64_t ld_
       piece > (1ll << 30))
     return MFSDP_ESHAPE;
   if (ld_w < dim) return MFSDP_EINVAL;
-  if (ld_w >= (1ll << 31) || cdiv(n, kTile) * cdiv(std::min(piece, vocab), kTile) >= (1ll << 31))
-    return MFSDP_ESHAPE;
+  // tiles (and the fp32 path's 32 x 32 blocks) of a piece are counted in 32 bits
+  const int64_t cols = std::max(std::min(piece, vocab), dim);
+  if (ld_w >= (1ll << 31) || cdiv(n, 32) * cdiv(cols, 32) >= (1ll << 31)) return MFSDP_ESHAPE;
   return MFSDP_OK;
 }
 
