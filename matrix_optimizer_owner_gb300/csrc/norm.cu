@@ -8,7 +8,7 @@
 //
 // Both directions are bound by memory: forward moves 2 and backward 3 values per element.
 // Rows of up to 1024 elements take a warp each (no block barrier; 8 rows in flight per block),
-// longer ones a block each with at most 32 elements per thread; rows beyond 16384 elements are
+// longer ones a block each with at most 32 elements per thread; rows beyond 8192 elements are
 // read in passes.  Backward keeps every column's dw and db sums in registers over the rows a
 // block walks; the blocks' sums go to the workspace and a second launch adds them in block
 // order: no atomics, the result does not depend on timing.
@@ -23,7 +23,7 @@ namespace {
 constexpr int kNormWarps = 8;         // warps per block of the warp-per-row kernels
 constexpr int kWarpRowMax = 1024;     // longest row one warp takes
 constexpr int kMaxChunks = 4;         // 8-element chunks per thread
-constexpr int kRegRowMax = 512 * 8 * kMaxChunks;
+constexpr int kRegRowMax = 512 * 8 * 2;
 
 struct NormArgs {
   int64_t rows, cols;
@@ -66,8 +66,66 @@ __device__ __forceinline__ void store_chunk(T* row, int64_t n, int t, int k, con
   }
 }
 
-// A thread's share of a row as it lies in memory, so that the next row's loads are in flight
-// while this row is worked on.
+// The rows a thread will need next, as they lie in memory: N matrices (x, or x and dy) with K
+// chunks of 8 elements each.  Rows of 16-byte vectors are copied ahead to shared memory
+// (cp.async, S rows deep); a thread reads back only what it copied, so no barrier is needed, and
+// the bytes in flight do not cost registers: with one row ahead in registers, 24 KB per SM were
+// in flight and the 768-wide backward pass stayed at 3.8 TB/s.
+template <typename T, int N, int TPR, int K>
+struct Ring {
+  static constexpr int kThreads = TPR == 32 ? 32 * kNormWarps : TPR;
+  static constexpr int kVecs = (int)sizeof(T) / 2;            // 16-byte vectors per chunk
+  static constexpr int kStage = N * K * kVecs * kThreads * 16;
+  static constexpr int kDepth = kStage * 4 <= 96 * 1024 ? 4 : kStage * 3 <= 96 * 1024 ? 3 : 2;
+  static constexpr int kBytes = kDepth * kStage;
+  uint32_t base;
+  __device__ __forceinline__ explicit Ring(const void* smem) {
+    base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+  }
+  __device__ __forceinline__ uint32_t at(int stage, int m, int k, int v) const {
+    return base + (uint32_t)((((stage * N + m) * K + k) * kVecs + v) * kThreads * 16);
+  }
+  // one matrix's row into a stage; chunks past the end are zero
+  __device__ __forceinline__ void copy(int stage, int m, const T* row, int n, int t) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int e = (k * TPR + t) * 8;
+      const T* src = row + (e < n ? e : 0);
+      const int bytes = e < n ? 16 : 0;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, m, k, v)),
+                     "l"(src + v * (16 / (int)sizeof(T))), "r"(bytes)
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // the oldest of kDepth groups has landed
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+  }
+  __device__ __forceinline__ void get(int stage, int m, int k, float (&v)[8]) const {
+    uint32_t w[4 * kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(at(stage, m, k, i))
+                   : "memory");
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    }
+  }
+};
+
+// A thread's share of a row in registers.
 template <typename T, int TPR, int K, bool VEC>
 struct RowChunks {
   Pack8<T> p[VEC ? K : 1];
@@ -96,6 +154,11 @@ struct RowChunks {
     }
   }
 };
+
+// bf16 rows of vectors go through the ring.  fp32 rows are faster in registers: 8192 rows of 2048
+// took 79 us for both passes, through the ring 106 (bf16: 54 and 50).
+template <typename T, bool VEC>
+constexpr bool kRing = VEC && sizeof(T) == 2;
 
 // The parameters of a thread's columns (`fill` where there are none).
 template <int TPR, int K, bool VEC>
@@ -128,16 +191,22 @@ __device__ __forceinline__ void load_params(const void* src, int is_bf16, int pv
 // buffers in turn, so one barrier per call is enough.
 template <int TPR>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float* red, int& turn) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (TPR == 32) return;
+  // both sums in one tree: the lower half of the warp goes on with a, the upper with b
+  const bool upper = threadIdx.x & 16;
+  float v = upper ? b : a;
+  v += __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (TPR == 32) {
+    const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+    a = upper ? w : v;
+    b = upper ? v : w;
+    return;
+  }
   constexpr int W = TPR / 32;
   float* buf = red + turn * 2 * W;
   turn ^= 1;
-  if ((threadIdx.x & 31) == 0) {
-    buf[threadIdx.x >> 5] = a;
-    buf[W + (threadIdx.x >> 5)] = b;
-  }
+  if ((threadIdx.x & 15) == 0) buf[(upper ? W : 0) + (threadIdx.x >> 5)] = v;
   __syncthreads();
   a = b = 0.f;
 #pragma unroll
@@ -159,19 +228,37 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
   const int64_t step = (int64_t)gridDim.x * kRowsPerBlock;
   int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + (TPR == 32 ? (threadIdx.x >> 5) : 0);
   int turn = 0;
-  RowChunks<T, TPR, K, VEC> cur, nxt;
-  if (row < p.rows) cur.load(static_cast<const T*>(p.x) + row * p.ld_x, p.cols, t);
+  extern __shared__ uint4 ring_smem[];
+  constexpr bool kUseRing = kRing<T, VEC>;
+  using R = Ring<T, 1, TPR, K>;
+  const R ring(ring_smem);
+  RowChunks<T, TPR, kUseRing ? 1 : K, VEC> cur, nxt;
+  auto fetch = [&](int64_t i, int stage) {
+    if (i < p.rows) ring.copy(stage, 0, static_cast<const T*>(p.x) + i * p.ld_x, (int)p.cols, t);
+    ring.commit();
+  };
+  if (kUseRing) {
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i) fetch(row + i * step, i);
+  } else if (row < p.rows) {
+    cur.load(static_cast<const T*>(p.x) + row * p.ld_x, p.cols, t);
+  }
   float w[K][8], b[K][8];
   load_params<TPR, K, VEC>(p.w, p.wbf16, p.pvec, p.cols, t, 1.f, w);
   load_params<TPR, K, VEC>(p.b, p.wbf16, p.pvec, p.cols, t, 0.f, b);
+  int stage = 0;
   for (; row < p.rows; row += step) {     // whole warps (or the whole block) stay together
-    if (row + step < p.rows)
+    if (kUseRing) {
+      fetch(row + (R::kDepth - 1) * step, stage == 0 ? R::kDepth - 1 : stage - 1);
+      ring.wait();
+    } else if (row + step < p.rows) {
       nxt.load(static_cast<const T*>(p.x) + (row + step) * p.ld_x, p.cols, t);
+    }
     float v[K][8];
     float s = 0.f, zero = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      cur.get(k, v[k]);
+      if (kUseRing) ring.get(stage, 0, k, v[k]); else cur.get(kUseRing ? 0 : k, v[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += v[k][j];
     }
@@ -202,7 +289,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
       for (int j = 0; j < 8; ++j) v[k][j] = fmaf((v[k][j] - mu) * r, w[k][j], b[k][j]);
       store_chunk<T, TPR, VEC>(yr, p.cols, t, k, v[k]);
     }
-    cur = nxt;
+    if (!kUseRing) cur = nxt;
+    stage = stage == R::kDepth - 1 ? 0 : stage + 1;
   }
 }
 
@@ -245,10 +333,10 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const __grid_co
 // ---------------------------------------------------------------- backward
 template <typename T, int TPR, int K, bool VEC>
 __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR,
-                                  TPR > 32 && K <= 2 ? 512 / TPR : 1)
+                                  TPR == 32 ? 1 : TPR == 256 && sizeof(T) == 2 && VEC ? 3 : 512 / TPR)
     norm_backward_kernel(const __grid_constant__ NormArgs p) {
   constexpr int kRowsPerBlock = TPR == 32 ? kNormWarps : 1;
-  // the next row is loaded ahead where its raw values fit in registers beside this row's
+  // rows outside the ring: the next one is loaded ahead where its raw values fit in registers
   constexpr bool kAhead = sizeof(T) * K <= 8;
   __shared__ float red[TPR == 32 ? 1 : 4 * (TPR / 32)];
   __shared__ float comb[TPR == 32 ? kNormWarps * 32 * 8 : 1];
@@ -259,37 +347,78 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR,
   int turn = 0;
   const int64_t step = (int64_t)gridDim.x * kRowsPerBlock;
   int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + sub;
-  using Chunks = RowChunks<T, TPR, K, VEC>;
+  extern __shared__ uint4 ring_smem[];
+  constexpr bool kUseRing = kRing<T, VEC>;
+  using R = Ring<T, 2, TPR, K>;
+  const R ring(ring_smem);
+  using Chunks = RowChunks<T, TPR, kUseRing ? 1 : K, VEC>;
   Chunks xc, gc, xn, gn;
+  auto fetch = [&](int64_t i, int stage) {
+    if (i < p.rows) {
+      ring.copy(stage, 0, static_cast<const T*>(p.x) + i * p.ld_x, (int)p.cols, t);
+      ring.copy(stage, 1, static_cast<const T*>(p.dy) + i * p.ld_dy, (int)p.cols, t);
+    }
+    ring.commit();
+  };
   auto load_row = [&](Chunks& x, Chunks& g, int64_t i) {
     x.load(static_cast<const T*>(p.x) + i * p.ld_x, p.cols, t);
     g.load(static_cast<const T*>(p.dy) + i * p.ld_dy, p.cols, t);
   };
-  if (row < p.rows) load_row(xc, gc, row);
+  if (kUseRing) {
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i) fetch(row + i * step, i);
+  } else if (row < p.rows) {
+    load_row(xc, gc, row);
+  }
   float aw[K][8], ab[K][8], w[K][8];
   load_params<TPR, K, VEC>(p.w, p.wbf16, p.pvec, p.cols, t, 1.f, w);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int j = 0; j < 8; ++j) aw[k][j] = ab[k][j] = 0.f;
+  int stage = 0;
+  float r_next = 0.f, mu_next = 0.f;       // the statistics, a row ahead too
+  auto fetch_stats = [&](int64_t i) {
+    if (i >= p.rows) return;
+    r_next = p.rstd_in[i];
+    if (p.layer) mu_next = p.mean_in[i];
+  };
+  fetch_stats(row);
   for (; row < p.rows; row += step) {
-    if (kAhead && row + step < p.rows) load_row(xn, gn, row + step);
+    const float r = r_next, mu = mu_next;
+    fetch_stats(row + step);
+    if (kUseRing) {
+      fetch(row + (R::kDepth - 1) * step, stage == 0 ? R::kDepth - 1 : stage - 1);
+      ring.wait();
+    } else if (kAhead && row + step < p.rows) {
+      load_row(xn, gn, row + step);
+    }
     T* dr = static_cast<T*>(p.dx) + row * p.ld_dx;
-    const float r = p.rstd_in[row], mu = p.layer ? p.mean_in[row] : 0.f;
-    float z[K][8], g[K][8];
+    // z and g of a chunk.  They are read again after the row's sums rather than kept across them:
+    // 32 registers less per thread and half as many warps more hide the sums' latency.
+    auto values = [&](int k, float (&z)[8], float (&g)[8]) {
+      if (kUseRing) {
+        ring.get(stage, 0, k, z);
+        ring.get(stage, 1, k, g);
+      } else {
+        xc.get(kUseRing ? 0 : k, z);
+        gc.get(kUseRing ? 0 : k, g);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = (z[j] - mu) * r;
+    };
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      xc.get(k, z[k]);
-      gc.get(k, g[k]);
+      float z[8], g[8];
+      values(k, z, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {   // past the row's end dy is 0: no contribution
-        z[k][j] = (z[k][j] - mu) * r;
-        aw[k][j] = fmaf(g[k][j], z[k][j], aw[k][j]);
-        ab[k][j] += g[k][j];
-        g[k][j] *= w[k][j];
-        s1 += g[k][j];
-        s2 = fmaf(g[k][j], z[k][j], s2);
+        aw[k][j] = fmaf(g[j], z[j], aw[k][j]);
+        ab[k][j] += g[j];
+        g[j] *= w[k][j];
+        s1 += g[j];
+        s2 = fmaf(g[j], z[j], s2);
       }
     }
     row_sum2<TPR>(s1, s2, red, turn);
@@ -297,11 +426,15 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR,
     s2 *= p.inv_n;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      float z[8], g[8];
+      values(k, z, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[k][j] = (g[k][j] - s1 - z[k][j] * s2) * r;
-      store_chunk<T, TPR, VEC>(dr, p.cols, t, k, g[k]);
+      for (int j = 0; j < 8; ++j) g[j] = (fmaf(g[j], w[k][j], -s1) - z[j] * s2) * r;
+      store_chunk<T, TPR, VEC>(dr, p.cols, t, k, g);
     }
-    if (kAhead) {
+    if (kUseRing) {
+      stage = stage == R::kDepth - 1 ? 0 : stage + 1;
+    } else if (kAhead) {
       xc = xn;
       gc = gn;
     } else if (row + step < p.rows) {
@@ -415,16 +548,18 @@ cudaError_t by_shape(int64_t cols, F&& f) {
   if (cols <= kWarpRowMax) { MFSDP_NORM_K(32) }
   if (cols <= 2048) return f.template operator()<T, 128, 2, VEC>();
   if (cols <= 4096) return f.template operator()<T, 256, 2, VEC>();
-  if (cols <= 8192) return f.template operator()<T, 512, 2, VEC>();
-  return f.template operator()<T, 512, 4, VEC>();
+  return f.template operator()<T, 512, 2, VEC>();
 #undef MFSDP_NORM_K
 }
 
-// Blocks of a kernel that an SM holds (at least 1).
+// Raises a kernel's shared-memory limit and counts the blocks that an SM holds (at least 1).
 template <typename K>
-int resident(K kernel, int threads) {
+int resident(K kernel, int threads, int smem) {
   int occ = 0;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0) == cudaSuccess &&
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return 1;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) == cudaSuccess &&
                  occ > 0
              ? occ
              : 1;
@@ -437,11 +572,12 @@ struct FwdLaunch {
   template <typename T, int TPR, int K, bool VEC>
   cudaError_t operator()() const {
     const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
-    static const int occ = resident(norm_forward_kernel<T, TPR, K, VEC>, threads);
+    constexpr int smem = kRing<T, VEC> ? Ring<T, 1, TPR, K>::kBytes : 0;
+    static const int occ = resident(norm_forward_kernel<T, TPR, K, VEC>, threads, smem);
     const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
     const int64_t g = std::min<int64_t>((int64_t)sms * occ, need);
-    return launch_pdl(norm_forward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), 0, st,
-                      a);
+    return launch_pdl(norm_forward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), smem,
+                      st, a);
   }
 };
 
@@ -453,11 +589,12 @@ struct BwdLaunch {
   template <typename T, int TPR, int K, bool VEC>
   cudaError_t operator()() const {
     const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
-    static const int occ = resident(norm_backward_kernel<T, TPR, K, VEC>, threads);
+    constexpr int smem = kRing<T, VEC> ? Ring<T, 2, TPR, K>::kBytes : 0;
+    static const int occ = resident(norm_backward_kernel<T, TPR, K, VEC>, threads, smem);
     const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
     const int64_t g = std::min({(int64_t)sms * occ, (int64_t)max_blocks, need});
     *blocks = (int)g;
-    return launch_pdl(norm_backward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), 0,
+    return launch_pdl(norm_backward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), smem,
                       st, a);
   }
 };

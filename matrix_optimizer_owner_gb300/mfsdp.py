@@ -449,18 +449,22 @@ def mfsdp_gemm_f32_batched(problems, trans_a: bool = False, trans_b: bool = Fals
 
 
 # ------------------------------------------------------------------------------- operators
-# A call on a small tensor is bound by the time spent here, so the checks are plain comparisons.
+# A call on a small tensor is bound by the time spent here, so each tensor is checked in one
+# helper call, by plain comparisons.
 _FLOAT_CODES, _INDEX_CODES = {}, {}
+_F32 = None
 
 
 def _learn_dtypes() -> None:
+    global _F32
     import torch
+    _F32 = torch.float32
     _FLOAT_CODES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
     _INDEX_CODES.update({torch.int32: INDEX_I32, torch.int64: INDEX_I64})
 
 
 def _float_code(t, name: str) -> int:
-    if not _FLOAT_CODES:
+    if _F32 is None:
         _learn_dtypes()
     code = _FLOAT_CODES.get(t.dtype)
     if code is None:
@@ -469,7 +473,7 @@ def _float_code(t, name: str) -> int:
 
 
 def _index_code(t, name: str) -> int:
-    if not _INDEX_CODES:
+    if _F32 is None:
         _learn_dtypes()
     code = _INDEX_CODES.get(t.dtype)
     if code is None:
@@ -477,75 +481,77 @@ def _index_code(t, name: str) -> int:
     return code
 
 
-def _like(t, ref, name: str) -> None:
-    if t.dtype != ref.dtype:
-        raise TypeError(f"{name}: expected {ref.dtype}, got {t.dtype}")
+def _refuse(t, shape, dtype, name: str) -> None:
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if len(shape) == 2 or t.is_contiguous():
+        raise ValueError(f"{name}: on {t.device}, expected tensors on the current CUDA device")
+    raise ValueError(f"{name}: expected a contiguous vector, got strides {t.stride()}")
 
 
-def _matrix(t, rows: int, cols: int, name: str) -> int:
-    """Pitch of a rows x cols tensor with unit column stride."""
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: expected a {rows} x {cols} tensor, got {tuple(t.shape)}")
+def _matrix(t, shape, dtype, dev: int, name: str) -> int:
+    """Pitch of a 2D tensor of unit column stride."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, shape, dtype, name)
     pitch, step = t.stride()
+    rows, cols = shape
     if step != 1 and cols > 1:
         raise ValueError(f"{name}: expected unit column stride, got strides {t.stride()}")
     return pitch if rows > 1 else max(pitch, cols)
 
 
-def _vector(t, n: int, name: str) -> None:
+def _vector(t, shape, dtype, dev: int, name: str) -> Optional[int]:
+    """Address of a contiguous vector, or None."""
     if t is None:
-        return
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
+        return None
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(t, shape, dtype, name)
+    return t.data_ptr()
 
 
-def _stat(t, n: int, name: str) -> None:
-    """A contiguous fp32 vector of n, or None."""
-    if t is None:
-        return
-    _vector(t, n, name)
-    if _float_code(t, name) != DTYPE_F32:
-        raise TypeError(f"{name}: expected float32, got {t.dtype}")
+def _two_dims(t, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions, got {tuple(t.shape)}")
+    return t.shape
 
 
-def _launch_stream(stream, *tensors) -> Optional[int]:
-    """The stream to launch on, once every tensor is known to lie on the current CUDA device (a
-    host pointer would fault the GPU)."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            raise ValueError(f"expected tensors on the current CUDA device, got {t.device}")
+def _device_stream(dev: int, stream) -> Optional[int]:
+    """The stream to launch on; `dev`, which holds every tensor, has to be the current CUDA
+    device (a host pointer would fault the GPU)."""
     import torch
-    if torch.cuda.current_device() != dev:
-        raise ValueError(f"expected tensors on the current CUDA device, got cuda:{dev}")
+    if dev < 0 or torch.cuda.current_device() != dev:
+        raise ValueError("expected tensors on the current CUDA device")
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(dev)
     return _stream(stream)
 
 
-def _workspace(ws, nbytes: int, device, stream):
+def _workspace(ws, nbytes: int, like, dev: int, stream):
     """The caller's uint8 workspace, or a fresh one that lives until `stream` is done with it."""
     if ws is not None:
+        if ws.get_device() != dev:
+            raise ValueError("expected the workspace on the current CUDA device")
         return ws, ws.numel() * ws.element_size()
     import torch
-    ws = torch.empty(nbytes or 1, dtype=torch.uint8, device=device)
+    ws = like.new_empty((nbytes or 1,), dtype=torch.uint8)
     if stream is not None:
         ws.record_stream(stream if hasattr(stream, "cuda_stream")
                          else torch.cuda.ExternalStream(stream))
     return ws, nbytes
 
 
-def _params_code(cols: int, named) -> int:
-    """The one dtype of the given vectors of `cols` parameters (fp32 when there is none)."""
-    code = None
-    for name, t in named:
-        if t is None:
-            continue
-        _vector(t, cols, name)
-        c = _float_code(t, name)
-        if code is not None and c != code:
-            raise TypeError("the norm's parameters and their gradients must share one dtype")
-        code = c
-    return DTYPE_F32 if code is None else code
+def _params_dtype(*params):
+    """The dtype of the first parameter vector there is (fp32 where there is none) and its
+    code; the others are compared with it."""
+    for name, t in params:
+        if t is not None:
+            return t.dtype, _float_code(t, name)
+    return _F32, DTYPE_F32
 
 
 def mfsdp_norm_forward(kind: int, x, weight, bias, eps: float, y, mean=None, rstd=None,
@@ -553,17 +559,20 @@ def mfsdp_norm_forward(kind: int, x, weight, bias, eps: float, y, mean=None, rst
     """Layer norm (``kind`` NORM_LAYER) or RMS norm (NORM_RMS) of the rows of ``x`` into ``y``.
     ``weight`` and ``bias`` may be None; ``mean`` and ``rstd`` (fp32, per row) are written where
     given, for ``mfsdp_norm_backward``."""
-    rows, cols = x.shape
-    code = _float_code(x, "x")
-    _like(y, x, "y")
-    ld_x, ld_y = _matrix(x, rows, cols, "x"), _matrix(y, rows, cols, "y")
-    _stat(mean, rows, "mean")
-    _stat(rstd, rows, "rstd")
-    pcode = _params_code(cols, (("weight", weight), ("bias", bias)))
-    st = _launch_stream(stream, x, weight, bias, y, mean, rstd)
+    shape = _two_dims(x, "x")
+    rows, cols = shape
+    code, dtype, dev = _float_code(x, "x"), x.dtype, x.get_device()
+    ld_x = _matrix(x, shape, dtype, dev, "x")
+    ld_y = _matrix(y, shape, dtype, dev, "y")
+    pdtype, pcode = _params_dtype(("weight", weight), ("bias", bias))
+    w = _vector(weight, (cols,), pdtype, dev, "weight")
+    b = _vector(bias, (cols,), pdtype, dev, "bias")
+    m = _vector(mean, (rows,), _F32, dev, "mean")
+    r = _vector(rstd, (rows,), _F32, dev, "rstd")
+    st = _device_stream(dev, stream)
     _check("mfsdp_norm_forward", _lib.load().mfsdp_norm_forward(
-        kind, rows, cols, code, pcode, x.data_ptr(), ld_x, _ptr(weight), _ptr(bias), eps,
-        y.data_ptr(), ld_y, _ptr(mean), _ptr(rstd), st))
+        kind, rows, cols, code, pcode, x.data_ptr(), ld_x, w, b, eps, y.data_ptr(), ld_y, m, r,
+        st))
 
 
 @functools.lru_cache(maxsize=256)
@@ -578,35 +587,40 @@ def mfsdp_norm_backward(kind: int, dy, x, weight, mean, rstd, dx, dweight=None, 
                         workspace=None, stream=None) -> None:
     """Gradients of ``mfsdp_norm_forward`` for its input and, where given, for the weight and
     the bias.  ``workspace`` (uint8) defaults to a fresh one."""
-    rows, cols = x.shape
-    code = _float_code(x, "x")
-    _like(dy, x, "dy")
-    _like(dx, x, "dx")
-    ld_dy, ld_x = _matrix(dy, rows, cols, "dy"), _matrix(x, rows, cols, "x")
-    ld_dx = _matrix(dx, rows, cols, "dx")
-    _stat(mean, rows, "mean")
-    _stat(rstd, rows, "rstd")
-    pcode = _params_code(cols, (("weight", weight), ("dweight", dweight), ("dbias", dbias)))
-    st = _launch_stream(stream, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
-    ws, nbytes = _workspace(workspace, mfsdp_norm_backward_workspace_bytes(rows, cols), x.device,
+    shape = _two_dims(x, "x")
+    rows, cols = shape
+    code, dtype, dev = _float_code(x, "x"), x.dtype, x.get_device()
+    ld_x = _matrix(x, shape, dtype, dev, "x")
+    ld_dy = _matrix(dy, shape, dtype, dev, "dy")
+    ld_dx = _matrix(dx, shape, dtype, dev, "dx")
+    pdtype, pcode = _params_dtype(("weight", weight), ("dweight", dweight), ("dbias", dbias))
+    w = _vector(weight, (cols,), pdtype, dev, "weight")
+    dw = _vector(dweight, (cols,), pdtype, dev, "dweight")
+    db = _vector(dbias, (cols,), pdtype, dev, "dbias")
+    m = _vector(mean, (rows,), _F32, dev, "mean")
+    r = _vector(rstd, (rows,), _F32, dev, "rstd")
+    st = _device_stream(dev, stream)
+    ws, nbytes = _workspace(workspace, mfsdp_norm_backward_workspace_bytes(rows, cols), x, dev,
                             stream)
     _check("mfsdp_norm_backward", _lib.load().mfsdp_norm_backward(
-        kind, rows, cols, code, pcode, _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(weight), _ptr(mean),
-        _ptr(rstd), _ptr(dx), ld_dx, _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, st))
+        kind, rows, cols, code, pcode, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, w, m, r,
+        dx.data_ptr(), ld_dx, dw, db, ws.data_ptr(), nbytes, st))
 
 
 def mfsdp_embedding_forward(table, ids, scale: float, out, stream=None) -> None:
     """``out[t] = scale * table[ids[t]]``; the table and the output may differ in dtype."""
-    vocab, dim = table.shape
-    n = ids.numel()
+    shape = _two_dims(table, "table")
+    vocab, dim = shape
+    n, dev = ids.numel(), table.get_device()
     tcode, ocode = _float_code(table, "table"), _float_code(out, "out")
     icode = _index_code(ids, "ids")
-    _vector(ids, n, "ids")
-    ld_t, ld_o = _matrix(table, vocab, dim, "table"), _matrix(out, n, dim, "out")
-    st = _launch_stream(stream, table, ids, out)
+    idp = _vector(ids, (n,), ids.dtype, dev, "ids")
+    ld_t = _matrix(table, shape, table.dtype, dev, "table")
+    ld_o = _matrix(out, (n, dim), out.dtype, dev, "out")
+    st = _device_stream(dev, stream)
     _check("mfsdp_embedding_forward", _lib.load().mfsdp_embedding_forward(
-        vocab, dim, tcode, table.data_ptr(), ld_t, n, icode, ids.data_ptr(), scale, ocode,
-        out.data_ptr(), ld_o, st))
+        vocab, dim, tcode, table.data_ptr(), ld_t, n, icode, idp, scale, ocode, out.data_ptr(),
+        ld_o, st))
 
 
 @functools.lru_cache(maxsize=256)
@@ -623,18 +637,20 @@ def mfsdp_embedding_backward(ids, dy, scale: float, dtable, padding_idx: int = -
     """Gradient of the table of ``mfsdp_embedding_forward``: overwrites ``dtable``, or adds to
     it with ``accumulate``.  Tokens of ``padding_idx`` take no part.  ``workspace`` (uint8)
     defaults to a fresh one."""
-    vocab, dim = dtable.shape
-    n = ids.numel()
+    shape = _two_dims(dtable, "dtable")
+    vocab, dim = shape
+    n, dev = ids.numel(), dtable.get_device()
     dcode, gcode = _float_code(dy, "dy"), _float_code(dtable, "dtable")
     icode = _index_code(ids, "ids")
-    _vector(ids, n, "ids")
-    ld_dy, ld_dt = _matrix(dy, n, dim, "dy"), _matrix(dtable, vocab, dim, "dtable")
-    st = _launch_stream(stream, dtable, dy, ids, workspace)
+    idp = _vector(ids, (n,), ids.dtype, dev, "ids")
+    ld_dy = _matrix(dy, (n, dim), dy.dtype, dev, "dy")
+    ld_dt = _matrix(dtable, shape, dtable.dtype, dev, "dtable")
+    st = _device_stream(dev, stream)
     ws, nbytes = _workspace(workspace, mfsdp_embedding_backward_workspace_bytes(vocab, dim, n),
-                            dtable.device, stream)
+                            dtable, dev, stream)
     _check("mfsdp_embedding_backward", _lib.load().mfsdp_embedding_backward(
-        vocab, dim, n, icode, _ptr(ids), padding_idx, scale, dcode, _ptr(dy), ld_dy,
-        1 if accumulate else 0, gcode, _ptr(dtable), ld_dt, _ptr(ws), nbytes, st))
+        vocab, dim, n, icode, idp, padding_idx, scale, dcode, dy.data_ptr(), ld_dy,
+        1 if accumulate else 0, gcode, dtable.data_ptr(), ld_dt, ws.data_ptr(), nbytes, st))
 
 
 @functools.lru_cache(maxsize=256)
@@ -648,20 +664,21 @@ def _head_workspace(n, dim, vocab, code, backward, misaligned, ld_w, piece) -> i
 def mfsdp_head_loss_workspace_bytes(n_tokens: int, dim: int, weight, backward: bool,
                                     piece: int = 0) -> int:
     vocab = weight.shape[0]
+    ld_w = _matrix(weight, (vocab, dim), weight.dtype, weight.get_device(), "weight")
     return _head_workspace(n_tokens, dim, vocab, _float_code(weight, "weight"),
-                           1 if backward else 0, weight.data_ptr() % 16,
-                           _matrix(weight, vocab, dim, "weight"), piece)
+                           1 if backward else 0, weight.data_ptr() % 16, ld_w, piece)
 
 
 def _head_args(hidden, weight, labels):
-    n, dim = hidden.shape
-    vocab = weight.shape[0]
-    code = _float_code(hidden, "hidden")
-    _like(weight, hidden, "weight")
+    shape = _two_dims(hidden, "hidden")
+    n, dim = shape
+    vocab = _two_dims(weight, "weight")[0]
+    code, dtype, dev = _float_code(hidden, "hidden"), hidden.dtype, hidden.get_device()
     icode = _index_code(labels, "labels")
-    _vector(labels, n, "labels")
-    ld_h, ld_w = _matrix(hidden, n, dim, "hidden"), _matrix(weight, vocab, dim, "weight")
-    return n, dim, vocab, code, icode, ld_h, ld_w
+    lab = _vector(labels, (n,), labels.dtype, dev, "labels")
+    ld_h = _matrix(hidden, shape, dtype, dev, "hidden")
+    ld_w = _matrix(weight, (vocab, dim), dtype, dev, "weight")
+    return n, dim, vocab, code, dtype, dev, icode, lab, ld_h, ld_w
 
 
 def mfsdp_head_loss_forward(hidden, weight, labels, loss, lse, ignore_index: int = -100,
@@ -669,16 +686,16 @@ def mfsdp_head_loss_forward(hidden, weight, labels, loss, lse, ignore_index: int
     """Per-token softmax cross entropy of ``hidden @ weight.T`` against ``labels`` into ``loss``
     and the log-sum-exp of the logits into ``lse`` (fp32, either may be None).  Tokens labelled
     ``ignore_index`` get 0 in both.  ``workspace`` (uint8) defaults to a fresh one."""
-    n, dim, vocab, code, icode, ld_h, ld_w = _head_args(hidden, weight, labels)
-    _stat(loss, n, "loss")
-    _stat(lse, n, "lse")
-    st = _launch_stream(stream, hidden, weight, labels, loss, lse, workspace)
+    n, dim, vocab, code, _, dev, icode, lab, ld_h, ld_w = _head_args(hidden, weight, labels)
+    los = _vector(loss, (n,), _F32, dev, "loss")
+    ls = _vector(lse, (n,), _F32, dev, "lse")
+    st = _device_stream(dev, stream)
     wp = weight.data_ptr()
     ws, nbytes = _workspace(workspace, _head_workspace(n, dim, vocab, code, 0, wp % 16, ld_w, 0),
-                            hidden.device, stream)
+                            hidden, dev, stream)
     _check("mfsdp_head_loss_forward", _lib.load().mfsdp_head_loss_forward(
-        n, dim, vocab, code, hidden.data_ptr(), ld_h, wp, ld_w, icode, labels.data_ptr(),
-        ignore_index, _ptr(loss), _ptr(lse), ws.data_ptr(), nbytes, st))
+        n, dim, vocab, code, hidden.data_ptr(), ld_h, wp, ld_w, icode, lab, ignore_index, los, ls,
+        ws.data_ptr(), nbytes, st))
 
 
 def mfsdp_head_loss_backward(hidden, weight, labels, lse, dloss, dhidden=None, dweight=None,
@@ -687,22 +704,20 @@ def mfsdp_head_loss_backward(hidden, weight, labels, lse, dloss, dhidden=None, d
     """Gradients of ``sum(dloss * loss)`` for the hidden states and the weight (either may be
     None), with ``lse`` from the forward pass; the logits are recomputed in pieces of ``piece``
     columns of the vocabulary (0: chosen)."""
-    n, dim, vocab, code, icode, ld_h, ld_w = _head_args(hidden, weight, labels)
-    _stat(lse, n, "lse")
-    _stat(dloss, n, "dloss")
+    n, dim, vocab, code, dtype, dev, icode, lab, ld_h, ld_w = _head_args(hidden, weight, labels)
+    ls = _vector(lse, (n,), _F32, dev, "lse")
+    dl = _vector(dloss, (n,), _F32, dev, "dloss")
     ld_dh = ld_dw = dim
+    dh = dw = None
     if dhidden is not None:
-        _like(dhidden, hidden, "dhidden")
-        ld_dh = _matrix(dhidden, n, dim, "dhidden")
+        ld_dh, dh = _matrix(dhidden, (n, dim), dtype, dev, "dhidden"), dhidden.data_ptr()
     if dweight is not None:
-        _like(dweight, hidden, "dweight")
-        ld_dw = _matrix(dweight, vocab, dim, "dweight")
-    st = _launch_stream(stream, hidden, weight, labels, lse, dloss, dhidden, dweight, workspace)
+        ld_dw, dw = _matrix(dweight, (vocab, dim), dtype, dev, "dweight"), dweight.data_ptr()
+    st = _device_stream(dev, stream)
     wp = weight.data_ptr()
     ws, nbytes = _workspace(workspace,
                             _head_workspace(n, dim, vocab, code, 1, wp % 16, ld_w, piece),
-                            hidden.device, stream)
+                            hidden, dev, stream)
     _check("mfsdp_head_loss_backward", _lib.load().mfsdp_head_loss_backward(
-        n, dim, vocab, code, hidden.data_ptr(), ld_h, wp, ld_w, icode, labels.data_ptr(),
-        ignore_index, _ptr(lse), _ptr(dloss), piece, _ptr(dhidden), ld_dh, _ptr(dweight), ld_dw,
-        ws.data_ptr(), nbytes, st))
+        n, dim, vocab, code, hidden.data_ptr(), ld_h, wp, ld_w, icode, lab, ignore_index, ls, dl,
+        piece, dh, ld_dh, dw, ld_dw, ws.data_ptr(), nbytes, st))
