@@ -5,14 +5,14 @@
 //
 // Both are bound by memory.  The gradient must not depend on timing, so the tokens are sorted
 // by id first (stable, so each id's tokens stay in order) instead of adding with atomics:
-//   1. sort     one cluster of eight blocks runs a stable radix sort of (id, token), least
+//   1. sort     one cluster of eight blocks (one block for up to kOneBlock tokens) runs a stable radix sort of (id, token), least
 //               significant digit first.  Per pass each warp counts the digits of its own
 //               contiguous share, the blocks exchange their digit totals through distributed
 //               shared memory, and every warp then places its share in order.  Cluster barriers
 //               separate the steps, so the whole sort is one launch.  The sort is bound by
 //               latency, so the launch's other blocks meanwhile write zeros over the first
 //               kFillBytes of the gradient, about what fits in the sort's time.
-//   2. sum      the sorted positions are cut into chunks of kChunkPos.  A chunk sums the runs
+//   2. sum      the sorted positions are cut into chunks of 16 or 32.  A chunk sums the runs
 //               of equal ids inside it in fp32 and writes each finished row once; a run that
 //               crosses a chunk boundary leaves fp32 partial rows in the workspace.  The work
 //               per block is the same whether one id owns half the tokens or none repeats.
@@ -28,13 +28,17 @@
 namespace mfsdp {
 namespace {
 
-constexpr int kSortBlocks = 8;              // cluster size
+constexpr int kSortBlocks = 8;              // cluster size beyond kOneBlock tokens
+constexpr int kOneBlock = 1024;             // tokens that one block sorts (4096 of them: 6 us more
+                                            // than the cluster)
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitMax = 9;                // bits per pass
 constexpr int kBinsMax = 1 << kDigitMax;
 constexpr int kSortSmem = (kSortWarps * kBinsMax + kBinsMax + kBinsMax + 32) * 4;
-constexpr int kChunkPos = 32;               // sorted positions per chunk
+// Sorted positions per chunk: 32, or 16 while 32 would give fewer than kFewChunks blocks' work.
+// 4096 tokens x 1024 took 46 us with 32 and 40 with 16, 8192 x 4096 172 and 177.
+constexpr int kChunkLong = 32, kChunkShort = 16, kFewChunks = 256;
 constexpr int kSumThreads = 128;
 constexpr int kZeroRows = 8;                // table rows per zeroing block of the sum launch
 constexpr int64_t kFillBytes = 80ll << 20;  // zeros written beside the sort (about 13 us)
@@ -149,8 +153,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32
   return v;
 }
 
-__global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads)
+// B blocks sort (a cluster where B > 1); the grid's other blocks write zeros.
+template <int B>
+__global__ void __launch_bounds__(kSortThreads)
     embedding_sort_kernel(const __grid_constant__ SortArgs p) {
+  auto barrier = [] {
+    if (B > 1) cluster_barrier(); else __syncthreads();
+  };
   extern __shared__ uint32_t sort_smem[];
   uint32_t* hist = sort_smem;                          // [warp][bin], then write positions
   uint32_t* total = hist + kSortWarps * kBinsMax;      // this block's digit totals
@@ -159,23 +168,23 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
   pdl_launch();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x >= kSortBlocks) {                     // whole clusters: zeros only
-    zero_fill(p, (int64_t)(blockIdx.x - kSortBlocks) * kSortThreads + tid,
-              (int64_t)(gridDim.x - kSortBlocks) * kSortThreads);
+  if (blockIdx.x >= B) {                               // whole clusters: zeros only
+    zero_fill(p, (int64_t)(blockIdx.x - B) * kSortThreads + tid,
+              (int64_t)(gridDim.x - B) * kSortThreads);
     return;
   }
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = B > 1 ? cluster_ctarank() : 0u;
   const int bins = 1 << p.digit;
   // every warp of the cluster owns one contiguous share of the positions; a short share's keys
   // stay in registers between counting and placing
-  const int64_t share = (p.n + kSortBlocks * kSortWarps - 1) / (kSortBlocks * kSortWarps);
+  const int64_t share = (p.n + B * kSortWarps - 1) / (B * kSortWarps);
   const int64_t i0 = ((int64_t)rank * kSortWarps + warp) * share;
   const int64_t i1 = i0 + share < p.n ? i0 + share : (int64_t)p.n;
   const bool keep = share <= 32 * kKeep;
   // (the array is padded to its 16-byte stores; a barrier of the first pass precedes the marks)
   if (p.present)
     for (int64_t i = (int64_t)rank * kSortThreads + tid; i < (p.vocab + 15) / 16;
-         i += kSortBlocks * kSortThreads)
+         i += B * kSortThreads)
       reinterpret_cast<uint4*>(p.present)[i] = make_uint4(0u, 0u, 0u, 0u);
 
   for (int pass = 0; pass < p.passes; ++pass) {
@@ -228,16 +237,16 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
       }
       total[tid] = s;
     }
-    cluster_barrier();
+    barrier();
     // digit b of this block starts after all smaller digits and the same digit of the blocks
     // before it
     uint32_t all = 0, before = 0;
     if (tid < bins) {
-      uint32_t c[kSortBlocks];
+      uint32_t c[B];
 #pragma unroll
-      for (int q = 0; q < kSortBlocks; ++q) c[q] = ld_cluster_u32(total + tid, (uint32_t)q);
+      for (int q = 0; q < B; ++q) c[q] = B > 1 ? ld_cluster_u32(total + tid, (uint32_t)q) : total[tid];
 #pragma unroll
-      for (int q = 0; q < kSortBlocks; ++q) {
+      for (int q = 0; q < B; ++q) {
         all += c[q];
         if ((uint32_t)q < rank) before += c[q];
       }
@@ -282,7 +291,7 @@ __global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThrea
         place(i < i1, i < i1 ? key_at(i, false) : 0u, i < i1 ? val_at(i) : 0u);
       }
     }
-    cluster_barrier();   // the pass's output, and the peers' totals, before the next pass
+    barrier();   // the pass's output, and the peers' totals, before the next pass
   }
 }
 
@@ -296,7 +305,7 @@ struct SumArgs {
   void* dtable;
   float* part;                 // [chunks][2][dim]: run from before the chunk, run into the next
   int64_t ld_dy, ld_dt, vocab;
-  int32_t n, dim, chunks, accumulate;
+  int32_t n, dim, chunk_len, chunks, accumulate;
   int32_t slabs, cols_shift;   // column threads per chunk = 1 << cols_shift
   float scale;
 };
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
   const int slab = (int)(unit % p.slabs);
   const int64_t chunk = unit / p.slabs;
   if (chunk >= p.chunks) return;
-  const int i0 = (int)(chunk * kChunkPos), i1 = min(p.n, i0 + kChunkPos);
+  const int i0 = (int)(chunk * p.chunk_len), i1 = min(p.n, i0 + p.chunk_len);
   if (VEC && col_of<VEC>(slab, tx, c, 0) >= p.dim) return;
   const uint32_t none = (uint32_t)p.vocab;
   const uint32_t prev = i0 > 0 ? p.key[i0 - 1] : none, next = i1 < p.n ? p.key[i1] : none;
@@ -439,7 +448,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const __gri
   const int slab = (int)(unit % p.slabs);
   const int64_t chunk = unit / p.slabs;
   if (chunk + 1 >= p.chunks) return;
-  const int i0 = (int)(chunk * kChunkPos), i1 = i0 + kChunkPos;
+  const int i0 = (int)(chunk * p.chunk_len), i1 = i0 + p.chunk_len;
   const uint32_t k = p.key[i1 - 1];
   if (k == (uint32_t)p.vocab || p.key[i1] != k) return;           // ends here
   if (i0 > 0 && p.key[i0 - 1] == k) return;                       // an earlier chunk's run
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const __gri
     constexpr int kAhead = 16;
     uint32_t next[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) next[u] = p.key[min(end + u, last) * kChunkPos];
+    for (int u = 0; u < kAhead; ++u) next[u] = p.key[min(end + u, last) * p.chunk_len];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       more = more && end <= last && next[u] == k;
@@ -494,6 +503,12 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const __gri
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
 
+// The columns are cut into slabs of at most kSumThreads threads of 8 columns.
+int64_t slabs_of(int64_t dim) { return cdiv(cdiv(dim, 8), kSumThreads); }
+int64_t chunk_len(int64_t n, int64_t dim) {
+  return cdiv(n, kChunkLong) * slabs_of(dim) < kFewChunks ? kChunkShort : kChunkLong;
+}
+
 struct BwdLayout {
   size_t key0, val0, key1, val1, present, part, total;
 };
@@ -510,14 +525,15 @@ BwdLayout bwd_layout(int64_t vocab, int64_t dim, int64_t n) {
   l.key1 = take((size_t)n * 4);
   l.val1 = take((size_t)n * 4);
   l.present = take((size_t)vocab);
-  l.part = take((size_t)((n + kChunkPos - 1) / kChunkPos) * 2 * (size_t)dim * 4);
+  const int64_t len = chunk_len(n, dim);
+  l.part = take((size_t)cdiv(n, len) * 2 * (size_t)dim * 4);
   l.total = off;
   return l;
 }
 
 int check_table(int64_t vocab, int64_t dim, int64_t n) {
   if (vocab < 1 || dim < 1 || n < 0 || vocab >= (1ll << 31) - 1 || dim >= (1ll << 27) ||
-      n >= (1ll << 31) - kChunkPos)
+      n >= (1ll << 31) - kChunkLong)
     return MFSDP_ESHAPE;
   return MFSDP_OK;
 }
@@ -536,6 +552,28 @@ cudaError_t run_forward(const EmbFwd& a, int sms, cudaStream_t st) {
                            0, st, a)
               : launch_pdl(embedding_forward_kernel<TT, TO, VEC, 1>, dim3((unsigned)grid), dim3(256),
                            0, st, a);
+}
+
+template <int B>
+cudaError_t launch_sort(const SortArgs& a, int64_t fill_blocks, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      embedding_sort_kernel<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = B;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(B + fill_blocks));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = kSortSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = B > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<B>, a);
 }
 
 template <typename TD, typename TG>
@@ -663,13 +701,14 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   a.vocab = vocab;
   a.n = (int32_t)n_tokens;
   a.dim = (int32_t)dim;
-  a.chunks = (int32_t)((n_tokens + kChunkPos - 1) / kChunkPos);
+  a.chunk_len = (int32_t)chunk_len(n_tokens, dim);
+  a.chunks = (int32_t)cdiv(n_tokens, a.chunk_len);
   a.accumulate = accumulate ? 1 : 0;
   a.scale = scale;
   const int64_t col_threads = (dim + 7) / 8;
   while ((1 << a.cols_shift) < kSumThreads && (1 << a.cols_shift) < col_threads) ++a.cols_shift;
   const int64_t tx = 1ll << a.cols_shift, ty = kSumThreads / tx;
-  a.slabs = (int32_t)((col_threads + tx - 1) / tx);
+  a.slabs = (int32_t)slabs_of(dim);
   const int64_t grid = ((int64_t)a.chunks * a.slabs + ty - 1) / ty;
   if (grid >= (1ll << 31)) return MFSDP_ESHAPE;
   if (n_tokens == 0 && accumulate) return MFSDP_OK;
@@ -690,7 +729,7 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
     s.fill_units = row_bytes / (s.fill_vec ? 16 : gb);
     fill_blocks = std::min(cdiv(s.fill_rows * s.fill_units, kSortThreads),
                            (int64_t)(2 * sms - kSortBlocks));
-    fill_blocks = cdiv(fill_blocks, kSortBlocks) * kSortBlocks;
+    fill_blocks = cdiv(fill_blocks, kSortBlocks) * kSortBlocks;  // whole clusters
     if (first < vocab) {
       s.present = reinterpret_cast<uint8_t*>(ws + l.present);
       a.present = s.present;
@@ -704,11 +743,8 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   const bool vec = vec_ok(dtable, ld_dtable, dim, grad_dtype) &&
                    (n_tokens == 0 || vec_ok(dy, ld_dy, dim, dy_dtype));
 
-  cudaError_t e = cudaFuncSetAttribute(embedding_sort_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-  if (e == cudaSuccess)
-    e = launch_pdl(embedding_sort_kernel, dim3((unsigned)(kSortBlocks + fill_blocks)),
-                   dim3(kSortThreads), kSortSmem, st, s);
+  cudaError_t e = n_tokens <= kOneBlock ? launch_sort<1>(s, fill_blocks, st)
+                                        : launch_sort<kSortBlocks>(s, fill_blocks, st);
   if (e == cudaSuccess && n_tokens > 0) {
     const bool db = dy_dtype == MFSDP_DTYPE_BF16, gb = grad_dtype == MFSDP_DTYPE_BF16;
     e = db ? (gb ? run_sum<bf16_t, bf16_t>(a, vec, zero_blocks, st)
