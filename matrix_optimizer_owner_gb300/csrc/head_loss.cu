@@ -61,7 +61,7 @@ struct HeadArgs {
   CUtensorMap h_k, h_mn;                   // compacted H: 64 x 128 K-major box, 3D MN-major view
   CUtensorMap w_k, w_mn;                   // W (or the copy of a piece): 64 x 128 box, and 64 x 64
                                            // boxes or the 3D view
-  CUtensorMap g_k, g_mn, g_st;             // G piece: 64 x 128, 3D view, 32 x 32 stores
+  CUtensorMap g_k, g_mn;                   // G pieces: 64 x 128 box, 3D view
   CUtensorMap dw_st, acc_st;               // dW bf16 and dH fp32 32 x 32 stores
   const int32_t* nlive;                    // live rows
   const int32_t* label;                    // [rows] of the compacted rows
@@ -74,6 +74,8 @@ struct HeadArgs {
   float* zlab;                             // [rows] the label's logit
   uint16_t* dw;                            // unaligned dW rows (dw_tma == 0)
   int64_t ld_dw;
+  uint16_t* g;                             // G pieces, rows of `piece` entries
+  int64_t piece;
   int32_t dim, vocab;
   // the piece whose G is multiplied and the piece of Z that is computed (kGrads: the next one):
   // columns [v0, v0 + width) of the vocabulary, W's map row of column v0, and the first row of
@@ -498,7 +500,6 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     // Warp w covers TMEM lane quarter (w & 3), 32 rows of the CTA's 128, and 128 columns.
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t stg0 = sbase + kHeadStaging + (uint32_t)(warp - 2) * kStagePerWarp;
-    uint32_t nstore = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     float scale = 0.f;                          // largest finite |dloss|
@@ -601,15 +602,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           if (q < nq) {                                   // warp-uniform
             __syncwarp();
             uint32_t (&a32)[32] = buf[q & 1];
-            const uint32_t stg = stg0 + (nstore & 1u) * 2048u;
-            // the halves alternate; a store before this tile may have used both
-            if (lane == 0) {
-              if (q == 0)
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-              else
-                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            // The block is staged so that a warp's stores cover whole 64-byte rows; the halves
+            // of the staging area alternate, so one barrier per chunk is enough.  (By TMA store
+            // a chunk waited for the area's last store to have been read.)
+            const uint32_t stg = stg0 + (q & 1) * 2048u;
+            if (q == 0) {                                 // a product's TMA store may be reading
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
             }
-            __syncwarp();
             tc_ld_wait(a32);
             if (q + 1 < nq) tc_ld32_issue(taddr + (uint32_t)(32 * (q + 1)), buf[(q + 1) & 1]);
             const int c0 = cb + 32 * q, left = P.z_width - c0, hit = lab - c0;
@@ -634,13 +634,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
                      make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
                                 pack_bf16x2(v[8 * k + 4], v[8 * k + 5]),
                                 pack_bf16x2(v[8 * k + 6], v[8 * k + 7])));
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
-              tma_store_block(&P.g_st, stg, c0, P.z_g_row0 + rw);
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            uint16_t* gp = P.g + (int64_t)(P.z_g_row0 + rw) * P.piece + c0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 8 * i + (lane >> 2), k = lane & 3;
+              *reinterpret_cast<uint4*>(gp + (int64_t)row * P.piece + 8 * k) =
+                  lds128(stg + stg_off(row, k));
             }
-            ++nstore;
           }
         }
       } else {
@@ -1293,8 +1294,8 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
     // (fp32: 128, its k-blocks are slower)
     s.splits = std::max<int64_t>(
         1, std::min({cdiv(units, tiles), s.piece / (bf ? 1024 : 128), (int64_t)kMaxSplits}));
-    s.kdh = up(cdiv(s.piece, s.splits), kBK);
-    s.splits = cdiv(s.piece, s.kdh);
+    s.kdh = up(cdiv(std::min(s.piece, vocab), s.splits), kBK);  // no slice of a whole piece is empty
+    s.splits = cdiv(std::min(s.piece, vocab), s.kdh);
     s.buffers = bf && s.pieces > 1 ? 2 : 1;
   }
   return s;
@@ -1529,7 +1530,8 @@ struct HeadCall {
       const uint16_t* g = at<uint16_t>(l.g);
       ok = ok && encode_map(&a.g_k, g, s.buffers * s.rows, s.piece, s.piece, 128u);
       ok = ok && encode_map3d(&a.g_mn, g, s.buffers * s.rows, s.piece, s.piece);
-      ok = ok && encode_map(&a.g_st, g, s.buffers * s.rows, s.piece, s.piece, 32u, 32u, false);
+      a.g = at<uint16_t>(l.g);
+      a.piece = s.piece;
       if (dh) ok = ok && encode_map_f32(&a.acc_st, at<float>(l.acc), s.splits * s.rows, s.pitch, s.pitch, 32u);
       a.dw_tma = dw && aligned_to(dw, 16) && ld_dw % 8 == 0;
       if (a.dw_tma) ok = ok && encode_map(&a.dw_st, dw, s.vocab, s.dim, ld_dw, 32u, 32u, false);
@@ -1719,7 +1721,8 @@ struct HeadCall {
         if (r != MFSDP_OK) return r;
       }
       if (dh) {
-        r = launch_gemm(dev + at0 + 2, d.data() + at0 + 2, (int)s.splits, 0, 1, st);
+        // (a narrower last piece may leave slices without columns: nothing to add there)
+        r = launch_gemm(dev + at0 + 2, d.data() + at0 + 2, (int)cdiv(width, s.kdh), 0, 1, st);
         if (r != MFSDP_OK) return r;
       }
     }
