@@ -633,8 +633,8 @@ int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_tokens, int32
 
 /*
  * Workspace of the head loss.  `backward` selects the call it is for; `weight` and `ld_weight`
- * are what that call will be given (only their alignment is looked at: a bf16 weight whose rows
- * do not start on 16-byte boundaries is copied piece by piece); `piece` as below, 0 for the
+ * are what that call will be given (only their alignment is looked at: a weight whose rows do not
+ * start on 16-byte boundaries is copied piece by piece); `piece` as below, 0 for the
  * forward pass.
  */
 int mfsdp_head_loss_workspace_bytes(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,

@@ -55,13 +55,13 @@ struct EmbFwd {
 };
 
 // ---------------------------------------------------------------- lookup
-// A unit is 8 elements (VEC) or one element of the output; a thread takes U of them, a grid
+// Rows of 16-byte vectors: a unit is 8 elements of the output; a thread takes U of them, a grid
 // apart, with their loads in flight together.
-template <typename TT, typename TO, bool VEC, int U>
+template <typename TT, typename TO, int U>
 __global__ void __launch_bounds__(256) embedding_forward_kernel(const __grid_constant__ EmbFwd p) {
   pdl_launch();
   pdl_wait();
-  const int per_row = VEC ? p.dim / 8 : p.dim;
+  const int per_row = p.dim / 8;
   const int64_t units = p.n * per_row, step = (int64_t)gridDim.x * 256;
   const int64_t u0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const bool small = units < (1ll << 31);
@@ -71,37 +71,52 @@ __global__ void __launch_bounds__(256) embedding_forward_kernel(const __grid_con
   for (int i = 0; i < U; ++i) {
     const int64_t u = u0 + i * step;
     t[i] = u >= units ? -1 : small ? (int64_t)((uint32_t)u / (uint32_t)per_row) : u / per_row;
-    c[i] = (int)(u - t[i] * per_row) * (VEC ? 8 : 1);
+    c[i] = (int)(u - t[i] * per_row) * 8;
     id[i] = t[i] >= 0 ? load_index(p.ids, p.is64, t[i]) : 0;
   }
-  Pack8<TT> a[VEC ? U : 1];
-  float e[VEC ? 1 : U];
+  Pack8<TT> a[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const bool ok = t[i] >= 0 && id[i] >= 0 && id[i] < p.vocab;
     if (t[i] >= 0 && !ok && c[i] == 0) atomicOr(p.status, kStatusBadIndex);
-    const TT* src = static_cast<const TT*>(p.table) + (ok ? id[i] * p.ld_table + c[i] : 0);
-    if (VEC) {
-      if (ok) a[VEC ? i : 0].load(src); else a[VEC ? i : 0].zero();
-    } else {
-      e[VEC ? 0 : i] = ok ? to_f32(*src) : 0.f;
-    }
+    if (ok) a[i].load(static_cast<const TT*>(p.table) + id[i] * p.ld_table + c[i]); else a[i].zero();
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     if (t[i] < 0) continue;
-    TO* dst = static_cast<TO*>(p.out) + t[i] * p.ld_out + c[i];
-    if (VEC) {
-      float v[8];
-      a[VEC ? i : 0].get(v);
+    float v[8];
+    a[i].get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= p.scale;
-      Pack8<TO> b;
-      b.set(v);
-      b.store(dst);
-    } else {
-      *dst = from_f32<TO>(e[VEC ? 0 : i] * p.scale);
-    }
+    for (int j = 0; j < 8; ++j) v[j] *= p.scale;
+    Pack8<TO> b;
+    b.set(v);
+    b.store(static_cast<TO*>(p.out) + t[i] * p.ld_out + c[i]);
+  }
+}
+
+// Other rows: a warp per token and 256 columns, eight elements 32 apart per lane.
+constexpr int kSegment = 256;
+template <typename TT, typename TO>
+__global__ void __launch_bounds__(256)
+    embedding_forward_any_kernel(const __grid_constant__ EmbFwd p) {
+  pdl_launch();
+  pdl_wait();
+  const int segs = (p.dim + kSegment - 1) / kSegment;
+  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), t = unit / segs;
+  if (t >= p.n) return;
+  const int c0 = (int)(unit - t * segs) * kSegment, lane = threadIdx.x & 31;
+  const int64_t id = load_index(p.ids, p.is64, t);
+  const bool ok = id >= 0 && id < p.vocab;
+  if (!ok && c0 == 0 && lane == 0) atomicOr(p.status, kStatusBadIndex);
+  const TT* src = static_cast<const TT*>(p.table) + (ok ? id : 0) * p.ld_table;
+  TO* dst = static_cast<TO*>(p.out) + t * p.ld_out;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = to_f32(src[min(c0 + 32 * j + lane, p.dim - 1)]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = c0 + 32 * j + lane;
+    if (c < p.dim) dst[c] = from_f32<TO>(ok ? v[j] * p.scale : 0.f);
   }
 }
 
@@ -542,16 +557,18 @@ bool vec_ok(const void* p, int64_t ld, int64_t dim, int32_t dtype) {
   return aligned_to(p, 16) && dim % 8 == 0 && (ld * (int64_t)dtype_bytes(dtype)) % 16 == 0;
 }
 
-template <typename TT, typename TO, bool VEC>
-cudaError_t run_forward(const EmbFwd& a, int sms, cudaStream_t st) {
-  const int64_t units = a.n * (VEC ? a.dim / 8 : a.dim);
+template <typename TT, typename TO>
+cudaError_t run_forward(const EmbFwd& a, bool vec, int sms, cudaStream_t st) {
+  if (!vec)
+    return launch_pdl(embedding_forward_any_kernel<TT, TO>,
+                      dim3((unsigned)cdiv(a.n * cdiv(a.dim, kSegment), 8)), dim3(256), 0, st, a);
   // four units per thread once that still fills the GPU
-  const bool four = units > (int64_t)sms * 2048 * 2;
-  const int64_t grid = (units + (four ? 1024 : 256) - 1) / (four ? 1024 : 256);
-  return four ? launch_pdl(embedding_forward_kernel<TT, TO, VEC, 4>, dim3((unsigned)grid), dim3(256),
-                           0, st, a)
-              : launch_pdl(embedding_forward_kernel<TT, TO, VEC, 1>, dim3((unsigned)grid), dim3(256),
-                           0, st, a);
+  const int64_t units = a.n * (a.dim / 8);
+  if (units > (int64_t)sms * 2048 * 2)
+    return launch_pdl(embedding_forward_kernel<TT, TO, 4>, dim3((unsigned)cdiv(units, 1024)),
+                      dim3(256), 0, st, a);
+  return launch_pdl(embedding_forward_kernel<TT, TO, 1>, dim3((unsigned)cdiv(units, 256)), dim3(256), 0,
+                    st, a);
 }
 
 template <int B>
@@ -609,7 +626,9 @@ extern "C" int mfsdp_embedding_forward(int64_t vocab, int64_t dim, int32_t table
       !aligned_to(ids, is64 ? 8 : 4))
     return MFSDP_EALIGN;
   const bool vec = vec_ok(table, ld_table, dim, table_dtype) && vec_ok(out, ld_out, dim, out_dtype);
-  if (n_tokens * (vec ? dim / 8 : dim) > (1ll << 31) * 1024 - 1024) return MFSDP_ESHAPE;
+  // blocks of the launch
+  if ((vec ? cdiv(n_tokens * (dim / 8), 1024) : cdiv(n_tokens * cdiv(dim, kSegment), 8)) >= (1ll << 31))
+    return MFSDP_ESHAPE;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;
@@ -631,7 +650,7 @@ extern "C" int mfsdp_embedding_forward(int64_t vocab, int64_t dim, int32_t table
   auto run = [&](auto in, auto out_t) {
     using TT = decltype(in);
     using TO = decltype(out_t);
-    return vec ? run_forward<TT, TO, true>(a, sms, st) : run_forward<TT, TO, false>(a, sms, st);
+    return run_forward<TT, TO>(a, vec, sms, st);
   };
   const cudaError_t e = tb ? (ob ? run(bf16_t(), bf16_t()) : run(bf16_t(), 0.f))
                            : (ob ? run(0.f, bf16_t()) : run(0.f, 0.f));

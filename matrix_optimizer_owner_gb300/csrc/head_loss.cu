@@ -825,7 +825,14 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
           v.store(d + e);
         }
       } else {
-        for (int e = lane; e < p.pitch; e += 32) d[e] = e < dim ? s[e] : from_f32<T>(0.f);
+        for (int e0 = lane; e0 < p.pitch; e0 += 256) {   // eight loads in flight
+          T v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = e0 + 32 * k < dim ? s[e0 + 32 * k] : from_f32<T>(0.f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (e0 + 32 * k < p.pitch) d[e0 + 32 * k] = v[k];
+        }
       }
     }
     base += total;
@@ -906,8 +913,9 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- few tokens
-// One to kFewTokens tokens are bound by reading W once: a matrix product's 256-row tile would
-// be empty but for them.  A warp takes kFewRows rows of W at a time (all their loads in flight
+// One token (up to kFewTokens where the tensor cores would need a copy of W or run 3xTF32) is
+// bound by reading W once: a matrix product's 256-row tile would be empty but for it.  One token
+// over 128256 x 4096 took 191 us here and 218 on the tensor cores, two 267 and 216.  A warp takes kFewRows rows of W at a time (all their loads in flight
 // together), multiplies them with the tokens' hidden rows, which the block holds in shared
 // memory in fp32, and keeps each token's running (max, sum) in registers.
 constexpr int kFewTokens = 4;
@@ -1055,8 +1063,10 @@ struct FinishArgs {
   int32_t n, dim, pitch, rows, splits, vec;
 };
 
+// A block per token, four columns per thread; the slices are added in order, eight of them in
+// flight (the sums' rows are aligned whatever the caller's are).
 template <typename T>
-__global__ void __launch_bounds__(128) head_finish_kernel(const __grid_constant__ FinishArgs p) {
+__global__ void __launch_bounds__(256) head_finish_kernel(const __grid_constant__ FinishArgs p) {
   pdl_launch();
   pdl_wait();
   const int t = blockIdx.x;
@@ -1064,45 +1074,75 @@ __global__ void __launch_bounds__(128) head_finish_kernel(const __grid_constant_
   const float scale = p.scale ? *p.scale : 1.f;
   T* out = static_cast<T*>(p.dh) + (int64_t)t * p.ld_dh;
   const int64_t slice = (int64_t)p.rows * p.pitch;
-  const float* a = p.acc + (int64_t)(r < 0 ? 0 : r) * p.pitch;
-  if (p.vec) {
-    for (int e = threadIdx.x * 8; e < p.dim; e += 1024) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (r >= 0)
-        for (int s = 0; s < p.splits; ++s) {
-          Pack8<float> q;
-          q.load(a + s * slice + e);
-          float x[8];
-          q.get(x);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] += x[k];
-        }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= scale;
-      Pack8<T> o;
-      o.set(v);
-      o.store(out + e);
+  const float* a = p.acc + (int64_t)max(r, 0) * p.pitch;
+  for (int e = threadIdx.x * 4; e < p.dim; e += 1024) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r >= 0) {
+#pragma unroll 8
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 x = *reinterpret_cast<const float4*>(a + s * slice + e);
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
+      }
     }
-  } else {
-    for (int e = threadIdx.x; e < p.dim; e += 128) {
-      float v = 0.f;
-      if (r >= 0)
-        for (int s = 0; s < p.splits; ++s) v += a[s * slice + e];
-      out[e] = from_f32<T>(v * scale);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] *= scale;
+    if (p.vec) {   // whole groups of four, aligned to them
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(out + e) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                        *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        *reinterpret_cast<float4*>(out + e) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (e + k < p.dim) out[e + k] = from_f32<T>(v[k]);
     }
   }
 }
 
-// Rows [0, rows) x cols of a bf16 matrix into a buffer of 16-byte aligned rows; the rows after
-// them (whole k-blocks) are zero.
+// Rows [0, rows) x cols of a matrix into a buffer of 16-byte aligned rows; the rows after them
+// (whole k-blocks) are zero.  A warp per row, eight words of loads in flight; a bf16 row may start
+// at an odd element, so its words are put together from halves.
+template <typename T>
 __global__ void __launch_bounds__(256)
-    head_copy_rows_kernel(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst, int rows,
+    head_copy_rows_kernel(const T* src, int64_t ld_src, T* dst, int64_t ld_dst, int rows, int total,
                           int cols) {
+  constexpr int E = 4 / (int)sizeof(T), U = 8;   // elements per word
   pdl_launch();
   pdl_wait();
-  const int64_t r = blockIdx.x;
-  for (int c = threadIdx.x; c < cols; c += 256)
-    dst[r * ld_dst + c] = r < rows ? src[r * ld_src + c] : (uint16_t)0;
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= total) return;
+  const T* from = src + (r < rows ? r : 0) * ld_src;
+  T* to = dst + r * ld_dst;
+  const int words = (cols + E - 1) / E;
+  for (int w0 = lane; w0 < words; w0 += 32 * U) {
+    T v[U][E];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < E; ++h) v[u][h] = from[min((w0 + 32 * u) * E + h, cols - 1)];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = (w0 + 32 * u) * E;
+      if (e >= cols) continue;
+      uint32_t word = 0u;
+      if (r < rows) {
+        if constexpr (E == 2) {
+          word = (uint32_t)__bfloat16_as_ushort(v[u][0]);
+          if (e + 1 < cols) word |= (uint32_t)__bfloat16_as_ushort(v[u][1]) << 16;
+        } else {
+          word = __float_as_uint(v[u][0]);
+        }
+      }
+      *reinterpret_cast<uint32_t*>(to + e) = word;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- fp32 path
@@ -1277,9 +1317,12 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   s.dtype = dtype;
   s.backward = backward;
   const bool bf = dtype == MFSDP_DTYPE_BF16;
+  // TMA reads rows that start on 16-byte boundaries
+  s.copy_w = !aligned_to(weight, 16) || ld_w % (bf ? 8 : 4) != 0;
   // the tokens' hidden rows have to fit in shared memory
-  s.few = !backward && n <= kFewTokens && up(dim, 8) * 4 * kFewTokens <= (200 << 10);
-  s.copy_w = bf && !s.few && (!aligned_to(weight, 16) || ld_w % 8 != 0);
+  s.few = !backward && n <= (bf && !s.copy_w ? 1 : kFewTokens) &&
+          up(dim, 8) * 4 * kFewTokens <= (200 << 10);
+  if (s.few) s.copy_w = false;
   s.rows = up(std::max<int64_t>(n, 1), kTile);
   s.pitch = up(dim, 64);
   s.piece = piece_columns(s, piece);
@@ -1292,8 +1335,9 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
     const int64_t units = bf ? sms / 2 : sms;
     const int64_t tiles = cdiv(std::max<int64_t>(n, 1), bf ? kTile : 128) * cdiv(dim, kTile);
     // (fp32: 128, its k-blocks are slower)
-    s.splits = std::max<int64_t>(
-        1, std::min({cdiv(units, tiles), s.piece / (bf ? 1024 : 128), (int64_t)kMaxSplits}));
+    // (in one wave: the fp32 GEMM runs the slices alone; the bf16 launch has other tiles too)
+    s.splits = std::max<int64_t>(1, std::min({bf ? cdiv(units, tiles) : units / tiles,
+                                              s.piece / (bf ? 1024 : 128), (int64_t)kMaxSplits}));
     s.kdh = up(cdiv(std::min(s.piece, vocab), s.splits), kBK);  // no slice of a whole piece is empty
     s.splits = cdiv(std::min(s.piece, vocab), s.kdh);
     s.buffers = bf && s.pieces > 1 ? 2 : 1;
@@ -1332,7 +1376,7 @@ HeadLayout head_layout(const HeadShape& s) {
   l.part = take(!s.backward && bf ? cdiv(s.piece, 128) * s.rows * 8 : 0);
   l.g = take(s.backward || !bf ? s.buffers * s.rows * s.piece * es : 0);
   l.acc = take(s.backward ? s.splits * s.rows * s.pitch * 4 : 0);
-  l.wcopy = take(s.copy_w ? s.buffers * s.piece * s.pitch * 2 : 0);
+  l.wcopy = take(s.copy_w ? s.buffers * s.piece * s.pitch * es : 0);
   const bool t32 = s.backward && !bf;        // fp32: transposed H, G piece and W piece
   l.ht = take(t32 ? s.pitch * s.rows * 4 : 0);
   l.gt = take(t32 ? s.piece * s.rows * 4 : 0);
@@ -1461,8 +1505,16 @@ struct HeadCall {
     f.vec = aligned_to(dh, 16) && s.dim % 8 == 0 &&
             (ld_dh * (int64_t)dtype_bytes(s.dtype)) % 16 == 0;
     return s.dtype == MFSDP_DTYPE_BF16
-               ? launch_pdl(head_finish_kernel<bf16_t>, dim3((unsigned)s.n), dim3(128), 0, st, f)
-               : launch_pdl(head_finish_kernel<float>, dim3((unsigned)s.n), dim3(128), 0, st, f);
+               ? launch_pdl(head_finish_kernel<bf16_t>, dim3((unsigned)s.n), dim3(256), 0, st, f)
+               : launch_pdl(head_finish_kernel<float>, dim3((unsigned)s.n), dim3(256), 0, st, f);
+  }
+
+  // `width` rows of the weight into whole k-blocks of aligned rows
+  template <typename T>
+  cudaError_t copy_rows(const T* from, T* to, int64_t width) const {
+    const int64_t total = up(width, kBK);
+    return launch_pdl(head_copy_rows_kernel<T>, dim3((unsigned)cdiv(total, 8)), dim3(256), 0, st, from,
+                      ld_w, to, s.pitch, (int)width, (int)total, (int)s.dim);
   }
 
   template <typename T, int NT>
@@ -1566,10 +1618,8 @@ struct HeadCall {
       a.z_w_row0 = s.copy_w ? (int32_t)(i % s.buffers * s.piece) : a.z_v0;
       a.z_g_row0 = (int32_t)(i % s.buffers * s.rows);
       if (i >= s.pieces || !s.copy_w) return cudaSuccess;
-      return launch_pdl(head_copy_rows_kernel, dim3((unsigned)up(a.z_width, kBK)), dim3(256), 0, st,
-                        static_cast<const uint16_t*>(weight) + (int64_t)a.z_v0 * ld_w, ld_w,
-                        at<uint16_t>(l.wcopy) + (int64_t)a.z_w_row0 * s.pitch, s.pitch,
-                        (int)a.z_width, (int)s.dim);
+      return copy_rows(static_cast<const bf16_t*>(weight) + (int64_t)a.z_v0 * ld_w,
+                       at<bf16_t>(l.wcopy) + (int64_t)a.z_w_row0 * s.pitch, a.z_width);
     };
     auto z_tiles = [&] { return ntm * cdiv(a.z_width, kTile); };
     cudaError_t e = gather();
@@ -1623,8 +1673,8 @@ struct HeadCall {
       GemmDesc q{};
       q.a = hc;
       q.lda = (int32_t)s.pitch;
-      q.b = w + v0 * ld_w;
-      q.ldb = (int32_t)ld_w;
+      q.b = s.copy_w ? at<float>(l.wcopy) : w + v0 * ld_w;
+      q.ldb = (int32_t)(s.copy_w ? s.pitch : ld_w);
       q.c = z;
       q.ldc = (int32_t)s.piece;
       q.m = (int32_t)s.n;
@@ -1680,6 +1730,8 @@ struct HeadCall {
     if (e != cudaSuccess) return MFSDP_ECUDA;
     for (int64_t i = 0; i < s.pieces; ++i) {
       const int64_t v0 = i * s.piece, width = std::min(s.piece, s.vocab - v0), at0 = i * per;
+      if (s.copy_w && copy_rows(w + v0 * ld_w, at<float>(l.wcopy), width) != cudaSuccess)
+        return MFSDP_ECUDA;
       int r = launch_gemm(dev + at0, d.data() + at0, 1, 0, 1, st);
       if (r != MFSDP_OK) return r;
       if (!s.backward) {
