@@ -320,7 +320,7 @@ struct SumArgs {
   void* dtable;
   float* part;                 // [chunks][2][dim]: run from before the chunk, run into the next
   int64_t ld_dy, ld_dt, vocab;
-  int32_t n, dim, chunk_len, chunks, accumulate;
+  int32_t n, dim, chunk_len, chunks;
   int32_t slabs, cols_shift;   // column threads per chunk = 1 << cols_shift
   float scale;
 };
@@ -331,34 +331,53 @@ __device__ __forceinline__ int col_of(int slab, int tx, int c, int j) {
   return VEC ? (slab * tx + c) * 8 + j : (slab * 8 + j) * tx + c;
 }
 
+// What the table holds in a thread's columns of row v (ACC: the gradient is added to it).
 template <typename TG, bool VEC>
-__device__ __forceinline__ void write_row(const SumArgs& p, uint32_t v, int slab, int tx, int c,
-                                          const float (&acc)[8]) {
-  TG* row = static_cast<TG*>(p.dtable) + (int64_t)v * p.ld_dt;
-  if (VEC) {
-    const int e = col_of<VEC>(slab, tx, c, 0);
-    if (e >= p.dim) return;
-    float o[8];
-    Pack8<TG> q;
-    if (p.accumulate) {
-      q.load(row + e);
-      q.get(o);
-    }
+struct OldRow {
+  Pack8<TG> q;
+  TG e[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const SumArgs& p, uint32_t v, int slab, int tx, int c) {
+    const TG* row = static_cast<const TG*>(p.dtable) + (int64_t)v * p.ld_dt;
+    if (VEC) {
+      q.load(row + col_of<VEC>(slab, tx, c, 0));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = p.accumulate ? fmaf(acc[j], p.scale, o[j]) : acc[j] * p.scale;
+      for (int j = 0; j < 8; ++j)
+        e[VEC ? 0 : j] = row[min(col_of<VEC>(slab, tx, c, j), p.dim - 1)];
+    }
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    if (VEC) {
+      q.get(o);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = to_f32(e[VEC ? 0 : j]);
+    }
+  }
+};
+
+template <typename TG, bool VEC, bool ACC>
+__device__ __forceinline__ void write_row(const SumArgs& p, uint32_t v, int slab, int tx, int c,
+                                          const float (&acc)[8], const OldRow<TG, VEC>& old) {
+  TG* row = static_cast<TG*>(p.dtable) + (int64_t)v * p.ld_dt;
+  float o[8];
+  if (ACC) old.get(o);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = ACC ? fmaf(acc[j], p.scale, o[j]) : acc[j] * p.scale;
+  if (VEC) {
+    Pack8<TG> q;
     q.set(o);
-    q.store(row + e);
+    q.store(row + col_of<VEC>(slab, tx, c, 0));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = col_of<VEC>(slab, tx, c, j);
-      if (e < p.dim)
-        row[e] = from_f32<TG>(p.accumulate ? fmaf(acc[j], p.scale, to_f32(row[e])) : acc[j] * p.scale);
+      if (e < p.dim) row[e] = from_f32<TG>(o[j]);
     }
   }
 }
 
-template <typename TD, typename TG, bool VEC>
+template <typename TD, typename TG, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid_constant__ SumArgs p) {
   pdl_launch();
   pdl_wait();
@@ -393,10 +412,10 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
   uint32_t cur = p.key[i0];
   bool from_before = i0 > 0 && prev == cur;
   float* part = p.part + chunk * 2 * p.dim;
-  auto flush = [&](bool to_next) {
+  auto flush = [&](bool to_next, const OldRow<TG, VEC>& old) {
     if (cur == none) return;
     if (!from_before && !to_next) {
-      write_row<TG, VEC>(p, cur, slab, tx, c, acc);
+      write_row<TG, VEC, ACC>(p, cur, slab, tx, c, acc, old);
     } else {
       float* dst = part + (from_before ? 0 : p.dim);
       if (VEC) {
@@ -413,7 +432,8 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
       }
     }
   };
-  constexpr int U = 8;   // rows loaded ahead
+  constexpr int U = ACC ? 4 : 8;   // rows loaded ahead; with ACC the table's rows beside them
+  OldRow<TG, VEC> before, old[ACC ? U : 1];
   for (int b = i0; b < i1; b += U) {
     uint32_t k[U];
     Pack8<TD> d[U];
@@ -432,12 +452,13 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
         for (int j = 0; j < 8; ++j)
           ds[VEC ? 0 : u][j] = to_f32(row[min(col_of<VEC>(slab, tx, c, j), p.dim - 1)]);
       }
+      if (ACC) old[ACC ? u : 0].load(p, k[u] == none ? 0u : k[u], slab, tx, c);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (b + u >= i1) break;
       if (k[u] != cur) {
-        flush(false);
+        flush(false, u == 0 ? before : old[ACC ? u - 1 : 0]);
         cur = k[u];
         from_before = false;
 #pragma unroll
@@ -448,12 +469,16 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const __grid
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += VEC ? v[j] : ds[VEC ? 0 : u][j];
     }
+    if (ACC)   // the batch's last row
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u == min(U, i1 - b) - 1) before = old[ACC ? u : 0];
   }
-  flush(i1 < p.n && next == cur);
+  flush(i1 < p.n && next == cur, before);
 }
 
 // A run that starts in this chunk and goes on: its partial rows, in chunk order.
-template <typename TG, bool VEC>
+template <typename TG, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const __grid_constant__ SumArgs p) {
   pdl_launch();
   pdl_wait();
@@ -483,6 +508,8 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const __gri
       end += more ? 1 : 0;
     }
   }
+  OldRow<TG, VEC> old;
+  if (ACC) old.load(p, k, slab, tx, c);
   constexpr int U = VEC ? 12 : 4;   // partial rows loaded ahead
   float acc[8];
 #pragma unroll
@@ -511,7 +538,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const __gri
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += q + u < end ? v[u][j] : 0.f;
   }
-  write_row<TG, VEC>(p, k, slab, tx, c, acc);
+  write_row<TG, VEC, ACC>(p, k, slab, tx, c, acc, old);
 }
 
 // ---------------------------------------------------------------- host
@@ -593,15 +620,21 @@ cudaError_t launch_sort(const SortArgs& a, int64_t fill_blocks, cudaStream_t st)
   return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<B>, a);
 }
 
-template <typename TD, typename TG>
-cudaError_t run_sum(const SumArgs& a, bool vec, int64_t zero_blocks, cudaStream_t st) {
-  cudaError_t e;
+template <typename TD, typename TG, bool VEC, bool ACC>
+cudaError_t launch_sum(const SumArgs& a, int64_t zero_blocks, cudaStream_t st) {
   const dim3 g((unsigned)a.sum_blocks), all((unsigned)(a.sum_blocks + zero_blocks)), b(kSumThreads);
-  e = vec ? launch_pdl(embedding_sum_kernel<TD, TG, true>, all, b, 0, st, a)
-          : launch_pdl(embedding_sum_kernel<TD, TG, false>, all, b, 0, st, a);
+  const cudaError_t e = launch_pdl(embedding_sum_kernel<TD, TG, VEC, ACC>, all, b, 0, st, a);
   if (e != cudaSuccess || a.chunks < 2) return e;
-  return vec ? launch_pdl(embedding_join_kernel<TG, true>, g, b, 0, st, a)
-             : launch_pdl(embedding_join_kernel<TG, false>, g, b, 0, st, a);
+  return launch_pdl(embedding_join_kernel<TG, VEC, ACC>, g, b, 0, st, a);
+}
+
+template <typename TD, typename TG>
+cudaError_t run_sum(const SumArgs& a, bool vec, bool acc, int64_t zero_blocks, cudaStream_t st) {
+  if (vec)
+    return acc ? launch_sum<TD, TG, true, true>(a, zero_blocks, st)
+               : launch_sum<TD, TG, true, false>(a, zero_blocks, st);
+  return acc ? launch_sum<TD, TG, false, true>(a, zero_blocks, st)
+             : launch_sum<TD, TG, false, false>(a, zero_blocks, st);
 }
 
 }  // namespace
@@ -722,7 +755,6 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   a.dim = (int32_t)dim;
   a.chunk_len = (int32_t)chunk_len(n_tokens, dim);
   a.chunks = (int32_t)cdiv(n_tokens, a.chunk_len);
-  a.accumulate = accumulate ? 1 : 0;
   a.scale = scale;
   const int64_t col_threads = (dim + 7) / 8;
   while ((1 << a.cols_shift) < kSumThreads && (1 << a.cols_shift) < col_threads) ++a.cols_shift;
@@ -766,10 +798,10 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
                                         : launch_sort<kSortBlocks>(s, fill_blocks, st);
   if (e == cudaSuccess && n_tokens > 0) {
     const bool db = dy_dtype == MFSDP_DTYPE_BF16, gb = grad_dtype == MFSDP_DTYPE_BF16;
-    e = db ? (gb ? run_sum<bf16_t, bf16_t>(a, vec, zero_blocks, st)
-                 : run_sum<bf16_t, float>(a, vec, zero_blocks, st))
-           : (gb ? run_sum<float, bf16_t>(a, vec, zero_blocks, st)
-                 : run_sum<float, float>(a, vec, zero_blocks, st));
+    e = db ? (gb ? run_sum<bf16_t, bf16_t>(a, vec, accumulate != 0, zero_blocks, st)
+                 : run_sum<bf16_t, float>(a, vec, accumulate != 0, zero_blocks, st))
+           : (gb ? run_sum<float, bf16_t>(a, vec, accumulate != 0, zero_blocks, st)
+                 : run_sum<float, float>(a, vec, accumulate != 0, zero_blocks, st));
   }
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }

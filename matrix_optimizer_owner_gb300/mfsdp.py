@@ -452,13 +452,15 @@ def mfsdp_gemm_f32_batched(problems, trans_a: bool = False, trans_b: bool = Fals
 # A call on a small tensor is bound by the time spent here, so each tensor is checked in one
 # helper call, by plain comparisons.
 _FLOAT_CODES, _INDEX_CODES = {}, {}
-_F32 = None
+_F32 = _current_device = _current_raw_stream = None
 
 
 def _learn_dtypes() -> None:
-    global _F32
+    global _F32, _current_device, _current_raw_stream
     import torch
     _F32 = torch.float32
+    _current_device = torch.cuda.current_device
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _FLOAT_CODES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
     _INDEX_CODES.update({torch.int32: INDEX_I32, torch.int64: INDEX_I64})
 
@@ -521,13 +523,10 @@ def _two_dims(t, name: str):
 def _device_stream(dev: int, stream) -> Optional[int]:
     """The stream to launch on; `dev`, which holds every tensor, has to be the current CUDA
     device (a host pointer would fault the GPU)."""
-    import torch
-    if dev < 0 or torch.cuda.current_device() != dev:
+    if dev < 0 or _current_device() != dev:
         raise ValueError("expected tensors on the current CUDA device")
-    if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            return raw(dev)
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(dev)
     return _stream(stream)
 
 
@@ -539,7 +538,7 @@ def _workspace(ws, nbytes: int, like, dev: int, stream):
         return ws, ws.numel() * ws.element_size()
     import torch
     ws = like.new_empty((nbytes or 1,), dtype=torch.uint8)
-    if stream is not None:
+    if stream is not None:  # the block may be reused on the current stream otherwise
         ws.record_stream(stream if hasattr(stream, "cuda_stream")
                          else torch.cuda.ExternalStream(stream))
     return ws, nbytes
