@@ -39,7 +39,7 @@
  *     Conditions found on the device (a bounded wait that ran out, a non-finite norm) are
  *     recorded in the device status word and returned by mfsdp_query_status.
  *   - bf16 buffers hold IEEE bfloat16 values (uint16_t storage).  fp32 buffers are float.
- *     All device buffers must be 16-byte aligned.
+ *     All device buffers must be 16-byte aligned, except where a call states otherwise.
  *   - Matrices are row-major rows x cols.  m = min(rows, cols), n = max(rows, cols).
  */
 #ifndef MFSDP_H
@@ -560,7 +560,8 @@ int mfsdp_owner_reduce_momentum_noalloc(const mfsdp_matrix* mats, int32_t n_mats
  * element boundary (rows that start on 16-byte boundaries and hold a multiple of 8 elements
  * are read and written as 16-byte vectors).  Every sum has a fixed order: results repeat bit
  * for bit.  Nothing is kept between calls.  Inputs and outputs must not overlap except where
- * stated.  Work is enqueued on `stream`; the calls can be captured in a CUDA graph.  Errors:
+ * stated.  Work is enqueued on `stream`; the calls can be captured in a CUDA graph (after a first
+ * call outside a capture, which loads the kernels).  Errors:
  * MFSDP_EINVAL (null pointer, bad enum, a pitch below the row length), MFSDP_ESHAPE,
  * MFSDP_EALIGN (a buffer is not aligned to its element, a workspace not to 256 bytes),
  * MFSDP_EWORKSPACE, MFSDP_ENODEVICE, MFSDP_ECUDA.

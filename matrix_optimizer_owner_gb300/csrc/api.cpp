@@ -172,6 +172,19 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUD
 
 uint64_t mfsdp::wait_limit_ns() { return g_wait_limit_ns.load(); }
 
+int* mfsdp::device_status() {
+  constexpr int kCached = 64;
+  static std::atomic<int*> cache[kCached];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  int* p = dev < kCached ? cache[dev].load() : nullptr;
+  if (!p) {
+    p = status_word_address();
+    if (dev < kCached) cache[dev].store(p);
+  }
+  return p;
+}
+
 int mfsdp::device_sms(int* sms) {
   constexpr int kCached = 64;
   static std::atomic<int> cache[kCached];   // per device: SM count, or -1 (not sm_103); 0 unknown

@@ -676,7 +676,7 @@ extern "C" int mfsdp_embedding_forward(int64_t vocab, int64_t dim, int32_t table
   a.dim = (int32_t)dim;
   a.is64 = is64;
   a.scale = scale;
-  a.status = status_word_address();
+  a.status = device_status();
   if (!a.status) return MFSDP_ECUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool tb = table_dtype == MFSDP_DTYPE_BF16, ob = out_dtype == MFSDP_DTYPE_BF16;
@@ -721,7 +721,7 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;
-  int* status = status_word_address();
+  int* status = device_status();
   if (!status) return MFSDP_ECUDA;
   char* ws = static_cast<char*>(workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

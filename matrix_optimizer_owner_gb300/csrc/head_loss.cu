@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <new>
 #include <type_traits>
 #include <vector>
 
@@ -1659,6 +1660,16 @@ struct HeadCall {
     return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
   }
 
+  int run() const {
+    if (s.few) return run_few();
+    if (s.dtype == MFSDP_DTYPE_BF16) return run_bf16();
+    try {
+      return run_f32();
+    } catch (const std::bad_alloc&) {  // the problem table of very many pieces
+      return MFSDP_ESHAPE;
+    }
+  }
+
   int run_f32() const {
     // problem tables of every piece: Z, dW, and dH's slices
     const int64_t per = s.backward ? 2 + s.splits : 1;
@@ -1841,7 +1852,7 @@ extern "C" int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vo
   if (n_tokens == 0) return MFSDP_OK;
   const int dst = device_sms(&c.sms);
   if (dst != MFSDP_OK) return dst;
-  c.status = status_word_address();
+  c.status = device_status();
   if (!c.status) return MFSDP_ECUDA;
   c.ws = static_cast<char*>(workspace);
   c.hidden = hidden;
@@ -1854,8 +1865,7 @@ extern "C" int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vo
   c.loss = loss;
   c.lse = lse;
   c.st = static_cast<cudaStream_t>(stream);
-  if (c.s.few) return c.run_few();
-  return dtype == MFSDP_DTYPE_BF16 ? c.run_bf16() : c.run_f32();
+  return c.run();
 }
 
 extern "C" int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab,
@@ -1884,7 +1894,7 @@ extern "C" int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t v
   if (!dhidden && !dweight) return MFSDP_OK;
   const int dst = device_sms(&c.sms);
   if (dst != MFSDP_OK) return dst;
-  c.status = status_word_address();
+  c.status = device_status();
   if (!c.status) return MFSDP_ECUDA;
   c.st = static_cast<cudaStream_t>(stream);
   if (n_tokens == 0) {   // no tokens: the weight's gradient is zero
@@ -1908,5 +1918,5 @@ extern "C" int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t v
   c.ld_dh = ld_dhidden;
   c.dw = dweight;
   c.ld_dw = ld_dweight;
-  return dtype == MFSDP_DTYPE_BF16 ? c.run_bf16() : c.run_f32();
+  return c.run();
 }

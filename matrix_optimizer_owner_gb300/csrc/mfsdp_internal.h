@@ -116,6 +116,7 @@ cudaError_t launch_adamw(const AdamParams& p, int contrib_dtype, cudaStream_t s)
 cudaError_t launch_copy2d(const CopyParams& p, cudaStream_t s);
 cudaError_t launch_wait_timeout_selftest(uint64_t limit_ns, int* status, cudaStream_t s);
 int* status_word_address();  // device address of this device's status word (nullptr on error)
+int* device_status();        // the same, looked up once per device
 uint64_t wait_limit_ns();    // limit of every bounded device-side wait (mfsdp_set_wait_limit_ns)
 int device_sms(int* sms);    // MFSDP status; the current device's SM count (sm_103 devices only)
 

@@ -13,6 +13,7 @@
 // block walks; the blocks' sums go to the workspace and a second launch adds them in block
 // order: no atomics, the result does not depend on timing.
 #include <algorithm>
+#include <atomic>
 
 #include "elem.cuh"
 #include "mfsdp.h"
@@ -552,17 +553,23 @@ cudaError_t by_shape(int64_t cols, F&& f) {
 #undef MFSDP_NORM_K
 }
 
-// Raises a kernel's shared-memory limit and counts the blocks that an SM holds (at least 1).
+// Raises a kernel's shared-memory limit and counts the blocks that an SM holds (at least 1), once
+// per device; `cache` is the kernel's own.
+constexpr int kCachedDevices = 64;
 template <typename K>
-int resident(K kernel, int threads, int smem) {
-  int occ = 0;
+int resident(std::atomic<int>* cache, K kernel, int threads, int smem) {
+  int dev = -1, occ = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev < kCachedDevices) occ = cache[dev].load();
+  if (occ > 0) return occ;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return 1;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) == cudaSuccess &&
-                 occ > 0
-             ? occ
-             : 1;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) != cudaSuccess ||
+      occ < 1)
+    return 1;
+  if (dev < kCachedDevices) cache[dev].store(occ);
+  return occ;
 }
 
 struct FwdLaunch {
@@ -573,7 +580,8 @@ struct FwdLaunch {
   cudaError_t operator()() const {
     const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
     constexpr int smem = kRing<T, VEC> ? Ring<T, 1, TPR, K>::kBytes : 0;
-    static const int occ = resident(norm_forward_kernel<T, TPR, K, VEC>, threads, smem);
+    static std::atomic<int> cache[kCachedDevices];
+    const int occ = resident(cache, norm_forward_kernel<T, TPR, K, VEC>, threads, smem);
     const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
     const int64_t g = std::min<int64_t>((int64_t)sms * occ, need);
     return launch_pdl(norm_forward_kernel<T, TPR, K, VEC>, dim3((unsigned)g), dim3(threads), smem,
@@ -590,7 +598,8 @@ struct BwdLaunch {
   cudaError_t operator()() const {
     const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
     constexpr int smem = kRing<T, VEC> ? Ring<T, 2, TPR, K>::kBytes : 0;
-    static const int occ = resident(norm_backward_kernel<T, TPR, K, VEC>, threads, smem);
+    static std::atomic<int> cache[kCachedDevices];
+    const int occ = resident(cache, norm_backward_kernel<T, TPR, K, VEC>, threads, smem);
     const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
     const int64_t g = std::min({(int64_t)sms * occ, (int64_t)max_blocks, need});
     *blocks = (int)g;
@@ -695,7 +704,7 @@ extern "C" int mfsdp_norm_backward(int32_t kind, int64_t rows, int64_t cols, int
   const size_t es = dtype_bytes(dtype), ps = dtype_bytes(param_dtype);
   if (!aligned_to(dy, es) || !aligned_to(x, es) || !aligned_to(dx, es) ||
       !aligned_to(weight, ps) || !aligned_to(dweight, ps) || !aligned_to(dbias, ps) ||
-      !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(workspace, 16))
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(workspace, 256))
     return MFSDP_EALIGN;
   size_t need = 0;
   mfsdp_norm_backward_workspace_bytes(rows, cols, &need);

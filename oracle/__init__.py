@@ -19,6 +19,12 @@ Source: "MatrixFSDP: communication-free matrix optimizers under ZeRO-3 parameter
   * ``shampoo`` — owner Shampoo: statistics, inverse fourth roots, update (§5.7).
   * ``soap``   — owner SOAP: Adam in the eigenbasis of the Shampoo statistics (§5.7).
 
+Beside the paper's step, the operators whose weights live in its AdamW share, from their
+definitions:
+  * ``norm``      — layer norm and RMS norm, forward and backward.
+  * ``embedding`` — lookup with a scale, and the table's gradient.
+  * ``head_loss`` — softmax cross entropy of an output head, and both gradients.
+
 Pins (checked by ``tests/test_oracle_pins.py`` against things other than this code):
   plan   — invariants, the list-scheduling bound, hand-worked assignments, brute force;
   reduce — exact sums of integer-valued contributions;

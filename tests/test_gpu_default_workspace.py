@@ -1,0 +1,81 @@
+"""The binding's default workspaces: one per host thread and stream, fresh ones for captures and
+for explicit streams, so that calls that overlap never share one."""
+
+import threading
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(n, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    ids = torch.randint(700, (n,), generator=gen, device="cuda")
+    return ids, torch.randn(n, 128, generator=gen, device="cuda")
+
+
+def _grad(ids, dy, out):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    mfsdp.mfsdp_embedding_backward(ids, dy, 1.0, out)
+    return out
+
+
+def test_kept_per_stream_and_grown():
+    from matrix_optimizer_owner_gb300 import mfsdp
+    out = torch.empty(700, 128, device="cuda")
+    _grad(*_case(10, 0), out)
+    raw = torch.cuda.current_stream().cuda_stream
+    key = (torch.cuda.current_device(), raw)
+    first = mfsdp._scratch.buffers[key][1]
+    _grad(*_case(10, 0), out)
+    assert mfsdp._scratch.buffers[key][1] is first
+    _grad(*_case(60000, 0), out)                     # a larger one replaces it
+    grown = mfsdp._scratch.buffers[key]
+    assert grown[1] is not first and grown[0] > first.numel()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        _grad(*_case(10, 0), torch.empty_like(out))
+    assert mfsdp._scratch.buffers[(key[0], s.cuda_stream)][1] is not grown[1]
+    torch.cuda.synchronize()
+
+
+def test_capture_does_not_use_the_kept_one():
+    from matrix_optimizer_owner_gb300 import mfsdp
+    ids, dy = _case(3000, 1)
+    want = _grad(ids, dy, torch.empty(700, 128, device="cuda")).clone()
+    out = torch.zeros_like(want)
+    kept = dict(mfsdp._scratch.buffers)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _grad(ids, dy, out)
+    assert mfsdp._scratch.buffers == kept
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_threads_and_streams_at_the_same_time():
+    torch.cuda.synchronize()
+    cases = [_case(2000 + 500 * i, 2 + i) for i in range(4)]
+    want = [_grad(ids, dy, torch.empty(700, 128, device="cuda")).clone() for ids, dy in cases]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        torch.cuda.set_device(0)
+        # two threads share a stream, two have their own
+        with torch.cuda.stream(streams[i]):
+            for _ in range(20):
+                got[i] = _grad(*cases[i], torch.empty(700, 128, device="cuda"))
+        streams[i].synchronize()
+
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    streams = [a, a, b, c]
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
