@@ -110,6 +110,7 @@ struct TileList {
     int kind, count, rounds, base, stride, rest;
   };
   static constexpr int kKinds = PHASE == kStats ? 1 : 3;
+  static constexpr int kNone = 0x7FFFFFFF; // load of an empty group
   int live, ntm, ntn, ntd, kdh, npairs;
   Deal deal[kKinds];
   int z_step, z_dn, z_dm;                  // a step of npairs Z tiles, in columns and rows
@@ -142,64 +143,82 @@ struct TileList {
           t = n[b]; n[b] = n[b + 1]; n[b + 1] = t;
           t = kind[b]; kind[b] = kind[b + 1]; kind[b + 1] = t;
         }
-    int cnt[4] = {npairs, 0, 0, 0}, load[4] = {0, 0, 0, 0}, first[4] = {0, 0, 0, 0}, groups = 1;
+    // The groups in order of load, empty ones last.  Every loop runs over all four with constant
+    // indices, so they stay in registers: each thread goes through this before its first tile.
+    int first[4] = {0, 0, 0, 0}, cnt[4] = {npairs, 0, 0, 0}, load[4] = {0, kNone, kNone, kNone};
 #pragma unroll
     for (int c = 0; c < 3; ++c) {
-      const int kc = max(k[c], 1);
-      int64_t total = (int64_t)n[c] * kc;
-      for (int g = 0; g < groups; ++g) total += (int64_t)cnt[g] * load[g];
-      int level = (int)(total / npairs), given, q[4];
-      for (;; level -= kc) {               // lower where a group is above the mean
-        given = 0;
-        for (int g = 0; g < groups; ++g) {
-          q[g] = max(0, (level - load[g]) / kc);
-          given += q[g] * cnt[g];
-        }
-        if (given <= n[c]) break;
-      }
       Deal d{kind[c], n[c], 0, 0, 1, 0};
-      int base = 0, mine = 0;
-      for (int g = 0; g < groups; ++g) {
-        if (pair >= first[g] && pair < first[g] + cnt[g]) {
-          mine = g;
-          d.rounds = q[g];
-          d.base = base + pair - first[g];
-          d.stride = cnt[g];
-        }
-        base += q[g] * cnt[g];
-        load[g] += q[g] * kc;
-      }
-      // the rest, in order of load
-      int order[4] = {0, 1, 2, 3};
-      for (int a = 0; a < groups; ++a)
-        for (int b = 0; b + 1 < groups; ++b)
-          if (load[order[b]] > load[order[b + 1]]) {
-            const int t = order[b]; order[b] = order[b + 1]; order[b + 1] = t;
+      const int kc = max(k[c], 1);
+      if (n[c] > 0) {
+        int64_t total = (int64_t)n[c] * kc;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) total += (int64_t)cnt[g] * (cnt[g] > 0 ? load[g] : 0);
+        int level = total < (1ll << 31) ? (int)((uint32_t)total / (uint32_t)npairs)
+                                        : (int)(total / npairs);
+        int given, q[4];
+        do {                               // lower where a group is above the mean
+          given = 0;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            q[g] = cnt[g] > 0 && level > load[g] ? (int)((uint32_t)(level - load[g]) / (uint32_t)kc) : 0;
+            given += q[g] * cnt[g];
           }
-      const int rest = n[c] - base, full = rest / npairs, extra = rest - full * npairs;
-      int before = 0, cut = -1, cut_at = 0;
-      for (int a = 0; a < groups; ++a) {
-        const int g = order[a];
-        if (g == mine) d.rest = base + before + pair - first[g];
-        load[g] += full * kc;
-        if (before + cnt[g] <= extra) {
-          load[g] += kc;
-        } else if (before < extra) {
-          cut = g;
-          cut_at = extra - before;
+          level -= kc;
+        } while (given > n[c]);
+        int base = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (pair >= first[g] && pair < first[g] + cnt[g]) {
+            d.rounds = q[g];
+            d.base = base + pair - first[g];
+            d.stride = cnt[g];
+          }
+          base += q[g] * cnt[g];
+          if (cnt[g] > 0) load[g] += q[g] * kc;
         }
-        before += cnt[g];
-      }
-      if (cut >= 0 && groups < 4) {        // the front part of one group took one more
-        first[groups] = first[cut] + cut_at;
-        cnt[groups] = cnt[cut] - cut_at;
-        load[groups] = load[cut];
-        cnt[cut] = cut_at;
-        load[cut] += kc;
-        ++groups;
+        sort_groups(first, cnt, load);
+        // what is left, in order of load
+        const int rest = n[c] - base, full = rest < npairs ? 0 : rest / npairs;
+        const int extra = rest - full * npairs;
+        int before = 0, cut = 0, cut_first = 0, cut_load = kNone;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (pair >= first[g] && pair < first[g] + cnt[g]) d.rest = base + before + pair - first[g];
+          const int took = max(0, min(extra - before, cnt[g]));   // pairs of it with one tile more
+          before += cnt[g];
+          if (cnt[g] == 0) continue;
+          load[g] += full * kc;
+          if (took > 0 && took < cnt[g]) {                        // at most one group is cut
+            cut = cnt[g] - took;
+            cut_first = first[g] + took;
+            cut_load = load[g];
+            cnt[g] = took;
+          }
+          if (took > 0) load[g] += kc;
+        }
+        if (cut > 0) {                     // the last place is free: two kinds make three groups
+          first[3] = cut_first;
+          cnt[3] = cut;
+          load[3] = cut_load;
+        }
+        sort_groups(first, cnt, load);
       }
       deal[c] = d;
     }
+  }
+
+  // Four groups by load.
+  static __device__ __forceinline__ void sort_groups(int (&first)[4], int (&cnt)[4], int (&load)[4]) {
+#pragma unroll
+    for (int a = 0; a < 3; ++a)
+#pragma unroll
+      for (int b = 0; b < 3 - a; ++b)
+        if (load[b] > load[b + 1]) {
+          int t = load[b]; load[b] = load[b + 1]; load[b + 1] = t;
+          t = cnt[b]; cnt[b] = cnt[b + 1]; cnt[b + 1] = t;
+          t = first[b]; first[b] = first[b + 1]; first[b + 1] = t;
+        }
   }
 
   // Tiles of this pair in deal c, and the contraction of its i-th one.
@@ -594,8 +613,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         const float dl = live && scale > 0.f ? P.dl[r] / scale : 0.f;
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
-        // whole k-blocks of G are written: the columns past the end are zero
-        const int nq = min(kHeadChunks, ((P.z_width + kBK - 1) / kBK * kBK - cb + 31) / 32);
+        // whole k-blocks of G are written, in both directions: the columns past the end and the
+        // rows past the live ones are zero (further rows only meet rows of dH that are not read)
+        const int nq = rw < (tiles.live + kBK - 1) / kBK * kBK
+                           ? min(kHeadChunks, ((P.z_width + kBK - 1) / kBK * kBK - cb + 31) / 32)
+                           : 0;
         uint32_t buf[2][32];
         if (nq > 0) tc_ld32_issue(taddr, buf[0]);
 #pragma unroll
