@@ -6,12 +6,19 @@
 // values (no cancellation of large means).  Backward, with z = (x - mu) r and g = dy w:
 //     dx = r (g - sum(g) / n [layer] - z sum(g z) / n),  dw = sum_rows dy z,  db = sum_rows dy.
 //
-// Both directions are bound by memory: forward moves 2 and backward 3 values per element.
-// Rows of up to 1024 elements take a warp each (no block barrier; 8 rows in flight per block),
-// longer ones a block each with at most 32 elements per thread; rows beyond 8192 elements are
-// read in passes.  Backward keeps every column's dw and db sums in registers over the rows a
-// block walks; the blocks' sums go to the workspace and a second launch adds them in block
+// Both directions are bound by memory: forward moves 2 and backward 3 values per element.  Rows of
+// up to 1024 elements take a warp each (no block barrier), longer ones a block with 16 elements
+// per thread; rows beyond 8192 elements are read in passes.  A persistent grid walks the rows with
+// the parameters in registers.  Backward keeps every column's dw and db sums in registers over the
+// rows a block walks; the blocks' sums go to the workspace and a second launch adds them in block
 // order: no atomics, the result does not depend on timing.
+//
+// Measured (bf16, all launches of both passes by graph replay, 6.78 TB/s being a copy's rate):
+// 16384 rows of 768 in 29 us, 3.5 TB/s of the 101 MB that have to move (15 us); 8192 rows of 4096
+// in 68 us, 3.9 TB/s of 268 MB (40 us).  What remains is latency: in the backward kernel memory is
+// busy half of the time, and the warps wait on the row sums' shuffles and shared-memory reads.  A
+// group of warps per row with one chunk per thread instead, for more warps, was slower at every
+// width (768: 65 us, 4096: 145).
 #include <algorithm>
 #include <atomic>
 
@@ -23,7 +30,6 @@ namespace {
 
 constexpr int kNormWarps = 8;         // warps per block of the warp-per-row kernels
 constexpr int kWarpRowMax = 1024;     // longest row one warp takes
-constexpr int kMaxChunks = 4;         // 8-element chunks per thread
 constexpr int kRegRowMax = 512 * 8 * 2;
 
 struct NormArgs {
@@ -67,62 +73,49 @@ __device__ __forceinline__ void store_chunk(T* row, int64_t n, int t, int k, con
   }
 }
 
-// The rows a thread will need next, as they lie in memory: N matrices (x, or x and dy) with K
-// chunks of 8 elements each.  Rows of 16-byte vectors are copied ahead to shared memory
-// (cp.async, S rows deep); a thread reads back only what it copied, so no barrier is needed, and
-// the bytes in flight do not cost registers: with one row ahead in registers, 24 KB per SM were
-// in flight and the 768-wide backward pass stayed at 3.8 TB/s.
-template <typename T, int N, int TPR, int K>
+// The bf16 rows a thread will need next, as they lie in memory: N matrices (x, or x and dy) with
+// K chunks of 8 elements each, copied ahead to shared memory (cp.async, kDepth rows deep).  A
+// thread reads back only what it copied, so no barrier is needed, and the bytes in flight do not
+// cost registers: with one row ahead in registers, 24 KB per SM were in flight and the 768-wide
+// backward pass stayed at 3.8 TB/s.
+template <int N, int TPR, int K>
 struct Ring {
   static constexpr int kThreads = TPR == 32 ? 32 * kNormWarps : TPR;
-  static constexpr int kVecs = (int)sizeof(T) / 2;            // 16-byte vectors per chunk
-  static constexpr int kStage = N * K * kVecs * kThreads * 16;
+  static constexpr int kStage = N * K * kThreads * 16;
   static constexpr int kDepth = kStage * 4 <= 96 * 1024 ? 4 : kStage * 3 <= 96 * 1024 ? 3 : 2;
   static constexpr int kBytes = kDepth * kStage;
   uint32_t base;
   __device__ __forceinline__ explicit Ring(const void* smem) {
     base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
   }
-  __device__ __forceinline__ uint32_t at(int stage, int m, int k, int v) const {
-    return base + (uint32_t)((((stage * N + m) * K + k) * kVecs + v) * kThreads * 16);
+  __device__ __forceinline__ uint32_t at(int stage, int m, int k) const {
+    return base + (uint32_t)(((stage * N + m) * K + k) * kThreads * 16);
   }
   // one matrix's row into a stage; chunks past the end are zero
-  __device__ __forceinline__ void copy(int stage, int m, const T* row, int n, int t) const {
+  __device__ __forceinline__ void copy(int stage, int m, const void* mat, int64_t at_row, int n,
+                                       int t) const {
+    const bf16_t* row = static_cast<const bf16_t*>(mat) + at_row;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int e = (k * TPR + t) * 8;
-      const T* src = row + (e < n ? e : 0);
-      const int bytes = e < n ? 16 : 0;
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, m, k, v)),
-                     "l"(src + v * (16 / (int)sizeof(T))), "r"(bytes)
-                     : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, m, k)),
+                   "l"(row + (e < n ? e : 0)), "r"(e < n ? 16 : 0)
+                   : "memory");
     }
   }
   __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
-  // the oldest of kDepth groups has landed
+  // the NR oldest of kDepth groups have landed
+  template <int NR>
   __device__ __forceinline__ void wait() const {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - NR) : "memory");
   }
   __device__ __forceinline__ void get(int stage, int m, int k, float (&v)[8]) const {
-    uint32_t w[4 * kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
-                   : "r"(at(stage, m, k, i))
-                   : "memory");
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    }
+    Pack8<bf16_t> p;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(p.a.x), "=r"(p.a.y), "=r"(p.a.z), "=r"(p.a.w)
+                 : "r"(at(stage, m, k))
+                 : "memory");
+    p.get(v);
   }
 };
 
@@ -217,6 +210,39 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* red, int& tu
   }
 }
 
+// The same for two rows at a time, (a.x, a.y) and (b.x, b.y), in one tree and with one barrier.
+template <int TPR>
+__device__ __forceinline__ void row_sum4(float2& a, float2& b, float* red, int& turn) {
+  // after two halvings lanes 0-7, 8-15, 16-23 and 24-31 hold one of the four values each
+  const bool hi = threadIdx.x & 16, odd = threadIdx.x & 8;
+  float x = hi ? b.x : a.x, y = hi ? b.y : a.y;
+  x += __shfl_xor_sync(0xFFFFFFFFu, hi ? a.x : b.x, 16);
+  y += __shfl_xor_sync(0xFFFFFFFFu, hi ? a.y : b.y, 16);
+  float v = odd ? y : x;
+  v += __shfl_xor_sync(0xFFFFFFFFu, odd ? x : y, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (TPR == 32) {
+    a = make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 8));
+    b = make_float2(__shfl_sync(0xFFFFFFFFu, v, 16), __shfl_sync(0xFFFFFFFFu, v, 24));
+    return;
+  }
+  constexpr int W = TPR / 32;
+  float* buf = red + turn * 4 * W;
+  turn ^= 1;
+  if ((threadIdx.x & 7) == 0) buf[threadIdx.x >> 3] = v;
+  __syncthreads();
+  a = b = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float4 q = reinterpret_cast<const float4*>(buf)[i];
+    a.x += q.x;
+    a.y += q.y;
+    b.x += q.z;
+    b.y += q.w;
+  }
+}
+
 // ---------------------------------------------------------------- forward
 template <typename T, int TPR, int K, bool VEC>
 __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
@@ -231,11 +257,11 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
   int turn = 0;
   extern __shared__ uint4 ring_smem[];
   constexpr bool kUseRing = kRing<T, VEC>;
-  using R = Ring<T, 1, TPR, K>;
+  using R = Ring<1, TPR, K>;
   const R ring(ring_smem);
   RowChunks<T, TPR, kUseRing ? 1 : K, VEC> cur, nxt;
   auto fetch = [&](int64_t i, int stage) {
-    if (i < p.rows) ring.copy(stage, 0, static_cast<const T*>(p.x) + i * p.ld_x, (int)p.cols, t);
+    if (i < p.rows) ring.copy(stage, 0, p.x, i * p.ld_x, (int)p.cols, t);
     ring.commit();
   };
   if (kUseRing) {
@@ -251,7 +277,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
   for (; row < p.rows; row += step) {     // whole warps (or the whole block) stay together
     if (kUseRing) {
       fetch(row + (R::kDepth - 1) * step, stage == 0 ? R::kDepth - 1 : stage - 1);
-      ring.wait();
+      ring.template wait<1>();
     } else if (row + step < p.rows) {
       nxt.load(static_cast<const T*>(p.x) + (row + step) * p.ld_x, p.cols, t);
     }
@@ -337,9 +363,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR,
                                   TPR == 32 ? 1 : TPR == 256 && sizeof(T) == 2 && VEC ? 3 : 512 / TPR)
     norm_backward_kernel(const __grid_constant__ NormArgs p) {
   constexpr int kRowsPerBlock = TPR == 32 ? kNormWarps : 1;
-  // rows outside the ring: the next one is loaded ahead where its raw values fit in registers
-  constexpr bool kAhead = sizeof(T) * K <= 8;
-  __shared__ float red[TPR == 32 ? 1 : 4 * (TPR / 32)];
+  __shared__ __align__(16) float red[TPR == 32 ? 4 : 8 * (TPR / 32)];
   __shared__ float comb[TPR == 32 ? kNormWarps * 32 * 8 : 1];
   pdl_launch();
   pdl_wait();
@@ -348,98 +372,139 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR,
   int turn = 0;
   const int64_t step = (int64_t)gridDim.x * kRowsPerBlock;
   int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + sub;
-  extern __shared__ uint4 ring_smem[];
-  constexpr bool kUseRing = kRing<T, VEC>;
-  using R = Ring<T, 2, TPR, K>;
-  const R ring(ring_smem);
-  using Chunks = RowChunks<T, TPR, kUseRing ? 1 : K, VEC>;
-  Chunks xc, gc, xn, gn;
-  auto fetch = [&](int64_t i, int stage) {
-    if (i < p.rows) {
-      ring.copy(stage, 0, static_cast<const T*>(p.x) + i * p.ld_x, (int)p.cols, t);
-      ring.copy(stage, 1, static_cast<const T*>(p.dy) + i * p.ld_dy, (int)p.cols, t);
-    }
-    ring.commit();
-  };
-  auto load_row = [&](Chunks& x, Chunks& g, int64_t i) {
-    x.load(static_cast<const T*>(p.x) + i * p.ld_x, p.cols, t);
-    g.load(static_cast<const T*>(p.dy) + i * p.ld_dy, p.cols, t);
-  };
-  if (kUseRing) {
-#pragma unroll
-    for (int i = 0; i < R::kDepth - 1; ++i) fetch(row + i * step, i);
-  } else if (row < p.rows) {
-    load_row(xc, gc, row);
-  }
   float aw[K][8], ab[K][8], w[K][8];
-  load_params<TPR, K, VEC>(p.w, p.wbf16, p.pvec, p.cols, t, 1.f, w);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int j = 0; j < 8; ++j) aw[k][j] = ab[k][j] = 0.f;
-  int stage = 0;
-  float r_next = 0.f, mu_next = 0.f;       // the statistics, a row ahead too
-  auto fetch_stats = [&](int64_t i) {
-    if (i >= p.rows) return;
-    r_next = p.rstd_in[i];
-    if (p.layer) mu_next = p.mean_in[i];
+  // a chunk's part of the row's sums and of the columns' (past the row's end dy is 0)
+  auto add = [&](int k, const float (&z)[8], float (&g)[8], float2& s) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      aw[k][j] = fmaf(g[j], z[j], aw[k][j]);
+      ab[k][j] += g[j];
+      g[j] *= w[k][j];
+      s.x += g[j];
+      s.y = fmaf(g[j], z[j], s.y);
+    }
   };
-  fetch_stats(row);
-  for (; row < p.rows; row += step) {
-    const float r = r_next, mu = mu_next;
-    fetch_stats(row + step);
-    if (kUseRing) {
-      fetch(row + (R::kDepth - 1) * step, stage == 0 ? R::kDepth - 1 : stage - 1);
-      ring.wait();
-    } else if (kAhead && row + step < p.rows) {
-      load_row(xn, gn, row + step);
-    }
-    T* dr = static_cast<T*>(p.dx) + row * p.ld_dx;
-    // z and g of a chunk.  They are read again after the row's sums rather than kept across them:
-    // 32 registers less per thread and half as many warps more hide the sums' latency.
-    auto values = [&](int k, float (&z)[8], float (&g)[8]) {
-      if (kUseRing) {
-        ring.get(stage, 0, k, z);
-        ring.get(stage, 1, k, g);
-      } else {
-        xc.get(kUseRing ? 0 : k, z);
-        gc.get(kUseRing ? 0 : k, g);
-      }
+  auto finish = [&](int k, int64_t i, const float (&z)[8], float (&g)[8], const float2& s, float r) {
+    const float s1 = p.layer ? s.x * p.inv_n : 0.f, s2 = s.y * p.inv_n;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = (z[j] - mu) * r;
+    for (int j = 0; j < 8; ++j) g[j] = (fmaf(g[j], w[k][j], -s1) - z[j] * s2) * r;
+    store_chunk<T, TPR, VEC>(static_cast<T*>(p.dx) + i * p.ld_dx, p.cols, t, k, g);
+  };
+  float2 stat[2], stat_next[2];            // (rstd, mean) of the rows, fetched ahead too
+  auto fetch_stats = [&](int64_t i, float2& v) {
+    if (i < p.rows) v = make_float2(p.rstd_in[i], p.layer ? p.mean_in[i] : 0.f);
+  };
+  if constexpr (kRing<T, VEC>) {
+    // Blocks of 128 and 256 threads take two rows at a time: the sums' shuffles, shared-memory
+    // reads and barrier are what their warps wait for, and one set of them serves both (8192 rows of
+    // 4096: 79 -> 73 us for both passes; a warp per row 28 -> 30, 512 threads per row 90 -> 96).  z
+    // and g are read from the ring again after the sums rather than kept across them: fewer
+    // registers, more warps.
+    constexpr int NR = TPR == 128 || TPR == 256 ? 2 : 1;
+    extern __shared__ uint4 ring_smem[];
+    using R = Ring<2, TPR, K>;
+    const R ring(ring_smem);
+    auto fetch = [&](int64_t i, int stage) {
+      if (i < p.rows) {
+        ring.copy(stage, 0, p.x, i * p.ld_x, (int)p.cols, t);
+        ring.copy(stage, 1, p.dy, i * p.ld_dy, (int)p.cols, t);
+      }
+      ring.commit();
     };
-    float s1 = 0.f, s2 = 0.f;
+    auto wrap = [](int stage) { return stage >= R::kDepth ? stage - R::kDepth : stage; };
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float z[8], g[8];
-      values(k, z, g);
+    for (int i = 0; i < R::kDepth - NR; ++i) fetch(row + i * step, i);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {   // past the row's end dy is 0: no contribution
-        aw[k][j] = fmaf(g[j], z[j], aw[k][j]);
-        ab[k][j] += g[j];
-        g[j] *= w[k][j];
-        s1 += g[j];
-        s2 = fmaf(g[j], z[j], s2);
+    for (int i = 0; i < NR; ++i) fetch_stats(row + i * step, stat_next[i]);
+    load_params<TPR, K, VEC>(p.w, p.wbf16, p.pvec, p.cols, t, 1.f, w);
+    for (int stage = 0; row < p.rows; row += NR * step, stage = wrap(stage + NR)) {
+      // the second row of the turn, if there is one (the same for the whole group)
+      const bool two = NR == 2 && row + step < p.rows;
+      const int other = wrap(stage + 1);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) stat[i] = stat_next[i];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) fetch_stats(row + (NR + i) * step, stat_next[i]);
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        fetch(row + (R::kDepth - NR + i) * step, wrap(stage + R::kDepth - NR + i));
+      ring.template wait<NR>();
+      auto values = [&](int st, const float2& rm, int k, float (&z)[8], float (&g)[8]) {
+        ring.get(st, 0, k, z);
+        ring.get(st, 1, k, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = (z[j] - rm.y) * rm.x;
+      };
+      float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float z[8], g[8];
+        values(stage, stat[0], k, z, g);
+        add(k, z, g, s0);
+        if (two) {
+          values(other, stat[1], k, z, g);
+          add(k, z, g, s1);
+        }
+      }
+      if (NR == 2) row_sum4<TPR>(s0, s1, red, turn);
+      else row_sum2<TPR>(s0.x, s0.y, red, turn);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float z[8], g[8];
+        values(stage, stat[0], k, z, g);
+        finish(k, row, z, g, s0, stat[0].x);
+        if (two) {
+          values(other, stat[1], k, z, g);
+          finish(k, row + step, z, g, s1, stat[1].x);
+        }
       }
     }
-    row_sum2<TPR>(s1, s2, red, turn);
-    s1 = p.layer ? s1 * p.inv_n : 0.f;
-    s2 *= p.inv_n;
+  } else {
+    // the next row is loaded ahead where its raw values fit in registers beside this row's
+    constexpr bool kAhead = sizeof(T) * K <= 8;
+    using Chunks = RowChunks<T, TPR, K, VEC>;
+    Chunks xc, gc, xn, gn;
+    auto load_row = [&](Chunks& x, Chunks& g, int64_t i) {
+      x.load(static_cast<const T*>(p.x) + i * p.ld_x, p.cols, t);
+      g.load(static_cast<const T*>(p.dy) + i * p.ld_dy, p.cols, t);
+    };
+    if (row < p.rows) load_row(xc, gc, row);
+    fetch_stats(row, stat_next[0]);
+    load_params<TPR, K, VEC>(p.w, p.wbf16, p.pvec, p.cols, t, 1.f, w);
+    for (; row < p.rows; row += step) {
+      stat[0] = stat_next[0];
+      fetch_stats(row + step, stat_next[0]);
+      if (kAhead && row + step < p.rows) load_row(xn, gn, row + step);
+      auto values = [&](int k, float (&z)[8], float (&g)[8]) {
+        xc.get(k, z);
+        gc.get(k, g);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float z[8], g[8];
-      values(k, z, g);
+        for (int j = 0; j < 8; ++j) z[j] = (z[j] - stat[0].y) * stat[0].x;
+      };
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = (fmaf(g[j], w[k][j], -s1) - z[j] * s2) * r;
-      store_chunk<T, TPR, VEC>(dr, p.cols, t, k, g);
-    }
-    if (kUseRing) {
-      stage = stage == R::kDepth - 1 ? 0 : stage + 1;
-    } else if (kAhead) {
-      xc = xn;
-      gc = gn;
-    } else if (row + step < p.rows) {
-      load_row(xc, gc, row + step);
+      for (int k = 0; k < K; ++k) {
+        float z[8], g[8];
+        values(k, z, g);
+        add(k, z, g, s);
+      }
+      row_sum2<TPR>(s.x, s.y, red, turn);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float z[8], g[8];
+        values(k, z, g);
+        finish(k, row, z, g, s, stat[0].x);
+      }
+      if (kAhead) {
+        xc = xn;
+        gc = gn;
+      } else if (row + step < p.rows) {
+        load_row(xc, gc, row + step);
+      }
     }
   }
   // this block's column sums, its warps added in warp order
@@ -579,7 +644,7 @@ struct FwdLaunch {
   template <typename T, int TPR, int K, bool VEC>
   cudaError_t operator()() const {
     const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
-    constexpr int smem = kRing<T, VEC> ? Ring<T, 1, TPR, K>::kBytes : 0;
+    constexpr int smem = kRing<T, VEC> ? Ring<1, TPR, K>::kBytes : 0;
     static std::atomic<int> cache[kCachedDevices];
     const int occ = resident(cache, norm_forward_kernel<T, TPR, K, VEC>, threads, smem);
     const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
@@ -597,7 +662,7 @@ struct BwdLaunch {
   template <typename T, int TPR, int K, bool VEC>
   cudaError_t operator()() const {
     const int threads = TPR == 32 ? 32 * kNormWarps : TPR;
-    constexpr int smem = kRing<T, VEC> ? Ring<T, 2, TPR, K>::kBytes : 0;
+    constexpr int smem = kRing<T, VEC> ? Ring<2, TPR, K>::kBytes : 0;
     static std::atomic<int> cache[kCachedDevices];
     const int occ = resident(cache, norm_backward_kernel<T, TPR, K, VEC>, threads, smem);
     const int64_t per = TPR == 32 ? kNormWarps : 1, need = (a.rows + per - 1) / per;
