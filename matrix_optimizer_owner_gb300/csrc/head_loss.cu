@@ -10,10 +10,11 @@
 // piece of Z from the same operands, writes that piece of G (bf16 operands: the only rounding
 // between the inputs and the gradients, within 2^-8 of an entry, the precision the product's
 // other factor has; dloss enters as its ratio to the largest |dloss|, which the gradients are
-// multiplied with in fp32 at the end, so a uniform dloss is not rounded at all), and multiplies it with W's rows for dH and with H for that piece's rows of
-// dW.  dH is summed over the pieces in fp32.  One launch multiplies a piece of G and computes
-// the next one (two pieces are kept): the many short tiles of Z fill the SMs that the few long
-// ones of dH and dW would leave idle at a launch's end.
+// multiplied with in fp32 at the end, so a uniform dloss is not rounded at all), and multiplies it
+// with W's rows for dH and with H for that piece's rows of dW.  dH is summed over the pieces in
+// fp32.  One launch multiplies a piece of G and computes the next one (two pieces are kept): the
+// many short tiles of Z fill the SMs that the few long ones of dH and dW would leave idle at a
+// launch's end.
 //
 // Tokens with the ignored label are dropped before any product: a first launch copies the live
 // rows of H together (padded to whole TMA rows), so they cost nothing, and whatever they hold
@@ -21,7 +22,18 @@
 //
 // bf16 inputs run on the CTA-pair tcgen05 kernel below (256 x 256 tiles, TMA operands,
 // accumulators in tensor memory).  fp32 inputs run on the library's fp32 GEMM (3xTF32) with a
-// piece of Z in the workspace.
+// piece of Z in the workspace.  Up to four tokens (one, with bf16 inputs that TMA can read) run
+// forward as a matrix-vector product that reads W once, without tensor cores.
+//
+// Training sizes are bound by the tensor cores: of the four products, forward's Z, its second
+// computation, dH and dW, the second costs the time that storing Z would cost in memory (8192 x
+// 50257 logits are 0.8 GB).  Measured (bf16, both passes, 1910 TFLOP/s being a large library
+// product's rate): 8192 tokens x 768 against 50257 rows in 1.5 ms, 1.69 PFLOP/s of the four
+// products; 3072 live tokens of 4096 x 4096 against 128256 rows in 7.1 to 7.5 ms, 1.7 to 1.8
+// PFLOP/s, where the power limit lowers the clock.  Forward alone runs at 1.85 and 2.0 PFLOP/s; a
+// piece of the backward pass at 768 keeps the tensor cores 79 % busy and moves 0.55 GB, the sums
+// of dH and the pieces of G, which stay in the L2 in part (71 % hits).  One token against 50257 x
+// 768 takes 15 us for W's 77 MB (5.0 TB/s; 11 us at a copy's rate).
 #include <algorithm>
 #include <atomic>
 #include <cstring>
@@ -77,7 +89,7 @@ struct HeadArgs {
   int64_t ld_dw;
   uint16_t* g;                             // G pieces, rows of `piece` entries
   int64_t piece;
-  int32_t dim, vocab;
+  int32_t dim;
   // the piece whose G is multiplied and the piece of Z that is computed (kGrads: the next one):
   // columns [v0, v0 + width) of the vocabulary, W's map row of column v0, and the first row of
   // the piece's G; width 0 where there is none
@@ -938,9 +950,10 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const __grid_constant__
 // ---------------------------------------------------------------- few tokens
 // One token (up to kFewTokens where the tensor cores would need a copy of W or run 3xTF32) is
 // bound by reading W once: a matrix product's 256-row tile would be empty but for it.  One token
-// over 128256 x 4096 took 191 us here and 218 on the tensor cores, two 267 and 216.  A warp takes kFewRows rows of W at a time (all their loads in flight
-// together), multiplies them with the tokens' hidden rows, which the block holds in shared
-// memory in fp32, and keeps each token's running (max, sum) in registers.
+// over 128256 x 4096 took 191 us here and 218 on the tensor cores, two 267 and 216.  A warp takes
+// kFewRows rows of W at a time (all their loads in flight together), multiplies them with the
+// tokens' hidden rows, which the block holds in shared memory in fp32, and keeps each token's
+// running (max, sum) in registers.
 constexpr int kFewTokens = 4;
 constexpr int kFewRows = 4;
 constexpr int kFewWarps = 8;
@@ -1083,7 +1096,7 @@ struct FinishArgs {
   const int32_t* pos;
   void* dh;
   int64_t ld_dh;
-  int32_t n, dim, pitch, rows, splits, vec;
+  int32_t dim, pitch, rows, splits, vec;
 };
 
 // A block per token, four columns per thread; the slices are added in order, eight of them in
@@ -1520,7 +1533,6 @@ struct HeadCall {
     f.pos = at<int32_t>(l.pos);
     f.dh = dh;
     f.ld_dh = ld_dh;
-    f.n = (int32_t)s.n;
     f.dim = (int32_t)s.dim;
     f.pitch = (int32_t)s.pitch;
     f.rows = (int32_t)s.rows;
@@ -1607,7 +1619,9 @@ struct HeadCall {
       ok = ok && encode_map3d(&a.g_mn, g, s.buffers * s.rows, s.piece, s.piece);
       a.g = at<uint16_t>(l.g);
       a.piece = s.piece;
-      if (dh) ok = ok && encode_map_f32(&a.acc_st, at<float>(l.acc), s.splits * s.rows, s.pitch, s.pitch, 32u);
+      if (dh)
+        ok = ok && encode_map_f32(&a.acc_st, at<float>(l.acc), s.splits * s.rows, s.pitch, s.pitch,
+                                  32u);
       a.dw_tma = dw && aligned_to(dw, 16) && ld_dw % 8 == 0;
       if (a.dw_tma) ok = ok && encode_map(&a.dw_st, dw, s.vocab, s.dim, ld_dw, 32u, 32u, false);
     }
@@ -1624,7 +1638,6 @@ struct HeadCall {
     a.dw = static_cast<uint16_t*>(dw);
     a.ld_dw = ld_dw;
     a.dim = (int32_t)s.dim;
-    a.vocab = (int32_t)s.vocab;
     a.rows = (int32_t)s.rows;
     a.splits = (int32_t)s.splits;
     a.want_dh = dh != nullptr;

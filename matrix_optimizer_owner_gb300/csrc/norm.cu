@@ -15,7 +15,7 @@
 //
 // Measured (bf16, all launches of both passes by graph replay, 6.78 TB/s being a copy's rate):
 // 16384 rows of 768 in 29 us, 3.5 TB/s of the 101 MB that have to move (15 us); 8192 rows of 4096
-// in 68 us, 3.9 TB/s of 268 MB (40 us).  What remains is latency: in the backward kernel memory is
+// in 67 us, 4.0 TB/s of 268 MB (40 us).  What remains is latency: in the backward kernel memory is
 // busy half of the time, and the warps wait on the row sums' shuffles and shared-memory reads.  A
 // group of warps per row with one chunk per thread instead, for more warps, was slower at every
 // width (768: 65 us, 4096: 145).
@@ -103,7 +103,9 @@ struct Ring {
                    : "memory");
     }
   }
-  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ void commit() const {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   // the NR oldest of kDepth groups have landed
   template <int NR>
   __device__ __forceinline__ void wait() const {
@@ -400,10 +402,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR,
   };
   if constexpr (kRing<T, VEC>) {
     // Blocks of 128 and 256 threads take two rows at a time: the sums' shuffles, shared-memory
-    // reads and barrier are what their warps wait for, and one set of them serves both (8192 rows of
-    // 4096: 79 -> 73 us for both passes; a warp per row 28 -> 30, 512 threads per row 90 -> 96).  z
-    // and g are read from the ring again after the sums rather than kept across them: fewer
-    // registers, more warps.
+    // reads and barrier are what their warps wait for, and one set of them serves both (8192 rows
+    // of 4096: 79 -> 73 us for both passes; a warp per row 28 -> 30, 512 threads per row 90 ->
+    // 96).  z and g are read from the ring again after the sums rather than kept across them:
+    // fewer registers, more warps.
     constexpr int NR = TPR == 128 || TPR == 256 ? 2 : 1;
     extern __shared__ uint4 ring_smem[];
     using R = Ring<2, TPR, K>;
