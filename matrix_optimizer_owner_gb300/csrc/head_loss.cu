@@ -22,7 +22,7 @@
 //
 // bf16 inputs run on the CTA-pair tcgen05 kernel below (256 x 256 tiles, TMA operands,
 // accumulators in tensor memory).  fp32 inputs run on the library's fp32 GEMM (3xTF32) with a
-// piece of Z in the workspace.  Up to four tokens (one, with bf16 inputs that TMA can read) run
+// piece of Z in the workspace, small ones on the CUDA cores.  Up to four tokens (one, with bf16 inputs that TMA can read) run
 // forward as a matrix-vector product that reads W once, without tensor cores.
 //
 // Training sizes are bound by the tensor cores: of the four products, forward's Z, its second
@@ -1292,6 +1292,278 @@ __global__ void head_descs_kernel(const __grid_constant__ DescArgs p) {
   for (int i = threadIdx.x; i < p.n; i += blockDim.x) p.out[i] = p.d[i];
 }
 
+// ---------------------------------------------------------------- small fp32 products
+// Up to kCoreFlops the fp32 products run on the CUDA cores, from operands as they lie (any
+// alignment, either one contiguous), so there is nothing to copy or transpose, and the epilogues
+// are fused: two launches forward and three backward, against four and nine.  Such sizes are
+// bound by latency, so tiles are small (32 x 32) and steps long (64 of the contraction): four
+// groups of two warps share a step, 4 x 4 entries per thread, and add up at the end.  A thread sums
+// its 16 of a step by themselves before it adds them.
+constexpr int kCoreTile = 32, kCoreK = 64, kCoreThreads = 256;
+constexpr int kCorePitch = kCoreTile + 4;  // the loader's banks are 4 k + row
+constexpr int kCoreGroups = 4;
+
+struct alignas(16) CoreSmem {
+  union {
+    struct {
+      float a[2][kCoreK][kCorePitch], b[2][kCoreK][kCorePitch];
+    };
+    float sum[kCoreGroups][kCoreTile][kCorePitch];
+  };
+};
+
+// Entry i of this thread in a 32 x 64 operand tile.  KMAJOR (the contraction is contiguous): 8 of k
+// by 4 rows per warp, whole sectors of memory and all banks of the transposed store.
+template <bool KMAJOR>
+__device__ __forceinline__ void core_place(int i, int& row, int& k) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  row = KMAJOR ? 4 * warp + (lane >> 3) : lane;
+  k = KMAJOR ? 8 * i + (lane & 7) : warp + 8 * i;
+}
+
+// Entries outside the matrix, or that `keep` drops, are zero whatever memory holds (indices are
+// clamped, so the loads need no branch).
+template <bool KMAJOR, typename Keep>
+__device__ __forceinline__ void core_load(const float* src, int64_t ld, int r0, int rows, int k0,
+                                          int k1, const Keep& keep, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    int row, k;
+    core_place<KMAJOR>(i, row, k);
+    const int64_t r = min(r0 + row, rows - 1), c = min(k0 + k, k1 - 1);
+    const float x = src[KMAJOR ? r * ld + c : c * ld + r];
+    v[i] = r0 + row < rows && k0 + k < k1 && keep((int)r, (int)c) ? x : 0.f;
+  }
+}
+
+template <bool KMAJOR>
+__device__ __forceinline__ void core_store(float (&tile)[kCoreK][kCorePitch], const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    int row, k;
+    core_place<KMAJOR>(i, row, k);
+    tile[k][row] = v[i];
+  }
+}
+
+// out = four columns, 4 (t % 8) on, of row t / 8 of the tile (m0, n0) of A B^T over [k0, k1), which
+// is not empty, for thread t.
+template <bool AK, bool BK, typename KeepA, typename KeepB>
+__device__ __forceinline__ void core_product(CoreSmem& sm, const float* a, int64_t lda, int m0,
+                                             int m, const KeepA& keep_a, const float* b,
+                                             int64_t ldb, int n0, int n, const KeepB& keep_b,
+                                             int k0, int k1, float (&out)[4]) {
+  constexpr int kShare = kCoreK / kCoreGroups;
+  const int grp = threadIdx.x >> 6, ty = (threadIdx.x >> 3) & 7, tx = threadIdx.x & 7;
+  float acc[4][4] = {};
+  float va[8], vb[8];
+  core_load<AK>(a, lda, m0, m, k0, k1, keep_a, va);
+  core_load<BK>(b, ldb, n0, n, k0, k1, keep_b, vb);
+  core_store<AK>(sm.a[0], va);
+  core_store<BK>(sm.b[0], vb);
+  __syncthreads();
+  for (int buf = 0; k0 < k1; k0 += kCoreK, buf ^= 1) {
+    const bool more = k0 + kCoreK < k1;
+    if (more) {
+      core_load<AK>(a, lda, m0, m, k0 + kCoreK, k1, keep_a, va);
+      core_load<BK>(b, ldb, n0, n, k0 + kCoreK, k1, keep_b, vb);
+    }
+    float sum[4][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < kShare; ++kk) {
+      const int k = grp * kShare + kk;
+      const float4 x = *reinterpret_cast<const float4*>(&sm.a[buf][k][4 * ty]);
+      const float4 y = *reinterpret_cast<const float4*>(&sm.b[buf][k][4 * tx]);
+      const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[i][j] = fmaf(xs[i], ys[j], sum[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] += sum[i][j];
+    if (more) {                            // the other buffer was last read before the barrier
+      core_store<AK>(sm.a[buf ^ 1], va);
+      core_store<BK>(sm.b[buf ^ 1], vb);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(&sm.sum[grp][4 * ty + i][4 * tx]) =
+        make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = 0.f;
+#pragma unroll
+  for (int g = 0; g < kCoreGroups; ++g) {
+    const float4 x =
+        *reinterpret_cast<const float4*>(&sm.sum[g][threadIdx.x >> 3][4 * (threadIdx.x & 7)]);
+    out[0] += x.x;
+    out[1] += x.y;
+    out[2] += x.z;
+    out[3] += x.w;
+  }
+}
+
+struct CoreArgs {
+  const float* hidden;
+  const float* weight;                     // the piece's first row
+  const void* labels;
+  int64_t ld_h, ld_w, ignore;
+  int32_t n, dim, vocab, is64;
+  int32_t v0, width;                       // the piece: vocabulary columns [v0, v0 + width)
+  float2* part;                            // forward: [n][parts] (max, sum) of a tile's row
+  float* zlab;                             // forward: [n]
+  int32_t parts;
+  float *loss, *lse;                       // forward, nullable
+  const float *lse_in, *dloss;             // backward
+  float* g;                                // backward: G of the piece, [n][piece]
+  int64_t piece;
+  int32_t* pos;                            // backward: [n] the token, -1: dropped
+  float* dw;                               // the piece's first row
+  int64_t ld_dw;
+  int32_t dw_tiles;
+  float* acc;                              // dH: [splits][rows][pitch]
+  int32_t rows, pitch, kdh, add;
+  int* status;
+};
+
+__device__ __forceinline__ int live_label(const CoreArgs& p, int t, bool& bad) {
+  const int64_t lab = load_index(p.labels, p.is64, t);
+  const bool live = lab != p.ignore && lab >= 0 && lab < p.vocab;
+  bad = !live && lab != p.ignore;
+  return live ? (int)lab : -1;
+}
+
+// A tile of Z: forward (max, sum) of its rows and the labels' logits, backward G.
+template <bool GRAD>
+__global__ void __launch_bounds__(kCoreThreads)
+    head_core_z_kernel(const __grid_constant__ CoreArgs p) {
+  __shared__ CoreSmem sm;
+  __shared__ int32_t label[kCoreTile];
+  pdl_launch();
+  pdl_wait();
+  const int ntm = (p.n + kCoreTile - 1) / kCoreTile;
+  const int tm = (int)blockIdx.x % ntm, tn = (int)blockIdx.x / ntm;
+  const int m0 = tm * kCoreTile, n0 = tn * kCoreTile;
+  if (threadIdx.x < kCoreTile) {
+    const int t = m0 + threadIdx.x;
+    bool bad = false;
+    const int lab = t < p.n ? live_label(p, t, bad) : -1;
+    label[threadIdx.x] = lab;
+    if (tn == 0 && p.v0 == 0) {
+      if (bad) atomicOr(p.status, kStatusBadIndex);
+      if (GRAD && t < p.n) p.pos[t] = lab >= 0 ? t : -1;
+    }
+  }
+  __syncthreads();
+  float z[4];
+  core_product<true, true>(
+      sm, p.hidden, p.ld_h, m0, p.n, [&](int r, int) { return label[r - m0] >= 0; }, p.weight,
+      p.ld_w, n0, p.width, [](int, int) { return true; }, 0, p.dim, z);
+  const int row = threadIdx.x >> 3, t = m0 + row, lab = label[row];
+  const int c0 = n0 + 4 * (threadIdx.x & 7);
+  if (GRAD) {
+    if (t >= p.n) return;
+    const float lse2 = lab >= 0 ? p.lse_in[t] * kLog2e : 0.f, dl = lab >= 0 ? p.dloss[t] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float g = 0.f;
+      if (lab >= 0) {
+        g = exp2f(fmaf(z[j], kLog2e, -lse2));
+        if (p.v0 + c0 + j == lab) g -= 1.f;
+        g *= dl;
+      }
+      if (c0 + j < p.width) p.g[(int64_t)t * p.piece + c0 + j] = g;
+    }
+  } else {
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c0 + j >= p.width) continue;
+      m = fmaxf(m, z[j]);
+      if (c0 + j == lab) p.zlab[t] = z[j];
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c0 + j < p.width) s += exp2f((z[j] - ref) * kLog2e);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)        // the eight threads of the row
+      merge_stats(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+    if ((threadIdx.x & 7) == 0 && lab >= 0) p.part[(int64_t)t * p.parts + tn] = make_float2(m, s);
+  }
+}
+
+// A warp per token: the tiles' pairs to loss and lse.
+__global__ void __launch_bounds__(kCoreThreads)
+    head_core_join_kernel(const __grid_constant__ CoreArgs p) {
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, t = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= p.n) return;
+  bool bad;
+  const bool live = live_label(p, t, bad) >= 0;
+  float m = -INFINITY, s = 0.f;
+  if (live) {
+#pragma unroll 4
+    for (int i = lane; i < p.parts; i += 32) {
+      const float2 v = p.part[(int64_t)t * p.parts + i];
+      merge_stats(m, s, v.x, v.y);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      merge_stats(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+  }
+  if (lane != 0) return;
+  const float l = live ? m + logf(s) : 0.f;
+  if (p.lse) p.lse[t] = l;
+  if (p.loss) p.loss[t] = live ? l - p.zlab[t] : 0.f;
+}
+
+// Both products of a piece's G: the tiles of dW, then those of dH's slices.
+__global__ void __launch_bounds__(kCoreThreads)
+    head_core_grad_kernel(const __grid_constant__ CoreArgs p) {
+  __shared__ CoreSmem sm;
+  pdl_launch();
+  pdl_wait();
+  const int ntd = (p.dim + kCoreTile - 1) / kCoreTile, ntm = (p.n + kCoreTile - 1) / kCoreTile;
+  const auto all = [](int, int) { return true; };
+  const bool of_w = (int)blockIdx.x < p.dw_tiles;
+  const int b = of_w ? (int)blockIdx.x : (int)blockIdx.x - p.dw_tiles;
+  const int n0 = b % ntd * kCoreTile, m0 = (of_w ? b / ntd : b / ntd % ntm) * kCoreTile;
+  float v[4];
+  float* out;
+  int64_t ld;
+  int rows;
+  if (of_w) {
+    core_product<false, false>(sm, p.g, p.piece, m0, p.width, all, p.hidden, p.ld_h, n0, p.dim,
+                               [&](int, int k) { return p.pos[k] >= 0; }, 0, p.n, v);
+    out = p.dw;
+    ld = p.ld_dw;
+    rows = p.width;
+  } else {
+    const int split = b / (ntd * ntm), k0 = split * p.kdh;
+    core_product<true, false>(sm, p.g, p.piece, m0, p.n, all, p.weight, p.ld_w, n0, p.dim, all, k0,
+                              min(p.width, k0 + p.kdh), v);
+    out = p.acc + (int64_t)split * p.rows * p.pitch;
+    ld = p.pitch;
+    rows = p.n;
+  }
+  const bool add = !of_w && p.add;
+  const int r = m0 + (threadIdx.x >> 3), c0 = n0 + 4 * (threadIdx.x & 7);
+  if (r >= rows) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (c0 + j >= p.dim) continue;
+    float* o = out + r * ld + c0 + j;
+    *o = add ? *o + v[j] : v[j];
+  }
+}
+
 // ---------------------------------------------------------------- host
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
@@ -1301,6 +1573,7 @@ struct HeadShape {
   int32_t dtype;
   bool backward, copy_w;
   bool few;                                // forward of few tokens: head_few_kernel
+  bool core;                               // fp32 on the CUDA cores
   int64_t rows, pitch;                     // compacted H (and dH slices)
   int64_t piece, pieces;                   // columns per piece
   int64_t splits;                          // dH slices
@@ -1318,6 +1591,11 @@ constexpr int64_t kMinElems = 32ll << 20;  // least entries of G per piece
 constexpr int64_t kZElems = 32ll << 20;    // entries of Z (fp32), or of a copied W, per piece
 constexpr int64_t kPartBytes = 64ll << 20; // bytes of the forward partials per piece
 constexpr int kMaxSplits = 64;
+// Largest fp32 product that runs on the CUDA cores, in operations of whole tiles.  Both passes
+// there and through the 3xTF32 GEMM: 333 tokens x 100 against 1031 rows (0.1 G) 44 and 102 us, 16 x
+// 256 against 20000 (0.3 G) 108 and 126, 128 x 512 against 4000 (0.5 G) 136 and 130, 4096 x 64
+// against 1000 (0.5 G) 189 and 292, 256 x 256 against 8000 (1.1 G) 216 and 124.
+constexpr int64_t kCoreFlops = 1ll << 29;
 constexpr int kGatherBlocks = 608;         // blocks of the gather launch, at most
 constexpr int kFewBlocks = 1024;           // blocks of the few-token kernel (bounds its workspace)
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
@@ -1358,7 +1636,11 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   // the tokens' hidden rows have to fit in shared memory
   s.few = !backward && n <= (bf && !s.copy_w ? 1 : kFewTokens) &&
           up(dim, 8) * 4 * kFewTokens <= (200 << 10);
-  if (s.few) s.copy_w = false;
+  // (counted as the tiles are; the product of the three would pass 64 bits)
+  s.core = !bf && !s.few &&
+           2 * up(std::max<int64_t>(n, 1), kCoreTile) * up(dim, kCoreK) <=
+               kCoreFlops / up(vocab, kCoreTile);
+  if (s.few || s.core) s.copy_w = false;
   s.rows = up(std::max<int64_t>(n, 1), kTile);
   s.pitch = up(dim, 64);
   s.piece = piece_columns(s, piece);
@@ -1376,6 +1658,14 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
                                               s.piece / (bf ? 1024 : 128), (int64_t)kMaxSplits}));
     s.kdh = up(cdiv(std::min(s.piece, vocab), s.splits), kBK);  // no slice of a whole piece is empty
     s.splits = cdiv(std::min(s.piece, vocab), s.kdh);
+    if (s.core) {                          // two blocks per SM, slices of at least 128 columns
+      const int64_t few_tiles = cdiv(std::max<int64_t>(n, 1), kCoreTile) * cdiv(dim, kCoreTile);
+      const int64_t cols = std::min(s.piece, vocab);
+      s.splits = std::max<int64_t>(1, std::min({2 * sms / few_tiles, cols / 128,
+                                                (int64_t)kMaxSplits}));
+      s.kdh = up(cdiv(cols, s.splits), kCoreK);
+      s.splits = cdiv(cols, s.kdh);
+    }
     s.buffers = bf && s.pieces > 1 ? 2 : 1;
   }
   return s;
@@ -1395,6 +1685,15 @@ HeadLayout head_layout(const HeadShape& s) {
   if (s.few) {
     l.zlab = take(kFewTokens * 4);
     l.part = take(kFewBlocks * kFewTokens * 8);
+    l.total = off;
+    return l;
+  }
+  if (s.core) {
+    l.pos = take(s.backward ? s.rows * 4 : 0);
+    l.zlab = take(s.rows * 4);
+    l.part = take(s.backward ? 0 : s.n * cdiv(s.vocab, kCoreTile) * 8);
+    l.g = take(s.backward ? s.n * s.piece * 4 : 0);
+    l.acc = take(s.backward ? s.splits * s.rows * s.pitch * 4 : 0);
     l.total = off;
     return l;
   }
@@ -1697,12 +1996,71 @@ struct HeadCall {
 
   int run() const {
     if (s.few) return run_few();
+    if (s.core) return run_core();
     if (s.dtype == MFSDP_DTYPE_BF16) return run_bf16();
     try {
       return run_f32();
     } catch (const std::bad_alloc&) {  // the problem table of very many pieces
       return MFSDP_ESHAPE;
     }
+  }
+
+  int run_core() const {
+    CoreArgs a{};
+    a.hidden = static_cast<const float*>(hidden);
+    a.weight = static_cast<const float*>(weight);
+    a.labels = labels;
+    a.ld_h = ld_h;
+    a.ld_w = ld_w;
+    a.ignore = ignore;
+    a.n = (int32_t)s.n;
+    a.dim = (int32_t)s.dim;
+    a.vocab = (int32_t)s.vocab;
+    a.is64 = index_dtype == MFSDP_INDEX_I64;
+    a.zlab = at<float>(l.zlab);
+    a.status = status;
+    const int64_t ntm = cdiv(s.n, kCoreTile), ntd = cdiv(s.dim, kCoreTile);
+    const dim3 threads(kCoreThreads);
+    cudaError_t e = cudaSuccess;
+    if (!s.backward) {
+      a.width = a.vocab;
+      a.part = at<float2>(l.part);
+      a.parts = (int32_t)cdiv(s.vocab, kCoreTile);
+      a.loss = loss;
+      a.lse = lse;
+      e = launch_pdl(head_core_z_kernel<false>, dim3((unsigned)(ntm * a.parts)), threads, 0, st, a);
+      if (e == cudaSuccess)
+        e = launch_pdl(head_core_join_kernel, dim3((unsigned)cdiv(s.n, 8)), threads, 0, st, a);
+      return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
+    }
+    a.lse_in = lse_in;
+    a.dloss = dloss;
+    a.g = at<float>(l.g);
+    a.piece = s.piece;
+    a.pos = at<int32_t>(l.pos);
+    a.ld_dw = ld_dw;
+    a.acc = at<float>(l.acc);
+    a.rows = (int32_t)s.rows;
+    a.pitch = (int32_t)s.pitch;
+    a.kdh = (int32_t)s.kdh;
+    for (int64_t i = 0; i < s.pieces && e == cudaSuccess; ++i) {
+      const int64_t v0 = i * s.piece, width = std::min(s.piece, s.vocab - v0);
+      a.weight = static_cast<const float*>(weight) + v0 * ld_w;
+      a.v0 = (int32_t)v0;
+      a.width = (int32_t)width;
+      a.dw = dw ? static_cast<float*>(dw) + v0 * ld_dw : nullptr;
+      a.dw_tiles = dw ? (int32_t)(cdiv(width, kCoreTile) * ntd) : 0;
+      a.add = i > 0;
+      // (a narrower last piece may leave slices without columns: nothing to add there)
+      const int64_t dh_tiles = dh ? ntm * ntd * cdiv(width, s.kdh) : 0;
+      e = launch_pdl(head_core_z_kernel<true>, dim3((unsigned)(ntm * cdiv(width, kCoreTile))),
+                     threads, 0, st, a);
+      if (e == cudaSuccess)
+        e = launch_pdl(head_core_grad_kernel, dim3((unsigned)(a.dw_tiles + dh_tiles)), threads, 0,
+                       st, a);
+    }
+    if (e == cudaSuccess && dh) e = finish();
+    return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
   }
 
   int run_f32() const {

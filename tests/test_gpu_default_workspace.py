@@ -23,6 +23,7 @@ def _grad(ids, dy, out):
 
 def test_kept_per_stream_and_grown():
     from matrix_optimizer_owner_gb300 import mfsdp
+    mfsdp._scratch.buffers.clear()                   # what earlier tests left
     out = torch.empty(700, 128, device="cuda")
     _grad(*_case(10, 0), out)
     raw = torch.cuda.current_stream().cuda_stream

@@ -161,6 +161,44 @@ def test_dropped_rows_may_hold_anything(dtype):
     assert not out[0][:3].any() and out[0][3] != 0
 
 
+# fp32 products on either side of what the CUDA cores take (2^29 operations): tiles of 32 and steps
+# of 64 that end inside, one token, many tokens, slices of dH, and the same beyond, on 3xTF32
+@pytest.mark.parametrize("n,dim,vocab", [
+    (5, 65, 33), (31, 64, 32), (33, 63, 65), (1, 300, 5000), (129, 1, 129), (2000, 33, 700),
+    (60, 1000, 2050), (520, 520, 1100), (40, 1400, 5000), (2100, 130, 1300)])
+@pytest.mark.parametrize("piece", [0, 300])
+def test_f32_small_and_large(n, dim, vocab, piece):
+    h, w, lab, dl = _case(n, dim, vocab, "f32", 0.2 if n > 1 else 0.0, seed=n + dim)
+    _verify(h, w, lab, dl, _run(h, w, lab, dl, piece=piece))
+
+
+@pytest.mark.parametrize("n,dim,vocab", [(100, 72, 500), (540, 520, 1000)])
+@pytest.mark.parametrize("pitch,offset", [(8, 8), (3, 0), (0, 1)])
+def test_f32_strides_small_and_large(n, dim, vocab, pitch, offset):
+    h, w, lab, dl = _case(n, dim, vocab, "f32", seed=pitch + offset, pitch=pitch, offset=offset)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dh = _mat(n, dim, "f32", gen, 1.0, pitch, offset)
+    dw = _mat(vocab, dim, "f32", gen, 1.0, pitch, offset)
+    _verify(h, w, lab, dl, _run(h, w, lab, dl, piece=512, dh=dh, dw=dw))
+
+
+@pytest.mark.parametrize("n,dim,vocab", [(100, 72, 500), (540, 520, 1000)])
+def test_f32_dropped_small_and_large(n, dim, vocab):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    h, w, lab, dl = _case(n, dim, vocab, "f32", 0.4, torch.int32, seed=12)
+    drop = lab == -100
+    h[drop] = float("nan")
+    dl[drop] = float("nan")
+    out = _run(h, w, lab, dl, piece=256)
+    dl[drop] = 0.0
+    _verify(h, w, lab, dl, out)
+    again = _run(h, w, lab, dl, piece=256)
+    assert all(torch.equal(a, b) for a, b in zip(again, out))
+    lab[:] = -100
+    assert not any(t.any().item() for t in _run(h, w, lab, dl, piece=256))
+    assert mfsdp.mfsdp_query_status() == 0
+
+
 def test_nan_stays_in_its_token():
     h, w, lab, dl = _case(300, 64, 500, "bf16", 0.0, seed=6)
     clean = _run(h, w, lab, dl)
