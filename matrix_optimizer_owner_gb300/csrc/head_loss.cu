@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         const int lab = live ? P.label[r] - P.z_v0 : -1;
         // a row that holds no token: exp2(z - inf) = 0
         const float lse2 = live ? P.lse2[r] : INFINITY;
-        const float dl = live && scale > 0.f ? P.dl[r] / scale : 0.f;
+        // (no finite dloss but zeros: an infinite or NaN one still reaches the gradients)
+        const float dl = live ? P.dl[r] / (scale > 0.f ? scale : 1.f) : 0.f;
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
         // whole k-blocks of G are written, in both directions: the columns past the end and the

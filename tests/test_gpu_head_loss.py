@@ -210,6 +210,28 @@ def test_nan_stays_in_its_token():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 300])
+def test_dloss_of_zeros_and_of_nan(dtype, n):
+    h, w, lab, dl = _case(n, 64, 500, dtype, 0.0, seed=13)
+    _, _, dh, dw = _run(h, w, lab, torch.zeros_like(dl))
+    assert not dh.any() and not dw.any()
+    # a loss that overflowed upstream: no gradient may look like a valid one
+    _, _, dh, dw = _run(h, w, lab, torch.full_like(dl, float("nan")))
+    assert dh.isnan().all() and dw.isnan().all()
+    _, _, dh, dw = _run(h, w, lab, torch.full_like(dl, float("inf")))
+    assert not torch.isfinite(dh).any() and not torch.isfinite(dw).any()
+    # one of them: its own row of dH, and dW
+    if n > 1:
+        clean = _run(h, w, lab, dl)[2]
+        dl[17] = float("nan")
+        _, _, dh, dw = _run(h, w, lab, dl)
+        keep = torch.arange(n, device="cuda") != 17
+        assert dh[17].isnan().all() and dw.isnan().all() and torch.isfinite(dh[keep]).all()
+        assert ((dh[keep].float() - clean[keep].float()).abs()
+                <= 2.0 ** -5 * clean[keep].float().abs().max()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_logits(dtype):
     # exp of the raw logits overflows and underflows: thousands on either side
     h, w, lab, dl = _case(260, 64, 800, dtype, 0.0, seed=7, std=60.0)
