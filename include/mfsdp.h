@@ -651,8 +651,8 @@ int mfsdp_head_loss_workspace_bytes(int64_t n_tokens, int64_t dim, int64_t vocab
  *                ignore_index is dropped too and sets MFSDP_EINDEX in the device status word.
  *   loss, lse    fp32 [n_tokens], nullable outputs; the backward pass takes lse.
  * bf16 products run on the tensor cores with fp32 accumulation; fp32 ones as 3xTF32
- * (mfsdp_gemm_f32_batched's accuracy), small ones in fp32 on the CUDA cores.  The vocabulary is
- * walked in tiles and never stored beyond one piece.  n_tokens == 0 is no work.
+ * (mfsdp_gemm_f32_batched's accuracy); small ones of both in fp32 on the CUDA cores.  The
+ * vocabulary is walked in tiles and never stored beyond one piece.  n_tokens == 0 is no work.
  */
 int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,
                             const void* hidden, int64_t ld_hidden, const void* weight,
@@ -667,7 +667,7 @@ int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_
  *     dhidden = g weight,   dweight = g^T hidden
  *   lse          as written by the forward pass;  dloss  fp32 [n_tokens].
  *   dhidden, dweight   of `dtype`, nullable, overwritten (rows of dropped tokens are zero).
- * With bf16 inputs g is rounded to bf16 between its two products (relative 2^-8 an entry); sums
+ * With bf16 inputs g may be rounded to bf16 between its two products (relative 2^-8 an entry); sums
  * are fp32 and each gradient is rounded once.  dhidden may be hidden's buffer (same pitch).
  */
 int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,

@@ -22,8 +22,9 @@
 //
 // bf16 inputs run on the CTA-pair tcgen05 kernel below (256 x 256 tiles, TMA operands,
 // accumulators in tensor memory).  fp32 inputs run on the library's fp32 GEMM (3xTF32) with a
-// piece of Z in the workspace, small ones on the CUDA cores.  Up to four tokens (one, with bf16 inputs that TMA can read) run
-// forward as a matrix-vector product that reads W once, without tensor cores.
+// piece of Z in the workspace.  Small products of both run on the CUDA cores.  Up to four tokens
+// (one, with bf16 inputs that TMA can read) run forward as a matrix-vector product that reads W
+// once, without tensor cores.
 //
 // Training sizes are bound by the tensor cores: of the four products, forward's Z, its second
 // computation, dH and dW, the second costs the time that storing Z would cost in memory (8192 x
@@ -1308,13 +1309,14 @@ __global__ void head_descs_kernel(const __grid_constant__ DescArgs p) {
   for (int i = threadIdx.x; i < p.n; i += blockDim.x) p.out[i] = p.d[i];
 }
 
-// ---------------------------------------------------------------- small fp32 products
-// Up to kCoreFlops the fp32 products run on the CUDA cores, from operands as they lie (any
-// alignment, either one contiguous), so there is nothing to copy or transpose, and the epilogues
-// are fused: two launches forward and three backward, against four and nine.  Such sizes are
-// bound by latency, so tiles are small (32 x 32) and steps long (64 of the contraction): four
-// groups of two warps share a step, 4 x 4 entries per thread, and add up at the end.  A thread sums
-// its 16 of a step by themselves before it adds them.
+// ---------------------------------------------------------------- small products
+// Up to kCoreFlops (bf16: kCoreFlopsBf16) the products run on the CUDA cores, from operands as
+// they lie (any alignment, either one contiguous), so there is nothing to copy or transpose, and
+// the epilogues are fused: two launches forward and three backward, against four and nine (bf16:
+// three and five or more).  G stays in fp32.  Such sizes are bound by latency, so tiles are small
+// (32 x 32) and steps long (64 of the contraction): four groups of two warps share a step, 4 x 4
+// entries per thread, and add up at the end.  A thread sums its 16 of a step by themselves before
+// it adds them.
 constexpr int kCoreTile = 32, kCoreK = 64, kCoreThreads = 256;
 constexpr int kCorePitch = kCoreTile + 4;  // the loader's banks are 4 k + row
 constexpr int kCoreGroups = 4;
@@ -1339,15 +1341,15 @@ __device__ __forceinline__ void core_place(int i, int& row, int& k) {
 
 // Entries outside the matrix, or that `keep` drops, are zero whatever memory holds (indices are
 // clamped, so the loads need no branch).
-template <bool KMAJOR, typename Keep>
-__device__ __forceinline__ void core_load(const float* src, int64_t ld, int r0, int rows, int k0,
+template <bool KMAJOR, typename T, typename Keep>
+__device__ __forceinline__ void core_load(const T* src, int64_t ld, int r0, int rows, int k0,
                                           int k1, const Keep& keep, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     int row, k;
     core_place<KMAJOR>(i, row, k);
     const int64_t r = min(r0 + row, rows - 1), c = min(k0 + k, k1 - 1);
-    const float x = src[KMAJOR ? r * ld + c : c * ld + r];
+    const float x = to_f32(src[KMAJOR ? r * ld + c : c * ld + r]);
     v[i] = r0 + row < rows && k0 + k < k1 && keep((int)r, (int)c) ? x : 0.f;
   }
 }
@@ -1364,11 +1366,11 @@ __device__ __forceinline__ void core_store(float (&tile)[kCoreK][kCorePitch], co
 
 // out = four columns, 4 (t % 8) on, of row t / 8 of the tile (m0, n0) of A B^T over [k0, k1), which
 // is not empty, for thread t.
-template <bool AK, bool BK, typename KeepA, typename KeepB>
-__device__ __forceinline__ void core_product(CoreSmem& sm, const float* a, int64_t lda, int m0,
-                                             int m, const KeepA& keep_a, const float* b,
-                                             int64_t ldb, int n0, int n, const KeepB& keep_b,
-                                             int k0, int k1, float (&out)[4]) {
+template <bool AK, bool BK, typename TA, typename TB, typename KeepA, typename KeepB>
+__device__ __forceinline__ void core_product(CoreSmem& sm, const TA* a, int64_t lda, int m0,
+                                             int m, const KeepA& keep_a, const TB* b, int64_t ldb,
+                                             int n0, int n, const KeepB& keep_b, int k0, int k1,
+                                             float (&out)[4]) {
   constexpr int kShare = kCoreK / kCoreGroups;
   const int grp = threadIdx.x >> 6, ty = (threadIdx.x >> 3) & 7, tx = threadIdx.x & 7;
   float acc[4][4] = {};
@@ -1425,8 +1427,8 @@ __device__ __forceinline__ void core_product(CoreSmem& sm, const float* a, int64
 }
 
 struct CoreArgs {
-  const float* hidden;
-  const float* weight;                     // the piece's first row
+  const void* hidden;
+  const void* weight;                      // the piece's first row
   const void* labels;
   int64_t ld_h, ld_w, ignore;
   int32_t n, dim, vocab, is64;
@@ -1439,7 +1441,7 @@ struct CoreArgs {
   float* g;                                // backward: G of the piece, [n][piece]
   int64_t piece;
   int32_t* pos;                            // backward: [n] the token, -1: dropped
-  float* dw;                               // the piece's first row
+  void* dw;                                // the piece's first row
   int64_t ld_dw;
   int32_t dw_tiles;
   float* acc;                              // dH: [splits][rows][pitch]
@@ -1455,7 +1457,7 @@ __device__ __forceinline__ int live_label(const CoreArgs& p, int t, bool& bad) {
 }
 
 // A tile of Z: forward (max, sum) of its rows and the labels' logits, backward G.
-template <bool GRAD>
+template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kCoreThreads)
     head_core_z_kernel(const __grid_constant__ CoreArgs p) {
   __shared__ CoreSmem sm;
@@ -1478,8 +1480,9 @@ __global__ void __launch_bounds__(kCoreThreads)
   __syncthreads();
   float z[4];
   core_product<true, true>(
-      sm, p.hidden, p.ld_h, m0, p.n, [&](int r, int) { return label[r - m0] >= 0; }, p.weight,
-      p.ld_w, n0, p.width, [](int, int) { return true; }, 0, p.dim, z);
+      sm, static_cast<const T*>(p.hidden), p.ld_h, m0, p.n,
+      [&](int r, int) { return label[r - m0] >= 0; }, static_cast<const T*>(p.weight), p.ld_w, n0,
+      p.width, [](int, int) { return true; }, 0, p.dim, z);
   const int row = threadIdx.x >> 3, t = m0 + row, lab = label[row];
   const int c0 = n0 + 4 * (threadIdx.x & 7);
   if (GRAD) {
@@ -1541,6 +1544,7 @@ __global__ void __launch_bounds__(kCoreThreads)
 }
 
 // Both products of a piece's G: the tiles of dW, then those of dH's slices.
+template <typename T>
 __global__ void __launch_bounds__(kCoreThreads)
     head_core_grad_kernel(const __grid_constant__ CoreArgs p) {
   __shared__ CoreSmem sm;
@@ -1551,33 +1555,27 @@ __global__ void __launch_bounds__(kCoreThreads)
   const bool of_w = (int)blockIdx.x < p.dw_tiles;
   const int b = of_w ? (int)blockIdx.x : (int)blockIdx.x - p.dw_tiles;
   const int n0 = b % ntd * kCoreTile, m0 = (of_w ? b / ntd : b / ntd % ntm) * kCoreTile;
-  float v[4];
-  float* out;
-  int64_t ld;
-  int rows;
-  if (of_w) {
-    core_product<false, false>(sm, p.g, p.piece, m0, p.width, all, p.hidden, p.ld_h, n0, p.dim,
-                               [&](int, int k) { return p.pos[k] >= 0; }, 0, p.n, v);
-    out = p.dw;
-    ld = p.ld_dw;
-    rows = p.width;
-  } else {
-    const int split = b / (ntd * ntm), k0 = split * p.kdh;
-    core_product<true, false>(sm, p.g, p.piece, m0, p.n, all, p.weight, p.ld_w, n0, p.dim, all, k0,
-                              min(p.width, k0 + p.kdh), v);
-    out = p.acc + (int64_t)split * p.rows * p.pitch;
-    ld = p.pitch;
-    rows = p.n;
-  }
-  const bool add = !of_w && p.add;
   const int r = m0 + (threadIdx.x >> 3), c0 = n0 + 4 * (threadIdx.x & 7);
-  if (r >= rows) return;
+  float v[4];
+  if (of_w) {
+    core_product<false, false>(sm, p.g, p.piece, m0, p.width, all, static_cast<const T*>(p.hidden),
+                               p.ld_h, n0, p.dim, [&](int, int k) { return p.pos[k] >= 0; }, 0,
+                               p.n, v);
+    if (r >= p.width) return;
+    T* out = static_cast<T*>(p.dw) + r * p.ld_dw + c0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (c0 + j >= p.dim) continue;
-    float* o = out + r * ld + c0 + j;
-    *o = add ? *o + v[j] : v[j];
+    for (int j = 0; j < 4; ++j)
+      if (c0 + j < p.dim) out[j] = from_f32<T>(v[j]);
+    return;
   }
+  const int split = b / (ntd * ntm), k0 = split * p.kdh;
+  core_product<true, false>(sm, p.g, p.piece, m0, p.n, all, static_cast<const T*>(p.weight), p.ld_w,
+                            n0, p.dim, all, k0, min(p.width, k0 + p.kdh), v);
+  if (r >= p.n) return;
+  float* out = p.acc + ((int64_t)split * p.rows + r) * p.pitch + c0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (c0 + j < p.dim) out[j] = p.add ? out[j] + v[j] : v[j];
 }
 
 // ---------------------------------------------------------------- host
@@ -1589,7 +1587,7 @@ struct HeadShape {
   int32_t dtype;
   bool backward, copy_w;
   bool few;                                // forward of few tokens: head_few_kernel
-  bool core;                               // fp32 on the CUDA cores
+  bool core;                               // small: on the CUDA cores
   int64_t rows, pitch;                     // compacted H (and dH slices)
   int64_t piece, pieces;                   // columns per piece
   int64_t splits;                          // dH slices
@@ -1612,6 +1610,10 @@ constexpr int kMaxSplits = 64;
 // 256 against 20000 (0.3 G) 108 and 126, 128 x 512 against 4000 (0.5 G) 136 and 130, 4096 x 64
 // against 1000 (0.5 G) 189 and 292, 256 x 256 against 8000 (1.1 G) 216 and 124.
 constexpr int64_t kCoreFlops = 1ll << 29;
+// The same for bf16, against the tensor cores: 100 x 100 against 1000 (0.03 G) 30 and 56 us, 4 x
+// 70 against 7784 (0.06 G) 43 and 55, 1024 x 64 against 1000 (0.13 G) 65 and 50, 16 x 256 against
+// 10000 (0.16 G) 65 and 52.
+constexpr int64_t kCoreFlopsBf16 = 64ll << 20;
 constexpr int kGatherBlocks = 608;         // blocks of the gather launch, at most
 constexpr int kFewBlocks = 1024;           // blocks of the few-token kernel (bounds its workspace)
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
@@ -1653,9 +1655,8 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   s.few = !backward && n <= (bf && !s.copy_w ? 1 : kFewTokens) &&
           up(dim, 8) * 4 * kFewTokens <= (200 << 10);
   // (counted as the tiles are; the product of the three would pass 64 bits)
-  s.core = !bf && !s.few &&
-           2 * up(std::max<int64_t>(n, 1), kCoreTile) * up(dim, kCoreK) <=
-               kCoreFlops / up(vocab, kCoreTile);
+  s.core = !s.few && 2 * up(std::max<int64_t>(n, 1), kCoreTile) * up(dim, kCoreK) <=
+                         (bf ? kCoreFlopsBf16 : kCoreFlops) / up(vocab, kCoreTile);
   if (s.few || s.core) s.copy_w = false;
   s.rows = up(std::max<int64_t>(n, 1), kTile);
   s.pitch = up(dim, 64);
@@ -1844,7 +1845,7 @@ struct HeadCall {
   cudaError_t finish() const {
     FinishArgs f{};
     f.acc = at<float>(l.acc);
-    f.scale = s.dtype == MFSDP_DTYPE_BF16 ? at<float>(l.scale) : nullptr;
+    f.scale = s.dtype == MFSDP_DTYPE_BF16 && !s.core ? at<float>(l.scale) : nullptr;
     f.pos = at<int32_t>(l.pos);
     f.dh = dh;
     f.ld_dh = ld_dh;
@@ -2012,7 +2013,8 @@ struct HeadCall {
 
   int run() const {
     if (s.few) return run_few();
-    if (s.core) return run_core();
+    if (s.core)
+      return s.dtype == MFSDP_DTYPE_BF16 ? run_core<bf16_t>() : run_core<float>();
     if (s.dtype == MFSDP_DTYPE_BF16) return run_bf16();
     try {
       return run_f32();
@@ -2021,10 +2023,11 @@ struct HeadCall {
     }
   }
 
+  template <typename T>
   int run_core() const {
     CoreArgs a{};
-    a.hidden = static_cast<const float*>(hidden);
-    a.weight = static_cast<const float*>(weight);
+    a.hidden = hidden;
+    a.weight = weight;
     a.labels = labels;
     a.ld_h = ld_h;
     a.ld_w = ld_w;
@@ -2044,7 +2047,8 @@ struct HeadCall {
       a.parts = (int32_t)cdiv(s.vocab, kCoreTile);
       a.loss = loss;
       a.lse = lse;
-      e = launch_pdl(head_core_z_kernel<false>, dim3((unsigned)(ntm * a.parts)), threads, 0, st, a);
+      e = launch_pdl(head_core_z_kernel<T, false>, dim3((unsigned)(ntm * a.parts)), threads, 0, st,
+                     a);
       if (e == cudaSuccess)
         e = launch_pdl(head_core_join_kernel, dim3((unsigned)cdiv(s.n, 8)), threads, 0, st, a);
       return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
@@ -2061,18 +2065,18 @@ struct HeadCall {
     a.kdh = (int32_t)s.kdh;
     for (int64_t i = 0; i < s.pieces && e == cudaSuccess; ++i) {
       const int64_t v0 = i * s.piece, width = std::min(s.piece, s.vocab - v0);
-      a.weight = static_cast<const float*>(weight) + v0 * ld_w;
+      a.weight = static_cast<const T*>(weight) + v0 * ld_w;
       a.v0 = (int32_t)v0;
       a.width = (int32_t)width;
-      a.dw = dw ? static_cast<float*>(dw) + v0 * ld_dw : nullptr;
+      a.dw = dw ? static_cast<T*>(dw) + v0 * ld_dw : nullptr;
       a.dw_tiles = dw ? (int32_t)(cdiv(width, kCoreTile) * ntd) : 0;
       a.add = i > 0;
       // (a narrower last piece may leave slices without columns: nothing to add there)
       const int64_t dh_tiles = dh ? ntm * ntd * cdiv(width, s.kdh) : 0;
-      e = launch_pdl(head_core_z_kernel<true>, dim3((unsigned)(ntm * cdiv(width, kCoreTile))),
+      e = launch_pdl(head_core_z_kernel<T, true>, dim3((unsigned)(ntm * cdiv(width, kCoreTile))),
                      threads, 0, st, a);
       if (e == cudaSuccess)
-        e = launch_pdl(head_core_grad_kernel, dim3((unsigned)(a.dw_tiles + dh_tiles)), threads, 0,
+        e = launch_pdl(head_core_grad_kernel<T>, dim3((unsigned)(a.dw_tiles + dh_tiles)), threads, 0,
                        st, a);
     }
     if (e == cudaSuccess && dh) e = finish();

@@ -199,6 +199,57 @@ def test_f32_dropped_small_and_large(n, dim, vocab):
     assert mfsdp.mfsdp_query_status() == 0
 
 
+# bf16 products that the tensor cores take (above 64 Mi operations): tiles, k-blocks and pieces
+# that end inside, few tokens, rows that TMA cannot read
+@pytest.mark.parametrize("n,dim,vocab", [
+    (255, 520, 515), (256, 512, 512), (257, 584, 513), (513, 72, 2049), (5, 1030, 2000),
+    (64, 64, 13000), (33, 1100, 1025), (1025, 320, 255), (2, 2049, 2000), (1, 3300, 1000)])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_bf16_tensor_core_sizes(n, dim, vocab, piece):
+    h, w, lab, dl = _case(n, dim, vocab, "bf16", 0.2 if n > 2 else 0.0, seed=n + dim)
+    _verify(h, w, lab, dl, _run(h, w, lab, dl, piece=piece))
+
+
+@pytest.mark.parametrize("pitch,offset", [(8, 0), (8, 8), (3, 0), (0, 1), (5, 3)])
+def test_bf16_tensor_core_strides(pitch, offset):
+    h, w, lab, dl = _case(270, 328, 900, "bf16", seed=pitch + offset, pitch=pitch, offset=offset)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dh = _mat(270, 328, "bf16", gen, 1.0, pitch, offset)
+    dw = _mat(900, 328, "bf16", gen, 1.0, pitch, offset)
+    for piece in (0, 256):
+        _verify(h, w, lab, dl, _run(h, w, lab, dl, piece=piece, dh=dh, dw=dw))
+
+
+def test_bf16_tensor_core_dropped_rows():
+    from matrix_optimizer_owner_gb300 import mfsdp
+    for ignored in (0.3, 0.97, 1.0):
+        h, w, lab, dl = _case(400, 264, 1100, "bf16", ignored, torch.int32, seed=14)
+        drop = lab == -100
+        h[drop] = float("nan")
+        dl[drop] = float("inf")
+        out = _run(h, w, lab, dl, piece=512)
+        dl[drop] = 0.0
+        _verify(h, w, lab, dl, out)
+        assert all(torch.equal(a, b) for a, b in zip(_run(h, w, lab, dl, piece=512), out))
+    assert mfsdp.mfsdp_query_status() == 0
+
+
+def test_bf16_tensor_core_large_logits_nan_and_dloss():
+    h, w, lab, dl = _case(260, 264, 1100, "bf16", 0.0, seed=15, std=30.0)
+    clean = _run(h, w, lab, dl)
+    assert all(torch.isfinite(t).all() for t in clean)
+    _verify(h, w, lab, dl, clean)
+    _, _, dh, dw = _run(h, w, lab, torch.zeros_like(dl))
+    assert not dh.any() and not dw.any()
+    _, _, dh, dw = _run(h, w, lab, torch.full_like(dl, float("nan")))
+    assert dh.isnan().all() and dw.isnan().all()
+    h[17, 3] = float("nan")
+    loss, lse, dh, _ = _run(h, w, lab, dl)
+    keep = torch.arange(260, device="cuda") != 17
+    assert loss[17].isnan() and lse[17].isnan() and dh[17].isnan().all()
+    assert torch.equal(loss[keep], clean[0][keep]) and torch.equal(dh[keep], clean[2][keep])
+
+
 def test_nan_stays_in_its_token():
     h, w, lab, dl = _case(300, 64, 500, "bf16", 0.0, seed=6)
     clean = _run(h, w, lab, dl)
