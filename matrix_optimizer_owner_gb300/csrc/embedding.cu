@@ -5,13 +5,14 @@
 //
 // Both are bound by memory.  The gradient must not depend on timing, so the tokens are sorted
 // by id first (stable, so each id's tokens stay in order) instead of adding with atomics:
-//   1. sort     one cluster of eight blocks (one block for up to kOneBlock tokens) runs a stable
-//               radix sort of (id, token), least significant digit first.  Per pass each warp
-//               counts the digits of its own contiguous share, the blocks exchange their digit
-//               totals through distributed shared memory, and every warp then places its share in
-//               order.  Cluster barriers separate the steps, so the whole sort is one launch.  The
-//               sort is bound by latency, so the launch's other blocks meanwhile write zeros over
-//               the first kFillBytes of the gradient, about what fits in the sort's time.
+//   1. sort     one cluster of eight blocks runs a stable radix sort of (id, token), least
+//               significant digit first.  Per pass each warp counts the digits of its own
+//               contiguous share, the blocks exchange their digit totals through distributed
+//               shared memory, and every warp then places its share in order.  Cluster barriers
+//               separate the steps, so the whole sort is one launch.  The sort is bound by
+//               latency, so the launch's other blocks meanwhile write zeros over the first
+//               kFillBytes of the gradient, about what fits in the sort's time.  Up to kRankMax
+//               tokens are not sorted: each one's place is counted, by blocks of their own.
 //   2. sum      the sorted positions are cut into chunks of 16 or 32.  A chunk sums the runs
 //               of equal ids inside it in fp32 and writes each finished row once; a run that
 //               crosses a chunk boundary leaves fp32 partial rows in the workspace.  The work
@@ -33,9 +34,12 @@
 namespace mfsdp {
 namespace {
 
-constexpr int kSortBlocks = 8;              // cluster size beyond kOneBlock tokens
-constexpr int kOneBlock = 1024;             // tokens that one block sorts (4096 of them: 6 us more
-                                            // than the cluster)
+constexpr int kSortBlocks = 8;              // cluster size
+// Tokens up to which places are counted (their square's comparisons) instead of sorted, where no
+// rows have to be marked: 1001 x 301 took 20 us so and 26 sorted, 3000 x 64 22 and 24, 4000 x 768
+// 28 both, 8192 x 768 50 and 34.
+constexpr int kRankMax = 4096;
+constexpr int kRankKeys = 64;               // tokens per block that counts
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitMax = 9;                // bits per pass
@@ -173,13 +177,10 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32
   return v;
 }
 
-// B blocks sort (a cluster where B > 1); the grid's other blocks write zeros.
-template <int B>
+// The first cluster sorts; the grid's other blocks write zeros.
 __global__ void __launch_bounds__(kSortThreads)
     embedding_sort_kernel(const __grid_constant__ SortArgs p) {
-  auto barrier = [] {
-    if (B > 1) cluster_barrier(); else __syncthreads();
-  };
+  constexpr int B = kSortBlocks;
   extern __shared__ uint32_t sort_smem[];
   uint32_t* hist = sort_smem;                          // [warp][bin], then write positions
   uint32_t* total = hist + kSortWarps * kBinsMax;      // this block's digit totals
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kSortThreads)
               (int64_t)(gridDim.x - B) * kSortThreads);
     return;
   }
-  const uint32_t rank = B > 1 ? cluster_ctarank() : 0u;
+  const uint32_t rank = cluster_ctarank();
   const int bins = 1 << p.digit;
   // every warp of the cluster owns one contiguous share of the positions; a short share's keys
   // stay in registers between counting and placing
@@ -257,14 +258,14 @@ __global__ void __launch_bounds__(kSortThreads)
       }
       total[tid] = s;
     }
-    barrier();
+    cluster_barrier();
     // digit b of this block starts after all smaller digits and the same digit of the blocks
     // before it
     uint32_t all = 0, before = 0;
     if (tid < bins) {
       uint32_t c[B];
 #pragma unroll
-      for (int q = 0; q < B; ++q) c[q] = B > 1 ? ld_cluster_u32(total + tid, (uint32_t)q) : total[tid];
+      for (int q = 0; q < B; ++q) c[q] = ld_cluster_u32(total + tid, (uint32_t)q);
 #pragma unroll
       for (int q = 0; q < B; ++q) {
         all += c[q];
@@ -311,7 +312,61 @@ __global__ void __launch_bounds__(kSortThreads)
         place(i < i1, i < i1 ? key_at(i, false) : 0u, i < i1 ? val_at(i) : 0u);
       }
     }
-    barrier();   // the pass's output, and the peers' totals, before the next pass
+    cluster_barrier();   // the pass's output, and the peers' totals, before the next pass
+  }
+}
+
+// Few tokens: a token's place is the number of tokens that go before it, counted by comparing it
+// with all of them.  Blocks of kRankKeys tokens count independently, so there is no exchange; the
+// grid's other blocks write zeros.
+__global__ void __launch_bounds__(kSortThreads)
+    embedding_rank_kernel(const __grid_constant__ SortArgs p) {
+  constexpr int kParts = kSortThreads / kRankKeys;       // threads per token
+  __shared__ alignas(16) uint32_t key[kRankMax];
+  __shared__ uint32_t place[kRankKeys];
+  pdl_launch();
+  pdl_wait();
+  const int tid = threadIdx.x, blocks = (p.n + kRankKeys - 1) / kRankKeys;
+  if ((int)blockIdx.x >= blocks) {
+    zero_fill(p, (int64_t)((int)blockIdx.x - blocks) * kSortThreads + tid,
+              (int64_t)((int)gridDim.x - blocks) * kSortThreads);
+    return;
+  }
+  const int first = (int)blockIdx.x * kRankKeys;         // this block's tokens
+  // ids outside the table and the padding id go behind every row, as key = vocab
+  const int part = (p.n + 4 * kParts - 1) / (4 * kParts) * 4;  // tokens per thread, whole vectors
+  for (int i = tid; i < part * kParts; i += kSortThreads) {
+    uint32_t k = 0xFFFFFFFFu;                            // past the end: behind everything
+    if (i < p.n) {
+      const int64_t id = load_index(p.ids, p.is64, i);
+      const bool in = id >= 0 && id < p.vocab;
+      if (!in && id != p.padding && i >= first && i < first + kRankKeys)
+        atomicOr(p.status, kStatusBadIndex);
+      k = in && id != p.padding ? (uint32_t)id : (uint32_t)p.vocab;
+    }
+    key[i] = k;
+  }
+  if (tid < kRankKeys) place[tid] = 0u;
+  __syncthreads();
+  const int i = first + tid % kRankKeys, j0 = tid / kRankKeys * part, j1 = j0 + part;
+  const uint32_t mine = i < p.n ? key[i] : 0u;
+  // earlier tokens go first among equals
+  uint32_t before = 0;
+  if (j1 <= first || j0 >= first + kRankKeys) {          // uniform in a warp
+    const uint32_t limit = mine + (j1 <= first ? 1u : 0u);
+#pragma unroll 4
+    for (int j = j0; j < j1; j += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(key + j);
+      before += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+    }
+  } else {
+    for (int j = j0; j < j1; ++j) before += key[j] < mine + (j < i ? 1u : 0u);
+  }
+  atomicAdd(&place[tid % kRankKeys], before);            // integers: any order
+  __syncthreads();
+  if (tid < kRankKeys && i < p.n) {
+    p.key1[place[tid]] = mine;
+    p.val1[place[tid]] = (uint32_t)i;
   }
 }
 
@@ -603,26 +658,25 @@ cudaError_t run_forward(const EmbFwd& a, bool vec, int sms, cudaStream_t st) {
                     st, a);
 }
 
-template <int B>
 cudaError_t launch_sort(const SortArgs& a, int64_t fill_blocks, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(
-      embedding_sort_kernel<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+      embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = B;
+  attr[1].val.clusterDim.x = kSortBlocks;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(B + fill_blocks));
+  cfg.gridDim = dim3((unsigned)(kSortBlocks + cdiv(fill_blocks, kSortBlocks) * kSortBlocks));
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = kSortSmem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = B > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<B>, a);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, embedding_sort_kernel, a);
 }
 
 template <typename TD, typename TG, bool VEC, bool ACC>
@@ -785,7 +839,6 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
     s.fill_units = row_bytes / (s.fill_vec ? 16 : gb);
     fill_blocks = std::min(cdiv(s.fill_rows * s.fill_units, kSortThreads),
                            (int64_t)(2 * sms - kSortBlocks));
-    fill_blocks = cdiv(fill_blocks, kSortBlocks) * kSortBlocks;  // whole clusters
     if (first < vocab) {
       s.present = reinterpret_cast<uint8_t*>(ws + l.present);
       a.present = s.present;
@@ -799,8 +852,15 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
   const bool vec = vec_ok(dtable, ld_dtable, dim, grad_dtype) &&
                    (n_tokens == 0 || vec_ok(dy, ld_dy, dim, dy_dtype));
 
-  cudaError_t e = n_tokens <= kOneBlock ? launch_sort<1>(s, fill_blocks, st)
-                                        : launch_sort<kSortBlocks>(s, fill_blocks, st);
+  // (counting marks no rows: the zeros beside it have to cover the table)
+  cudaError_t e = cudaSuccess;
+  if (n_tokens <= kRankMax && !s.present) {
+    const int64_t blocks = cdiv(n_tokens, kRankKeys) + fill_blocks;
+    if (blocks > 0)
+      e = launch_pdl(embedding_rank_kernel, dim3((unsigned)blocks), dim3(kSortThreads), 0, st, s);
+  } else {
+    e = launch_sort(s, fill_blocks, st);
+  }
   if (e == cudaSuccess && n_tokens > 0) {
     const bool db = dy_dtype == MFSDP_DTYPE_BF16, gb = grad_dtype == MFSDP_DTYPE_BF16;
     e = db ? (gb ? run_sum<bf16_t, bf16_t>(a, vec, accumulate != 0, zero_blocks, st)

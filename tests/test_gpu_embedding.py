@@ -121,6 +121,48 @@ def test_backward_widths_and_types(dim, dy, grad):
     _check(150, dim, 70, "skew", dy, grad, scale=3.5, seed=dim, index=torch.int32)
 
 
+# places counted (up to 4096 tokens) and sorted, around the counting blocks' 64 tokens
+@pytest.mark.parametrize("n", [2, 63, 64, 127, 1000, 4032, 4095, 4096, 4097, 9000])
+@pytest.mark.parametrize("how", ["uniform", "skew", "down"])
+def test_backward_counted_and_sorted(n, how):
+    _check(n, 24, 700, how, seed=n, index=torch.int32 if n % 2 else torch.int64)
+    _check(n, 24, 700, how, seed=n, padding=3, accumulate=True)
+
+
+# a table whose zeros do not fit beside the sort: few tokens are sorted there too
+@pytest.mark.parametrize("n", [1, 2000])
+def test_backward_few_tokens_of_a_large_table(n):
+    _check(n, 512, 90001, "skew", dy="bf16", grad="bf16", seed=n)
+
+
+# one, two and three passes of the sort, at the digit boundaries, counted and sorted
+@pytest.mark.parametrize("vocab", [1, 2, 511, 512, 513, 50257, 262143, 262144, 300001])
+def test_backward_vocabularies_sorted(vocab):
+    _check(4500, 16, vocab, "skew", seed=vocab)
+    _check(4500, 16, vocab, "down", seed=vocab + 1)
+
+
+@pytest.mark.parametrize("n", [300, 5000])
+def test_backward_ids_outside_counted_and_sorted(n):
+    from matrix_optimizer_owner_gb300 import _lib, mfsdp
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    ids = _ids(n, 60, gen, "uniform")
+    dy = _mat(n, 40, "f32", gen)
+    keep = torch.rand(n, generator=gen, device="cuda") < 0.8
+    want, got = (torch.empty(60, 40, device="cuda") for _ in range(2))
+    zeroed = dy * keep[:, None]
+    mfsdp.mfsdp_embedding_backward(ids, zeroed, 1.0, want)
+    assert mfsdp.mfsdp_query_status() == 0
+    bad = torch.tensor([60, -1, 1 << 40, -(1 << 40)], device="cuda")[torch.arange(n) % 4]
+    dy[~keep] = float("nan")                         # not read into any row
+    ids = torch.where(keep, ids, bad)
+    mfsdp.mfsdp_embedding_backward(ids, dy, 1.0, got)
+    assert _lib.STATUS_NAMES[mfsdp.mfsdp_query_status()] == "MFSDP_EINDEX"
+    assert torch.allclose(got, want, rtol=0, atol=n * 2.0 ** -20)
+    mfsdp.mfsdp_embedding_backward(torch.where(keep, ids, 60), dy, 1.0, got, padding_idx=60)
+    assert mfsdp.mfsdp_query_status() == 0           # a padding id outside the table
+
+
 # one, two and three passes of the sort, at the digit boundaries
 @pytest.mark.parametrize("vocab", [1, 2, 511, 512, 513, 50257, 262143, 262144, 300001])
 def test_backward_vocabularies(vocab):
