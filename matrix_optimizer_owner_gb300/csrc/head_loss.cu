@@ -23,8 +23,8 @@
 // bf16 inputs run on the CTA-pair tcgen05 kernel below (256 x 256 tiles, TMA operands,
 // accumulators in tensor memory).  fp32 inputs run on the library's fp32 GEMM (3xTF32) with a
 // piece of Z in the workspace.  Small products of both run on the CUDA cores.  Up to four tokens
-// (one, with bf16 inputs that TMA can read) run forward as a matrix-vector product that reads W
-// once, without tensor cores.
+// (forward one and backward two, with bf16 inputs that TMA can read) take one pass over W in each
+// direction, without tensor cores.
 //
 // Training sizes are bound by the tensor cores: of the four products, forward's Z, its second
 // computation, dH and dW, the second costs the time that storing Z would cost in memory (8192 x
@@ -1106,6 +1106,181 @@ __global__ void __launch_bounds__(kFewJoinThreads)
   if (p.loss) p.loss[t] = live ? l - zlab : 0.f;
 }
 
+// The backward pass of few tokens, one pass over W: 16 rows at a time, a warp computes a row's
+// logits and G; then every thread takes columns of those rows, for the rows of dW and for its
+// sums of dH, which stay in shared memory until the block's last rows.  Bound by memory: W is read
+// and dW written once (the columns' second read of a row comes from the L1 or L2).
+constexpr int kFewGradWarps = 16;
+constexpr int kFewGradThreads = 32 * kFewGradWarps;
+struct FewGradArgs {
+  const void *hidden, *weight, *labels;
+  int64_t ld_h, ld_w, ignore;
+  const float *lse, *dloss;
+  void *dh, *dw;                           // nullable
+  int64_t ld_dh, ld_dw;
+  float* acc;                              // [blocks][n][pitch]
+  int32_t n, dim, vocab, is64, blocks, pitch;
+  int* status;
+};
+
+__device__ __forceinline__ int few_label(const FewGradArgs& p, int t, bool& bad) {
+  const int64_t l = load_index(p.labels, p.is64, t);
+  const bool live = l != p.ignore && l >= 0 && l < p.vocab;
+  bad = !live && l != p.ignore;
+  return live ? (int)l : -1;
+}
+
+template <typename T, int C>
+__device__ __forceinline__ void load_columns(const T* p, float (&x)[C]) {
+  if constexpr (C == 1) {
+    x[0] = to_f32(*p);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    x[0] = __uint_as_float(q.x << 16);
+    x[1] = __uint_as_float(q.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(q.y << 16);
+    x[3] = __uint_as_float(q.y & 0xFFFF0000u);
+  } else {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    x[0] = q.x;
+    x[1] = q.y;
+    x[2] = q.z;
+    x[3] = q.w;
+  }
+}
+
+template <typename T, int C>
+__device__ __forceinline__ void store_columns(T* p, const float (&x)[C]) {
+  if constexpr (C == 1)
+    *p = from_f32<T>(x[0]);
+  else if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  else
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// C columns per thread at a time: 4 where every row is aligned to them, else 1.
+template <typename T, int NT, int C>
+__global__ void __launch_bounds__(kFewGradThreads)
+    head_few_grad_kernel(const __grid_constant__ FewGradArgs p) {
+  extern __shared__ float few_h[];         // hidden rows, then the sums: [NT][dim rounded up to 8]
+  __shared__ float gs[kFewGradWarps][NT];
+  pdl_launch();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int dim8 = (p.dim + 7) / 8 * 8;
+  float* sums = few_h + NT * dim8;
+  int lab[NT];
+  float lse2[NT], dl[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int at = min(t, p.n - 1);
+    bool bad;
+    lab[t] = few_label(p, at, bad);
+    if (bad && t < p.n && blockIdx.x == 0 && tid == 0) atomicOr(p.status, kStatusBadIndex);
+    if (t >= p.n) lab[t] = -1;
+    lse2[t] = p.lse[at] * kLog2e;
+    dl[t] = p.dloss[at];
+    const T* h = static_cast<const T*>(p.hidden) + (int64_t)at * p.ld_h;
+    for (int e = tid; e < dim8; e += kFewGradThreads) {
+      const float x = to_f32(h[min(e, p.dim - 1)]);
+      few_h[t * dim8 + e] = lab[t] >= 0 && e < p.dim ? x : 0.f;
+      sums[t * dim8 + e] = 0.f;
+    }
+  }
+  __syncthreads();
+  const T* w = static_cast<const T*>(p.weight);
+  T* dw = static_cast<T*>(p.dw);
+  for (int v0 = (int)blockIdx.x * kFewGradWarps; v0 < p.vocab; v0 += p.blocks * kFewGradWarps) {
+    const int v = v0 + warp;
+    const T* row = w + (int64_t)min(v, p.vocab - 1) * p.ld_w;
+    float dot[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) dot[t] = 0.f;
+#pragma unroll 8
+    for (int e = lane * C; e < p.dim; e += 32 * C) {
+      float x[C];
+      load_columns<T, C>(row + e, x);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < C; ++k) dot[t] = fmaf(x[k], few_h[t * dim8 + e + k], dot[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float z = warp_sum(dot[t]);
+      if (lane == 0) {
+        float g = 0.f;
+        if (lab[t] >= 0 && v < p.vocab) {
+          g = exp2f(fmaf(z, kLog2e, -lse2[t]));
+          if (v == lab[t]) g -= 1.f;
+          g *= dl[t];
+        }
+        gs[warp][t] = g;
+      }
+    }
+    __syncthreads();
+    const int rows = min(kFewGradWarps, p.vocab - v0);
+    for (int e = tid * C; e < p.dim; e += kFewGradThreads * C) {
+      float h[NT][C], a[NT][C];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          h[t][k] = few_h[t * dim8 + e + k];
+          a[t][k] = sums[t * dim8 + e + k];
+        }
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) {
+        float x[C], d[C];
+        if (p.dh) load_columns<T, C>(w + (int64_t)(v0 + r) * p.ld_w + e, x);
+#pragma unroll
+        for (int k = 0; k < C; ++k) d[k] = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float g = gs[r][t];
+#pragma unroll
+          for (int k = 0; k < C; ++k) {
+            d[k] = fmaf(g, h[t][k], d[k]);
+            if (p.dh) a[t][k] = fmaf(g, x[k], a[t][k]);
+          }
+        }
+        if (dw) store_columns<T, C>(dw + (int64_t)(v0 + r) * p.ld_dw + e, d);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < C; ++k) sums[t * dim8 + e + k] = a[t][k];   // this thread's columns
+    }
+    __syncthreads();
+  }
+  if (!p.dh) return;
+  for (int t = 0; t < p.n; ++t)
+    for (int e = tid; e < p.dim; e += kFewGradThreads)
+      p.acc[((int64_t)blockIdx.x * p.n + t) * p.pitch + e] = sums[t * dim8 + e];
+}
+
+// 32 columns of a token's dH: 32 groups add the blocks' sums, then the groups are added in order.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+    head_few_finish_kernel(const __grid_constant__ FewGradArgs p) {
+  __shared__ float sm[32][33];
+  pdl_launch();
+  pdl_wait();
+  const int t = blockIdx.y, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int e = (int)blockIdx.x * 32 + lane, at = min(e, p.dim - 1);
+  float v = 0.f;
+#pragma unroll 4
+  for (int b = grp; b < p.blocks; b += 32) v += p.acc[((int64_t)b * p.n + t) * p.pitch + at];
+  sm[grp][lane] = v;
+  __syncthreads();
+  if (grp != 0 || e >= p.dim) return;
+  for (int g = 1; g < 32; ++g) v += sm[g][lane];
+  bool bad;
+  const bool live = few_label(p, t, bad) >= 0;
+  static_cast<T*>(p.dh)[t * p.ld_dh + e] = from_f32<T>(live ? v : 0.f);
+}
+
 // ---------------------------------------------------------------- dH: slices to the caller's rows
 struct FinishArgs {
   const float* acc;                        // [splits][rows][pitch]
@@ -1586,7 +1761,7 @@ struct HeadShape {
   int64_t n, dim, vocab;
   int32_t dtype;
   bool backward, copy_w;
-  bool few;                                // forward of few tokens: head_few_kernel
+  bool few;                                // few tokens: head_few_kernel, head_few_grad_kernel
   bool core;                               // small: on the CUDA cores
   int64_t rows, pitch;                     // compacted H (and dH slices)
   int64_t piece, pieces;                   // columns per piece
@@ -1616,6 +1791,7 @@ constexpr int64_t kCoreFlops = 1ll << 29;
 constexpr int64_t kCoreFlopsBf16 = 64ll << 20;
 constexpr int kGatherBlocks = 608;         // blocks of the gather launch, at most
 constexpr int kFewBlocks = 1024;           // blocks of the few-token kernel (bounds its workspace)
+constexpr int kFewGradBlocks = 304;        // and of its backward pass
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
 
 // Columns per piece, whole tiles.  Every piece is a launch whose last wave and ramp cost some
@@ -1640,6 +1816,9 @@ int64_t piece_columns(const HeadShape& s, int64_t asked) {
   return std::min(c, up(s.vocab, kTile));
 }
 
+// The few-token kernels are built for 1, 2 and 4 tokens.
+int64_t few_width(int64_t n) { return n <= 2 ? std::max<int64_t>(n, 1) : 4; }
+
 HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool backward,
                      const void* weight, int64_t ld_w, int64_t piece, int sms) {
   HeadShape s{};
@@ -1651,12 +1830,18 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   const bool bf = dtype == MFSDP_DTYPE_BF16;
   // TMA reads rows that start on 16-byte boundaries
   s.copy_w = !aligned_to(weight, 16) || ld_w % (bf ? 8 : 4) != 0;
-  // the tokens' hidden rows have to fit in shared memory
-  s.few = !backward && n <= (bf && !s.copy_w ? 1 : kFewTokens) &&
-          up(dim, 8) * 4 * kFewTokens <= (200 << 10);
   // (counted as the tiles are; the product of the three would pass 64 bits)
-  s.core = !s.few && 2 * up(std::max<int64_t>(n, 1), kCoreTile) * up(dim, kCoreK) <=
-                         (bf ? kCoreFlopsBf16 : kCoreFlops) / up(vocab, kCoreTile);
+  const bool small = 2 * up(std::max<int64_t>(n, 1), kCoreTile) * up(dim, kCoreK) <=
+                     (bf ? kCoreFlopsBf16 : kCoreFlops) / up(vocab, kCoreTile);
+  // Few tokens, whose hidden rows (and sums) have to fit in shared memory.  Backward against the
+  // other paths: 1 token x 2981 and 3264 fp32 rows 72 and 305 us, 4 x 768 and 50257 fp32 rows 233
+  // and 355, 4 x 70 and 7784 bf16 rows 30 and 44; bf16 that the tensor cores can read, 2 x 2048 and
+  // 32000 rows 124 and 165, 1 x 768 and 50257 116 and 105, 4 x 4096 and 128256 1150 and 798.
+  s.few = backward ? n >= 1 && n <= kFewTokens && (!bf || s.copy_w || n <= 2 || small) &&
+                         2 * up(dim, 8) * 4 * few_width(n) <= (200 << 10)
+                   : n <= (bf && !s.copy_w ? 1 : kFewTokens) &&
+                         up(dim, 8) * 4 * kFewTokens <= (200 << 10);
+  s.core = !s.few && small;
   if (s.few || s.core) s.copy_w = false;
   s.rows = up(std::max<int64_t>(n, 1), kTile);
   s.pitch = up(dim, 64);
@@ -1699,6 +1884,11 @@ HeadLayout head_layout(const HeadShape& s) {
   };
   const bool bf = s.dtype == MFSDP_DTYPE_BF16;
   const int64_t es = bf ? 2 : 4;
+  if (s.few && s.backward) {
+    l.acc = take(kFewGradBlocks * s.n * s.pitch * 4);
+    l.total = off;
+    return l;
+  }
   if (s.few) {
     l.zlab = take(kFewTokens * 4);
     l.part = take(kFewBlocks * kFewTokens * 8);
@@ -2012,6 +2202,8 @@ struct HeadCall {
   }
 
   int run() const {
+    if (s.few && s.backward)
+      return s.dtype == MFSDP_DTYPE_BF16 ? run_few_grad<bf16_t>() : run_few_grad<float>();
     if (s.few) return run_few();
     if (s.core)
       return s.dtype == MFSDP_DTYPE_BF16 ? run_core<bf16_t>() : run_core<float>();
@@ -2021,6 +2213,62 @@ struct HeadCall {
     } catch (const std::bad_alloc&) {  // the problem table of very many pieces
       return MFSDP_ESHAPE;
     }
+  }
+
+  template <typename T, int NT, int C>
+  cudaError_t launch_few_grad(const FewGradArgs& a, size_t smem) const {
+    if (smem > 48 * 1024) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(head_few_grad_kernel<T, NT, C>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(head_few_grad_kernel<T, NT, C>, dim3((unsigned)a.blocks),
+                      dim3(kFewGradThreads), smem, st, a);
+  }
+
+  template <typename T>
+  int run_few_grad() const {
+    FewGradArgs a{};
+    a.hidden = hidden;
+    a.weight = weight;
+    a.labels = labels;
+    a.ld_h = ld_h;
+    a.ld_w = ld_w;
+    a.ignore = ignore;
+    a.lse = lse_in;
+    a.dloss = dloss;
+    a.dh = dh;
+    a.dw = dw;
+    a.ld_dh = ld_dh;
+    a.ld_dw = ld_dw;
+    a.acc = at<float>(l.acc);
+    a.n = (int32_t)s.n;
+    a.dim = (int32_t)s.dim;
+    a.vocab = (int32_t)s.vocab;
+    a.is64 = index_dtype == MFSDP_INDEX_I64;
+    a.pitch = (int32_t)s.pitch;
+    a.status = status;
+    const bool vec = s.dim % 4 == 0 && aligned_to(weight, 4 * sizeof(T)) && ld_w % 4 == 0 &&
+                     (!dw || (aligned_to(dw, 4 * sizeof(T)) && ld_dw % 4 == 0));
+    const int nt = (int)few_width(s.n);
+    const size_t smem = (size_t)up(s.dim, 8) * 8 * nt;
+    const int64_t per_sm = smem <= (100 << 10) ? 2 : 1;
+    a.blocks = (int32_t)std::min({per_sm * sms, (int64_t)kFewGradBlocks,
+                                  cdiv(s.vocab, kFewGradWarps)});
+    cudaError_t e;
+    if (vec)
+      e = nt == 1   ? launch_few_grad<T, 1, 4>(a, smem)
+          : nt == 2 ? launch_few_grad<T, 2, 4>(a, smem)
+                    : launch_few_grad<T, 4, 4>(a, smem);
+    else
+      e = nt == 1   ? launch_few_grad<T, 1, 1>(a, smem)
+          : nt == 2 ? launch_few_grad<T, 2, 1>(a, smem)
+                    : launch_few_grad<T, 4, 1>(a, smem);
+    if (e == cudaSuccess && dh)
+      e = launch_pdl(head_few_finish_kernel<T>, dim3((unsigned)cdiv(s.dim, 32), (unsigned)s.n),
+                     dim3(1024), 0, st, a);
+    return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
   }
 
   template <typename T>

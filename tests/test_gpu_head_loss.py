@@ -199,11 +199,61 @@ def test_f32_dropped_small_and_large(n, dim, vocab):
     assert mfsdp.mfsdp_query_status() == 0
 
 
+# the backward pass of up to four tokens: one pass over W, more rows than its blocks take at once,
+# odd widths, and widths whose sums do not fit beside it
+@pytest.mark.parametrize("n", [1, 2, 3, 4])
+@pytest.mark.parametrize("dim,vocab", [(1, 1), (3, 17), (64, 16), (130, 5000), (1024, 9999),
+                                       (6400, 300), (6408, 300), (13000, 200)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_few_tokens_backward(n, dim, vocab, dtype):
+    h, w, lab, dl = _case(n, dim, vocab, dtype, 0.0, torch.int32, seed=n + dim)
+    if n > 2:
+        lab[1] = -100
+        h[1] = float("nan")
+        dl[1] = float("nan")
+    out = _run(h, w, lab, dl)
+    if n > 2:
+        dl[1] = 0.0
+    _verify(h, w, lab, dl, out)
+    again = _run(h, w, lab, dl)
+    assert all(torch.equal(a, b) for a, b in zip(again, out))
+    assert torch.equal(_run(h, w, lab, dl, want="h")[2], out[2])
+    assert torch.equal(_run(h, w, lab, dl, want="w")[3], out[3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pitch,offset", [(8, 0), (4, 4), (3, 0), (0, 1)])
+def test_few_tokens_backward_strides(dtype, pitch, offset):
+    h, w, lab, dl = _case(3, 104, 3000, dtype, 0.0, seed=pitch + offset, pitch=pitch, offset=offset)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dh = _mat(3, 104, dtype, gen, 1.0, pitch, offset)
+    dw = _mat(3000, 104, dtype, gen, 1.0, pitch, offset)
+    _verify(h, w, lab, dl, _run(h, w, lab, dl, dh=dh, dw=dw))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_few_tokens_backward_bad_label_and_infinite_weight(dtype):
+    from matrix_optimizer_owner_gb300 import _lib, mfsdp
+    h, w, lab, dl = _case(3, 100, 700, dtype, 0.0, seed=16)
+    lab[1] = 700
+    w[5, 7] = float("inf")
+    _, _, dh, _ = _run(h, w, lab, dl)
+    assert not dh[1].any()                           # a dropped token, whatever W holds
+    assert _lib.STATUS_NAMES[mfsdp.mfsdp_query_status()] == "MFSDP_EINDEX"
+    inplace = h.clone()
+    w[5, 7] = 0.0
+    loss, lse, dh, dw = _run(h, w, lab, dl)
+    mfsdp.mfsdp_head_loss_backward(inplace, w, lab, lse, dl, inplace, dw)
+    assert torch.equal(inplace, dh)
+    mfsdp.mfsdp_query_status()
+
+
 # bf16 products that the tensor cores take (above 64 Mi operations): tiles, k-blocks and pieces
 # that end inside, few tokens, rows that TMA cannot read
 @pytest.mark.parametrize("n,dim,vocab", [
     (255, 520, 515), (256, 512, 512), (257, 584, 513), (513, 72, 2049), (5, 1030, 2000),
-    (64, 64, 13000), (33, 1100, 1025), (1025, 320, 255), (2, 2049, 2000), (1, 3300, 1000)])
+    (64, 64, 13000), (33, 1100, 1025), (1025, 320, 255), (2, 2049, 2000), (1, 3300, 1000),
+    (3, 1088, 2000), (4, 2048, 777)])
 @pytest.mark.parametrize("piece", [0, 256])
 def test_bf16_tensor_core_sizes(n, dim, vocab, piece):
     h, w, lab, dl = _case(n, dim, vocab, "bf16", 0.2 if n > 2 else 0.0, seed=n + dim)
