@@ -557,20 +557,22 @@ _scratch = _Scratch()
 
 def _workspace(ws, nbytes: int, like, dev: int, stream, raw: int):
     """The caller's uint8 workspace, or this thread's for the current stream.  A call on another
-    stream, in a graph capture or with a large workspace gets a fresh one, which lives until the
-    stream is done with it."""
+    stream, in a graph capture or with a large workspace gets a fresh one from the pool of the
+    stream it runs on: whatever used that memory before, and whatever gets it next, is ordered
+    with the call by that stream.  (The current stream's pool may hand out memory that kernels
+    queued there still use.)"""
     if ws is not None:
         if ws.get_device() != dev:
             raise ValueError("expected the workspace on the current CUDA device")
         return ws, ws.numel() * ws.element_size()
     if stream is None and nbytes <= _Scratch.LIMIT and not _is_capturing():
         return _scratch.get(nbytes, like, dev, raw), nbytes
+    if stream is None:
+        return like.new_empty((nbytes or 1,), dtype=_U8), nbytes
     import torch
-    ws = like.new_empty((nbytes or 1,), dtype=_U8)
-    if stream is not None:  # the block may be reused on the current stream otherwise
-        ws.record_stream(stream if hasattr(stream, "cuda_stream")
-                         else torch.cuda.ExternalStream(stream))
-    return ws, nbytes
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                           else torch.cuda.ExternalStream(stream)):
+        return like.new_empty((nbytes or 1,), dtype=_U8), nbytes
 
 
 def _params_dtype(*params):

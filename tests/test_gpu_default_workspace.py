@@ -80,3 +80,26 @@ def test_threads_and_streams_at_the_same_time():
         t.join()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_explicit_stream_leaves_the_current_streams_memory_alone():
+    """A temporary of the workspace's size is freed while kernels queued on the current stream still
+    use it.  A call on another stream must not take its memory."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    torch.cuda.synchronize()
+    ids, dy = _case(3000, 9)
+    want = _grad(ids, dy, torch.empty(700, 128, device="cuda")).clone()
+    nbytes = mfsdp.mfsdp_embedding_backward_workspace_bytes(700, 128, 3000)
+    for handle in (False, True):
+        out, seen = torch.zeros_like(want), torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        temp = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        temp.fill_(7)
+        torch.cuda._sleep(50_000_000)                # some 25 ms
+        seen.copy_(temp)
+        del temp                                     # free for the current stream, not for others
+        mfsdp.mfsdp_embedding_backward(ids, dy, 1.0, out,
+                                       stream=s.cuda_stream if handle else s)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and bool((seen == 7).all())

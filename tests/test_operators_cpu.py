@@ -190,3 +190,41 @@ def test_binding_refuses_wrong_tensors():
         mfsdp.mfsdp_head_loss_forward(x, table, lab, f.double(), f)
     with pytest.raises(ValueError, match="CUDA device"):
         mfsdp.mfsdp_head_loss_backward(x, table, lab, f, f, x, table)
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_fresh_workspace_comes_from_the_stream_it_is_used_on(monkeypatch, as_handle):
+    import contextlib
+
+    import torch
+
+    from matrix_optimizer_owner_gb300 import mfsdp
+    current, made_on = ["default"], []
+
+    class Stream:
+        cuda_stream = 77
+
+    @contextlib.contextmanager
+    def switch(s):
+        current.append(s.cuda_stream)
+        yield
+        current.pop()
+
+    class Like:
+        def new_empty(self, shape, dtype):
+            made_on.append(current[-1])
+            return torch.empty(shape, dtype=torch.uint8)
+
+    class External(Stream):
+        def __init__(self, handle):
+            assert handle == 77
+
+    monkeypatch.setattr(torch.cuda, "stream", switch)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(mfsdp, "_is_capturing", lambda: False)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    ws, size = mfsdp._workspace(None, 100, Like(), 0, 77 if as_handle else Stream(), 77)
+    assert made_on == [77] and ws.numel() == size == 100
+    # on the current stream: a large one is fresh and made there
+    mfsdp._workspace(None, mfsdp._Scratch.LIMIT + 1, Like(), 0, None, 5)
+    assert made_on == [77, "default"] and current == ["default"]
