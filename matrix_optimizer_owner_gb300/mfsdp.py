@@ -421,6 +421,19 @@ def mfsdp_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
            _lib.load().mfsdp_selftest_wait_timeout(limit_ns, _stream(stream)))
 
 
+def _fresh_workspace(nbytes: int, like, stream):
+    """A uint8 workspace on `like`'s device from the pool of the stream the call runs on (None: the
+    current one): whatever used that memory before, and whatever gets it next, is ordered with the
+    call by that stream.  (The current stream's pool may hand out memory that kernels queued there
+    still use.)"""
+    import torch
+    if stream is None:
+        return like.new_empty((nbytes or 1,), dtype=torch.uint8)
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                           else torch.cuda.ExternalStream(stream)):
+        return like.new_empty((nbytes or 1,), dtype=torch.uint8)
+
+
 # ------------------------------------------------------------------------------- fp32 GEMM
 def mfsdp_gemm_f32_batched(problems, trans_a: bool = False, trans_b: bool = False,
                            workspace=None, stream=None) -> None:
@@ -441,8 +454,8 @@ def mfsdp_gemm_f32_batched(problems, trans_a: bool = False, trans_b: bool = Fals
         tab[i] = GemmProblem(a.data_ptr(), b.data_ptr(), c.data_ptr(), m, nn, k, a.stride(0),
                              b.stride(0), c.stride(0), alpha, beta)
     if workspace is None:
-        workspace = torch.empty(max(lib.mfsdp_gemm_f32_workspace_bytes(n), 1), dtype=torch.uint8,
-                                device=problems[0][2].device if n else None)
+        workspace = _fresh_workspace(lib.mfsdp_gemm_f32_workspace_bytes(n),
+                                     problems[0][2] if n else torch.empty(0), stream)
     _check("mfsdp_gemm_f32_batched",
            lib.mfsdp_gemm_f32_batched(tab, n, 1 if trans_a else 0, 1 if trans_b else 0,
                                       _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -557,22 +570,14 @@ _scratch = _Scratch()
 
 def _workspace(ws, nbytes: int, like, dev: int, stream, raw: int):
     """The caller's uint8 workspace, or this thread's for the current stream.  A call on another
-    stream, in a graph capture or with a large workspace gets a fresh one from the pool of the
-    stream it runs on: whatever used that memory before, and whatever gets it next, is ordered
-    with the call by that stream.  (The current stream's pool may hand out memory that kernels
-    queued there still use.)"""
+    stream, in a graph capture or with a large workspace gets a fresh one."""
     if ws is not None:
         if ws.get_device() != dev:
             raise ValueError("expected the workspace on the current CUDA device")
         return ws, ws.numel() * ws.element_size()
     if stream is None and nbytes <= _Scratch.LIMIT and not _is_capturing():
         return _scratch.get(nbytes, like, dev, raw), nbytes
-    if stream is None:
-        return like.new_empty((nbytes or 1,), dtype=_U8), nbytes
-    import torch
-    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
-                           else torch.cuda.ExternalStream(stream)):
-        return like.new_empty((nbytes or 1,), dtype=_U8), nbytes
+    return _fresh_workspace(nbytes, like, stream), nbytes
 
 
 def _params_dtype(*params):

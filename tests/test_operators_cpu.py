@@ -228,3 +228,43 @@ def test_fresh_workspace_comes_from_the_stream_it_is_used_on(monkeypatch, as_han
     # on the current stream: a large one is fresh and made there
     mfsdp._workspace(None, mfsdp._Scratch.LIMIT + 1, Like(), 0, None, 5)
     assert made_on == [77, "default"] and current == ["default"]
+
+
+def test_gemm_workspace_comes_from_the_stream_it_is_used_on(monkeypatch):
+    import contextlib
+
+    import torch
+
+    from matrix_optimizer_owner_gb300 import mfsdp
+    current, made_on = ["default"], []
+
+    class Stream:
+        cuda_stream = 77
+
+    class FakeLib:                       # no kernel sees these host tensors
+        def mfsdp_gemm_f32_workspace_bytes(self, n):
+            return 256 * n
+
+        def mfsdp_gemm_f32_batched(self, *args):
+            assert args[-1] == 77
+            return 0
+
+    @contextlib.contextmanager
+    def switch(s):
+        current.append(s.cuda_stream)
+        yield
+        current.pop()
+
+    def recorded(f):
+        def g(*args, **kw):
+            made_on.append(current[-1])
+            return f(*args, **kw)
+        return g
+
+    a = torch.zeros(4, 4)
+    monkeypatch.setattr(torch.cuda, "stream", switch)
+    monkeypatch.setattr(mfsdp._lib, "load", FakeLib)
+    monkeypatch.setattr(torch, "empty", recorded(torch.empty))
+    monkeypatch.setattr(torch.Tensor, "new_empty", recorded(torch.Tensor.new_empty))
+    mfsdp.mfsdp_gemm_f32_batched([(a, a, a.clone(), 1.0, 0.0)], stream=Stream())
+    assert made_on == [77]
