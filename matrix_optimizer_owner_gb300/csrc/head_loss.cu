@@ -1793,6 +1793,7 @@ constexpr int kGatherBlocks = 608;         // blocks of the gather launch, at mo
 constexpr int kFewBlocks = 1024;           // blocks of the few-token kernel (bounds its workspace)
 constexpr int kFewGradBlocks = 304;        // and of its backward pass
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
+constexpr int kFewSmem = 200 << 10;        // dynamic shared memory the few-token kernels may take
 
 // Columns per piece, whole tiles.  Every piece is a launch whose last wave and ramp cost some
 // 20 us, so the backward pass takes what the rows of H and the sums of dH leave of kWorkBytes
@@ -1838,9 +1839,9 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   // and 355, 4 x 70 and 7784 bf16 rows 30 and 44; bf16 that the tensor cores can read, 2 x 2048 and
   // 32000 rows 124 and 165, 1 x 768 and 50257 116 and 105, 4 x 4096 and 128256 1150 and 798.
   s.few = backward ? n >= 1 && n <= kFewTokens && (!bf || s.copy_w || n <= 2 || small) &&
-                         2 * up(dim, 8) * 4 * few_width(n) <= (200 << 10)
+                         2 * up(dim, 8) * 4 * few_width(n) <= kFewSmem
                    : n <= (bf && !s.copy_w ? 1 : kFewTokens) &&
-                         up(dim, 8) * 4 * kFewTokens <= (200 << 10);
+                         up(dim, 8) * 4 * kFewTokens <= kFewSmem;
   s.core = !s.few && small;
   if (s.few || s.core) s.copy_w = false;
   s.rows = up(std::max<int64_t>(n, 1), kTile);
@@ -1959,6 +1960,20 @@ int head_pairs(int sms) {
   return n;
 }
 
+// Raises a few-token kernel's shared-memory limit, once per device; `done` is the kernel's own.  The
+// limit belongs to the kernel, not to a launch: set to what each call needs, a narrow call of one
+// host thread would take it from under a wide call of another before that one launches.
+constexpr int kFewDevices = 64;
+template <typename K>
+cudaError_t allow_few_smem(std::atomic<bool>* done, K kernel) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < kFewDevices && done[dev].load())) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  if (e == cudaSuccess && dev < kFewDevices) done[dev].store(true);
+  return e;
+}
+
 template <int PHASE>
 cudaError_t launch_head(const HeadArgs& a, int64_t tiles, int pairs, cudaStream_t st) {
   cudaLaunchAttribute attr[2];
@@ -2061,8 +2076,8 @@ struct HeadCall {
   template <typename T, int NT>
   cudaError_t launch_few(const FewArgs& a, size_t smem) const {
     if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(
-          head_few_kernel<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      static std::atomic<bool> done[kFewDevices];
+      const cudaError_t e = allow_few_smem(done, head_few_kernel<T, NT>);
       if (e != cudaSuccess) return e;
     }
     return launch_pdl(head_few_kernel<T, NT>, dim3((unsigned)a.blocks), dim3(32 * kFewWarps), smem, st,
@@ -2091,7 +2106,7 @@ struct HeadCall {
     a.status = status;
     const int nt = s.n == 1 ? 1 : s.n == 2 ? 2 : 4;
     const size_t smem = (size_t)up(s.dim, 8) * 4 * nt;
-    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(4, (200 << 10) / (int64_t)smem));
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(4, kFewSmem / (int64_t)smem));
     a.blocks = (int32_t)std::min<int64_t>(std::min(per_sm * sms, (int64_t)kFewBlocks),
                                           cdiv(s.vocab, kFewWarps * kFewRows));
     cudaError_t e;
@@ -2218,9 +2233,8 @@ struct HeadCall {
   template <typename T, int NT, int C>
   cudaError_t launch_few_grad(const FewGradArgs& a, size_t smem) const {
     if (smem > 48 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(head_few_grad_kernel<T, NT, C>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      static std::atomic<bool> done[kFewDevices];
+      const cudaError_t e = allow_few_smem(done, head_few_grad_kernel<T, NT, C>);
       if (e != cudaSuccess) return e;
     }
     return launch_pdl(head_few_grad_kernel<T, NT, C>, dim3((unsigned)a.blocks),

@@ -103,3 +103,57 @@ def test_explicit_stream_leaves_the_current_streams_memory_alone():
                                        stream=s.cuda_stream if handle else s)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and bool((seen == 7).all())
+
+
+def test_threads_with_few_token_heads_of_different_widths():
+    """A kernel's shared-memory limit is shared by all host threads: a narrow call must not lower it
+    between a wide call's setting and its launch.  (The C entry points, called back to back: the
+    binding's own time between two calls would hide it.)"""
+    from matrix_optimizer_owner_gb300 import _lib, mfsdp
+    lib = _lib.load()
+
+    def case(dim, seed):
+        """Arguments of both calls, and the tensors they point to."""
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        h = torch.randn(4, dim, generator=gen, device="cuda")
+        w = torch.randn(64, dim, generator=gen, device="cuda") / dim ** 0.5
+        lab = torch.randint(64, (4,), generator=gen, device="cuda")
+        loss, lse = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+        out = [loss, lse, torch.empty_like(h), torch.empty_like(w)]
+        ws = [torch.empty(mfsdp.mfsdp_head_loss_workspace_bytes(4, dim, w, back),
+                          dtype=torch.uint8, device="cuda") for back in (False, True)]
+        st = torch.cuda.Stream()
+        both = (4, dim, 64, mfsdp.DTYPE_F32, h.data_ptr(), dim, w.data_ptr(), dim, mfsdp.INDEX_I64,
+                lab.data_ptr(), -100)
+        fwd = both + (loss.data_ptr(), lse.data_ptr(), ws[0].data_ptr(), ws[0].numel(),
+                      st.cuda_stream)
+        bwd = both + (lse.data_ptr(), lse.data_ptr(), 0, out[2].data_ptr(), dim, out[3].data_ptr(),
+                      dim, ws[1].data_ptr(), ws[1].numel(), st.cuda_stream)
+        return fwd, bwd, out, (h, w, lab, ws, st)
+
+    # backward at 6400 takes all that the path may use, at 1600 a quarter; forward at 12800 and 3400
+    cases = [case(d, i) for i, d in enumerate((6400, 1600, 12800, 3400))]
+    torch.cuda.synchronize()
+    for fwd, bwd, _, _ in cases:
+        assert lib.mfsdp_head_loss_forward(*fwd) == 0 and lib.mfsdp_head_loss_backward(*bwd) == 0
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in c[2]] for c in cases]
+    start, status = threading.Barrier(4), [set() for _ in range(4)]
+
+    def work(i):
+        torch.cuda.set_device(0)
+        call, args = ((lib.mfsdp_head_loss_backward, cases[i][1]) if i < 2
+                      else (lib.mfsdp_head_loss_forward, cases[i][0]))
+        start.wait()
+        for _ in range(5000):
+            status[i].add(call(*args))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [{0}] * 4
+    for (_, _, out, _), ref in zip(cases, want):
+        assert all(torch.equal(x, y) for x, y in zip(out, ref))
