@@ -1775,10 +1775,11 @@ struct HeadLayout {
   size_t ht, gt, wt, descs, total;
 };
 
-constexpr int64_t kWorkBytes = 390ll << 20;  // what the backward pass's buffers may come to
-constexpr int64_t kMinElems = 32ll << 20;  // least entries of G per piece
-constexpr int64_t kZElems = 32ll << 20;    // entries of Z (fp32), or of a copied W, per piece
-constexpr int64_t kPartBytes = 64ll << 20; // bytes of the forward partials per piece
+constexpr int64_t kWorkBytes = 390ll << 20;   // what the backward pass's buffers may come to
+constexpr int64_t kMinBytes = 128ll << 20;   // least of them for a piece's columns
+constexpr int64_t kZBytes = 128ll << 20;     // fp32 forward: a piece of Z
+constexpr int64_t kPartBytes = 64ll << 20;   // bf16 forward: a piece's partials
+constexpr int64_t kMinColumns = 4096;        // least columns of a piece
 constexpr int kMaxSplits = 64;
 // Largest fp32 product that runs on the CUDA cores, in operations of whole tiles.  Both passes
 // there and through the 3xTF32 GEMM: 333 tokens x 100 against 1031 rows (0.1 G) 44 and 102 us, 16 x
@@ -1795,26 +1796,53 @@ constexpr int kFewGradBlocks = 304;        // and of its backward pass
 constexpr int kLayoutSms = 152;            // the workspace's layout does not ask the device
 constexpr int kFewSmem = 200 << 10;        // dynamic shared memory the few-token kernels may take
 
-// Columns per piece, whole tiles.  Every piece is a launch whose last wave and ramp cost some
-// 20 us, so the backward pass takes what the rows of H and the sums of dH leave of kWorkBytes
-// for its two pieces of G: 8192 tokens x 768 ran in 1.54 ms with 48 Mi entries per piece and in
-// 1.53 with 96, 4096 tokens x 4096 in 7.41 and 7.23.
-int64_t piece_columns(const HeadShape& s, int64_t asked) {
-  int64_t c;
-  if (asked > 0) {
-    c = asked;
-  } else if (s.dtype == MFSDP_DTYPE_F32) {
-    c = std::max<int64_t>(kZElems / s.rows, 4096);
-  } else if (s.backward) {
-    const int64_t fixed = s.rows * s.pitch * (2 + 4);
-    c = std::max<int64_t>(std::max(kMinElems, (kWorkBytes - fixed) / 4) / s.rows, 4096);
-  } else if (s.copy_w) {
-    c = std::max<int64_t>(kZElems / s.pitch, 4096);
-  } else {
-    c = std::max<int64_t>(kPartBytes / (8 * s.rows) * 128, 4096);
+// Slices of dH that a piece of any width may get (head_shape cuts narrow pieces into fewer).  dH has
+// few tiles when there are few tokens: its contraction (the piece's columns) is cut until the tiles
+// fill the GPU, in one wave where the fp32 GEMM runs the slices alone (the bf16 launch has other
+// tiles too).
+int64_t most_splits(const HeadShape& s, int sms) {
+  const bool bf = s.dtype == MFSDP_DTYPE_BF16;
+  const int64_t units = bf ? sms / 2 : sms;
+  const int64_t tiles = cdiv(std::max<int64_t>(s.n, 1), bf ? kTile : 128) * cdiv(s.dim, kTile);
+  return std::max<int64_t>(1, std::min<int64_t>(bf ? cdiv(units, tiles) : units / tiles, kMaxSplits));
+}
+
+// Columns per piece, whole tiles: what a budget leaves for the buffers that grow with a piece, each
+// of them counted.  Every piece is a launch whose last wave and ramp cost some 20 us, so the
+// backward pass takes what the rows of H and the slices of dH leave of kWorkBytes: 8192 tokens x 768
+// ran in 1.54 ms with 48 Mi entries per piece and in 1.53 with 96, 4096 tokens x 4096 in 7.41 and
+// 7.23.  A piece takes kMinBytes, and kMinColumns, where that is more.
+// With few tokens a piece's Z has few tiles, so it is cut to whole waves of them (64 tokens x 4090
+// against 128256 copied bf16 rows, backward: 19456 columns, one wave, 1.84 ms, 24576 columns 1.97,
+// 32768 2.49, and 1.53 with the whole of W, 1 GB, copied); a wave of the fp32 GEMM's takes up to
+// half of W's bytes (64 tokens x 4096 against 128256 fp32 rows, both passes: 4.1 ms with all of W,
+// 2.1 GB, transposed at a time, 4.4 with half of that, 5.0 within kWorkBytes).
+int64_t piece_columns(const HeadShape& s, int64_t asked, int sms) {
+  const bool bf = s.dtype == MFSDP_DTYPE_BF16;
+  const int64_t es = bf ? 2 : 4, copy = s.copy_w ? s.pitch * es : 0, n = std::max<int64_t>(s.n, 1);
+  auto within = [&](int64_t budget) {
+    if (s.backward) {
+      // bf16: the copy of H and the slices; two pieces of G, two of a copied W.  fp32: H transposed
+      // too; Z, G transposed, and W transposed (where a copied W was)
+      const int64_t fixed = s.rows * s.pitch * (es * (bf ? 1 : 2) + 4 * most_splits(s, sms));
+      const int64_t column = bf ? 2 * (s.rows * es + copy) : (2 * s.rows + s.pitch) * es;
+      return std::max(budget - fixed, kMinBytes) / column;
+    }
+    // a half-tile's (max, sum) or Z, and a copied W
+    const int64_t bytes = bf ? kPartBytes : kZBytes;
+    return std::min(bytes / (bf ? cdiv(8 * s.rows, 128) : s.rows * es),
+                    s.copy_w ? (std::max(budget, kWorkBytes) - bytes) / copy : INT64_MAX);
+  };
+  int64_t c = asked;
+  if (asked == 0) {
+    c = within(kWorkBytes);
+    // columns of one wave of Z's tiles (256 x 256 per CTA pair, fp32 128 x 256 per CTA)
+    const int64_t wave = (bf ? sms / 2 / cdiv(n, kTile) : sms / cdiv(n, 128)) * kTile;
+    if (!bf) c = std::max(c, std::min(wave, within(s.vocab * s.pitch * es / 2)));
+    if (c < s.vocab && wave >= kMinColumns && c > wave) c -= c % wave;
+    c = std::max(c, kMinColumns);
   }
-  c = up(c, kTile);
-  return std::min(c, up(s.vocab, kTile));
+  return std::min(up(c, kTile), up(s.vocab, kTile));
 }
 
 // The few-token kernels are built for 1, 2 and 4 tokens.
@@ -1846,19 +1874,13 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
   if (s.few || s.core) s.copy_w = false;
   s.rows = up(std::max<int64_t>(n, 1), kTile);
   s.pitch = up(dim, 64);
-  s.piece = piece_columns(s, piece);
+  s.piece = piece_columns(s, piece, sms);
   s.pieces = cdiv(vocab, s.piece);
   s.splits = 1;
   s.buffers = 1;
   if (backward) {
-    // dH has few tiles when there are few tokens: cut its contraction (the piece's columns)
-    // until the tiles fill the GPU; a slice keeps at least 1024 columns
-    const int64_t units = bf ? sms / 2 : sms;
-    const int64_t tiles = cdiv(std::max<int64_t>(n, 1), bf ? kTile : 128) * cdiv(dim, kTile);
-    // (fp32: 128, its k-blocks are slower)
-    // (in one wave: the fp32 GEMM runs the slices alone; the bf16 launch has other tiles too)
-    s.splits = std::max<int64_t>(1, std::min({bf ? cdiv(units, tiles) : units / tiles,
-                                              s.piece / (bf ? 1024 : 128), (int64_t)kMaxSplits}));
+    // a slice keeps at least 1024 columns (fp32: 128, its k-blocks are slower)
+    s.splits = std::max<int64_t>(1, std::min(most_splits(s, sms), s.piece / (bf ? 1024 : 128)));
     s.kdh = up(cdiv(std::min(s.piece, vocab), s.splits), kBK);  // no slice of a whole piece is empty
     s.splits = cdiv(std::min(s.piece, vocab), s.kdh);
     if (s.core) {                          // two blocks per SM, slices of at least 128 columns
@@ -1923,7 +1945,8 @@ HeadLayout head_layout(const HeadShape& s) {
   const bool t32 = s.backward && !bf;        // fp32: transposed H, G piece and W piece
   l.ht = take(t32 ? s.pitch * s.rows * 4 : 0);
   l.gt = take(t32 ? s.piece * s.rows * 4 : 0);
-  l.wt = take(t32 ? s.pitch * s.piece * 4 : 0);
+  // (the transposed piece is made after the copied one's last use, in the same place)
+  l.wt = t32 && s.copy_w ? l.wcopy : take(t32 ? s.pitch * s.piece * 4 : 0);
   l.descs = take(bf ? 0 : (int64_t)sizeof(GemmDesc) * (s.pieces * (2 + s.splits)));
   l.total = off;
   return l;
