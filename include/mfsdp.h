@@ -673,8 +673,9 @@ int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_
  * columns, and its buffers some 130 MB.
  *   lse          as written by the forward pass;  dloss  fp32 [n_tokens].
  *   dhidden, dweight   of `dtype`, nullable, overwritten (rows of dropped tokens are zero).
- * With bf16 inputs g may be rounded to bf16 between its two products (relative 2^-8 an entry); sums
- * are fp32 and each gradient is rounded once.  dhidden may be hidden's buffer (same pitch).
+ * With bf16 inputs g may be rounded to bf16 between its two products (relative 2^-8 an entry).  What
+ * all rows of the weight have in common, which g's rows cancel, does not enter dhidden's error.
+ * Sums are fp32 and each gradient is rounded once.  dhidden may be hidden's buffer (same pitch).
  */
 int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,
                              const void* hidden, int64_t ld_hidden, const void* weight,

@@ -424,3 +424,42 @@ def test_other_stream_and_graph(dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert mfsdp.mfsdp_query_status() == 0
+
+
+@pytest.mark.parametrize("vocab,piece,pitch", [(8192, 0, 0), (8192, 2048, 0), (8001, 1024, 8),
+                                               (5000, 256, 3)])
+def test_common_part_of_the_weight_stays_out_of_dhidden(vocab, piece, pitch):
+    """W's rows share a part c, 20 times their spread.  A row of G sums to zero, so c cancels in dH =
+    G W, and an error dG of G (its rounding to bf16 among them) must not meet it:
+        |dH - ref| <= dG |W - c| + dG d + acc(V) |G| |W| + 2^-20 |G| |c| + 2^-8 |ref|
+    with dG as in this file's head, d = 5 / sqrt(128) of W's spread for a c estimated from some 128
+    rows, and the tensor cores' sum over V.  Labels are confident, so that G's largest entry is
+    rounded too."""
+    n, dim = 256, 64
+    gen = torch.Generator(device="cuda").manual_seed(vocab + piece)
+    spread = 2.0 / dim ** 0.5
+    rows = torch.randn(vocab, dim, generator=gen, device="cuda") * spread
+    common = torch.randn(dim, generator=gen, device="cuda") * 20 * spread
+    w = _mat(vocab, dim, "bf16", gen, 1.0, pitch)
+    w.copy_(rows + common)
+    lab = torch.randint(vocab, (n,), generator=gen, device="cuda")
+    h = (torch.randn(n, dim, generator=gen, device="cuda") + 0.6 / spread * rows[lab]).bfloat16()
+    dl = torch.ones(n, device="cuda")
+    dh = torch.empty_like(h)
+    _, _, dh, _ = _run(h, w, lab, dl, piece=piece, dh=dh)
+    H, W, L = _np(h), _np(w), lab.cpu().numpy()
+    _, lse = oracle.forward(H, W, L)
+    z = H @ W.T
+    dz = _acc(dim, "bf16") * (np.abs(H) @ np.abs(W).T)
+    dlse = dz.max(axis=1) + 2.0 ** -18 * (1 + np.abs(lse))
+    _, G = oracle.logit_gradient(H, W, L, _np(dl))
+    p = np.exp(z - lse[:, None])
+    assert 0.2 < p[np.arange(n), L].mean() < 0.9
+    rel = 2 * (dz.max(axis=1) + dlse)[:, None] + 2.0 ** -19 * (1 + np.abs(z) + np.abs(lse)[:, None])
+    dG = p * rel + np.abs(G) * 2.0 ** -8
+    ref, _ = oracle.backward(H, W, L, _np(dl))
+    c = W.mean(axis=0)
+    aG = np.abs(G) + dG
+    tol = dG @ (np.abs(W - c) + 5 / 128 ** 0.5 * W.std(axis=0)) + _acc(vocab, "bf16") * (aG @ np.abs(W))
+    tol += 2.0 ** -20 * aG.sum(axis=1, keepdims=True) * np.abs(c) + 2.0 ** -8 * np.abs(ref)
+    assert (np.abs(_np(dh) - ref) <= tol).all()
