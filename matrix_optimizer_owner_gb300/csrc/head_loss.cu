@@ -1937,9 +1937,16 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
                      (bf ? kCoreFlopsBf16 : kCoreFlops) / up(vocab, kCoreTile);
   // Few tokens, whose hidden rows (and sums) have to fit in shared memory.  Backward against the
   // other paths: 1 token x 2981 and 3264 fp32 rows 72 and 305 us, 4 x 768 and 50257 fp32 rows 233
-  // and 355, 4 x 70 and 7784 bf16 rows 30 and 44; bf16 that the tensor cores can read, 2 x 2048 and
-  // 32000 rows 124 and 165, 1 x 768 and 50257 116 and 105, 4 x 4096 and 128256 1150 and 798.
-  s.few = backward ? n >= 1 && n <= kFewTokens && (!bf || s.copy_w || n <= 2 || small) &&
+  // and 355, 4 x 70 and 7784 bf16 rows 30 and 44.
+  // bf16 that the tensor cores can read, both passes of one token (of two): 2048 and 128256 rows
+  // 349 and 428 (360 and 447) us, 1024 and 50257 100 and 132 (110 and 144), 256 and 50257 51 and 77,
+  // 768 and 32000 75 and 116, but 768 and 50257 115 and 109 (116 and 121), 512 and 128256 197 and
+  // 168 (196 and 182), 768 and 128256 258 and 207 (249 and 221), 640 and 80000 153 and 144 (152 and
+  // 154).  Between 256 and 1024 columns the rounds of loads are short and threads idle in the second
+  // phase, so there the tensor cores take large weights.  (4 x 4096 and 128256: 1150 and 798.)
+  const bool tensor = dim > 256 && dim < 1024 && dim * vocab > (n + 1) * (18 << 20);
+  s.few = backward ? n >= 1 && n <= kFewTokens &&
+                         (!bf || s.copy_w || small || (n <= 2 && !tensor)) &&
                          2 * up(dim, 8) * 4 * few_width(n) <= kFewSmem
                    : n <= (bf && !s.copy_w ? 1 : kFewTokens) &&
                          up(dim, 8) * 4 * kFewTokens <= kFewSmem;

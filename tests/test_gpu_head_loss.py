@@ -463,3 +463,12 @@ def test_common_part_of_the_weight_stays_out_of_dhidden(vocab, piece, pitch):
     tol = dG @ (np.abs(W - c) + 5 / 128 ** 0.5 * W.std(axis=0)) + _acc(vocab, "bf16") * (aG @ np.abs(W))
     tol += 2.0 ** -20 * aG.sum(axis=1, keepdims=True) * np.abs(c) + 2.0 ** -8 * np.abs(ref)
     assert (np.abs(_np(dh) - ref) <= tol).all()
+
+
+# one and two tokens on the tensor cores: widths between 256 and 1024 with large weights
+@pytest.mark.parametrize("n,dim,vocab", [(1, 640, 60000), (2, 768, 80000), (1, 960, 40001)])
+def test_few_tokens_backward_on_the_tensor_cores(n, dim, vocab):
+    h, w, lab, dl = _case(n, dim, vocab, "bf16", 0.0, seed=n + dim)
+    out = _run(h, w, lab, dl)
+    _verify(h, w, lab, dl, out)
+    assert all(torch.equal(a, b) for a, b in zip(_run(h, w, lab, dl), out))

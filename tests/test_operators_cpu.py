@@ -296,3 +296,17 @@ def test_head_loss_workspace_is_bounded(lib, dtype, n, dim, ld, vocab):
     columns = max(bound if copied else (64 if es == 2 else 128) << 20,
                   4096 * (rows + (pitch if copied else 0)) * es) * 17 // 16
     assert need(0, 0) <= rows * pitch * es + small + columns
+
+
+@pytest.mark.parametrize("n,dim,vocab,tensor", [
+    (1, 768, 50257, True), (1, 512, 128256, True), (1, 960, 50257, True), (2, 768, 128256, True),
+    (2, 768, 50257, False), (1, 768, 32000, False), (1, 256, 250000, False),
+    (1, 1024, 128256, False), (2, 4096, 128256, False), (3, 768, 8000, True)])
+def test_head_loss_few_token_backward_follows_its_measurements(lib, n, dim, vocab, tensor):
+    """Aligned bf16 rows: one pass over W (which needs the sums of 304 blocks only) or the tensor
+    cores (which need pieces of G), whichever was faster at these sizes."""
+    out = C.c_size_t(0)
+    assert lib.mfsdp_head_loss_workspace_bytes(n, dim, vocab, 1, 1, P, dim, 0, C.byref(out)) == 0
+    one_pass = 304 * n * dim * 4
+    assert (out.value > 2 * one_pass + (2 << 20)) == tensor
+    assert tensor or out.value <= one_pass + 1024
