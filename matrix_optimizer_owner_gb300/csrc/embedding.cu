@@ -11,8 +11,10 @@
 //               shared memory, and every warp then places its share in order.  Cluster barriers
 //               separate the steps, so the whole sort is one launch.  The sort is bound by
 //               latency, so the launch's other blocks meanwhile write zeros over the first
-//               kFillBytes of the gradient, about what fits in the sort's time.  Up to kRankMax
-//               tokens are not sorted: each one's place is counted, by blocks of their own.
+//               kFillBytes of the gradient, about what fits in the sort's time.  Where those are
+//               the whole table, up to kRankMax tokens are not sorted: each one's place is
+//               counted, by blocks of their own.  Where they are not, one block sorts up to
+//               kOneBlock tokens.
 //   2. sum      the sorted positions are cut into chunks of 16 or 32.  A chunk sums the runs
 //               of equal ids inside it in fp32 and writes each finished row once; a run that
 //               crosses a chunk boundary leaves fp32 partial rows in the workspace.  The work
@@ -34,7 +36,10 @@
 namespace mfsdp {
 namespace {
 
-constexpr int kSortBlocks = 8;              // cluster size
+constexpr int kSortBlocks = 8;              // cluster size beyond kOneBlock tokens
+// Tokens that one block sorts: 1 x 768 of 100000 rows 32 us and with the cluster 36, 300 x 768 33 and
+// 37, 512 x 2048 of 32000 31 and 34, 1000 x 768 38 both, 4096 x 768 40 and 38.
+constexpr int kOneBlock = 1024;
 // Tokens up to which places are counted (their square's comparisons) instead of sorted, where no
 // rows have to be marked: 1001 x 301 took 20 us so and 26 sorted, 3000 x 64 22 and 24, 4000 x 768
 // 28 both, 8192 x 768 50 and 34.
@@ -177,10 +182,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32
   return v;
 }
 
-// The first cluster sorts; the grid's other blocks write zeros.
+// B blocks sort (the first cluster where B > 1); the grid's other blocks write zeros.
+template <int B>
 __global__ void __launch_bounds__(kSortThreads)
     embedding_sort_kernel(const __grid_constant__ SortArgs p) {
-  constexpr int B = kSortBlocks;
+  auto barrier = [] {
+    if (B > 1) cluster_barrier(); else __syncthreads();
+  };
   extern __shared__ uint32_t sort_smem[];
   uint32_t* hist = sort_smem;                          // [warp][bin], then write positions
   uint32_t* total = hist + kSortWarps * kBinsMax;      // this block's digit totals
@@ -194,7 +202,7 @@ __global__ void __launch_bounds__(kSortThreads)
               (int64_t)(gridDim.x - B) * kSortThreads);
     return;
   }
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = B > 1 ? cluster_ctarank() : 0u;
   const int bins = 1 << p.digit;
   // every warp of the cluster owns one contiguous share of the positions; a short share's keys
   // stay in registers between counting and placing
@@ -258,14 +266,14 @@ __global__ void __launch_bounds__(kSortThreads)
       }
       total[tid] = s;
     }
-    cluster_barrier();
+    barrier();
     // digit b of this block starts after all smaller digits and the same digit of the blocks
     // before it
     uint32_t all = 0, before = 0;
     if (tid < bins) {
       uint32_t c[B];
 #pragma unroll
-      for (int q = 0; q < B; ++q) c[q] = ld_cluster_u32(total + tid, (uint32_t)q);
+      for (int q = 0; q < B; ++q) c[q] = B > 1 ? ld_cluster_u32(total + tid, (uint32_t)q) : total[tid];
 #pragma unroll
       for (int q = 0; q < B; ++q) {
         all += c[q];
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kSortThreads)
         place(i < i1, i < i1 ? key_at(i, false) : 0u, i < i1 ? val_at(i) : 0u);
       }
     }
-    cluster_barrier();   // the pass's output, and the peers' totals, before the next pass
+    barrier();   // the pass's output, and the peers' totals, before the next pass
   }
 }
 
@@ -672,25 +680,26 @@ cudaError_t run_forward(const EmbFwd& a, bool vec, int sms, cudaStream_t st) {
                     st, a);
 }
 
+template <int B>
 cudaError_t launch_sort(const SortArgs& a, int64_t fill_blocks, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(
-      embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+      embedding_sort_kernel<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kSortBlocks;
+  attr[1].val.clusterDim.x = B;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(kSortBlocks + cdiv(fill_blocks, kSortBlocks) * kSortBlocks));
+  cfg.gridDim = dim3((unsigned)(B + cdiv(fill_blocks, B) * B));   // whole clusters
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = kSortSmem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, embedding_sort_kernel, a);
+  cfg.numAttrs = B > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, embedding_sort_kernel<B>, a);
 }
 
 template <typename TD, typename TG, bool VEC, bool ACC>
@@ -875,7 +884,8 @@ extern "C" int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_to
     if (blocks > 0)
       e = launch_pdl(embedding_rank_kernel, dim3((unsigned)blocks), dim3(kSortThreads), 0, st, s);
   } else {
-    e = launch_sort(s, fill_blocks, st);
+    e = n_tokens <= kOneBlock && s.present ? launch_sort<1>(s, fill_blocks, st)
+                                           : launch_sort<kSortBlocks>(s, fill_blocks, st);
   }
   if (e == cudaSuccess && n_tokens > 0) {
     const bool db = dy_dtype == MFSDP_DTYPE_BF16, gb = grad_dtype == MFSDP_DTYPE_BF16;

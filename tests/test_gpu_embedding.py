@@ -249,3 +249,11 @@ def test_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(g2, g)
+
+
+# the same, sorted by one block (up to 1024 tokens) and by the cluster
+@pytest.mark.parametrize("n", [1, 31, 33, 500, 1023, 1024, 1025])
+@pytest.mark.parametrize("how", ["uniform", "one", "down"])
+def test_backward_few_tokens_of_a_large_table_sorted_by_one_block(n, how):
+    _check(n, 264, 170001, how, dy="bf16", grad="bf16", seed=n, padding=5,
+           index=torch.int32 if n % 2 else torch.int64)
