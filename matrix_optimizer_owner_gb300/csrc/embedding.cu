@@ -89,10 +89,12 @@ __global__ void __launch_bounds__(256) embedding_forward_kernel(const __grid_con
     id[i] = t[i] >= 0 ? load_index(p.ids, p.is64, t[i]) : 0;
   }
   Pack8<TT> a[U];
+  float scale[U];                          // 0 for a row of zeros, whatever the caller's scale is
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const bool ok = t[i] >= 0 && id[i] >= 0 && id[i] < p.vocab;
     if (t[i] >= 0 && !ok && c[i] == 0) atomicOr(p.status, kStatusBadIndex);
+    scale[i] = ok ? p.scale : 0.f;
     if (ok) a[i].load(static_cast<const TT*>(p.table) + id[i] * p.ld_table + c[i]); else a[i].zero();
   }
 #pragma unroll
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(256) embedding_forward_kernel(const __grid_con
     float v[8];
     a[i].get(v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= p.scale;
+    for (int j = 0; j < 8; ++j) v[j] *= scale[i];
     Pack8<TO> b;
     b.set(v);
     b.store(static_cast<TO*>(p.out) + t[i] * p.ld_out + c[i]);

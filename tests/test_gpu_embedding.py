@@ -257,3 +257,16 @@ def test_other_stream_and_graph():
 def test_backward_few_tokens_of_a_large_table_sorted_by_one_block(n, how):
     _check(n, 264, 170001, how, dy="bf16", grad="bf16", seed=n, padding=5,
            index=torch.int32 if n % 2 else torch.int64)
+
+
+@pytest.mark.parametrize("dim", [16, 17])                # rows of vectors, and others
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), -3.0])
+def test_forward_bad_ids_give_zeros_at_any_scale(dim, scale):
+    from matrix_optimizer_owner_gb300 import _lib, mfsdp
+    w = torch.ones(10, dim, device="cuda")
+    ids = torch.tensor([3, -1, 10], device="cuda")
+    o = torch.empty(3, dim, device="cuda")
+    mfsdp.mfsdp_embedding_forward(w, ids, scale, o)
+    assert not o[1:].any() and not torch.signbit(o[1:]).any()
+    assert torch.equal(o[:1], torch.full_like(o[:1], scale)) or o[:1].isnan().all()
+    assert _lib.STATUS_NAMES[mfsdp.mfsdp_query_status()] == "MFSDP_EINDEX"
