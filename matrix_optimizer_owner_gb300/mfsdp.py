@@ -574,6 +574,8 @@ def _workspace(ws, nbytes: int, like, dev: int, stream, raw: int):
     if ws is not None:
         if ws.get_device() != dev:
             raise ValueError("expected the workspace on the current CUDA device")
+        if not ws.is_contiguous():       # an expanded tensor has less memory than elements
+            raise ValueError(f"expected a contiguous workspace, got strides {ws.stride()}")
         return ws, ws.numel() * ws.element_size()
     if stream is None and nbytes <= _Scratch.LIMIT and not _is_capturing():
         return _scratch.get(nbytes, like, dev, raw), nbytes

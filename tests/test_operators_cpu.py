@@ -310,3 +310,14 @@ def test_head_loss_few_token_backward_follows_its_measurements(lib, n, dim, voca
     one_pass = 304 * n * dim * 4
     assert (out.value > 2 * one_pass + (2 << 20)) == tensor
     assert tensor or out.value <= one_pass + 1024
+
+
+def test_binding_refuses_a_workspace_with_less_memory_than_elements():
+    import torch
+
+    from matrix_optimizer_owner_gb300 import mfsdp
+    one = torch.empty(1, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="contiguous"):
+        mfsdp._workspace(one.expand(4096), 4096, one, one.get_device(), None, 0)
+    ws = torch.empty(4096, dtype=torch.float32)
+    assert mfsdp._workspace(ws, 4096, one, one.get_device(), None, 0) == (ws, 4 * 4096)
