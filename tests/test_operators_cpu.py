@@ -321,3 +321,22 @@ def test_binding_refuses_a_workspace_with_less_memory_than_elements():
         mfsdp._workspace(one.expand(4096), 4096, one, one.get_device(), None, 0)
     ws = torch.empty(4096, dtype=torch.float32)
     assert mfsdp._workspace(ws, 4096, one, one.get_device(), None, 0) == (ws, 4 * 4096)
+
+
+def test_kept_workspaces_are_bounded_and_can_be_released(monkeypatch):
+    import torch
+
+    from matrix_optimizer_owner_gb300 import mfsdp
+    monkeypatch.setattr(mfsdp, "_is_capturing", lambda: False)
+    monkeypatch.setattr(mfsdp, "_U8", torch.uint8)
+    monkeypatch.setattr(mfsdp, "_scratch", mfsdp._Scratch())
+    like, kept = torch.empty(1), mfsdp._scratch.buffers
+    for stream in range(20):
+        mfsdp._workspace(None, 100, like, 0, None, stream)
+        assert (0, stream) in kept and len(kept) <= 8
+    first = kept[(0, 19)][1]
+    assert mfsdp._workspace(None, 100, like, 0, None, 19)[0] is first
+    mfsdp._workspace(None, 2 << 20, like, 0, None, 12)       # a larger one replaces its own only
+    assert len(kept) == 8 and kept[(0, 12)][0] == 2 << 20 and kept[(0, 19)][1] is first
+    mfsdp.mfsdp_release_workspaces()
+    assert not kept
