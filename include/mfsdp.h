@@ -637,7 +637,7 @@ int mfsdp_embedding_backward(int64_t vocab, int64_t dim, int64_t n_tokens, int32
  * are what that call will be given (only their alignment is looked at: a weight whose rows do not
  * start on 16-byte boundaries is copied piece by piece); `piece` as below, 0 for the
  * forward pass, which needs a copy of hidden and, beside it, some 70 MB in bf16, 130 in fp32 and
- * 400 where the weight is copied (half an fp32 weight's bytes, or what 4096 columns take, where
+ * 400 where the weight is copied (up to an fp32 weight's bytes, or what 4096 columns take, where
  * that is more).
  */
 int mfsdp_head_loss_workspace_bytes(int64_t n_tokens, int64_t dim, int64_t vocab, int32_t dtype,
@@ -667,10 +667,10 @@ int mfsdp_head_loss_forward(int64_t n_tokens, int64_t dim, int64_t vocab, int32_
  * dloss[t] (0 for dropped tokens), recomputed in pieces of `piece` columns of the vocabulary
  * (rounded up to 256):
  *     dhidden = g weight,   dweight = g^T hidden
- * piece == 0 chooses them for a workspace of some 400 MB in all (half an fp32 weight's bytes where
- * that is more).  It is more where the parts that do not depend on the piece (a copy of hidden, two
- * in fp32, and the fp32 sums of dhidden) leave too little of that: a piece has at least 4096
- * columns, and its buffers some 130 MB.
+ * piece == 0 chooses them for a workspace of some 400 MB in all (in fp32 up to the weight's bytes
+ * where that is more and few tokens need wide pieces).  It is more where the parts that do not
+ * depend on the piece (a copy of hidden, two in fp32, and the fp32 sums of dhidden) leave too little
+ * of that: a piece has at least 4096 columns, and its buffers some 130 MB.
  *   lse          as written by the forward pass;  dloss  fp32 [n_tokens].
  *   dhidden, dweight   of `dtype`, nullable, overwritten (rows of dropped tokens are zero).
  * With bf16 inputs g may be rounded to bf16 between its two products (relative 2^-8 an entry).  What

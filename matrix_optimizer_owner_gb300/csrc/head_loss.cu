@@ -1849,7 +1849,7 @@ struct HeadLayout {
 
 constexpr int64_t kWorkBytes = 390ll << 20;   // what the backward pass's buffers may come to
 constexpr int64_t kMinBytes = 128ll << 20;   // least of them for a piece's columns
-constexpr int64_t kZBytes = 128ll << 20;     // fp32 forward: a piece of Z
+constexpr int64_t kZBytes = 128ll << 20;     // fp32: a piece of Z
 constexpr int64_t kPartBytes = 64ll << 20;   // bf16 forward: a piece's partials
 constexpr int64_t kMinColumns = 4096;        // least columns of a piece
 constexpr int kMaxSplits = 64;
@@ -1884,35 +1884,45 @@ int64_t most_splits(const HeadShape& s, int sms) {
 // backward pass takes what the rows of H and the slices of dH leave of kWorkBytes: 8192 tokens x 768
 // ran in 1.54 ms with 48 Mi entries per piece and in 1.53 with 96, 4096 tokens x 4096 in 7.41 and
 // 7.23.  A piece takes kMinBytes, and kMinColumns, where that is more.
-// With few tokens a piece's Z has few tiles, so it is cut to whole waves of them (64 tokens x 4090
-// against 128256 copied bf16 rows, backward: 19456 columns, one wave, 1.84 ms, 24576 columns 1.97,
-// 32768 2.49, and 1.53 with the whole of W, 1 GB, copied); a wave of the fp32 GEMM's takes up to
-// half of W's bytes (64 tokens x 4096 against 128256 fp32 rows, both passes: 4.1 ms with all of W,
-// 2.1 GB, transposed at a time, 4.4 with half of that, 5.0 within kWorkBytes).
+// With few tokens a piece's Z has few tiles and leaves most of the GPU idle unless the piece is wide.
+// An fp32 piece may therefore come to one wave of them within W's bytes, and a piece that does not
+// hold the vocabulary is cut to whole waves where that saves some (64 tokens x 4090 against 128256
+// copied bf16 rows, backward: one wave, 19456 columns, 1.84 ms, 24576 columns 1.97, 32768 2.49).
+// Holding all of a copied or transposed W would be faster by a few per cent and take its size in
+// memory (both passes: 64 x 4096 against 128256 fp32 rows 4.1 ms with 2.3 GB and 4.4 with 0.7, 39 x
+// 3143 against 110695 copied bf16 rows 1.6 with 0.8 GB and 1.8 with 0.4).
 int64_t piece_columns(const HeadShape& s, int64_t asked, int sms) {
   const bool bf = s.dtype == MFSDP_DTYPE_BF16;
-  const int64_t es = bf ? 2 : 4, copy = s.copy_w ? s.pitch * es : 0, n = std::max<int64_t>(s.n, 1);
-  auto within = [&](int64_t budget) {
-    if (s.backward) {
-      // bf16: the copy of H and the slices; two pieces of G (their row sums are 1 / 128 of them), two
-      // of a copied W.  fp32: H transposed too; Z, G transposed, and W transposed (where a copied W
-      // was)
-      const int64_t fixed = s.rows * s.pitch * (es * (bf ? 1 : 2) + 4 * most_splits(s, sms));
-      const int64_t column = bf ? 2 * (s.rows * es + copy) : (2 * s.rows + s.pitch) * es;
-      return std::max(budget - fixed, kMinBytes) / column;
-    }
+  const int64_t es = bf ? 2 : 4, copy = s.copy_w ? s.pitch * es : 0;
+  const int64_t weight = s.vocab * s.pitch * es;
+  // Z's tiles (256 x 256 per CTA pair, fp32 128 x 256 per CTA): rows of them, and the columns of a
+  // wave
+  const int64_t units = bf ? sms / 2 : sms;
+  const int64_t ntm = cdiv(std::max<int64_t>(s.n, 1), bf ? kTile : 128), wave = units / ntm * kTile;
+  int64_t c = asked;
+  if (asked == 0 && s.backward) {
+    // bf16: the copy of H and the slices; two pieces of G (their row sums are 1 / 128 of them), two
+    // of a copied W.  fp32: H transposed too; Z, G transposed, and W transposed (where a copied W
+    // was)
+    const int64_t fixed = s.rows * s.pitch * (es * (bf ? 1 : 2) + 4 * most_splits(s, sms));
+    const int64_t column = bf ? 2 * (s.rows * es + copy) : (2 * s.rows + s.pitch) * es;
+    c = std::max(kWorkBytes - fixed, kMinBytes) / column;
+    if (!bf)
+      c = std::min(std::max(c, std::min(wave, (weight - fixed) / column)), kZBytes / (s.rows * es));
+  } else if (asked == 0) {
     // a half-tile's (max, sum) or Z, and a copied W
     const int64_t bytes = bf ? kPartBytes : kZBytes;
-    return std::min(bytes / (bf ? cdiv(8 * s.rows, 128) : s.rows * es),
-                    s.copy_w ? (std::max(budget, kWorkBytes) - bytes) / copy : INT64_MAX);
-  };
-  int64_t c = asked;
+    c = bytes / (bf ? cdiv(8 * s.rows, 128) : s.rows * es);
+    if (s.copy_w)
+      c = std::min(c, std::max((kWorkBytes - bytes) / copy, bf ? 0 : std::min(wave, weight / copy)));
+  }
   if (asked == 0) {
-    c = within(kWorkBytes);
-    // columns of one wave of Z's tiles (256 x 256 per CTA pair, fp32 128 x 256 per CTA)
-    const int64_t wave = (bf ? sms / 2 / cdiv(n, kTile) : sms / cdiv(n, 128)) * kTile;
-    if (!bf) c = std::max(c, std::min(wave, within(s.vocab * s.pitch * es / 2)));
-    if (c < s.vocab && wave >= kMinColumns && c > wave) c -= c % wave;
+    auto waves = [&](int64_t c) {
+      return s.vocab / c * cdiv(ntm * cdiv(c, kTile), units) +
+             cdiv(ntm * cdiv(s.vocab % c, kTile), units);
+    };
+    const int64_t whole = wave > 0 ? c - c % wave : 0;
+    if (c < s.vocab && whole >= kMinColumns && waves(whole) < waves(c)) c = whole;
     c = std::max(c, kMinColumns);
   }
   return std::min(up(c, kTile), up(s.vocab, kTile));
@@ -1952,7 +1962,7 @@ HeadShape head_shape(int64_t n, int64_t dim, int64_t vocab, int32_t dtype, bool 
                          up(dim, 8) * 4 * kFewTokens <= kFewSmem;
   s.core = !s.few && small;
   if (s.few || s.core) s.copy_w = false;
-  s.rows = up(std::max<int64_t>(n, 1), kTile);
+  s.rows = up(std::max<int64_t>(n, 1), bf ? kTile : 32);   // (the fp32 GEMM takes any count)
   s.pitch = up(dim, 64);
   s.piece = piece_columns(s, piece, sms);
   s.pieces = cdiv(vocab, s.piece);

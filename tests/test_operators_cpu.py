@@ -276,10 +276,11 @@ def test_gemm_workspace_comes_from_the_stream_it_is_used_on(monkeypatch):
                                     (4095, 4095), (16384, 16384)])
 @pytest.mark.parametrize("vocab", [50257, 128256])
 def test_head_loss_workspace_is_bounded(lib, dtype, n, dim, ld, vocab):
-    """Whatever the rows' alignment: the backward pass 400 MiB (half of an fp32 W's bytes where that
-    is more), or what does not depend on the piece with 128 MiB or 4096 columns beside it; forward a
-    copy of hidden with 64 MiB (bf16), 128 MiB (fp32) or as much as backward (a copied W), or with
-    4096 columns.  A piece is rounded up to a whole tile, 1/16 of the least one."""
+    """Whatever the rows' alignment: the backward pass 400 MiB (an fp32 W's bytes, for one wave of
+    columns at most, where that is more), or what does not depend on the piece with 128 MiB or 4096
+    columns; forward a copy of hidden with 64 MiB (bf16) or 128 MiB (fp32), with a copied W 390 MiB or
+    a wave of an fp32 W's rows, or with 4096 columns.  A piece is rounded up to a whole tile, 1/16 of
+    the least one."""
     def need(backward, piece):
         out = C.c_size_t(0)
         assert lib.mfsdp_head_loss_workspace_bytes(n, dim, vocab, dtype, backward, P, ld, piece,
@@ -288,14 +289,19 @@ def test_head_loss_workspace_is_bounded(lib, dtype, n, dim, ld, vocab):
 
     rows, pitch, es = (n + 255) // 256 * 256, (dim + 63) // 64 * 64, 2 if dtype == 1 else 4
     copied = ld * es % 16 != 0
+    weight = vocab * pitch * es
     bound = 400 << 20
     if es == 4:
-        bound = max(bound, vocab * pitch * 2)
-    assert need(1, 0) <= max(bound * 17 // 16, need(1, 4096) * 17 // 16 + (128 << 20))
+        bound = max(bound, min(weight * 65 // 64, need(1, 152 * 256)))
+    assert need(1, 0) <= max(bound, need(1, 4096) * 17 // 16 + (128 << 20))
     small = 40 * rows + (1 << 20)                 # labels, statistics and the like
-    columns = max(bound if copied else (64 if es == 2 else 128) << 20,
-                  4096 * (rows + (pitch if copied else 0)) * es) * 17 // 16
-    assert need(0, 0) <= rows * pitch * es + small + columns
+    columns = 4096 * (rows + (pitch if copied else 0)) * es * 17 // 16
+    columns = max(columns, (64 if es == 2 else 128) << 20)
+    if copied:
+        columns = max(columns, 390 << 20)
+        if es == 4:
+            columns = max(columns, min(weight, 152 * 256 * pitch * 4) + (128 << 20))
+    assert need(0, 0) <= rows * pitch * es + small + columns * 65 // 64
 
 
 @pytest.mark.parametrize("n,dim,vocab,tensor", [
