@@ -32,15 +32,18 @@
 // (forward one and backward two, with bf16 inputs that TMA can read) take one pass over W in each
 // direction, without tensor cores.
 //
-// Training sizes are bound by the tensor cores: of the four products, forward's Z, its second
-// computation, dH and dW, the second costs the time that storing Z would cost in memory (8192 x
-// 50257 logits are 0.8 GB).  Measured (bf16, both passes, 1910 TFLOP/s being a large library
-// product's rate): 8192 tokens x 768 against 50257 rows in 1.5 ms, 1.69 PFLOP/s of the four
-// products; 3072 live tokens of 4096 x 4096 against 128256 rows in 7.1 to 7.5 ms, 1.7 to 1.8
-// PFLOP/s, where the power limit lowers the clock.  Forward alone runs at 1.85 and 2.0 PFLOP/s; a
-// piece of the backward pass at 768 keeps the tensor cores 79 % busy and moves 0.55 GB, the sums
-// of dH and the pieces of G, which stay in the L2 in part (71 % hits).  One token against 50257 x
-// 768 takes 15 us for W's 77 MB (5.0 TB/s; 11 us at a copy's rate).
+// Training sizes are bound by the tensor cores: four products, forward's Z, its second computation,
+// dH and dW.  The second costs 2 K / 1.9e15 s a logit, and storing Z in fp32 and reading it again 8
+// / 6.8e12: equal at a width K of 1100, so below it recomputing is the faster way.  Above it (4096
+// wide: 1.7 ms of products against 0.5 ms) keeping Z would be, for n x vocab x 4 bytes (1.6 GB) held
+// from one pass to the other, which these calls do not ask of the caller.  Measured (bf16, both
+// passes, 1910 TFLOP/s being a large library product's rate): 8192 tokens x 768 against 50257 rows
+// in 1.57 ms, 1.72 when called back to back, 1.6 and 1.5 PFLOP/s of the four products; 3072 live
+// tokens of 4096 x 4096 against 128256 rows in 7.4 to 7.8 ms, 1.65 to 1.75 PFLOP/s, where the power
+// limit lowers the clock.  Forward alone runs at 1.85 and 2.0 PFLOP/s; a piece of the backward pass
+// at 768 keeps the tensor cores 78 % busy and reads 0.55 GB, the sums of dH and the pieces of G,
+// which stay in the L2 in part (72 % hits).  One token against 50257 x 768 takes 19 us for W's 77
+// MB where W comes from memory (4.0 TB/s; 11 us at a copy's rate), 14 where it is in the L2.
 #include <algorithm>
 #include <atomic>
 #include <cstring>
