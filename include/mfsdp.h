@@ -686,6 +686,82 @@ int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab, int32
                              void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Operators of linear layers trained in 8 bits: what computes the matrices' gradients that
+ * mfsdp_owner_reduce_momentum takes as contributions, with the operands of the products in
+ * 8-bit floating point.  The paper has no counterpart to them.
+ *
+ * What is said above of all operators holds here (row-major with a pitch, fp32 arithmetic, one
+ * rounding to nearest even, fixed order of sums, capture, errors), and for 8-bit matrices:
+ *   value = q 2^(s - 127):  q e4m3 (largest 448) or e5m2 (largest 57344), s one byte per group.
+ *   groups      ROW: 128 consecutive values of a row (the last group of a row may be shorter),
+ *               scales [rows x ceil(cols / 128)]; COL: 128 consecutive values of a column, scales
+ *               [ceil(rows / 128) x cols]; TILE: 128 x 128 values.  Groups start at multiples of
+ *               128 of the matrix.
+ *   data        16-byte aligned, with a pitch `ld` that is a multiple of 16 (else MFSDP_EALIGN).
+ *               Bytes of a row past its last column are neither read for their value nor written.
+ *   writing     s is the least one (from 0) for which the group's largest finite magnitude is at
+ *               most the type's largest value, so nothing saturates; infinities and NaN become NaN
+ *               of their own element and leave the others alone.
+ *   reading     s = 255 makes its group NaN.
+ * ------------------------------------------------------------------------------------------ */
+
+typedef enum { MFSDP_FP8_E4M3 = 0, MFSDP_FP8_E5M2 = 1 } mfsdp_fp8_dtype;
+typedef enum { MFSDP_GROUPS_ROW = 0, MFSDP_GROUPS_COL = 1, MFSDP_GROUPS_TILE = 2 } mfsdp_groups;
+
+typedef struct {
+  void* data;        /* [rows x cols] bytes, pitch ld */
+  int64_t ld;
+  void* scales;      /* bytes, pitch ld_scales */
+  int64_t ld_scales;
+  int32_t dtype;     /* mfsdp_fp8_dtype */
+  int32_t groups;    /* mfsdp_groups */
+} mfsdp_fp8_matrix;
+
+/*
+ * An f32 or bf16 matrix x [rows x cols] in 8 bits.  `out` is of any grouping; `also` (nullable) is a
+ * second result from the same read, a COL one beside a ROW one (or the other way round): the two
+ * operands that a gradient or an activation is in a training step.  rows == 0 is no work.  rows,
+ * cols < 2^31.
+ */
+int mfsdp_quantize_fp8(int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t ld_x,
+                       const mfsdp_fp8_matrix* out, const mfsdp_fp8_matrix* also, void* stream);
+
+/*
+ * The same from an 8-bit matrix of any grouping: an activation that was kept as a product's operand
+ * (ROW) becomes the operand of its weight's gradient (COL).  Of the same type, only values that
+ * become subnormal under their new group's scale are rounded.  The results must not be the source's
+ * buffers.
+ */
+int mfsdp_regroup_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_matrix* src,
+                      const mfsdp_fp8_matrix* out, const mfsdp_fp8_matrix* also, void* stream);
+
+/* The values of an 8-bit matrix in f32 or bf16 (exact in both above their subnormals; what is beyond
+ * their range, as fp32's largest value is when it is rounded to 8 bits, becomes infinity). */
+int mfsdp_dequantize_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_matrix* src, int32_t dtype,
+                         void* out, int64_t ld_out, void* stream);
+
+/* Workspace of mfsdp_gemm_fp8: 0 unless few tiles of C make it split the contraction. */
+int mfsdp_gemm_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t* bytes_out);
+
+/*
+ * C = op(A) op(B), or C += op(A) op(B) with `accumulate`: op(A) [m x k], op(B) [k x n] of 8-bit
+ * matrices, C [m x n] of c_dtype (f32 or bf16).
+ *   trans_a     0: A is stored [m x k], 1: [k x m];  trans_b  0: B is stored [k x n], 1: [n x k].
+ *   groups      a scale has to be shared along the contraction: ROW or TILE where it runs along the
+ *               stored rows (trans_a = 0, trans_b = 1), COL or TILE where it runs down the columns
+ *               (else MFSDP_EINVAL).  The types of A and B are independent.
+ * A linear layer y = x W^T (W [out x in], TILE) takes x ROW and trans_b = 1 forward, dy ROW and W as
+ * it is for dx = dy W, and dy COL and x COL with trans_a = 1 for dW = dy^T x.
+ * Products run on the tensor cores (block-scaled) with fp32 accumulation; sums kept in fp32 are added
+ * up outside them every 1024 of k.  k == 0 writes zeros (or leaves C as it is).  m, n or k up to
+ * 2^31 - 513.  `workspace` may be NULL where mfsdp_gemm_fp8_workspace_bytes gives 0.
+ * A device wait that runs out sets MFSDP_ETIMEOUT in the status word.
+ */
+int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_matrix* a, int32_t trans_a,
+                   const mfsdp_fp8_matrix* b, int32_t trans_b, int32_t accumulate, int32_t c_dtype,
+                   void* c, int64_t ld_c, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------------------------ */
 

@@ -50,6 +50,11 @@ class GemmProblem(C.Structure):
                 ("ldc", C.c_int32), ("alpha", C.c_float), ("beta", C.c_float)]
 
 
+class Fp8Struct(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("ld", C.c_int64), ("scales", C.c_void_p),
+                ("ld_scales", C.c_int64), ("dtype", C.c_int32), ("groups", C.c_int32)]
+
+
 class CostModel(C.Structure):
     _fields_ = [("param_bytes", C.c_int32), ("grad_bytes", C.c_int32),
                 ("state_bytes", C.c_int32), ("ns_steps", C.c_int32)]
@@ -128,6 +133,15 @@ SIGNATURES = {
     "mfsdp_head_loss_backward": (C.c_int, [_i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _i32,
                                            _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                            C.c_size_t, _vp]),
+    "mfsdp_quantize_fp8": (C.c_int, [_i64, _i64, _i32, _vp, _i64, C.POINTER(Fp8Struct),
+                                     C.POINTER(Fp8Struct), _vp]),
+    "mfsdp_regroup_fp8": (C.c_int, [_i64, _i64, C.POINTER(Fp8Struct), C.POINTER(Fp8Struct),
+                                    C.POINTER(Fp8Struct), _vp]),
+    "mfsdp_dequantize_fp8": (C.c_int, [_i64, _i64, C.POINTER(Fp8Struct), _i32, _vp, _i64, _vp]),
+    "mfsdp_gemm_fp8_workspace_bytes": (C.c_int, [_i64, _i64, _i64, C.POINTER(C.c_size_t)]),
+    "mfsdp_gemm_fp8": (C.c_int, [_i64, _i64, _i64, C.POINTER(Fp8Struct), _i32,
+                                 C.POINTER(Fp8Struct), _i32, _i32, _i32, _vp, _i64, _vp,
+                                 C.c_size_t, _vp]),
     "mfsdp_query_status": (C.c_int, [_vp, C.POINTER(_i32)]),
     "mfsdp_status_string": (C.c_char_p, [C.c_int]),
     "mfsdp_set_wait_limit_ns": (C.c_int, [_u64]),

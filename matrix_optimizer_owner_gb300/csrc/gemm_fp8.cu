@@ -1,0 +1,1056 @@
+// Products of 8-bit matrices with a power-of-two scale per 128 of the contraction:
+//     C = op(A) op(B),  C_mn = sum_b 2^(sa_mb + sb_nb) sum_{k in block b} qa_mk qb_kn   (fp32 sums)
+// on the tensor cores' block-scaled form (tcgen05.mma kind::mxf8f6f4): the products of a block are
+// scaled while they are added up, so a tile's accumulator stays in tensor memory over the whole
+// contraction and nothing is read back between blocks.  That form wants a scale byte per row and 32
+// of k; a byte serves the four instructions of a block of 128, and the four bytes of a 32-bit word
+// four blocks, picked by the instruction's scale id.
+//
+// An operand whose contraction runs down its columns (both of the weight's gradient, the weight of
+// the input's gradient) is read as it lies: the tensor cores take it MN-major, no copy is transposed.
+#include <algorithm>
+#include <atomic>
+
+#include "fp8.cuh"
+#include "umma.cuh"
+
+namespace mfsdp {
+
+namespace {
+
+constexpr int kB8 = 128;                    // k of a pipeline stage and of a scale
+constexpr uint32_t kBox8 = 128 * 128;       // one operand box: 128 rows of 128 bytes
+
+// ---------------------------------------------------------------- operands
+// K-major: rows of 128 k-bytes, eight-row swizzle atoms 1024 bytes apart, the k-step j of 32 starts
+// 32 bytes further.  MN-major: 128 output indices a row, one k a row; the k-step j starts 32 rows
+// further.
+__device__ __forceinline__ uint64_t operand_desc8(uint32_t base, int mn_major, int j) {
+  return mn_major ? smem_desc(base + (uint32_t)j * 4096u, kBox8, 1024u)
+                  : smem_desc(base + (uint32_t)j * 32u, 16u, 1024u);
+}
+// Scale words: 32 rows of 16 bytes, unswizzled (eight rows 128 bytes apart from the next eight).
+__device__ __forceinline__ uint64_t scale_desc(uint32_t base) {
+  return (uint64_t)((base >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
+}
+// Instruction descriptor, kind::mxf8f6f4: B's scale id (bits 4-5), the types of A (7-9) and B (10-12;
+// e4m3 0, e5m2 1), A / B MN-major (15 / 16), N >> 3 (17-22), e8m0 scales (23), M >> 4 (24-28), A's
+// scale id (29-30).
+__host__ __device__ constexpr uint32_t idesc8(int a_e5m2, int b_e5m2, int a_mn, int b_mn, int m,
+                                              int n) {
+  return ((uint32_t)a_e5m2 << 7) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)a_mn << 15) |
+         ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t with_scale_id(uint32_t idesc, int id) {
+  return idesc | ((uint32_t)id << 4) | ((uint32_t)id << 29);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                     uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if (CTAS == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// 512 bytes of scale words into four columns, the same for all four lane quarters.
+template <int CTAS>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  if (CTAS == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+// Arrival on the pair leader's barrier that publishes this CTA's shared memory to the leader's
+// thread (which hands it to the tensor cores).
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- scales
+struct ScaleArgs {
+  const uint8_t* s;
+  int64_t sr, sk;             // bytes between rows' groups and between blocks of k
+  int32_t shift;              // 7: a scale serves 128 rows
+  int32_t word;               // four blocks' bytes lie in an aligned word
+};
+// The scale bytes of blocks kb .. kb + 3 of one row; 1 past the end (where the operand is zero).
+__device__ __forceinline__ uint32_t scale_word(const ScaleArgs& p, int64_t row, int64_t rows, int kb,
+                                               int nkb) {
+  if (row >= rows) return 0x7F7F7F7Fu;
+  const uint8_t* s = p.s + (row >> p.shift) * p.sr + (int64_t)kb * p.sk;
+  if (p.word && (kb & 3) == 0 && kb + 4 <= nkb) return *reinterpret_cast<const uint32_t*>(s);
+  uint32_t w = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w |= (kb + j < nkb ? (uint32_t)s[j * p.sk] : 127u) << (8 * j);
+  return w;
+}
+
+struct Gemm8Args {
+  CUtensorMap a, b;
+  ScaleArgs sa, sb;
+  int32_t m, n, nkb;          // C's sizes and the blocks of k
+  int32_t a_mn, b_mn;
+  uint32_t idesc;
+  int32_t tiles_m, tiles_n, splits, kb_split;
+  int32_t chunk;              // blocks added up in tensor memory before registers take over
+  void* c;
+  int64_t ld_c;
+  int32_t c_bf16, accumulate, vec;
+  float* part;                // splits > 1: [splits][m][ld_part]
+  int64_t ld_part;
+  int64_t sw, st;             // narrow kernel: C's strides along the wide and the narrow side
+  uint64_t wait_limit_ns;
+  int* status;
+};
+
+// ---------------------------------------------------------------- 256 x 256 tiles
+constexpr int kPairThreads = 352;           // warp 0 TMA, 1 MMA, 2 scales, 3-10 epilogue
+constexpr int kEpi0 = 3, kEpiN = 8;
+constexpr int kStages8 = 6;
+constexpr uint32_t kStageBytes8 = 2 * kBox8;
+constexpr int kSfStages = 3;
+constexpr uint32_t kSfBytes = 3 * 512;      // A's 128 rows and B's 256
+constexpr uint32_t kStg8 = kStages8 * kStageBytes8;
+constexpr uint32_t kSf8 = kStg8 + kEpiN * 2048;
+constexpr uint32_t kBars8 = kSf8 + kSfStages * kSfBytes;
+constexpr uint32_t kPairSmem = 1024 + kBars8 + 256;
+static_assert(kPairSmem <= 227 * 1024, "shared memory");
+// Tensor memory: two accumulators of 256 columns and the scales do not fit 512 columns, so the
+// accumulators share the 32 columns 224-255 (the last of the first one, the first of the second).
+// The epilogue reads the shared columns of a tile first and says so, and the next tile's products
+// wait for that alone.
+constexpr uint32_t kAcc1 = 224, kSfCol = 480;
+constexpr int kRasterRows = 8;              // tile rows that walk the columns together
+
+struct PairItem {
+  int tm, tn, split, kb0, nk;
+};
+__device__ __forceinline__ PairItem pair_item(const Gemm8Args& P, int w) {
+  PairItem t;
+  const int tiles = P.tiles_m * P.tiles_n;
+  t.split = w / tiles;
+  const int i = w - t.split * tiles;
+  const int per = kRasterRows * P.tiles_n, group = i / per;
+  const int rows = min(kRasterRows, P.tiles_m - group * kRasterRows);
+  const int j = i - group * per;
+  t.tm = group * kRasterRows + j % rows;
+  t.tn = j / rows;
+  t.kb0 = t.split * P.kb_split;
+  t.nk = min(P.kb_split, P.nkb - t.kb0);
+  return t;
+}
+
+// A staged block of 32 rows x 64 bytes (32 bf16 or 16 fp32 columns) to C or to a split's partial sums.
+struct BlockOut {
+  const Gemm8Args& P;
+  int64_t r0;                 // the block's first row
+  int lane;
+  float* part;                // nullable
+
+  __device__ __forceinline__ void store(uint32_t stg, int64_t c0) const {
+    const bool f32 = part || !P.c_bf16;
+    const int per = f32 ? 4 : 8, width = f32 ? 16 : 32;
+    if (part ? true : P.vec) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2), k = lane & 3;
+        const int64_t r = r0 + row, c = c0 + k * per;
+        if (r >= P.m || c >= P.n) continue;
+        const uint4 w = lds128(stg + stg_off(row, k));
+        if (part) {           // rows of whole vectors
+          *reinterpret_cast<uint4*>(part + r * P.ld_part + c) = w;
+        } else if (c + per <= P.n) {
+          uint4* d = f32 ? reinterpret_cast<uint4*>(static_cast<float*>(P.c) + r * P.ld_c + c)
+                         : reinterpret_cast<uint4*>(static_cast<bf16_t*>(P.c) + r * P.ld_c + c);
+          *d = w;
+        } else {
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          for (int j = 0; c + j < P.n; ++j) {
+            if (f32)
+              static_cast<uint32_t*>(P.c)[r * P.ld_c + c + j] = j == 0 ? u[0] : j == 1 ? u[1] : u[2];
+            else
+              static_cast<uint16_t*>(P.c)[r * P.ld_c + c + j] = (uint16_t)(
+                  ((j >> 1) == 0 ? u[0] : (j >> 1) == 1 ? u[1] : (j >> 1) == 2 ? u[2] : u[3]) >>
+                  (16 * (j & 1)));
+          }
+        }
+      }
+    } else {                  // a row of the block at a time, a lane a column
+      for (int i = 0; i < 32; ++i) {
+        const int64_t r = r0 + i, c = c0 + lane;
+        if (r >= P.m || lane >= width || c >= P.n) continue;
+        if (f32)
+          static_cast<uint32_t*>(P.c)[r * P.ld_c + c] = lds32(stg + stg_off(i, lane >> 2) + (lane & 3) * 4);
+        else
+          static_cast<uint16_t*>(P.c)[r * P.ld_c + c] = (uint16_t)(
+              lds32(stg + stg_off(i, lane >> 3) + (uint32_t)((lane & 6) * 2)) >> (16 * (lane & 1)));
+      }
+    }
+  }
+};
+
+// What C held, for this lane's row and 32 columns (added before the rounding).
+__device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c0, float (&v)[32]) {
+  if (r >= P.m) return;
+  if (P.vec && c0 + 32 <= P.n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float o[8];
+      if (P.c_bf16) {
+        Pack8<bf16_t> q;
+        q.load(static_cast<const bf16_t*>(P.c) + r * P.ld_c + c0 + 8 * k);
+        q.get(o);
+      } else {
+        Pack8<float> q;
+        q.load(static_cast<const float*>(P.c) + r * P.ld_c + c0 + 8 * k);
+        q.get(o);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * k + j] += o[j];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (c0 + k < P.n)
+        v[k] += P.c_bf16 ? to_f32(static_cast<const bf16_t*>(P.c)[r * P.ld_c + c0 + k])
+                         : static_cast<const float*>(P.c)[r * P.ld_c + c0 + k];
+  }
+}
+
+// CHUNKED: a tile's contraction is cut into chunks that are added up in registers.
+template <bool CHUNKED>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ Gemm8Args P) {
+  constexpr int S = kStages8, F = kSfStages;
+  extern __shared__ uint8_t smem_raw[];
+  pdl_launch();
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBars8);
+  // full[S] | empty[S] | sf_full[F] | sf_empty[F] | sf_free[2] | tfull[2] | tempty[2] | early[2] | drain
+  constexpr int full0 = 0, empty0 = S, sf_full0 = 2 * S, sf_empty0 = 2 * S + F,
+                sf_free0 = 2 * S + 2 * F, tfull0 = sf_free0 + 2, tempty0 = tfull0 + 2,
+                early0 = tempty0 + 2, drain = early0 + 2;
+  static_assert((drain + 2) * 8 <= 256, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar(full0 + s), 1);
+      mbar_init(bar(empty0 + s), 1);
+    }
+    for (int s = 0; s < F; ++s) {
+      mbar_init(bar(sf_full0 + s), 2);
+      mbar_init(bar(sf_empty0 + s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar(sf_free0 + a), 1);
+      mbar_init(bar(tfull0 + a), 1);
+      mbar_init(bar(tempty0 + a), 2 * kEpiN);
+      mbar_init(bar(early0 + a), 2 * (kEpiN / 2));
+    }
+    mbar_init(bar(drain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  pdl_wait();
+  const uint32_t tmem_base = *tmem_slot;
+  uint32_t peer_base;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(peer_base)
+               : "r"(map_rank(smem_u32(tmem_slot), rank ^ 1u))
+               : "memory");
+  const bool usable = peer_base == tmem_base;
+  if (!usable && threadIdx.x == 0) atomicOr(P.status, kStatusTmemMismatch);
+  const Guard g{abort_flag, P.wait_limit_ns, P.status};
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int items = P.tiles_m * P.tiles_n * P.splits;
+
+  if (!usable) {
+    // nothing runs: fall through to the teardown
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 1, armed = 0, last_par = 0;
+      bool ok = true;
+      for (int w = pair; w < items && ok; w += npairs) {
+        const PairItem t = pair_item(P, w);
+        const int a0 = t.tm * 256 + 128 * (int)rank, b0 = t.tn * 256 + 128 * (int)rank;
+        for (int kb = t.kb0; kb < t.kb0 + t.nk; ++kb) {
+          if (!mbar_wait(bar(empty0 + stage), ph, g)) { ok = false; break; }
+          const uint32_t fb_local = bar(full0 + stage), fb = map_rank(fb_local, 0);
+          const uint32_t dst = sbase + (uint32_t)stage * kStageBytes8;
+          const int k0 = kb * kB8;
+          expect_tx_p(leader, fb_local, 2u * kStageBytes8);
+          tma_load_pair_p(true, dst, &P.a, P.a_mn ? a0 : k0, P.a_mn ? k0 : a0, fb);
+          tma_load_pair_p(true, dst + kBox8, &P.b, P.b_mn ? b0 : k0, P.b_mn ? k0 : b0, fb);
+          armed |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | ((ph ^ 1u) << stage);
+          if (++stage == S) { stage = 0; ph ^= 1u; }
+        }
+      }
+      // teardown: the leader's full barriers count both CTAs' bytes
+      if (leader)
+        for (int st = 0; st < S; ++st)
+          if (armed & (1u << st)) mbar_wait(bar(full0 + st), (last_par >> st) & 1u, g, false);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    if (lane == 0 && leader) {
+      int stage = 0, sf = 0, acc = 0, buf = 0;
+      uint32_t phase = 0, sf_phase = 0, acc_phase = 0, buf_phase = 1;
+      bool ok = true, first = true;
+      for (int w = pair; w < items && ok; w += npairs) {
+        const PairItem t = pair_item(P, w);
+        const int chunk = CHUNKED ? P.chunk : t.nk;
+        for (int kb = 0; kb < t.nk && ok; ++kb) {
+          const int in_chunk = CHUNKED ? kb % chunk : kb;
+          if (in_chunk == 0) {
+            if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g)) { ok = false; break; }
+            // the columns shared with the accumulator before this one
+            if (!first && !mbar_wait_cl(bar(early0 + (acc ^ 1)), acc ? acc_phase : acc_phase ^ 1u, g)) {
+              ok = false;
+              break;
+            }
+            first = false;
+            tc_fence_after();
+          }
+          const uint32_t sfa = tmem_base + kSfCol + (uint32_t)buf * 16u, sfb = sfa + 4u;
+          if ((kb & 3) == 0) {
+            // the scales of four blocks, into the columns that the last but one group has left
+            if (!mbar_wait_cl(bar(sf_full0 + sf), sf_phase, g) ||
+                !mbar_wait(bar(sf_free0 + buf), buf_phase, g)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t src = sbase + kSf8 + (uint32_t)sf * kSfBytes;
+            copy_scales<2>(sfa, scale_desc(src));
+            copy_scales<2>(sfb, scale_desc(src + 512u));
+            copy_scales<2>(sfb + 4u, scale_desc(src + 1024u));
+            tc_commit_pair(bar(sf_empty0 + sf), 0x3);
+            if (++sf == F) { sf = 0; sf_phase ^= 1u; }
+          }
+          if (!mbar_wait(bar(full0 + stage), phase, g)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d = tmem_base + (acc ? kAcc1 : 0u);
+          const uint32_t sm_a = sbase + (uint32_t)stage * kStageBytes8;
+          const uint32_t idesc = with_scale_id(P.idesc, kb & 3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma8<2>(d, operand_desc8(sm_a, P.a_mn, j), operand_desc8(sm_a + kBox8, P.b_mn, j), idesc,
+                    sfa, sfb, (in_chunk | j) != 0);
+          tc_commit_pair(bar(empty0 + stage), 0x3);
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+          if ((kb & 3) == 3 || kb + 1 == t.nk) {
+            tc_commit_pair(bar(sf_free0 + buf), 0x1);
+            buf ^= 1;
+            if (buf == 0) buf_phase ^= 1u;
+          }
+          if (in_chunk + 1 == chunk || kb + 1 == t.nk) {
+            tc_commit_pair(bar(tfull0 + acc), 0x3);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+          }
+        }
+      }
+      tc_commit_pair(bar(drain), 0x1);
+      mbar_wait(bar(drain), 0u, g, false);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales (both CTAs)
+    // A lane gathers the words of rows lane, lane + 32, ...: 16 bytes of each 128-row block.
+    int sf = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int w = pair; w < items && ok; w += npairs) {
+      const PairItem t = pair_item(P, w);
+      const int64_t a0 = (int64_t)t.tm * 256 + 128 * rank + lane, b0 = (int64_t)t.tn * 256 + lane;
+      for (int kb = 0; kb < t.nk; kb += 4) {
+        uint32_t v[12];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = scale_word(P.sa, a0 + 32 * j, P.m, t.kb0 + kb, P.nkb);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[4 + j] = scale_word(P.sb, b0 + 32 * j, P.n, t.kb0 + kb, P.nkb);
+        if (!mbar_wait(bar(sf_empty0 + sf), ph, g)) { ok = false; break; }
+        const uint32_t dst = sbase + kSf8 + (uint32_t)sf * kSfBytes + (uint32_t)lane * 16u;
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          sts128(dst + 512u * j, make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_leader(map_rank(bar(sf_full0 + sf), 0));
+        if (++sf == F) { sf = 0; ph ^= 1u; }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    // Warp w covers TMEM lane quarter (w & 3), 32 rows of the CTA's 128, and 128 columns.
+    const int quarter = warp & 3, half = (warp - kEpi0) >> 2;
+    const uint32_t stg = sbase + kStg8 + (uint32_t)(warp - kEpi0) * 2048u;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int w = pair; w < items && ok; w += npairs) {
+      const PairItem t = pair_item(P, w);
+      const int64_t rw = (int64_t)t.tm * 256 + 128 * rank + quarter * 32;
+      const int64_t cb = (int64_t)t.tn * 256 + half * 128;
+      const int nq = rw < P.m && cb < P.n ? (int)min((int64_t)4, (P.n - cb + 31) / 32) : 0;
+      float* part = P.splits > 1 ? P.part + (int64_t)t.split * P.m * P.ld_part : nullptr;
+      const BlockOut out{P, rw, lane, part};
+      const bool old = P.accumulate && !part;
+      auto put = [&](int q, const uint32_t (&a)[32]) {
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(a[k]);
+        const int64_t c0 = cb + 32 * q;
+        if (old) add_old(P, rw + lane, c0, v);
+        if (!part && P.c_bf16) {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sts128(stg + stg_off(lane, k),
+                   make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                              pack_bf16x2(v[8 * k + 4], v[8 * k + 5]),
+                              pack_bf16x2(v[8 * k + 6], v[8 * k + 7])));
+          __syncwarp();
+          out.store(stg, c0);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sts128(stg + stg_off(lane, k),
+                     make_uint4(__float_as_uint(v[16 * h + 4 * k]), __float_as_uint(v[16 * h + 4 * k + 1]),
+                                __float_as_uint(v[16 * h + 4 * k + 2]),
+                                __float_as_uint(v[16 * h + 4 * k + 3])));
+            __syncwarp();
+            out.store(stg, c0 + 16 * h);
+          }
+        }
+      };
+      // the shared columns: this warp's chunk `sh` of this accumulator, if it holds them
+      auto shared_chunk = [&]() { return acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1); };
+      auto base = [&]() {
+        return tmem_base + ((uint32_t)(quarter * 32) << 16) + (acc ? kAcc1 : 0u) +
+               (uint32_t)(half * 128);
+      };
+      auto release = [&](int which) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(bar(which + acc), 0));
+      };
+      if (CHUNKED) {
+        float sum[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sum[q][k] = 0.f;
+        for (int left = t.nk; left > 0; left -= P.chunk) {
+          if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) { ok = false; break; }
+          tc_fence_after();
+          const int sh = shared_chunk();
+          auto add = [&](int q) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[16];
+              asm volatile(
+                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+                  "%10, %11, %12, %13, %14, %15}, [%16];\ntcgen05.wait::ld.sync.aligned;\n"
+                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                    "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                    "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                  : "r"(base() + (uint32_t)(32 * q + 16 * h))
+                  : "memory");
+#pragma unroll
+              for (int k = 0; k < 16; ++k) sum[q][16 * h + k] += __uint_as_float(r[k]);
+            }
+          };
+          if (sh == 3) {                                  // warp-uniform
+            add(3);
+            release(early0);
+            add(0);
+          } else {
+            add(0);
+            if (sh == 0) release(early0);
+          }
+          add(1);
+          add(2);
+          if (sh != 3) add(3);
+          release(tempty0);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < nq) {
+            uint32_t a[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(sum[q][k]);
+            put(q, a);
+          }
+      } else {
+        if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
+        tc_fence_after();
+        const int sh = shared_chunk();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int q = sh == 3 ? (i + 3) & 3 : i;        // the shared columns first
+          uint32_t a[32];
+          if (q < nq || q == sh) {
+            tc_ld32_issue(base() + (uint32_t)(32 * q), a);
+            tc_ld_wait(a);
+          }
+          if (q == sh) release(early0);
+          if (i == 3) release(tempty0);                   // the last read: the stores can follow it
+          if (q < nq) put(q, a);
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while its peer may still use its memory
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- partial sums
+struct JoinArgs8 {
+  const float* part;
+  int64_t m, n, ld_part, ld_c;
+  int32_t splits, c_bf16, accumulate, vec;
+  void* c;
+};
+// Adds a split contraction's partial sums in order: four consecutive columns a thread.
+__global__ void __launch_bounds__(256) gemm_fp8_join_kernel(const __grid_constant__ JoinArgs8 p) {
+  pdl_launch();
+  pdl_wait();
+  const int64_t quads = p.ld_part / 4, total = p.m * quads, step = (int64_t)gridDim.x * 256;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
+    const int64_t r = e / quads, c = (e % quads) * 4;
+    const float* s = p.part + r * p.ld_part + c;
+    float4 v = p.splits ? *reinterpret_cast<const float4*>(s) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 1; i < p.splits; ++i) {
+      const float4 o = *reinterpret_cast<const float4*>(s + (int64_t)i * p.m * p.ld_part);
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
+    float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!p.accumulate || c + j >= p.n) continue;
+      const int64_t at = r * p.ld_c + c + j;
+      f[j] += p.c_bf16 ? to_f32(static_cast<const bf16_t*>(p.c)[at])
+                       : static_cast<const float*>(p.c)[at];
+    }
+    if (p.vec && c + 4 <= p.n) {
+      if (p.c_bf16)
+        *reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.c) + r * p.ld_c + c) =
+            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.c) + r * p.ld_c + c) =
+            make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c + j >= p.n) continue;
+        if (p.c_bf16)
+          static_cast<bf16_t*>(p.c)[r * p.ld_c + c + j] = from_f32<bf16_t>(f[j]);
+        else
+          static_cast<float*>(p.c)[r * p.ld_c + c + j] = f[j];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few rows or columns
+// The narrow side has up to NT indices.  A CTA takes 128 indices of the wide side (the tensor cores'
+// M) and a slice of k; the CTAs of a cluster hold the slices of one tile, and each adds a part of the
+// tile over the slices, in order, out of the others' shared memory.  Bound by reading the wide
+// operand once.
+constexpr int kNarrowThreads = 192;         // warp 0 TMA, 1 MMA, 2 scales, 2-5 epilogue
+constexpr int kNarrowSf = 2;
+template <int NT>
+struct Narrow {
+  static constexpr uint32_t kStage = kBox8 + NT * 128u;
+  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
+  static constexpr uint32_t kSf = kStages * kStage;
+  static constexpr uint32_t kBars = kSf + kNarrowSf * 1024u;
+  static constexpr uint32_t kSmem = 1024 + kBars + 256;
+  static constexpr uint32_t kCols = NT == 16 ? 32 : NT == 32 ? 64 : NT == 64 ? 128 : 256;
+  static_assert(128 * NT * 4 <= kStages * kStage, "the partial sums lie in the stages");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kNarrowThreads, 2)
+    gemm_fp8_narrow_kernel(const __grid_constant__ Gemm8Args P) {
+  using C = Narrow<NT>;
+  constexpr int S = C::kStages, F = kNarrowSf;
+  extern __shared__ uint8_t smem_raw[];
+  pdl_launch();
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  constexpr int full0 = 0, empty0 = S, sf_full0 = 2 * S, sf_empty0 = 2 * S + F,
+                sf_free0 = 2 * S + 2 * F, done = sf_free0 + 2;
+  static_assert((done + 2) * 8 <= 256, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar(full0 + s), 1);
+      mbar_init(bar(empty0 + s), 1);
+    }
+    for (int s = 0; s < F; ++s) {
+      mbar_init(bar(sf_full0 + s), 1);
+      mbar_init(bar(sf_empty0 + s), 1);
+      mbar_init(bar(sf_free0 + s), 1);
+    }
+    mbar_init(bar(done), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  const uint32_t tmem_base = *tmem_slot;
+  const Guard g{abort_flag, P.wait_limit_ns, P.status};
+  // the grid's x is (tile, slice) with the slice fastest: a cluster is one tile
+  const int split = (int)(blockIdx.x % (unsigned)P.splits);
+  const int tile = (int)(blockIdx.x / (unsigned)P.splits);
+  const int w0 = (tile % P.tiles_m) * 128, t0 = tile / P.tiles_m * NT;
+  const int kb0 = min(split * P.kb_split, P.nkb), nk = min(P.kb_split, P.nkb - kb0);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 1, armed = 0, last_par = 0;
+      for (int kb = kb0; kb < kb0 + nk; ++kb) {
+        if (!mbar_wait(bar(empty0 + stage), ph, g)) break;
+        const uint32_t fb = bar(full0 + stage), dst = sbase + (uint32_t)stage * C::kStage;
+        const int k0 = kb * kB8;
+        expect_tx_p(true, fb, C::kStage);
+        tma_load_p(true, dst, &P.a, P.a_mn ? w0 : k0, P.a_mn ? k0 : w0, fb);
+        tma_load_p(true, dst + kBox8, &P.b, P.b_mn ? t0 : k0, P.b_mn ? k0 : t0, fb);
+        armed |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | ((ph ^ 1u) << stage);
+        if (++stage == S) { stage = 0; ph ^= 1u; }
+      }
+      for (int st = 0; st < S; ++st)
+        if (armed & (1u << st)) mbar_wait(bar(full0 + st), (last_par >> st) & 1u, g, false);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, sf = 0, buf = 0;
+      uint32_t phase = 0, sf_phase = 0, buf_phase = 1;
+      for (int kb = 0; kb < nk; ++kb) {
+        const uint32_t sfa = tmem_base + NT + (uint32_t)buf * 8u, sfb = sfa + 4u;
+        if ((kb & 3) == 0) {
+          if (!mbar_wait(bar(sf_full0 + sf), sf_phase, g) ||
+              !mbar_wait(bar(sf_free0 + buf), buf_phase, g))
+            break;
+          tc_fence_after();
+          const uint32_t src = sbase + C::kSf + (uint32_t)sf * 1024u;
+          copy_scales<1>(sfa, scale_desc(src));
+          copy_scales<1>(sfb, scale_desc(src + 512u));
+          tc_commit(bar(sf_empty0 + sf));
+          if (++sf == F) { sf = 0; sf_phase ^= 1u; }
+        }
+        if (!mbar_wait(bar(full0 + stage), phase, g)) break;
+        tc_fence_after();
+        const uint32_t sm_a = sbase + (uint32_t)stage * C::kStage;
+        const uint32_t idesc = with_scale_id(P.idesc, kb & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma8<1>(tmem_base, operand_desc8(sm_a, P.a_mn, j), operand_desc8(sm_a + kBox8, P.b_mn, j),
+                  idesc, sfa, sfb, (kb | j) != 0);
+        tc_commit(bar(empty0 + stage));
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+        if ((kb & 3) == 3) {
+          tc_commit(bar(sf_free0 + buf));
+          buf ^= 1;
+          if (buf == 0) buf_phase ^= 1u;
+        }
+      }
+      tc_commit(bar(done));
+      mbar_wait(bar(done), 0u, g, false);
+    }
+  } else if (warp == 2) {
+    int sf = 0;
+    uint32_t ph = 1;
+    for (int kb = 0; kb < nk; kb += 4) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = scale_word(P.sa, w0 + 32 * j + lane, P.m, kb0 + kb, P.nkb);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[4 + j] = 32 * j + lane < NT ? scale_word(P.sb, t0 + 32 * j + lane, P.n, kb0 + kb, P.nkb)
+                                      : 0x7F7F7F7Fu;
+      if (!mbar_wait(bar(sf_empty0 + sf), ph, g)) break;
+      const uint32_t dst = sbase + C::kSf + (uint32_t)sf * 1024u + (uint32_t)lane * 16u;
+      sts128(dst, make_uint4(v[0], v[1], v[2], v[3]));
+      sts128(dst + 512u, make_uint4(v[4], v[5], v[6], v[7]));
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sf_full0 + sf));
+      if (++sf == F) { sf = 0; ph ^= 1u; }
+    }
+  }
+  __syncwarp();
+  // The products are done (the MMA thread has waited for them), and with them every copy into the
+  // stages, whose memory takes the sums now.
+  __syncthreads();
+  tc_fence_after();
+  float* sums = reinterpret_cast<float*>(smem);           // [NT][128]
+  if (warp >= 2) {
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t ta = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+    for (int q = 0; q < NT / 16; ++q) {
+      uint32_t r[16];
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+          "%10, %11, %12, %13, %14, %15}, [%16];\ntcgen05.wait::ld.sync.aligned;\n"
+          : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+            "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+            "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+          : "r"(ta + (uint32_t)(16 * q))
+          : "memory");
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        sums[(16 * q + k) * 128 + row] = nk > 0 ? __uint_as_float(r[k]) : 0.f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  {
+    // this CTA's share of the tile: narrow indices split, split + splits, ..., two rows of 64 lanes
+    const int live = min(NT, P.n - t0), wide = min(128, P.m - w0);
+    const uint32_t mine = smem_u32(sums);
+    for (int e = threadIdx.x; e < 128 * NT; e += kNarrowThreads) {
+      const int t = e >> 7, r = e & 127;
+      if (t % P.splits != split || t >= live || r >= wide) continue;
+      float v = 0.f;
+      for (int i = 0; i < P.splits; ++i) {
+        float o;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(o)
+                     : "r"(map_rank(mine + (uint32_t)e * 4u, (uint32_t)i))
+                     : "memory");
+        v = i == 0 ? o : v + o;
+      }
+      const int64_t at = (int64_t)(w0 + r) * P.sw + (int64_t)(t0 + t) * P.st;
+      if (P.c_bf16) {
+        bf16_t* c = static_cast<bf16_t*>(P.c) + at;
+        *c = from_f32<bf16_t>(P.accumulate ? v + to_f32(*c) : v);
+      } else {
+        float* c = static_cast<float*>(P.c) + at;
+        *c = P.accumulate ? v + *c : v;
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while another may still read its sums
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(C::kCols)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- host
+constexpr int kPairs = 76;                  // CTA pairs of the device: what the plans count on
+constexpr int64_t kNarrowMost = 128;        // widest narrow side
+
+struct Gemm8Plan {
+  bool narrow = false, swap = false;        // swap: the narrow side is A's
+  int nt = 0;
+  int splits = 1, kb_split = 0;
+  int64_t ld_part = 0;
+  size_t bytes = 0;
+};
+
+Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
+  Gemm8Plan p;
+  const int nkb = (int)((k + kB8 - 1) / kB8);
+  if (std::min(m, n) <= kNarrowMost) {
+    p.narrow = true;
+    p.swap = m <= n;
+    const int64_t few = std::min(m, n), wide = std::max(m, n);
+    p.nt = few <= 16 ? 16 : few <= 32 ? 32 : few <= 64 ? 64 : 128;
+    const int64_t tiles = (wide + 127) / 128;
+    // slices of k until the device is covered twice, of two blocks at least
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= 4 * kPairs && nkb >= 4 * s) s *= 2;
+    p.splits = s;
+    p.kb_split = (nkb + s - 1) / s;
+    return p;
+  }
+  const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  // Splits of k that shorten the longest pair's work: rounds of (blocks + what a tile costs beside
+  // them), and a pass over the partial sums.
+  double best = 0.;
+  for (int s = 1; s <= 32 && (s == 1 || nkb / s >= 4); ++s) {
+    const int per = ((nkb + s - 1) / s + 3) / 4 * 4;
+    const int64_t real = (nkb + per - 1) / per;
+    if (s > 1 && real != s) continue;
+    const int64_t rounds = (tiles * s + kPairs - 1) / kPairs;
+    // in block times (0.27 us): 3 beside a tile's own; the join's bytes at 6 TB/s and its launch
+    double cost = (double)rounds * (per + 3);
+    if (s > 1) cost += 8. + (double)s * m * n * 8. / 6e12 / 0.27e-6;
+    if (s == 1 || cost < best * 0.97) {
+      best = cost;
+      p.splits = s;
+      p.kb_split = per;
+    }
+  }
+  if (p.splits == 1) p.kb_split = nkb;
+  p.ld_part = (n + 3) / 4 * 4;
+  p.bytes = p.splits > 1 ? (size_t)p.splits * m * p.ld_part * 4 : 0;
+  return p;
+}
+
+int check_sizes(int64_t m, int64_t n, int64_t k) {
+  return m < 0 || n < 0 || k < 0 || m >= (1ll << 31) - 512 || n >= (1ll << 31) - 512 ||
+                 k >= (1ll << 31) - 512
+             ? MFSDP_ESHAPE
+             : MFSDP_OK;
+}
+
+ScaleArgs scales_of(const mfsdp_fp8_matrix& m, bool along_rows) {
+  // along_rows: the contraction runs down the stored rows
+  ScaleArgs s{};
+  s.s = static_cast<const uint8_t*>(m.scales);
+  s.sr = along_rows ? 1 : m.ld_scales;
+  s.sk = along_rows ? m.ld_scales : 1;
+  s.shift = m.groups == MFSDP_GROUPS_TILE ? 7 : 0;
+  s.word = !along_rows && m.ld_scales % 4 == 0 && aligned_to(m.scales, 4);
+  return s;
+}
+
+template <typename K>
+cudaError_t allow_smem(std::atomic<bool>* done, K kernel, uint32_t bytes) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev].load())) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true);
+  return e;
+}
+
+cudaError_t launch_clusters(void (*kernel)(const Gemm8Args), unsigned grid, unsigned cluster,
+                            unsigned threads, uint32_t smem, cudaStream_t st, const Gemm8Args& a) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int NT>
+cudaError_t launch_narrow(const Gemm8Args& a, int64_t tiles, cudaStream_t st) {
+  static std::atomic<bool> done[64];
+  cudaError_t e = allow_smem(done, gemm_fp8_narrow_kernel<NT>, Narrow<NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(gemm_fp8_narrow_kernel<NT>, (unsigned)(tiles * a.splits),
+                         (unsigned)a.splits, kNarrowThreads, Narrow<NT>::kSmem, st, a);
+}
+
+}  // namespace
+}  // namespace mfsdp
+
+using namespace mfsdp;
+
+extern "C" int mfsdp_gemm_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t* bytes_out) {
+  if (!bytes_out) return MFSDP_EINVAL;
+  const int chk = check_sizes(m, n, k);
+  if (chk != MFSDP_OK) return chk;
+  *bytes_out = m && n ? plan_gemm(m, n, k).bytes : 0;
+  return MFSDP_OK;
+}
+
+extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_matrix* a,
+                              int32_t trans_a, const mfsdp_fp8_matrix* b, int32_t trans_b,
+                              int32_t accumulate, int32_t c_dtype, void* c, int64_t ld_c,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!a || !b || !dtype_ok(c_dtype)) return MFSDP_EINVAL;
+  int chk = check_sizes(m, n, k);
+  if (chk != MFSDP_OK) return chk;
+  chk = trans_a ? check_fp8(*a, k, m, -1) : check_fp8(*a, m, k, -1);
+  if (chk == MFSDP_OK) chk = trans_b ? check_fp8(*b, n, k, -1) : check_fp8(*b, k, n, -1);
+  if (chk != MFSDP_OK) return chk;
+  // a scale has to be the same for 128 of the contraction
+  if (a->groups == (trans_a ? MFSDP_GROUPS_ROW : MFSDP_GROUPS_COL) ||
+      b->groups == (trans_b ? MFSDP_GROUPS_COL : MFSDP_GROUPS_ROW))
+    return MFSDP_EINVAL;
+  if (m == 0 || n == 0) return MFSDP_OK;
+  if (!c || ld_c < n) return MFSDP_EINVAL;
+  if (!aligned_to(c, dtype_bytes(c_dtype))) return MFSDP_EALIGN;
+  const Gemm8Plan plan = plan_gemm(m, n, k);
+  if (plan.bytes) {
+    if (!workspace) return MFSDP_EINVAL;
+    if (!aligned_to(workspace, 256)) return MFSDP_EALIGN;
+    if (workspace_bytes < plan.bytes) return MFSDP_EWORKSPACE;
+  }
+  if (k == 0 && accumulate) return MFSDP_OK;
+  int sms = 0;
+  const int dst = device_sms(&sms);
+  if (dst != MFSDP_OK) return dst;
+  int* status = device_status();
+  if (!status) return MFSDP_ECUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int vec = vector_rows(c, ld_c, c_dtype);
+  JoinArgs8 j{};
+  j.part = static_cast<const float*>(workspace);
+  j.m = m;
+  j.n = n;
+  j.ld_part = (n + 3) / 4 * 4;
+  j.ld_c = ld_c;
+  j.splits = k ? plan.splits : 0;
+  j.c_bf16 = c_dtype == MFSDP_DTYPE_BF16;
+  j.accumulate = accumulate != 0;
+  j.vec = vec;
+  j.c = c;
+  const dim3 join_grid((unsigned)std::min<int64_t>((m * (j.ld_part / 4) + 255) / 256, sms * 16ll));
+  if (k == 0)
+    return launch_pdl(gemm_fp8_join_kernel, join_grid, dim3(256), 0, st, j) == cudaSuccess
+               ? MFSDP_OK : MFSDP_ECUDA;
+
+  Gemm8Args g{};
+  const mfsdp_fp8_matrix *wide = plan.swap ? b : a, *other = plan.swap ? a : b;
+  // whether the contraction runs down the stored rows
+  const bool a_rows = trans_a != 0, b_rows = trans_b == 0;
+  const bool w_rows = plan.swap ? b_rows : a_rows, o_rows = plan.swap ? a_rows : b_rows;
+  g.m = (int32_t)(plan.swap ? n : m);
+  g.n = (int32_t)(plan.swap ? m : n);
+  g.nkb = (int32_t)((k + kB8 - 1) / kB8);
+  g.a_mn = w_rows;
+  g.b_mn = o_rows;
+  const int nt = plan.narrow && o_rows ? 128 : plan.nt;   // MN-major boxes are 128 indices wide
+  bool ok = encode_map_u8(&g.a, wide->data, w_rows ? k : g.m, w_rows ? g.m : k, wide->ld, 128u);
+  ok = ok && encode_map_u8(&g.b, other->data, o_rows ? k : g.n, o_rows ? g.n : k, other->ld,
+                           plan.narrow && !o_rows ? (uint32_t)nt : 128u);
+  if (!ok) return MFSDP_ECUDA;
+  g.sa = scales_of(*wide, w_rows);
+  g.sb = scales_of(*other, o_rows);
+  g.idesc = idesc8(wide->dtype == MFSDP_FP8_E5M2, other->dtype == MFSDP_FP8_E5M2, g.a_mn, g.b_mn,
+                   plan.narrow ? 128 : 256, plan.narrow ? nt : 256);
+  g.splits = plan.splits;
+  g.kb_split = plan.kb_split;
+  g.c = c;
+  g.ld_c = ld_c;
+  g.c_bf16 = j.c_bf16;
+  g.accumulate = j.accumulate;
+  g.vec = vec;
+  g.part = static_cast<float*>(workspace);
+  g.ld_part = plan.ld_part;
+  g.wait_limit_ns = wait_limit_ns();
+  g.status = status;
+  cudaError_t e;
+  if (plan.narrow) {
+    g.tiles_m = (g.m + 127) / 128;
+    g.tiles_n = 1;
+    g.sw = plan.swap ? 1 : ld_c;
+    g.st = plan.swap ? ld_c : 1;
+    const int64_t tiles = g.tiles_m;
+    e = nt == 16   ? launch_narrow<16>(g, tiles, st)
+        : nt == 32 ? launch_narrow<32>(g, tiles, st)
+        : nt == 64 ? launch_narrow<64>(g, tiles, st)
+                   : launch_narrow<128>(g, tiles, st);
+    return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
+  }
+  g.tiles_m = (g.m + 255) / 256;
+  g.tiles_n = (g.n + 255) / 256;
+  // The tensor cores cut each of their additions towards zero, which grows with the contraction:
+  // sums that are kept in fp32 are added up in registers every 1024 of k, others where the cuts
+  // would come near half a bf16 step.
+  const bool chunked = !g.c_bf16 || g.kb_split > 512;
+  g.chunk = 8;
+  const int pairs = std::max(1, std::min(sms / 2, g.tiles_m * g.tiles_n * g.splits));
+  static std::atomic<bool> done[2][64];
+  if (chunked) {
+    e = allow_smem(done[1], gemm_fp8_pair_kernel<true>, kPairSmem);
+    if (e == cudaSuccess)
+      e = launch_clusters(gemm_fp8_pair_kernel<true>, 2 * pairs, 2, kPairThreads, kPairSmem, st, g);
+  } else {
+    e = allow_smem(done[0], gemm_fp8_pair_kernel<false>, kPairSmem);
+    if (e == cudaSuccess)
+      e = launch_clusters(gemm_fp8_pair_kernel<false>, 2 * pairs, 2, kPairThreads, kPairSmem, st, g);
+  }
+  if (e == cudaSuccess && g.splits > 1)
+    e = launch_pdl(gemm_fp8_join_kernel, join_grid, dim3(256), 0, st, j);
+  return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
+}

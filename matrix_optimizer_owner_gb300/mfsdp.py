@@ -11,10 +11,10 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import threading
-from typing import Optional, Sequence, Tuple
+from typing import Any, NamedTuple, Optional, Sequence, Tuple
 
 from . import _lib
-from ._lib import CostModel, GemmProblem, Matrix, ParamDesc, RankResources, Segment
+from ._lib import CostModel, Fp8Struct, GemmProblem, Matrix, ParamDesc, RankResources, Segment
 
 POLICY_ROLE_GREEDY = 0
 POLICY_SCOPE_GREEDY = 1
@@ -24,6 +24,11 @@ INDEX_I32 = 0
 INDEX_I64 = 1
 NORM_LAYER = 0
 NORM_RMS = 1
+GROUPS_ROW = 0
+GROUPS_COL = 1
+GROUPS_TILE = 2
+FP8_E4M3 = 0
+FP8_E5M2 = 1
 LR_ORIGINAL = 0
 LR_MATCH_RMS_ADAMW = 1
 
@@ -770,3 +775,133 @@ def mfsdp_head_loss_backward(hidden, weight, labels, lse, dloss, dhidden=None, d
     _check("mfsdp_head_loss_backward", _lib.load().mfsdp_head_loss_backward(
         n, dim, vocab, code, hidden.data_ptr(), ld_h, wp, ld_w, icode, lab, ignore_index, ls, dl,
         piece, dh, ld_dh, dw, ld_dw, ws.data_ptr(), nbytes, st))
+
+
+# ------------------------------------------------------------------------------- 8-bit operators
+class Fp8Matrix(NamedTuple):
+    """An 8-bit matrix: ``data`` [rows, cols] of float8_e4m3fn or float8_e5m2 (16-byte aligned, rows a
+    multiple of 16 bytes apart), ``scales`` of float8_e8m0fnu (or uint8), one per group of 128 values
+    as ``groups`` (GROUPS_ROW, GROUPS_COL, GROUPS_TILE) says."""
+    data: Any
+    scales: Any
+    groups: int
+
+
+def fp8_scale_shape(rows: int, cols: int, groups: int) -> Tuple[int, int]:
+    return (rows if groups == GROUPS_ROW else -(-rows // 128),
+            cols if groups == GROUPS_COL else -(-cols // 128))
+
+
+def fp8_empty(rows: int, cols: int, groups: int, dtype=None, device="cuda") -> Fp8Matrix:
+    """An 8-bit matrix (of float8_e4m3fn unless ``dtype`` says otherwise) of uninitialised values."""
+    import torch
+    pitch = -(-cols // 16) * 16
+    data = torch.empty((rows, pitch), dtype=dtype or torch.float8_e4m3fn, device=device)
+    scales = torch.empty(fp8_scale_shape(rows, cols, groups), dtype=torch.float8_e8m0fnu,
+                         device=device)
+    return Fp8Matrix(data[:, :cols], scales, groups)
+
+
+_FP8_CODES, _SCALE_TYPES = {}, ()
+
+
+def _learn_fp8() -> None:
+    global _SCALE_TYPES
+    import torch
+    _learn_dtypes()
+    _FP8_CODES.update({torch.float8_e4m3fn: FP8_E4M3, torch.float8_e5m2: FP8_E5M2})
+    _SCALE_TYPES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _fp8(m, shape, dev: int, name: str, groups: Optional[int] = None) -> Optional[Fp8Struct]:
+    """The C description of an 8-bit matrix (None for None)."""
+    if m is None:
+        return None
+    data, scales, kind = m
+    if not _FP8_CODES:
+        _learn_fp8()
+    code = _FP8_CODES.get(data.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected float8_e4m3fn or float8_e5m2, got {data.dtype}")
+    if kind not in (GROUPS_ROW, GROUPS_COL, GROUPS_TILE):
+        raise ValueError(f"{name}: unknown groups {kind}")
+    if groups is not None and kind != groups:
+        raise ValueError(f"{name}: expected groups {groups}, got {kind}")
+    ld = _matrix(data, shape, data.dtype, dev, name)
+    rows, cols = shape
+    if rows <= 1:
+        ld = -(-ld // 16) * 16             # a single row has no pitch
+    if scales.dtype not in _SCALE_TYPES:
+        raise TypeError(f"{name}: expected float8_e8m0fnu or uint8 scales, got {scales.dtype}")
+    ld_s = _matrix(scales, fp8_scale_shape(rows, cols, kind), scales.dtype, dev, name + " scales")
+    return Fp8Struct(data.data_ptr(), ld, scales.data_ptr(), ld_s, code, kind)
+
+
+def mfsdp_quantize_fp8(x, out: Fp8Matrix, also: Optional[Fp8Matrix] = None, stream=None) -> None:
+    """``x`` (float32 or bfloat16) in 8 bits: into ``out``, of any grouping, and from the same read
+    into ``also``, a GROUPS_COL matrix beside a GROUPS_ROW one."""
+    shape = _two_dims(x, "x")
+    code, dev = _float_code(x, "x"), x.get_device()
+    ld = _matrix(x, shape, x.dtype, dev, "x")
+    o, a = _fp8(out, shape, dev, "out"), _fp8(also, shape, dev, "also")
+    st = _device_stream(dev, stream)
+    _check("mfsdp_quantize_fp8", _lib.load().mfsdp_quantize_fp8(
+        shape[0], shape[1], code, x.data_ptr(), ld, o, a, st))
+
+
+def mfsdp_regroup_fp8(src: Fp8Matrix, out: Fp8Matrix, also: Optional[Fp8Matrix] = None,
+                      stream=None) -> None:
+    """``src`` in another grouping (or type): what ``mfsdp_quantize_fp8`` gives for its values."""
+    shape = _two_dims(src.data, "src")
+    dev = src.data.get_device()
+    s = _fp8(src, shape, dev, "src")
+    o, a = _fp8(out, shape, dev, "out"), _fp8(also, shape, dev, "also")
+    st = _device_stream(dev, stream)
+    _check("mfsdp_regroup_fp8", _lib.load().mfsdp_regroup_fp8(shape[0], shape[1], s, o, a, st))
+
+
+def mfsdp_dequantize_fp8(src: Fp8Matrix, out, stream=None) -> None:
+    """The values of ``src`` into ``out`` (float32 or bfloat16)."""
+    shape = _two_dims(src.data, "src")
+    dev = src.data.get_device()
+    s = _fp8(src, shape, dev, "src")
+    code = _float_code(out, "out")
+    ld = _matrix(out, shape, out.dtype, dev, "out")
+    st = _device_stream(dev, stream)
+    _check("mfsdp_dequantize_fp8", _lib.load().mfsdp_dequantize_fp8(
+        shape[0], shape[1], s, code, out.data_ptr(), ld, st))
+
+
+@functools.lru_cache(maxsize=256)
+def mfsdp_gemm_fp8_workspace_bytes(m: int, n: int, k: int) -> int:
+    out = C.c_size_t(0)
+    _check("mfsdp_gemm_fp8_workspace_bytes",
+           _lib.load().mfsdp_gemm_fp8_workspace_bytes(m, n, k, C.byref(out)))
+    return out.value
+
+
+def mfsdp_gemm_fp8(a: Fp8Matrix, b: Fp8Matrix, c, trans_a: bool = False, trans_b: bool = False,
+                   accumulate: bool = False, workspace=None, stream=None) -> None:
+    """``c = op(a) @ op(b)`` of 8-bit matrices (op = transpose where ``trans_a`` / ``trans_b``), in
+    float32 or bfloat16; added to ``c`` with ``accumulate``.  Scales are shared along the contraction:
+    GROUPS_ROW or GROUPS_TILE for ``a`` and for ``b`` with ``trans_b``, GROUPS_COL or GROUPS_TILE for
+    ``b`` and for ``a`` with ``trans_a``.  ``workspace`` (uint8) defaults to this thread's for the
+    current stream."""
+    sa, sb = _two_dims(a.data, "a"), _two_dims(b.data, "b")
+    m, k = (sa[1], sa[0]) if trans_a else (sa[0], sa[1])
+    kb, n = (sb[1], sb[0]) if trans_b else (sb[0], sb[1])
+    if kb != k:
+        raise ValueError(f"a and b: contractions of {k} and {kb}")
+    dev = c.get_device()
+    code = _float_code(c, "c")
+    ld = _matrix(c, (m, n), c.dtype, dev, "c")
+    fa, fb = _fp8(a, sa, dev, "a"), _fp8(b, sb, dev, "b")
+    st = _device_stream(dev, stream)
+    need = mfsdp_gemm_fp8_workspace_bytes(m, n, k)
+    wp, nbytes = None, 0
+    if need or workspace is not None:
+        ws, nbytes = _workspace(workspace, need, c, dev, stream, st)
+        wp = ws.data_ptr()
+    _check("mfsdp_gemm_fp8", _lib.load().mfsdp_gemm_fp8(
+        m, n, k, fa, 1 if trans_a else 0, fb, 1 if trans_b else 0, 1 if accumulate else 0, code,
+        c.data_ptr(), ld, wp, nbytes, st))
