@@ -761,6 +761,71 @@ int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_matrix* a, i
                    const mfsdp_fp8_matrix* b, int32_t trans_b, int32_t accumulate, int32_t c_dtype,
                    void* c, int64_t ld_c, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Residual addition and norm of every row: h = x + residual (h = x without one), mu, r and
+ *     y = (h - mu) r weight + bias
+ * as mfsdp_norm_forward has them, of the unrounded h.
+ *   residual     nullable.
+ *   h            nullable output of `dtype` (the residual stream); h8  nullable, h in 8 bits (ROW):
+ *                a checkpoint for the backward pass.
+ *   y, y8        the result in `dtype` and in 8 bits (ROW): at least one.
+ *   mean, rstd   nullable outputs, as mfsdp_norm_forward's.
+ * h and y may be x's or residual's buffer (same pitch), not both the same one.  rows == 0 is no work.
+ */
+int mfsdp_norm_residual_forward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                                int32_t param_dtype, const void* x, int64_t ld_x,
+                                const void* residual, int64_t ld_residual, const void* weight,
+                                const void* bias, float eps, void* h, int64_t ld_h, void* y,
+                                int64_t ld_y, const mfsdp_fp8_matrix* y8,
+                                const mfsdp_fp8_matrix* h8, float* mean, float* rstd, void* stream);
+
+/*
+ * Gradient of mfsdp_norm_residual_forward for x (and, the same, for residual): mfsdp_norm_backward's dx
+ * at h, and dres added to it.
+ *   dres         nullable: the gradient that reaches h beside the norm.
+ *   h or h8      one of them: h as the forward pass stored it, or its 8-bit checkpoint (ROW).
+ *   workspace    >= mfsdp_norm_backward_workspace_bytes(rows, cols).
+ * The other arguments are mfsdp_norm_backward's.  dx may be dy's, dres's or h's buffer (same pitch).
+ */
+int mfsdp_norm_residual_backward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                                 int32_t param_dtype, const void* dy, int64_t ld_dy,
+                                 const void* dres, int64_t ld_dres, const void* h, int64_t ld_h,
+                                 const mfsdp_fp8_matrix* h8, const void* weight, const float* mean,
+                                 const float* rstd, void* dx, int64_t ld_dx, void* dweight,
+                                 void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef enum { MFSDP_ACT_SWIGLU = 0, MFSDP_ACT_GELU = 1 } mfsdp_activation;
+
+/*
+ * The activation of a feed-forward layer, elementwise over [rows x cols]:
+ *     SWIGLU  y = gate / (1 + exp(-gate)) up
+ *     GELU    y = gate (1 + tanh(sqrt(2 / pi) (gate + 0.044715 gate^3))) / 2; takes no up
+ *   y, y8         the result in `dtype` and in 8 bits (ROW): at least one.
+ *   gate8, up8    nullable: the inputs in 8 bits (ROW), checkpoints for the backward pass.
+ * gate and up may be two halves of one buffer's rows.  rows == 0 is no work.  rows, cols < 2^31.
+ */
+int mfsdp_activation_forward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                             const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                             void* y, int64_t ld_y, const mfsdp_fp8_matrix* y8,
+                             const mfsdp_fp8_matrix* gate8, const mfsdp_fp8_matrix* up8,
+                             void* stream);
+
+/*
+ * Gradients of mfsdp_activation_forward, at the inputs or at their 8-bit checkpoints (both in the same
+ * form; ROW).
+ *   dgate, dup            nullable outputs of `dtype`;
+ *   dgate_row, dup_row    nullable, in 8 bits, ROW (for dx = dy W);
+ *   dgate_col, dup_col    nullable, in 8 bits, COL (for dW = dy^T x).
+ * At least one output.  dgate may be dy's or gate's buffer, dup dy's or up's (same pitch).
+ */
+int mfsdp_activation_backward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
+                              const void* dy, int64_t ld_dy, const void* gate, int64_t ld_gate,
+                              const mfsdp_fp8_matrix* gate8, const void* up, int64_t ld_up,
+                              const mfsdp_fp8_matrix* up8, void* dgate, int64_t ld_dgate, void* dup,
+                              int64_t ld_dup, const mfsdp_fp8_matrix* dgate_row,
+                              const mfsdp_fp8_matrix* dgate_col, const mfsdp_fp8_matrix* dup_row,
+                              const mfsdp_fp8_matrix* dup_col, void* stream);
+
 /* ------------------------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------------------------ */

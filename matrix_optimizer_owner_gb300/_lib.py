@@ -142,6 +142,20 @@ SIGNATURES = {
     "mfsdp_gemm_fp8": (C.c_int, [_i64, _i64, _i64, C.POINTER(Fp8Struct), _i32,
                                  C.POINTER(Fp8Struct), _i32, _i32, _i32, _vp, _i64, _vp,
                                  C.c_size_t, _vp]),
+    "mfsdp_norm_residual_forward": (C.c_int, [_i32, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _i64,
+                                              _vp, _vp, _f32, _vp, _i64, _vp, _i64,
+                                              C.POINTER(Fp8Struct), C.POINTER(Fp8Struct), _vp, _vp,
+                                              _vp]),
+    "mfsdp_norm_residual_backward": (C.c_int, [_i32, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _i64,
+                                               _vp, _i64, C.POINTER(Fp8Struct), _vp, _vp, _vp, _vp,
+                                               _i64, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "mfsdp_activation_forward": (C.c_int, [_i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64,
+                                           C.POINTER(Fp8Struct), C.POINTER(Fp8Struct),
+                                           C.POINTER(Fp8Struct), _vp]),
+    "mfsdp_activation_backward": (C.c_int, [_i32, _i64, _i64, _i32, _vp, _i64, _vp, _i64,
+                                            C.POINTER(Fp8Struct), _vp, _i64, C.POINTER(Fp8Struct),
+                                            _vp, _i64, _vp, _i64] + [C.POINTER(Fp8Struct)] * 4
+                                  + [_vp]),
     "mfsdp_query_status": (C.c_int, [_vp, C.POINTER(_i32)]),
     "mfsdp_status_string": (C.c_char_p, [C.c_int]),
     "mfsdp_set_wait_limit_ns": (C.c_int, [_u64]),

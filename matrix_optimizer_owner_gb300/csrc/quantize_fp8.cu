@@ -5,6 +5,7 @@
 // (exact) and rounded once.  From 8 bits to 8 bits a value keeps its significand, and the change of
 // groups rounds only what becomes subnormal.  Bound by memory: the source once, a byte per value out.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8.cuh"
 

@@ -27,6 +27,8 @@ NORM_RMS = 1
 GROUPS_ROW = 0
 GROUPS_COL = 1
 GROUPS_TILE = 2
+ACT_SWIGLU = 0
+ACT_GELU = 1
 FP8_E4M3 = 0
 FP8_E5M2 = 1
 LR_ORIGINAL = 0
@@ -905,3 +907,110 @@ def mfsdp_gemm_fp8(a: Fp8Matrix, b: Fp8Matrix, c, trans_a: bool = False, trans_b
     _check("mfsdp_gemm_fp8", _lib.load().mfsdp_gemm_fp8(
         m, n, k, fa, 1 if trans_a else 0, fb, 1 if trans_b else 0, 1 if accumulate else 0, code,
         c.data_ptr(), ld, wp, nbytes, st))
+
+
+def _rows(t, shape, dtype, dev: int, name: str):
+    """Address and pitch of a 2D tensor that may be None."""
+    if t is None:
+        return None, shape[1]
+    return t.data_ptr(), _matrix(t, shape, dtype, dev, name)
+
+
+def mfsdp_norm_residual_forward(kind: int, x, residual, weight, bias, eps: float, h=None, y=None,
+                                y8: Optional[Fp8Matrix] = None, h8: Optional[Fp8Matrix] = None,
+                                mean=None, rstd=None, stream=None) -> None:
+    """``h = x + residual`` (``residual`` may be None) and its layer or RMS norm into ``y``, into
+    ``y8`` (8 bits, GROUPS_ROW), or both.  ``h`` (the residual stream), ``h8`` (its 8-bit checkpoint),
+    ``mean`` and ``rstd`` are written where given, for ``mfsdp_norm_residual_backward``."""
+    shape = _two_dims(x, "x")
+    rows, cols = shape
+    code, dtype, dev = _float_code(x, "x"), x.dtype, x.get_device()
+    ld_x = _matrix(x, shape, dtype, dev, "x")
+    rp, ld_r = _rows(residual, shape, dtype, dev, "residual")
+    hp, ld_h = _rows(h, shape, dtype, dev, "h")
+    yp, ld_y = _rows(y, shape, dtype, dev, "y")
+    fy, fh = _fp8(y8, shape, dev, "y8", GROUPS_ROW), _fp8(h8, shape, dev, "h8", GROUPS_ROW)
+    pdtype, pcode = _params_dtype(("weight", weight), ("bias", bias))
+    w = _vector(weight, (cols,), pdtype, dev, "weight")
+    b = _vector(bias, (cols,), pdtype, dev, "bias")
+    m = _vector(mean, (rows,), _F32, dev, "mean")
+    r = _vector(rstd, (rows,), _F32, dev, "rstd")
+    st = _device_stream(dev, stream)
+    _check("mfsdp_norm_residual_forward", _lib.load().mfsdp_norm_residual_forward(
+        kind, rows, cols, code, pcode, x.data_ptr(), ld_x, rp, ld_r, w, b, eps, hp, ld_h, yp, ld_y,
+        fy, fh, m, r, st))
+
+
+def mfsdp_norm_residual_backward(kind: int, dy, dres, h, weight, mean, rstd, dx, dweight=None,
+                                 dbias=None, workspace=None, stream=None) -> None:
+    """Gradient of ``mfsdp_norm_residual_forward`` for its inputs into ``dx``, with ``dres`` (may be
+    None), the gradient that reaches ``h`` beside the norm, added; and for the weight and the bias
+    where given.  ``h`` is what the forward pass wrote: the tensor, or the ``Fp8Matrix`` checkpoint."""
+    shape = _two_dims(dy, "dy")
+    rows, cols = shape
+    code, dtype, dev = _float_code(dy, "dy"), dy.dtype, dy.get_device()
+    ld_dy = _matrix(dy, shape, dtype, dev, "dy")
+    rp, ld_r = _rows(dres, shape, dtype, dev, "dres")
+    kept = isinstance(h, Fp8Matrix)
+    fh = _fp8(h, shape, dev, "h", GROUPS_ROW) if kept else None
+    hp, ld_h = _rows(None if kept else h, shape, dtype, dev, "h")
+    ld_dx = _matrix(dx, shape, dtype, dev, "dx")
+    pdtype, pcode = _params_dtype(("weight", weight), ("dweight", dweight), ("dbias", dbias))
+    w = _vector(weight, (cols,), pdtype, dev, "weight")
+    dw = _vector(dweight, (cols,), pdtype, dev, "dweight")
+    db = _vector(dbias, (cols,), pdtype, dev, "dbias")
+    m = _vector(mean, (rows,), _F32, dev, "mean")
+    r = _vector(rstd, (rows,), _F32, dev, "rstd")
+    st = _device_stream(dev, stream)
+    ws, nbytes = _workspace(workspace, mfsdp_norm_backward_workspace_bytes(rows, cols), dy, dev,
+                            stream, st)
+    _check("mfsdp_norm_residual_backward", _lib.load().mfsdp_norm_residual_backward(
+        kind, rows, cols, code, pcode, dy.data_ptr(), ld_dy, rp, ld_r, hp, ld_h, fh, w, m, r,
+        dx.data_ptr(), ld_dx, dw, db, ws.data_ptr(), nbytes, st))
+
+
+def mfsdp_activation_forward(kind: int, gate, up, y=None, y8: Optional[Fp8Matrix] = None,
+                             gate8: Optional[Fp8Matrix] = None, up8: Optional[Fp8Matrix] = None,
+                             stream=None) -> None:
+    """SwiGLU of ``gate`` and ``up`` (ACT_SWIGLU) or GELU of ``gate`` (ACT_GELU; ``up`` is None) into
+    ``y``, into ``y8`` (8 bits, GROUPS_ROW), or both.  ``gate8`` and ``up8`` take the inputs in 8 bits
+    (GROUPS_ROW) where given, for ``mfsdp_activation_backward``."""
+    shape = _two_dims(gate, "gate")
+    code, dtype, dev = _float_code(gate, "gate"), gate.dtype, gate.get_device()
+    ld_g = _matrix(gate, shape, dtype, dev, "gate")
+    up_p, ld_u = _rows(up, shape, dtype, dev, "up")
+    yp, ld_y = _rows(y, shape, dtype, dev, "y")
+    fy, fg, fu = (_fp8(m, shape, dev, name, GROUPS_ROW)
+                  for m, name in ((y8, "y8"), (gate8, "gate8"), (up8, "up8")))
+    st = _device_stream(dev, stream)
+    _check("mfsdp_activation_forward", _lib.load().mfsdp_activation_forward(
+        kind, shape[0], shape[1], code, gate.data_ptr(), ld_g, up_p, ld_u, yp, ld_y, fy, fg, fu, st))
+
+
+def mfsdp_activation_backward(kind: int, dy, gate, up, dgate=None, dup=None,
+                              dgate8: Optional[Fp8Matrix] = None, dup8: Optional[Fp8Matrix] = None,
+                              dgate8_col: Optional[Fp8Matrix] = None,
+                              dup8_col: Optional[Fp8Matrix] = None, stream=None) -> None:
+    """Gradients of ``mfsdp_activation_forward`` for its inputs.  ``gate`` and ``up`` are the forward
+    pass's tensors or its ``Fp8Matrix`` checkpoints (both the same).  Each gradient is written in
+    ``dy``'s dtype (``dgate``, ``dup``), in 8 bits for the product with the weight (``dgate8``,
+    ``dup8``, GROUPS_ROW) and for the weight's gradient (``dgate8_col``, ``dup8_col``, GROUPS_COL),
+    wherever given."""
+    shape = _two_dims(dy, "dy")
+    code, dtype, dev = _float_code(dy, "dy"), dy.dtype, dy.get_device()
+    ld_dy = _matrix(dy, shape, dtype, dev, "dy")
+    args = []
+    for t, name in ((gate, "gate"), (up, "up")):
+        kept = isinstance(t, Fp8Matrix)
+        args += [*_rows(None if kept else t, shape, dtype, dev, name),
+                 _fp8(t, shape, dev, name, GROUPS_ROW) if kept else None]
+    gp, ld_g = _rows(dgate, shape, dtype, dev, "dgate")
+    up_p, ld_u = _rows(dup, shape, dtype, dev, "dup")
+    fgr, fgc = _fp8(dgate8, shape, dev, "dgate8", GROUPS_ROW), _fp8(dgate8_col, shape, dev,
+                                                                   "dgate8_col", GROUPS_COL)
+    fur, fuc = _fp8(dup8, shape, dev, "dup8", GROUPS_ROW), _fp8(dup8_col, shape, dev, "dup8_col",
+                                                               GROUPS_COL)
+    st = _device_stream(dev, stream)
+    _check("mfsdp_activation_backward", _lib.load().mfsdp_activation_backward(
+        kind, shape[0], shape[1], code, dy.data_ptr(), ld_dy, *args, gp, ld_g, up_p, ld_u, fgr, fgc,
+        fur, fuc, st))

@@ -64,12 +64,21 @@ def values(q, s, groups):
     return q * spread(v, *q.shape, groups)
 
 
+def _gelu(gate):
+    """((1 + tanh u) / 2, du/dgate), u = sqrt(2 / pi) (gate + 0.044715 gate^3); the first as
+    1 / (1 + exp(-2 u)), which has no cancellation where it is small."""
+    c = np.sqrt(2 / np.pi)
+    with np.errstate(over="ignore"):
+        p = 1 / (1 + np.exp(-2 * c * (gate + 0.044715 * gate ** 3)))
+    return p, c * (1 + 3 * 0.044715 * gate ** 2)
+
+
 def activation(kind, gate, up):
     """SwiGLU gate sigmoid(gate) up, or GELU (tanh form) of gate."""
     gate = f64(gate)
     if kind == "swiglu":
         return gate / (1 + np.exp(-gate)) * f64(up)
-    return 0.5 * gate * (1 + np.tanh(np.sqrt(2 / np.pi) * (gate + 0.044715 * gate ** 3)))
+    return gate * _gelu(gate)[0]
 
 
 def activation_grads(kind, dy, gate, up):
@@ -78,6 +87,5 @@ def activation_grads(kind, dy, gate, up):
     if kind == "swiglu":
         p = 1 / (1 + np.exp(-gate))
         return dy * f64(up) * p * (1 + gate * (1 - p)), dy * gate * p
-    c = np.sqrt(2 / np.pi)
-    t = np.tanh(c * (gate + 0.044715 * gate ** 3))
-    return dy * (0.5 * (1 + t) + 0.5 * gate * (1 - t * t) * c * (1 + 3 * 0.044715 * gate ** 2)), None
+    p, slope = _gelu(gate)
+    return dy * (p + gate * 2 * p * (1 - p) * slope), None
