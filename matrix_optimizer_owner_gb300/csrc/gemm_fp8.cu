@@ -83,23 +83,85 @@ __device__ __forceinline__ void fence_async_smem() {
 }
 
 // ---------------------------------------------------------------- scales
+enum ScaleForm : int32_t { kBytes = 0, kRowWords = 1, kColWords = 2 };
 struct ScaleArgs {
   const uint8_t* s;
   int64_t sr, sk;             // bytes between rows' groups and between blocks of k
   int32_t shift;              // 7: a scale serves 128 rows
-  int32_t word;               // four blocks' bytes lie in an aligned word
+  int32_t form;               // kRowWords: four blocks' bytes lie in an aligned word;
+                              // kColWords: four rows' do
 };
-// The scale bytes of blocks kb .. kb + 3 of one row; 1 past the end (where the operand is zero).
-__device__ __forceinline__ uint32_t scale_word(const ScaleArgs& p, int64_t row, int64_t rows, int kb,
-                                               int nkb) {
-  if (row >= rows) return 0x7F7F7F7Fu;
-  const uint8_t* s = p.s + (row >> p.shift) * p.sr + (int64_t)kb * p.sk;
-  if (p.word && (kb & 3) == 0 && kb + 4 <= nkb) return *reinterpret_cast<const uint32_t*>(s);
-  uint32_t w = 0u;
+
+// The scale words of 128 rows from row0 (a multiple of 128) and blocks kb .. kb + 3: word j of lane l
+// is that of row row0 + 32 j + l, or with kColWords of row0 + 4 l + j.  Past the end, where the
+// operand is zero, scales are 1.  Every load is issued before any is used (addresses are clamped
+// rather than guarded): one after the other, a group of loads would take longer than its products.
+__device__ __forceinline__ void load_scales(const ScaleArgs& p, int64_t row0, int64_t rows, int kb,
+                                            int nkb, int lane, uint32_t (&v)[4]) {
+  const int live = min(4, nkb - kb);                     // >= 1
+  const uint32_t past = live < 4 ? 0x7F7F7F7Fu << (8 * live) : 0u;
+  const uint32_t keep = live < 4 ? (1u << (8 * live)) - 1u : 0xFFFFFFFFu;
+  if (p.form == kColWords && live == 4 && row0 + 128 <= rows) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = *reinterpret_cast<const uint32_t*>(p.s + row0 + 4 * lane + (int64_t)(kb + j) * p.sk);
+    // from four rows of a block a word to four blocks of a row a word
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+    const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+    v[0] = __byte_perm(a, b, 0x5410);
+    v[1] = __byte_perm(a, b, 0x7632);
+    v[2] = __byte_perm(c, d, 0x5410);
+    v[3] = __byte_perm(c, d, 0x7632);
+    return;
+  }
+  if (p.shift) {                                         // the same for all 128 rows
+    const uint8_t* s = p.s + (min(row0, rows - 1) >> 7) * p.sr + (int64_t)kb * p.sk;
+    uint32_t w = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w |= (uint32_t)s[min(j, live - 1) * p.sk] << (8 * j);
+    w = (w & keep) | past;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = w;
+    return;
+  }
+  const uint8_t* s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t r = row0 + (p.form == kColWords ? 4 * lane + j : 32 * j + lane);
+    s[j] = p.s + min(r, rows - 1) * p.sr + (int64_t)kb * p.sk;
+  }
+  if (p.form == kRowWords && (kb & 3) == 0 && live == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(s[j]);
+  } else {
+    uint32_t b[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[j][i] = s[j][min(i, live - 1) * p.sk];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = ((b[j][0] | (b[j][1] << 8) | (b[j][2] << 16) | (b[j][3] << 24)) & keep) | past;
+  }
+}
+// ... into their 512 bytes of shared memory: row r at 16 (r % 32) + 4 (r / 32).  Rows past the end
+// have another row's scales beside zero values; only a NaN among those must not reach them.
+__device__ __forceinline__ void store_scales(const ScaleArgs& p, uint32_t dst, int64_t row0,
+                                             int64_t rows, int lane, uint32_t (&v)[4]) {
+  const bool cols = p.form == kColWords;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    w |= (kb + j < nkb ? (uint32_t)s[j * p.sk] : 127u) << (8 * j);
-  return w;
+    if (row0 + (cols ? 4 * lane + j : 32 * j + lane) >= rows) v[j] = 0x7F7F7F7Fu;
+  if (!cols) {
+    sts128(dst + (uint32_t)lane * 16u, make_uint4(v[0], v[1], v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t r = 4u * (uint32_t)lane + (uint32_t)j;
+      sts32(dst + (r & 31u) * 16u + (r >> 5) * 4u, v[j]);
+    }
+  }
 }
 
 struct Gemm8Args {
@@ -125,12 +187,12 @@ constexpr int kPairThreads = 352;           // warp 0 TMA, 1 MMA, 2 scales, 3-10
 constexpr int kEpi0 = 3, kEpiN = 8;
 constexpr int kStages8 = 6;
 constexpr uint32_t kStageBytes8 = 2 * kBox8;
-constexpr int kSfStages = 3;
+constexpr int kSfStages = 6;
 constexpr uint32_t kSfBytes = 3 * 512;      // A's 128 rows and B's 256
 constexpr uint32_t kStg8 = kStages8 * kStageBytes8;
 constexpr uint32_t kSf8 = kStg8 + kEpiN * 2048;
 constexpr uint32_t kBars8 = kSf8 + kSfStages * kSfBytes;
-constexpr uint32_t kPairSmem = 1024 + kBars8 + 256;
+constexpr uint32_t kPairSmem = 1024 + kBars8 + 512;
 static_assert(kPairSmem <= 227 * 1024, "shared memory");
 // Tensor memory: two accumulators of 256 columns and the scales do not fit 512 columns, so the
 // accumulators share the 32 columns 224-255 (the last of the first one, the first of the second).
@@ -249,7 +311,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   constexpr int full0 = 0, empty0 = S, sf_full0 = 2 * S, sf_empty0 = 2 * S + F,
                 sf_free0 = 2 * S + 2 * F, tfull0 = sf_free0 + 2, tempty0 = tfull0 + 2,
                 early0 = tempty0 + 2, drain = early0 + 2;
-  static_assert((drain + 2) * 8 <= 256, "barriers");
+  static_assert((drain + 2) * 8 <= 512, "barriers");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_u32(bars + i); };
@@ -394,24 +456,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ scales (both CTAs)
-    // A lane gathers the words of rows lane, lane + 32, ...: 16 bytes of each 128-row block.
     int sf = 0;
     uint32_t ph = 1;
     bool ok = true;
     for (int w = pair; w < items && ok; w += npairs) {
       const PairItem t = pair_item(P, w);
-      const int64_t a0 = (int64_t)t.tm * 256 + 128 * rank + lane, b0 = (int64_t)t.tn * 256 + lane;
+      const int64_t a0 = (int64_t)t.tm * 256 + 128 * rank, b0 = (int64_t)t.tn * 256;
       for (int kb = 0; kb < t.nk; kb += 4) {
-        uint32_t v[12];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = scale_word(P.sa, a0 + 32 * j, P.m, t.kb0 + kb, P.nkb);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[4 + j] = scale_word(P.sb, b0 + 32 * j, P.n, t.kb0 + kb, P.nkb);
+        uint32_t va[4], vb[4], vc[4];
+        load_scales(P.sa, a0, P.m, t.kb0 + kb, P.nkb, lane, va);
+        load_scales(P.sb, b0, P.n, t.kb0 + kb, P.nkb, lane, vb);
+        load_scales(P.sb, b0 + 128, P.n, t.kb0 + kb, P.nkb, lane, vc);
         if (!mbar_wait(bar(sf_empty0 + sf), ph, g)) { ok = false; break; }
-        const uint32_t dst = sbase + kSf8 + (uint32_t)sf * kSfBytes + (uint32_t)lane * 16u;
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          sts128(dst + 512u * j, make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        const uint32_t dst = sbase + kSf8 + (uint32_t)sf * kSfBytes;
+        store_scales(P.sa, dst, a0, P.m, lane, va);
+        store_scales(P.sb, dst + 512u, b0, P.n, lane, vb);
+        store_scales(P.sb, dst + 1024u, b0 + 128, P.n, lane, vc);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_leader(map_rank(bar(sf_full0 + sf), 0));
@@ -678,7 +738,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   // the grid's x is (tile, slice) with the slice fastest: a cluster is one tile
   const int split = (int)(blockIdx.x % (unsigned)P.splits);
   const int tile = (int)(blockIdx.x / (unsigned)P.splits);
-  const int w0 = (tile % P.tiles_m) * 128, t0 = tile / P.tiles_m * NT;
+  const int w0 = tile * 128;
   const int kb0 = min(split * P.kb_split, P.nkb), nk = min(P.kb_split, P.nkb - kb0);
 
   if (warp == 0) {
@@ -691,7 +751,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         const int k0 = kb * kB8;
         expect_tx_p(true, fb, C::kStage);
         tma_load_p(true, dst, &P.a, P.a_mn ? w0 : k0, P.a_mn ? k0 : w0, fb);
-        tma_load_p(true, dst + kBox8, &P.b, P.b_mn ? t0 : k0, P.b_mn ? k0 : t0, fb);
+        tma_load_p(true, dst + kBox8, &P.b, P.b_mn ? 0 : k0, P.b_mn ? k0 : 0, fb);
         armed |= 1u << stage;
         last_par = (last_par & ~(1u << stage)) | ((ph ^ 1u) << stage);
         if (++stage == S) { stage = 0; ph ^= 1u; }
@@ -739,18 +799,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     int sf = 0;
     uint32_t ph = 1;
     for (int kb = 0; kb < nk; kb += 4) {
-      uint32_t v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = scale_word(P.sa, w0 + 32 * j + lane, P.m, kb0 + kb, P.nkb);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[4 + j] = 32 * j + lane < NT ? scale_word(P.sb, t0 + 32 * j + lane, P.n, kb0 + kb, P.nkb)
-                                      : 0x7F7F7F7Fu;
+      uint32_t va[4], vb[4];
+      load_scales(P.sa, w0, P.m, kb0 + kb, P.nkb, lane, va);
+      load_scales(P.sb, 0, P.n, kb0 + kb, P.nkb, lane, vb);
       if (!mbar_wait(bar(sf_empty0 + sf), ph, g)) break;
-      const uint32_t dst = sbase + C::kSf + (uint32_t)sf * 1024u + (uint32_t)lane * 16u;
-      sts128(dst, make_uint4(v[0], v[1], v[2], v[3]));
-      sts128(dst + 512u, make_uint4(v[4], v[5], v[6], v[7]));
+      const uint32_t dst = sbase + C::kSf + (uint32_t)sf * 1024u;
+      store_scales(P.sa, dst, w0, P.m, lane, va);
+      store_scales(P.sb, dst + 512u, 0, P.n, lane, vb);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sf_full0 + sf));
@@ -787,7 +842,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   cluster_sync_all();
   {
     // this CTA's share of the tile: narrow indices split, split + splits, ..., two rows of 64 lanes
-    const int live = min(NT, P.n - t0), wide = min(128, P.m - w0);
+    const int live = min(NT, P.n), wide = min(128, P.m - w0);
     const uint32_t mine = smem_u32(sums);
     for (int e = threadIdx.x; e < 128 * NT; e += kNarrowThreads) {
       const int t = e >> 7, r = e & 127;
@@ -801,7 +856,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                      : "memory");
         v = i == 0 ? o : v + o;
       }
-      const int64_t at = (int64_t)(w0 + r) * P.sw + (int64_t)(t0 + t) * P.st;
+      const int64_t at = (int64_t)(w0 + r) * P.sw + (int64_t)t * P.st;
       if (P.c_bf16) {
         bf16_t* c = static_cast<bf16_t*>(P.c) + at;
         *c = from_f32<bf16_t>(P.accumulate ? v + to_f32(*c) : v);
@@ -887,7 +942,8 @@ ScaleArgs scales_of(const mfsdp_fp8_matrix& m, bool along_rows) {
   s.sr = along_rows ? 1 : m.ld_scales;
   s.sk = along_rows ? m.ld_scales : 1;
   s.shift = m.groups == MFSDP_GROUPS_TILE ? 7 : 0;
-  s.word = !along_rows && m.ld_scales % 4 == 0 && aligned_to(m.scales, 4);
+  if (m.ld_scales % 4 == 0 && aligned_to(m.scales, 4))
+    s.form = !along_rows ? kRowWords : s.shift ? kBytes : kColWords;
   return s;
 }
 
