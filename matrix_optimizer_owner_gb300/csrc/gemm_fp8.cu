@@ -29,6 +29,19 @@ __device__ __forceinline__ uint64_t operand_desc8(uint32_t base, int mn_major, i
   return mn_major ? smem_desc(base + (uint32_t)j * 4096u, kBox8, 1024u)
                   : smem_desc(base + (uint32_t)j * 32u, 16u, 1024u);
 }
+// The same with the low word's changing part apart: `at` is a stage's offset, in 16 bytes.
+struct Desc8 {
+  uint32_t lo, hi, step;
+  __device__ __forceinline__ Desc8(uint32_t base, int mn_major) {
+    const uint64_t d = operand_desc8(base, mn_major, 0);
+    lo = (uint32_t)d;
+    hi = (uint32_t)(d >> 32);
+    step = mn_major ? 4096u >> 4 : 32u >> 4;
+  }
+  __device__ __forceinline__ uint64_t at(uint32_t off, int j) const {
+    return ((uint64_t)hi << 32) | (lo + off + (uint32_t)j * step);
+  }
+};
 // Scale words: 32 rows of 16 bytes, unswizzled (eight rows 128 bytes apart from the next eight).
 __device__ __forceinline__ uint64_t scale_desc(uint32_t base) {
   return (uint64_t)((base >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
@@ -94,55 +107,75 @@ struct ScaleArgs {
 
 // The scale words of 128 rows from row0 (a multiple of 128) and blocks kb .. kb + 3: word j of lane l
 // is that of row row0 + 32 j + l, or with kColWords of row0 + 4 l + j.  Past the end, where the
-// operand is zero, scales are 1.  Every load is issued before any is used (addresses are clamped
-// rather than guarded): one after the other, a group of loads would take longer than its products.
-__device__ __forceinline__ void load_scales(const ScaleArgs& p, int64_t row0, int64_t rows, int kb,
-                                            int nkb, int lane, uint32_t (&v)[4]) {
-  const int live = min(4, nkb - kb);                     // >= 1
-  const uint32_t past = live < 4 ? 0x7F7F7F7Fu << (8 * live) : 0u;
-  const uint32_t keep = live < 4 ? (1u << (8 * live)) - 1u : 0xFFFFFFFFu;
-  if (p.form == kColWords && live == 4 && row0 + 128 <= rows) {
-    uint32_t w[4];
+// operand is zero, scales are 1.  In two steps, the loads and what is made of them, so that a warp has
+// all loads of a group under way before it waits for one (addresses are clamped rather than guarded):
+// with a wait after each of a group's three loads, the scales took 3400 cycles per four blocks, whose
+// products take 2048.
+struct ScaleAt {
+  int64_t row0;
+  int kb, live;               // live: blocks, 1 to 4
+  int how;                    // 0 words of four rows, 1 one row group, 2 words of four blocks, 3 bytes
+  __device__ __forceinline__ ScaleAt(const ScaleArgs& p, int64_t row0_, int64_t rows, int kb_, int nkb)
+      : row0(row0_), kb(kb_), live(min(4, nkb - kb_)) {
+    how = p.form == kColWords && live == 4 && row0 + 128 <= rows ? 0
+          : p.shift                                              ? 1
+          : p.form == kRowWords && (kb & 3) == 0 && live == 4    ? 2
+                                                                 : 3;
+  }
+};
+struct ScaleRaw {
+  uint32_t r[16];
+};
+__device__ __forceinline__ void issue_scales(const ScaleArgs& p, const ScaleAt& at, int64_t rows,
+                                             int lane, ScaleRaw& raw) {
+  if (at.how == 0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      w[j] = *reinterpret_cast<const uint32_t*>(p.s + row0 + 4 * lane + (int64_t)(kb + j) * p.sk);
+      raw.r[j] = *reinterpret_cast<const uint32_t*>(p.s + at.row0 + 4 * lane +
+                                                    (int64_t)(at.kb + j) * p.sk);
+  } else if (at.how == 1) {                              // the same for all 128 rows
+    const uint8_t* s = p.s + (min(at.row0, rows - 1) >> 7) * p.sr + (int64_t)at.kb * p.sk;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) raw.r[j] = s[min(j, at.live - 1) * p.sk];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t r = at.row0 + (p.form == kColWords ? 4 * lane + j : 32 * j + lane);
+      const uint8_t* s = p.s + min(r, rows - 1) * p.sr + (int64_t)at.kb * p.sk;
+      if (at.how == 2) {
+        raw.r[j] = *reinterpret_cast<const uint32_t*>(s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw.r[4 * j + i] = s[min(i, at.live - 1) * p.sk];
+      }
+    }
+  }
+}
+__device__ __forceinline__ void finish_scales(const ScaleAt& at, const ScaleRaw& raw,
+                                              uint32_t (&v)[4]) {
+  const uint32_t past = at.live < 4 ? 0x7F7F7F7Fu << (8 * at.live) : 0u;
+  const uint32_t keep = at.live < 4 ? (1u << (8 * at.live)) - 1u : 0xFFFFFFFFu;
+  const uint32_t(&r)[16] = raw.r;
+  if (at.how == 0) {
     // from four rows of a block a word to four blocks of a row a word
-    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
-    const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+    const uint32_t a = __byte_perm(r[0], r[1], 0x5140), b = __byte_perm(r[2], r[3], 0x5140);
+    const uint32_t c = __byte_perm(r[0], r[1], 0x7362), d = __byte_perm(r[2], r[3], 0x7362);
     v[0] = __byte_perm(a, b, 0x5410);
     v[1] = __byte_perm(a, b, 0x7632);
     v[2] = __byte_perm(c, d, 0x5410);
     v[3] = __byte_perm(c, d, 0x7632);
-    return;
-  }
-  if (p.shift) {                                         // the same for all 128 rows
-    const uint8_t* s = p.s + (min(row0, rows - 1) >> 7) * p.sr + (int64_t)kb * p.sk;
-    uint32_t w = 0u;
+  } else if (at.how == 2) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w |= (uint32_t)s[min(j, live - 1) * p.sk] << (8 * j);
-    w = (w & keep) | past;
+    for (int j = 0; j < 4; ++j) v[j] = r[j];
+  } else if (at.how == 1) {
+    const uint32_t w = ((r[0] | (r[1] << 8) | (r[2] << 16) | (r[3] << 24)) & keep) | past;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = w;
-    return;
-  }
-  const uint8_t* s[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t r = row0 + (p.form == kColWords ? 4 * lane + j : 32 * j + lane);
-    s[j] = p.s + min(r, rows - 1) * p.sr + (int64_t)kb * p.sk;
-  }
-  if (p.form == kRowWords && (kb & 3) == 0 && live == 4) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(s[j]);
   } else {
-    uint32_t b[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[j][i] = s[j][min(i, live - 1) * p.sk];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = ((b[j][0] | (b[j][1] << 8) | (b[j][2] << 16) | (b[j][3] << 24)) & keep) | past;
+      v[j] = ((r[4 * j] | (r[4 * j + 1] << 8) | (r[4 * j + 2] << 16) | (r[4 * j + 3] << 24)) & keep) |
+             past;
   }
 }
 // ... into their 512 bytes of shared memory: row r at 16 (r % 32) + 4 (r / 32).  Rows past the end
@@ -171,7 +204,6 @@ struct Gemm8Args {
   int32_t a_mn, b_mn;
   uint32_t idesc;
   int32_t tiles_m, tiles_n, splits, kb_split;
-  int32_t chunk;              // blocks added up in tensor memory before registers take over
   void* c;
   int64_t ld_c;
   int32_t c_bf16, accumulate, vec;
@@ -183,12 +215,12 @@ struct Gemm8Args {
 };
 
 // ---------------------------------------------------------------- 256 x 256 tiles
-constexpr int kPairThreads = 352;           // warp 0 TMA, 1 MMA, 2 scales, 3-10 epilogue
-constexpr int kEpi0 = 3, kEpiN = 8;
+constexpr int kPairThreads = 384;           // warp 0 TMA, 1 MMA, 2-3 scales, 4-11 epilogue
+constexpr int kEpi0 = 4, kEpiN = 8;
 constexpr int kStages8 = 6;
 constexpr uint32_t kStageBytes8 = 2 * kBox8;
-constexpr int kSfStages = 6;
-constexpr uint32_t kSfBytes = 3 * 512;      // A's 128 rows and B's 256
+constexpr int kSfStages = 4;
+constexpr uint32_t kSfBytes = 2 * 3 * 512;  // eight blocks of A's 128 rows and B's 256
 constexpr uint32_t kStg8 = kStages8 * kStageBytes8;
 constexpr uint32_t kSf8 = kStg8 + kEpiN * 2048;
 constexpr uint32_t kBars8 = kSf8 + kSfStages * kSfBytes;
@@ -199,6 +231,7 @@ static_assert(kPairSmem <= 227 * 1024, "shared memory");
 // The epilogue reads the shared columns of a tile first and says so, and the next tile's products
 // wait for that alone.
 constexpr uint32_t kAcc1 = 224, kSfCol = 480;
+constexpr int kChunk8 = 8;                  // blocks added up in tensor memory (CHUNKED): 1024 of k
 constexpr int kRasterRows = 8;              // tile rows that walk the columns together
 
 struct PairItem {
@@ -393,88 +426,117 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader only)
+    // One thread issues every product of the pair, so what it does between them has to stay below
+    // their own time (512 cycles a block): descriptors differ by a sum in their low word, and a
+    // group's four blocks are unrolled with their scale ids.
     if (lane == 0 && leader) {
       int stage = 0, sf = 0, acc = 0, buf = 0;
       uint32_t phase = 0, sf_phase = 0, acc_phase = 0, buf_phase = 1;
       bool ok = true, first = true;
+      const Desc8 da(sbase, P.a_mn), db(sbase + kBox8, P.b_mn);
       for (int w = pair; w < items && ok; w += npairs) {
         const PairItem t = pair_item(P, w);
-        const int chunk = CHUNKED ? P.chunk : t.nk;
-        for (int kb = 0; kb < t.nk && ok; ++kb) {
-          const int in_chunk = CHUNKED ? kb % chunk : kb;
+        int in_chunk = 0;                                 // blocks in the accumulator
+        for (int kb = 0; kb < t.nk && ok; kb += 4) {
           if (in_chunk == 0) {
-            if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g)) { ok = false; break; }
-            // the columns shared with the accumulator before this one
-            if (!first && !mbar_wait_cl(bar(early0 + (acc ^ 1)), acc ? acc_phase : acc_phase ^ 1u, g)) {
+            // the accumulator, and the columns that it shares with the one before
+            if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g) ||
+                (!first &&
+                 !mbar_wait_cl(bar(early0 + (acc ^ 1)), acc ? acc_phase : acc_phase ^ 1u, g))) {
               ok = false;
               break;
             }
             first = false;
-            tc_fence_after();
           }
+          // the scales of four blocks, into the columns that the last but one group has left
           const uint32_t sfa = tmem_base + kSfCol + (uint32_t)buf * 16u, sfb = sfa + 4u;
-          if ((kb & 3) == 0) {
-            // the scales of four blocks, into the columns that the last but one group has left
-            if (!mbar_wait_cl(bar(sf_full0 + sf), sf_phase, g) ||
-                !mbar_wait(bar(sf_free0 + buf), buf_phase, g)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t src = sbase + kSf8 + (uint32_t)sf * kSfBytes;
-            copy_scales<2>(sfa, scale_desc(src));
-            copy_scales<2>(sfb, scale_desc(src + 512u));
-            copy_scales<2>(sfb + 4u, scale_desc(src + 1024u));
+          if (((kb & 4) == 0 && !mbar_wait_cl(bar(sf_full0 + sf), sf_phase, g)) ||
+              !mbar_wait(bar(sf_free0 + buf), buf_phase, g)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t src = sbase + kSf8 + (uint32_t)sf * kSfBytes + (kb & 4 ? 1536u : 0u);
+          copy_scales<2>(sfa, scale_desc(src));
+          copy_scales<2>(sfb, scale_desc(src + 512u));
+          copy_scales<2>(sfb + 4u, scale_desc(src + 1024u));
+          if ((kb & 4) || kb + 4 >= t.nk) {               // the stage's last group
             tc_commit_pair(bar(sf_empty0 + sf), 0x3);
             if (++sf == F) { sf = 0; sf_phase ^= 1u; }
           }
-          if (!mbar_wait(bar(full0 + stage), phase, g)) { ok = false; break; }
-          tc_fence_after();
           const uint32_t d = tmem_base + (acc ? kAcc1 : 0u);
-          const uint32_t sm_a = sbase + (uint32_t)stage * kStageBytes8;
-          const uint32_t idesc = with_scale_id(P.idesc, kb & 3);
+          const int live = min(4, t.nk - kb);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma8<2>(d, operand_desc8(sm_a, P.a_mn, j), operand_desc8(sm_a + kBox8, P.b_mn, j), idesc,
-                    sfa, sfb, (in_chunk | j) != 0);
-          tc_commit_pair(bar(empty0 + stage), 0x3);
-          if (++stage == S) { stage = 0; phase ^= 1u; }
-          if ((kb & 3) == 3 || kb + 1 == t.nk) {
-            tc_commit_pair(bar(sf_free0 + buf), 0x1);
-            buf ^= 1;
-            if (buf == 0) buf_phase ^= 1u;
+          for (int i = 0; i < 4; ++i) {
+            if (i < live && ok) {
+              ok = mbar_wait(bar(full0 + stage), phase, g);
+              if (ok) {
+                tc_fence_after();
+                const uint32_t at = (uint32_t)stage * (kStageBytes8 >> 4);
+                const uint32_t idesc = with_scale_id(P.idesc, i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  mma8<2>(d, da.at(at, j), db.at(at, j), idesc, sfa, sfb, (in_chunk | i | j) != 0);
+                tc_commit_pair(bar(empty0 + stage), 0x3);
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+              }
+            }
           }
-          if (in_chunk + 1 == chunk || kb + 1 == t.nk) {
+          if (!ok) break;
+          tc_commit_pair(bar(sf_free0 + buf), 0x1);
+          buf ^= 1;
+          if (buf == 0) buf_phase ^= 1u;
+          in_chunk += 4;
+          if (kb + 4 >= t.nk || (CHUNKED && in_chunk == kChunk8)) {
             tc_commit_pair(bar(tfull0 + acc), 0x3);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
+            in_chunk = 0;
           }
         }
       }
       tc_commit_pair(bar(drain), 0x1);
       mbar_wait(bar(drain), 0u, g, false);
     }
-  } else if (warp == 2) {
+  } else if (warp < kEpi0) {
     // ------------------------------------------------------------ scales (both CTAs)
-    int sf = 0;
+    // A stage holds the scales of eight blocks; the two warps take the stages in turn, each with all
+    // of its loads under way before it waits for one.
+    int sf = 0, turn = 0;
     uint32_t ph = 1;
     bool ok = true;
     for (int w = pair; w < items && ok; w += npairs) {
       const PairItem t = pair_item(P, w);
       const int64_t a0 = (int64_t)t.tm * 256 + 128 * rank, b0 = (int64_t)t.tn * 256;
-      for (int kb = 0; kb < t.nk; kb += 4) {
-        uint32_t va[4], vb[4], vc[4];
-        load_scales(P.sa, a0, P.m, t.kb0 + kb, P.nkb, lane, va);
-        load_scales(P.sb, b0, P.n, t.kb0 + kb, P.nkb, lane, vb);
-        load_scales(P.sb, b0 + 128, P.n, t.kb0 + kb, P.nkb, lane, vc);
-        if (!mbar_wait(bar(sf_empty0 + sf), ph, g)) { ok = false; break; }
-        const uint32_t dst = sbase + kSf8 + (uint32_t)sf * kSfBytes;
-        store_scales(P.sa, dst, a0, P.m, lane, va);
-        store_scales(P.sb, dst + 512u, b0, P.n, lane, vb);
-        store_scales(P.sb, dst + 1024u, b0 + 128, P.n, lane, vc);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_leader(map_rank(bar(sf_full0 + sf), 0));
+      for (int kb = 0; kb < t.nk; kb += 8) {
+        if (turn == warp - 2) {
+          ScaleRaw raw[2][3];
+          auto each = [&](auto&& f) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (kb + 4 * h >= t.nk) break;
+              const int k0 = t.kb0 + kb + 4 * h;
+              f(P.sa, ScaleAt(P.sa, a0, P.m, k0, P.nkb), P.m, h, 0);
+              f(P.sb, ScaleAt(P.sb, b0, P.n, k0, P.nkb), P.n, h, 1);
+              f(P.sb, ScaleAt(P.sb, b0 + 128, P.n, k0, P.nkb), P.n, h, 2);
+            }
+          };
+          each([&](const ScaleArgs& p, const ScaleAt& at, int64_t rows, int h, int i) {
+            issue_scales(p, at, rows, lane, raw[h][i]);
+          });
+          ok = mbar_wait(bar(sf_empty0 + sf), ph, g);
+          if (!ok) break;
+          const uint32_t dst = sbase + kSf8 + (uint32_t)sf * kSfBytes;
+          each([&](const ScaleArgs& p, const ScaleAt& at, int64_t rows, int h, int i) {
+            uint32_t v[4];
+            finish_scales(at, raw[h][i], v);
+            store_scales(p, dst + 1536u * h + 512u * i, at.row0, rows, lane, v);
+          });
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_leader(map_rank(bar(sf_full0 + sf), 0));
+        }
+        turn ^= 1;
         if (++sf == F) { sf = 0; ph ^= 1u; }
       }
     }
@@ -542,7 +604,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int k = 0; k < 32; ++k) sum[q][k] = 0.f;
-        for (int left = t.nk; left > 0; left -= P.chunk) {
+        for (int left = t.nk; left > 0; left -= kChunk8) {
           if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) { ok = false; break; }
           tc_fence_after();
           const int sh = shared_chunk();
@@ -800,8 +862,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     uint32_t ph = 1;
     for (int kb = 0; kb < nk; kb += 4) {
       uint32_t va[4], vb[4];
-      load_scales(P.sa, w0, P.m, kb0 + kb, P.nkb, lane, va);
-      load_scales(P.sb, 0, P.n, kb0 + kb, P.nkb, lane, vb);
+      const ScaleAt a(P.sa, w0, P.m, kb0 + kb, P.nkb), b(P.sb, 0, P.n, kb0 + kb, P.nkb);
+      ScaleRaw ra, rb;
+      issue_scales(P.sa, a, P.m, lane, ra);
+      issue_scales(P.sb, b, P.n, lane, rb);
+      finish_scales(a, ra, va);
+      finish_scales(b, rb, vb);
       if (!mbar_wait(bar(sf_empty0 + sf), ph, g)) break;
       const uint32_t dst = sbase + C::kSf + (uint32_t)sf * 1024u;
       store_scales(P.sa, dst, w0, P.m, lane, va);
@@ -1094,7 +1160,6 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   // sums that are kept in fp32 are added up in registers every 1024 of k, others where the cuts
   // would come near half a bf16 step.
   const bool chunked = !g.c_bf16 || g.kb_split > 512;
-  g.chunk = 8;
   const int pairs = std::max(1, std::min(sms / 2, g.tiles_m * g.tiles_n * g.splits));
   static std::atomic<bool> done[2][64];
   if (chunked) {
