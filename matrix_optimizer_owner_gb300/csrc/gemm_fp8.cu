@@ -206,7 +206,8 @@ struct Gemm8Args {
   int32_t tiles_m, tiles_n, splits, kb_split;
   void* c;
   int64_t ld_c;
-  int32_t c_bf16, accumulate, vec;
+  int32_t c_bf16, accumulate;
+  int32_t vec;                // C's rows: 0 as they come, 1 on 16-byte boundaries, 2 on 32-byte ones
   float* part;                // splits > 1: [splits][m][ld_part]
   int64_t ld_part;
   int64_t sw, st;             // narrow kernel: C's strides along the wide and the narrow side
@@ -252,54 +253,103 @@ __device__ __forceinline__ PairItem pair_item(const Gemm8Args& P, int w) {
   return t;
 }
 
-// A staged block of 32 rows x 64 bytes (32 bf16 or 16 fp32 columns) to C or to a split's partial sums.
-struct BlockOut {
-  const Gemm8Args& P;
-  int64_t r0;                 // the block's first row
-  int lane;
-  float* part;                // nullable
+__device__ __forceinline__ void st256(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
-  __device__ __forceinline__ void store(uint32_t stg, int64_t c0) const {
-    const bool f32 = part || !P.c_bf16;
-    const int per = f32 ? 4 : 8, width = f32 ? 16 : 32;
-    if (part ? true : P.vec) {
+// 32 columns of a lane's row to C or to a split's partial sums.  Rows on 32-byte boundaries are
+// written straight from registers, a whole sector at a time: staged through shared memory, so that a
+// warp's stores covered 64 bytes of a row, a tile's epilogue took twice the time (3.7 us).  Rows
+// without 16-byte alignment go through the warp's staging area (2 KB), a row of the block at a time.
+__device__ __forceinline__ void put_row(const Gemm8Args& P, float* part, int64_t rw, int lane,
+                                        int64_t c0, uint32_t stg, const float (&v)[32]) {
+  const int64_t r = rw + lane;
+  const bool f32 = part || !P.c_bf16;
+  if (part || P.vec) {
+    if (r >= P.m) return;
+    if (!f32) {
+      uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 8 * i + (lane >> 2), k = lane & 3;
-        const int64_t r = r0 + row, c = c0 + k * per;
-        if (r >= P.m || c >= P.n) continue;
-        const uint4 w = lds128(stg + stg_off(row, k));
-        if (part) {           // rows of whole vectors
-          *reinterpret_cast<uint4*>(part + r * P.ld_part + c) = w;
-        } else if (c + per <= P.n) {
-          uint4* d = f32 ? reinterpret_cast<uint4*>(static_cast<float*>(P.c) + r * P.ld_c + c)
-                         : reinterpret_cast<uint4*>(static_cast<bf16_t*>(P.c) + r * P.ld_c + c);
-          *d = w;
-        } else {
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          for (int j = 0; c + j < P.n; ++j) {
-            if (f32)
-              static_cast<uint32_t*>(P.c)[r * P.ld_c + c + j] = j == 0 ? u[0] : j == 1 ? u[1] : u[2];
-            else
-              static_cast<uint16_t*>(P.c)[r * P.ld_c + c + j] = (uint16_t)(
-                  ((j >> 1) == 0 ? u[0] : (j >> 1) == 1 ? u[1] : (j >> 1) == 2 ? u[2] : u[3]) >>
-                  (16 * (j & 1)));
+      for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+      bf16_t* d = static_cast<bf16_t*>(P.c) + r * P.ld_c + c0;
+      if (c0 + 32 <= P.n && P.vec == 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t o[8] = {w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
+                                 w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
+          st256(d + 16 * h, o);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (c0 + 8 * h + 8 <= P.n) {
+            reinterpret_cast<uint4*>(d)[h] =
+                make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+          } else {
+#pragma unroll
+            for (int k = 8 * h; k < 8 * h + 8; ++k)
+              if (c0 + k < P.n)
+                reinterpret_cast<uint16_t*>(d)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
           }
         }
       }
-    } else {                  // a row of the block at a time, a lane a column
-      for (int i = 0; i < 32; ++i) {
-        const int64_t r = r0 + i, c = c0 + lane;
-        if (r >= P.m || lane >= width || c >= P.n) continue;
-        if (f32)
-          static_cast<uint32_t*>(P.c)[r * P.ld_c + c] = lds32(stg + stg_off(i, lane >> 2) + (lane & 3) * 4);
-        else
-          static_cast<uint16_t*>(P.c)[r * P.ld_c + c] = (uint16_t)(
-              lds32(stg + stg_off(i, lane >> 3) + (uint32_t)((lane & 6) * 2)) >> (16 * (lane & 1)));
+    } else {
+      float* d = part ? part + r * P.ld_part + c0 : static_cast<float*>(P.c) + r * P.ld_c + c0;
+      // (a split's rows are padded to whole vectors)
+      const int64_t n = part ? P.ld_part : P.n;
+      const bool wide = part || P.vec == 2;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if (c0 + 8 * h + 8 <= n) {
+          if (wide) {
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[8 * h + k]);
+            st256(d + 8 * h, o);
+          } else {
+            reinterpret_cast<float4*>(d)[2 * h] =
+                make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
+            reinterpret_cast<float4*>(d)[2 * h + 1] =
+                make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 8 * h; k < 8 * h + 8; ++k)
+            if (c0 + k < n) d[k] = v[k];
+        }
       }
     }
+    return;
   }
-};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {             // 32 columns of bf16, or 16 of fp32 at a time
+    if (!f32 && h == 1) break;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = f32 ? __float_as_uint(v[16 * h + 4 * k + i])
+                   : pack_bf16x2(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+      sts128(stg + stg_off(lane, k), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+    __syncwarp();
+    const int64_t c = c0 + 16 * h + lane;
+    const bool in = (f32 ? lane < 16 : true) && c < P.n;
+    for (int i = 0; i < 32 && rw + i < P.m; ++i) {
+      if (!in) continue;
+      const int64_t at = (rw + i) * P.ld_c + c;
+      if (f32)
+        static_cast<uint32_t*>(P.c)[at] = lds32(stg + stg_off(i, lane >> 2) + (lane & 3) * 4);
+      else
+        static_cast<uint16_t*>(P.c)[at] = (uint16_t)(
+            lds32(stg + stg_off(i, lane >> 3) + (uint32_t)((lane & 6) * 2)) >> (16 * (lane & 1)));
+    }
+  }
+}
 
 // What C held, for this lane's row and 32 columns (added before the rounding).
 __device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c0, float (&v)[32]) {
@@ -554,38 +604,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t cb = (int64_t)t.tn * 256 + half * 128;
       const int nq = rw < P.m && cb < P.n ? (int)min((int64_t)4, (P.n - cb + 31) / 32) : 0;
       float* part = P.splits > 1 ? P.part + (int64_t)t.split * P.m * P.ld_part : nullptr;
-      const BlockOut out{P, rw, lane, part};
       const bool old = P.accumulate && !part;
-      auto put = [&](int q, const uint32_t (&a)[32]) {
-        float v[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(a[k]);
-        const int64_t c0 = cb + 32 * q;
-        if (old) add_old(P, rw + lane, c0, v);
-        if (!part && P.c_bf16) {
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            sts128(stg + stg_off(lane, k),
-                   make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                              pack_bf16x2(v[8 * k + 4], v[8 * k + 5]),
-                              pack_bf16x2(v[8 * k + 6], v[8 * k + 7])));
-          __syncwarp();
-          out.store(stg, c0);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              sts128(stg + stg_off(lane, k),
-                     make_uint4(__float_as_uint(v[16 * h + 4 * k]), __float_as_uint(v[16 * h + 4 * k + 1]),
-                                __float_as_uint(v[16 * h + 4 * k + 2]),
-                                __float_as_uint(v[16 * h + 4 * k + 3])));
-            __syncwarp();
-            out.store(stg, c0 + 16 * h);
-          }
-        }
+      auto put = [&](int q, float (&v)[32]) {
+        if (old) add_old(P, rw + lane, cb + 32 * q, v);
+        put_row(P, part, rw, lane, cb + 32 * q, stg, v);
       };
       // the shared columns: this warp's chunk `sh` of this accumulator, if it holds them
       auto shared_chunk = [&]() { return acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1); };
@@ -642,27 +664,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (q < nq) {
-            uint32_t a[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(sum[q][k]);
-            put(q, a);
-          }
+          if (q < nq) put(q, sum[q]);
       } else {
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
-        const int sh = shared_chunk();
-#pragma unroll 1
+        const int sh = shared_chunk(), first = sh == 3 ? 3 : 0;   // the shared columns first
+        uint32_t buf[2][32];
+        tc_ld32_issue(base() + (uint32_t)(32 * first), buf[0]);
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int q = sh == 3 ? (i + 3) & 3 : i;        // the shared columns first
-          uint32_t a[32];
-          if (q < nq || q == sh) {
-            tc_ld32_issue(base() + (uint32_t)(32 * q), a);
-            tc_ld_wait(a);
-          }
+          const int q = (i + first) & 3;
+          uint32_t (&a)[32] = buf[i & 1];
+          tc_ld_wait(a);
           if (q == sh) release(early0);
-          if (i == 3) release(tempty0);                   // the last read: the stores can follow it
-          if (q < nq) put(q, a);
+          if (i < 3)
+            tc_ld32_issue(base() + (uint32_t)(32 * ((q + 1) & 3)), buf[(i + 1) & 1]);
+          else
+            release(tempty0);                             // the last read: the stores can follow it
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(a[k]);
+          if (q < nq) put(q, v);
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
@@ -989,7 +1011,7 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
     }
   }
   if (p.splits == 1) p.kb_split = nkb;
-  p.ld_part = (n + 3) / 4 * 4;
+  p.ld_part = (n + 7) / 8 * 8;
   p.bytes = p.splits > 1 ? (size_t)p.splits * m * p.ld_part * 4 : 0;
   return p;
 }
@@ -1094,12 +1116,13 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   int* status = device_status();
   if (!status) return MFSDP_ECUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int vec = vector_rows(c, ld_c, c_dtype);
+  const int vec = !vector_rows(c, ld_c, c_dtype) ? 0
+                  : aligned_to(c, 32) && (ld_c * (int64_t)dtype_bytes(c_dtype)) % 32 == 0 ? 2 : 1;
   JoinArgs8 j{};
   j.part = static_cast<const float*>(workspace);
   j.m = m;
   j.n = n;
-  j.ld_part = (n + 3) / 4 * 4;
+  j.ld_part = (n + 7) / 8 * 8;
   j.ld_c = ld_c;
   j.splits = k ? plan.splits : 0;
   j.c_bf16 = c_dtype == MFSDP_DTYPE_BF16;
