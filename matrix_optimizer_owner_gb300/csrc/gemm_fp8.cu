@@ -259,14 +259,42 @@ __device__ __forceinline__ void st256(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// 32 columns of a lane's row to C or to a split's partial sums.  Rows on 32-byte boundaries are
-// written straight from registers, a whole sector at a time: staged through shared memory, so that a
-// warp's stores covered 64 bytes of a row, a tile's epilogue took twice the time (3.7 us).  Rows
-// without 16-byte alignment go through the warp's staging area (2 KB), a row of the block at a time.
-__device__ __forceinline__ void put_row(const Gemm8Args& P, float* part, int64_t rw, int lane,
-                                        int64_t c0, uint32_t stg, const float (&v)[32]) {
+// What C held, for this lane's row and 32 columns (added before the rounding).
+__device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c0, float (&v)[32]) {
+  if (r >= P.m) return;
+  if (P.vec && c0 + 32 <= P.n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float o[8];
+      if (P.c_bf16) {
+        Pack8<bf16_t> q;
+        q.load(static_cast<const bf16_t*>(P.c) + r * P.ld_c + c0 + 8 * k);
+        q.get(o);
+      } else {
+        Pack8<float> q;
+        q.load(static_cast<const float*>(P.c) + r * P.ld_c + c0 + 8 * k);
+        q.get(o);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * k + j] += o[j];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (c0 + k < P.n)
+        v[k] += P.c_bf16 ? to_f32(static_cast<const bf16_t*>(P.c)[r * P.ld_c + c0 + k])
+                         : static_cast<const float*>(P.c)[r * P.ld_c + c0 + k];
+  }
+}
+
+// 32 columns of a lane's row to C or to a split's partial sums, whatever C's rows, edges and old values
+// are.  Rows without 16-byte alignment go through the warp's staging area (2 KB), a row of the block at
+// a time.
+__device__ __noinline__ void put_row(const Gemm8Args& P, float* part, int64_t rw, int lane,
+                                     int64_t c0, uint32_t stg, float (&v)[32]) {
   const int64_t r = rw + lane;
   const bool f32 = part || !P.c_bf16;
+  if (P.accumulate && !part) add_old(P, r, c0, v);
   if (part || P.vec) {
     if (r >= P.m) return;
     if (!f32) {
@@ -274,46 +302,29 @@ __device__ __forceinline__ void put_row(const Gemm8Args& P, float* part, int64_t
 #pragma unroll
       for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
       bf16_t* d = static_cast<bf16_t*>(P.c) + r * P.ld_c + c0;
-      if (c0 + 32 <= P.n && P.vec == 2) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t o[8] = {w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
-                                 w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
-          st256(d + 16 * h, o);
-        }
-      } else {
+      for (int h = 0; h < 4; ++h) {
+        if (c0 + 8 * h + 8 <= P.n) {
+          reinterpret_cast<uint4*>(d)[h] =
+              make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          if (c0 + 8 * h + 8 <= P.n) {
-            reinterpret_cast<uint4*>(d)[h] =
-                make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-          } else {
-#pragma unroll
-            for (int k = 8 * h; k < 8 * h + 8; ++k)
-              if (c0 + k < P.n)
-                reinterpret_cast<uint16_t*>(d)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-          }
+          for (int k = 8 * h; k < 8 * h + 8; ++k)
+            if (c0 + k < P.n)
+              reinterpret_cast<uint16_t*>(d)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
         }
       }
     } else {
       float* d = part ? part + r * P.ld_part + c0 : static_cast<float*>(P.c) + r * P.ld_c + c0;
       // (a split's rows are padded to whole vectors)
       const int64_t n = part ? P.ld_part : P.n;
-      const bool wide = part || P.vec == 2;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         if (c0 + 8 * h + 8 <= n) {
-          if (wide) {
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[8 * h + k]);
-            st256(d + 8 * h, o);
-          } else {
-            reinterpret_cast<float4*>(d)[2 * h] =
-                make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
-            reinterpret_cast<float4*>(d)[2 * h + 1] =
-                make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
-          }
+          reinterpret_cast<float4*>(d)[2 * h] =
+              make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
+          reinterpret_cast<float4*>(d)[2 * h + 1] =
+              make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
         } else {
 #pragma unroll
           for (int k = 8 * h; k < 8 * h + 8; ++k)
@@ -351,31 +362,32 @@ __device__ __forceinline__ void put_row(const Gemm8Args& P, float* part, int64_t
   }
 }
 
-// What C held, for this lane's row and 32 columns (added before the rounding).
-__device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c0, float (&v)[32]) {
+// The same where all 32 columns are there, rows start on 32-byte boundaries and nothing is added: a
+// lane writes its row straight from registers, a whole sector at a time.  (Staged through shared
+// memory, so that a warp's stores covered 64 bytes of a row, a tile's epilogue took twice the time.  It
+// has few instructions on purpose: with every case inlined and unrolled, the warps waited mostly for
+// instructions.)
+__device__ __forceinline__ void put_whole(const Gemm8Args& P, float* part, int64_t r, int64_t c0,
+                                          const float (&v)[32]) {
   if (r >= P.m) return;
-  if (P.vec && c0 + 32 <= P.n) {
+  if (!part && P.c_bf16) {
+    bf16_t* d = static_cast<bf16_t*>(P.c) + r * P.ld_c + c0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float o[8];
-      if (P.c_bf16) {
-        Pack8<bf16_t> q;
-        q.load(static_cast<const bf16_t*>(P.c) + r * P.ld_c + c0 + 8 * k);
-        q.get(o);
-      } else {
-        Pack8<float> q;
-        q.load(static_cast<const float*>(P.c) + r * P.ld_c + c0 + 8 * k);
-        q.get(o);
-      }
+    for (int h = 0; h < 2; ++h) {
+      uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 * k + j] += o[j];
+      for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(v[16 * h + 2 * k], v[16 * h + 2 * k + 1]);
+      st256(d + 16 * h, o);
     }
   } else {
+    float* d = part ? part + r * P.ld_part + c0 : static_cast<float*>(P.c) + r * P.ld_c + c0;
 #pragma unroll
-    for (int k = 0; k < 32; ++k)
-      if (c0 + k < P.n)
-        v[k] += P.c_bf16 ? to_f32(static_cast<const bf16_t*>(P.c)[r * P.ld_c + c0 + k])
-                         : static_cast<const float*>(P.c)[r * P.ld_c + c0 + k];
+    for (int h = 0; h < 4; ++h) {
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[8 * h + k]);
+      st256(d + 8 * h, o);
+    }
   }
 }
 
@@ -604,10 +616,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t cb = (int64_t)t.tn * 256 + half * 128;
       const int nq = rw < P.m && cb < P.n ? (int)min((int64_t)4, (P.n - cb + 31) / 32) : 0;
       float* part = P.splits > 1 ? P.part + (int64_t)t.split * P.m * P.ld_part : nullptr;
-      const bool old = P.accumulate && !part;
+      const bool plain = part || (P.vec == 2 && !P.accumulate);
       auto put = [&](int q, float (&v)[32]) {
-        if (old) add_old(P, rw + lane, cb + 32 * q, v);
-        put_row(P, part, rw, lane, cb + 32 * q, stg, v);
+        const int64_t c0 = cb + 32 * q;
+        if (plain && c0 + 32 <= P.n) {
+          put_whole(P, part, rw + lane, c0, v);
+        } else {
+          float o[32];                                    // (the call's copy: v stays in registers)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = v[k];
+          put_row(P, part, rw, lane, c0, stg, o);
+        }
       };
       // the shared columns: this warp's chunk `sh` of this accumulator, if it holds them
       auto shared_chunk = [&]() { return acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1); };
@@ -669,22 +688,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
         const int sh = shared_chunk(), first = sh == 3 ? 3 : 0;   // the shared columns first
+        const uint32_t at = base();
         uint32_t buf[2][32];
-        tc_ld32_issue(base() + (uint32_t)(32 * first), buf[0]);
+        tc_ld32_issue(at + (uint32_t)(32 * first), buf[0]);
+#pragma unroll 1
+        for (int i = 0; i < 4; i += 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int q = (i + first) & 3;
-          uint32_t (&a)[32] = buf[i & 1];
-          tc_ld_wait(a);
-          if (q == sh) release(early0);
-          if (i < 3)
-            tc_ld32_issue(base() + (uint32_t)(32 * ((q + 1) & 3)), buf[(i + 1) & 1]);
-          else
-            release(tempty0);                             // the last read: the stores can follow it
-          float v[32];
+          for (int h = 0; h < 2; ++h) {
+            const int q = (i + h + first) & 3;
+            uint32_t (&a)[32] = buf[h];
+            tc_ld_wait(a);
+            if (q == sh) release(early0);
+            if (i + h < 3)
+              tc_ld32_issue(at + (uint32_t)(32 * ((q + 1) & 3)), buf[h ^ 1]);
+            else
+              release(tempty0);                           // the last read: the stores can follow it
+            float v[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(a[k]);
-          if (q < nq) put(q, v);
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(a[k]);
+            if (q < nq) put(q, v);
+          }
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
