@@ -33,137 +33,149 @@ struct ActArgs {
   int32_t vec;
 };
 
-// 1 / (1 + exp(-x)); exp and the division are the special-function unit's (within 2 ulp each).
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-template <bool GLU>
-__device__ __forceinline__ float act(float g, float u) {
-  if (GLU) return g * sigmoid(g) * u;
-  const float k = 1.5957691216057308f;                 // 2 sqrt(2 / pi)
-  return g * sigmoid(k * g * fmaf(0.044715f, g * g, 1.f));
+// 1 / (1 + exp(-x)).  Beside bf16 rows, whose time leaves room for some twenty instructions a value,
+// exp and the division are the special-function unit's (within 2 ulp each); fp32 ones move twice the
+// bytes and take the exact ones.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x);
+template <>
+__device__ __forceinline__ float sigmoid<bf16_t>(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+  return r;
 }
-template <bool GLU>
-__device__ __forceinline__ void act_grads(float dy, float g, float u, float& dg, float& du) {
-  const float k = 1.5957691216057308f;
-  if (GLU) {
-    const float p = sigmoid(g), s = dy * p;
-    dg = s * u * fmaf(g, 1.f - p, 1.f);
-    du = s * g;
-  } else {
-    // beyond 16 p is 0 or 1 in fp32, and the polynomial may be too large for it
-    const float g2 = g * g, p = sigmoid(k * g * fmaf(0.044715f, g2, 1.f));
-    const float slope = fabsf(g) > 16.f ? 0.f : g * k * fmaf(3.f * 0.044715f, g2, 1.f);
-    dg = dy * fmaf(slope, p * (1.f - p), p);
-    du = 0.f;
-  }
+template <>
+__device__ __forceinline__ float sigmoid<float>(float x) {
+  return 1.f / (1.f + expf(-x));
+}
+
+constexpr float kGelu = 1.5957691216057308f;           // 2 sqrt(2 / pi)
+// The share of the gate that passes.
+template <typename T, bool GLU>
+__device__ __forceinline__ float gate_of(float g) {
+  return sigmoid<T>(GLU ? g : kGelu * g * fmaf(0.044715f, g * g, 1.f));
+}
+template <typename T, bool GLU>
+__device__ __forceinline__ float act(float g, float u) {
+  const float y = g * gate_of<T, GLU>(g);
+  return GLU ? y * u : y;
+}
+template <typename T, bool GLU>
+__device__ __forceinline__ float grad_gate(float dy, float g, float u) {
+  const float p = gate_of<T, GLU>(g);
+  if (GLU) return dy * p * u * fmaf(g, 1.f - p, 1.f);
+  // beyond 16 p is 0 or 1 in fp32, and the polynomial may be too large for it
+  const float slope = fabsf(g) > 16.f ? 0.f : g * kGelu * fmaf(3.f * 0.044715f, g * g, 1.f);
+  return dy * fmaf(slope, p * (1.f - p), p);
 }
 
 template <typename T>
 __device__ __forceinline__ void store_values(T* base, int64_t ld, const TileAt& at, int i, int vec,
                                              const float (&v)[8]) {
-  const int64_t r = at.row(i);
-  const int n = at.width();
-  if (r >= at.rows || n == 0) return;
-  T* d = base + r * ld + at.col();
-  if (vec && n == 8) {
+  if (!at.has(i)) return;
+  T* d = base + (at.row() + i * kTileRows) * ld + at.col;
+  if (vec && at.width == 8) {
     Pack8<T> p;
     p.set(v);
     p.store(d);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) d[j] = from_f32<T>(v[j]);
+      if (j < at.width) d[j] = from_f32<T>(v[j]);
   }
-}
-__device__ __forceinline__ void clean(float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = finite_or_nan(v[j]);
 }
 
 template <typename T, bool GLU>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 2 : 1)
     activation_forward_kernel(const __grid_constant__ ActArgs p) {
   pdl_launch();
   pdl_wait();
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     const TileAt at(tile, p.rows, p.cols);
-    TileRaw<T> gate, up;
-    gate.load(at, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
-    if (GLU) up.load(at, static_cast<const T*>(p.up), p.ld_up, p.vec);
 #pragma unroll
-    for (int i = 0; i < kTilePasses; ++i) {
-      float g[8], u[8], y[8];
-      gate.get(i, g);
-      if (GLU) up.get(i, u);
+    for (int half = 0; half < kTilePasses; half += 2) {    // (all passes at once would spill)
+      Pack8<T> graw[2], uraw[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = act<GLU>(g[j], GLU ? u[j] : 0.f);
-      if (p.y) store_values(static_cast<T*>(p.y), p.ld_y, at, i, p.vec, y);
-      if (p.y8.q) {
-        clean(y);
-        quantize_row(at, i, y, p.y8);
+      for (int h = 0; h < 2; ++h) {
+        load_pass(graw[h], at, half + h, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
+        if (GLU) load_pass(uraw[h], at, half + h, static_cast<const T*>(p.up), p.ld_up, p.vec);
       }
-      if (p.gate8.q) {
-        clean(g);
-        quantize_row(at, i, g, p.gate8);
-      }
-      if (GLU && p.up8.q) {
-        clean(u);
-        quantize_row(at, i, u, p.up8);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = half + h;
+        float g[8], u[8], y[8];
+        graw[h].get(g);
+        if (GLU) uraw[h].get(u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = act<T, GLU>(g[j], GLU ? u[j] : 0.f);
+        if (p.y) store_values(static_cast<T*>(p.y), p.ld_y, at, i, p.vec, y);
+        if (p.y8.q) quantize_row(at, i, y, p.y8);
+        if (p.gate8.q) quantize_row(at, i, g, p.gate8);
+        if (GLU && p.up8.q) quantize_row(at, i, u, p.up8);
       }
     }
   }
 }
 
+// The gate's gradient, then up's: one of them in registers at a time, and p computed twice, so that
+// two blocks share an SM and one loads while the other computes.
 template <typename T, bool GLU, typename Raw>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 2 : 1)
     activation_backward_kernel(const __grid_constant__ ActArgs p) {
   __shared__ __align__(16) TileSmem sm;
   pdl_launch();
   pdl_wait();
+  constexpr bool kKept = std::is_same<Raw, TileRaw8>::value;
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     const TileAt at(tile, p.rows, p.cols);
     TileRaw<T> dy;
     Raw gate, up;
     dy.load(at, static_cast<const T*>(p.dy), p.ld_dy, p.vec);
-    if constexpr (std::is_same<Raw, TileRaw8>::value) {
+    if constexpr (kKept) {
       gate.load(at, p.gate8);
       if (GLU) up.load(at, p.up8);
     } else {
       gate.load(at, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
       if (GLU) up.load(at, static_cast<const T*>(p.up), p.ld_up, p.vec);
     }
-    float dg[kTilePasses][8], du[kTilePasses][8];
-#pragma unroll
-    for (int i = 0; i < kTilePasses; ++i) {
-      float d[8], g[8], u[8];
-      dy.get(i, d);
-      gate.get(i, g);
-      if (GLU) up.get(i, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        act_grads<GLU>(d[j], g[j], GLU ? u[j] : 0.f, dg[i][j], du[i][j]);
-    }
-    auto emit = [&](float (&v)[kTilePasses][8], void* out, int64_t ld, const Fp8Ref& row,
-                    const Fp8Ref& col) {
+    auto emit = [&](TileValues& v, void* out, int64_t ld, const Fp8Ref& row, const Fp8Ref& col) {
       if (out)
 #pragma unroll
         for (int i = 0; i < kTilePasses; ++i)
           store_values(static_cast<T*>(out), ld, at, i, p.vec, v[i]);
-#pragma unroll
-      for (int i = 0; i < kTilePasses; ++i) clean(v[i]);
       if (row.q)
 #pragma unroll
         for (int i = 0; i < kTilePasses; ++i) quantize_row(at, i, v[i], row);
       if (col.q) {
-        quantize_cols<false>(at, sm, col, [&](int i, float (&w)[8]) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = v[i][j];
-        });
+        quantize_cols<false>(at, sm, col, v);
         __syncthreads();
       }
     };
-    emit(dg, p.dgate, p.ld_dgate, p.dgate_row, p.dgate_col);
-    if (GLU) emit(du, p.dup, p.ld_dup, p.dup_row, p.dup_col);
+    auto gate_value = [&](int i, float (&g)[8]) {
+      if constexpr (kKept) gate.get(i, p.gate8.e5m2, g); else gate.get(i, g);
+    };
+    TileValues v;
+#pragma unroll
+    for (int i = 0; i < kTilePasses; ++i) {
+      float d[8], g[8], u[8];
+      dy.get(i, d);
+      gate_value(i, g);
+      if constexpr (GLU && kKept) up.get(i, p.up8.e5m2, u);
+      if constexpr (GLU && !kKept) up.get(i, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = grad_gate<T, GLU>(d[j], g[j], GLU ? u[j] : 0.f);
+    }
+    emit(v, p.dgate, p.ld_dgate, p.dgate_row, p.dgate_col);
+    if (!GLU || !(p.dup || p.dup_row.q || p.dup_col.q)) continue;
+#pragma unroll
+    for (int i = 0; i < kTilePasses; ++i) {
+      float d[8], g[8];
+      dy.get(i, d);
+      gate_value(i, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = d[j] * g[j] * gate_of<T, GLU>(g[j]);
+    }
+    emit(v, p.dup, p.ld_dup, p.dup_row, p.dup_col);
   }
 }
 

@@ -36,43 +36,61 @@ struct NrArgs {
   int pvec, vec;                  // 16-byte accesses of the parameters; of every row
 };
 
-// Eight consecutive elements of a row of n, zeros past its end.
+// Eight consecutive elements of a row from c on, `left` of them (1 to 8; 0 or less: none) in it and
+// zeros past its end.
 template <typename T>
-__device__ __forceinline__ void load_chunk(Pack8<T>& p, const T* row, int64_t c, int64_t n, int vec) {
-  if (c >= n) {
-    p.zero();
-  } else if (vec && c + 8 <= n) {
+__device__ __forceinline__ void load_chunk(Pack8<T>& p, const T* row, int64_t c, int left, int vec) {
+  if (left >= 8 && vec) {
     p.load(row + c);
   } else {
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < n ? to_f32(row[c + j]) : 0.f;
+    for (int j = 0; j < 8; ++j) v[j] = j < left ? to_f32(row[c + j]) : 0.f;
     p.set(v);
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_part(T* row, int64_t c, int64_t n, int vec,
-                                           const float (&v)[8]) {
-  if (vec && c + 8 <= n) {
+__device__ __forceinline__ void store_part(T* row, int64_t c, int left, int vec, const float (&v)[8]) {
+  if (left >= 8 && vec) {
     Pack8<T> p;
     p.set(v);
     p.store(row + c);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j < n) row[c + j] = from_f32<T>(v[j]);
+      if (j < left) row[c + j] = from_f32<T>(v[j]);
+  }
+}
+__device__ __forceinline__ void zero_past(float (&v)[8], int left) {
+  if (left >= 8) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < left ? v[j] : 0.f;
+}
+// The parameters of a thread's chunk, `fill` where there are none.
+__device__ __forceinline__ void load_param8(const void* src, int is_bf16, int pvec, int64_t c, int left,
+                                            float fill, float (&v)[8]) {
+  if (src && pvec && left >= 8) {
+    if (is_bf16) {
+      Pack8<bf16_t> q;
+      q.load(static_cast<const bf16_t*>(src) + c);
+      q.get(v);
+    } else {
+      Pack8<float> q;
+      q.load(static_cast<const float*>(src) + c);
+      q.get(v);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = src && j < left ? load_param(src, is_bf16, c + j) : fill;
   }
 }
 // A thread's part of a 1 x 128 group (zeros past the row's end); 16 neighbouring threads call.
-__device__ __forceinline__ void store_group(const Fp8Ref& m, int64_t row, int64_t c, int64_t n,
+__device__ __forceinline__ void store_group(const Fp8Ref& m, int64_t row, int64_t c, int left,
                                             float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = c + j < n ? finite_or_nan(v[j]) : 0.f;
-  const uint32_t byte = scale_byte(half_warp_max(largest(v)), m.e5m2);
-  if (c >= n) return;
-  store_fp8(m.q + row * m.ld + c, pack_fp8(v, inverse_scale(byte), m.e5m2),
-            n - c < 8 ? (int)(n - c) : 8);
-  if ((c & (kGroup - 1)) == 0) m.s[row * m.ld_s + c / kGroup] = (uint8_t)byte;
+  const uint32_t byte = scale_byte(group_max(v), m.e5m2);
+  if (left <= 0) return;
+  store_fp8(m.q + row * m.ld + c, pack_fp8(v, inverse_scale(byte), m.e5m2), left);
+  if ((threadIdx.x & 15) == 0) m.s[row * m.ld_s + c / kGroup] = (uint8_t)byte;
 }
 
 // ---------------------------------------------------------------- forward
@@ -85,41 +103,52 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
   const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : blockIdx.x;
   pdl_wait();
   if (row >= p.rows) return;              // whole warps
-  const int64_t n = p.cols;
+  const int n = (int)p.cols;              // (rows this long fit registers)
+  auto col = [&](int k) { return (k * TPR + t) * 8; };
   Pack8<T> xp[K], rp[K];
+  const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int64_t c = elem_of<TPR, true>(t, k, 0);
-    load_chunk(xp[k], static_cast<const T*>(p.x) + row * p.ld_x, c, n, p.vec);
-    if (p.res) load_chunk(rp[k], static_cast<const T*>(p.res) + row * p.ld_res, c, n, p.vec);
-    else rp[k].zero();
+  for (int k = 0; k < K; ++k) load_chunk(xp[k], xr, col(k), n - col(k), p.vec);
+  if (p.res) {
+    const T* rr = static_cast<const T*>(p.res) + row * p.ld_res;
+#pragma unroll
+    for (int k = 0; k < K; ++k) load_chunk(rp[k], rr, col(k), n - col(k), p.vec);
   }
   float v[K][8], s = 0.f, zero = 0.f;
   int turn = 0;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float r[8];
-    xp[k].get(v[k]);
-    rp[k].get(r);
+  for (int k = 0; k < K; ++k) xp[k].get(v[k]);
+  if (p.res)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (p.res) v[k][j] += r[j];
-      s += v[k][j];
+    for (int k = 0; k < K; ++k) {
+      float r[8];
+      rp[k].get(r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] += r[j];
     }
-  }
+  // what does not wait for the row's sums
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (p.h) store_part(static_cast<T*>(p.h) + row * p.ld_h, col(k), n - col(k), p.vec, v[k]);
   float mu = 0.f;
   if (p.layer) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[k][j];
     row_sum2<TPR>(s, zero, red, turn);
     mu = s * p.inv_n;
   }
   float q = 0.f;
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int k = 0; k < K; ++k) {
+    float d[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float d = elem_of<TPR, true>(t, k, j) < n ? v[k][j] - mu : 0.f;
-      q = fmaf(d, d, q);
-    }
+    for (int j = 0; j < 8; ++j) d[j] = v[k][j] - mu;
+    zero_past(d, n - col(k));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q = fmaf(d[j], d[j], q);
+  }
   zero = 0.f;
   row_sum2<TPR>(q, zero, red, turn);
   const float r = 1.f / sqrtf(fmaf(q, p.inv_n, p.eps));
@@ -129,18 +158,26 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int64_t c = elem_of<TPR, true>(t, k, 0);
-    float w[1][8], b[1][8], y[8];
-    load_params<TPR, 1, true>(p.w ? static_cast<const char*>(p.w) + (p.wbf16 ? 2 : 4) * (c - t * 8) : nullptr,
-                              p.wbf16, p.pvec, n - (c - t * 8), t, 1.f, w);
-    load_params<TPR, 1, true>(p.b ? static_cast<const char*>(p.b) + (p.wbf16 ? 2 : 4) * (c - t * 8) : nullptr,
-                              p.wbf16, p.pvec, n - (c - t * 8), t, 0.f, b);
+    const int c = col(k), left = n - c;
+    float w[8], y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = fmaf((v[k][j] - mu) * r, w[0][j], b[0][j]);
-    if (p.h) store_part(static_cast<T*>(p.h) + row * p.ld_h, c, n, p.vec, v[k]);
-    if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, n, p.vec, y);
-    if (p.y8.q) store_group(p.y8, row, c, n, y);
-    if (p.h8.q) store_group(p.h8, row, c, n, v[k]);
+    for (int j = 0; j < 8; ++j) y[j] = (v[k][j] - mu) * r;
+    if (p.w) {
+      load_param8(p.w, p.wbf16, p.pvec, c, left, 1.f, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= w[j];
+    }
+    if (p.b) {
+      load_param8(p.b, p.wbf16, p.pvec, c, left, 0.f, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] += w[j];
+    }
+    if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, left, p.vec, y);
+    if (p.y8.q) {
+      zero_past(y, left);
+      store_group(p.y8, row, c, left, y);
+    }
+    if (p.h8.q) store_group(p.h8, row, c, left, v[k]);
   }
 }
 
@@ -154,13 +191,14 @@ __global__ void __launch_bounds__(1024)
   const int64_t row = blockIdx.x, n = p.cols;
   const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
   const T* rr = p.res ? static_cast<const T*>(p.res) + row * p.ld_res : nullptr;
+  auto left_of = [&](int64_t c) { return (int)max((int64_t)0, min((int64_t)8, n - c)); };
   auto sum = [&](int64_t c, float (&v)[8]) {
     Pack8<T> a;
-    load_chunk(a, xr, c, n, p.vec);
+    load_chunk(a, xr, c, left_of(c), p.vec);
     a.get(v);
     if (!rr) return;
     float r[8];
-    load_chunk(a, rr, c, n, p.vec);
+    load_chunk(a, rr, c, left_of(c), p.vec);
     a.get(r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += r[j];
@@ -203,10 +241,14 @@ __global__ void __launch_bounds__(1024)
       const float b = p.b && c + j < n ? load_param(p.b, p.wbf16, c + j) : 0.f;
       y[j] = fmaf((v[j] - mu) * r, w, b);
     }
-    if (p.h) store_part(static_cast<T*>(p.h) + row * p.ld_h, c, n, p.vec, v);
-    if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, n, p.vec, y);
-    if (p.y8.q) store_group(p.y8, row, c, n, y);
-    if (p.h8.q) store_group(p.h8, row, c, n, v);
+    const int left = left_of(c);
+    if (p.h) store_part(static_cast<T*>(p.h) + row * p.ld_h, c, left, p.vec, v);
+    if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, left, p.vec, y);
+    if (p.y8.q) {
+      zero_past(y, left);
+      store_group(p.y8, row, c, left, y);
+    }
+    if (p.h8.q) store_group(p.h8, row, c, left, v);
   }
 }
 
@@ -249,7 +291,7 @@ struct Rows {
       return;
     }
     Pack8<T> p;
-    load_chunk(p, row, c, n, 0);
+    load_chunk(p, row, c, (int)max((int64_t)0, min((int64_t)8, n - c)), 0);
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -377,7 +419,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) g[j] = fmaf(fmaf(g[j], w[k][j], -s1) - z[j] * s2, r, d[j]);
-    store_part(static_cast<T*>(p.dx) + i * p.ld_dx, elem_of<TPR, true>(t, k, 0), n, p.vec, g);
+    {
+      const int64_t c = elem_of<TPR, true>(t, k, 0);
+      store_part(static_cast<T*>(p.dx) + i * p.ld_dx, c, (int)(n - c), p.vec, g);
+    }
   };
   for (int stage = 0; row < p.rows; row += NR * step, stage = wrap(stage + NR)) {
     // the second row of the turn, if there is one (the same for the whole group)

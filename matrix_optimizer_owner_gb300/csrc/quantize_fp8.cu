@@ -23,33 +23,40 @@ struct QuantArgs {
 enum Form : int { kRow = 1, kCol = 2, kTile = 4 };
 
 template <typename Raw, int FORMS>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kTileThreads, 2)
     quantize_kernel(const __grid_constant__ QuantArgs p) {
   __shared__ __align__(16) TileSmem sm;
   pdl_launch();
   pdl_wait();
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     const TileAt at(tile, p.rows, p.cols);
-    Raw raw;
-    if constexpr (std::is_same<Raw, TileRaw8>::value)
+    TileValues v;
+    if constexpr (std::is_same<Raw, TileRaw8>::value) {
+      Raw raw;
       raw.load(at, p.src);
-    else
-      raw.load(at, static_cast<const typename Raw::Elem*>(p.x), p.ld, p.vec);
-    auto get = [&](int i, float (&v)[8]) {
-      raw.get(i, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = finite_or_nan(v[j]);
-    };
+      for (int i = 0; i < kTilePasses; ++i) raw.get(i, p.src.e5m2, v[i]);
+      if (p.src.groups == MFSDP_GROUPS_COL) {
+        const uint8_t* s = p.src.s + at.r0 / kGroup * p.src.ld_s + at.col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float f = j < at.width ? scale_value(s[j]) : 1.f;
+#pragma unroll
+          for (int i = 0; i < kTilePasses; ++i) v[i][j] *= f;
+        }
+      }
+    } else {
+      Raw raw;
+      raw.load(at, static_cast<const typename Raw::Elem*>(p.x), p.ld, p.vec);
+#pragma unroll
+      for (int i = 0; i < kTilePasses; ++i) raw.get(i, v[i]);
+    }
     if (FORMS & kRow) {
 #pragma unroll
-      for (int i = 0; i < kTilePasses; ++i) {
-        float v[8];
-        get(i, v);
-        quantize_row(at, i, v, p.row);
-      }
+      for (int i = 0; i < kTilePasses; ++i) quantize_row(at, i, v[i], p.row);
     }
     if (FORMS & (kCol | kTile)) {
-      quantize_cols<(FORMS & kTile) != 0>(at, sm, p.other, get);
+      quantize_cols<(FORMS & kTile) != 0>(at, sm, p.other, v);
       if (tile + gridDim.x < p.tiles) __syncthreads();
     }
   }
