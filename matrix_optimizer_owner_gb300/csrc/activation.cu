@@ -13,7 +13,7 @@
 // Bound by memory, with little to spare: a value costs two special-function instructions and some forty
 // others in the backward pass.
 #include <algorithm>
-#include <type_traits>
+#include <atomic>
 
 #include "fp8.cuh"
 
@@ -40,8 +40,9 @@ template <typename T>
 __device__ __forceinline__ float sigmoid(float x);
 template <>
 __device__ __forceinline__ float sigmoid<bf16_t>(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
 template <>
@@ -69,114 +70,284 @@ __device__ __forceinline__ float grad_gate(float dy, float g, float u) {
   return dy * fmaf(slope, p * (1.f - p), p);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_values(T* base, int64_t ld, const TileAt& at, int i, int vec,
+template <typename T, typename At>
+__device__ __forceinline__ void store_values(T* base, int64_t ld, const At& at, int i, int vec,
                                              const float (&v)[8]) {
   if (!at.has(i)) return;
-  T* d = base + (at.row() + i * kTileRows) * ld + at.col;
-  if (vec && at.width == 8) {
+  T* d = base + (at.row + i * kTileRows) * ld + at.col;
+  if (At::kFull || (vec && at.width() == 8)) {
     Pack8<T> p;
     p.set(v);
     p.store(d);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < at.width) d[j] = from_f32<T>(v[j]);
+      if (j < at.width()) d[j] = from_f32<T>(v[j]);
   }
 }
 
+template <typename T, bool GLU, typename At>
+__device__ __forceinline__ void forward_pair(const ActArgs& p, const At& at, int i) {
+  Pack8<T> graw[2], uraw[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_pass(graw[h], at, i + h, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
+    if (GLU) load_pass(uraw[h], at, i + h, static_cast<const T*>(p.up), p.ld_up, p.vec);
+  }
+  float g[2][8], u[2][8], y[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    graw[h].get(g[h]);
+    if (GLU) uraw[h].get(u[h]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[h][j] = act<T, GLU>(g[h][j], GLU ? u[h][j] : 0.f);
+    if (p.y) store_values(static_cast<T*>(p.y), p.ld_y, at, i + h, p.vec, y[h]);
+  }
+  if (p.y8.q) quantize_rows(at, i, y[0], y[1], p.y8);
+  if (p.gate8.q) quantize_rows(at, i, g[0], g[1], p.gate8);
+  if (GLU && p.up8.q) quantize_rows(at, i, u[0], u[1], p.up8);
+}
+
+// Half a tile a block: no group runs down the columns here, and a thread's two rows fit its registers.
 template <typename T, bool GLU>
 __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 2 : 1)
     activation_forward_kernel(const __grid_constant__ ActArgs p) {
   pdl_launch();
   pdl_wait();
-  for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    const TileAt at(tile, p.rows, p.cols);
-#pragma unroll
-    for (int half = 0; half < kTilePasses; half += 2) {    // (all passes at once would spill)
-      Pack8<T> graw[2], uraw[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        load_pass(graw[h], at, half + h, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
-        if (GLU) load_pass(uraw[h], at, half + h, static_cast<const T*>(p.up), p.ld_up, p.vec);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = half + h;
-        float g[8], u[8], y[8];
-        graw[h].get(g);
-        if (GLU) uraw[h].get(u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = act<T, GLU>(g[j], GLU ? u[j] : 0.f);
-        if (p.y) store_values(static_cast<T*>(p.y), p.ld_y, at, i, p.vec, y);
-        if (p.y8.q) quantize_row(at, i, y, p.y8);
-        if (p.gate8.q) quantize_row(at, i, g, p.gate8);
-        if (GLU && p.up8.q) quantize_row(at, i, u, p.up8);
-      }
-    }
+  const int64_t halves = ((p.rows + kGroup - 1) / kGroup) * 2;
+  const int32_t tc = (int32_t)blockIdx.x;
+  for (int64_t h = blockIdx.y; h < halves; h += gridDim.y) {
+    const int64_t tr = h >> 1;
+    const int i = (int)(h & 1) * 2;
+    if (full_tile(tr, tc, p.rows, p.cols, p.vec))
+      forward_pair<T, GLU>(p, TileAt<true>(tr, tc, p.rows, p.cols), i);
+    else
+      forward_pair<T, GLU>(p, TileAt<false>(tr, tc, p.rows, p.cols), i);
   }
 }
 
-// The gate's gradient, then up's: one of them in registers at a time, and p computed twice, so that
-// two blocks share an SM and one loads while the other computes.
-template <typename T, bool GLU, typename Raw>
-__global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 2 : 1)
+// The inputs of the tiles that a block will need next, copied ahead to shared memory as they lie in
+// memory (cp.async where rows start on 16-byte boundaries).  A thread reads back only what it copied, so
+// no barrier is needed.
+template <typename T, bool GLU, bool KEPT>
+struct Ahead {
+  static constexpr int P = sizeof(T) / 2;                   // 16-byte planes of eight values
+  static constexpr int kInput = KEPT ? 8 : 16 * P;          // bytes of eight values of gate or up
+  static constexpr int kPass = kTileThreads * (16 * P + (GLU ? 2 : 1) * kInput);
+  static constexpr int kStage = kTilePasses * kPass;
+  static constexpr int kDepth = 3 * kStage <= 200 * 1024 ? 3 : 2 * kStage <= 200 * 1024 ? 2 : 1;
+  static constexpr int kBytes = kDepth * kStage;
+  uint32_t base;
+  __device__ __forceinline__ explicit Ahead(const void* smem)
+      : base((uint32_t)__cvta_generic_to_shared(smem)) {}
+  // matrix m (0 dy, 1 gate, 2 up), plane q of this thread's values of pass i
+  __device__ __forceinline__ uint32_t at(int stage, int i, int m, int q) const {
+    return base + (uint32_t)(stage * kStage + i * kPass +
+                             (m == 0 ? 0 : kTileThreads * (16 * P + (m - 1) * kInput)) +
+                             q * kTileThreads * 16) +
+           threadIdx.x * (m > 0 && KEPT ? 8 : 16);
+  }
+  template <typename At>
+  __device__ __forceinline__ void copy(int stage, int m, const At& at_, const T* src, int64_t ld,
+                                       int vec) const {
+    const T* s = src + at_.row * ld + at_.col;
+#pragma unroll
+    for (int i = 0; i < kTilePasses; ++i) {
+      if (vec) {
+        const int left = at_.has(i) ? at_.width() * (int)sizeof(T) : 0;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          const int bytes = max(0, min(16, left - 16 * q));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(stage, i, m, q)),
+                       "l"(bytes ? reinterpret_cast<const char*>(s + i * (kTileRows * ld)) + 16 * q
+                                 : reinterpret_cast<const char*>(src)),
+                       "r"(bytes)
+                       : "memory");
+        }
+      } else {
+        Pack8<T> p;
+        load_pass(p, at_, i, src, ld, 0);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(stage, i, m, q)),
+                       "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]), "r"(w[4 * q + 3])
+                       : "memory");
+      }
+    }
+  }
+  template <typename At>
+  __device__ __forceinline__ void copy8(int stage, int m, const At& at_, const Fp8Ref& src) const {
+    const uint8_t* s = src.q + at_.row * src.ld + at_.col;
+#pragma unroll
+    for (int i = 0; i < kTilePasses; ++i) {
+      const int bytes = at_.has(i) ? at_.width() : 0;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at(stage, i, m, 0)),
+                   "l"(bytes ? s + i * (kTileRows * src.ld) : src.q), "r"(bytes)
+                   : "memory");
+    }
+  }
+  __device__ __forceinline__ void get(int stage, int i, int m, float (&v)[8]) const {
+    Pack8<T> p;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&p);
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * q]), "=r"(w[4 * q + 1]), "=r"(w[4 * q + 2]), "=r"(w[4 * q + 3])
+                   : "r"(at(stage, i, m, q))
+                   : "memory");
+    p.get(v);
+  }
+  __device__ __forceinline__ void get8(int stage, int i, int m, int e5m2, uint32_t byte,
+                                       float (&v)[8]) const {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(r.x), "=r"(r.y)
+                 : "r"(at(stage, i, m, 0))
+                 : "memory");
+    unpack_fp8(r, e5m2, scale_value(byte), v);
+  }
+};
+
+// A block walks the tiles with the next ones' inputs under way.  It holds one gradient in registers at a
+// time, the gate's and then up's, and computes p for both.
+template <typename T, bool GLU, bool KEPT>
+__global__ void __launch_bounds__(kTileThreads, 1)
     activation_backward_kernel(const __grid_constant__ ActArgs p) {
+  using A = Ahead<T, GLU, KEPT>;
+  constexpr int D = A::kDepth;
   __shared__ __align__(16) TileSmem sm;
+  extern __shared__ uint4 ahead_smem[];
+  const A in(ahead_smem);
   pdl_launch();
   pdl_wait();
-  constexpr bool kKept = std::is_same<Raw, TileRaw8>::value;
-  for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    const TileAt at(tile, p.rows, p.cols);
-    TileRaw<T> dy;
-    Raw gate, up;
-    dy.load(at, static_cast<const T*>(p.dy), p.ld_dy, p.vec);
-    if constexpr (kKept) {
-      gate.load(at, p.gate8);
-      if (GLU) up.load(at, p.up8);
-    } else {
-      gate.load(at, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
-      if (GLU) up.load(at, static_cast<const T*>(p.up), p.ld_up, p.vec);
+  // tiles blockIdx.x, + gridDim.x, ...: a tile row and column group each, carried along (a division per
+  // tile would cost as much as a tenth of the tile)
+  const int32_t groups = (int32_t)((p.cols + kGroup - 1) / kGroup);
+  const int32_t step_r = (int32_t)(gridDim.x / (unsigned)groups);
+  const int32_t step_c = (int32_t)(gridDim.x % (unsigned)groups);
+  const int64_t tile_rows = (p.rows + kGroup - 1) / kGroup;
+  struct Tile {
+    int64_t r;
+    int32_t c;
+  };
+  auto after = [&](Tile t) {
+    t.r += step_r;
+    t.c += step_c;
+    if (t.c >= groups) {
+      t.c -= groups;
+      ++t.r;
     }
-    auto emit = [&](TileValues& v, void* out, int64_t ld, const Fp8Ref& row, const Fp8Ref& col) {
-      if (out)
+    return t;
+  };
+  auto fetch = [&](const Tile& tile, int stage) {
+    if (tile.r < tile_rows) {
+      const TileAt<false> at(tile.r, tile.c, p.rows, p.cols);
+      in.copy(stage, 0, at, static_cast<const T*>(p.dy), p.ld_dy, p.vec);
+      if constexpr (KEPT) {
+        in.copy8(stage, 1, at, p.gate8);
+        if (GLU) in.copy8(stage, 2, at, p.up8);
+      } else {
+        in.copy(stage, 1, at, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
+        if (GLU) in.copy(stage, 2, at, static_cast<const T*>(p.up), p.ld_up, p.vec);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  struct Scales {
+    uint32_t s[KEPT ? kTilePasses : 1][KEPT && GLU ? 2 : 1];
+  };
+  auto fetch_scales = [&](const Tile& tile, Scales& v) {
+    if (!KEPT || tile.r >= tile_rows) return;
+    const TileAt<false> at(tile.r, tile.c, p.rows, p.cols);
+    const uint8_t* g = p.gate8.s + at.row * p.gate8.ld_s + at.group;
+    const uint8_t* u = GLU ? p.up8.s + at.row * p.up8.ld_s + at.group : nullptr;
 #pragma unroll
-        for (int i = 0; i < kTilePasses; ++i)
-          store_values(static_cast<T*>(out), ld, at, i, p.vec, v[i]);
-      if (row.q)
+    for (int i = 0; i < kTilePasses; ++i) {
+      v.s[KEPT ? i : 0][0] = at.has(i) ? g[i * (kTileRows * p.gate8.ld_s)] : 127u;
+      if (GLU) v.s[KEPT ? i : 0][KEPT && GLU ? 1 : 0] = at.has(i) ? u[i * (kTileRows * p.up8.ld_s)] : 127u;
+    }
+  };
+  Tile tile{(int64_t)(blockIdx.x / (unsigned)groups), (int32_t)(blockIdx.x % (unsigned)groups)};
+  Tile far = tile;                         // the next tile to copy
+  Scales cur, next;
 #pragma unroll
-        for (int i = 0; i < kTilePasses; ++i) quantize_row(at, i, v[i], row);
-      if (col.q) {
-        quantize_cols<false>(at, sm, col, v);
-        __syncthreads();
+  for (int i = 0; i < D - 1; ++i, far = after(far)) fetch(far, i);
+  fetch_scales(tile, next);
+  for (int stage = 0; tile.r < tile_rows; stage = stage + 1 == D ? 0 : stage + 1) {
+    const Tile here = tile;
+    tile = after(tile);
+    cur = next;
+    fetch_scales(tile, next);
+    fetch(far, stage == 0 ? D - 1 : stage - 1);
+    far = after(far);
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    auto process = [&](const auto& at) {
+      auto input = [&](int i, int m, float (&v)[8]) {
+        if constexpr (KEPT)
+          in.get8(stage, i, m, m == 1 ? p.gate8.e5m2 : p.up8.e5m2, cur.s[i][GLU ? m - 1 : 0], v);
+        else
+          in.get(stage, i, m, v);
+      };
+      auto emit = [&](TileValues& v, void* out, int64_t ld, const Fp8Ref& row, const Fp8Ref& col) {
+        if (out)
+#pragma unroll
+          for (int i = 0; i < kTilePasses; ++i)
+            store_values(static_cast<T*>(out), ld, at, i, p.vec, v[i]);
+        if (row.q)
+#pragma unroll
+          for (int i = 0; i < kTilePasses; i += 2) quantize_rows(at, i, v[i], v[i + 1], row);
+        if (col.q) {
+          quantize_cols<false>(at, sm, col, v);
+          __syncthreads();
+        }
+      };
+      TileValues v;
+      if (p.dgate || p.dgate_row.q || p.dgate_col.q) {
+#pragma unroll
+        for (int i = 0; i < kTilePasses; ++i) {
+          float d[8], g[8], u[8];
+          in.get(stage, i, 0, d);
+          input(i, 1, g);
+          if constexpr (GLU) input(i, 2, u);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = grad_gate<T, GLU>(d[j], g[j], GLU ? u[j] : 0.f);
+        }
+        emit(v, p.dgate, p.ld_dgate, p.dgate_row, p.dgate_col);
+      }
+      if (GLU && (p.dup || p.dup_row.q || p.dup_col.q)) {
+#pragma unroll
+        for (int i = 0; i < kTilePasses; ++i) {
+          float d[8], g[8];
+          in.get(stage, i, 0, d);
+          input(i, 1, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] = d[j] * g[j] * gate_of<T, GLU>(g[j]);
+        }
+        emit(v, p.dup, p.ld_dup, p.dup_row, p.dup_col);
       }
     };
-    auto gate_value = [&](int i, float (&g)[8]) {
-      if constexpr (kKept) gate.get(i, p.gate8.e5m2, g); else gate.get(i, g);
-    };
-    TileValues v;
-#pragma unroll
-    for (int i = 0; i < kTilePasses; ++i) {
-      float d[8], g[8], u[8];
-      dy.get(i, d);
-      gate_value(i, g);
-      if constexpr (GLU && kKept) up.get(i, p.up8.e5m2, u);
-      if constexpr (GLU && !kKept) up.get(i, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = grad_gate<T, GLU>(d[j], g[j], GLU ? u[j] : 0.f);
-    }
-    emit(v, p.dgate, p.ld_dgate, p.dgate_row, p.dgate_col);
-    if (!GLU || !(p.dup || p.dup_row.q || p.dup_col.q)) continue;
-#pragma unroll
-    for (int i = 0; i < kTilePasses; ++i) {
-      float d[8], g[8];
-      dy.get(i, d);
-      gate_value(i, g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = d[j] * g[j] * gate_of<T, GLU>(g[j]);
-    }
-    emit(v, p.dup, p.ld_dup, p.dup_row, p.dup_col);
+    if (full_tile(here.r, here.c, p.rows, p.cols, p.vec))
+      process(TileAt<true>(here.r, here.c, p.rows, p.cols));
+    else
+      process(TileAt<false>(here.r, here.c, p.rows, p.cols));
   }
+}
+
+template <typename T, bool GLU, bool KEPT>
+cudaError_t launch_backward(const ActArgs& a, int sms, cudaStream_t st) {
+  static std::atomic<bool> done[64];
+  constexpr int smem = Ahead<T, GLU, KEPT>::kBytes;
+  const auto kernel = activation_backward_kernel<T, GLU, KEPT>;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !done[dev].load())) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(a.tiles, sms)), dim3(kTileThreads), smem, st,
+                    a);
 }
 
 int check_kind(int32_t kind, int64_t rows, int64_t cols, int32_t dtype) {
@@ -234,7 +405,9 @@ extern "C" int mfsdp_activation_forward(int32_t kind, int64_t rows, int64_t cols
   a.y8 = ref_of(y8);
   a.gate8 = ref_of(gate8);
   a.up8 = ref_of(up8);
-  const dim3 grid((unsigned)std::min<int64_t>(a.tiles, 1ll << 30)), block(kTileThreads);
+  dim3 grid = tile_grid(rows, cols);
+  const dim3 block(kTileThreads);
+  grid.y = std::min(65535u, 2 * grid.y);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == MFSDP_DTYPE_BF16;
   const cudaError_t e =
@@ -295,20 +468,18 @@ extern "C" int mfsdp_activation_backward(
   a.dgate_col = ref_of(dgate_col);
   a.dup_row = ref_of(dup_row);
   a.dup_col = ref_of(dup_col);
-  const dim3 grid((unsigned)std::min<int64_t>(a.tiles, 1ll << 30)), block(kTileThreads);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, st, a); };
   const bool bf = dtype == MFSDP_DTYPE_BF16;
   cudaError_t e;
   if (gate8)
-    e = glu ? (bf ? go(activation_backward_kernel<bf16_t, true, TileRaw8>)
-                  : go(activation_backward_kernel<float, true, TileRaw8>))
-            : (bf ? go(activation_backward_kernel<bf16_t, false, TileRaw8>)
-                  : go(activation_backward_kernel<float, false, TileRaw8>));
+    e = glu ? (bf ? launch_backward<bf16_t, true, true>(a, sms, st)
+                  : launch_backward<float, true, true>(a, sms, st))
+            : (bf ? launch_backward<bf16_t, false, true>(a, sms, st)
+                  : launch_backward<float, false, true>(a, sms, st));
   else
-    e = glu ? (bf ? go(activation_backward_kernel<bf16_t, true, TileRaw<bf16_t>>)
-                  : go(activation_backward_kernel<float, true, TileRaw<float>>))
-            : (bf ? go(activation_backward_kernel<bf16_t, false, TileRaw<bf16_t>>)
-                  : go(activation_backward_kernel<float, false, TileRaw<float>>));
+    e = glu ? (bf ? launch_backward<bf16_t, true, false>(a, sms, st)
+                  : launch_backward<float, true, false>(a, sms, st))
+            : (bf ? launch_backward<bf16_t, false, false>(a, sms, st)
+                  : launch_backward<float, false, false>(a, sms, st));
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }

@@ -12,6 +12,7 @@
 
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <cfloat>
 
 #include "elem.cuh"
@@ -46,12 +47,29 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 __device__ __forceinline__ float finite_or_nan(float v) {
   return fabsf(v) <= FLT_MAX ? v : __uint_as_float(0x7FC00000u);
 }
-// The larger magnitude, NaN if one of them is: what tells a group with values that are not finite from
-// the others without looking at each value twice.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest magnitude of three, NaN if one of them is: what tells a group with values that are not
+// finite from the others without looking at each value twice.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) { return max3_nan(a, b, b); }
+// The larger of each half.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// A partial maximum as what is reduced across threads: its exponent, one higher where the significand
+// is above 1.75, so that a group's scale is the largest one less the type's.  kMaybe and above: an
+// infinity, a NaN, or a value beyond 1.75 2^127, which are told apart where the group is looked at again.
+constexpr uint32_t kMaybe = 255u;
+__device__ __forceinline__ uint32_t scale_part(float amax) {
+  return (__float_as_uint(amax) + 0x1FFFFFu) >> 23;
+}
+__device__ __forceinline__ uint32_t scale_of_part(uint32_t part, int e5m2) {
+  return (uint32_t)max((int)part - (e5m2 ? 15 : 8), 0);
 }
 
 // ---- eight consecutive values
@@ -105,34 +123,37 @@ __device__ __forceinline__ uint2 load_fp8(const uint8_t* p, int n) {
   return r;
 }
 
-// NaN where a value is not finite (or an infinity).
+// The largest magnitude; NaN or an infinity where a value is not finite.
 __device__ __forceinline__ float largest(const float (&v)[8]) {
-  float a = fabsf(v[0]);
-#pragma unroll
-  for (int j = 1; j < 8; ++j) a = max_nan(a, v[j]);
-  return a;
+  const float a = max3_nan(v[0], v[1], v[2]), b = max3_nan(v[3], v[4], v[5]);
+  return max3_nan(a, b, max_nan(v[6], v[7]));
 }
-// Over the 16 lanes that share a row's group.
-__device__ __forceinline__ float half_warp_max(float a) {
+// Two values at a time over the 16 lanes that share a row's group.
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t w) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-  return a;
+  for (int o = 8; o > 0; o >>= 1) w = max_u16x2(w, __shfl_xor_sync(0xFFFFFFFFu, w, o));
+  return w;
 }
-// The largest finite magnitude of the group that 16 lanes hold (8 values each); values that are not
-// finite become NaN.
-__device__ __forceinline__ float group_max(float (&v)[8]) {
-  float a = half_warp_max(largest(v));
-  if (!(a <= FLT_MAX)) {                           // the same for the half-warp; rare
-    a = 0.f;
+// The scale of a group with values that are not finite, which become NaN; the group's 16 lanes call.
+__device__ __forceinline__ uint32_t cleaned_scale(float (&v)[8], int e5m2) {
+  float a = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = finite_or_nan(v[j]);
-      a = fmaxf(a, fabsf(v[j]));
-    }
-    const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, o));
+  for (int j = 0; j < 8; ++j) {
+    v[j] = finite_or_nan(v[j]);
+    a = fmaxf(a, fabsf(v[j]));
   }
-  return a;
+  const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, o));
+  return scale_byte(a, e5m2);
+}
+// The scales of two groups, 8 values a lane of each; their lanes' largest values are reduced together.
+__device__ __forceinline__ void group_scales(float (&u)[8], float (&v)[8], int u_e5m2, int v_e5m2,
+                                             uint32_t& su, uint32_t& sv) {
+  const uint32_t w = half_warp_max(scale_part(largest(u)) | (scale_part(largest(v)) << 16));
+  su = scale_of_part(w & 0xFFFFu, u_e5m2);
+  sv = scale_of_part(w >> 16, v_e5m2);
+  if ((w & 0xFFFFu) >= kMaybe) su = cleaned_scale(u, u_e5m2);   // the same for the half-warp; rare
+  if ((w >> 16) >= kMaybe) sv = cleaned_scale(v, v_e5m2);
 }
 
 // ---- tiles
@@ -143,47 +164,61 @@ constexpr int kTileThreads = 512;
 constexpr int kTileRows = kTileThreads / 16;      // rows per pass
 constexpr int kTilePasses = kGroup / kTileRows;
 struct TileSmem {
-  float col[kTileThreads / 32][kGroup];
-  float top[kGroup];
+  uint32_t col[kTileThreads / 32][kGroup / 2];     // a warp's scales, two columns a word
+  float top[kGroup];                               // the columns' inverse scales
 };
 
+// FULL: the tile has all its rows and columns, and every matrix rows for 16-byte accesses: no test per
+// value or chunk remains.
+template <bool FULL>
 struct TileAt {
+  static constexpr bool kFull = FULL;
   int64_t r0;                                      // the tile's first row
-  int64_t col;                                     // this thread's first column
-  int64_t group;                                   // the tile's column group
-  int row16, lane16;
+  int64_t row;                                     // this thread's first row and column
+  int64_t col;
+  int32_t group;                                   // the tile's column group
+  int lane16;
   int left;                                        // the tile's rows from this thread's first one on
-  int width;                                       // columns of this thread's chunk, 0 to 8
   int cols_here;                                   // columns of the tile
-  __device__ __forceinline__ TileAt(int64_t tile, int64_t rows, int64_t cols)
-      : row16(threadIdx.x >> 4), lane16(threadIdx.x & 15) {
-    const int64_t tc = (cols + kGroup - 1) / kGroup, tr = tile / tc;
-    group = tile - tr * tc;
+  // tile row tr and column group tc
+  __device__ __forceinline__ TileAt(int64_t tr, int32_t tc, int64_t rows, int64_t cols)
+      : group(tc), lane16(threadIdx.x & 15) {
+    const int row16 = threadIdx.x >> 4;
     r0 = tr * kGroup;
-    col = group * kGroup + lane16 * 8;
+    row = r0 + row16;
+    col = (int64_t)tc * kGroup + lane16 * 8;
     left = (int)min((int64_t)kGroup, rows - r0) - row16;
-    cols_here = (int)min((int64_t)kGroup, cols - group * kGroup);
-    width = max(0, min(8, cols_here - lane16 * 8));
+    cols_here = (int)min((int64_t)kGroup, cols - (int64_t)tc * kGroup);
   }
-  __device__ __forceinline__ int64_t row() const { return r0 + row16; }      // of pass 0
-  __device__ __forceinline__ bool has(int i) const { return i * kTileRows < left; }
+  __device__ __forceinline__ bool has(int i) const { return FULL || i * kTileRows < left; }
+  __device__ __forceinline__ int width() const {   // columns of this thread's chunk, 0 to 8
+    return FULL ? 8 : max(0, min(8, cols_here - lane16 * 8));
+  }
 };
+__device__ __forceinline__ bool full_tile(int64_t tr, int32_t tc, int64_t rows, int64_t cols, int vec) {
+  return vec && (tr + 1) * kGroup <= rows && ((int64_t)tc + 1) * kGroup <= cols;
+}
+// The blocks of a launch: x the column groups, y the tile rows (walked where there are more).
+inline dim3 tile_grid(int64_t rows, int64_t cols) {
+  return dim3((unsigned)((cols + kGroup - 1) / kGroup),
+              (unsigned)std::min<int64_t>((rows + kGroup - 1) / kGroup, 65535));
+}
 inline int64_t tiles_of(int64_t rows, int64_t cols) {
   return ((rows + kGroup - 1) / kGroup) * ((cols + kGroup - 1) / kGroup);
 }
 using TileValues = float[kTilePasses][8];
 
 // One pass of a tile of an f32 or bf16 matrix; zeros past its edges.
-template <typename T>
-__device__ __forceinline__ void load_pass(Pack8<T>& p, const TileAt& at, int i, const T* src, int64_t ld,
+template <typename T, typename At>
+__device__ __forceinline__ void load_pass(Pack8<T>& p, const At& at, int i, const T* src, int64_t ld,
                                           int vec) {
-  const T* s = src + (at.row() + i * kTileRows) * ld + at.col;
-  if (vec && at.width == 8) {
+  const T* s = src + (at.row + i * kTileRows) * ld + at.col;
+  if (At::kFull || (vec && at.width() == 8)) {
     if (at.has(i)) p.load(s); else p.zero();
   } else {
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = at.has(i) && j < at.width ? to_f32(s[j]) : 0.f;
+    for (int j = 0; j < 8; ++j) v[j] = at.has(i) && j < at.width() ? to_f32(s[j]) : 0.f;
     p.set(v);
   }
 }
@@ -192,7 +227,8 @@ template <typename T>
 struct TileRaw {
   using Elem = T;
   Pack8<T> p[kTilePasses];
-  __device__ __forceinline__ void load(const TileAt& at, const T* src, int64_t ld, int vec) {
+  template <typename At>
+  __device__ __forceinline__ void load(const At& at, const T* src, int64_t ld, int vec) {
 #pragma unroll
     for (int i = 0; i < kTilePasses; ++i) load_pass(p[i], at, i, src, ld, vec);
   }
@@ -202,15 +238,16 @@ struct TileRaw {
 struct TileRaw8 {
   uint2 p[kTilePasses];
   float s[kTilePasses];                            // of the row's group (1 for COL groups)
-  __device__ __forceinline__ void load(const TileAt& at, const Fp8Ref& m) {
-    const uint8_t* q = m.q + at.row() * m.ld + at.col;
+  template <typename At>
+  __device__ __forceinline__ void load(const At& at, const Fp8Ref& m) {
+    const uint8_t* q = m.q + at.row * m.ld + at.col;
     const bool rows = m.groups == MFSDP_GROUPS_ROW;
-    const uint8_t* sp = m.s + (rows ? at.row() : at.r0 / kGroup) * m.ld_s + at.group;
+    const uint8_t* sp = m.s + (rows ? at.row : at.r0 / kGroup) * m.ld_s + at.group;
 #pragma unroll
     for (int i = 0; i < kTilePasses; ++i) {
-      const bool in = at.has(i) && at.width > 0;
+      const bool in = at.has(i) && at.width() > 0;
       p[i] = make_uint2(0u, 0u);
-      if (in) p[i] = load_fp8(q + i * (kTileRows * m.ld), at.width);
+      if (in) p[i] = load_fp8(q + i * (kTileRows * m.ld), at.width());
       s[i] = 1.f;
       if (in && m.groups != MFSDP_GROUPS_COL)
         s[i] = scale_value(sp[rows ? i * (kTileRows * m.ld_s) : 0]);
@@ -221,89 +258,110 @@ struct TileRaw8 {
   }
 };
 
-// The tile as 1 x 128 groups.  Whole half-warps take part.
-__device__ __forceinline__ void quantize_row(const TileAt& at, int i, float (&v)[8], const Fp8Ref& m) {
-  const uint32_t byte = scale_byte(group_max(v), m.e5m2);
-  if (!at.has(i) || at.width == 0) return;
-  const int64_t r = at.row() + i * kTileRows;
-  store_fp8(m.q + r * m.ld + at.col, pack_fp8(v, inverse_scale(byte), m.e5m2), at.width);
-  if (at.lane16 == 0) m.s[r * m.ld_s + at.group] = (uint8_t)byte;
+// Two passes of the tile as 1 x 128 groups.  Whole half-warps take part.
+template <typename At>
+__device__ __forceinline__ void quantize_rows(const At& at, int i, float (&u)[8], float (&v)[8],
+                                              const Fp8Ref& m) {
+  uint32_t su, sv;
+  group_scales(u, v, m.e5m2, m.e5m2, su, sv);
+  if (at.width() == 0) return;
+  const int64_t r = at.row + i * kTileRows;
+  uint8_t* q = m.q + r * m.ld + at.col;
+  uint8_t* s = m.s + r * m.ld_s + at.group;
+  if (at.has(i)) {
+    store_fp8(q, pack_fp8(u, inverse_scale(su), m.e5m2), at.width());
+    if (at.lane16 == 0) *s = (uint8_t)su;
+  }
+  if (at.has(i + 1)) {
+    store_fp8(q + kTileRows * m.ld, pack_fp8(v, inverse_scale(sv), m.e5m2), at.width());
+    if (at.lane16 == 0) s[kTileRows * m.ld_s] = (uint8_t)sv;
+  }
 }
 
 // The tile as 128 x 1 groups (COL) or one group (TILE); every thread of the block calls, and values that
 // are not finite become NaN.  The shared memory is free again after the block's next barrier.
-template <bool WHOLE>
-__device__ __forceinline__ void quantize_cols(const TileAt& at, TileSmem& sm, const Fp8Ref& m,
+template <bool WHOLE, typename At>
+__device__ __forceinline__ void quantize_cols(const At& at, TileSmem& sm, const Fp8Ref& m,
                                               TileValues& v) {
+  static_assert(kTilePasses == 4, "four rows a thread");
   const int warp = threadIdx.x >> 5;
   float inv[8];
-  // the columns' (or the tile's) largest values; once more without those that are not finite, if some are
-  for (bool clean = false;; clean = true) {
-    float a[8];
+  // the columns' (or the tile's) scales; once more without the values that are not finite, if some are
+  for (bool again = false;; again = true) {
+    if (again) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = fabsf(v[0][j]);
+      for (int i = 0; i < kTilePasses; ++i)
 #pragma unroll
-      for (int i = 1; i < kTilePasses; ++i)
-        a[j] = clean ? fmaxf(a[j], fabsf(v[i][j])) : max_nan(a[j], v[i][j]);
-      if (clean) a[j] = fmaxf(a[j], 0.f);
-    }
-    bool bad = false;
-    if (WHOLE) {
-      float t = largest(a);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t = max_nan(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
-      if ((threadIdx.x & 31) == 0) sm.top[warp] = t;
+        for (int j = 0; j < 8; ++j) v[i][j] = finite_or_nan(v[i][j]);
       __syncthreads();
-      t = sm.top[0];
+    }
+    uint32_t w[4];                                 // two columns' scales each
 #pragma unroll
-      for (int w = 1; w < kTileThreads / 32; ++w) t = max_nan(t, sm.top[w]);
-      bad = !(t <= FLT_MAX);
-      if (!bad) {
-        const uint32_t byte = scale_byte(t, m.e5m2);
-        if (threadIdx.x == 0) m.s[at.r0 / kGroup * m.ld_s + at.group] = (uint8_t)byte;
-        inv[0] = inverse_scale(byte);
-      } else {
-        __syncthreads();                           // the next round writes sm.top again
+    for (int k = 0; k < 4; ++k) {
+      uint32_t b[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 2 * k + h;
+        const float a =
+            again ? fmaxf(fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])),
+                                fmaxf(fabsf(v[2][j]), fabsf(v[3][j]))), 0.f)
+                  : max_nan(max3_nan(v[0][j], v[1][j], v[2][j]), v[3][j]);
+        b[h] = scale_part(a);
       }
+      w[k] = b[0] | (b[1] << 16);
+    }
+    bool bad;
+    if (WHOLE) {
+      uint32_t t = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t = max_u16x2(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+      if ((threadIdx.x & 31) == 0) sm.col[warp][0] = t;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kTileThreads / 32; ++k) t = max_u16x2(t, sm.col[k][0]);
+      const uint32_t part = max(t & 0xFFFFu, t >> 16), byte = scale_of_part(part, m.e5m2);
+      bad = part >= kMaybe && !again;
+      if (threadIdx.x == 0 && !bad) m.s[at.r0 / kGroup * m.ld_s + at.group] = (uint8_t)byte;
+      inv[0] = inverse_scale(byte);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = max_nan(a[j], __shfl_xor_sync(0xFFFFFFFFu, a[j], 16));
-      if ((threadIdx.x & 16) == 0) {
-        float4* d = reinterpret_cast<float4*>(&sm.col[warp][at.lane16 * 8]);
-        d[0] = make_float4(a[0], a[1], a[2], a[3]);
-        d[1] = make_float4(a[4], a[5], a[6], a[7]);
-      }
+      for (int k = 0; k < 4; ++k) w[k] = max_u16x2(w[k], __shfl_xor_sync(0xFFFFFFFFu, w[k], 16));
+      if ((threadIdx.x & 16) == 0)
+        *reinterpret_cast<uint4*>(&sm.col[warp][at.lane16 * 4]) = make_uint4(w[0], w[1], w[2], w[3]);
       __syncthreads();
-      if (threadIdx.x < kGroup) {
-        float t = sm.col[0][threadIdx.x];
+      bad = false;
+      if (threadIdx.x < kGroup / 2) {
+        uint32_t t = sm.col[0][threadIdx.x];
 #pragma unroll
-        for (int w = 1; w < kTileThreads / 32; ++w) t = max_nan(t, sm.col[w][threadIdx.x]);
-        bad = !(t <= FLT_MAX);
-        const uint32_t byte = bad ? 0u : scale_byte(t, m.e5m2);
-        sm.top[threadIdx.x] = inverse_scale(byte);
-        if (!bad && (int)threadIdx.x < at.cols_here)
-          m.s[at.r0 / kGroup * m.ld_s + at.group * kGroup + threadIdx.x] = (uint8_t)byte;
+        for (int k = 1; k < kTileThreads / 32; ++k) t = max_u16x2(t, sm.col[k][threadIdx.x]);
+        const uint32_t lo = scale_of_part(t & 0xFFFFu, m.e5m2), hi = scale_of_part(t >> 16, m.e5m2);
+        bad = ((t & 0xFFFFu) >= kMaybe || (t >> 16) >= kMaybe) && !again;
+        sm.top[2 * threadIdx.x] = inverse_scale(lo);
+        sm.top[2 * threadIdx.x + 1] = inverse_scale(hi);
+        uint8_t* s = m.s + at.r0 / kGroup * m.ld_s + at.group * kGroup + 2 * threadIdx.x;
+        if ((int)(2 * threadIdx.x) < at.cols_here) s[0] = (uint8_t)lo;
+        if ((int)(2 * threadIdx.x) + 1 < at.cols_here) s[1] = (uint8_t)hi;
       }
       bad = __syncthreads_or(bad);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) inv[j] = sm.top[at.lane16 * 8 + j];
+      for (int k = 0; k < 2; ++k) {
+        const float4 f = reinterpret_cast<const float4*>(sm.top)[at.lane16 * 2 + k];
+        inv[4 * k] = f.x;
+        inv[4 * k + 1] = f.y;
+        inv[4 * k + 2] = f.z;
+        inv[4 * k + 3] = f.w;
+      }
     }
     if (!bad) break;
-#pragma unroll
-    for (int i = 0; i < kTilePasses; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = finite_or_nan(v[i][j]);
-    __syncthreads();
   }
-  uint8_t* q = m.q + at.row() * m.ld + at.col;
+  if (at.width() == 0) return;
+  uint8_t* q = m.q + at.row * m.ld + at.col;
 #pragma unroll
   for (int i = 0; i < kTilePasses; ++i) {
     float u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = v[i][j] * inv[WHOLE ? 0 : j];
-    if (at.has(i) && at.width > 0)
-      store_fp8(q + i * (kTileRows * m.ld), pack_fp8(u, m.e5m2), at.width);
+    if (at.has(i)) store_fp8(q + i * (kTileRows * m.ld), pack_fp8(u, m.e5m2), at.width());
   }
 }
 

@@ -84,13 +84,22 @@ __device__ __forceinline__ void load_param8(const void* src, int is_bf16, int pv
     for (int j = 0; j < 8; ++j) v[j] = src && j < left ? load_param(src, is_bf16, c + j) : fill;
   }
 }
-// A thread's part of a 1 x 128 group (zeros past the row's end); 16 neighbouring threads call.
-__device__ __forceinline__ void store_group(const Fp8Ref& m, int64_t row, int64_t c, int left,
-                                            float (&v)[8]) {
-  const uint32_t byte = scale_byte(group_max(v), m.e5m2);
+// A thread's parts of a row's 1 x 128 groups of y and of h (zeros past the row's end); 16 neighbouring
+// threads call.
+__device__ __forceinline__ void store_groups(const NrArgs& p, int64_t row, int64_t c, int left,
+                                             float (&y)[8], float (&h)[8]) {
+  if (!p.y8.q && !p.h8.q) return;
+  uint32_t sy, sh;
+  group_scales(y, h, p.y8.e5m2, p.h8.e5m2, sy, sh);
   if (left <= 0) return;
-  store_fp8(m.q + row * m.ld + c, pack_fp8(v, inverse_scale(byte), m.e5m2), left);
-  if ((threadIdx.x & 15) == 0) m.s[row * m.ld_s + c / kGroup] = (uint8_t)byte;
+  if (p.y8.q) {
+    store_fp8(p.y8.q + row * p.y8.ld + c, pack_fp8(y, inverse_scale(sy), p.y8.e5m2), left);
+    if ((threadIdx.x & 15) == 0) p.y8.s[row * p.y8.ld_s + c / kGroup] = (uint8_t)sy;
+  }
+  if (p.h8.q) {
+    store_fp8(p.h8.q + row * p.h8.ld + c, pack_fp8(h, inverse_scale(sh), p.h8.e5m2), left);
+    if ((threadIdx.x & 15) == 0) p.h8.s[row * p.h8.ld_s + c / kGroup] = (uint8_t)sh;
+  }
 }
 
 // ---------------------------------------------------------------- forward
@@ -173,11 +182,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
       for (int j = 0; j < 8; ++j) y[j] += w[j];
     }
     if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, left, p.vec, y);
-    if (p.y8.q) {
-      zero_past(y, left);
-      store_group(p.y8, row, c, left, y);
-    }
-    if (p.h8.q) store_group(p.h8, row, c, left, v[k]);
+    zero_past(y, left);
+    store_groups(p, row, c, left, y, v[k]);
   }
 }
 
@@ -244,11 +250,8 @@ __global__ void __launch_bounds__(1024)
     const int left = left_of(c);
     if (p.h) store_part(static_cast<T*>(p.h) + row * p.ld_h, c, left, p.vec, v);
     if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, left, p.vec, y);
-    if (p.y8.q) {
-      zero_past(y, left);
-      store_group(p.y8, row, c, left, y);
-    }
-    if (p.h8.q) store_group(p.h8, row, c, left, v);
+    zero_past(y, left);
+    store_groups(p, row, c, left, y, v);
   }
 }
 

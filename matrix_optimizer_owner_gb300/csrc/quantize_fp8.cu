@@ -14,7 +14,7 @@ namespace {
 
 struct QuantArgs {
   const void* x;
-  int64_t rows, cols, ld, tiles;
+  int64_t rows, cols, ld;
   int32_t vec;
   Fp8Ref src;                 // an 8-bit source
   Fp8Ref row, other;          // 1 x 128 groups; 128 x 1 or 128 x 128 ones
@@ -22,43 +22,50 @@ struct QuantArgs {
 
 enum Form : int { kRow = 1, kCol = 2, kTile = 4 };
 
+template <typename Raw, int FORMS, typename At>
+__device__ __forceinline__ void quantize_tile(const QuantArgs& p, const At& at, TileSmem& sm) {
+  TileValues v;
+  if constexpr (std::is_same<Raw, TileRaw8>::value) {
+    Raw raw;
+    raw.load(at, p.src);
+#pragma unroll
+    for (int i = 0; i < kTilePasses; ++i) raw.get(i, p.src.e5m2, v[i]);
+    if (p.src.groups == MFSDP_GROUPS_COL) {
+      const uint8_t* s = p.src.s + at.r0 / kGroup * p.src.ld_s + at.col;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = j < at.width() ? scale_value(s[j]) : 1.f;
+#pragma unroll
+        for (int i = 0; i < kTilePasses; ++i) v[i][j] *= f;
+      }
+    }
+  } else {
+    Raw raw;
+    raw.load(at, static_cast<const typename Raw::Elem*>(p.x), p.ld, p.vec);
+#pragma unroll
+    for (int i = 0; i < kTilePasses; ++i) raw.get(i, v[i]);
+  }
+  if (FORMS & kRow) {
+#pragma unroll
+    for (int i = 0; i < kTilePasses; i += 2) quantize_rows(at, i, v[i], v[i + 1], p.row);
+  }
+  if (FORMS & (kCol | kTile)) quantize_cols<(FORMS & kTile) != 0>(at, sm, p.other, v);
+}
+
 template <typename Raw, int FORMS>
 __global__ void __launch_bounds__(kTileThreads, 2)
     quantize_kernel(const __grid_constant__ QuantArgs p) {
   __shared__ __align__(16) TileSmem sm;
   pdl_launch();
   pdl_wait();
-  for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    const TileAt at(tile, p.rows, p.cols);
-    TileValues v;
-    if constexpr (std::is_same<Raw, TileRaw8>::value) {
-      Raw raw;
-      raw.load(at, p.src);
-#pragma unroll
-      for (int i = 0; i < kTilePasses; ++i) raw.get(i, p.src.e5m2, v[i]);
-      if (p.src.groups == MFSDP_GROUPS_COL) {
-        const uint8_t* s = p.src.s + at.r0 / kGroup * p.src.ld_s + at.col;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float f = j < at.width ? scale_value(s[j]) : 1.f;
-#pragma unroll
-          for (int i = 0; i < kTilePasses; ++i) v[i][j] *= f;
-        }
-      }
-    } else {
-      Raw raw;
-      raw.load(at, static_cast<const typename Raw::Elem*>(p.x), p.ld, p.vec);
-#pragma unroll
-      for (int i = 0; i < kTilePasses; ++i) raw.get(i, v[i]);
-    }
-    if (FORMS & kRow) {
-#pragma unroll
-      for (int i = 0; i < kTilePasses; ++i) quantize_row(at, i, v[i], p.row);
-    }
-    if (FORMS & (kCol | kTile)) {
-      quantize_cols<(FORMS & kTile) != 0>(at, sm, p.other, v);
-      if (tile + gridDim.x < p.tiles) __syncthreads();
-    }
+  const int64_t tile_rows = (p.rows + kGroup - 1) / kGroup;
+  const int32_t tc = (int32_t)blockIdx.x;
+  for (int64_t tr = blockIdx.y; tr < tile_rows; tr += gridDim.y) {
+    if (full_tile(tr, tc, p.rows, p.cols, p.vec))
+      quantize_tile<Raw, FORMS>(p, TileAt<true>(tr, tc, p.rows, p.cols), sm);
+    else
+      quantize_tile<Raw, FORMS>(p, TileAt<false>(tr, tc, p.rows, p.cols), sm);
+    if ((FORMS & (kCol | kTile)) && tr + gridDim.y < tile_rows) __syncthreads();
   }
 }
 
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__
 
 template <typename Raw>
 cudaError_t launch_quantize(const QuantArgs& a, int forms, cudaStream_t st) {
-  const dim3 grid((unsigned)std::min<int64_t>(a.tiles, 1ll << 30)), block(kTileThreads);
+  const dim3 grid = tile_grid(a.rows, a.cols), block(kTileThreads);
   switch (forms) {
     case kRow: return launch_pdl(quantize_kernel<Raw, kRow>, grid, block, 0, st, a);
     case kCol: return launch_pdl(quantize_kernel<Raw, kCol>, grid, block, 0, st, a);
@@ -157,7 +164,6 @@ extern "C" int mfsdp_quantize_fp8(int64_t rows, int64_t cols, int32_t dtype, con
   a.rows = rows;
   a.cols = cols;
   a.ld = ld_x;
-  a.tiles = tiles_of(rows, cols);
   a.vec = vector_rows(x, ld_x, dtype);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == MFSDP_DTYPE_BF16
@@ -183,7 +189,7 @@ extern "C" int mfsdp_regroup_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_mat
   a.src = ref_of(src);
   a.rows = rows;
   a.cols = cols;
-  a.tiles = tiles_of(rows, cols);
+  a.vec = 1;
   const cudaError_t e = launch_quantize<TileRaw8>(a, forms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }
