@@ -62,12 +62,18 @@ __device__ __forceinline__ float act(float g, float u) {
   return GLU ? y * u : y;
 }
 template <typename T, bool GLU>
-__device__ __forceinline__ float grad_gate(float dy, float g, float u) {
+__device__ __forceinline__ void act_grads(float dy, float g, float u, float& dg, float& du) {
   const float p = gate_of<T, GLU>(g);
-  if (GLU) return dy * p * u * fmaf(g, 1.f - p, 1.f);
-  // beyond 16 p is 0 or 1 in fp32, and the polynomial may be too large for it
-  const float slope = fabsf(g) > 16.f ? 0.f : g * kGelu * fmaf(3.f * 0.044715f, g * g, 1.f);
-  return dy * fmaf(slope, p * (1.f - p), p);
+  if (GLU) {
+    const float s = dy * p;
+    dg = s * u * fmaf(g, 1.f - p, 1.f);
+    du = s * g;
+  } else {
+    // beyond 16 p is 0 or 1 in fp32, and the polynomial may be too large for it
+    const float slope = fabsf(g) > 16.f ? 0.f : g * kGelu * fmaf(3.f * 0.044715f, g * g, 1.f);
+    dg = dy * fmaf(slope, p * (1.f - p), p);
+    du = 0.f;
+  }
 }
 
 template <typename T, typename At>
@@ -86,43 +92,46 @@ __device__ __forceinline__ void store_values(T* base, int64_t ld, const At& at, 
   }
 }
 
-template <typename T, bool GLU, typename At>
-__device__ __forceinline__ void forward_pair(const ActArgs& p, const At& at, int i) {
-  Pack8<T> graw[2], uraw[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    load_pass(graw[h], at, i + h, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
-    if (GLU) load_pass(uraw[h], at, i + h, static_cast<const T*>(p.up), p.ld_up, p.vec);
-  }
-  float g[2][8], u[2][8], y[2][8];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    graw[h].get(g[h]);
-    if (GLU) uraw[h].get(u[h]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[h][j] = act<T, GLU>(g[h][j], GLU ? u[h][j] : 0.f);
-    if (p.y) store_values(static_cast<T*>(p.y), p.ld_y, at, i + h, p.vec, y[h]);
-  }
-  if (p.y8.q) quantize_rows(at, i, y[0], y[1], p.y8);
-  if (p.gate8.q) quantize_rows(at, i, g[0], g[1], p.gate8);
-  if (GLU && p.up8.q) quantize_rows(at, i, u[0], u[1], p.up8);
-}
-
-// Half a tile a block: no group runs down the columns here, and a thread's two rows fit its registers.
+// A block takes 32 rows of 128 columns, a thread 16 consecutive columns of one.  The results are made one
+// after the other from the raw inputs, which keeps a thread within 64 registers.
+constexpr int kFwdThreads = 256;
+constexpr int kFwdRows = kFwdThreads / 8;
 template <typename T, bool GLU>
-__global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kFwdThreads, sizeof(T) == 2 ? 4 : 2)
     activation_forward_kernel(const __grid_constant__ ActArgs p) {
   pdl_launch();
+  Sixteen at;
+  at.group = (int32_t)blockIdx.x;
+  at.col = (int64_t)at.group * kGroup + (threadIdx.x & 7) * 16;
+  at.width = (int)max((int64_t)0, min((int64_t)16, p.cols - at.col));
   pdl_wait();
-  const int64_t halves = ((p.rows + kGroup - 1) / kGroup) * 2;
-  const int32_t tc = (int32_t)blockIdx.x;
-  for (int64_t h = blockIdx.y; h < halves; h += gridDim.y) {
-    const int64_t tr = h >> 1;
-    const int i = (int)(h & 1) * 2;
-    if (full_tile(tr, tc, p.rows, p.cols, p.vec))
-      forward_pair<T, GLU>(p, TileAt<true>(tr, tc, p.rows, p.cols), i);
-    else
-      forward_pair<T, GLU>(p, TileAt<false>(tr, tc, p.rows, p.cols), i);
+  const int64_t row_blocks = (p.rows + kFwdRows - 1) / kFwdRows;
+  for (int64_t b = blockIdx.y; b < row_blocks; b += gridDim.y) {
+    at.row = b * kFwdRows + (threadIdx.x >> 3);
+    at.has = at.row < p.rows;
+    const int n = at.has ? at.width : 0;
+    Pack8<T> graw[2], uraw[2];
+    load_sixteen(graw, static_cast<const T*>(p.gate) + at.row * p.ld_gate + at.col, n, p.vec);
+    if (GLU) load_sixteen(uraw, static_cast<const T*>(p.up) + at.row * p.ld_up + at.col, n, p.vec);
+    {
+      float y[16], u[16];
+      get_sixteen(graw, y);
+      if (GLU) get_sixteen(uraw, u);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] = act<T, GLU>(y[j], GLU ? u[j] : 0.f);
+      if (p.y) store_sixteen(static_cast<T*>(p.y) + at.row * p.ld_y + at.col, n, p.vec, y);
+      if (p.y8.q) quantize_sixteen(at, y, eighth_warp_max(scale_part(largest(y))), p.y8);
+    }
+    if (p.gate8.q) {
+      float g[16];
+      get_sixteen(graw, g);
+      quantize_sixteen(at, g, eighth_warp_max(scale_part(largest(g))), p.gate8);
+    }
+    if (GLU && p.up8.q) {
+      float u[16];
+      get_sixteen(uraw, u);
+      quantize_sixteen(at, u, eighth_warp_max(scale_part(largest(u))), p.up8);
+    }
   }
 }
 
@@ -209,8 +218,8 @@ struct Ahead {
   }
 };
 
-// A block walks the tiles with the next ones' inputs under way.  It holds one gradient in registers at a
-// time, the gate's and then up's, and computes p for both.
+// A block walks the tiles with the next ones' inputs under way, and holds both gradients in registers
+// (one after the other, with p computed twice, took a fifth more instructions).
 template <typename T, bool GLU, bool KEPT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     activation_backward_kernel(const __grid_constant__ ActArgs p) {
@@ -302,30 +311,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           __syncthreads();
         }
       };
-      TileValues v;
-      if (p.dgate || p.dgate_row.q || p.dgate_col.q) {
+      TileValues dg, du;
 #pragma unroll
-        for (int i = 0; i < kTilePasses; ++i) {
-          float d[8], g[8], u[8];
-          in.get(stage, i, 0, d);
-          input(i, 1, g);
-          if constexpr (GLU) input(i, 2, u);
+      for (int i = 0; i < kTilePasses; ++i) {
+        float d[8], g[8], u[8];
+        in.get(stage, i, 0, d);
+        input(i, 1, g);
+        if constexpr (GLU) input(i, 2, u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = grad_gate<T, GLU>(d[j], g[j], GLU ? u[j] : 0.f);
-        }
-        emit(v, p.dgate, p.ld_dgate, p.dgate_row, p.dgate_col);
+        for (int j = 0; j < 8; ++j)
+          act_grads<T, GLU>(d[j], g[j], GLU ? u[j] : 0.f, dg[i][j], du[i][j]);
       }
-      if (GLU && (p.dup || p.dup_row.q || p.dup_col.q)) {
-#pragma unroll
-        for (int i = 0; i < kTilePasses; ++i) {
-          float d[8], g[8];
-          in.get(stage, i, 0, d);
-          input(i, 1, g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = d[j] * g[j] * gate_of<T, GLU>(g[j]);
-        }
-        emit(v, p.dup, p.ld_dup, p.dup_row, p.dup_col);
-      }
+      if (p.dgate || p.dgate_row.q || p.dgate_col.q)
+        emit(dg, p.dgate, p.ld_dgate, p.dgate_row, p.dgate_col);
+      if (GLU && (p.dup || p.dup_row.q || p.dup_col.q))
+        emit(du, p.dup, p.ld_dup, p.dup_row, p.dup_col);
     };
     if (full_tile(here.r, here.c, p.rows, p.cols, p.vec))
       process(TileAt<true>(here.r, here.c, p.rows, p.cols));
@@ -405,9 +405,9 @@ extern "C" int mfsdp_activation_forward(int32_t kind, int64_t rows, int64_t cols
   a.y8 = ref_of(y8);
   a.gate8 = ref_of(gate8);
   a.up8 = ref_of(up8);
-  dim3 grid = tile_grid(rows, cols);
-  const dim3 block(kTileThreads);
-  grid.y = std::min(65535u, 2 * grid.y);
+  const dim3 grid((unsigned)((cols + kGroup - 1) / kGroup),
+                  (unsigned)std::min<int64_t>((rows + kFwdRows - 1) / kFwdRows, 65535));
+  const dim3 block(kFwdThreads);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == MFSDP_DTYPE_BF16;
   const cudaError_t e =

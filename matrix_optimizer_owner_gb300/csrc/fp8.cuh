@@ -156,6 +156,103 @@ __device__ __forceinline__ void group_scales(float (&u)[8], float (&v)[8], int u
   if ((w >> 16) >= kMaybe) sv = cleaned_scale(v, v_e5m2);
 }
 
+// ---- sixteen consecutive values a thread, where no group runs down the columns: eight lanes hold a
+// group of 128, and what a row costs apart from its values falls on twice as many of them
+struct Sixteen {
+  int64_t row, col;
+  int32_t group;
+  int width;                                       // columns of this thread, 0 to 16
+  bool has;                                        // the row exists
+};
+__device__ __forceinline__ float largest(const float (&v)[16]) {
+  float a = max3_nan(v[0], v[1], v[2]);
+#pragma unroll
+  for (int j = 3; j + 1 < 16; j += 2) a = max3_nan(a, v[j], v[j + 1]);
+  return max_nan(a, v[15]);
+}
+__device__ __forceinline__ uint32_t eighth_warp_max(uint32_t w) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) w = max_u16x2(w, __shfl_xor_sync(0xFFFFFFFFu, w, o));
+  return w;
+}
+__device__ __forceinline__ uint32_t cleaned_scale(float (&v)[16], int e5m2) {
+  float a = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    v[j] = finite_or_nan(v[j]);
+    a = fmaxf(a, fabsf(v[j]));
+  }
+  const uint32_t eighth = 0xFFu << (threadIdx.x & 24);
+  for (int o = 4; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(eighth, a, o));
+  return scale_byte(a, e5m2);
+}
+// Whole warps call; values past the row's end are zero.
+__device__ __forceinline__ void quantize_sixteen(const Sixteen& at, float (&v)[16], uint32_t part,
+                                                 const Fp8Ref& m) {
+  uint32_t byte = scale_of_part(part, m.e5m2);
+  if (part >= kMaybe) byte = cleaned_scale(v, m.e5m2);   // the same for the eight lanes; rare
+  if (!at.has || at.width <= 0) return;
+  const float inv = inverse_scale(byte);
+  float lo[8], hi[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    lo[j] = v[j] * inv;
+    hi[j] = v[8 + j] * inv;
+  }
+  const uint2 a = pack_fp8(lo, m.e5m2), b = pack_fp8(hi, m.e5m2);
+  uint8_t* q = m.q + at.row * m.ld + at.col;
+  if (at.width >= 16) {
+    *reinterpret_cast<uint4*>(q) = make_uint4(a.x, a.y, b.x, b.y);
+  } else {
+    store_fp8(q, a, min(at.width, 8));
+    if (at.width > 8) store_fp8(q + 8, b, at.width - 8);
+  }
+  if ((threadIdx.x & 7) == 0) m.s[at.row * m.ld_s + at.group] = (uint8_t)byte;
+}
+// `count` values (0 to 16) of a row from p on; zeros past them.
+template <typename T>
+__device__ __forceinline__ void load_sixteen(Pack8<T> (&r)[2], const T* p, int count, int vec) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (vec && count >= 8 * h + 8) {
+      r[h].load(p + 8 * h);
+    } else {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 8 * h + j < count ? to_f32(p[8 * h + j]) : 0.f;
+      r[h].set(v);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_sixteen(T* p, int count, int vec, const float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = v[8 * h + j];
+    if (vec && count >= 8 * h + 8) {
+      Pack8<T> k;
+      k.set(u);
+      k.store(p + 8 * h);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * h + j < count) p[8 * h + j] = from_f32<T>(u[j]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void get_sixteen(const Pack8<T> (&r)[2], float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float u[8];
+    r[h].get(u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[8 * h + j] = u[j];
+  }
+}
+
 // ---- tiles
 // A block of 512 threads holds a tile of 128 x 128 values: a half-warp a row, eight consecutive
 // columns a thread, four rows 32 apart.  Row scales come from one shuffle tree, column scales from
