@@ -232,7 +232,7 @@ static_assert(kPairSmem <= 227 * 1024, "shared memory");
 // The epilogue reads the shared columns of a tile first and says so, and the next tile's products
 // wait for that alone.
 constexpr uint32_t kAcc1 = 224, kSfCol = 480;
-constexpr int kChunk8 = 8;                  // blocks added up in tensor memory (CHUNKED): 1024 of k
+constexpr int kChunk8 = 32;                 // blocks added up in tensor memory (CHUNKED): 4096 of k
 constexpr int kRasterRows = 8;              // tile rows that walk the columns together
 
 struct PairItem {
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   // the grid's x is (tile, slice) with the slice fastest: a cluster is one tile
   const int split = (int)(blockIdx.x % (unsigned)P.splits);
   const int tile = (int)(blockIdx.x / (unsigned)P.splits);
-  const int w0 = tile * 128;
+  const int w0 = tile / P.tiles_n * 128, t0 = tile % P.tiles_n * NT;
   const int kb0 = min(split * P.kb_split, P.nkb), nk = min(P.kb_split, P.nkb - kb0);
 
   if (warp == 0) {
@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         const int k0 = kb * kB8;
         expect_tx_p(true, fb, C::kStage);
         tma_load_p(true, dst, &P.a, P.a_mn ? w0 : k0, P.a_mn ? k0 : w0, fb);
-        tma_load_p(true, dst + kBox8, &P.b, P.b_mn ? 0 : k0, P.b_mn ? k0 : 0, fb);
+        tma_load_p(true, dst + kBox8, &P.b, P.b_mn ? t0 : k0, P.b_mn ? k0 : t0, fb);
         armed |= 1u << stage;
         last_par = (last_par & ~(1u << stage)) | ((ph ^ 1u) << stage);
         if (++stage == S) { stage = 0; ph ^= 1u; }
@@ -907,7 +907,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     uint32_t ph = 1;
     for (int kb = 0; kb < nk; kb += 4) {
       uint32_t va[4], vb[4];
-      const ScaleAt a(P.sa, w0, P.m, kb0 + kb, P.nkb), b(P.sb, 0, P.n, kb0 + kb, P.nkb);
+      const ScaleAt a(P.sa, w0, P.m, kb0 + kb, P.nkb), b(P.sb, t0, P.n, kb0 + kb, P.nkb);
       ScaleRaw ra, rb;
       issue_scales(P.sa, a, P.m, lane, ra);
       issue_scales(P.sb, b, P.n, lane, rb);
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
       if (!mbar_wait(bar(sf_empty0 + sf), ph, g)) break;
       const uint32_t dst = sbase + C::kSf + (uint32_t)sf * 1024u;
       store_scales(P.sa, dst, w0, P.m, lane, va);
-      store_scales(P.sb, dst + 512u, 0, P.n, lane, vb);
+      store_scales(P.sb, dst + 512u, t0, P.n, lane, vb);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sf_full0 + sf));
@@ -952,28 +952,43 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   __syncthreads();
   cluster_sync_all();
   {
-    // this CTA's share of the tile: narrow indices split, split + splits, ..., two rows of 64 lanes
-    const int live = min(NT, P.n), wide = min(128, P.m - w0);
+    // this CTA's share of the tile: narrow indices split, split + splits, ...; a thread adds four
+    // consecutive wide indices over the slices, in order
+    const int live = min(NT, P.n - t0), wide = min(128, P.m - w0);
     const uint32_t mine = smem_u32(sums);
-    for (int e = threadIdx.x; e < 128 * NT; e += kNarrowThreads) {
-      const int t = e >> 7, r = e & 127;
-      if (t % P.splits != split || t >= live || r >= wide) continue;
-      float v = 0.f;
+    const int r = (threadIdx.x & 31) * 4;
+    for (int t = split + (int)(threadIdx.x >> 5) * P.splits; t < live && r < wide;
+         t += kNarrowThreads / 32 * P.splits) {
+      float v[4];
+#pragma unroll 4
       for (int i = 0; i < P.splits; ++i) {
-        float o;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(o)
-                     : "r"(map_rank(mine + (uint32_t)e * 4u, (uint32_t)i))
+        float o[4];
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+                     : "r"(map_rank(mine + (uint32_t)(t * 128 + r) * 4u, (uint32_t)i))
                      : "memory");
-        v = i == 0 ? o : v + o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = i == 0 ? o[k] : v[k] + o[k];
       }
-      const int64_t at = (int64_t)(w0 + r) * P.sw + (int64_t)t * P.st;
-      if (P.c_bf16) {
-        bf16_t* c = static_cast<bf16_t*>(P.c) + at;
-        *c = from_f32<bf16_t>(P.accumulate ? v + to_f32(*c) : v);
+      const int64_t at = (int64_t)(w0 + r) * P.sw + (int64_t)(t0 + t) * P.st;
+      if (P.sw == 1 && P.vec && r + 4 <= wide && !P.accumulate) {
+        if (P.c_bf16)
+          *reinterpret_cast<uint2*>(static_cast<bf16_t*>(P.c) + at) =
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(P.c) + at) = make_float4(v[0], v[1], v[2], v[3]);
       } else {
-        float* c = static_cast<float*>(P.c) + at;
-        *c = P.accumulate ? v + *c : v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (r + k >= wide) break;
+          if (P.c_bf16) {
+            bf16_t* c = static_cast<bf16_t*>(P.c) + at + k * P.sw;
+            *c = from_f32<bf16_t>(P.accumulate ? v[k] + to_f32(*c) : v[k]);
+          } else {
+            float* c = static_cast<float*>(P.c) + at + k * P.sw;
+            *c = P.accumulate ? v[k] + *c : v[k];
+          }
+        }
       }
     }
   }
@@ -989,7 +1004,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 
 // ---------------------------------------------------------------- host
 constexpr int kPairs = 76;                  // CTA pairs of the device: what the plans count on
-constexpr int64_t kNarrowMost = 128;        // widest narrow side
 
 struct Gemm8Plan {
   bool narrow = false, swap = false;        // swap: the narrow side is A's
@@ -999,14 +1013,15 @@ struct Gemm8Plan {
   size_t bytes = 0;
 };
 
+// What a call is split into, from its sizes alone.  Times in us, as measured.
 Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
   Gemm8Plan p;
   const int nkb = (int)((k + kB8 - 1) / kB8);
-  if (std::min(m, n) <= kNarrowMost) {
+  const int64_t few = std::min(m, n), wide = std::max(m, n);
+  if (few <= 64) {
     p.narrow = true;
     p.swap = m <= n;
-    const int64_t few = std::min(m, n), wide = std::max(m, n);
-    p.nt = few <= 16 ? 16 : few <= 32 ? 32 : few <= 64 ? 64 : 128;
+    p.nt = few <= 16 ? 16 : few <= 32 ? 32 : 64;
     const int64_t tiles = (wide + 127) / 128;
     // slices of k until the device is covered twice, of two blocks at least
     int s = 1;
@@ -1015,25 +1030,41 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
     p.kb_split = (nkb + s - 1) / s;
     return p;
   }
-  const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  // Splits of k that shorten the longest pair's work: rounds of (blocks + what a tile costs beside
-  // them), and a pass over the partial sums.
-  double best = 0.;
-  for (int s = 1; s <= 32 && (s == 1 || nkb / s >= 4); ++s) {
-    const int per = ((nkb + s - 1) / s + 3) / 4 * 4;
-    const int64_t real = (nkb + per - 1) / per;
-    if (s > 1 && real != s) continue;
-    const int64_t rounds = (tiles * s + kPairs - 1) / kPairs;
-    // in block times (0.27 us): 3 beside a tile's own; the join's bytes at 6 TB/s and its launch
-    double cost = (double)rounds * (per + 3);
-    if (s > 1) cost += 8. + (double)s * m * n * 8. / 6e12 / 0.27e-6;
-    if (s == 1 || cost < best * 0.97) {
-      best = cost;
-      p.splits = s;
-      p.kb_split = per;
+  // 128 x 128 tiles, C's rows the wide side: rounds of two CTAs an SM, up to eight slices of k
+  const int64_t small = ((m + 127) / 128) * ((n + 127) / 128);
+  int ns = 1;
+  double narrow = 0.;
+  for (int s = 1; s <= 8 && s <= std::max(1, nkb); ++s) {
+    const int per = (nkb + s - 1) / s;
+    const int64_t rounds = (small * s + 4 * kPairs - 1) / (4 * kPairs);
+    const double t = 3. + (double)rounds * (per * 0.55 + 2.5) + 0.1 * s;
+    if (s == 1 || t < narrow * 0.98) {
+      narrow = t;
+      ns = s;
     }
   }
-  if (p.splits == 1) p.kb_split = nkb;
+  // 256 x 256 tiles on CTA pairs; with slices of k, a pass over the partial sums
+  const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  double pair = 0.;
+  for (int s = 1; s <= 32 && (s == 1 || nkb / s >= 4); ++s) {
+    const int per = ((nkb + s - 1) / s + 3) / 4 * 4;
+    if (s > 1 && (nkb + per - 1) / per != s) continue;
+    const int64_t rounds = (tiles * s + kPairs - 1) / kPairs;
+    double t = 4. + (double)rounds * ((s == 1 ? nkb : per) * 0.32 + 1.5);
+    if (s > 1) t += 2.5 + (double)s * m * n * 8. / 6e6;
+    if (s == 1 || t < pair * 0.97) {
+      pair = t;
+      p.splits = s;
+      p.kb_split = s == 1 ? nkb : per;
+    }
+  }
+  if (narrow < pair) {
+    p.narrow = p.swap = true;
+    p.nt = 128;
+    p.splits = ns;
+    p.kb_split = (nkb + ns - 1) / ns;
+    return p;
+  }
   p.ld_part = (n + 7) / 8 * 8;
   p.bytes = p.splits > 1 ? (size_t)p.splits * m * p.ld_part * 4 : 0;
   return p;
@@ -1190,10 +1221,10 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   cudaError_t e;
   if (plan.narrow) {
     g.tiles_m = (g.m + 127) / 128;
-    g.tiles_n = 1;
+    g.tiles_n = (int32_t)((g.n + nt - 1) / nt);
     g.sw = plan.swap ? 1 : ld_c;
     g.st = plan.swap ? ld_c : 1;
-    const int64_t tiles = g.tiles_m;
+    const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
     e = nt == 16   ? launch_narrow<16>(g, tiles, st)
         : nt == 32 ? launch_narrow<32>(g, tiles, st)
         : nt == 64 ? launch_narrow<64>(g, tiles, st)
@@ -1202,10 +1233,10 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   }
   g.tiles_m = (g.m + 255) / 256;
   g.tiles_n = (g.n + 255) / 256;
-  // The tensor cores cut each of their additions towards zero, which grows with the contraction:
-  // sums that are kept in fp32 are added up in registers every 1024 of k, others where the cuts
-  // would come near half a bf16 step.
-  const bool chunked = !g.c_bf16 || g.kb_split > 512;
+  // The tensor cores cut each of their additions towards zero, which grows with the contraction: sums
+  // that are kept in fp32 are added up in registers every 4096 of k (2e-7 of a Gaussian product's
+  // entries, 5e-7 at 14336), others where the cuts would come near half a bf16 step.
+  const bool chunked = g.kb_split > (g.c_bf16 ? 512 : kChunk8);
   const int pairs = std::max(1, std::min(sms / 2, g.tiles_m * g.tiles_n * g.splits));
   static std::atomic<bool> done[2][64];
   if (chunked) {

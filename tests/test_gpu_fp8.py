@@ -4,7 +4,7 @@ A scaled value is exact and its rounding is defined, so 8-bit results are equal 
 
 A product's entry is a sum of K exact products, S = sum |a b|: the tensor cores add them 32 at a time
 into fp32 without rounding to nearest, so |dc| <= (K / 32 + 8) 2^-22 S, and sums outside them (chunks
-of 1024, slices of the contraction, what C held) add at most (K / 1024 + 34) 2^-24 (S + |c|); a result in
+and slices of the contraction, what C held) add at most (K / 1024 + 34) 2^-24 (S + |c|); a result in
 bf16 is rounded once (2^-9 of a power of two: 2^-8 of the value).
 """
 
@@ -190,7 +190,8 @@ ORIENT = [(False, True), (False, False), (True, False), (True, True)]
 
 @pytest.mark.parametrize("trans_a,trans_b", ORIENT)
 @pytest.mark.parametrize("m,n,k", [(256, 256, 128), (512, 256, 1024), (257, 300, 130),
-                                   (300, 513, 700), (129, 1000, 1), (1000, 140, 2049)])
+                                   (300, 513, 700), (129, 1000, 1), (1000, 140, 2049),
+                                   (70, 300, 900), (1500, 2300, 384), (260, 300, 20000)])
 def test_gemm(m, n, k, trans_a, trans_b):
     _product(m, n, k, trans_a, trans_b, "f32", extra=1)
     _product(m, n, k, trans_a, trans_b, "bf16")
