@@ -740,9 +740,6 @@ int mfsdp_regroup_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_matrix* src,
 int mfsdp_dequantize_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_matrix* src, int32_t dtype,
                          void* out, int64_t ld_out, void* stream);
 
-/* Workspace of mfsdp_gemm_fp8: 0 unless few tiles of C make it split the contraction. */
-int mfsdp_gemm_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t* bytes_out);
-
 /*
  * C = op(A) op(B), or C += op(A) op(B) with `accumulate`: op(A) [m x k], op(B) [k x n] of 8-bit
  * matrices, C [m x n] of c_dtype (f32 or bf16).
@@ -754,12 +751,12 @@ int mfsdp_gemm_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t* byte
  * it is for dx = dy W, and dy COL and x COL with trans_a = 1 for dW = dy^T x.
  * Products run on the tensor cores (block-scaled) with fp32 accumulation; sums kept in fp32 are added
  * up outside them every 4096 of k (8192 where C has few rows or columns).  k == 0 writes zeros (or leaves C as it is).  m, n or k up to
- * 2^31 - 513.  `workspace` may be NULL where mfsdp_gemm_fp8_workspace_bytes gives 0.
+ * 2^31 - 513.
  * A device wait that runs out sets MFSDP_ETIMEOUT in the status word.
  */
 int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_matrix* a, int32_t trans_a,
                    const mfsdp_fp8_matrix* b, int32_t trans_b, int32_t accumulate, int32_t c_dtype,
-                   void* c, int64_t ld_c, void* workspace, size_t workspace_bytes, void* stream);
+                   void* c, int64_t ld_c, void* stream);
 
 /*
  * Residual addition and norm of every row: h = x + residual (h = x without one), mu, r and

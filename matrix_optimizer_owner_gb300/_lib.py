@@ -138,10 +138,8 @@ SIGNATURES = {
     "mfsdp_regroup_fp8": (C.c_int, [_i64, _i64, C.POINTER(Fp8Struct), C.POINTER(Fp8Struct),
                                     C.POINTER(Fp8Struct), _vp]),
     "mfsdp_dequantize_fp8": (C.c_int, [_i64, _i64, C.POINTER(Fp8Struct), _i32, _vp, _i64, _vp]),
-    "mfsdp_gemm_fp8_workspace_bytes": (C.c_int, [_i64, _i64, _i64, C.POINTER(C.c_size_t)]),
     "mfsdp_gemm_fp8": (C.c_int, [_i64, _i64, _i64, C.POINTER(Fp8Struct), _i32,
-                                 C.POINTER(Fp8Struct), _i32, _i32, _i32, _vp, _i64, _vp,
-                                 C.c_size_t, _vp]),
+                                 C.POINTER(Fp8Struct), _i32, _i32, _i32, _vp, _i64, _vp]),
     "mfsdp_norm_residual_forward": (C.c_int, [_i32, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _i64,
                                               _vp, _vp, _f32, _vp, _i64, _vp, _i64,
                                               C.POINTER(Fp8Struct), C.POINTER(Fp8Struct), _vp, _vp,

@@ -26,7 +26,7 @@ LIB = os.path.join(OUT_DIR, "libmfsdp.so")
 SOURCES = ["api.cpp", "plan.cpp", "stream_kernels.cu", "ns_gemm.cu", "noalloc.cu", "repack.cu",
            "shampoo.cu", "soap.cu", "tf32_gemm.cu", "norm.cu", "embedding.cu",
            "head_loss.cu", "quantize_fp8.cu", "gemm_fp8.cu",
-           "norm_residual.cu", "activation.cu"]
+           "norm_residual.cu", "norm_residual_backward.cu", "activation.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]
 

@@ -203,13 +203,12 @@ struct Gemm8Args {
   int32_t m, n, nkb;          // C's sizes and the blocks of k
   int32_t a_mn, b_mn;
   uint32_t idesc;
-  int32_t tiles_m, tiles_n, splits, kb_split;
+  int32_t tiles_m, tiles_n;
+  int32_t splits, kb_split;   // narrow kernel: slices of k
   void* c;
   int64_t ld_c;
   int32_t c_bf16, accumulate;
   int32_t vec;                // C's rows: 0 as they come, 1 on 16-byte boundaries, 2 on 32-byte ones
-  float* part;                // splits > 1: [splits][m][ld_part]
-  int64_t ld_part;
   int64_t sw, st;             // narrow kernel: C's strides along the wide and the narrow side
   uint64_t wait_limit_ns;
   int* status;
@@ -235,22 +234,14 @@ constexpr uint32_t kAcc1 = 224, kSfCol = 480;
 constexpr int kChunk8 = 32;                 // blocks added up in tensor memory (CHUNKED): 4096 of k
 constexpr int kRasterRows = 8;              // tile rows that walk the columns together
 
-struct PairItem {
-  int tm, tn, split, kb0, nk;
+struct PairTile {
+  int tm, tn;
 };
-__device__ __forceinline__ PairItem pair_item(const Gemm8Args& P, int w) {
-  PairItem t;
-  const int tiles = P.tiles_m * P.tiles_n;
-  t.split = w / tiles;
-  const int i = w - t.split * tiles;
+__device__ __forceinline__ PairTile pair_tile(const Gemm8Args& P, int i) {
   const int per = kRasterRows * P.tiles_n, group = i / per;
   const int rows = min(kRasterRows, P.tiles_m - group * kRasterRows);
   const int j = i - group * per;
-  t.tm = group * kRasterRows + j % rows;
-  t.tn = j / rows;
-  t.kb0 = t.split * P.kb_split;
-  t.nk = min(P.kb_split, P.nkb - t.kb0);
-  return t;
+  return PairTile{group * kRasterRows + j % rows, j / rows};
 }
 
 __device__ __forceinline__ void st256(void* p, const uint32_t (&w)[8]) {
@@ -287,15 +278,14 @@ __device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c
   }
 }
 
-// 32 columns of a lane's row to C or to a split's partial sums, whatever C's rows, edges and old values
-// are.  Rows without 16-byte alignment go through the warp's staging area (2 KB), a row of the block at
+// 32 columns of a lane's row to C, whatever C's rows, edges and old values are.  Rows without 16-byte alignment go through the warp's staging area (2 KB), a row of the block at
 // a time.
-__device__ __noinline__ void put_row(const Gemm8Args& P, float* part, int64_t rw, int lane,
-                                     int64_t c0, uint32_t stg, float (&v)[32]) {
+__device__ __noinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane, int64_t c0, uint32_t stg,
+                                     float (&v)[32]) {
   const int64_t r = rw + lane;
-  const bool f32 = part || !P.c_bf16;
-  if (P.accumulate && !part) add_old(P, r, c0, v);
-  if (part || P.vec) {
+  const bool f32 = !P.c_bf16;
+  if (P.accumulate) add_old(P, r, c0, v);
+  if (P.vec) {
     if (r >= P.m) return;
     if (!f32) {
       uint32_t w[16];
@@ -315,12 +305,10 @@ __device__ __noinline__ void put_row(const Gemm8Args& P, float* part, int64_t rw
         }
       }
     } else {
-      float* d = part ? part + r * P.ld_part + c0 : static_cast<float*>(P.c) + r * P.ld_c + c0;
-      // (a split's rows are padded to whole vectors)
-      const int64_t n = part ? P.ld_part : P.n;
+      float* d = static_cast<float*>(P.c) + r * P.ld_c + c0;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        if (c0 + 8 * h + 8 <= n) {
+        if (c0 + 8 * h + 8 <= P.n) {
           reinterpret_cast<float4*>(d)[2 * h] =
               make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
           reinterpret_cast<float4*>(d)[2 * h + 1] =
@@ -328,7 +316,7 @@ __device__ __noinline__ void put_row(const Gemm8Args& P, float* part, int64_t rw
         } else {
 #pragma unroll
           for (int k = 8 * h; k < 8 * h + 8; ++k)
-            if (c0 + k < n) d[k] = v[k];
+            if (c0 + k < P.n) d[k] = v[k];
         }
       }
     }
@@ -367,10 +355,10 @@ __device__ __noinline__ void put_row(const Gemm8Args& P, float* part, int64_t rw
 // memory, so that a warp's stores covered 64 bytes of a row, a tile's epilogue took twice the time.  It
 // has few instructions on purpose: with every case inlined and unrolled, the warps waited mostly for
 // instructions.)
-__device__ __forceinline__ void put_whole(const Gemm8Args& P, float* part, int64_t r, int64_t c0,
+__device__ __forceinline__ void put_whole(const Gemm8Args& P, int64_t r, int64_t c0,
                                           const float (&v)[32]) {
   if (r >= P.m) return;
-  if (!part && P.c_bf16) {
+  if (P.c_bf16) {
     bf16_t* d = static_cast<bf16_t*>(P.c) + r * P.ld_c + c0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -380,7 +368,7 @@ __device__ __forceinline__ void put_whole(const Gemm8Args& P, float* part, int64
       st256(d + 16 * h, o);
     }
   } else {
-    float* d = part ? part + r * P.ld_part + c0 : static_cast<float*>(P.c) + r * P.ld_c + c0;
+    float* d = static_cast<float*>(P.c) + r * P.ld_c + c0;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       uint32_t o[8];
@@ -455,7 +443,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (!usable && threadIdx.x == 0) atomicOr(P.status, kStatusTmemMismatch);
   const Guard g{abort_flag, P.wait_limit_ns, P.status};
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int items = P.tiles_m * P.tiles_n * P.splits;
+  const int tiles = P.tiles_m * P.tiles_n;
 
   if (!usable) {
     // nothing runs: fall through to the teardown
@@ -465,10 +453,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int stage = 0;
       uint32_t ph = 1, armed = 0, last_par = 0;
       bool ok = true;
-      for (int w = pair; w < items && ok; w += npairs) {
-        const PairItem t = pair_item(P, w);
+      for (int w = pair; w < tiles && ok; w += npairs) {
+        const PairTile t = pair_tile(P, w);
         const int a0 = t.tm * 256 + 128 * (int)rank, b0 = t.tn * 256 + 128 * (int)rank;
-        for (int kb = t.kb0; kb < t.kb0 + t.nk; ++kb) {
+        for (int kb = 0; kb < P.nkb; ++kb) {
           if (!mbar_wait(bar(empty0 + stage), ph, g)) { ok = false; break; }
           const uint32_t fb_local = bar(full0 + stage), fb = map_rank(fb_local, 0);
           const uint32_t dst = sbase + (uint32_t)stage * kStageBytes8;
@@ -496,10 +484,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t phase = 0, sf_phase = 0, acc_phase = 0, buf_phase = 1;
       bool ok = true, first = true;
       const Desc8 da(sbase, P.a_mn), db(sbase + kBox8, P.b_mn);
-      for (int w = pair; w < items && ok; w += npairs) {
-        const PairItem t = pair_item(P, w);
+      for (int w = pair; w < tiles && ok; w += npairs) {
+        const PairTile t = pair_tile(P, w);
         int in_chunk = 0;                                 // blocks in the accumulator
-        for (int kb = 0; kb < t.nk && ok; kb += 4) {
+        for (int kb = 0; kb < P.nkb && ok; kb += 4) {
           if (in_chunk == 0) {
             // the accumulator, and the columns that it shares with the one before
             if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g) ||
@@ -522,12 +510,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           copy_scales<2>(sfa, scale_desc(src));
           copy_scales<2>(sfb, scale_desc(src + 512u));
           copy_scales<2>(sfb + 4u, scale_desc(src + 1024u));
-          if ((kb & 4) || kb + 4 >= t.nk) {               // the stage's last group
+          if ((kb & 4) || kb + 4 >= P.nkb) {               // the stage's last group
             tc_commit_pair(bar(sf_empty0 + sf), 0x3);
             if (++sf == F) { sf = 0; sf_phase ^= 1u; }
           }
           const uint32_t d = tmem_base + (acc ? kAcc1 : 0u);
-          const int live = min(4, t.nk - kb);
+          const int live = min(4, P.nkb - kb);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (i < live && ok) {
@@ -549,7 +537,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           buf ^= 1;
           if (buf == 0) buf_phase ^= 1u;
           in_chunk += 4;
-          if (kb + 4 >= t.nk || (CHUNKED && in_chunk == kChunk8)) {
+          if (kb + 4 >= P.nkb || (CHUNKED && in_chunk == kChunk8)) {
             tc_commit_pair(bar(tfull0 + acc), 0x3);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
@@ -567,17 +555,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     int sf = 0, turn = 0;
     uint32_t ph = 1;
     bool ok = true;
-    for (int w = pair; w < items && ok; w += npairs) {
-      const PairItem t = pair_item(P, w);
+    for (int w = pair; w < tiles && ok; w += npairs) {
+      const PairTile t = pair_tile(P, w);
       const int64_t a0 = (int64_t)t.tm * 256 + 128 * rank, b0 = (int64_t)t.tn * 256;
-      for (int kb = 0; kb < t.nk; kb += 8) {
+      for (int kb = 0; kb < P.nkb; kb += 8) {
         if (turn == warp - 2) {
           ScaleRaw raw[2][3];
           auto each = [&](auto&& f) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (kb + 4 * h >= t.nk) break;
-              const int k0 = t.kb0 + kb + 4 * h;
+              if (kb + 4 * h >= P.nkb) break;
+              const int k0 = kb + 4 * h;
               f(P.sa, ScaleAt(P.sa, a0, P.m, k0, P.nkb), P.m, h, 0);
               f(P.sb, ScaleAt(P.sb, b0, P.n, k0, P.nkb), P.n, h, 1);
               f(P.sb, ScaleAt(P.sb, b0 + 128, P.n, k0, P.nkb), P.n, h, 2);
@@ -610,22 +598,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int w = pair; w < items && ok; w += npairs) {
-      const PairItem t = pair_item(P, w);
+    for (int w = pair; w < tiles && ok; w += npairs) {
+      const PairTile t = pair_tile(P, w);
       const int64_t rw = (int64_t)t.tm * 256 + 128 * rank + quarter * 32;
       const int64_t cb = (int64_t)t.tn * 256 + half * 128;
       const int nq = rw < P.m && cb < P.n ? (int)min((int64_t)4, (P.n - cb + 31) / 32) : 0;
-      float* part = P.splits > 1 ? P.part + (int64_t)t.split * P.m * P.ld_part : nullptr;
-      const bool plain = part || (P.vec == 2 && !P.accumulate);
+      const bool plain = P.vec == 2 && !P.accumulate;
       auto put = [&](int q, float (&v)[32]) {
         const int64_t c0 = cb + 32 * q;
         if (plain && c0 + 32 <= P.n) {
-          put_whole(P, part, rw + lane, c0, v);
+          put_whole(P, rw + lane, c0, v);
         } else {
           float o[32];                                    // (the call's copy: v stays in registers)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = v[k];
-          put_row(P, part, rw, lane, c0, stg, o);
+          put_row(P, rw, lane, c0, stg, o);
         }
       };
       // the shared columns: this warp's chunk `sh` of this accumulator, if it holds them
@@ -645,7 +632,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int k = 0; k < 32; ++k) sum[q][k] = 0.f;
-        for (int left = t.nk; left > 0; left -= kChunk8) {
+        for (int left = P.nkb; left > 0; left -= kChunk8) {
           if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) { ok = false; break; }
           tc_fence_after();
           const int sh = shared_chunk();
@@ -727,55 +714,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------- partial sums
-struct JoinArgs8 {
-  const float* part;
-  int64_t m, n, ld_part, ld_c;
-  int32_t splits, c_bf16, accumulate, vec;
+// An empty contraction.
+struct ZeroArgs8 {
   void* c;
+  int64_t m, n, ld_c;
+  int32_t c_bf16;
 };
-// Adds a split contraction's partial sums in order: four consecutive columns a thread.
-__global__ void __launch_bounds__(256) gemm_fp8_join_kernel(const __grid_constant__ JoinArgs8 p) {
+__global__ void __launch_bounds__(256) gemm_fp8_zero_kernel(const __grid_constant__ ZeroArgs8 p) {
   pdl_launch();
   pdl_wait();
-  const int64_t quads = p.ld_part / 4, total = p.m * quads, step = (int64_t)gridDim.x * 256;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
-    const int64_t r = e / quads, c = (e % quads) * 4;
-    const float* s = p.part + r * p.ld_part + c;
-    float4 v = p.splits ? *reinterpret_cast<const float4*>(s) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 1; i < p.splits; ++i) {
-      const float4 o = *reinterpret_cast<const float4*>(s + (int64_t)i * p.m * p.ld_part);
-      v.x += o.x;
-      v.y += o.y;
-      v.z += o.z;
-      v.w += o.w;
-    }
-    float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (!p.accumulate || c + j >= p.n) continue;
-      const int64_t at = r * p.ld_c + c + j;
-      f[j] += p.c_bf16 ? to_f32(static_cast<const bf16_t*>(p.c)[at])
-                       : static_cast<const float*>(p.c)[at];
-    }
-    if (p.vec && c + 4 <= p.n) {
-      if (p.c_bf16)
-        *reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.c) + r * p.ld_c + c) =
-            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-      else
-        *reinterpret_cast<float4*>(static_cast<float*>(p.c) + r * p.ld_c + c) =
-            make_float4(f[0], f[1], f[2], f[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (c + j >= p.n) continue;
-        if (p.c_bf16)
-          static_cast<bf16_t*>(p.c)[r * p.ld_c + c + j] = from_f32<bf16_t>(f[j]);
-        else
-          static_cast<float*>(p.c)[r * p.ld_c + c + j] = f[j];
-      }
-    }
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < p.m * p.n; e += (int64_t)gridDim.x * 256) {
+    const int64_t at = e / p.n * p.ld_c + e % p.n;
+    if (p.c_bf16) static_cast<bf16_t*>(p.c)[at] = from_f32<bf16_t>(0.f);
+    else static_cast<float*>(p.c)[at] = 0.f;
   }
 }
 
@@ -1009,8 +960,6 @@ struct Gemm8Plan {
   bool narrow = false, swap = false;        // swap: the narrow side is A's
   int nt = 0;
   int splits = 1, kb_split = 0;
-  int64_t ld_part = 0;
-  size_t bytes = 0;
 };
 
 // What a call is split into, from its sizes alone.  Times in us, as measured.
@@ -1043,30 +992,15 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
       ns = s;
     }
   }
-  // 256 x 256 tiles on CTA pairs; with slices of k, a pass over the partial sums
+  // 256 x 256 tiles on CTA pairs
   const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  double pair = 0.;
-  for (int s = 1; s <= 32 && (s == 1 || nkb / s >= 4); ++s) {
-    const int per = ((nkb + s - 1) / s + 3) / 4 * 4;
-    if (s > 1 && (nkb + per - 1) / per != s) continue;
-    const int64_t rounds = (tiles * s + kPairs - 1) / kPairs;
-    double t = 4. + (double)rounds * ((s == 1 ? nkb : per) * 0.32 + 1.5);
-    if (s > 1) t += 2.5 + (double)s * m * n * 8. / 6e6;
-    if (s == 1 || t < pair * 0.97) {
-      pair = t;
-      p.splits = s;
-      p.kb_split = s == 1 ? nkb : per;
-    }
-  }
+  const double pair = 5. + (double)((tiles + kPairs - 1) / kPairs) * (nkb * 0.34 + 2.);
   if (narrow < pair) {
     p.narrow = p.swap = true;
     p.nt = 128;
     p.splits = ns;
     p.kb_split = (nkb + ns - 1) / ns;
-    return p;
   }
-  p.ld_part = (n + 7) / 8 * 8;
-  p.bytes = p.splits > 1 ? (size_t)p.splits * m * p.ld_part * 4 : 0;
   return p;
 }
 
@@ -1132,18 +1066,10 @@ cudaError_t launch_narrow(const Gemm8Args& a, int64_t tiles, cudaStream_t st) {
 
 using namespace mfsdp;
 
-extern "C" int mfsdp_gemm_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, size_t* bytes_out) {
-  if (!bytes_out) return MFSDP_EINVAL;
-  const int chk = check_sizes(m, n, k);
-  if (chk != MFSDP_OK) return chk;
-  *bytes_out = m && n ? plan_gemm(m, n, k).bytes : 0;
-  return MFSDP_OK;
-}
-
 extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_matrix* a,
                               int32_t trans_a, const mfsdp_fp8_matrix* b, int32_t trans_b,
                               int32_t accumulate, int32_t c_dtype, void* c, int64_t ld_c,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              void* stream) {
   if (!a || !b || !dtype_ok(c_dtype)) return MFSDP_EINVAL;
   int chk = check_sizes(m, n, k);
   if (chk != MFSDP_OK) return chk;
@@ -1158,11 +1084,6 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   if (!c || ld_c < n) return MFSDP_EINVAL;
   if (!aligned_to(c, dtype_bytes(c_dtype))) return MFSDP_EALIGN;
   const Gemm8Plan plan = plan_gemm(m, n, k);
-  if (plan.bytes) {
-    if (!workspace) return MFSDP_EINVAL;
-    if (!aligned_to(workspace, 256)) return MFSDP_EALIGN;
-    if (workspace_bytes < plan.bytes) return MFSDP_EWORKSPACE;
-  }
   if (k == 0 && accumulate) return MFSDP_OK;
   int sms = 0;
   const int dst = device_sms(&sms);
@@ -1172,21 +1093,12 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int vec = !vector_rows(c, ld_c, c_dtype) ? 0
                   : aligned_to(c, 32) && (ld_c * (int64_t)dtype_bytes(c_dtype)) % 32 == 0 ? 2 : 1;
-  JoinArgs8 j{};
-  j.part = static_cast<const float*>(workspace);
-  j.m = m;
-  j.n = n;
-  j.ld_part = (n + 7) / 8 * 8;
-  j.ld_c = ld_c;
-  j.splits = k ? plan.splits : 0;
-  j.c_bf16 = c_dtype == MFSDP_DTYPE_BF16;
-  j.accumulate = accumulate != 0;
-  j.vec = vec;
-  j.c = c;
-  const dim3 join_grid((unsigned)std::min<int64_t>((m * (j.ld_part / 4) + 255) / 256, sms * 16ll));
-  if (k == 0)
-    return launch_pdl(gemm_fp8_join_kernel, join_grid, dim3(256), 0, st, j) == cudaSuccess
-               ? MFSDP_OK : MFSDP_ECUDA;
+  if (k == 0) {
+    const ZeroArgs8 z{c, m, n, ld_c, c_dtype == MFSDP_DTYPE_BF16};
+    const dim3 grid((unsigned)std::min<int64_t>((m * n + 255) / 256, sms * 16ll));
+    return launch_pdl(gemm_fp8_zero_kernel, grid, dim3(256), 0, st, z) == cudaSuccess ? MFSDP_OK
+                                                                                      : MFSDP_ECUDA;
+  }
 
   Gemm8Args g{};
   const mfsdp_fp8_matrix *wide = plan.swap ? b : a, *other = plan.swap ? a : b;
@@ -1211,11 +1123,9 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   g.kb_split = plan.kb_split;
   g.c = c;
   g.ld_c = ld_c;
-  g.c_bf16 = j.c_bf16;
-  g.accumulate = j.accumulate;
+  g.c_bf16 = c_dtype == MFSDP_DTYPE_BF16;
+  g.accumulate = accumulate != 0;
   g.vec = vec;
-  g.part = static_cast<float*>(workspace);
-  g.ld_part = plan.ld_part;
   g.wait_limit_ns = wait_limit_ns();
   g.status = status;
   cudaError_t e;
@@ -1236,8 +1146,8 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   // The tensor cores cut each of their additions towards zero, which grows with the contraction: sums
   // that are kept in fp32 are added up in registers every 4096 of k (2e-7 of a Gaussian product's
   // entries, 5e-7 at 14336), others where the cuts would come near half a bf16 step.
-  const bool chunked = g.kb_split > (g.c_bf16 ? 512 : kChunk8);
-  const int pairs = std::max(1, std::min(sms / 2, g.tiles_m * g.tiles_n * g.splits));
+  const bool chunked = g.nkb > (g.c_bf16 ? 512 : kChunk8);
+  const int pairs = std::max(1, std::min(sms / 2, g.tiles_m * g.tiles_n));
   static std::atomic<bool> done[2][64];
   if (chunked) {
     e = allow_smem(done[1], gemm_fp8_pair_kernel<true>, kPairSmem);
@@ -1248,7 +1158,5 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
     if (e == cudaSuccess)
       e = launch_clusters(gemm_fp8_pair_kernel<false>, 2 * pairs, 2, kPairThreads, kPairSmem, st, g);
   }
-  if (e == cudaSuccess && g.splits > 1)
-    e = launch_pdl(gemm_fp8_join_kernel, join_grid, dim3(256), 0, st, j);
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }

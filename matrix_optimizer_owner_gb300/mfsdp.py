@@ -874,21 +874,12 @@ def mfsdp_dequantize_fp8(src: Fp8Matrix, out, stream=None) -> None:
         shape[0], shape[1], s, code, out.data_ptr(), ld, st))
 
 
-@functools.lru_cache(maxsize=256)
-def mfsdp_gemm_fp8_workspace_bytes(m: int, n: int, k: int) -> int:
-    out = C.c_size_t(0)
-    _check("mfsdp_gemm_fp8_workspace_bytes",
-           _lib.load().mfsdp_gemm_fp8_workspace_bytes(m, n, k, C.byref(out)))
-    return out.value
-
-
 def mfsdp_gemm_fp8(a: Fp8Matrix, b: Fp8Matrix, c, trans_a: bool = False, trans_b: bool = False,
-                   accumulate: bool = False, workspace=None, stream=None) -> None:
+                   accumulate: bool = False, stream=None) -> None:
     """``c = op(a) @ op(b)`` of 8-bit matrices (op = transpose where ``trans_a`` / ``trans_b``), in
     float32 or bfloat16; added to ``c`` with ``accumulate``.  Scales are shared along the contraction:
     GROUPS_ROW or GROUPS_TILE for ``a`` and for ``b`` with ``trans_b``, GROUPS_COL or GROUPS_TILE for
-    ``b`` and for ``a`` with ``trans_a``.  ``workspace`` (uint8) defaults to this thread's for the
-    current stream."""
+    ``b`` and for ``a`` with ``trans_a``."""
     sa, sb = _two_dims(a.data, "a"), _two_dims(b.data, "b")
     m, k = (sa[1], sa[0]) if trans_a else (sa[0], sa[1])
     kb, n = (sb[1], sb[0]) if trans_b else (sb[0], sb[1])
@@ -899,14 +890,9 @@ def mfsdp_gemm_fp8(a: Fp8Matrix, b: Fp8Matrix, c, trans_a: bool = False, trans_b
     ld = _matrix(c, (m, n), c.dtype, dev, "c")
     fa, fb = _fp8(a, sa, dev, "a"), _fp8(b, sb, dev, "b")
     st = _device_stream(dev, stream)
-    need = mfsdp_gemm_fp8_workspace_bytes(m, n, k)
-    wp, nbytes = None, 0
-    if need or workspace is not None:
-        ws, nbytes = _workspace(workspace, need, c, dev, stream, st)
-        wp = ws.data_ptr()
     _check("mfsdp_gemm_fp8", _lib.load().mfsdp_gemm_fp8(
         m, n, k, fa, 1 if trans_a else 0, fb, 1 if trans_b else 0, 1 if accumulate else 0, code,
-        c.data_ptr(), ld, wp, nbytes, st))
+        c.data_ptr(), ld, st))
 
 
 def _rows(t, shape, dtype, dev: int, name: str):

@@ -160,7 +160,7 @@ def _operand(rows, cols, groups, kind, gen, extra=0, spread=3):
 
 
 def _product(m, n, k, trans_a, trans_b, dtype, kinds=("e4m3", "e4m3"), groups=None, accumulate=False,
-             seed=0, extra=0, offset=0, pitch=0, ws=None):
+             seed=0, extra=0, offset=0, pitch=0):
     from matrix_optimizer_owner_gb300 import mfsdp
     gen = torch.Generator(device="cuda").manual_seed(seed)
     ga = (groups or ("", ""))[0] or ("col" if trans_a else "row")
@@ -170,8 +170,7 @@ def _product(m, n, k, trans_a, trans_b, dtype, kinds=("e4m3", "e4m3"), groups=No
     base = torch.randn(m * (n + pitch) + offset, generator=gen, device="cuda").to(TYPES[dtype])
     c = base[offset:].view(m, n + pitch)[:, :n]
     old, keep = _np(c).copy(), base[offset:].view(m, n + pitch)[:, n:].clone()
-    mfsdp.mfsdp_gemm_fp8(a, b, c, trans_a=trans_a, trans_b=trans_b, accumulate=accumulate,
-                         workspace=ws)
+    mfsdp.mfsdp_gemm_fp8(a, b, c, trans_a=trans_a, trans_b=trans_b, accumulate=accumulate)
     A, B = va.T if trans_a else va, vb if not trans_b else vb.T
     ref, S = A @ B, np.abs(A) @ np.abs(B)
     if accumulate:
@@ -260,16 +259,14 @@ def test_gemm_nan_stays_in_its_row(m, n):
 
 
 def test_gemm_repeats_and_streams():
-    """The same bits each time, on another stream too, with the caller's workspace."""
+    """The same bits each time, on another stream too."""
     from matrix_optimizer_owner_gb300 import mfsdp
     for m, n, k in ((300, 260, 20000), (600, 700, 512), (7, 900, 4096)):
         a, b, c = _product(m, n, k, True, False, "f32")
         first = c.clone()
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
-        need = mfsdp.mfsdp_gemm_fp8_workspace_bytes(m, n, k)
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
-        for kw in (dict(), dict(stream=s), dict(workspace=ws)):
+        for kw in (dict(), dict(stream=s)):
             c.zero_()
             s.wait_stream(torch.cuda.current_stream())
             mfsdp.mfsdp_gemm_fp8(a, b, c, trans_a=True, **kw)
