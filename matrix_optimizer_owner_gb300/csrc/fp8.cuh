@@ -93,16 +93,29 @@ __device__ __forceinline__ uint2 pack_fp8(const float (&v)[8], float inv, int e5
   for (int j = 0; j < 8; ++j) u[j] = v[j] * inv;
   return pack_fp8(u, e5m2);
 }
-__device__ __forceinline__ void unpack_fp8(uint2 r, int e5m2, float scale, float (&v)[8]) {
+__device__ __forceinline__ void unpack_fp8(uint2 r, int e5m2, float (&v)[8]) {
   const uint32_t w[4] = {r.x & 0xFFFFu, r.x >> 16, r.y & 0xFFFFu, r.y >> 16};
+  __half2_raw h[4];
+  if (e5m2) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      h[k] = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[k], __NV_E5M2);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      h[k] = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[k], __NV_E4M3);
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[k],
-                                                     e5m2 ? __NV_E5M2 : __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[2 * k] = f.x * scale;
-    v[2 * k + 1] = f.y * scale;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+    v[2 * k] = f.x;
+    v[2 * k + 1] = f.y;
   }
+}
+__device__ __forceinline__ void unpack_fp8(uint2 r, int e5m2, float scale, float (&v)[8]) {
+  unpack_fp8(r, e5m2, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= scale;
 }
 // The first n (1 to 8) bytes of a chunk at p, which starts on an 8-byte boundary.
 __device__ __forceinline__ void store_fp8(uint8_t* p, uint2 r, int n) {

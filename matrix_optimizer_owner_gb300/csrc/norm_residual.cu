@@ -3,7 +3,7 @@
 // Per row of n elements (RMS norm: mu = 0 and no bias):
 //     h = x + r,  mu = sum(h) / n,  s = 1 / sqrt(sum((h - mu)^2) / n + eps),  y = (h - mu) s w + b
 // h and y leave in the caller's type, in 8 bits (1 x 128 groups), or both, each rounded once from the
-// fp32 value.  Bound by memory.  A row lies in registers over a warp (up to 1024 elements) or a block, so
+// fp32 value.  Bound by memory.  A row lies in registers over a warp (up to 768 elements) or a block, so
 // neighbouring threads hold a group of 128 and its largest value takes a few shuffles.
 #include "norm_residual.cuh"
 
@@ -11,9 +11,9 @@ namespace mfsdp {
 namespace {
 
 // ---------------------------------------------------------------- forward
-// Rows of up to 1024 elements: a warp each, eight consecutive elements a lane, K times.
+// Rows of up to 768 elements: a warp each, eight consecutive elements a lane, K times.
 template <typename T, int K>
-__global__ void __launch_bounds__(32 * kNormWarps)
+__global__ void __launch_bounds__(32 * kNormWarps, sizeof(T) == 2 ? 4 : 2)
     norm_residual_forward_kernel(const __grid_constant__ NrArgs p) {
   constexpr int TPR = 32;
   float* red = nullptr;                   // (a warp's sums need no shared memory)
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(32 * kNormWarps)
   }
 }
 
-// Rows of more than 1024 elements: a block each, sixteen consecutive elements a thread.  Eight lanes hold
+// Rows of more than 768 elements: a block each, sixteen consecutive elements a thread.  Eight lanes hold
 // a group of 128, and what a row costs apart from its values falls on twice as many of them (8192 rows
 // of 4096: 49 us with eight a thread).
 template <typename T, int TPR, bool LAYER>
@@ -244,23 +244,26 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ---------------------------------------------------------------- dispatch
-struct NrForward {
-  const NrArgs& a;
-  cudaStream_t st;
-  template <typename T, int TPR, int K>
-  cudaError_t operator()() const {
-    if constexpr (TPR == 32) {
-      return launch_pdl(norm_residual_forward_kernel<T, K>,
-                        dim3((unsigned)((a.rows + kNormWarps - 1) / kNormWarps)),
-                        dim3(32 * kNormWarps), 0, st, a);
-    } else {
-      const dim3 grid((unsigned)a.rows), block(TPR);
-      return a.layer
-                 ? launch_pdl(norm_residual_forward_wide_kernel<T, TPR, true>, grid, block, 0, st, a)
+template <typename T, int TPR>
+cudaError_t launch_wide(const NrArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)a.rows), block(TPR);
+  return a.layer ? launch_pdl(norm_residual_forward_wide_kernel<T, TPR, true>, grid, block, 0, st, a)
                  : launch_pdl(norm_residual_forward_wide_kernel<T, TPR, false>, grid, block, 0, st, a);
-    }
-  }
-};
+}
+template <typename T>
+cudaError_t launch_forward(const NrArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.rows + kNormWarps - 1) / kNormWarps)), block(32 * kNormWarps);
+  if (a.cols <= 256) return launch_pdl(norm_residual_forward_kernel<T, 1>, grid, block, 0, st, a);
+  if (a.cols <= 512) return launch_pdl(norm_residual_forward_kernel<T, 2>, grid, block, 0, st, a);
+  // (768 in 64 threads of sixteen leaves a quarter of them idle: 29 -> 36 us for 16384 rows; 1024 fills
+  // them: 46 -> 32)
+  if (a.cols <= 768) return launch_pdl(norm_residual_forward_kernel<T, 3>, grid, block, 0, st, a);
+  if (a.cols <= 1024) return launch_wide<T, 64>(a, st);
+  if (a.cols <= 2048) return launch_wide<T, 128>(a, st);
+  if (a.cols <= 4096) return launch_wide<T, 256>(a, st);
+  if (a.cols <= kRegRowMax) return launch_wide<T, 512>(a, st);
+  return launch_pdl(norm_residual_forward_long_kernel<T>, dim3((unsigned)a.rows), dim3(1024), 0, st, a);
+}
 
 }  // namespace
 }  // namespace mfsdp
@@ -316,15 +319,6 @@ extern "C" int mfsdp_norm_residual_forward(
           (!h || vector_rows(h, ld_h, dtype)) && (!y || vector_rows(y, ld_y, dtype));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == MFSDP_DTYPE_BF16;
-  cudaError_t e;
-  if (cols > kRegRowMax) {
-    e = bf ? launch_pdl(norm_residual_forward_long_kernel<bf16_t>, dim3((unsigned)rows), dim3(1024), 0,
-                        st, a)
-           : launch_pdl(norm_residual_forward_long_kernel<float>, dim3((unsigned)rows), dim3(1024), 0,
-                        st, a);
-  } else {
-    const NrForward f{a, st};
-    e = bf ? by_row_shape<bf16_t>(cols, f) : by_row_shape<float>(cols, f);
-  }
+  const cudaError_t e = bf ? launch_forward<bf16_t>(a, st) : launch_forward<float>(a, st);
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }

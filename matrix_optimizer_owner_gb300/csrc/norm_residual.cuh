@@ -1,5 +1,5 @@
-// What the two directions of the norm with a residual share: their arguments, a thread's chunk of a row
-// with its edges, and the choice of a kernel's shape.
+// What the two directions of the norm with a residual share: their arguments, and a thread's chunk of
+// a row with its edges.
 #pragma once
 
 #include "fp8.cuh"
@@ -89,18 +89,6 @@ __device__ __forceinline__ void store_groups(const NrArgs& p, int64_t row, int64
     store_fp8(p.h8.q + row * p.h8.ld + c, pack_fp8(h, inverse_scale(sh), p.h8.e5m2), left);
     if ((threadIdx.x & 15) == 0) p.h8.s[row * p.h8.ld_s + c / kGroup] = (uint8_t)sh;
   }
-}
-
-// TPR and K are the smallest that hold the row; f is called with the kernel's shape.
-template <typename T, typename F>
-cudaError_t by_row_shape(int64_t cols, F&& f) {
-  if (cols <= 256) return f.template operator()<T, 32, 1>();
-  if (cols <= 512) return f.template operator()<T, 32, 2>();
-  if (cols <= 768) return f.template operator()<T, 32, 3>();
-  if (cols <= kWarpRowMax) return f.template operator()<T, 32, 4>();
-  if (cols <= 2048) return f.template operator()<T, 128, 2>();
-  if (cols <= 4096) return f.template operator()<T, 256, 2>();
-  return f.template operator()<T, 512, 2>();
 }
 
 }  // namespace

@@ -6,6 +6,7 @@
 // over a warp (up to 1024 elements) or a block, with the next rows under way to shared memory; a block's
 // column sums stay in registers and are joined by a second launch, in block order.
 #include <algorithm>
+#include <type_traits>
 
 #include "norm_residual.cuh"
 
@@ -82,18 +83,18 @@ struct Rows {
                    : "memory");
     p.get(v);
   }
-  __device__ __forceinline__ void get8(int stage, int k, int e5m2, float scale, float (&v)[8]) const {
+  __device__ __forceinline__ void get8(int stage, int k, int e5m2, float (&v)[8]) const {
     uint2 r;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
                  : "=r"(r.x), "=r"(r.y)
                  : "r"(at(stage, k, 2, 0))
                  : "memory");
-    unpack_fp8(r, e5m2, scale, v);
+    unpack_fp8(r, e5m2, v);
   }
 };
 
 template <typename T, int TPR, int K, bool H8, bool LAYER>
-__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR, TPR == 32 ? 2 : 1)
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR)
     norm_residual_backward_kernel(const __grid_constant__ NrArgs p) {
   using R = Rows<T, TPR, K, H8>;
   constexpr int NR = R::NR, D = R::kDepth;
@@ -169,11 +170,18 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR, TPR == 32 ?
     }
   };
   auto values = [&](int st, const Stat& s, int k, float (&z)[8], float (&g)[8]) {
-    if (H8) ring.get8(st, k, p.h8.e5m2, scale_value(s.byte[H8 ? k : 0]), z);
-    else ring.get(st, k, 2, z);
+    // (an 8-bit h takes its scale and rstd in one factor: a power of two changes no rounding)
+    float f = s.rstd;
+    if (H8) {
+      f *= scale_value(s.byte[H8 ? k : 0]);
+      ring.get8(st, k, p.h8.e5m2, z);
+    } else {
+      ring.get(st, k, 2, z);
+    }
     ring.get(st, k, 0, g);
+    const float shift = -s.mean * s.rstd;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = LAYER ? (z[j] - s.mean) * s.rstd : z[j] * s.rstd;
+    for (int j = 0; j < 8; ++j) z[j] = LAYER ? fmaf(z[j], f, shift) : z[j] * f;
   };
   // a chunk's part of the row's sums and of the columns' (past the row's end dy is 0)
   auto add = [&](int k, const float (&z)[8], float (&g)[8], float2& s) {
@@ -188,11 +196,20 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR, TPR == 32 ?
       s.y = fmaf(g[j], z[j], s.y);
     }
   };
+  // (`weighted`: g holds g w already)
   auto finish = [&](int st, int k, int64_t i, const float (&z)[8], float (&g)[8], const float2& s,
-                    float r) {
+                    float r, auto weighted) {
     const float s1 = LAYER ? s.x * p.inv_n : 0.f, s2 = s.y * p.inv_n;
-    float d[8], wk[8];
-    weights(k, wk);
+    float d[8];
+    if constexpr (!decltype(weighted)::value) {
+      float wk[8];
+      weights(k, wk);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = fmaf(g[j], wk[j], -s1);
+    } else if (LAYER) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] -= s1;
+    }
     if (p.dres) {
       ring.get(st, k, 1, d);
     } else {
@@ -200,7 +217,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR, TPR == 32 ?
       for (int j = 0; j < 8; ++j) d[j] = 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = fmaf(fmaf(g[j], wk[j], -s1) - z[j] * s2, r, d[j]);
+    for (int j = 0; j < 8; ++j) g[j] = fmaf(fmaf(-z[j], s2, g[j]), r, d[j]);
     {
       const int64_t c = elem_of<TPR, true>(t, k, 0);
       store_part(static_cast<T*>(p.dx) + i * p.ld_dx, c, (int)(n - c), p.vec, g);
@@ -218,26 +235,41 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarps : TPR, TPR == 32 ?
     for (int i = 0; i < NR; ++i) fetch(row + (D - NR + i) * step, wrap(stage + D - NR + i));
     ring.wait();
     float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+    if constexpr (TPR == 32) {
+      // a warp's row: z and g w stay in registers over the row's sums
+      float z[K][8], g[K][8];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float z[8], g[8];
-      values(stage, stat[0], k, z, g);
-      add(k, z, g, s0);
-      if (two) {
-        values(other, stat[NR - 1], k, z, g);
-        add(k, z, g, s1);
+      for (int k = 0; k < K; ++k) {
+        values(stage, stat[0], k, z[k], g[k]);
+        add(k, z[k], g[k], s0);
       }
-    }
-    if (NR == 2) row_sum4<TPR>(s0, s1, red, turn);
-    else row_sum2<TPR>(s0.x, s0.y, red, turn);
+      row_sum2<TPR>(s0.x, s0.y, red, turn);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float z[8], g[8];
-      values(stage, stat[0], k, z, g);
-      finish(stage, k, row, z, g, s0, stat[0].rstd);
-      if (two) {
-        values(other, stat[NR - 1], k, z, g);
-        finish(other, k, row + step, z, g, s1, stat[NR - 1].rstd);
+      for (int k = 0; k < K; ++k)
+        finish(stage, k, row, z[k], g[k], s0, stat[0].rstd, std::true_type());
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float z[8], g[8];
+        values(stage, stat[0], k, z, g);
+        add(k, z, g, s0);
+        if (two) {
+          values(other, stat[NR - 1], k, z, g);
+          add(k, z, g, s1);
+        }
+      }
+      if (NR == 2) row_sum4<TPR>(s0, s1, red, turn);
+      else row_sum2<TPR>(s0.x, s0.y, red, turn);
+      // (read from the ring again rather than kept: fewer registers, more warps)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float z[8], g[8];
+        values(stage, stat[0], k, z, g);
+        finish(stage, k, row, z, g, s0, stat[0].rstd, std::false_type());
+        if (two) {
+          values(other, stat[NR - 1], k, z, g);
+          finish(other, k, row + step, z, g, s1, stat[NR - 1].rstd, std::false_type());
+        }
       }
     }
   }
@@ -292,9 +324,8 @@ __global__ void __launch_bounds__(1024)
       float h;
       if (p.h8.q) {
         float v[8];
-        unpack_fp8(make_uint2(p.h8.q[row * p.h8.ld + e], 0u), p.h8.e5m2,
-                   scale_value(p.h8.s[row * p.h8.ld_s + e / kGroup]), v);
-        h = v[0];
+        unpack_fp8(make_uint2(p.h8.q[row * p.h8.ld + e], 0u), p.h8.e5m2, v);
+        h = v[0] * scale_value(p.h8.s[row * p.h8.ld_s + e / kGroup]);
       } else {
         h = to_f32((static_cast<const T*>(p.h_in) + row * p.ld_h)[e]);
       }
@@ -318,6 +349,18 @@ __global__ void __launch_bounds__(1024)
       dr[e] = from_f32<T>(fmaf(g - s1 - z * s2, r, er ? to_f32(er[e]) : 0.f));
     }
   }
+}
+
+// TPR and K are the smallest that hold the row; f is called with the kernel's shape.
+template <typename T, typename F>
+cudaError_t by_row_shape(int64_t cols, F&& f) {
+  if (cols <= 256) return f.template operator()<T, 32, 1>();
+  if (cols <= 512) return f.template operator()<T, 32, 2>();
+  if (cols <= 768) return f.template operator()<T, 32, 3>();
+  if (cols <= kWarpRowMax) return f.template operator()<T, 32, 4>();
+  if (cols <= 2048) return f.template operator()<T, 128, 2>();
+  if (cols <= 4096) return f.template operator()<T, 256, 2>();
+  return f.template operator()<T, 512, 2>();
 }
 
 template <bool H8, bool LAYER>
