@@ -805,6 +805,7 @@ def fp8_empty(rows: int, cols: int, groups: int, dtype=None, device="cuda") -> F
 
 
 _FP8_CODES, _SCALE_TYPES = {}, ()
+_GROUP_KINDS = (GROUPS_ROW, GROUPS_COL, GROUPS_TILE)
 
 
 def _learn_fp8() -> None:
@@ -816,23 +817,43 @@ def _learn_fp8() -> None:
 
 
 def _fp8(m, shape, dev: int, name: str, groups: Optional[int] = None) -> Optional[Fp8Struct]:
-    """The C description of an 8-bit matrix (None for None)."""
+    """The C description of an 8-bit matrix (None for None).  What a well-formed one needs is looked at
+    in one go; anything else is sorted out by ``_fp8_checked``."""
     if m is None:
         return None
+    data, scales, kind = m
+    code = _FP8_CODES.get(data.dtype)
+    rows, cols = shape
+    ld, step = data.stride()
+    ld_s, step_s = scales.stride()
+    s_shape = (rows if kind == 0 else (rows + 127) >> 7, cols if kind == 1 else (cols + 127) >> 7)
+    if (code is None or step != 1 or step_s != 1 or (groups is not None and kind != groups)
+            or data.shape != shape or scales.shape != s_shape or data.get_device() != dev
+            or scales.get_device() != dev or scales.dtype not in _SCALE_TYPES
+            or kind not in _GROUP_KINDS):
+        return _fp8_checked(m, shape, dev, name, groups)
+    if rows < 2:                           # a single row has no pitch
+        ld = (max(ld, cols) + 15) & -16
+    if s_shape[0] < 2:
+        ld_s = max(ld_s, s_shape[1])
+    return Fp8Struct(data.data_ptr(), ld, scales.data_ptr(), ld_s, code, kind)
+
+
+def _fp8_checked(m, shape, dev: int, name: str, groups: Optional[int]) -> Fp8Struct:
     data, scales, kind = m
     if not _FP8_CODES:
         _learn_fp8()
     code = _FP8_CODES.get(data.dtype)
     if code is None:
         raise TypeError(f"{name}: expected float8_e4m3fn or float8_e5m2, got {data.dtype}")
-    if kind not in (GROUPS_ROW, GROUPS_COL, GROUPS_TILE):
+    if kind not in _GROUP_KINDS:
         raise ValueError(f"{name}: unknown groups {kind}")
     if groups is not None and kind != groups:
         raise ValueError(f"{name}: expected groups {groups}, got {kind}")
     ld = _matrix(data, shape, data.dtype, dev, name)
     rows, cols = shape
     if rows <= 1:
-        ld = -(-ld // 16) * 16             # a single row has no pitch
+        ld = (ld + 15) & -16
     if scales.dtype not in _SCALE_TYPES:
         raise TypeError(f"{name}: expected float8_e8m0fnu or uint8 scales, got {scales.dtype}")
     ld_s = _matrix(scales, fp8_scale_shape(rows, cols, kind), scales.dtype, dev, name + " scales")
