@@ -972,9 +972,10 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
     p.swap = m <= n;
     p.nt = few <= 16 ? 16 : few <= 32 ? 32 : 64;
     const int64_t tiles = (wide + 127) / 128;
-    // slices of k until the device is covered twice, of two blocks at least
-    int s = 1;
-    while (s < 8 && tiles * s * 2 <= 4 * kPairs && nkb >= 4 * s) s *= 2;
+    // as many slices of k, of two blocks at least, as run at a time: an SM draws some 43 GB/s from
+    // memory, whatever it has under way (one, two or three CTAs with 3 to 9 stages each took the same
+    // time a block), so what counts is that all of them draw
+    const int s = (int)std::max<int64_t>(1, std::min({4 * kPairs / tiles, (int64_t)8, (int64_t)nkb / 2}));
     p.splits = s;
     p.kb_split = (nkb + s - 1) / s;
     return p;
