@@ -103,6 +103,7 @@ struct ScaleArgs {
   int32_t shift;              // 7: a scale serves 128 rows
   int32_t form;               // kRowWords: four blocks' bytes lie in an aligned word;
                               // kColWords: four rows' do
+  int32_t pairs;              // kRowWords: eight blocks' bytes in two aligned words
 };
 
 // The scale words of 128 rows from row0 (a multiple of 128) and blocks kb .. kb + 3: word j of lane l
@@ -114,11 +115,12 @@ struct ScaleArgs {
 struct ScaleAt {
   int64_t row0;
   int kb, live;               // live: blocks, 1 to 4
-  int how;                    // 0 words of four rows, 1 one row group, 2 words of four blocks, 3 bytes
+  int how;                    // 0 words of four rows, 1 one row group's bytes, 2 words of four blocks,
+                              // 3 bytes, 4 one row group's word
   __device__ __forceinline__ ScaleAt(const ScaleArgs& p, int64_t row0_, int64_t rows, int kb_, int nkb)
       : row0(row0_), kb(kb_), live(min(4, nkb - kb_)) {
     how = p.form == kColWords && live == 4 && row0 + 128 <= rows ? 0
-          : p.shift                                              ? 1
+          : p.shift ? (p.form == kRowWords && (kb & 3) == 0 && live == 4 ? 4 : 1)
           : p.form == kRowWords && (kb & 3) == 0 && live == 4    ? 2
                                                                  : 3;
   }
@@ -133,20 +135,32 @@ __device__ __forceinline__ void issue_scales(const ScaleArgs& p, const ScaleAt& 
     for (int j = 0; j < 4; ++j)
       raw.r[j] = *reinterpret_cast<const uint32_t*>(p.s + at.row0 + 4 * lane +
                                                     (int64_t)(at.kb + j) * p.sk);
-  } else if (at.how == 1) {                              // the same for all 128 rows
+  } else if (at.how == 1 || at.how == 4) {               // the same for all 128 rows
     const uint8_t* s = p.s + (min(at.row0, rows - 1) >> 7) * p.sr + (int64_t)at.kb * p.sk;
+    if (at.how == 4) {
+      raw.r[0] = *reinterpret_cast<const uint32_t*>(s);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) raw.r[j] = s[min(j, at.live - 1) * p.sk];
+      for (int j = 0; j < 4; ++j) {
+        raw.r[j] = *s;
+        s += j + 1 < at.live ? p.sk : 0;
+      }
+    }
   } else {
+    const uint8_t* base = p.s + (int64_t)at.kb * p.sk;
+    const int64_t d1 = at.live > 1 ? p.sk : 0, d2 = at.live > 2 ? d1 + p.sk : d1,
+                  d3 = at.live > 3 ? d2 + p.sk : d2;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t r = at.row0 + (p.form == kColWords ? 4 * lane + j : 32 * j + lane);
-      const uint8_t* s = p.s + min(r, rows - 1) * p.sr + (int64_t)at.kb * p.sk;
+      const uint8_t* s = base + min(r, rows - 1) * p.sr;
       if (at.how == 2) {
         raw.r[j] = *reinterpret_cast<const uint32_t*>(s);
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) raw.r[4 * j + i] = s[min(i, at.live - 1) * p.sk];
+        raw.r[4 * j] = s[0];
+        raw.r[4 * j + 1] = s[d1];
+        raw.r[4 * j + 2] = s[d2];
+        raw.r[4 * j + 3] = s[d3];
       }
     }
   }
@@ -167,6 +181,9 @@ __device__ __forceinline__ void finish_scales(const ScaleAt& at, const ScaleRaw&
   } else if (at.how == 2) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = r[j];
+  } else if (at.how == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = r[0];
   } else if (at.how == 1) {
     const uint32_t w = ((r[0] | (r[1] << 8) | (r[2] << 16) | (r[3] << 24)) & keep) | past;
 #pragma unroll
@@ -177,6 +194,20 @@ __device__ __forceinline__ void finish_scales(const ScaleAt& at, const ScaleRaw&
       v[j] = ((r[4 * j] | (r[4 * j + 1] << 8) | (r[4 * j + 2] << 16) | (r[4 * j + 3] << 24)) & keep) |
              past;
   }
+}
+// Both groups of a stage's eight blocks in one load a row, where the words allow it.
+__device__ __forceinline__ bool issue_scale_pairs(const ScaleArgs& p, int64_t row0, int64_t rows, int kb,
+                                                  int nkb, int lane, ScaleRaw& lo, ScaleRaw& hi) {
+  if (!p.pairs || (kb & 7) != 0 || kb + 8 > nkb) return false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (p.shift && j > 0) break;
+    const int64_t r = min(row0 + 32 * j + lane, rows - 1) >> p.shift;
+    const uint2 w = *reinterpret_cast<const uint2*>(p.s + r * p.sr + kb);
+    lo.r[j] = w.x;
+    hi.r[j] = w.y;
+  }
+  return true;
 }
 // ... into their 512 bytes of shared memory: row r at 16 (r % 32) + 4 (r / 32).  Rows past the end
 // have another row's scales beside zero values; only a NaN among those must not reach them.
@@ -571,8 +602,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               f(P.sb, ScaleAt(P.sb, b0 + 128, P.n, k0, P.nkb), P.n, h, 2);
             }
           };
+          const bool pa = issue_scale_pairs(P.sa, a0, P.m, kb, P.nkb, lane, raw[0][0], raw[1][0]);
+          const bool pb = issue_scale_pairs(P.sb, b0, P.n, kb, P.nkb, lane, raw[0][1], raw[1][1]) &&
+                          issue_scale_pairs(P.sb, b0 + 128, P.n, kb, P.nkb, lane, raw[0][2], raw[1][2]);
           each([&](const ScaleArgs& p, const ScaleAt& at, int64_t rows, int h, int i) {
-            issue_scales(p, at, rows, lane, raw[h][i]);
+            if (!(i == 0 ? pa : pb)) issue_scales(p, at, rows, lane, raw[h][i]);
           });
           ok = mbar_wait(bar(sf_empty0 + sf), ph, g);
           if (!ok) break;
@@ -1021,6 +1055,7 @@ ScaleArgs scales_of(const mfsdp_fp8_matrix& m, bool along_rows) {
   s.shift = m.groups == MFSDP_GROUPS_TILE ? 7 : 0;
   if (m.ld_scales % 4 == 0 && aligned_to(m.scales, 4))
     s.form = !along_rows ? kRowWords : s.shift ? kBytes : kColWords;
+  s.pairs = s.form == kRowWords && m.ld_scales % 8 == 0 && aligned_to(m.scales, 8);
   return s;
 }
 
