@@ -750,7 +750,7 @@ int mfsdp_dequantize_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_matrix* src
  * A linear layer y = x W^T (W [out x in], TILE) takes x ROW and trans_b = 1 forward, dy ROW and W as
  * it is for dx = dy W, and dy COL and x COL with trans_a = 1 for dW = dy^T x.
  * Products run on the tensor cores (block-scaled) with fp32 accumulation; sums kept in fp32 are added
- * up outside them every 4096 of k (8192 where C has few rows or columns).  k == 0 writes zeros (or leaves C as it is).  m, n or k up to
+ * up outside them every 8192 of k.  k == 0 writes zeros (or leaves C as it is).  m, n or k up to
  * 2^31 - 513.
  * A device wait that runs out sets MFSDP_ETIMEOUT in the status word.
  */

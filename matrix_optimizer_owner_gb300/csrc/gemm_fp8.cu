@@ -262,7 +262,7 @@ static_assert(kPairSmem <= 227 * 1024, "shared memory");
 // The epilogue reads the shared columns of a tile first and says so, and the next tile's products
 // wait for that alone.
 constexpr uint32_t kAcc1 = 224, kSfCol = 480;
-constexpr int kChunk8 = 32;                 // blocks added up in tensor memory (CHUNKED): 4096 of k
+constexpr int kChunk8 = 64;                 // blocks added up in tensor memory (CHUNKED): 8192 of k
 constexpr int kRasterRows = 8;              // tile rows that walk the columns together
 
 struct PairTile {
@@ -311,10 +311,11 @@ __device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c
 
 // 32 columns of a lane's row to C, whatever C's rows, edges and old values are.  Rows without 16-byte alignment go through the warp's staging area (2 KB), a row of the block at
 // a time.
-__device__ __noinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane, int64_t c0, uint32_t stg,
-                                     float (&v)[32]) {
+template <bool BF16>
+__device__ __forceinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane, int64_t c0,
+                                        uint32_t stg, float (&v)[32]) {
   const int64_t r = rw + lane;
-  const bool f32 = !P.c_bf16;
+  constexpr bool f32 = !BF16;
   if (P.accumulate) add_old(P, r, c0, v);
   if (P.vec) {
     if (r >= P.m) return;
@@ -367,51 +368,67 @@ __device__ __noinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane, i
       sts128(stg + stg_off(lane, k), make_uint4(w[0], w[1], w[2], w[3]));
     }
     __syncwarp();
-    const int64_t c = c0 + 16 * h + lane;
-    const bool in = (f32 ? lane < 16 : true) && c < P.n;
-    for (int i = 0; i < 32 && rw + i < P.m; ++i) {
-      if (!in) continue;
-      const int64_t at = (rw + i) * P.ld_c + c;
-      if (f32)
-        static_cast<uint32_t*>(P.c)[at] = lds32(stg + stg_off(i, lane >> 2) + (lane & 3) * 4);
-      else
-        static_cast<uint16_t*>(P.c)[at] = (uint16_t)(
-            lds32(stg + stg_off(i, lane >> 3) + (uint32_t)((lane & 6) * 2)) >> (16 * (lane & 1)));
+    // a row of bf16, or two of fp32, at a time
+    const int col = f32 ? lane & 15 : lane, row0 = f32 ? lane >> 4 : 0, step = f32 ? 2 : 1;
+    const int64_t c = c0 + 16 * h + col;
+    const int64_t at = (rw + row0) * P.ld_c + c, next = step * P.ld_c;
+    const int rows = c < P.n ? (int)min((int64_t)32, P.m - rw) - row0 : 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; i += step) {
+      const int row = i + row0;
+      if (f32) {
+        const uint32_t w = lds32(stg + stg_off(row, col >> 2) + (uint32_t)(col & 3) * 4u);
+        if (i < rows) static_cast<uint32_t*>(P.c)[at + (i >> 1) * next] = w;
+      } else {
+        const uint32_t w = lds32(stg + stg_off(row, col >> 3) + (uint32_t)((col & 6) * 2));
+        if (i < rows)
+          static_cast<uint16_t*>(P.c)[at + i * next] = (uint16_t)(w >> (16 * (col & 1)));
+      }
     }
   }
 }
 
-// The same where all 32 columns are there, rows start on 32-byte boundaries and nothing is added: a
-// lane writes its row straight from registers, a whole sector at a time.  (Staged through shared
-// memory, so that a warp's stores covered 64 bytes of a row, a tile's epilogue took twice the time.  It
-// has few instructions on purpose: with every case inlined and unrolled, the warps waited mostly for
-// instructions.)
+// The same where rows start on 32-byte boundaries and nothing is added: a lane writes its row straight
+// from registers, a whole sector at a time.  (Staged through shared memory, so that a warp's stores
+// covered 64 bytes of a row, a tile's epilogue took twice the time.)
+template <bool BF16>
 __device__ __forceinline__ void put_whole(const Gemm8Args& P, int64_t r, int64_t c0,
                                           const float (&v)[32]) {
   if (r >= P.m) return;
-  if (P.c_bf16) {
-    bf16_t* d = static_cast<bf16_t*>(P.c) + r * P.ld_c + c0;
+  constexpr int kWords = BF16 ? 16 : 32;
+  uint32_t w[kWords];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+  for (int k = 0; k < kWords; ++k)
+    w[k] = BF16 ? pack_bf16x2(v[BF16 ? 2 * k : k], v[BF16 ? 2 * k + 1 : k]) : __float_as_uint(v[k]);
+  void* d = BF16 ? static_cast<void*>(static_cast<bf16_t*>(P.c) + r * P.ld_c + c0)
+                 : static_cast<void*>(static_cast<float*>(P.c) + r * P.ld_c + c0);
+  if (c0 + 32 <= P.n) {
+#pragma unroll
+    for (int h = 0; h < kWords / 8; ++h) {
       uint32_t o[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(v[16 * h + 2 * k], v[16 * h + 2 * k + 1]);
-      st256(d + 16 * h, o);
+      for (int k = 0; k < 8; ++k) o[k] = w[8 * h + k];
+      st256(static_cast<uint32_t*>(d) + 8 * h, o);
     }
   } else {
-    float* d = static_cast<float*>(P.c) + r * P.ld_c + c0;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t o[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[8 * h + k]);
-      st256(d + 8 * h, o);
+    for (int k = 0; k < 32; ++k) {
+      if (c0 + k >= P.n) break;
+      if (BF16)
+        static_cast<uint16_t*>(d)[k] = (uint16_t)(w[BF16 ? k >> 1 : 0] >> (16 * (k & 1)));
+      else
+        static_cast<uint32_t*>(d)[k] = w[BF16 ? 0 : k];
     }
   }
 }
 
 // CHUNKED: a tile's contraction is cut into chunks that are added up in registers.
-template <bool CHUNKED>
+// SPLIT: few tiles with a long contraction.  Two pairs (a cluster of four CTAs) take half of k each of one
+// tile; then each takes half of the columns and gets the other's sums of them through its shared memory.
+// PLAIN: C's rows start on 32-byte boundaries and it is not added to.  The other forms of the epilogue are
+// kernels of their own: beside each other in one kernel they cost its common path up to a sixth (the
+// warps wait for instructions).
+template <bool CHUNKED, bool SPLIT, bool BF16, bool PLAIN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ Gemm8Args P) {
   constexpr int S = kStages8, F = kSfStages;
@@ -431,7 +448,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   auto bar = [&](int i) { return smem_u32(bars + i); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t cta = cluster_rank(), rank = cta & 1u;  // within the pair
+  const uint32_t lead = cta & ~1u;                       // the pair's leader
+  const uint16_t both = (uint16_t)(0x3u << lead);
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -468,12 +487,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint32_t peer_base;
   asm volatile("ld.shared::cluster.u32 %0, [%1];"
                : "=r"(peer_base)
-               : "r"(map_rank(smem_u32(tmem_slot), rank ^ 1u))
+               : "r"(map_rank(smem_u32(tmem_slot), cta ^ 1u))
                : "memory");
   const bool usable = peer_base == tmem_base;
   if (!usable && threadIdx.x == 0) atomicOr(P.status, kStatusTmemMismatch);
   const Guard g{abort_flag, P.wait_limit_ns, P.status};
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int pair = SPLIT ? blockIdx.x >> 2 : blockIdx.x >> 1, npairs = SPLIT ? gridDim.x >> 2 : gridDim.x >> 1;
+  // this pair's blocks of k
+  const int kb0 = SPLIT && lead ? P.kb_split : 0, nkb = SPLIT ? (lead ? P.nkb - kb0 : P.kb_split) : P.nkb;
   const int tiles = P.tiles_m * P.tiles_n;
 
   if (!usable) {
@@ -487,11 +508,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int w = pair; w < tiles && ok; w += npairs) {
         const PairTile t = pair_tile(P, w);
         const int a0 = t.tm * 256 + 128 * (int)rank, b0 = t.tn * 256 + 128 * (int)rank;
-        for (int kb = 0; kb < P.nkb; ++kb) {
+        for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait(bar(empty0 + stage), ph, g)) { ok = false; break; }
-          const uint32_t fb_local = bar(full0 + stage), fb = map_rank(fb_local, 0);
+          const uint32_t fb_local = bar(full0 + stage), fb = map_rank(fb_local, lead);
           const uint32_t dst = sbase + (uint32_t)stage * kStageBytes8;
-          const int k0 = kb * kB8;
+          const int k0 = (kb0 + kb) * kB8;
           expect_tx_p(leader, fb_local, 2u * kStageBytes8);
           tma_load_pair_p(true, dst, &P.a, P.a_mn ? a0 : k0, P.a_mn ? k0 : a0, fb);
           tma_load_pair_p(true, dst + kBox8, &P.b, P.b_mn ? b0 : k0, P.b_mn ? k0 : b0, fb);
@@ -518,7 +539,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int w = pair; w < tiles && ok; w += npairs) {
         const PairTile t = pair_tile(P, w);
         int in_chunk = 0;                                 // blocks in the accumulator
-        for (int kb = 0; kb < P.nkb && ok; kb += 4) {
+        for (int kb = 0; kb < nkb && ok; kb += 4) {
           if (in_chunk == 0) {
             // the accumulator, and the columns that it shares with the one before
             if (!mbar_wait_cl(bar(tempty0 + acc), acc_phase ^ 1u, g) ||
@@ -541,12 +562,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           copy_scales<2>(sfa, scale_desc(src));
           copy_scales<2>(sfb, scale_desc(src + 512u));
           copy_scales<2>(sfb + 4u, scale_desc(src + 1024u));
-          if ((kb & 4) || kb + 4 >= P.nkb) {               // the stage's last group
-            tc_commit_pair(bar(sf_empty0 + sf), 0x3);
+          if ((kb & 4) || kb + 4 >= nkb) {               // the stage's last group
+            tc_commit_pair(bar(sf_empty0 + sf), both);
             if (++sf == F) { sf = 0; sf_phase ^= 1u; }
           }
           const uint32_t d = tmem_base + (acc ? kAcc1 : 0u);
-          const int live = min(4, P.nkb - kb);
+          const int live = min(4, nkb - kb);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (i < live && ok) {
@@ -558,25 +579,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                   mma8<2>(d, da.at(at, j), db.at(at, j), idesc, sfa, sfb, (in_chunk | i | j) != 0);
-                tc_commit_pair(bar(empty0 + stage), 0x3);
+                tc_commit_pair(bar(empty0 + stage), both);
                 if (++stage == S) { stage = 0; phase ^= 1u; }
               }
             }
           }
           if (!ok) break;
-          tc_commit_pair(bar(sf_free0 + buf), 0x1);
+          tc_commit_pair(bar(sf_free0 + buf), (uint16_t)(1u << lead));
           buf ^= 1;
           if (buf == 0) buf_phase ^= 1u;
           in_chunk += 4;
-          if (kb + 4 >= P.nkb || (CHUNKED && in_chunk == kChunk8)) {
-            tc_commit_pair(bar(tfull0 + acc), 0x3);
+          if (kb + 4 >= nkb || (CHUNKED && in_chunk == kChunk8)) {
+            tc_commit_pair(bar(tfull0 + acc), both);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
             in_chunk = 0;
           }
         }
       }
-      tc_commit_pair(bar(drain), 0x1);
+      tc_commit_pair(bar(drain), (uint16_t)(1u << lead));
       mbar_wait(bar(drain), 0u, g, false);
     }
   } else if (warp < kEpi0) {
@@ -589,22 +610,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int w = pair; w < tiles && ok; w += npairs) {
       const PairTile t = pair_tile(P, w);
       const int64_t a0 = (int64_t)t.tm * 256 + 128 * rank, b0 = (int64_t)t.tn * 256;
-      for (int kb = 0; kb < P.nkb; kb += 8) {
+      for (int kb = 0; kb < nkb; kb += 8) {
         if (turn == warp - 2) {
           ScaleRaw raw[2][3];
           auto each = [&](auto&& f) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (kb + 4 * h >= P.nkb) break;
-              const int k0 = kb + 4 * h;
+              if (kb + 4 * h >= nkb) break;
+              const int k0 = kb0 + kb + 4 * h;
               f(P.sa, ScaleAt(P.sa, a0, P.m, k0, P.nkb), P.m, h, 0);
               f(P.sb, ScaleAt(P.sb, b0, P.n, k0, P.nkb), P.n, h, 1);
               f(P.sb, ScaleAt(P.sb, b0 + 128, P.n, k0, P.nkb), P.n, h, 2);
             }
           };
-          const bool pa = issue_scale_pairs(P.sa, a0, P.m, kb, P.nkb, lane, raw[0][0], raw[1][0]);
-          const bool pb = issue_scale_pairs(P.sb, b0, P.n, kb, P.nkb, lane, raw[0][1], raw[1][1]) &&
-                          issue_scale_pairs(P.sb, b0 + 128, P.n, kb, P.nkb, lane, raw[0][2], raw[1][2]);
+          const bool pa = issue_scale_pairs(P.sa, a0, P.m, kb0 + kb, P.nkb, lane, raw[0][0], raw[1][0]);
+          const bool pb = issue_scale_pairs(P.sb, b0, P.n, kb0 + kb, P.nkb, lane, raw[0][1], raw[1][1]) &&
+                          issue_scale_pairs(P.sb, b0 + 128, P.n, kb0 + kb, P.nkb, lane, raw[0][2], raw[1][2]);
           each([&](const ScaleArgs& p, const ScaleAt& at, int64_t rows, int h, int i) {
             if (!(i == 0 ? pa : pb)) issue_scales(p, at, rows, lane, raw[h][i]);
           });
@@ -618,7 +639,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           });
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_leader(map_rank(bar(sf_full0 + sf), 0));
+          if (lane == 0) mbar_arrive_leader(map_rank(bar(sf_full0 + sf), lead));
         }
         turn ^= 1;
         if (++sf == F) { sf = 0; ph ^= 1u; }
@@ -637,17 +658,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t rw = (int64_t)t.tm * 256 + 128 * rank + quarter * 32;
       const int64_t cb = (int64_t)t.tn * 256 + half * 128;
       const int nq = rw < P.m && cb < P.n ? (int)min((int64_t)4, (P.n - cb + 31) / 32) : 0;
-      const bool plain = P.vec == 2 && !P.accumulate;
       auto put = [&](int q, float (&v)[32]) {
-        const int64_t c0 = cb + 32 * q;
-        if (plain && c0 + 32 <= P.n) {
-          put_whole(P, rw + lane, c0, v);
-        } else {
-          float o[32];                                    // (the call's copy: v stays in registers)
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = v[k];
-          put_row(P, rw, lane, c0, stg, o);
-        }
+        if (PLAIN) put_whole<BF16>(P, rw + lane, cb + 32 * q, v);
+        else put_row<BF16>(P, rw, lane, cb + 32 * q, stg, v);
       };
       // the shared columns: this warp's chunk `sh` of this accumulator, if it holds them
       auto shared_chunk = [&]() { return acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1); };
@@ -658,7 +671,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       auto release = [&](int which) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_rank(bar(which + acc), 0));
+        if (lane == 0) mbar_arrive_cluster(map_rank(bar(which + acc), lead));
       };
       if (CHUNKED) {
         float sum[4][32];
@@ -666,7 +679,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int k = 0; k < 32; ++k) sum[q][k] = 0.f;
-        for (int left = P.nkb; left > 0; left -= kChunk8) {
+        for (int left = nkb; left > 0; left -= kChunk8) {
           if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) { ok = false; break; }
           tc_fence_after();
           const int sh = shared_chunk();
@@ -705,33 +718,86 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (q < nq) put(q, sum[q]);
+      } else if (SPLIT) {
+        mbar_wait(bar(tfull0), 0u, g);                    // (the sums are read below)
+        tc_fence_after();
       } else {
         if (!mbar_wait(bar(tfull0 + acc), acc_phase, g)) break;
         tc_fence_after();
         const int sh = shared_chunk(), first = sh == 3 ? 3 : 0;   // the shared columns first
         const uint32_t at = base();
-        uint32_t buf[2][32];
-        tc_ld32_issue(at + (uint32_t)(32 * first), buf[0]);
 #pragma unroll 1
-        for (int i = 0; i < 4; i += 2) {
+        for (int i = 0; i < 4; ++i) {
+          const int q = (i + first) & 3;
+          uint32_t a[32];
+          tc_ld32_issue(at + (uint32_t)(32 * q), a);
+          tc_ld_wait(a);
+          if (q == sh) release(early0);
+          if (i == 3) release(tempty0);                   // the last read: the stores can follow it
+          float v[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = (i + h + first) & 3;
-            uint32_t (&a)[32] = buf[h];
-            tc_ld_wait(a);
-            if (q == sh) release(early0);
-            if (i + h < 3)
-              tc_ld32_issue(at + (uint32_t)(32 * ((q + 1) & 3)), buf[h ^ 1]);
-            else
-              release(tempty0);                           // the last read: the stores can follow it
-            float v[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(a[k]);
-            if (q < nq) put(q, v);
-          }
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(a[k]);
+          if (q < nq) put(q, v);
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  }
+
+  if (SPLIT) {
+    // Both pairs' products are done, and with them every copy into the stages, which take the other
+    // pair's sums: a warp's 32 columns as eight rows of 512 bytes.  Half 0 of the columns is the first
+    // pair's, half 1 the second's.
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after();
+    const int quarter = warp & 3, first = ((warp - kEpi0) >> 2) * 2;   // two chunks of a half each
+    const int own = (int)(lead >> 1);
+    const PairTile t = pair_tile(P, pair);
+    const int64_t rw = (int64_t)t.tm * 256 + 128 * rank + quarter * 32;
+    const int64_t cb = (int64_t)t.tn * 256 + own * 128;
+    const uint32_t at = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    auto place = [&](int q, int i) {
+      return (uint32_t)(((quarter * 4 + q) * 8 + i) * 512 + lane * 16);
+    };
+    if (usable && warp >= kEpi0) {
+#pragma unroll 1
+      for (int q = first; q < first + 2; ++q) {
+        uint32_t a[32];
+        tc_ld32_issue(at + (uint32_t)((own ^ 1) * 128 + 32 * q), a);
+        tc_ld_wait(a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           map_rank(sbase + place(q, i), cta ^ 2u)),
+                       "r"(a[4 * i]), "r"(a[4 * i + 1]), "r"(a[4 * i + 2]), "r"(a[4 * i + 3])
+                       : "memory");
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    if (usable && warp >= kEpi0 && rw < P.m) {
+      const uint32_t stg = sbase + kStg8 + (uint32_t)(warp - kEpi0) * 2048u;
+#pragma unroll 1
+      for (int q = first; q < first + 2; ++q) {
+        const int64_t c0 = cb + 32 * q;
+        if (c0 >= P.n) break;                             // warp-uniform
+        uint32_t a[32];
+        tc_ld32_issue(at + (uint32_t)(own * 128 + 32 * q), a);
+        tc_ld_wait(a);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 o = lds128(sbase + place(q, i));
+          v[4 * i] = __uint_as_float(a[4 * i]) + __uint_as_float(o.x);   // (a sum of two: any order)
+          v[4 * i + 1] = __uint_as_float(a[4 * i + 1]) + __uint_as_float(o.y);
+          v[4 * i + 2] = __uint_as_float(a[4 * i + 2]) + __uint_as_float(o.z);
+          v[4 * i + 3] = __uint_as_float(a[4 * i + 3]) + __uint_as_float(o.w);
+        }
+        if (PLAIN) put_whole<BF16>(P, rw + lane, c0, v);
+        else put_row<BF16>(P, rw, lane, c0, stg, v);
       }
     }
   }
@@ -992,6 +1058,7 @@ constexpr int kPairs = 76;                  // CTA pairs of the device: what the
 
 struct Gemm8Plan {
   bool narrow = false, swap = false;        // swap: the narrow side is A's
+  bool halves = false;                      // two pairs a tile
   int nt = 0;
   int splits = 1, kb_split = 0;
 };
@@ -1029,8 +1096,15 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
   }
   // 256 x 256 tiles on CTA pairs
   const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  const double pair = 5. + (double)((tiles + kPairs - 1) / kPairs) * (nkb * 0.34 + 2.);
+  double pair = 5. + (double)((tiles + kPairs - 1) / kPairs) * (nkb * 0.34 + 2.);
+  if (2 * tiles <= kPairs && nkb >= 16) {
+    p.kb_split = ((nkb + 1) / 2 + 7) / 8 * 8;
+    const double t = 9. + p.kb_split * 0.34;
+    p.halves = t < pair;
+    pair = std::min(pair, t);
+  }
   if (narrow < pair) {
+    p.halves = false;
     p.narrow = p.swap = true;
     p.nt = 128;
     p.splits = ns;
@@ -1086,6 +1160,16 @@ cudaError_t launch_clusters(void (*kernel)(const Gemm8Args), unsigned grid, unsi
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <bool CHUNKED, bool SPLIT, bool PLAIN>
+cudaError_t launch_pair(const Gemm8Args& a, int grid, cudaStream_t st) {
+  static std::atomic<bool> done[2][64];
+  const auto kernel = a.c_bf16 ? gemm_fp8_pair_kernel<CHUNKED, SPLIT, true, PLAIN>
+                               : gemm_fp8_pair_kernel<CHUNKED, SPLIT, false, PLAIN>;
+  const cudaError_t e = allow_smem(done[a.c_bf16 ? 1 : 0], kernel, kPairSmem);
+  return e != cudaSuccess ? e
+                          : launch_clusters(kernel, grid, SPLIT ? 4 : 2, kPairThreads, kPairSmem, st, a);
 }
 
 template <int NT>
@@ -1180,19 +1264,19 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   g.tiles_m = (g.m + 255) / 256;
   g.tiles_n = (g.n + 255) / 256;
   // The tensor cores cut each of their additions towards zero, which grows with the contraction: sums
-  // that are kept in fp32 are added up in registers every 4096 of k (2e-7 of a Gaussian product's
+  // that are kept in fp32 are added up in registers every 8192 of k (3e-7 of a Gaussian product's
   // entries, 5e-7 at 14336), others where the cuts would come near half a bf16 step.
-  const bool chunked = g.nkb > (g.c_bf16 ? 512 : kChunk8);
-  const int pairs = std::max(1, std::min(sms / 2, g.tiles_m * g.tiles_n));
-  static std::atomic<bool> done[2][64];
-  if (chunked) {
-    e = allow_smem(done[1], gemm_fp8_pair_kernel<true>, kPairSmem);
-    if (e == cudaSuccess)
-      e = launch_clusters(gemm_fp8_pair_kernel<true>, 2 * pairs, 2, kPairThreads, kPairSmem, st, g);
-  } else {
-    e = allow_smem(done[0], gemm_fp8_pair_kernel<false>, kPairSmem);
-    if (e == cudaSuccess)
-      e = launch_clusters(gemm_fp8_pair_kernel<false>, 2 * pairs, 2, kPairThreads, kPairSmem, st, g);
-  }
+  const int most = g.c_bf16 ? 512 : kChunk8;
+  const int tiles = g.tiles_m * g.tiles_n;
+  const int pairs = std::max(1, std::min(sms / 2, tiles));
+  const bool plain = g.vec == 2 && !g.accumulate;
+  if (plan.halves && g.kb_split <= most)
+    e = plain ? launch_pair<false, true, true>(g, 4 * tiles, st)
+              : launch_pair<false, true, false>(g, 4 * tiles, st);
+  else if (g.nkb > most)
+    e = launch_pair<true, false, false>(g, 2 * pairs, st);
+  else
+    e = plain ? launch_pair<false, false, true>(g, 2 * pairs, st)
+              : launch_pair<false, false, false>(g, 2 * pairs, st);
   return e == cudaSuccess ? MFSDP_OK : MFSDP_ECUDA;
 }

@@ -184,6 +184,14 @@ def _product(m, n, k, trans_a, trans_b, dtype, kinds=("e4m3", "e4m3"), groups=No
     return a, b, c
 
 
+@pytest.mark.parametrize("m,n,k", [(1400, 1500, 10253), (1280, 1030, 9000), (700, 2500, 12288)])
+def test_gemm_few_tiles_long_contraction(m, n, k):
+    """Two halves of the contraction at a time, joined at the end."""
+    _product(m, n, k, True, False, "f32")
+    _product(m, n, k, False, True, "bf16", pitch=1)
+    _product(m, n, k, True, False, "bf16", accumulate=True, kinds=("e5m2", "e4m3"))
+
+
 ORIENT = [(False, True), (False, False), (True, False), (True, True)]
 
 
