@@ -1063,12 +1063,18 @@ struct Gemm8Plan {
   int splits = 1, kb_split = 0;
 };
 
+// The tensor cores cut each of their additions towards zero, which grows with the contraction: sums that
+// are kept in fp32 leave tensor memory every 8192 of k (3e-7 of a Gaussian product's entries, 5e-7 at
+// 14336), others where the cuts would come near half a bf16 step.
+int most_blocks(bool c_bf16) { return c_bf16 ? 512 : kChunk8; }
+
 // What a call is split into, from its sizes alone.  Times in us, as measured.
-Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
+Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16) {
   Gemm8Plan p;
   const int nkb = (int)((k + kB8 - 1) / kB8);
   const int64_t few = std::min(m, n), wide = std::max(m, n);
-  if (few <= 64) {
+  const int least = (nkb + most_blocks(c_bf16) - 1) / most_blocks(c_bf16);   // slices
+  if (few <= 64 && least <= 8) {
     p.narrow = true;
     p.swap = m <= n;
     p.nt = few <= 16 ? 16 : few <= 32 ? 32 : 64;
@@ -1076,20 +1082,21 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
     // as many slices of k, of two blocks at least, as run at a time: an SM draws some 43 GB/s from
     // memory, whatever it has under way (one, two or three CTAs with 3 to 9 stages each took the same
     // time a block), so what counts is that all of them draw
-    const int s = (int)std::max<int64_t>(1, std::min({4 * kPairs / tiles, (int64_t)8, (int64_t)nkb / 2}));
+    const int s =
+        (int)std::max<int64_t>(std::max(1, least), std::min({4 * kPairs / tiles, (int64_t)8, (int64_t)nkb / 2}));
     p.splits = s;
     p.kb_split = (nkb + s - 1) / s;
     return p;
   }
   // 128 x 128 tiles, C's rows the wide side: rounds of two CTAs an SM, up to eight slices of k
   const int64_t small = ((m + 127) / 128) * ((n + 127) / 128);
-  int ns = 1;
+  int ns = 0;
   double narrow = 0.;
-  for (int s = 1; s <= 8 && s <= std::max(1, nkb); ++s) {
+  for (int s = std::max(1, least); s <= 8 && s <= std::max(1, nkb); ++s) {
     const int per = (nkb + s - 1) / s;
     const int64_t rounds = (small * s + 4 * kPairs - 1) / (4 * kPairs);
     const double t = 3. + (double)rounds * (per * 0.55 + 2.5) + 0.1 * s;
-    if (s == 1 || t < narrow * 0.98) {
+    if (ns == 0 || t < narrow * 0.98) {
       narrow = t;
       ns = s;
     }
@@ -1103,7 +1110,7 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k) {
     p.halves = t < pair;
     pair = std::min(pair, t);
   }
-  if (narrow < pair) {
+  if (ns && narrow < pair) {
     p.halves = false;
     p.narrow = p.swap = true;
     p.nt = 128;
@@ -1203,7 +1210,25 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   if (m == 0 || n == 0) return MFSDP_OK;
   if (!c || ld_c < n) return MFSDP_EINVAL;
   if (!aligned_to(c, dtype_bytes(c_dtype))) return MFSDP_EALIGN;
-  const Gemm8Plan plan = plan_gemm(m, n, k);
+  const bool c_bf16 = c_dtype == MFSDP_DTYPE_BF16;
+  // More of k than eight slices take at fp32's chunks: one such piece after the other, added to C.
+  constexpr int64_t piece = 8ll * kChunk8 * kB8;
+  if (!c_bf16 && k > piece && plan_gemm(m, n, piece, false).narrow) {
+    for (int64_t k0 = 0; k0 < k; k0 += piece) {
+      mfsdp_fp8_matrix pa = *a, pb = *b;
+      auto shift = [&](mfsdp_fp8_matrix& x, bool down) {  // down: the contraction runs down the rows
+        x.data = static_cast<uint8_t*>(x.data) + k0 * (down ? x.ld : 1);
+        x.scales = static_cast<uint8_t*>(x.scales) + k0 / kB8 * (down ? x.ld_scales : 1);
+      };
+      shift(pa, trans_a != 0);
+      shift(pb, trans_b == 0);
+      chk = mfsdp_gemm_fp8(m, n, std::min(piece, k - k0), &pa, trans_a, &pb, trans_b,
+                           accumulate || k0 > 0, c_dtype, c, ld_c, stream);
+      if (chk != MFSDP_OK) return chk;
+    }
+    return MFSDP_OK;
+  }
+  const Gemm8Plan plan = plan_gemm(m, n, k, c_bf16);
   if (k == 0 && accumulate) return MFSDP_OK;
   int sms = 0;
   const int dst = device_sms(&sms);
@@ -1214,7 +1239,7 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   const int vec = !vector_rows(c, ld_c, c_dtype) ? 0
                   : aligned_to(c, 32) && (ld_c * (int64_t)dtype_bytes(c_dtype)) % 32 == 0 ? 2 : 1;
   if (k == 0) {
-    const ZeroArgs8 z{c, m, n, ld_c, c_dtype == MFSDP_DTYPE_BF16};
+    const ZeroArgs8 z{c, m, n, ld_c, c_bf16};
     const dim3 grid((unsigned)std::min<int64_t>((m * n + 255) / 256, sms * 16ll));
     return launch_pdl(gemm_fp8_zero_kernel, grid, dim3(256), 0, st, z) == cudaSuccess ? MFSDP_OK
                                                                                       : MFSDP_ECUDA;
@@ -1243,7 +1268,7 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   g.kb_split = plan.kb_split;
   g.c = c;
   g.ld_c = ld_c;
-  g.c_bf16 = c_dtype == MFSDP_DTYPE_BF16;
+  g.c_bf16 = c_bf16;
   g.accumulate = accumulate != 0;
   g.vec = vec;
   g.wait_limit_ns = wait_limit_ns();
@@ -1263,10 +1288,7 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   }
   g.tiles_m = (g.m + 255) / 256;
   g.tiles_n = (g.n + 255) / 256;
-  // The tensor cores cut each of their additions towards zero, which grows with the contraction: sums
-  // that are kept in fp32 are added up in registers every 8192 of k (3e-7 of a Gaussian product's
-  // entries, 5e-7 at 14336), others where the cuts would come near half a bf16 step.
-  const int most = g.c_bf16 ? 512 : kChunk8;
+  const int most = most_blocks(c_bf16);
   const int tiles = g.tiles_m * g.tiles_n;
   const int pairs = std::max(1, std::min(sms / 2, tiles));
   const bool plain = g.vec == 2 && !g.accumulate;

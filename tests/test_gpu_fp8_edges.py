@@ -1,0 +1,150 @@
+"""The 8-bit operators at the ends of their ranges: contractions that outgrow an accumulator, very many
+rows, gradients written over their inputs, results of several calls in flight.
+
+A product's sums leave the tensor cores every 8192 of k when they are kept in fp32, each chunk within
+(8192 / 32 + 8) 2^-22 of its sum of absolute products, and K / 8192 + 16 additions in registers or to C
+follow, each rounded once: |dc| <= 264 * 2^-22 S + (K / 8192 + 16) 2^-24 (S + |c|).  In bf16 a chunk is
+65536, (65536 / 32 + 8) 2^-22 S, and the result is rounded once (2^-8 of it).
+"""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _positive(rows, cols, gen, extra=0):
+    """Values from 1 to 1.875, all scales 1, as 8-bit data in a wider buffer."""
+    pitch = -(-cols // 16) * 16 + 16 * extra
+    return torch.randint(0x38, 0x40, (rows, pitch), generator=gen, device="cuda",
+                         dtype=torch.uint8).view(torch.float8_e4m3fn)[:, :cols]
+
+
+def _matrix(data, groups):
+    from matrix_optimizer_owner_gb300 import mfsdp
+    scales = torch.full(mfsdp.fp8_scale_shape(*data.shape, groups), 127, dtype=torch.uint8,
+                        device="cuda")
+    return mfsdp.Fp8Matrix(data, scales, groups)
+
+
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("dtype,m,n,k", [("f32", 16, 20, 1 << 20), ("f32", 100, 128, 200001),
+                                         ("f32", 3, 40000, 16384), ("f32", 400, 300, 70000),
+                                         ("bf16", 8, 40, 525300), ("bf16", 70, 90, 140000)])
+def test_gemm_long_contraction(dtype, m, n, k, down):
+    """Sums of one sign, where what an accumulator cuts off adds up."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    a = _positive(*((k, m) if down else (m, k)), gen, extra=1)
+    b = _positive(*((k, n) if down else (n, k)), gen)
+    A, B = (a.T, b) if down else (a, b.T)
+    ref = torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    for k0 in range(0, k, 8192):                    # sums of multiples of 1/64 below 2^53: exact
+        ref += A[:, k0:k0 + 8192].double() @ B[k0:k0 + 8192].double()
+    c = torch.empty(m, n, dtype=TYPES[dtype], device="cuda")
+    g = mfsdp.GROUPS_COL if down else mfsdp.GROUPS_ROW
+    am, bm = _matrix(a, g), _matrix(b, g)
+    chunk = 8192 if dtype == "f32" else 65536
+    rate = (chunk / 32 + 8) * 2.0 ** -22
+    for times in (1, 2):                            # the second one adds to C
+        old = c.double() if times == 2 else torch.zeros_like(ref)
+        mfsdp.mfsdp_gemm_fp8(am, bm, c, trans_a=down, trans_b=not down, accumulate=times == 2)
+        want = ref + old
+        tol = rate * ref + (k / 8192 + 16) * 2.0 ** -24 * (ref + want)
+        if dtype == "bf16":
+            tol = tol + 2.0 ** -8 * want
+        err = (c.double() - want).abs()
+        assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_gemm_very_many_rows():
+    from matrix_optimizer_owner_gb300 import mfsdp
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    a, b = _positive((1 << 24) + 5, 3, gen), _positive(2, 3, gen)
+    c = torch.empty(a.shape[0], 2, device="cuda")
+    mfsdp.mfsdp_gemm_fp8(_matrix(a, 0), _matrix(b, 0), c, trans_b=True)
+    assert torch.equal(c, a.float() @ b.float().T)  # 3 products of multiples of 1/64: exact
+
+
+def test_very_many_rows():
+    """More rows than a grid has blocks for, in one call and in pieces of it."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    rows, cols, at = 65535 * 128 + 1000, 2, 65535 * 128 - 256
+    x = torch.randn(rows, cols, device="cuda").to(torch.bfloat16)
+    row, col = (mfsdp.fp8_empty(rows, cols, groups=g, device="cuda")
+                for g in (mfsdp.GROUPS_ROW, mfsdp.GROUPS_COL))
+    mfsdp.mfsdp_quantize_fp8(x, col, row)           # either order
+    part = [mfsdp.fp8_empty(rows - at, cols, groups=g, device="cuda")
+            for g in (mfsdp.GROUPS_ROW, mfsdp.GROUPS_COL)]
+    mfsdp.mfsdp_quantize_fp8(x[at:], *part)
+    for whole, p, s0 in ((row, part[0], at), (col, part[1], at // 128)):
+        assert torch.equal(whole.data[at:].view(torch.uint8), p.data.view(torch.uint8))
+        assert torch.equal(whole.scales[s0:], p.scales)
+    rows, at = 65535 * 32 + 500, 65535 * 32 - 100
+    gate, up, y = x[:rows], x[rows:2 * rows], torch.empty(rows, cols, dtype=x.dtype, device="cuda")
+    mfsdp.mfsdp_activation_forward(mfsdp.ACT_SWIGLU, gate, up, y)
+    tail = torch.empty_like(y[at:])
+    mfsdp.mfsdp_activation_forward(mfsdp.ACT_SWIGLU, gate[at:], up[at:], tail)
+    assert torch.equal(y[at:], tail)
+    dg, du, dgt, dut = (torch.empty_like(t) for t in (y, y, tail, tail))
+    mfsdp.mfsdp_activation_backward(mfsdp.ACT_SWIGLU, y, gate, up, dg, du)
+    mfsdp.mfsdp_activation_backward(mfsdp.ACT_SWIGLU, tail, gate[at:], up[at:], dgt, dut)
+    assert torch.equal(dg[at:], dgt) and torch.equal(du[at:], dut)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(300, 520), (2000, 4096), (130, 257)])
+def test_activation_gradients_in_place(dtype, rows, cols):
+    """Gradients over dy's, gate's or up's buffer are those of buffers of their own."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    dy, gate, up = (torch.randn(rows, cols, generator=gen, device="cuda").to(TYPES[dtype])
+                    for _ in range(3))
+    want = torch.empty_like(dy), torch.empty_like(dy)
+    mfsdp.mfsdp_activation_backward(mfsdp.ACT_SWIGLU, dy, gate, up, *want)
+    for first, second in ((0, 2), (1, 0), (1, 2)):
+        ins = [t.clone() for t in (dy, gate, up)]
+        mfsdp.mfsdp_activation_backward(mfsdp.ACT_SWIGLU, *ins, ins[first], ins[second])
+        assert torch.equal(ins[first], want[0]) and torch.equal(ins[second], want[1])
+    g = torch.empty_like(dy)
+    mfsdp.mfsdp_activation_backward(mfsdp.ACT_GELU, dy, gate, None, dgate=g)
+    for i in (0, 1):
+        ins = [dy.clone(), gate.clone()]
+        mfsdp.mfsdp_activation_backward(mfsdp.ACT_GELU, *ins, None, dgate=ins[i])
+        assert torch.equal(ins[i], g)
+
+
+def test_norm_gradients_of_two_graphs():
+    """Two captured backward passes keep their sums apart, replayed in turn and at once."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    sets = []
+    for rows, cols in ((700, 768), (900, 768)):
+        dy, h = (torch.randn(rows, cols, generator=gen, device="cuda").to(torch.bfloat16)
+                 for _ in range(2))
+        w = torch.randn(cols, generator=gen, device="cuda")
+        rstd = torch.rand(rows, generator=gen, device="cuda") + 0.5
+        dx, dw = torch.empty_like(dy), torch.empty_like(w)
+
+        def run(dy=dy, h=h, w=w, rstd=rstd, dx=dx, dw=dw):
+            mfsdp.mfsdp_norm_residual_backward(mfsdp.NORM_RMS, dy, None, h, w, None, rstd, dx, dw)
+
+        run()
+        want = dx.clone(), dw.clone()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        sets.append((graph, dx, dw, want, run))     # (run keeps the inputs that the graph reads)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for _, dx, dw, *_ in sets:
+            dx.zero_(), dw.zero_()
+        torch.cuda.synchronize()
+        for s, (graph, *_) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, dx, dw, want, _ in sets:
+            assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
