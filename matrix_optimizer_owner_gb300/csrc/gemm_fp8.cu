@@ -229,7 +229,7 @@ __device__ __forceinline__ void store_scales(const ScaleArgs& p, uint32_t dst, i
 }
 
 struct Gemm8Args {
-  CUtensorMap a, b;
+  CUtensorMap a, b, cm;       // cm: C in blocks of 32 rows of 64 bytes (PLAIN)
   ScaleArgs sa, sb;
   int32_t m, n, nkb;          // C's sizes and the blocks of k
   int32_t a_mn, b_mn;
@@ -239,7 +239,7 @@ struct Gemm8Args {
   void* c;
   int64_t ld_c;
   int32_t c_bf16, accumulate;
-  int32_t vec;                // C's rows: 0 as they come, 1 on 16-byte boundaries, 2 on 32-byte ones
+  int32_t vec;                // C's rows start on 16-byte boundaries
   int64_t sw, st;             // narrow kernel: C's strides along the wide and the narrow side
   uint64_t wait_limit_ns;
   int* status;
@@ -275,9 +275,12 @@ __device__ __forceinline__ PairTile pair_tile(const Gemm8Args& P, int i) {
   return PairTile{group * kRasterRows + j % rows, j / rows};
 }
 
-__device__ __forceinline__ void st256(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+// Adds a staging block to C in memory (fp32, to nearest): one addition per element and call, so there is
+// no order to depend on.
+__device__ __forceinline__ void tma_add_block(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
                : "memory");
 }
 
@@ -309,8 +312,8 @@ __device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c
   }
 }
 
-// 32 columns of a lane's row to C, whatever C's rows, edges and old values are.  Rows without 16-byte alignment go through the warp's staging area (2 KB), a row of the block at
-// a time.
+// 32 columns of a lane's row to C, whatever C's rows, edges and old values are.  Rows without 16-byte
+// alignment go through the warp's staging area (2 KB), a row of the block at a time.
 template <bool BF16>
 __device__ __forceinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane, int64_t c0,
                                         uint32_t stg, float (&v)[32]) {
@@ -388,36 +391,35 @@ __device__ __forceinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane
   }
 }
 
-// The same where rows start on 32-byte boundaries and nothing is added: a lane writes its row straight
-// from registers, a whole sector at a time.  (Staged through shared memory, so that a warp's stores
-// covered 64 bytes of a row, a tile's epilogue took twice the time.)
+// The same where rows start on 16-byte boundaries and C in bf16 is not added to: the warp's block leaves by
+// TMA, which cuts it at C's edges, 64 bytes of each row at a time.  (Stored by the lanes from registers, 32 bytes of
+// a row each: 24.8 us for 8192 x 4096 x 128 against 18.1, 3.8 TB/s, with a fill at 4.0; 35 against 30 for
+// 16384 x 2304 x 768.  Two staging blocks a warp, for a stage of operands less, changed nothing.)
 template <bool BF16>
-__device__ __forceinline__ void put_whole(const Gemm8Args& P, int64_t r, int64_t c0,
-                                          const float (&v)[32]) {
-  if (r >= P.m) return;
-  constexpr int kWords = BF16 ? 16 : 32;
-  uint32_t w[kWords];
+__device__ __forceinline__ void put_block(const Gemm8Args& P, int64_t rw, int lane, int64_t c0,
+                                          uint32_t stg, const float (&v)[32]) {
+  constexpr int kCols = BF16 ? 32 : 16;
 #pragma unroll
-  for (int k = 0; k < kWords; ++k)
-    w[k] = BF16 ? pack_bf16x2(v[BF16 ? 2 * k : k], v[BF16 ? 2 * k + 1 : k]) : __float_as_uint(v[k]);
-  void* d = BF16 ? static_cast<void*>(static_cast<bf16_t*>(P.c) + r * P.ld_c + c0)
-                 : static_cast<void*>(static_cast<float*>(P.c) + r * P.ld_c + c0);
-  if (c0 + 32 <= P.n) {
+  for (int h = 0; h < 32 / kCols; ++h) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
 #pragma unroll
-    for (int h = 0; h < kWords / 8; ++h) {
-      uint32_t o[8];
+    for (int k = 0; k < 4; ++k) {
+      uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = w[8 * h + k];
-      st256(static_cast<uint32_t*>(d) + 8 * h, o);
+      for (int i = 0; i < 4; ++i)
+        w[i] = BF16 ? pack_bf16x2(v[8 * k + 2 * i], v[8 * k + 2 * i + 1])
+                    : __float_as_uint(v[(BF16 ? 0 : 16 * h) + 4 * k + i]);
+      sts128(stg + stg_off(lane, k), make_uint4(w[0], w[1], w[2], w[3]));
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      if (c0 + k >= P.n) break;
-      if (BF16)
-        static_cast<uint16_t*>(d)[k] = (uint16_t)(w[BF16 ? k >> 1 : 0] >> (16 * (k & 1)));
-      else
-        static_cast<uint32_t*>(d)[k] = w[BF16 ? 0 : k];
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (c0 + kCols * h < P.n) {
+        if (!BF16 && P.accumulate) tma_add_block(&P.cm, stg, (int)c0 + kCols * h, (int)rw);
+        else tma_store_block(&P.cm, stg, (int)c0 + kCols * h, (int)rw);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
 }
@@ -425,7 +427,7 @@ __device__ __forceinline__ void put_whole(const Gemm8Args& P, int64_t r, int64_t
 // CHUNKED: a tile's contraction is cut into chunks that are added up in registers.
 // SPLIT: few tiles with a long contraction.  Two pairs (a cluster of four CTAs) take half of k each of one
 // tile; then each takes half of the columns and gets the other's sums of them through its shared memory.
-// PLAIN: C's rows start on 32-byte boundaries and it is not added to.  The other forms of the epilogue are
+// PLAIN: C's rows start on 16-byte boundaries and it is overwritten, or in fp32.  The other forms of the epilogue are
 // kernels of their own: beside each other in one kernel they cost its common path up to a sixth (the
 // warps wait for instructions).
 template <bool CHUNKED, bool SPLIT, bool BF16, bool PLAIN>
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t cb = (int64_t)t.tn * 256 + half * 128;
       const int nq = rw < P.m && cb < P.n ? (int)min((int64_t)4, (P.n - cb + 31) / 32) : 0;
       auto put = [&](int q, float (&v)[32]) {
-        if (PLAIN) put_whole<BF16>(P, rw + lane, cb + 32 * q, v);
+        if (PLAIN) put_block<BF16>(P, rw, lane, cb + 32 * q, stg, v);
         else put_row<BF16>(P, rw, lane, cb + 32 * q, stg, v);
       };
       // the shared columns: this warp's chunk `sh` of this accumulator, if it holds them
@@ -796,12 +798,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           v[4 * i + 2] = __uint_as_float(a[4 * i + 2]) + __uint_as_float(o.z);
           v[4 * i + 3] = __uint_as_float(a[4 * i + 3]) + __uint_as_float(o.w);
         }
-        if (PLAIN) put_whole<BF16>(P, rw + lane, c0, v);
+        if (PLAIN) put_block<BF16>(P, rw, lane, c0, stg, v);
         else put_row<BF16>(P, rw, lane, c0, stg, v);
       }
     }
   }
 
+  if (PLAIN) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncwarp();
   __syncthreads();
@@ -1236,8 +1239,6 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   int* status = device_status();
   if (!status) return MFSDP_ECUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int vec = !vector_rows(c, ld_c, c_dtype) ? 0
-                  : aligned_to(c, 32) && (ld_c * (int64_t)dtype_bytes(c_dtype)) % 32 == 0 ? 2 : 1;
   if (k == 0) {
     const ZeroArgs8 z{c, m, n, ld_c, c_bf16};
     const dim3 grid((unsigned)std::min<int64_t>((m * n + 255) / 256, sms * 16ll));
@@ -1270,7 +1271,7 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   g.ld_c = ld_c;
   g.c_bf16 = c_bf16;
   g.accumulate = accumulate != 0;
-  g.vec = vec;
+  g.vec = vector_rows(c, ld_c, c_dtype);
   g.wait_limit_ns = wait_limit_ns();
   g.status = status;
   cudaError_t e;
@@ -1291,12 +1292,15 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   const int most = most_blocks(c_bf16);
   const int tiles = g.tiles_m * g.tiles_n;
   const int pairs = std::max(1, std::min(sms / 2, tiles));
-  const bool plain = g.vec == 2 && !g.accumulate;
+  const bool plain = g.vec && (!g.accumulate || !c_bf16) &&
+                     (c_bf16 ? encode_map(&g.cm, c, m, n, ld_c, 32u, 32u, false)
+                             : encode_map_f32(&g.cm, static_cast<float*>(c), m, n, ld_c, 32u, 16u));
   if (plan.halves && g.kb_split <= most)
     e = plain ? launch_pair<false, true, true>(g, 4 * tiles, st)
               : launch_pair<false, true, false>(g, 4 * tiles, st);
   else if (g.nkb > most)
-    e = launch_pair<true, false, false>(g, 2 * pairs, st);
+    e = plain ? launch_pair<true, false, true>(g, 2 * pairs, st)
+              : launch_pair<true, false, false>(g, 2 * pairs, st);
   else
     e = plain ? launch_pair<false, false, true>(g, 2 * pairs, st)
               : launch_pair<false, false, false>(g, 2 * pairs, st);

@@ -201,10 +201,11 @@ cudaError_t launch_ns_pair_split(const NsLaunchParams& p, int pairs, cudaStream_
 bool encode_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld,
                 uint32_t box_rows, uint32_t box_cols = 64, bool swizzle128 = true);
 bool encode_map3d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld);
-// 2D fp32 tensor map (boxes of 32 columns x box_rows rows, 128-byte swizzle); false when the
-// driver refuses it (the base must be 16-byte aligned and ld a multiple of 4).
+// 2D fp32 tensor map (boxes of 32 columns x box_rows rows, 128-byte swizzle, or of 16 columns with a
+// 64-byte one); false when the driver refuses it (the base must be 16-byte aligned and ld a multiple
+// of 4).
 bool encode_map_f32(CUtensorMap* map, const float* base, int64_t rows, int64_t cols, int64_t ld,
-                    uint32_t box_rows);
+                    uint32_t box_rows, uint32_t box_cols = 32);
 // 2D byte tensor map (boxes of 128 columns x box_rows rows, 128-byte swizzle); false when the driver
 // refuses it (the base must be 16-byte aligned and ld a multiple of 16).
 bool encode_map_u8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld,
