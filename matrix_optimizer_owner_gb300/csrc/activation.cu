@@ -10,8 +10,9 @@
 // take, so that no gradient is written in 16 bits and read again to be quantized.  A block holds a tile of
 // 128 x 128 values, which both groupings end inside.
 //
-// Bound by memory, with little to spare: a value costs two special-function instructions and some forty
-// others in the backward pass.
+// Forward is bound by memory, with little to spare (8192 x 14336 SwiGLU with all three results in 8 bits:
+// 163 us, 5.0 TB/s).  Backward is bound by what the warps can issue: a value's four results cost some
+// fifty instructions (the same size from the checkpoints, 8 bytes a value: 268 us, 3.5 TB/s).
 #include <algorithm>
 #include <atomic>
 
@@ -251,15 +252,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   auto fetch = [&](const Tile& tile, int stage) {
     if (tile.r < tile_rows) {
-      const TileAt<false> at(tile.r, tile.c, p.rows, p.cols);
-      in.copy(stage, 0, at, static_cast<const T*>(p.dy), p.ld_dy, p.vec);
-      if constexpr (KEPT) {
-        in.copy8(stage, 1, at, p.gate8);
-        if (GLU) in.copy8(stage, 2, at, p.up8);
-      } else {
-        in.copy(stage, 1, at, static_cast<const T*>(p.gate), p.ld_gate, p.vec);
-        if (GLU) in.copy(stage, 2, at, static_cast<const T*>(p.up), p.ld_up, p.vec);
-      }
+      auto all = [&](const auto& at) {
+        const int vec = at.kFull || p.vec;
+        in.copy(stage, 0, at, static_cast<const T*>(p.dy), p.ld_dy, vec);
+        if constexpr (KEPT) {
+          in.copy8(stage, 1, at, p.gate8);
+          if (GLU) in.copy8(stage, 2, at, p.up8);
+        } else {
+          in.copy(stage, 1, at, static_cast<const T*>(p.gate), p.ld_gate, vec);
+          if (GLU) in.copy(stage, 2, at, static_cast<const T*>(p.up), p.ld_up, vec);
+        }
+      };
+      if (full_tile(tile.r, tile.c, p.rows, p.cols, p.vec))
+        all(TileAt<true>(tile.r, tile.c, p.rows, p.cols));
+      else
+        all(TileAt<false>(tile.r, tile.c, p.rows, p.cols));
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -268,14 +275,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   auto fetch_scales = [&](const Tile& tile, Scales& v) {
     if (!KEPT || tile.r >= tile_rows) return;
-    const TileAt<false> at(tile.r, tile.c, p.rows, p.cols);
-    const uint8_t* g = p.gate8.s + at.row * p.gate8.ld_s + at.group;
-    const uint8_t* u = GLU ? p.up8.s + at.row * p.up8.ld_s + at.group : nullptr;
+    auto all = [&](const auto& at) {
+      const uint8_t* g = p.gate8.s + at.row * p.gate8.ld_s + at.group;
+      const uint8_t* u = GLU ? p.up8.s + at.row * p.up8.ld_s + at.group : nullptr;
 #pragma unroll
-    for (int i = 0; i < kTilePasses; ++i) {
-      v.s[KEPT ? i : 0][0] = at.has(i) ? g[i * (kTileRows * p.gate8.ld_s)] : 127u;
-      if (GLU) v.s[KEPT ? i : 0][KEPT && GLU ? 1 : 0] = at.has(i) ? u[i * (kTileRows * p.up8.ld_s)] : 127u;
-    }
+      for (int i = 0; i < kTilePasses; ++i) {
+        v.s[KEPT ? i : 0][0] = at.has(i) ? g[i * (kTileRows * p.gate8.ld_s)] : 127u;
+        if (GLU) v.s[KEPT ? i : 0][KEPT && GLU ? 1 : 0] = at.has(i) ? u[i * (kTileRows * p.up8.ld_s)] : 127u;
+      }
+    };
+    if (full_tile(tile.r, tile.c, p.rows, p.cols, p.vec))
+      all(TileAt<true>(tile.r, tile.c, p.rows, p.cols));
+    else
+      all(TileAt<false>(tile.r, tile.c, p.rows, p.cols));
   };
   Tile tile{(int64_t)(blockIdx.x / (unsigned)groups), (int32_t)(blockIdx.x % (unsigned)groups)};
   Tile far = tile;                         // the next tile to copy
@@ -306,10 +318,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (row.q)
 #pragma unroll
           for (int i = 0; i < kTilePasses; i += 2) quantize_rows(at, i, v[i], v[i + 1], row);
-        if (col.q) {
-          quantize_cols<false>(at, sm, col, v);
-          __syncthreads();
-        }
+        if (col.q) quantize_cols<false>(at, sm, col, v);
       };
       TileValues dg, du;
 #pragma unroll

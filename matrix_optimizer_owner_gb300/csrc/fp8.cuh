@@ -39,8 +39,11 @@ __device__ __forceinline__ uint32_t scale_byte(float amax, int e5m2) {
 __device__ __forceinline__ float inverse_scale(uint32_t byte) {   // byte <= 247
   return __uint_as_float((254u - byte) << 23);
 }
+// (in bf16 every one is exact, 255 a NaN)
 __device__ __forceinline__ float scale_value(uint32_t byte) {
-  return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"((uint16_t)byte));
+  return __uint_as_float(r << 16);
 }
 
 // Infinities become NaN, which fmaxf passes over.
@@ -72,6 +75,27 @@ __device__ __forceinline__ uint32_t scale_of_part(uint32_t part, int e5m2) {
   return (uint32_t)max((int)part - (e5m2 ? 15 : 8), 0);
 }
 
+// ---- two values in one instruction, each rounded as by the scalar one
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split_pair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void scale_pairs(const float (&v)[N], float f, float (&u)[N]) {
+  const uint64_t ff = pair_of(f, f);
+#pragma unroll
+  for (int j = 0; j < N; j += 2) split_pair(mul2(pair_of(v[j], v[j + 1]), ff), u[j], u[j + 1]);
+}
+
 // ---- eight consecutive values
 __device__ __forceinline__ uint32_t pack4(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x5410); }
 __device__ __forceinline__ uint2 pack_fp8(const float (&v)[8], int e5m2) {
@@ -89,8 +113,7 @@ __device__ __forceinline__ uint2 pack_fp8(const float (&v)[8], int e5m2) {
 }
 __device__ __forceinline__ uint2 pack_fp8(const float (&v)[8], float inv, int e5m2) {
   float u[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) u[j] = v[j] * inv;
+  scale_pairs(v, inv, u);
   return pack_fp8(u, e5m2);
 }
 __device__ __forceinline__ void unpack_fp8(uint2 r, int e5m2, float (&v)[8]) {
@@ -113,9 +136,9 @@ __device__ __forceinline__ void unpack_fp8(uint2 r, int e5m2, float (&v)[8]) {
   }
 }
 __device__ __forceinline__ void unpack_fp8(uint2 r, int e5m2, float scale, float (&v)[8]) {
-  unpack_fp8(r, e5m2, v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= scale;
+  float u[8];
+  unpack_fp8(r, e5m2, u);
+  scale_pairs(u, scale, v);
 }
 // The first n (1 to 8) bytes of a chunk at p, which starts on an 8-byte boundary.
 __device__ __forceinline__ void store_fp8(uint8_t* p, uint2 r, int n) {
@@ -209,9 +232,11 @@ __device__ __forceinline__ void quantize_sixteen(const Sixteen& at, float (&v)[1
   float lo[8], hi[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    lo[j] = v[j] * inv;
-    hi[j] = v[8 + j] * inv;
+    lo[j] = v[j];
+    hi[j] = v[8 + j];
   }
+  scale_pairs(lo, inv, lo);
+  scale_pairs(hi, inv, hi);
   const uint2 a = pack_fp8(lo, m.e5m2), b = pack_fp8(hi, m.e5m2);
   uint8_t* q = m.q + at.row * m.ld + at.col;
   if (at.width >= 16) {
@@ -389,7 +414,8 @@ __device__ __forceinline__ void quantize_rows(const At& at, int i, float (&u)[8]
 }
 
 // The tile as 128 x 1 groups (COL) or one group (TILE); every thread of the block calls, and values that
-// are not finite become NaN.  The shared memory is free again after the block's next barrier.
+// are not finite become NaN.  Another tile as 128 x 1 groups may follow at once: what it writes to the
+// shared memory was last read before a barrier that it has passed.  One group's needs a barrier between.
 template <bool WHOLE, typename At>
 __device__ __forceinline__ void quantize_cols(const At& at, TileSmem& sm, const Fp8Ref& m,
                                               TileValues& v) {
@@ -470,7 +496,9 @@ __device__ __forceinline__ void quantize_cols(const At& at, TileSmem& sm, const 
   for (int i = 0; i < kTilePasses; ++i) {
     float u[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = v[i][j] * inv[WHOLE ? 0 : j];
+    for (int j = 0; j < 8; j += 2)
+      split_pair(mul2(pair_of(v[i][j], v[i][j + 1]), pair_of(inv[WHOLE ? 0 : j], inv[WHOLE ? 0 : j + 1])),
+                 u[j], u[j + 1]);
     if (at.has(i)) store_fp8(q + i * (kTileRows * m.ld), pack_fp8(u, m.e5m2), at.width());
   }
 }
