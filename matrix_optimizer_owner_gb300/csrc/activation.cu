@@ -12,7 +12,7 @@
 //
 // Forward is bound by memory, with little to spare (8192 x 14336 SwiGLU with all three results in 8 bits:
 // 163 us, 5.0 TB/s).  Backward is bound by what the warps can issue: a value's four results cost some
-// fifty instructions (the same size from the checkpoints, 8 bytes a value: 268 us, 3.5 TB/s).
+// fifty instructions (the same size from the checkpoints, 8 bytes a value: 242 us, 3.9 TB/s).
 #include <algorithm>
 #include <atomic>
 
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     activation_backward_kernel(const __grid_constant__ ActArgs p) {
   using A = Ahead<T, GLU, KEPT>;
   constexpr int D = A::kDepth;
-  __shared__ __align__(16) TileSmem sm;
+  __shared__ __align__(16) TileSmem<GLU ? 2 : 1> sm;
   extern __shared__ uint4 ahead_smem[];
   const A in(ahead_smem);
   pdl_launch();
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         else
           in.get(stage, i, m, v);
       };
-      auto emit = [&](TileValues& v, void* out, int64_t ld, const Fp8Ref& row, const Fp8Ref& col) {
+      auto emit = [&](TileValues& v, void* out, int64_t ld, const Fp8Ref& row) {
         if (out)
 #pragma unroll
           for (int i = 0; i < kTilePasses; ++i)
@@ -318,7 +318,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (row.q)
 #pragma unroll
           for (int i = 0; i < kTilePasses; i += 2) quantize_rows(at, i, v[i], v[i + 1], row);
-        if (col.q) quantize_cols<false>(at, sm, col, v);
       };
       TileValues dg, du;
 #pragma unroll
@@ -331,10 +330,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int j = 0; j < 8; ++j)
           act_grads<T, GLU>(d[j], g[j], GLU ? u[j] : 0.f, dg[i][j], du[i][j]);
       }
-      if (p.dgate || p.dgate_row.q || p.dgate_col.q)
-        emit(dg, p.dgate, p.ld_dgate, p.dgate_row, p.dgate_col);
-      if (GLU && (p.dup || p.dup_row.q || p.dup_col.q))
-        emit(du, p.dup, p.ld_dup, p.dup_row, p.dup_col);
+      emit(dg, p.dgate, p.ld_dgate, p.dgate_row);
+      if (GLU) emit(du, p.dup, p.ld_dup, p.dup_row);
+      if constexpr (GLU) {
+        if (p.dgate_col.q && p.dup_col.q) quantize_cols<2>(at, sm, {&p.dgate_col, &p.dup_col}, {&dg, &du});
+        else if (p.dgate_col.q) quantize_cols<1>(at, sm, {&p.dgate_col}, {&dg});
+        else if (p.dup_col.q) quantize_cols<1>(at, sm, {&p.dup_col}, {&du});
+      } else {
+        if (p.dgate_col.q) quantize_cols<1>(at, sm, {&p.dgate_col}, {&dg});
+      }
     };
     if (full_tile(here.r, here.c, p.rows, p.cols, p.vec))
       process(TileAt<true>(here.r, here.c, p.rows, p.cols));

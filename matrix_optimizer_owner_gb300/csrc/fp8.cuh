@@ -298,9 +298,10 @@ __device__ __forceinline__ void get_sixteen(const Pack8<T> (&r)[2], float (&v)[1
 constexpr int kTileThreads = 512;
 constexpr int kTileRows = kTileThreads / 16;      // rows per pass
 constexpr int kTilePasses = kGroup / kTileRows;
+template <int N = 1>
 struct TileSmem {
-  uint32_t col[kTileThreads / 32][kGroup / 2];     // a warp's scales, two columns a word
-  float top[kGroup];                               // the columns' inverse scales
+  uint32_t col[N][kTileThreads / 32][kGroup / 2];  // a warp's scales, two columns a word
+  float top[N][kGroup];                            // the columns' inverse scales
 };
 
 // FULL: the tile has all its rows and columns, and every matrix rows for 16-byte accesses: no test per
@@ -413,94 +414,131 @@ __device__ __forceinline__ void quantize_rows(const At& at, int i, float (&u)[8]
   }
 }
 
-// The tile as 128 x 1 groups (COL) or one group (TILE); every thread of the block calls, and values that
-// are not finite become NaN.  Another tile as 128 x 1 groups may follow at once: what it writes to the
-// shared memory was last read before a barrier that it has passed.  One group's needs a barrier between.
-template <bool WHOLE, typename At>
-__device__ __forceinline__ void quantize_cols(const At& at, TileSmem& sm, const Fp8Ref& m,
-                                              TileValues& v) {
+// The columns' scales of a thread's four rows, two columns a word.
+__device__ __forceinline__ void column_parts(const TileValues& v, bool again, uint32_t (&w)[4]) {
   static_assert(kTilePasses == 4, "four rows a thread");
-  const int warp = threadIdx.x >> 5;
-  float inv[8];
-  // the columns' (or the tile's) scales; once more without the values that are not finite, if some are
-  for (bool again = false;; again = true) {
-    if (again) {
 #pragma unroll
-      for (int i = 0; i < kTilePasses; ++i)
+  for (int k = 0; k < 4; ++k) {
+    uint32_t b[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = finite_or_nan(v[i][j]);
-      __syncthreads();
+    for (int h = 0; h < 2; ++h) {
+      const int j = 2 * k + h;
+      const float a = again ? fmaxf(fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])),
+                                          fmaxf(fabsf(v[2][j]), fabsf(v[3][j]))), 0.f)
+                            : max_nan(max3_nan(v[0][j], v[1][j], v[2][j]), v[3][j]);
+      b[h] = scale_part(a);
     }
-    uint32_t w[4];                                 // two columns' scales each
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t b[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 2 * k + h;
-        const float a =
-            again ? fmaxf(fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])),
-                                fmaxf(fabsf(v[2][j]), fabsf(v[3][j]))), 0.f)
-                  : max_nan(max3_nan(v[0][j], v[1][j], v[2][j]), v[3][j]);
-        b[h] = scale_part(a);
-      }
-      w[k] = b[0] | (b[1] << 16);
-    }
-    bool bad;
-    if (WHOLE) {
-      uint32_t t = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t = max_u16x2(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
-      if ((threadIdx.x & 31) == 0) sm.col[warp][0] = t;
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kTileThreads / 32; ++k) t = max_u16x2(t, sm.col[k][0]);
-      const uint32_t part = max(t & 0xFFFFu, t >> 16), byte = scale_of_part(part, m.e5m2);
-      bad = part >= kMaybe && !again;
-      if (threadIdx.x == 0 && !bad) m.s[at.r0 / kGroup * m.ld_s + at.group] = (uint8_t)byte;
-      inv[0] = inverse_scale(byte);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = max_u16x2(w[k], __shfl_xor_sync(0xFFFFFFFFu, w[k], 16));
-      if ((threadIdx.x & 16) == 0)
-        *reinterpret_cast<uint4*>(&sm.col[warp][at.lane16 * 4]) = make_uint4(w[0], w[1], w[2], w[3]);
-      __syncthreads();
-      bad = false;
-      if (threadIdx.x < kGroup / 2) {
-        uint32_t t = sm.col[0][threadIdx.x];
-#pragma unroll
-        for (int k = 1; k < kTileThreads / 32; ++k) t = max_u16x2(t, sm.col[k][threadIdx.x]);
-        const uint32_t lo = scale_of_part(t & 0xFFFFu, m.e5m2), hi = scale_of_part(t >> 16, m.e5m2);
-        bad = ((t & 0xFFFFu) >= kMaybe || (t >> 16) >= kMaybe) && !again;
-        sm.top[2 * threadIdx.x] = inverse_scale(lo);
-        sm.top[2 * threadIdx.x + 1] = inverse_scale(hi);
-        uint8_t* s = m.s + at.r0 / kGroup * m.ld_s + at.group * kGroup + 2 * threadIdx.x;
-        if ((int)(2 * threadIdx.x) < at.cols_here) s[0] = (uint8_t)lo;
-        if ((int)(2 * threadIdx.x) + 1 < at.cols_here) s[1] = (uint8_t)hi;
-      }
-      bad = __syncthreads_or(bad);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float4 f = reinterpret_cast<const float4*>(sm.top)[at.lane16 * 2 + k];
-        inv[4 * k] = f.x;
-        inv[4 * k + 1] = f.y;
-        inv[4 * k + 2] = f.z;
-        inv[4 * k + 3] = f.w;
-      }
-    }
-    if (!bad) break;
+    w[k] = b[0] | (b[1] << 16);
   }
-  if (at.width() == 0) return;
+}
+__device__ __forceinline__ void clean_values(TileValues& v) {
+#pragma unroll
+  for (int i = 0; i < kTilePasses; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = finite_or_nan(v[i][j]);
+}
+template <typename At>
+__device__ __forceinline__ void store_columns(const At& at, const Fp8Ref& m, const TileValues& v,
+                                              const float (&inv)[8]) {
   uint8_t* q = m.q + at.row * m.ld + at.col;
 #pragma unroll
   for (int i = 0; i < kTilePasses; ++i) {
     float u[8];
 #pragma unroll
     for (int j = 0; j < 8; j += 2)
-      split_pair(mul2(pair_of(v[i][j], v[i][j + 1]), pair_of(inv[WHOLE ? 0 : j], inv[WHOLE ? 0 : j + 1])),
-                 u[j], u[j + 1]);
+      split_pair(mul2(pair_of(v[i][j], v[i][j + 1]), pair_of(inv[j], inv[j + 1])), u[j], u[j + 1]);
     if (at.has(i)) store_fp8(q + i * (kTileRows * m.ld), pack_fp8(u, m.e5m2), at.width());
   }
+}
+
+// N matrices' tiles as 128 x 1 groups, with the barriers of one; every thread of the block calls, and
+// values that are not finite become NaN.  Another tile may follow at once: what it writes to the shared
+// memory was last read before a barrier that it has passed.
+template <int N, int M, typename At>
+__device__ __forceinline__ void quantize_cols(const At& at, TileSmem<M>& sm, const Fp8Ref* const (&m)[N],
+                                              TileValues* const (&v)[N]) {
+  static_assert(N <= M && N <= 2, "one or two");
+  const int warp = threadIdx.x >> 5;
+  // the columns' scales; once more without the values that are not finite, if some are
+  for (bool again = false;; again = true) {
+    if (again) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) clean_values(*v[n]);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      uint32_t w[4];
+      column_parts(*v[n], again, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = max_u16x2(w[k], __shfl_xor_sync(0xFFFFFFFFu, w[k], 16));
+      if ((threadIdx.x & 16) == 0)
+        *reinterpret_cast<uint4*>(&sm.col[n][warp][at.lane16 * 4]) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncthreads();
+    bool bad = false;
+    if (threadIdx.x < N * (kGroup / 2)) {
+      const int n = N == 1 ? 0 : threadIdx.x / (kGroup / 2), c = threadIdx.x % (kGroup / 2);
+      const int e5m2 = n ? m[N - 1]->e5m2 : m[0]->e5m2;
+      uint32_t t = sm.col[n][0][c];
+#pragma unroll
+      for (int k = 1; k < kTileThreads / 32; ++k) t = max_u16x2(t, sm.col[n][k][c]);
+      const uint32_t lo = scale_of_part(t & 0xFFFFu, e5m2), hi = scale_of_part(t >> 16, e5m2);
+      bad = ((t & 0xFFFFu) >= kMaybe || (t >> 16) >= kMaybe) && !again;
+      sm.top[n][2 * c] = inverse_scale(lo);
+      sm.top[n][2 * c + 1] = inverse_scale(hi);
+      uint8_t* s = (n ? m[N - 1]->s : m[0]->s) + at.r0 / kGroup * (n ? m[N - 1]->ld_s : m[0]->ld_s) +
+                   at.group * kGroup + 2 * c;
+      if (2 * c < at.cols_here) s[0] = (uint8_t)lo;
+      if (2 * c + 1 < at.cols_here) s[1] = (uint8_t)hi;
+    }
+    if (!__syncthreads_or(bad)) break;
+  }
+  if (at.width() == 0) return;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float inv[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 f = reinterpret_cast<const float4*>(sm.top[n])[at.lane16 * 2 + k];
+      inv[4 * k] = f.x;
+      inv[4 * k + 1] = f.y;
+      inv[4 * k + 2] = f.z;
+      inv[4 * k + 3] = f.w;
+    }
+    store_columns(at, *m[n], *v[n], inv);
+  }
+}
+
+// The tile as one group.  Another tile's shared memory needs a barrier between.
+template <typename At>
+__device__ __forceinline__ void quantize_whole(const At& at, TileSmem<1>& sm, const Fp8Ref& m,
+                                               TileValues& v) {
+  uint32_t byte;
+  for (bool again = false;; again = true) {
+    if (again) {
+      clean_values(v);
+      __syncthreads();
+    }
+    uint32_t w[4];
+    column_parts(v, again, w);
+    uint32_t t = max_u16x2(max_u16x2(w[0], w[1]), max_u16x2(w[2], w[3]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t = max_u16x2(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+    if ((threadIdx.x & 31) == 0) sm.col[0][threadIdx.x >> 5][0] = t;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kTileThreads / 32; ++k) t = max_u16x2(t, sm.col[0][k][0]);
+    const uint32_t part = max(t & 0xFFFFu, t >> 16);
+    byte = scale_of_part(part, m.e5m2);
+    if (part < kMaybe || again) break;             // the same for all threads
+  }
+  if (threadIdx.x == 0) m.s[at.r0 / kGroup * m.ld_s + at.group] = (uint8_t)byte;
+  if (at.width() == 0) return;
+  float inv[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) inv[j] = inverse_scale(byte);
+  store_columns(at, m, v, inv);
 }
 
 // ---- host checks

@@ -23,7 +23,7 @@ struct QuantArgs {
 enum Form : int { kRow = 1, kCol = 2, kTile = 4 };
 
 template <typename Raw, int FORMS, typename At>
-__device__ __forceinline__ void quantize_tile(const QuantArgs& p, const At& at, TileSmem& sm) {
+__device__ __forceinline__ void quantize_tile(const QuantArgs& p, const At& at, TileSmem<>& sm) {
   TileValues v;
   if constexpr (std::is_same<Raw, TileRaw8>::value) {
     Raw raw;
@@ -49,13 +49,14 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, const At& at, 
 #pragma unroll
     for (int i = 0; i < kTilePasses; i += 2) quantize_rows(at, i, v[i], v[i + 1], p.row);
   }
-  if (FORMS & (kCol | kTile)) quantize_cols<(FORMS & kTile) != 0>(at, sm, p.other, v);
+  if (FORMS & kCol) quantize_cols<1>(at, sm, {&p.other}, {&v});
+  if (FORMS & kTile) quantize_whole(at, sm, p.other, v);
 }
 
 template <typename Raw, int FORMS>
 __global__ void __launch_bounds__(kTileThreads, 2)
     quantize_kernel(const __grid_constant__ QuantArgs p) {
-  __shared__ __align__(16) TileSmem sm;
+  __shared__ __align__(16) TileSmem<> sm;
   pdl_launch();
   pdl_wait();
   const int64_t tile_rows = (p.rows + kGroup - 1) / kGroup;
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       quantize_tile<Raw, FORMS>(p, TileAt<true>(tr, tc, p.rows, p.cols), sm);
     else
       quantize_tile<Raw, FORMS>(p, TileAt<false>(tr, tc, p.rows, p.cols), sm);
-    if ((FORMS & (kCol | kTile)) && tr + gridDim.y < tile_rows) __syncthreads();
+    if ((FORMS & kTile) && tr + gridDim.y < tile_rows) __syncthreads();
   }
 }
 
