@@ -11,8 +11,9 @@ namespace mfsdp {
 namespace {
 
 // ---------------------------------------------------------------- forward
-// Rows of up to 768 elements: a warp each, eight consecutive elements a lane, K times.
-template <typename T, int K>
+// Rows of up to 768 elements: a warp each, eight consecutive elements a lane, K times.  FULL: rows of K
+// times 256 elements, every one for 16-byte accesses: no test per chunk remains.
+template <typename T, int K, bool FULL>
 __global__ void __launch_bounds__(32 * kNormWarps, sizeof(T) == 2 ? 4 : 2)
     norm_residual_forward_kernel(const __grid_constant__ NrArgs p) {
   constexpr int TPR = 32;
@@ -23,15 +24,17 @@ __global__ void __launch_bounds__(32 * kNormWarps, sizeof(T) == 2 ? 4 : 2)
   pdl_wait();
   if (row >= p.rows) return;              // whole warps
   const int n = (int)p.cols;              // (rows this long fit registers)
+  const int vec = FULL ? 1 : p.vec, pvec = FULL ? 1 : p.pvec;
   auto col = [&](int k) { return (k * TPR + t) * 8; };
+  auto left_of = [&](int k) { return FULL ? 8 : n - col(k); };
   Pack8<T> xp[K], rp[K];
   const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
 #pragma unroll
-  for (int k = 0; k < K; ++k) load_chunk(xp[k], xr, col(k), n - col(k), p.vec);
+  for (int k = 0; k < K; ++k) load_chunk(xp[k], xr, col(k), left_of(k), vec);
   if (p.res) {
     const T* rr = static_cast<const T*>(p.res) + row * p.ld_res;
 #pragma unroll
-    for (int k = 0; k < K; ++k) load_chunk(rp[k], rr, col(k), n - col(k), p.vec);
+    for (int k = 0; k < K; ++k) load_chunk(rp[k], rr, col(k), left_of(k), vec);
   }
   float v[K][8], s = 0.f, zero = 0.f;
   int turn = 0;
@@ -48,7 +51,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, sizeof(T) == 2 ? 4 : 2)
   // what does not wait for the row's sums
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (p.h) store_part(static_cast<T*>(p.h) + row * p.ld_h, col(k), n - col(k), p.vec, v[k]);
+    if (p.h) store_part(static_cast<T*>(p.h) + row * p.ld_h, col(k), left_of(k), vec, v[k]);
   float mu = 0.f;
   if (p.layer) {
 #pragma unroll
@@ -64,7 +67,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, sizeof(T) == 2 ? 4 : 2)
     float d[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[j] = v[k][j] - mu;
-    zero_past(d, n - col(k));
+    zero_past(d, left_of(k));
 #pragma unroll
     for (int j = 0; j < 8; ++j) q = fmaf(d[j], d[j], q);
   }
@@ -77,21 +80,21 @@ __global__ void __launch_bounds__(32 * kNormWarps, sizeof(T) == 2 ? 4 : 2)
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = col(k), left = n - c;
+    const int c = col(k), left = left_of(k);
     float w[8], y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = (v[k][j] - mu) * r;
     if (p.w) {
-      load_param8(p.w, p.wbf16, p.pvec, c, left, 1.f, w);
+      load_param8(p.w, p.wbf16, pvec, c, left, 1.f, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] *= w[j];
     }
     if (p.b) {
-      load_param8(p.b, p.wbf16, p.pvec, c, left, 0.f, w);
+      load_param8(p.b, p.wbf16, pvec, c, left, 0.f, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] += w[j];
     }
-    if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, left, p.vec, y);
+    if (p.y) store_part(static_cast<T*>(p.y) + row * p.ld_y, c, left, vec, y);
     zero_past(y, left);
     store_groups(p, row, c, left, y, v[k]);
   }
@@ -250,14 +253,20 @@ cudaError_t launch_wide(const NrArgs& a, cudaStream_t st) {
   return a.layer ? launch_pdl(norm_residual_forward_wide_kernel<T, TPR, true>, grid, block, 0, st, a)
                  : launch_pdl(norm_residual_forward_wide_kernel<T, TPR, false>, grid, block, 0, st, a);
 }
+template <typename T, int K>
+cudaError_t launch_warps(const NrArgs& a, dim3 grid, dim3 block, cudaStream_t st) {
+  return a.cols == K * 256 && a.vec && a.pvec
+             ? launch_pdl(norm_residual_forward_kernel<T, K, true>, grid, block, 0, st, a)
+             : launch_pdl(norm_residual_forward_kernel<T, K, false>, grid, block, 0, st, a);
+}
 template <typename T>
 cudaError_t launch_forward(const NrArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)((a.rows + kNormWarps - 1) / kNormWarps)), block(32 * kNormWarps);
-  if (a.cols <= 256) return launch_pdl(norm_residual_forward_kernel<T, 1>, grid, block, 0, st, a);
-  if (a.cols <= 512) return launch_pdl(norm_residual_forward_kernel<T, 2>, grid, block, 0, st, a);
+  if (a.cols <= 256) return launch_warps<T, 1>(a, grid, block, st);
+  if (a.cols <= 512) return launch_warps<T, 2>(a, grid, block, st);
   // (768 in 64 threads of sixteen leaves a quarter of them idle: 29 -> 36 us for 16384 rows; 1024 fills
   // them: 46 -> 32)
-  if (a.cols <= 768) return launch_pdl(norm_residual_forward_kernel<T, 3>, grid, block, 0, st, a);
+  if (a.cols <= 768) return launch_warps<T, 3>(a, grid, block, st);
   if (a.cols <= 1024) return launch_wide<T, 64>(a, st);
   if (a.cols <= 2048) return launch_wide<T, 128>(a, st);
   if (a.cols <= 4096) return launch_wide<T, 256>(a, st);
