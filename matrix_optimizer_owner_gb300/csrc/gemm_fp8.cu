@@ -1203,8 +1203,10 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   if (!a || !b || !dtype_ok(c_dtype)) return MFSDP_EINVAL;
   int chk = check_sizes(m, n, k);
   if (chk != MFSDP_OK) return chk;
-  chk = trans_a ? check_fp8(*a, k, m, -1) : check_fp8(*a, m, k, -1);
-  if (chk == MFSDP_OK) chk = trans_b ? check_fp8(*b, n, k, -1) : check_fp8(*b, k, n, -1);
+  const bool none = m == 0 || n == 0 || k == 0;           // nothing of A or B is read
+  chk = trans_a ? check_fp8(*a, none ? 0 : k, m, -1) : check_fp8(*a, none ? 0 : m, k, -1);
+  if (chk == MFSDP_OK)
+    chk = trans_b ? check_fp8(*b, none ? 0 : n, k, -1) : check_fp8(*b, none ? 0 : k, n, -1);
   if (chk != MFSDP_OK) return chk;
   // a scale has to be the same for 128 of the contraction
   if (a->groups == (trans_a ? MFSDP_GROUPS_ROW : MFSDP_GROUPS_COL) ||

@@ -58,6 +58,22 @@ def test_gemm_long_contraction(dtype, m, n, k, down):
         assert (err <= tol).all(), float((err / tol).max())
 
 
+@pytest.mark.parametrize("trans_a,trans_b", [(False, True), (False, False), (True, False), (True, True)])
+def test_gemm_of_nothing(trans_a, trans_b):
+    """Empty in any direction: no rows, no columns, or a contraction of nothing, which is zero."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    for m, n, k in ((300, 20, 0), (0, 20, 100), (300, 0, 100), (0, 0, 0)):
+        a = mfsdp.fp8_empty(*((k, m) if trans_a else (m, k)),
+                            mfsdp.GROUPS_COL if trans_a else mfsdp.GROUPS_ROW)
+        b = mfsdp.fp8_empty(*((n, k) if trans_b else (k, n)),
+                            mfsdp.GROUPS_ROW if trans_b else mfsdp.GROUPS_COL)
+        c = torch.ones(m, n, device="cuda")
+        mfsdp.mfsdp_gemm_fp8(a, b, c, trans_a=trans_a, trans_b=trans_b, accumulate=True)
+        assert (c == 1).all()
+        mfsdp.mfsdp_gemm_fp8(a, b, c, trans_a=trans_a, trans_b=trans_b)
+        assert (c == 0).all()
+
+
 def test_gemm_very_many_rows():
     from matrix_optimizer_owner_gb300 import mfsdp
     gen = torch.Generator(device="cuda").manual_seed(1)
