@@ -1007,23 +1007,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
   cluster_sync_all();
   {
     // this CTA's share of the tile: narrow indices split, split + splits, ...; a thread adds four
-    // consecutive wide indices over the slices, in order
+    // consecutive wide indices over the slices, in order, with all loads of two narrow indices under way
+    // before it waits for one (one after the other they took 4 us of a small product's 10)
     const int live = min(NT, P.n - t0), wide = min(128, P.m - w0);
     const uint32_t mine = smem_u32(sums);
-    const int r = (threadIdx.x & 31) * 4;
-    for (int t = split + (int)(threadIdx.x >> 5) * P.splits; t < live && r < wide;
-         t += kNarrowThreads / 32 * P.splits) {
-      float v[4];
-#pragma unroll 4
-      for (int i = 0; i < P.splits; ++i) {
-        float o[4];
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
-                     : "r"(map_rank(mine + (uint32_t)(t * 128 + r) * 4u, (uint32_t)i))
-                     : "memory");
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = i == 0 ? o[k] : v[k] + o[k];
-      }
+    const int r = (threadIdx.x & 31) * 4, step = kNarrowThreads / 32 * P.splits;
+    auto put = [&](int t, const float (&v)[4]) {
       const int64_t at = (int64_t)(w0 + r) * P.sw + (int64_t)(t0 + t) * P.st;
       if (P.sw == 1 && P.vec && r + 4 <= wide && !P.accumulate) {
         if (P.c_bf16)
@@ -1042,6 +1031,43 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
             float* c = static_cast<float*>(P.c) + at + k * P.sw;
             *c = P.accumulate ? v[k] + *c : v[k];
           }
+        }
+      }
+    };
+    constexpr int U = 2;                                  // (one: up to 9 % more for tiles of 128)
+    if (P.splits == 1) {
+      if (r < wide)
+#pragma unroll 4
+        for (int t = (int)(threadIdx.x >> 5); t < live; t += kNarrowThreads / 32) {
+          const float4 o = *reinterpret_cast<const float4*>(sums + t * 128 + r);
+          const float v[4] = {o.x, o.y, o.z, o.w};
+          put(t, v);
+        }
+    } else if (r < wide) {
+      for (int t = split + (int)(threadIdx.x >> 5) * P.splits; t < live; t += U * step) {
+        float o[U][8][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            // (beyond the last slice or index nothing is read)
+            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
+                         " @p ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n}\n"
+                         : "=f"(o[u][i][0]), "=f"(o[u][i][1]), "=f"(o[u][i][2]), "=f"(o[u][i][3])
+                         : "r"(map_rank(mine + (uint32_t)((t + u * step) * 128 + r) * 4u,
+                                        (uint32_t)min(i, P.splits - 1))),
+                           "r"((int)(i < P.splits && t + u * step < live)));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (t + u * step >= live) break;
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[k] = o[u][0][k];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) v[k] = i < P.splits ? v[k] + o[u][i][k] : v[k];
+          }
+          put(t + u * step, v);
         }
       }
     }
@@ -1091,14 +1117,19 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16) {
     p.kb_split = (nkb + s - 1) / s;
     return p;
   }
-  // 128 x 128 tiles, C's rows the wide side: rounds of two CTAs an SM, up to eight slices of k
+  // 128 x 128 tiles, C's rows the wide side: rounds of two CTAs an SM, up to eight slices of k.  A block of k
+  // takes 0.4 us on an SM's only CTA and 0.5 beside another one; what is left, mostly the sums' way through
+  // distributed shared memory, grows with the CTAs that send theirs at the same time (6.8 us for 32 of
+  // them, 9.8 for 288), and a CTA that adds and writes a whole tile takes 2 us more.
   const int64_t small = ((m + 127) / 128) * ((n + 127) / 128);
   int ns = 0;
   double narrow = 0.;
   for (int s = std::max(1, least); s <= 8 && s <= std::max(1, nkb); ++s) {
     const int per = (nkb + s - 1) / s;
-    const int64_t rounds = (small * s + 4 * kPairs - 1) / (4 * kPairs);
-    const double t = 3. + (double)rounds * (per * 0.55 + 2.5) + 0.1 * s;
+    const int64_t ctas = small * s, rounds = (ctas + 4 * kPairs - 1) / (4 * kPairs);
+    const int64_t at_once = std::min<int64_t>(ctas, 4 * kPairs);
+    const double t = (double)rounds * (per * (at_once > 2 * kPairs ? 0.5 : 0.4) + (s == 1 ? 8.2 : 6.2) +
+                                       0.0125 * (double)at_once);
     if (ns == 0 || t < narrow * 0.98) {
       narrow = t;
       ns = s;
@@ -1106,7 +1137,7 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16) {
   }
   // 256 x 256 tiles on CTA pairs
   const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  double pair = 5. + (double)((tiles + kPairs - 1) / kPairs) * (nkb * 0.34 + 2.);
+  double pair = 7.5 + (double)((tiles + kPairs - 1) / kPairs) * (nkb * 0.3 + 2.);
   if (2 * tiles <= kPairs && nkb >= 16) {
     p.kb_split = ((nkb + 1) / 2 + 7) / 8 * 8;
     const double t = 9. + p.kb_split * 0.34;
