@@ -239,7 +239,7 @@ struct Gemm8Args {
   void* c;
   int64_t ld_c;
   int32_t c_bf16, accumulate;
-  int32_t vec;                // C's rows start on 16-byte boundaries
+  int32_t vec;                // C's rows start on 16-byte boundaries (narrow kernel: on those of four entries)
   int64_t sw, st;             // narrow kernel: C's strides along the wide and the narrow side
   uint64_t wait_limit_ns;
   int* status;
@@ -1012,9 +1012,33 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     const int live = min(NT, P.n - t0), wide = min(128, P.m - w0);
     const uint32_t mine = smem_u32(sums);
     const int r = (threadIdx.x & 31) * 4, step = kNarrowThreads / 32 * P.splits;
+    auto place = [&](int t) { return (int64_t)(w0 + r) * P.sw + (int64_t)(t0 + t) * P.st; };
+    const bool four = P.sw == 1 && P.vec && r + 4 <= wide;
+    auto load_old = [&](int t, float (&v)[4]) {
+      const int64_t at = place(t);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = 0.f;
+      if (four) {
+        if (P.c_bf16) {
+          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const bf16_t*>(P.c) + at);
+          v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+          v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+        } else {
+          const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(P.c) + at);
+          v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (r + k >= wide) break;
+          v[k] = P.c_bf16 ? to_f32(static_cast<const bf16_t*>(P.c)[at + k * P.sw])
+                          : static_cast<const float*>(P.c)[at + k * P.sw];
+        }
+      }
+    };
     auto put = [&](int t, const float (&v)[4]) {
-      const int64_t at = (int64_t)(w0 + r) * P.sw + (int64_t)(t0 + t) * P.st;
-      if (P.sw == 1 && P.vec && r + 4 <= wide && !P.accumulate) {
+      const int64_t at = place(t);
+      if (four) {
         if (P.c_bf16)
           *reinterpret_cast<uint2*>(static_cast<bf16_t*>(P.c) + at) =
               make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
@@ -1024,20 +1048,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (r + k >= wide) break;
-          if (P.c_bf16) {
-            bf16_t* c = static_cast<bf16_t*>(P.c) + at + k * P.sw;
-            *c = from_f32<bf16_t>(P.accumulate ? v[k] + to_f32(*c) : v[k]);
-          } else {
-            float* c = static_cast<float*>(P.c) + at + k * P.sw;
-            *c = P.accumulate ? v[k] + *c : v[k];
-          }
+          if (P.c_bf16) static_cast<bf16_t*>(P.c)[at + k * P.sw] = from_f32<bf16_t>(v[k]);
+          else static_cast<float*>(P.c)[at + k * P.sw] = v[k];
         }
       }
     };
     constexpr int U = 2;                                  // (one: up to 9 % more for tiles of 128)
-    if (P.splits == 1) {
+    if (P.splits == 1 && !P.accumulate) {
       if (r < wide)
-#pragma unroll 4
+#pragma unroll 1
         for (int t = (int)(threadIdx.x >> 5); t < live; t += kNarrowThreads / 32) {
           const float4 o = *reinterpret_cast<const float4*>(sums + t * 128 + r);
           const float v[4] = {o.x, o.y, o.z, o.w};
@@ -1045,7 +1064,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         }
     } else if (r < wide) {
       for (int t = split + (int)(threadIdx.x >> 5) * P.splits; t < live; t += U * step) {
-        float o[U][8][4];
+        float o[U][8][4], old[U][4];
+        if (P.accumulate)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (t + u * step < live) load_old(t + u * step, old[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -1066,6 +1089,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
             v[k] = o[u][0][k];
 #pragma unroll
             for (int i = 1; i < 8; ++i) v[k] = i < P.splits ? v[k] + o[u][i][k] : v[k];
+            v[k] = P.accumulate ? v[k] + old[u][k] : v[k];
           }
           put(t + u * step, v);
         }
@@ -1098,7 +1122,7 @@ struct Gemm8Plan {
 int most_blocks(bool c_bf16) { return c_bf16 ? 512 : kChunk8; }
 
 // What a call is split into, from its sizes alone.  Times in us, as measured.
-Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16) {
+Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16, bool accumulate) {
   Gemm8Plan p;
   const int nkb = (int)((k + kB8 - 1) / kB8);
   const int64_t few = std::min(m, n), wide = std::max(m, n);
@@ -1118,9 +1142,9 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16) {
     return p;
   }
   // 128 x 128 tiles, C's rows the wide side: rounds of two CTAs an SM, up to eight slices of k.  A block of k
-  // takes 0.4 us on an SM's only CTA and 0.5 beside another one; what is left, mostly the sums' way through
-  // distributed shared memory, grows with the CTAs that send theirs at the same time (6.8 us for 32 of
-  // them, 9.8 for 288), and a CTA that adds and writes a whole tile takes 2 us more.
+  // takes 0.4 us on an SM's only CTA and 0.5 beside another one.  The rest grows with the CTAs: 5.4 us for
+  // one and 7 for 256 without slices; 6.8 for 32 and 9.8 for 288 where slices' sums go through distributed
+  // shared memory at the same time.  What C holds is read by the CTAs that add it, a few rows at a time.
   const int64_t small = ((m + 127) / 128) * ((n + 127) / 128);
   int ns = 0;
   double narrow = 0.;
@@ -1128,8 +1152,9 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16) {
     const int per = (nkb + s - 1) / s;
     const int64_t ctas = small * s, rounds = (ctas + 4 * kPairs - 1) / (4 * kPairs);
     const int64_t at_once = std::min<int64_t>(ctas, 4 * kPairs);
-    const double t = (double)rounds * (per * (at_once > 2 * kPairs ? 0.5 : 0.4) + (s == 1 ? 8.2 : 6.2) +
-                                       0.0125 * (double)at_once);
+    const double rest = s == 1 ? 5.3 + 0.0065 * (double)at_once : 6.2 + 0.0125 * (double)at_once;
+    const double old = accumulate ? 10. / s : 0.;
+    const double t = (double)rounds * (per * (at_once > 2 * kPairs ? 0.5 : 0.4) + rest + old);
     if (ns == 0 || t < narrow * 0.98) {
       narrow = t;
       ns = s;
@@ -1249,7 +1274,7 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   const bool c_bf16 = c_dtype == MFSDP_DTYPE_BF16;
   // More of k than eight slices take at fp32's chunks: one such piece after the other, added to C.
   constexpr int64_t piece = 8ll * kChunk8 * kB8;
-  if (!c_bf16 && k > piece && plan_gemm(m, n, piece, false).narrow) {
+  if (!c_bf16 && k > piece && plan_gemm(m, n, piece, false, true).narrow) {
     for (int64_t k0 = 0; k0 < k; k0 += piece) {
       mfsdp_fp8_matrix pa = *a, pb = *b;
       auto shift = [&](mfsdp_fp8_matrix& x, bool down) {  // down: the contraction runs down the rows
@@ -1264,7 +1289,7 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
     }
     return MFSDP_OK;
   }
-  const Gemm8Plan plan = plan_gemm(m, n, k, c_bf16);
+  const Gemm8Plan plan = plan_gemm(m, n, k, c_bf16, accumulate != 0);
   if (k == 0 && accumulate) return MFSDP_OK;
   int sms = 0;
   const int dst = device_sms(&sms);
@@ -1304,7 +1329,9 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   g.ld_c = ld_c;
   g.c_bf16 = c_bf16;
   g.accumulate = accumulate != 0;
-  g.vec = vector_rows(c, ld_c, c_dtype);
+  // 16-byte accesses of C's rows; the narrow kernel's are of four entries
+  g.vec = plan.narrow ? ld_c % 4 == 0 && aligned_to(c, 4 * dtype_bytes(c_dtype))
+                      : vector_rows(c, ld_c, c_dtype);
   g.wait_limit_ns = wait_limit_ns();
   g.status = status;
   cudaError_t e;
