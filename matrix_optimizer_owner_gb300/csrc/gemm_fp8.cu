@@ -1,10 +1,16 @@
 // Products of 8-bit matrices with a power-of-two scale per 128 of the contraction:
 //     C = op(A) op(B),  C_mn = sum_b 2^(sa_mb + sb_nb) sum_{k in block b} qa_mk qb_kn   (fp32 sums)
 // on the tensor cores' block-scaled form (tcgen05.mma kind::mxf8f6f4): the products of a block are
-// scaled while they are added up, so a tile's accumulator stays in tensor memory over the whole
-// contraction and nothing is read back between blocks.  That form wants a scale byte per row and 32
-// of k; a byte serves the four instructions of a block of 128, and the four bytes of a 32-bit word
-// four blocks, picked by the instruction's scale id.
+// scaled while they are added up, so a tile's accumulator stays in tensor memory and nothing is read
+// back between blocks (only every 8192 of k for sums kept in fp32: see most_blocks).  That form wants a
+// scale byte per row and 32 of k; a byte serves the four instructions of a block of 128, and the four
+// bytes of a 32-bit word four blocks, picked by the instruction's scale id.
+//
+// Large products are bound by the tensor cores, and where they run back to back by the power limit
+// (8192 x 14336 x 4096: 296 us, 3250 TFLOP/s, in a short burst; 342 us in a row); short contractions with a large
+// result by writing it (16384 x 2304 x 768: 30 us; 8192 x 4096 x 128: 18 us, 3.8 TB/s); few rows by
+// reading the wide operand once (1 x 14336 x 4096: 13 us, 4.5 TB/s); small ones by the latency of their
+// steps (333 x 1500 x 1001: 8.7 us).
 //
 // An operand whose contraction runs down its columns (both of the weight's gradient, the weight of
 // the input's gradient) is read as it lies: the tensor cores take it MN-major, no copy is transposed.
@@ -246,6 +252,9 @@ struct Gemm8Args {
 };
 
 // ---------------------------------------------------------------- 256 x 256 tiles
+// A pair of CTAs shares a tile, 128 of its rows each, and each half of B's 256 columns: 64 KB of operands
+// and 2048 cycles of tensor cores per four blocks.  The grid is persistent: the copies and the scales of
+// the next tile run ahead while the epilogue writes this one.
 constexpr int kPairThreads = 384;           // warp 0 TMA, 1 MMA, 2-3 scales, 4-11 epilogue
 constexpr int kEpi0 = 4, kEpiN = 8;
 constexpr int kStages8 = 6;
@@ -837,7 +846,9 @@ __global__ void __launch_bounds__(256) gemm_fp8_zero_kernel(const __grid_constan
 // The narrow side has up to NT indices.  A CTA takes 128 indices of the wide side (the tensor cores'
 // M) and a slice of k; the CTAs of a cluster hold the slices of one tile, and each adds a part of the
 // tile over the slices, in order, out of the others' shared memory.  Bound by reading the wide
-// operand once.
+// operand once: an SM draws some 43 GB/s, and the tiles do not divide among 152 of them (1 x 14336 x 4096:
+// 13.0 us, 4.5 TB/s; 1 x 28672 x 8192: 39 us, 6.0 TB/s).  With NT = 128 also small products of any shape,
+// which tiles of 256 would leave most SMs idle for.
 constexpr int kNarrowThreads = 192;         // warp 0 TMA, 1 MMA, 2 scales, 2-5 epilogue
 constexpr int kNarrowSf = 2;
 template <int NT>

