@@ -813,7 +813,8 @@ int mfsdp_activation_forward(int32_t kind, int64_t rows, int64_t cols, int32_t d
  *   dgate, dup            nullable outputs of `dtype`;
  *   dgate_row, dup_row    nullable, in 8 bits, ROW (for dx = dy W);
  *   dgate_col, dup_col    nullable, in 8 bits, COL (for dW = dy^T x).
- * At least one output.  dgate may be dy's or gate's buffer, dup dy's or up's (same pitch).
+ * At least one output.  dgate may be dy's or gate's buffer, dup dy's or up's (same pitch).  Two
+ * results have two buffers.
  */
 int mfsdp_activation_backward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
                               const void* dy, int64_t ld_dy, const void* gate, int64_t ld_gate,

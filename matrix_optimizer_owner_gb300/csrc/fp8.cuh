@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <initializer_list>
 
 #include "elem.cuh"
 #include "mfsdp.h"
@@ -542,6 +543,14 @@ __device__ __forceinline__ void quantize_whole(const At& at, TileSmem<1>& sm, co
 }
 
 // ---- host checks
+// Whether results have buffers of their own (null: not wanted).
+inline bool distinct(std::initializer_list<const void*> results) {
+  for (auto i = results.begin(); i != results.end(); ++i)
+    for (auto j = results.begin(); j != i; ++j)
+      if (*i && *i == *j) return false;
+  return true;
+}
+inline const void* data_of(const mfsdp_fp8_matrix* m) { return m ? m->data : nullptr; }
 inline bool groups_ok(int32_t g) { return g >= MFSDP_GROUPS_ROW && g <= MFSDP_GROUPS_TILE; }
 inline int64_t scale_rows(int32_t g, int64_t rows) {
   return g == MFSDP_GROUPS_ROW ? rows : (rows + kGroup - 1) / kGroup;

@@ -181,6 +181,20 @@ def test_activation_backward_refusals(lib, change, status):
     assert _call(lib.mfsdp_activation_backward, ACT_BWD, **change) == status
 
 
+def test_results_have_buffers_of_their_own(lib):
+    """A buffer that two results share, or a result of 8 bits and its source."""
+    row, col, tile = _m(), _m(groups=COL), _m(groups=TILE)         # all of the same memory
+    assert lib.mfsdp_quantize_fp8(8, 200, 0, P + 4096, 200, row, col, None) == EINVAL
+    assert lib.mfsdp_quantize_fp8(8, 200, 0, P, 200, tile, None, None) == EINVAL
+    assert lib.mfsdp_regroup_fp8(8, 200, row, tile, None, None) == EINVAL
+    assert _call(lib.mfsdp_norm_residual_forward, NORM_FWD) == EINVAL           # h and y
+    assert _call(lib.mfsdp_norm_residual_forward, NORM_FWD, h=P + 4096, y8=row) == EINVAL
+    assert _call(lib.mfsdp_activation_forward, ACT_FWD, y=None, y8=row, gate8=row) == EINVAL
+    assert _call(lib.mfsdp_activation_backward, ACT_BWD) == EINVAL              # dgate and dup
+    assert _call(lib.mfsdp_activation_backward, ACT_BWD, dup=None, dgate=P + 4096, dg_row=row,
+                 dg_col=col) == EINVAL
+
+
 # ------------------------------------------------------------------------------------ the binding
 def test_binding_refuses_host_tensors_and_shapes():
     from matrix_optimizer_owner_gb300 import mfsdp

@@ -58,6 +58,41 @@ def test_gemm_long_contraction(dtype, m, n, k, down):
         assert (err <= tol).all(), float((err / tol).max())
 
 
+@pytest.mark.parametrize("m", [300, 8])
+@pytest.mark.parametrize("sa,sb", [(254, 0), (0, 254), (250, 4), (1, 127), (0, 128), (64, 64), (254, 127),
+                                   (254, 254), (0, 0)])
+def test_gemm_scales_far_apart(m, sa, sb):
+    """A block's two scales act as one power of two, however large the one and small the other."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    a, b = _matrix(_positive(m, 256, gen), 0), _matrix(_positive(400, 256, gen), 0)
+    a.scales.fill_(sa), b.scales.fill_(sb)
+    c = torch.empty(m, 400, device="cuda")
+    mfsdp.mfsdp_gemm_fp8(a, b, c, trans_b=True)
+    want = (a.data.double() @ b.data.double().T) * 2.0 ** (sa + sb - 254)   # exact, or out of range
+    assert torch.equal(c, want.float())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(5, 397, 256), (397, 5, 256), (300, 397, 256), (130, 1001, 384),
+                                   (2000, 2301, 256), (1100, 1301, 9000), (260, 301, 20000)])
+def test_gemm_edges_of_aligned_rows(m, n, k, dtype):
+    """Rows on 16-byte boundaries whose last columns fill no access, overwritten and added to.  The sums
+    are multiples of 1/64 below 2^18, so those of fp32 are exact and bf16 ones rounded once."""
+    from matrix_optimizer_owner_gb300 import mfsdp
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    a, b = _positive(m, k, gen), _positive(n, k, gen)
+    base = torch.randint(-64, 64, (m, -(-n // 8) * 8), generator=gen, device="cuda").to(TYPES[dtype])
+    c, keep = base[:, :n], base[:, n:].clone()
+    ref = torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    for k0 in range(0, k, 4096):
+        ref += a[:, k0:k0 + 4096].double() @ b[:, k0:k0 + 4096].double().T
+    for accumulate in (True, False):
+        want = ref + (c.double() if accumulate else 0)
+        mfsdp.mfsdp_gemm_fp8(_matrix(a, 0), _matrix(b, 0), c, trans_b=True, accumulate=accumulate)
+        assert torch.equal(c, want.to(TYPES[dtype])) and torch.equal(base[:, n:], keep)
+
+
 @pytest.mark.parametrize("trans_a,trans_b", [(False, True), (False, False), (True, False), (True, True)])
 def test_gemm_of_nothing(trans_a, trans_b):
     """Empty in any direction: no rows, no columns, or a contraction of nothing, which is zero."""
