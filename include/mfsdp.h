@@ -703,6 +703,7 @@ int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab, int32
  *               most the type's largest value, so nothing saturates; infinities and NaN become NaN
  *               of their own element and leave the others alone.
  *   reading     s = 255 makes its group NaN.
+ * Two results of a call never share a buffer (MFSDP_EINVAL where they start at one address).
  * ------------------------------------------------------------------------------------------ */
 
 typedef enum { MFSDP_FP8_E4M3 = 0, MFSDP_FP8_E5M2 = 1 } mfsdp_fp8_dtype;
@@ -813,8 +814,7 @@ int mfsdp_activation_forward(int32_t kind, int64_t rows, int64_t cols, int32_t d
  *   dgate, dup            nullable outputs of `dtype`;
  *   dgate_row, dup_row    nullable, in 8 bits, ROW (for dx = dy W);
  *   dgate_col, dup_col    nullable, in 8 bits, COL (for dW = dy^T x).
- * At least one output.  dgate may be dy's or gate's buffer, dup dy's or up's (same pitch).  Two
- * results have two buffers.
+ * At least one output.  dgate may be dy's or gate's buffer, dup dy's or up's (same pitch).
  */
 int mfsdp_activation_backward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype,
                               const void* dy, int64_t ld_dy, const void* gate, int64_t ld_gate,
