@@ -400,8 +400,8 @@ __device__ __forceinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane
   }
 }
 
-// The same where rows start on 16-byte boundaries and C in bf16 is not added to: the warp's block leaves by
-// TMA, which cuts it at C's edges, 64 bytes of each row at a time.  (Stored by the lanes from registers, 32 bytes of
+// The same where rows start and end on 16-byte boundaries and C in bf16 is not added to: the warp's block
+// leaves by TMA, which cuts it at C's edges, 64 bytes of each row at a time.  (Stored by the lanes from registers, 32 bytes of
 // a row each: 24.8 us for 8192 x 4096 x 128 against 18.1, 3.8 TB/s, with a fill at 4.0; 35 against 30 for
 // 16384 x 2304 x 768.  Two staging blocks a warp, for a stage of operands less, changed nothing.)
 template <bool BF16>
@@ -436,7 +436,7 @@ __device__ __forceinline__ void put_block(const Gemm8Args& P, int64_t rw, int la
 // CHUNKED: a tile's contraction is cut into chunks that are added up in registers.
 // SPLIT: few tiles with a long contraction.  Two pairs (a cluster of four CTAs) take half of k each of one
 // tile; then each takes half of the columns and gets the other's sums of them through its shared memory.
-// PLAIN: C's rows start on 16-byte boundaries and it is overwritten, or in fp32.  The other forms of the epilogue are
+// PLAIN: C's rows start and end on 16-byte boundaries and it is overwritten, or in fp32.  The other forms of the epilogue are
 // kernels of their own: beside each other in one kernel they cost its common path up to a sixth (the
 // warps wait for instructions).
 template <bool CHUNKED, bool SPLIT, bool BF16, bool PLAIN>
@@ -1363,7 +1363,8 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   const int most = most_blocks(c_bf16);
   const int tiles = g.tiles_m * g.tiles_n;
   const int pairs = std::max(1, std::min(sms / 2, tiles));
-  const bool plain = g.vec && (!g.accumulate || !c_bf16) &&
+  // (A store by TMA writes whole groups of 16 bytes: past the last column, where that is inside one.)
+  const bool plain = g.vec && (n * (int64_t)dtype_bytes(c_dtype)) % 16 == 0 && (!g.accumulate || !c_bf16) &&
                      (c_bf16 ? encode_map(&g.cm, c, m, n, ld_c, 32u, 32u, false)
                              : encode_map_f32(&g.cm, static_cast<float*>(c), m, n, ld_c, 32u, 16u));
   if (plan.halves && g.kb_split <= most)

@@ -75,7 +75,8 @@ def test_gemm_scales_far_apart(m, sa, sb):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("m,n,k", [(5, 397, 256), (397, 5, 256), (300, 397, 256), (130, 1001, 384),
-                                   (2000, 2301, 256), (1100, 1301, 9000), (260, 301, 20000)])
+                                   (2000, 2301, 256), (1100, 1301, 9000), (260, 301, 20000),
+                                   (2600, 2301, 640), (2600, 2300, 640), (2600, 2301, 9000)])
 def test_gemm_edges_of_aligned_rows(m, n, k, dtype):
     """Rows on 16-byte boundaries whose last columns fill no access, overwritten and added to.  The sums
     are multiples of 1/64 below 2^18, so those of fp32 are exact and bf16 ones rounded once."""
