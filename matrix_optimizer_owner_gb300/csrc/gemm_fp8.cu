@@ -1119,6 +1119,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 
 // ---------------------------------------------------------------- host
 constexpr int kPairs = 76;                  // CTA pairs of the device: what the plans count on
+// Clusters of so many CTAs, two an SM, that run at a time: sizes that do not divide the SMs of a part of
+// the device leave some of them over (1 x 6144 x 4096: 48 clusters of six 12.4 us, of five 7.5).
+constexpr int kClusters[9] = {0, 304, 152, 96, 72, 56, 46, 32, 32};
 
 struct Gemm8Plan {
   bool narrow = false, swap = false;        // swap: the narrow side is A's
@@ -1146,8 +1149,9 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16, bool accumulat
     // as many slices of k, of two blocks at least, as run at a time: an SM draws some 43 GB/s from
     // memory, whatever it has under way (one, two or three CTAs with 3 to 9 stages each took the same
     // time a block), so what counts is that all of them draw
-    const int s =
-        (int)std::max<int64_t>(std::max(1, least), std::min({4 * kPairs / tiles, (int64_t)8, (int64_t)nkb / 2}));
+    int s = 8;
+    while (s > 1 && (tiles > kClusters[s] || s > nkb / 2)) --s;
+    s = std::max(s, least);
     p.splits = s;
     p.kb_split = (nkb + s - 1) / s;
     return p;
@@ -1161,8 +1165,8 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16, bool accumulat
   double narrow = 0.;
   for (int s = std::max(1, least); s <= 8 && s <= std::max(1, nkb); ++s) {
     const int per = (nkb + s - 1) / s;
-    const int64_t ctas = small * s, rounds = (ctas + 4 * kPairs - 1) / (4 * kPairs);
-    const int64_t at_once = std::min<int64_t>(ctas, 4 * kPairs);
+    const int64_t rounds = (small + kClusters[s] - 1) / kClusters[s];
+    const int64_t at_once = std::min<int64_t>(small * s, 4 * kPairs);
     const double rest = s == 1 ? 5.3 + 0.0065 * (double)at_once : 6.2 + 0.0125 * (double)at_once;
     const double old = accumulate ? 10. / s : 0.;
     const double t = (double)rounds * (per * (at_once > 2 * kPairs ? 0.5 : 0.4) + rest + old);
