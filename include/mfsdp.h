@@ -702,7 +702,8 @@ int mfsdp_head_loss_backward(int64_t n_tokens, int64_t dim, int64_t vocab, int32
  *   writing     s is the least one (from 0) for which the group's largest finite magnitude is at
  *               most the type's largest value, so nothing saturates; infinities and NaN become NaN
  *               of their own element and leave the others alone.
- *   reading     s = 255 makes its group NaN.
+ *   reading     s = 255 makes its group NaN.  2^128, which fp32's largest values are in 8 bits, and more
+ *               is fp32's largest value where a regrouping or an activation's gradient starts from it.
  * Two results of a call never share a buffer (MFSDP_EINVAL where they start at one address).
  * ------------------------------------------------------------------------------------------ */
 
@@ -730,8 +731,8 @@ int mfsdp_quantize_fp8(int64_t rows, int64_t cols, int32_t dtype, const void* x,
 /*
  * The same from an 8-bit matrix of any grouping: an activation that was kept as a product's operand
  * (ROW) becomes the operand of its weight's gradient (COL).  Of the same type, only values that
- * become subnormal under their new group's scale are rounded.  The results must not be the source's
- * buffers.
+ * become subnormal under their new group's scale are rounded, and magnitudes above 2^128, which only
+ * scales made elsewhere give, become 2^128.  The results must not be the source's buffers.
  */
 int mfsdp_regroup_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_matrix* src,
                       const mfsdp_fp8_matrix* out, const mfsdp_fp8_matrix* also, void* stream);

@@ -215,7 +215,7 @@ struct Ahead {
                  : "=r"(r.x), "=r"(r.y)
                  : "r"(at(stage, i, m, 0))
                  : "memory");
-    unpack_fp8(r, e5m2, scale_value(byte), v);
+    held_values(r, e5m2, scale_value(byte), v);
   }
 };
 

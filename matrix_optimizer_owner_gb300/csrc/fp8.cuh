@@ -90,6 +90,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// ... cut towards zero: what is beyond fp32 becomes its largest value, not infinity.
+__device__ __forceinline__ uint64_t mul2_cut(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 template <int N>
 __device__ __forceinline__ void scale_pairs(const float (&v)[N], float f, float (&u)[N]) {
   const uint64_t ff = pair_of(f, f);
@@ -140,6 +146,17 @@ __device__ __forceinline__ void unpack_fp8(uint2 r, int e5m2, float scale, float
   float u[8];
   unpack_fp8(r, e5m2, u);
   scale_pairs(u, scale, v);
+}
+// The values that 8 bits hold, as fp32 arithmetic goes on with them.  A product with a scale is exact
+// wherever fp32 has it, and fp32's largest values, which are 2^128 in 8 bits, are beyond it: cut, they are
+// the largest value again, which rounds to 2^128 once more, in both types.
+__device__ __forceinline__ float held_value(float q, float scale) { return __fmul_rz(q, scale); }
+__device__ __forceinline__ void held_values(uint2 r, int e5m2, float scale, float (&v)[8]) {
+  float u[8];
+  unpack_fp8(r, e5m2, u);
+  const uint64_t ff = pair_of(scale, scale);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) split_pair(mul2_cut(pair_of(u[j], u[j + 1]), ff), v[j], v[j + 1]);
 }
 // The first n (1 to 8) bytes of a chunk at p, which starts on an 8-byte boundary.
 __device__ __forceinline__ void store_fp8(uint8_t* p, uint2 r, int n) {
@@ -391,7 +408,7 @@ struct TileRaw8 {
     }
   }
   __device__ __forceinline__ void get(int i, int e5m2, float (&v)[8]) const {
-    unpack_fp8(p[i], e5m2, s[i], v);
+    held_values(p[i], e5m2, s[i], v);
   }
 };
 
