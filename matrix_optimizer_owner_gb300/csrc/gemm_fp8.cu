@@ -1178,9 +1178,12 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16, bool accumulat
   // 256 x 256 tiles on CTA pairs
   const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
   double pair = 7.5 + (double)((tiles + kPairs - 1) / kPairs) * (nkb * 0.3 + 2.);
-  if (2 * tiles <= kPairs && nkb >= 16) {
-    p.kb_split = ((nkb + 1) / 2 + 7) / 8 * 8;
-    const double t = 9. + p.kb_split * 0.34;
+  // ... or two pairs a tile, where an accumulator takes half of k (longer fp32 sums compare what they run as:
+  // 2304 x 768 x 32768 in five slices 69 us, on one pair a tile 98)
+  const int half = ((nkb + 1) / 2 + 7) / 8 * 8;
+  if (2 * tiles <= kPairs && nkb >= 16 && half <= most_blocks(c_bf16)) {
+    p.kb_split = half;
+    const double t = 9. + half * 0.34;
     p.halves = t < pair;
     pair = std::min(pair, t);
   }
@@ -1371,7 +1374,7 @@ extern "C" int mfsdp_gemm_fp8(int64_t m, int64_t n, int64_t k, const mfsdp_fp8_m
   const bool plain = g.vec && (n * (int64_t)dtype_bytes(c_dtype)) % 16 == 0 && (!g.accumulate || !c_bf16) &&
                      (c_bf16 ? encode_map(&g.cm, c, m, n, ld_c, 32u, 32u, false)
                              : encode_map_f32(&g.cm, static_cast<float*>(c), m, n, ld_c, 32u, 16u));
-  if (plan.halves && g.kb_split <= most)
+  if (plan.halves)
     e = plain ? launch_pair<false, true, true>(g, 4 * tiles, st)
               : launch_pair<false, true, false>(g, 4 * tiles, st);
   else if (g.nkb > most)
