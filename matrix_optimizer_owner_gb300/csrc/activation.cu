@@ -460,9 +460,9 @@ extern "C" int mfsdp_activation_backward(
       (chk = check_rows(dgate, ld_dgate, cols, dtype, a.vec)) != MFSDP_OK ||
       (chk = check_rows(dup, ld_dup, cols, dtype, a.vec)) != MFSDP_OK)
     return chk;
-  if (!distinct({dgate, dup, data_of(dgate_row), data_of(dgate_col), data_of(dup_row), data_of(dup_col),
-                 data_of(gate8), data_of(up8)}))
-    return MFSDP_EINVAL;
+  const std::initializer_list<const void*> results = {dgate, dup, data_of(dgate_row), data_of(dgate_col),
+                                                      data_of(dup_row), data_of(dup_col)};
+  if (!distinct(results) || !apart(results, {data_of(gate8), data_of(up8)})) return MFSDP_EINVAL;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;

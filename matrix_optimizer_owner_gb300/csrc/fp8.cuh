@@ -567,6 +567,13 @@ inline bool distinct(std::initializer_list<const void*> results) {
       if (*i && *i == *j) return false;
   return true;
 }
+// Whether no result is an input's buffer (inputs may share theirs).
+inline bool apart(std::initializer_list<const void*> results, std::initializer_list<const void*> inputs) {
+  for (const void* r : results)
+    for (const void* i : inputs)
+      if (r && r == i) return false;
+  return true;
+}
 inline const void* data_of(const mfsdp_fp8_matrix* m) { return m ? m->data : nullptr; }
 inline bool groups_ok(int32_t g) { return g >= MFSDP_GROUPS_ROW && g <= MFSDP_GROUPS_TILE; }
 inline int64_t scale_rows(int32_t g, int64_t rows) {
