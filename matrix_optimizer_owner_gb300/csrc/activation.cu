@@ -403,7 +403,8 @@ extern "C" int mfsdp_activation_forward(int32_t kind, int64_t rows, int64_t cols
       (chk = check_rows(up, ld_up, cols, dtype, a.vec)) != MFSDP_OK ||
       (chk = check_rows(y, ld_y, cols, dtype, a.vec)) != MFSDP_OK)
     return chk;
-  if (!distinct({y, data_of(y8), data_of(gate8), data_of(up8)})) return MFSDP_EINVAL;
+  if (!distinct({y, data_of(y8), bytes_of(y8), data_of(gate8), bytes_of(gate8), data_of(up8), bytes_of(up8)}))
+    return MFSDP_EINVAL;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;
@@ -460,9 +461,11 @@ extern "C" int mfsdp_activation_backward(
       (chk = check_rows(dgate, ld_dgate, cols, dtype, a.vec)) != MFSDP_OK ||
       (chk = check_rows(dup, ld_dup, cols, dtype, a.vec)) != MFSDP_OK)
     return chk;
-  const std::initializer_list<const void*> results = {dgate, dup, data_of(dgate_row), data_of(dgate_col),
-                                                      data_of(dup_row), data_of(dup_col)};
-  if (!distinct(results) || !apart(results, {data_of(gate8), data_of(up8)})) return MFSDP_EINVAL;
+  const std::initializer_list<const void*> results = {
+      dgate, dup, data_of(dgate_row), bytes_of(dgate_row), data_of(dgate_col), bytes_of(dgate_col),
+      data_of(dup_row), bytes_of(dup_row), data_of(dup_col), bytes_of(dup_col)};
+  if (!distinct(results) || !apart(results, {data_of(gate8), bytes_of(gate8), data_of(up8), bytes_of(up8)}))
+    return MFSDP_EINVAL;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;

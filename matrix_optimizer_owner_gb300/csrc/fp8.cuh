@@ -575,6 +575,7 @@ inline bool apart(std::initializer_list<const void*> results, std::initializer_l
   return true;
 }
 inline const void* data_of(const mfsdp_fp8_matrix* m) { return m ? m->data : nullptr; }
+inline const void* bytes_of(const mfsdp_fp8_matrix* m) { return m ? m->scales : nullptr; }
 inline bool groups_ok(int32_t g) { return g >= MFSDP_GROUPS_ROW && g <= MFSDP_GROUPS_TILE; }
 inline int64_t scale_rows(int32_t g, int64_t rows) {
   return g == MFSDP_GROUPS_ROW ? rows : (rows + kGroup - 1) / kGroup;

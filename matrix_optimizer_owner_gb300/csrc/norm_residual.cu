@@ -300,7 +300,7 @@ extern "C" int mfsdp_norm_residual_forward(
       !aligned_to(weight, ps) || !aligned_to(bias, ps) || !aligned_to(mean, 4) ||
       !aligned_to(rstd, 4))
     return MFSDP_EALIGN;
-  if (!distinct({h, y, data_of(h8), data_of(y8)})) return MFSDP_EINVAL;
+  if (!distinct({h, y, data_of(h8), bytes_of(h8), data_of(y8), bytes_of(y8), mean, rstd})) return MFSDP_EINVAL;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;

@@ -422,6 +422,7 @@ extern "C" int mfsdp_norm_residual_backward(
   size_t need = 0;
   mfsdp_norm_backward_workspace_bytes(rows, cols, &need);
   if (workspace_bytes < need) return MFSDP_EWORKSPACE;
+  if (!distinct({dx, dweight, dbias})) return MFSDP_EINVAL;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;

@@ -160,7 +160,7 @@ extern "C" int mfsdp_quantize_fp8(int64_t rows, int64_t cols, int32_t dtype, con
   if (rows == 0) return MFSDP_OK;
   if (!x || ld_x < cols) return MFSDP_EINVAL;
   if (!aligned_to(x, dtype_bytes(dtype))) return MFSDP_EALIGN;
-  if (!distinct({x, data_of(out), data_of(also)})) return MFSDP_EINVAL;
+  if (!distinct({x, data_of(out), bytes_of(out), data_of(also), bytes_of(also)})) return MFSDP_EINVAL;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;
@@ -187,7 +187,8 @@ extern "C" int mfsdp_regroup_fp8(int64_t rows, int64_t cols, const mfsdp_fp8_mat
   if (chk == MFSDP_OK) chk = check_outputs(rows, cols, out, also, a, forms);
   if (chk != MFSDP_OK) return chk;
   if (rows == 0) return MFSDP_OK;
-  if (!distinct({src->data, data_of(out), data_of(also)})) return MFSDP_EINVAL;
+  if (!distinct({src->data, src->scales, data_of(out), bytes_of(out), data_of(also), bytes_of(also)}))
+    return MFSDP_EINVAL;
   int sms = 0;
   const int dst = device_sms(&sms);
   if (dst != MFSDP_OK) return dst;
