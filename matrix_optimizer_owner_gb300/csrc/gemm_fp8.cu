@@ -1179,9 +1179,10 @@ Gemm8Plan plan_gemm(int64_t m, int64_t n, int64_t k, bool c_bf16, bool accumulat
   const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
   double pair = 7.5 + (double)((tiles + kPairs - 1) / kPairs) * (nkb * 0.3 + 2.);
   // ... or two pairs a tile, where an accumulator takes half of k (longer fp32 sums compare what they run as:
-  // 2304 x 768 x 32768 in five slices 69 us, on one pair a tile 98)
+  // 2304 x 768 x 32768 in five slices 69 us, on one pair a tile 98) and the clusters of four, a CTA an SM,
+  // run at a time (9216 x 256 x 16384, 36 tiles: 40 us; 37 took 69, without halves 44)
   const int half = ((nkb + 1) / 2 + 7) / 8 * 8;
-  if (2 * tiles <= kPairs && nkb >= 16 && half <= most_blocks(c_bf16)) {
+  if (2 * tiles <= kClusters[4] && nkb >= 16 && half <= most_blocks(c_bf16)) {
     p.kb_split = half;
     const double t = 9. + half * 0.34;
     p.halves = t < pair;

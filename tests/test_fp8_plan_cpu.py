@@ -16,7 +16,7 @@ HARNESS = r"""
 %s
 int main() {
   const int64_t sides[] = {1, 2, 16, 17, 64, 65, 100, 128, 129, 256, 300, 513, 768, 1024, 1536, 2304, 4096,
-                           14336, 40000};
+                           9216, 9472, 14336, 40000};
   const int64_t ks[] = {1, 128, 129, 1000, 1920, 2048, 4096, 8192, 8193, 16256, 16384, 16385, 17000, 20480,
                         32768, 65536, 65537, 131072, 200000, 524288, 600000, 4000000};
   long counts[3] = {0, 0, 0};
@@ -34,7 +34,7 @@ int main() {
                    (int64_t)p.splits * p.kb_split >= nkb && std::min(m, n) <= (p.nt < 128 ? p.nt : 1 << 30);
             if (p.halves)
               ok = ok && p.kb_split > 0 && p.kb_split < nkb && p.kb_split %% 8 == 0 && p.kb_split <= most &&
-                   nkb - p.kb_split <= most && 2 * tiles <= kPairs;
+                   nkb - p.kb_split <= most && 2 * tiles <= kClusters[4];   // (one CTA an SM)
             ++counts[p.halves ? 2 : p.narrow ? 1 : 0];
             if (!ok) {
               std::printf("%%lld x %%lld x %%lld %%s%%s: narrow %%d halves %%d splits %%d of %%d blocks\n", (long long)m,
