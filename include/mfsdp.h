@@ -799,6 +799,8 @@ typedef enum { MFSDP_ACT_SWIGLU = 0, MFSDP_ACT_GELU = 1 } mfsdp_activation;
  * The activation of a feed-forward layer, elementwise over [rows x cols]:
  *     SWIGLU  y = gate / (1 + exp(-gate)) up
  *     GELU    y = gate (1 + tanh(sqrt(2 / pi) (gate + 0.044715 gate^3))) / 2; takes no up
+ * The share of the gate that passes, 1 / (1 + exp(-a)), counts as 0 where it is below 2^-126 (bf16) or
+ * where exp(-a) is beyond fp32 (f32).
  *   y, y8         the result in `dtype` and in 8 bits (ROW): at least one.
  *   gate8, up8    nullable: the inputs in 8 bits (ROW), checkpoints for the backward pass.
  * gate and up may be two halves of one buffer's rows.  rows == 0 is no work.  rows, cols < 2^31.

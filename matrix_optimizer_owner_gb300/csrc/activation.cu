@@ -11,8 +11,10 @@
 // 128 x 128 values, which both groupings end inside.
 //
 // Forward is bound by memory, with little to spare (8192 x 14336 SwiGLU with all three results in 8 bits:
-// 163 us, 5.0 TB/s).  Backward is bound by what the warps can issue: a value's four results cost some
-// fifty instructions (the same size from the checkpoints, 8 bytes a value: 242 us, 3.9 TB/s).
+// 163 us, 5.0 TB/s; GELU 128 us).  Backward fills no unit (2048 rows of it: 57 % of the issue slots, 45 % of the
+// ALU, 34 % of the memory): a value's four results cost some fifty instructions, and the gradients fill the
+// registers for one block of 16 warps an SM, which meet at two barriers a tile (the same size from the
+// checkpoints, 8 bytes a value: 242 us, 3.9 TB/s; GELU 152 us).
 #include <algorithm>
 #include <atomic>
 
@@ -35,8 +37,9 @@ struct ActArgs {
 };
 
 // 1 / (1 + exp(-x)).  Beside bf16 rows, whose time leaves room for some twenty instructions a value,
-// exp and the division are the special-function unit's (within 2 ulp each); fp32 ones move twice the
-// bytes and take the exact ones.
+// exp and the division are the special-function unit's: the product with log2(e) is rounded before the
+// power of two is taken, so exp is within (2 + 1.2 |x|) 2^-23 of itself, the division within 2^-22, and
+// results below 2^-126 (x < -87.3) are 0.  fp32 ones move twice the bytes and take the exact ones.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float x);
 template <>

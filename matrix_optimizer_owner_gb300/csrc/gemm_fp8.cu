@@ -8,7 +8,8 @@
 //
 // Large products are bound by the tensor cores, and where they run back to back by the power limit
 // (8192 x 14336 x 4096: 296 us, 3250 TFLOP/s, in a short burst; 342 us in a row); short contractions with a large
-// result by writing it (16384 x 2304 x 768: 30 us; 8192 x 4096 x 128: 18 us, 3.8 TB/s); few rows by
+// result by writing it (16384 x 2304 x 768: 30 us at 2070 MHz, 35 to 38 at the 1.6 GHz that large products in a
+// row leave; 8192 x 4096 x 128: 18 us, 3.8 TB/s); few rows by
 // reading the wide operand once (1 x 14336 x 4096: 13 us, 4.5 TB/s); small ones by the latency of their
 // steps (333 x 1500 x 1001: 8.7 us).
 //
@@ -322,7 +323,9 @@ __device__ __forceinline__ void add_old(const Gemm8Args& P, int64_t r, int64_t c
 }
 
 // 32 columns of a lane's row to C, whatever C's rows, edges and old values are.  Rows without 16-byte
-// alignment go through the warp's staging area (2 KB), a row of the block at a time.
+// alignment go through the warp's staging area (2 KB), a row of the block at a time.  What bf16 C held is
+// read here, by each lane from its own row, and waited for (16384 x 768 x 2304: 29 us overwritten, 52 added to;
+// 4096 x 4096 x 4096: 52 and 60).
 template <bool BF16>
 __device__ __forceinline__ void put_row(const Gemm8Args& P, int64_t rw, int lane, int64_t c0,
                                         uint32_t stg, float (&v)[32]) {
@@ -1120,7 +1123,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 // ---------------------------------------------------------------- host
 constexpr int kPairs = 76;                  // CTA pairs of the device: what the plans count on
 // Clusters of so many CTAs, two an SM, that run at a time: sizes that do not divide the SMs of a part of
-// the device leave some of them over (1 x 6144 x 4096: 48 clusters of six 12.4 us, of five 7.5).
+// the device leave some of them over (1 x 6144 x 4096: 48 clusters of six 12.4 us, of five 7.5).  One cluster
+// more is a second round (1 x 16384 of k, 32 and 33 clusters of eight: 10.8 and 13.1 us; 1 x 8192 of k, 96 and 97 of
+// three: 15.4 and 19.2; 56 and 57 of five, 46 and 47 of six, 72 and 73 of four alike).
 constexpr int kClusters[9] = {0, 304, 152, 96, 72, 56, 46, 32, 32};
 
 struct Gemm8Plan {

@@ -3,9 +3,11 @@
 // Per row of n elements (RMS norm: mu = 0 and no bias):
 //     h = x + r,  mu = sum(h) / n,  s = 1 / sqrt(sum((h - mu)^2) / n + eps),  y = (h - mu) s w + b
 // h and y leave in the caller's type, in 8 bits (1 x 128 groups), or both, each rounded once from the
-// fp32 value.  Bound by memory (8192 x 4096 bf16, RMS, h in bf16 and y in 8 bits: 41 us, 5.7 TB/s), short rows by
-// what the warps can issue as well (16384 x 768, layer norm, h in 8 bits too: 23 us, 4.3 TB/s).  A row lies in registers over a warp (up to 768 elements) or a block, so
-// neighbouring threads hold a group of 128 and its largest value takes a few shuffles.
+// fp32 value.  Bound by memory (8192 x 4096 bf16, RMS, h in bf16 and y in 8 bits: 41 us, 5.7 TB/s; 46 with the
+// weight in fp32).  Short rows fill neither it nor the issue slots (16384 x 768, layer norm, h in 8 bits too:
+// 23 us, 4.3 TB/s, 37 instructions a value at 60 % of the slots): a warp loads nothing while it reduces its row.
+// A row lies in registers over a warp (up to 768 elements) or a block, so neighbouring threads hold a group of
+// 128 and its largest value takes a few shuffles.
 #include "norm_residual.cuh"
 
 namespace mfsdp {
